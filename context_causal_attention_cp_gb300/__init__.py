@@ -7,16 +7,23 @@ absence raises: there is no CPU fallback.
 """
 
 from .api import (  # noqa: F401
+    KVCache,
     PassQSchedule,
     ShardPlan,
+    SharedPlan,
+    alloc_kv_cache,
     alloc_plan,
+    alloc_shared_workspace,
     check_status,
     cp_attn_partial,
     cp_attn_partial_accumulate,
     cp_attn_partial_kv,
     cp_attn_partial_restore,
     cp_attn_prefill,
+    cp_attn_shared,
     cp_attn_split_kv,
+    cp_kv_dequantize,
+    cp_kv_quantize,
     cp_lse_merge,
     cp_partial_kv_workspace_size,
     cp_partial_kv_workspace_size_segs,
@@ -29,9 +36,13 @@ from .api import (  # noqa: F401
     cp_select_pass_cost,
     cp_shard_plan,
     cp_shard_plan_sizes,
+    cp_shared_workspace_size,
     make_plan,
+    make_shared_plan,
+    make_shared_plan_segs,
     new_status,
     pass_q_schedule,
     pass_q_schedule_host,
     segments_host,
+    shared_segments,
 )

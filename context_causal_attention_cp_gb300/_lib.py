@@ -36,6 +36,21 @@ vp = ctypes.c_void_p
 i32 = ctypes.c_int
 i64 = ctypes.c_int64
 
+
+
+class KvCodes(ctypes.Structure):
+    """cp_kv_codes_t"""
+    _fields_ = [("codes", vp), ("scales", vp), ("row_stride", i64), ("head_stride", i64),
+                ("scale_stride", i64)]
+
+
+class SharedPlanInfo(ctypes.Structure):
+    """cp_shared_plan_t"""
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("num_q_rows", "Hq", "Hkv", "num_ctas", "num_units", "num_pieces", "num_entries",
+                 "kv_rows", "needs_merge", "budget")] + [("ws_rows", i64), ("table_ints", i64)]
+
+
 # name -> (restype, argtypes); must match include/cpattn.h
 SIGNATURES = {
     "cp_shard_plan_sizes": (i32, [c_i32p, c_i32p, i32, i32, i32, c_i32p, c_i32p, c_i32p]),
@@ -81,6 +96,16 @@ SIGNATURES = {
     "cp_attn_partial_kv_noalloc": (i32, [vp, i32, vp, i32, vp, i32, vp, i64, i64, vp, i64, i64,
                                          i32, i32, i32, i32, i32, ctypes.c_float, i32, i32, i32,
                                          vp, vp, i32, vp, i32, i64, vp, vp]),
+    "cp_kv_quantize": (i32, [vp, i64, i64, vp, i64, i64, i32, i32, i32, i32, i32, vp,
+                             ctypes.POINTER(KvCodes), ctypes.POINTER(KvCodes), i32, vp, vp]),
+    "cp_kv_dequantize": (i32, [ctypes.POINTER(KvCodes), ctypes.POINTER(KvCodes), i32, i32, i32, i32,
+                               vp, i32, vp, vp, i32, vp, vp]),
+    "cp_shared_plan_size": (i32, [vp, i32, i32, i32, i32, i32, ctypes.POINTER(SharedPlanInfo)]),
+    "cp_shared_plan": (i32, [vp, i32, ctypes.POINTER(SharedPlanInfo), vp]),
+    "cp_shared_workspace_size": (i32, [ctypes.POINTER(SharedPlanInfo), i32, ctypes.POINTER(i64)]),
+    "cp_attn_shared": (i32, [ctypes.POINTER(SharedPlanInfo), vp, vp, i64, i64, vp, i64, i64, vp,
+                             vp, i64, i64, vp, i64, i32, i32, i32, ctypes.c_float, vp, i32, vp,
+                             vp, i64, vp, vp]),
     "cp_attn_debug": (i32, [i32, ctypes.c_longlong]),
     "cp_status_string": (ctypes.c_char_p, [i32]),
 }

@@ -11,7 +11,7 @@ Layouts (see include/cpattn.h):
 """
 
 from dataclasses import dataclass
-from typing import List, Sequence
+from typing import List, Optional, Sequence
 
 import ctypes
 import math
@@ -715,3 +715,277 @@ def cp_select_pass_cost(new_tokens: int, cached_tokens: int, Hq: int, Hkv: int, 
     if r < 0:
         L.check(r, "cp_select_pass_cost")
     return ("pass_q" if r == L.PASS_Q else "pass_kv"), ekv.value, eq.value
+
+
+# --------------------------------------------------------- quantised KV cache --
+@dataclass
+class KVCache:
+    """Quantised KV rows (see cp_kv_codes_t in cpattn.h): codes float8_e4m3fn
+    [rows, Hkv, d | dv] (last dim contiguous) and their scales fp32 [Hkv, rows]
+    (last dim contiguous).  ``v`` is None where V is part of K (absorbed MLA)."""
+    k: torch.Tensor
+    k_scale: torch.Tensor
+    v: Optional[torch.Tensor] = None
+    v_scale: Optional[torch.Tensor] = None
+
+    @property
+    def rows(self):
+        return self.k.shape[0]
+
+
+def alloc_kv_cache(rows, Hkv, d, dv=None, device="cuda") -> KVCache:
+    """A cache of ``rows`` zero rows; ``dv`` None: K alone."""
+    def side(dim):
+        return (torch.zeros((rows, Hkv, dim), dtype=torch.uint8,
+                            device=device).view(torch.float8_e4m3fn),
+                torch.ones((Hkv, rows), dtype=torch.float32, device=device))
+    k, ks = side(d)
+    v, vs = side(dv) if dv is not None else (None, None)
+    return KVCache(k, ks, v, vs)
+
+
+def _check_codes(codes, scales, name, ref, rows, Hkv):
+    _dev(codes, name, torch.float8_e4m3fn, ref, contiguous=False)
+    _dev(scales, name + "_scale", torch.float32, ref, contiguous=False)
+    if codes.dim() != 3 or codes.shape[0] != rows or codes.shape[1] != Hkv or \
+            (codes.numel() and codes.stride(2) != 1):
+        raise ValueError(f"{name} must be [{rows}, {Hkv}, dim] with a contiguous last dim")
+    if tuple(scales.shape) != (Hkv, rows) or (scales.numel() and scales.stride(1) != 1):
+        raise ValueError(f"{name}_scale must be [{Hkv}, {rows}] with a contiguous last dim")
+
+
+def _codes(codes, scales):
+    # a tensor of one row or head may carry any stride for that dim
+    rows, Hkv, dim = codes.shape
+    hs = codes.stride(1) if Hkv > 1 else dim
+    rs = codes.stride(0) if rows > 1 else (Hkv - 1) * hs + dim
+    ss = scales.stride(0) if Hkv > 1 else max(scales.stride(0), rows)
+    return L.KvCodes(codes.data_ptr(), scales.data_ptr(), rs, hs, ss)
+
+
+def _cache_sides(cache, ref=None):
+    rows, Hkv = cache.k.shape[0], cache.k.shape[1]
+    if cache.k.dim() != 3:
+        raise ValueError("cache.k must be [rows, Hkv, d]")
+    if (cache.v is None) != (cache.v_scale is None):
+        raise ValueError("cache.v and cache.v_scale go together")
+    _check_codes(cache.k, cache.k_scale, "cache.k", ref, rows, Hkv)
+    if cache.v is not None:
+        _check_codes(cache.v, cache.v_scale, "cache.v", cache.k, rows, Hkv)
+    return (_codes(cache.k, cache.k_scale),
+            None if cache.v is None else _codes(cache.v, cache.v_scale))
+
+
+def cp_kv_quantize(cache: KVCache, k, v=None, slots=None, *, status=None, stream=None) -> KVCache:
+    """Quantise new rows into the cache (see cp_kv_quantize in cpattn.h).
+
+    k [n, Hkv, d] and v [n, Hkv, dv]: bf16 or fp32 (the same), last dim
+    contiguous.  ``slots``: int32 [n], the cache row of each new row (negative:
+    skipped); without it row i goes to cache row i.
+    """
+    lib = L.load()
+    kc, vc = _cache_sides(cache)
+    if (v is None) != (cache.v is None):
+        raise ValueError("v goes with a cache that has V")
+    for x, c, name in ((k, cache.k, "k"), (v, cache.v, "v")):
+        if x is None and name == "v":
+            continue
+        _dev(x, name, (torch.bfloat16, torch.float32), cache.k, contiguous=False)
+        if x.dtype != k.dtype:
+            raise TypeError("k and v must have one dtype")
+        if x.dim() != 3 or x.shape[0] != k.shape[0] or tuple(x.shape[1:]) != tuple(c.shape[1:]):
+            raise ValueError(f"{name} must be [n, {c.shape[1]}, {c.shape[2]}]")
+        if x.numel() and x.stride(2) != 1:
+            raise ValueError(f"{name} needs a contiguous last dim")
+    n = k.shape[0]
+    if slots is not None:
+        _dev(slots, "slots", torch.int32, cache.k)
+        if slots.dim() != 1 or slots.shape[0] < n:
+            raise ValueError("slots must be int32 with one entry per row")
+    _status(status, cache.k)
+    vx = k if v is None else v
+    with torch.cuda.device(cache.k.device):
+        L.check(lib.cp_kv_quantize(
+            _p(k), k.stride(0), k.stride(1), _p(v), vx.stride(0), vx.stride(1),
+            1 if k.dtype == torch.float32 else 0, n, k.shape[1], k.shape[2], vx.shape[2],
+            _p(slots), kc, vc, cache.rows, _p(status), _stream(stream)), "cp_kv_quantize")
+    return cache
+
+
+def cp_kv_dequantize(cache: KVCache, idx=None, *, out_k=None, out_v=None, out_fp32=False,
+                     status=None, stream=None):
+    """Read cache rows back: out[i] = value of cache row idx[i] (without ``idx``:
+    of row i), bf16 or fp32 (see cp_kv_dequantize in cpattn.h).  A negative
+    index leaves its output row as it is.  Returns (k [n, Hkv, d], v [n, Hkv,
+    dv] or None)."""
+    lib = L.load()
+    kc, vc = _cache_sides(cache)
+    n = cache.rows
+    if idx is not None:
+        _dev(idx, "idx", torch.int32, cache.k)
+        if idx.dim() != 1:
+            raise ValueError("idx must be a 1-D int32 index")
+        n = idx.shape[0]
+    dtype = torch.float32 if out_fp32 else torch.bfloat16
+    if out_k is None:
+        out_k = torch.empty((n,) + tuple(cache.k.shape[1:]), dtype=dtype, device=cache.k.device)
+    if out_v is not None and cache.v is None:
+        raise ValueError("out_v goes with a cache that has V")
+    if out_v is None and cache.v is not None:
+        out_v = torch.empty((n,) + tuple(cache.v.shape[1:]), dtype=out_k.dtype,
+                            device=cache.k.device)
+    for out, c, name in ((out_k, cache.k, "out_k"), (out_v, cache.v, "out_v")):
+        if out is None:
+            continue
+        _dev(out, name, (torch.bfloat16, torch.float32), cache.k)
+        if out.dtype != out_k.dtype:
+            raise TypeError("out_k and out_v must have one dtype")
+        _shape(out, name, (n,) + tuple(c.shape[1:]))
+    _status(status, cache.k)
+    with torch.cuda.device(cache.k.device):
+        L.check(lib.cp_kv_dequantize(
+            kc, vc, cache.rows, cache.k.shape[1], cache.k.shape[2],
+            0 if cache.v is None else cache.v.shape[2], _p(idx), n, _p(out_k), _p(out_v),
+            1 if out_k.dtype == torch.float32 else 0, _p(status), _stream(stream)),
+            "cp_kv_dequantize")
+    return out_k, out_v
+
+
+# ----------------------------------------------------------- shared prefix --
+@dataclass
+class SharedPlan:
+    """The plan of cp_attn_shared for one set of lengths (see cpattn.h)."""
+    info: L.SharedPlanInfo
+    table: torch.Tensor          # int32 [table_ints], device
+    segs_host: torch.Tensor      # int32 [S, 8], host: the segments it was made from
+
+    @property
+    def num_q_rows(self):
+        return self.info.num_q_rows
+
+
+def shared_segments(q_lens, own_lens, prefix_len, *, prefix_row0=0, own_row0=None):
+    """Host segment table (int32 [S, 8]) of a batch behind one shared prefix.
+
+    Request b has q_lens[b] query rows (in request order) and own_lens[b] own
+    keys, its query rows' keys the last of them; they lie at KV rows own_row0[b]
+    ..  (default: all requests' own keys in order behind the prefix).  Query
+    row i of the request sees the prefix and its own keys 0 .. own_lens[b] -
+    q_lens[b] + i.  The prefix lies at KV rows prefix_row0 ..
+    """
+    q_lens, own_lens = [int(x) for x in q_lens], [int(x) for x in own_lens]
+    if len(q_lens) != len(own_lens):
+        raise ValueError("q_lens and own_lens differ in length")
+    if min(q_lens + own_lens + [int(prefix_len)]) < 0:
+        raise ValueError("lengths must not be negative")
+    N = sum(q_lens)
+    segs = []
+    if N > 0 and prefix_len > 0:
+        segs.append((0, N, prefix_len - 1, 0, prefix_row0, prefix_len, 0, -1))
+    row, at = 0, prefix_row0 + prefix_len
+    if own_row0 is not None and len(own_row0) != len(q_lens):
+        raise ValueError("own_row0 needs one row per request")
+    for b, (n, kv) in enumerate(zip(q_lens, own_lens)):
+        if n > 0:
+            segs.append((row, n, kv - n, 1, at if own_row0 is None else int(own_row0[b]), kv, row,
+                         b))
+        row += n
+        at += kv
+    return torch.tensor(segs, dtype=torch.int32).reshape(-1, 8)
+
+
+def make_shared_plan_segs(segs_host, num_q_rows, Hq, Hkv, *, num_ctas=None,
+                          device="cuda") -> SharedPlan:
+    """The plan for an explicit host segment table (int32 [S, 8])."""
+    lib = L.load()
+    sh = torch.as_tensor(segs_host, dtype=torch.int32).contiguous()
+    if sh.dim() != 2 or sh.shape[1] != 8 or sh.is_cuda:
+        raise ValueError("segs_host must be a host int32 [S, 8] table (cp_segment_t rows)")
+    if num_ctas is None:
+        num_ctas = torch.cuda.get_device_properties(device).multi_processor_count
+    info = L.SharedPlanInfo()
+    L.check(lib.cp_shared_plan_size(ctypes.c_void_p(sh.data_ptr()), sh.shape[0], int(num_q_rows),
+                                    int(Hq), int(Hkv), int(num_ctas), ctypes.byref(info)),
+            "cp_shared_plan_size")
+    table = torch.empty(info.table_ints, dtype=torch.int32)
+    L.check(lib.cp_shared_plan(ctypes.c_void_p(sh.data_ptr()), sh.shape[0], ctypes.byref(info),
+                               ctypes.c_void_p(table.data_ptr())), "cp_shared_plan")
+    return SharedPlan(info=info, table=table.to(device), segs_host=sh)
+
+
+def make_shared_plan(q_lens, own_lens, prefix_len, Hq, Hkv, *, prefix_row0=0, own_row0=None,
+                     num_ctas=None, device="cuda") -> SharedPlan:
+    """The plan of a batch behind one shared prefix (see shared_segments); it
+    depends on the lengths alone and serves every layer of a step."""
+    segs = shared_segments(q_lens, own_lens, prefix_len, prefix_row0=prefix_row0,
+                           own_row0=own_row0)
+    return make_shared_plan_segs(segs, sum(int(x) for x in q_lens), Hq, Hkv, num_ctas=num_ctas,
+                                 device=device)
+
+
+def cp_shared_workspace_size(plan: SharedPlan, dv) -> int:
+    """Workspace bytes of cp_attn_shared for this plan."""
+    nbytes = ctypes.c_int64()
+    L.check(L.load().cp_shared_workspace_size(ctypes.byref(plan.info), int(dv),
+                                              ctypes.byref(nbytes)), "cp_shared_workspace_size")
+    return nbytes.value
+
+
+def alloc_shared_workspace(plan: SharedPlan, dv) -> torch.Tensor:
+    return torch.empty(cp_shared_workspace_size(plan, dv), dtype=torch.uint8,
+                       device=plan.table.device)
+
+
+def cp_attn_shared(plan: SharedPlan, q, k, v, scale, *, k_scale=None, v_scale=None, out=None,
+                   lse=None, out_fp32=False, workspace=None, status=None, stream=None):
+    """Attention of a batch that shares keys (see cp_attn_shared in cpattn.h).
+
+    q bf16 [N, Hq, d]; k, v bf16 [kv_rows, Hkv, d], or with ``k_scale`` and
+    ``v_scale`` the float8_e4m3fn codes of a KVCache.  Rows of no segment are
+    left as they are in ``out`` and ``lse`` (and are undefined in new ones).
+    ``workspace``: alloc_shared_workspace(plan, dv), allocated when omitted.
+    Returns (O [N, Hq, dv], LSE [N, Hq], workspace).
+    """
+    lib = L.load()
+    info = plan.info
+    _dev(q, "q", torch.bfloat16, plan.table, contiguous=False)
+    quant = k_scale is not None
+    if quant != (v_scale is not None):
+        raise ValueError("k_scale and v_scale go together")
+    kv_dtype = torch.float8_e4m3fn if quant else torch.bfloat16
+    _dev(k, "k", kv_dtype, q, contiguous=False)
+    _dev(v, "v", kv_dtype, q, contiguous=False)
+    if q.dim() != 3 or k.dim() != 3 or v.dim() != 3:
+        raise ValueError("q, k and v are [rows, heads, dim]")
+    N, Hq, d = q.shape
+    rows, Hkv, dv = v.shape
+    if k.shape[0] != rows or k.shape[1] != Hkv or k.shape[2] != d:
+        raise ValueError("k and v disagree on rows or heads, or k and q on the head dim")
+    if (N, Hq, Hkv) != (info.num_q_rows, info.Hq, info.Hkv):
+        raise ValueError(f"the plan is for {info.num_q_rows} query rows, {info.Hq} / {info.Hkv} "
+                         f"heads; got {N}, {Hq} / {Hkv}")
+    if (N and q.stride(2) != 1) or (rows and (k.stride(2) != 1 or v.stride(2) != 1)):
+        raise ValueError("q, k and v need a contiguous last dim")
+    kc, vc = _codes(k, k_scale if quant else k), _codes(v, v_scale if quant else v)
+    scale_stride = 0
+    if quant:
+        _check_codes(k, k_scale, "k", q, rows, Hkv)
+        _check_codes(v, v_scale, "v", q, rows, Hkv)
+        scale_stride = kc.scale_stride
+        if vc.scale_stride != scale_stride:
+            raise ValueError("k_scale and v_scale must have one row stride")
+    out, lse = _attn_outputs(out, lse, N, Hq, dv, out_fp32, q)
+    if out.shape[0] != N:
+        raise ValueError("out needs one row per query row")
+    if workspace is None:
+        workspace = alloc_shared_workspace(plan, dv)
+    _dev(workspace, "workspace", torch.uint8, q)
+    _status(status, q)
+    with torch.cuda.device(q.device):
+        L.check(lib.cp_attn_shared(
+            info, _p(plan.table), _p(q), q.stride(0) if N > 1 else Hq * d,
+            q.stride(1) if Hq > 1 else d, _p(k), kc.row_stride, kc.head_stride, _p(k_scale), _p(v),
+            vc.row_stride, vc.head_stride, _p(v_scale), scale_stride, rows, d, dv, float(scale),
+            _p(out), 1 if out.dtype == torch.float32 else 0, _p(lse), _p(workspace),
+            workspace.numel(), _p(status), _stream(stream)), "cp_attn_shared")
+    return out, lse, workspace

@@ -517,6 +517,134 @@ int cp_restore(const void* src, int num_src_rows, const int32_t* idx_dev, int ro
                int64_t row_bytes, void* dst, int32_t* status_dev, cudaStream_t stream);
 
 /* ------------------------------------------------------------------------ */
+/* Quantised KV cache: rows of 8-bit floating-point codes (e4m3) with one
+ * power-of-two scale per row and KV head.  (No counterpart on the source
+ * pages; the cached prefix of [SGL-ZZ] held in half the bytes.)
+ *
+ * For the vector x[0..dim) of one row and one head:
+ *     a = max over the finite x_c of |x_c|
+ *     e = clamp(ceil(log2(a / 448)), -117, 119)         (a = 0: e = -117)
+ *     scale = 2^e,  code_c = e4m3(x_c / scale)
+ * rounded to nearest even and saturated at +-448 (infinities among them; a NaN
+ * stays a NaN).  The code stands for code_c * scale, which is exact in bf16
+ * and fp32: the division by a power of two rounds nothing, the smallest
+ * non-zero code gives 2^-126 and the largest 448 * 2^119, so reading a row back
+ * (or feeding it to the tensor cores as bf16) adds no second rounding.
+ *
+ * cp_kv_codes_t: one of K and V.  Row r, head h, column c has its code at
+ * codes[r*row_stride + h*head_stride + c] (strides in bytes, multiples of 16,
+ * heads and rows not overlapping; codes 16-byte aligned) and its scale at
+ * scales[h*scale_stride + r] (4-byte aligned, scale_stride >= the cache's
+ * rows): a run of rows has its scales in consecutive words. */
+typedef struct {
+  void* codes;
+  float* scales;
+  int64_t row_stride, head_stride, scale_stride;
+} cp_kv_codes_t;
+
+/* Quantise num_rows new rows of K (and V) into cache rows.
+ *   k: bf16 or fp32 (x_is_fp32) rows; element (row, head, c) at
+ *     k[row*k_row_stride + head*k_head_stride + c] (strides in elements,
+ *     multiples of 16 bytes, >= 0).  v likewise; v and v_cache NULL: K alone (the
+ *     latent rows of absorbed MLA, whose V is part of K).
+ *   d, dv: multiples of 16, at most 1024 (dv ignored without v).
+ *   slots: device int32 [num_rows], the cache row of each new row, or NULL (row
+ *     i).  A negative slot is padding: its row is skipped.  A slot at or past
+ *     cache_rows sets CPATTN_ERR_RANGE and is skipped.  The non-negative slots
+ *     must differ: a cache row named twice ends with codes and scales of either.
+ * Rows of the cache that no slot names are not touched. */
+int cp_kv_quantize(const void* k, int64_t k_row_stride, int64_t k_head_stride, const void* v,
+                   int64_t v_row_stride, int64_t v_head_stride, int x_is_fp32, int num_rows,
+                   int Hkv, int d, int dv, const int32_t* slots, const cp_kv_codes_t* k_cache,
+                   const cp_kv_codes_t* v_cache, int cache_rows, int32_t* status_dev,
+                   cudaStream_t stream);
+
+/* Read cache rows back: row i of k_out [num_rows, Hkv, d] (and v_out [num_rows,
+ * Hkv, dv]), contiguous bf16 or fp32 (out_is_fp32), is the value of cache row
+ * idx[i] (idx NULL: row i).  With idx naming a request's cached rows in key
+ * order this makes the gathered KV buffer of cp_attn_partial.  A negative index
+ * leaves its output row as it is; one at or past cache_rows also sets
+ * CPATTN_ERR_RANGE.  An index may be named any number of times.  v_cache and
+ * v_out NULL: K alone. */
+int cp_kv_dequantize(const cp_kv_codes_t* k_cache, const cp_kv_codes_t* v_cache, int cache_rows,
+                     int Hkv, int d, int dv, const int32_t* idx, int num_rows, void* k_out,
+                     void* v_out, int out_is_fp32, int32_t* status_dev, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* Attention for a batch that shares keys: a prefix common to many requests is
+ * read once for all of their queries and heads, each request's own keys behind
+ * it once for its own, and the partial results are merged.  [CPB-3.3],
+ * [CPB-3.6] (the partials and their merge; the shared prefix itself has no
+ * counterpart on the source pages)
+ *
+ * A host table of segments (cp_segment_t) says which query rows see which key
+ * runs.  Row i of a segment (query row q_row0 + i) has position q_pos0 +
+ * i*q_pos_step within the segment's key run and sees its keys 0 .. position (KV
+ * rows kv_row0 + key); a negative position sees none.  kv_len >= the last row's
+ * position + 1 and >= 0; q_pos_step >= 0; tok0 and req are not used.  Segments
+ * may share query rows: a row attends to the union of the runs of all the
+ * segments that hold it (a key that two of them give is counted twice).  A
+ * shared prefix of P keys is one segment over all rows of the batch with q_pos0
+ * = P - 1 and step 0; a request's own keys are one with step 1 whose last
+ * position is its last own key.  Nested prefixes are further segments.
+ *     L = ln(sum over the row's keys of exp(S_k)),  O = sum exp(S_k - L) V_k,
+ * S_k as in cp_attn_partial; a row whose segments give it no key has O = 0 and
+ * L = -inf.  Rows of no segment are left as they are in o and lse.
+ *
+ * The plan (host only) packs the query heads of a KV head and the rows that see
+ * the same run into tiles of up to CPATTN_SHARED_ROWS rows (row i, head j of the
+ * group at i*(Hq/Hkv) + j), and cuts the (tile, KV head, keys) work into
+ * num_ctas shares of about equal cost, each a list of pieces.  It depends on the
+ * lengths alone: one plan serves every layer of a step.
+ *   num_ctas in [1, 4096]: thread blocks of the launch (the device's SM count).
+ *   Hq % Hkv == 0; num_segs and the tiles times Hkv up to 2^22, query rows, KV
+ *   rows and partial rows below 2^31 (CPATTN_ERR_TOO_LARGE).
+ * cp_shared_plan_size fills *plan; cp_shared_plan then writes plan->table_ints
+ * words to table (host), which the caller copies to the device. */
+#define CPATTN_SHARED_ROWS 256
+typedef struct {
+  int32_t num_q_rows, Hq, Hkv, num_ctas;
+  int32_t num_units, num_pieces, num_entries;
+  int32_t kv_rows;     /* KV rows that the segments reach */
+  int32_t needs_merge; /* some row has more than one partial, or none */
+  int32_t budget;      /* cost of the largest share */
+  int64_t ws_rows;     /* partial rows in the workspace */
+  int64_t table_ints;  /* size of the table, int32 words */
+} cp_shared_plan_t;
+int cp_shared_plan_size(const cp_segment_t* segs_host, int num_segs, int num_q_rows, int Hq,
+                        int Hkv, int num_ctas, cp_shared_plan_t* plan);
+int cp_shared_plan(const cp_segment_t* segs_host, int num_segs, const cp_shared_plan_t* plan,
+                   int32_t* table);
+/* Workspace bytes of cp_attn_shared for this plan (at least 16). */
+int cp_shared_workspace_size(const cp_shared_plan_t* plan, int dv, int64_t* bytes);
+
+/* The attention.
+ *   plan: host; table_dev: its table on the device (16-byte aligned).
+ *   q: bf16, element (row, head, c) at q[row*q_row_stride + head*q_head_stride +
+ *     c], num_q_rows rows (strides in elements, multiples of 16 bytes, >= 0).
+ *   k, v: with k_scales NULL, bf16 rows as in cp_attn_partial.  Otherwise e4m3
+ *     codes with the strides in bytes and the scales of cp_kv_codes_t (k_scales,
+ *     v_scales; one scale_stride for both).  (d, dv): (64, 64) and (128, 128).
+ *     Key and value rows outside the segments' runs, or past num_kv_rows, may hold
+ *     anything; a value row that some row of a tile sees must be finite for the
+ *     others.
+ *   o: [num_q_rows, Hq, dv] contiguous, bf16 or fp32; lse: fp32 [num_q_rows, Hq].
+ *   workspace: device, 16-byte aligned, at least cp_shared_workspace_size bytes;
+ *     overwritten; not to be shared by calls that may run at the same time.
+ * P is rounded to bf16 for the second product, as in cp_attn_partial.  One or two
+ * launches (the merge only where plan->needs_merge), no order of atomics: the
+ * same call gives the same bits.  num_kv_rows < plan->kv_rows:
+ * CPATTN_ERR_INVALID_ARG.  A table that does not match the plan sets
+ * CPATTN_ERR_RANGE and what it spoils is skipped. */
+int cp_attn_shared(const cp_shared_plan_t* plan, const int32_t* table_dev, const void* q,
+                   int64_t q_row_stride, int64_t q_head_stride, const void* k,
+                   int64_t k_row_stride, int64_t k_head_stride, const float* k_scales,
+                   const void* v, int64_t v_row_stride, int64_t v_head_stride,
+                   const float* v_scales, int64_t scale_stride, int num_kv_rows, int d, int dv,
+                   float scale, void* o, int o_is_fp32, float* lse, void* workspace,
+                   int64_t workspace_bytes, int32_t* status_dev, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------ */
 /* Test hook for the failure path of the attention pipeline (no counterpart on
  * the source pages).  Process-wide; affects launches made after the call.
  *   CPATTN_DEBUG_WAIT_LIMIT_NS: time limit of every mbarrier wait inside the
