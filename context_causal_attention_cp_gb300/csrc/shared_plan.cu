@@ -16,9 +16,14 @@
 namespace cpattn {
 namespace {
 
-constexpr int kKeys = 128;          // keys of one KV tile
-constexpr int kTileCost = 16;       // one KV tile
+constexpr int kKeys = kSharedTileKeys;
+constexpr int kTileCost = 16;       // one KV tile for one MMA tile of rows
+constexpr int kDualCost = 24;       // one KV tile for two
 constexpr int kPieceCost = 16;      // a piece's fixed part
+constexpr int tile_cost(int rows) { return shared_dual(rows) ? kDualCost : kTileCost; }
+// partial rows that a piece leaves
+constexpr bool split(int rows, long long keys) { return !shared_dual(rows) && keys > kKeys; }
+constexpr int parts(int rows, long long keys) { return split(rows, keys) ? 2 * rows : rows; }
 constexpr long long kMaxUnits = 1LL << 22;
 
 long long last_pos(const cp_segment_t& s) {
@@ -56,7 +61,7 @@ int deal(const cp_segment_t* segs, int num_segs, int g, int Hkv, long long budge
       long long key0 = 0;
       while (key0 < keys) {
         const long long tiles = (keys - key0 + kKeys - 1) / kKeys;
-        long long fit = (budget - used - kPieceCost) / kTileCost;
+        long long fit = (budget - used - kPieceCost) / tile_cost(rows);
         if (fit < 1) {
           if (++cta >= max_ctas) {
             full = true;
@@ -69,7 +74,7 @@ int deal(const cp_segment_t* segs, int num_segs, int g, int Hkv, long long budge
         const long long n = std::min(keys - key0, fit * kKeys);
         f(cta, s, r0, rows, h, key0, n);
         key0 += n;
-        used += kPieceCost + fit * kTileCost;
+        used += kPieceCost + fit * tile_cost(rows);
       }
     }
   });
@@ -117,16 +122,13 @@ extern "C" int cp_shared_plan_size(const cp_segment_t* segs, int num_segs, int n
       kv_rows = std::max(kv_rows, s.kv_row0 + std::max<long long>(0, last_pos(s) + 1));
   }
   if (tiles * Hkv > kMaxUnits || entries > 0x3fffffffLL) return CPATTN_ERR_TOO_LARGE;
-  long long cost = 0, most = 0;
-  for_each_tile(segs, num_segs, g, [&](const cp_segment_t&, long long, int, long long keys) {
-    if (keys == 0) return;
-    const long long c = kPieceCost + (keys + kKeys - 1) / kKeys * kTileCost;
-    cost += c * Hkv;
-    most = std::max(most, c);
+  long long cost = 0;
+  for_each_tile(segs, num_segs, g, [&](const cp_segment_t&, long long, int rows, long long keys) {
+    if (keys > 0) cost += (kPieceCost + (keys + kKeys - 1) / kKeys * tile_cost(rows)) * Hkv;
   });
   // one block more than the average needs at most: the average, a whole piece
   // and a cut on either side
-  long long lo = kPieceCost + kTileCost, hi = cost / num_ctas + 2 * (kPieceCost + kTileCost);
+  long long lo = kPieceCost + kTileCost, hi = cost / num_ctas + 2 * (kPieceCost + kDualCost);
   auto none = [](auto&&...) {};
   while (deal(segs, num_segs, g, Hkv, hi, num_ctas, none, none) > num_ctas) hi *= 2;
   while (lo < hi) {
@@ -137,9 +139,9 @@ extern "C" int cp_shared_plan_size(const cp_segment_t* segs, int num_segs, int n
   if (hi > 0x7fffffffLL) return CPATTN_ERR_TOO_LARGE;
   long long pieces = 0, ws_rows = 0;
   deal(segs, num_segs, g, Hkv, hi, num_ctas, none,
-       [&](int, const cp_segment_t&, long long, int rows, int, long long, long long) {
+       [&](int, const cp_segment_t&, long long, int rows, int, long long, long long keys) {
          ++pieces;
-         ws_rows += rows;
+         ws_rows += parts(rows, keys);
        });
   if (ws_rows > 0x7fffffffLL || pieces > 0x7fffffffLL) return CPATTN_ERR_TOO_LARGE;
   plan->num_q_rows = num_q_rows;
@@ -180,9 +182,9 @@ extern "C" int cp_shared_plan(const cp_segment_t* segs, int num_segs, const cp_s
   auto none = [](auto&&...) {};
   const int used =
       deal(segs, num_segs, g, Hkv, plan->budget, plan->num_ctas, none,
-           [&](int, const cp_segment_t&, long long, int rows, int, long long, long long) {
+           [&](int, const cp_segment_t&, long long, int rows, int, long long, long long keys) {
              ++np;
-             ws += rows;
+             ws += parts(rows, keys);
            });
   if (used > plan->num_ctas || np != plan->num_pieces || ws != plan->ws_rows)
     return CPATTN_ERR_INVALID_ARG;
@@ -223,7 +225,8 @@ extern "C" int cp_shared_plan(const cp_segment_t* segs, int num_segs, const cp_s
          p.key0 = (int32_t)key0;
          p.keys = (int32_t)keys;
          p.ws_row = ws_row;
-         ws_row += rows;
+         p.flags = split(rows, keys) ? kPieceSplit : 0;
+         ws_row += parts(rows, keys);
          pieces[piece++] = p;
        });
   unit_first[unit] = piece;

@@ -27,11 +27,19 @@ struct SharedPiece {
   int32_t key0;      // its key number within the segment's run
   int32_t keys;      // keys of the piece, >= 1
   int32_t ws_row;    // first partial row in the workspace
-  int32_t flags;     // kPieceDirect: the unit's only partial, written to o and lse
+  int32_t flags;     // kPieceSplit: two partials, the second at ws_row + rows
   int32_t unused;
 };
 static_assert(sizeof(SharedPiece) == 48, "three 16-byte words");
-constexpr int kPieceDirect = 1;
+constexpr int kPieceSplit = 2;
+constexpr int kSharedTileRows = 128;  // packed rows of one MMA tile
+constexpr int kSharedTileKeys = 128;  // keys of one KV tile
+
+// A unit of more than kSharedTileRows rows is two MMA tiles that use every KV
+// tile (dual).  A smaller one is a single MMA tile whose KV tiles are dealt
+// alternately to the two softmax warpgroups; each keeps its own sum, so a piece
+// of two or more KV tiles leaves two partials (split).
+__host__ __device__ __forceinline__ bool shared_dual(int rows) { return rows > kSharedTileRows; }
 
 struct SharedTable {
   long long unit_first, row_first, entries, pieces, total;  // word offsets (cta_first at 0)
