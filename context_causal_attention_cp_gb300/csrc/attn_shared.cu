@@ -8,22 +8,31 @@
 // in fp32; the merge combines a row's partials by the log-sum-exp rule
 //     m = max L_j, w_j = exp(L_j - m), O = sum w_j O_j / sum w_j, L = m + ln sum w_j.
 //
-// attn_shared_kernel: one resident block per SM walks its pieces; its loads run
-// ahead across piece ends.
+// attn_shared_kernel: one resident block per SM walks its pieces; its loads, its
+// MMAs and its queries run ahead across piece ends.
 //   warps 0-7    two softmax warpgroups (streams), one row per thread: query rows
 //                to shared memory (any group size, any stride), S from TMEM, online
-//                softmax in base 2 with a lazily moved maximum, P back to TMEM as
-//                bf16, the partial to the workspace.
-//   warp 8       TMA producer: K and V tiles of 128 keys, in the order of use,
-//                through one ring.
-//   warp 9       MMA issuer: S = Q K^T and O += P V (tcgen05), the two streams in
-//                turn, so that one stream's softmax runs under the other's MMAs.
-//   warp 10      zeroes the V rows behind a piece's last key (0 * NaN is NaN, so
-//                masking P alone would not keep stale rows out).
-//   warps 12-15  (e4m3 cache) codes to bf16 tiles, exactly: code * 2^e has 4
-//                significant bits.  Rows behind the last key become zeros there.
-// A unit of two MMA tiles (dual) gives both streams every KV tile; a smaller
-// unit deals its KV tiles alternately to the streams, each with its own sums.
+//                softmax in base 2 with a lazily moved maximum, P back to TMEM in 16
+//                bits, the partial to the workspace.
+//   warp 8       producer: K and V tiles of 128 keys by TMA, in the order of use,
+//                through one ring; of a run's last tile only the rows it has.
+//   warps 9, 10  MMA issuers, one per stream: S = Q K^T and O += P V (tcgen05); one
+//                stream's softmax runs under the other's MMAs.  Two, because one
+//                thread's issue of both streams took 2300 cycles a step against 1270
+//                of tensor work.
+//   warps 12-15  (e4m3 cache) codes to f16 tiles.
+// A unit of two MMA tiles (dual) gives both streams every KV tile; the pieces of
+// smaller units belong to one stream each, and the streams' KV tiles alternate.
+//
+// e4m3 cache: both products run in f16, which holds a code exactly and takes two
+// instructions for two codes (bf16 takes 6.5, more than a step has issue slots
+// for).  K row r enters as code * 2^(e_r - E), E the tile's largest e, and 2^E goes
+// into the scores' factor: what a row far below the tile's largest loses is below
+// 2^-33 of that largest, less than an fp32 score resolves.  V the same with E the
+// largest e that the stream has met in the piece; O is rescaled when that grows.  A
+// query row enters as f16 times the power of two that brings its largest element to
+// [2^14, 2^15), so that elements down to 2^-30 of it keep bf16's 8 bits.  P in f16 is
+// off by 2^-12 of a weight (bf16: 2^-9).
 #include <algorithm>
 #include <cstdint>
 
@@ -38,11 +47,13 @@ namespace {
 
 constexpr int kRows = CPATTN_SHARED_ROWS;
 constexpr int BN = kSharedTileKeys;
-constexpr int kConvertWarp = 12;  // first of the four that decode e4m3 tiles
+constexpr int kTailRows = 16;                   // box rows of the loads of a run's last tile
+constexpr int kProducerWarp = 8, kMmaWarp = 9;  // MMA: 9 and 10
+constexpr int kConvertWarp = 12;                // to 15
 
 struct SharedParams {
   const int32_t* table;
-  long long unit_first, row_first, entries, pieces;  // word offsets
+  long long pieces, units, row_first, entries;  // word offsets
   int num_units, num_pieces, num_entries, num_q_rows, Hq, Hkv, g;
   long long ws_rows;
   const __nv_bfloat16* q;
@@ -68,119 +79,305 @@ struct SharedCfg {
   static constexpr int kRegsSoftmax = 200, kRegsOther = QUANT ? 56 : 104;
   static_assert(kRegsSoftmax * 256 + kRegsOther * (kThreads - 256) <= kRegsLaunch * kThreads,
                 "register split exceeds the launch allocation");
-  static constexpr int kProducerWarp = 8, kMmaWarp = 9, kFixWarp = 10;
   static constexpr int kQTile = BM * D * 2;
-  static constexpr int kTile = BN * D * 2;     // a bf16 K or V tile
-  static constexpr int kRawTile = BN * D;      // an e4m3 K or V tile
+  static constexpr int kTile = BN * D * 2;  // a K or V tile of 16-bit elements
+  static constexpr int kRawTile = BN * D;   // an e4m3 K or V tile
   // 227 KB hold five tiles of 32 KB beside the queries, or three and four of codes
   static constexpr int kStages = QUANT ? 3 : 5;
   static constexpr int kRawStages = QUANT ? 4 : 0;
   static constexpr int kRingOff = 2 * kQTile;
   static constexpr int kRawOff = kRingOff + kStages * kTile;
-  static constexpr int kBarOff = kRawOff + kRawStages * kRawTile;
-  static constexpr int kNumBars = 2 * kStages + 2 * kRawStages + 8 + 3;
-  static constexpr int kSmemBytes = kBarOff + kNumBars * 8 + 16 + 1024;  // + align slack
-  static_assert(kSmemBytes <= 232448, "shared memory budget");
+  static constexpr int kMulOff = kRawOff + kRawStages * kRawTile;  // f16 factor of each raw row
+  static constexpr int kNoteOff = kMulOff + kRawStages * BN * 2;   // RawNote of each raw tile
+  static constexpr int kExpOff = kNoteOff + kRawStages * 16;       // exponents, see RawNote::which
+  static constexpr int kBarOff = kExpOff + 48;
+  static constexpr int kNumBars = 4 * kStages + 2 * kRawStages + 8 + 2;
+  static constexpr int kWordOff = kBarOff + kNumBars * 8;  // TMEM slot, abort, loads, phases, tiles[2]
+  static constexpr int kSmemBytes = kWordOff + 32 + 1024;  // + align slack
+  static_assert(kBarOff % 8 == 0 && kSmemBytes <= 232448, "shared memory budget");
   static constexpr int kTmemCols = 512;  // S of each stream, then O of each
 };
 
-// A piece of the table, checked against the buffers; false (and
-// CPATTN_ERR_RANGE) when it does not fit them.  Every warp of the block reads
-// the same words and decides the same.
-__device__ __forceinline__ bool load_piece(const SharedParams& p, int i, SharedPiece& pc) {
+// What the producer tells the converters about a raw tile.
+struct RawNote {
+  static constexpr int kNoteV = 8;
+  int live;     // rows up to the run's end
+  int which;    // RingTile::which, | kNoteV of a V tile
+  int ek, ev;   // of a K tile: E of it, and E of its V tile
+};
+
+// Bounded waits, of one thread and of a whole warp (uniform).  They read the timer
+// only after a few hundred polls: it is far from the SM, and a read at every wait
+// that does not succeed at once costs more than the wait.
+constexpr uint32_t kPollsPerCheck = 256;
+__device__ __forceinline__ bool give_up(uint64_t& t0, const volatile int* abort, uint64_t timeout) {
+  const uint64_t now = global_timer_ns();
+  if (t0 == 0) t0 = now;
+  return (abort && *abort != 0) || now - t0 > timeout;
+}
+__device__ __forceinline__ bool wait_one(uint64_t* bar, uint32_t parity, const volatile int* abort,
+                                         uint64_t timeout) {
+  uint64_t t0 = 0;
+  for (uint32_t i = 1; !mbar_try_wait(bar, parity); ++i)
+    if (i % kPollsPerCheck == 0 && give_up(t0, abort, timeout)) return false;
+  return true;
+}
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, const volatile int* abort,
+                                          uint64_t timeout) {
+  uint64_t t0 = 0;
+  for (uint32_t i = 1; !__all_sync(0xffffffffu, mbar_try_wait(bar, parity)); ++i)
+    if (i % kPollsPerCheck == 0 &&
+        __shfl_sync(0xffffffffu, (int)give_up(t0, abort, timeout), 0))
+      return false;
+  return true;
+}
+
+__device__ __forceinline__ SharedPiece load_piece(const SharedParams& p, int i) {
   const int4* w = reinterpret_cast<const int4*>(p.table + p.pieces) + 3LL * i;
   const int4 a = __ldg(w), b = __ldg(w + 1), c = __ldg(w + 2);
-  pc = SharedPiece{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, c.x, c.y, c.z, c.w};
-  const int parts = pc.flags & kPieceSplit ? 2 : 1;
-  const bool ok = pc.rows >= 1 && pc.rows <= kRows && pc.r0 >= 0 && pc.q_row0 >= 0 &&
-                  (long long)pc.q_row0 + ((long long)pc.r0 + pc.rows - 1) / p.g < p.num_q_rows &&
-                  pc.kv_head >= 0 && pc.kv_head < p.Hkv && pc.keys >= 1 && pc.key0 >= 0 &&
-                  pc.kv_row >= 0 && (long long)pc.kv_row + pc.keys <= p.num_kv_rows &&
-                  pc.ws_row >= 0 && (long long)pc.ws_row + (long long)parts * pc.rows <= p.ws_rows &&
-                  (parts == 2) == (!shared_dual(pc.rows) && pc.keys > BN);
-  if (!ok) set_status(p.status, CPATTN_ERR_RANGE);
+  return SharedPiece{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, c.x, c.y, {c.z, c.w}};
+}
+__device__ __forceinline__ bool piece_ok(const SharedParams& p, const SharedPiece& pc, bool dual) {
+  return pc.rows >= 1 && pc.rows <= kRows && shared_dual(pc.rows) == dual && pc.r0 >= 0 &&
+         pc.q_row0 >= 0 &&
+         (long long)pc.q_row0 + ((long long)pc.r0 + pc.rows - 1) / p.g < p.num_q_rows &&
+         pc.kv_head >= 0 && pc.kv_head < p.Hkv && pc.keys >= 1 && pc.key0 >= 0 && pc.kv_row >= 0 &&
+         (long long)pc.kv_row + pc.keys <= p.num_kv_rows && pc.ws_row >= 0 &&
+         (long long)pc.ws_row + shared_reps(pc.rows) * pc.rows <= p.ws_rows;
+}
+__device__ __forceinline__ int num_tiles(int keys) { return (keys - 1) / BN + 1; }
+
+// This block's list, and a check of every piece in it against the buffers: the
+// roles below walk the list on their own and rely on it.  tiles[s]: KV tiles of
+// stream s's small units (zeroed by the caller before a barrier).  All threads
+// call it; false (and CPATTN_ERR_RANGE) when the list cannot be run.
+__device__ __forceinline__ bool load_list(const SharedParams& p, SharedCta& c, int* tiles) {
+  const int4* w = reinterpret_cast<const int4*>(p.table) + 2LL * blockIdx.x;
+  const int4 a = __ldg(w);
+  c = SharedCta{a.x, a.y, a.z, a.w, __ldg(&w[1].x), {0, 0, 0}};
+  bool ok = c.dual0 >= 0 && c.dual0 <= c.dual1 && c.dual1 <= p.num_pieces && c.single0 >= 0 &&
+            c.single0 <= c.single1 && c.single1 <= c.single2 && c.single2 <= p.num_pieces;
+  if (ok) {
+    for (int i = c.dual0 + threadIdx.x; i < c.dual1; i += blockDim.x)
+      ok = ok && piece_ok(p, load_piece(p, i), true);
+    for (int i = c.single0 + threadIdx.x; i < c.single2; i += blockDim.x) {
+      const SharedPiece pc = load_piece(p, i);
+      ok = ok && piece_ok(p, pc, false);
+      if (ok) atomicAdd(tiles + (i >= c.single1), num_tiles(pc.keys));
+    }
+  }
+  ok = __syncthreads_and(ok);
+  ok = ok && (tiles[0] == tiles[1] || tiles[0] == tiles[1] + 1);
+  if (!ok && threadIdx.x == 0) set_status(p.status, CPATTN_ERR_RANGE);
   return ok;
 }
 
-// Order of a piece's K and V tiles in the ring, T KV tiles in all: the order in
-// which the MMA warp first uses them (see its loop).  dual: K0 V0 K1 V1 ...;
-// otherwise K0 K1 V0 K2 V1 ... K(T-1) V(T-2) V(T-1).
-__device__ __forceinline__ int k_place(bool dual, int t) { return dual ? 2 * t : (t == 0 ? 0 : 2 * t - 1); }
-__device__ __forceinline__ int v_place(bool dual, int t, int T) {
-  return dual ? 2 * t + 1 : (t == T - 1 ? 2 * T - 1 : 2 * t + 2);
-}
-__device__ __forceinline__ void tile_at(bool dual, int j, int T, bool& is_v, int& t) {
-  if (dual) {
-    is_v = j & 1;
-    t = j >> 1;
-  } else if (j == 2 * T - 1) {
-    is_v = true;
-    t = T - 1;
-  } else if (j == 0 || (j & 1)) {
-    is_v = false;
-    t = (j + 1) >> 1;
-  } else {
-    is_v = true;
-    t = (j - 2) >> 1;
+// One K or V tile of the ring.
+struct RingTile {
+  int kv_row, kv_head, live;  // its first row, head, and rows up to the run's end
+  bool is_v, first;           // first: of its piece
+  int which;  // 2 * stream + (step of the stream) % 2; of a dual unit: 4 + tile % 2
+  __device__ __forceinline__ int user() const { return which >> 1; }  // stream, or 2: both
+};
+// Calls f(tile) for the K and V tiles of a list in the order in which the MMA warps
+// use them, until it returns false: K0 V0 K1 V1 ... for dual units, then K0 K1 V0
+// K2 V1 ... for the steps of the small units, step n being the next KV tile of
+// stream n & 1.
+template <class F>
+__device__ __forceinline__ bool for_each_ring_tile(const SharedParams& p, const SharedCta& c,
+                                                   int steps, F&& f) {
+  int tile = 0;
+  for (int i = c.dual0; i < c.dual1; ++i) {
+    const SharedPiece pc = load_piece(p, i);
+    RingTile r{pc.kv_row, pc.kv_head, pc.keys, false, true, 0};
+    for (const int end = 2 * (tile + num_tiles(pc.keys)); 2 * tile < end;) {
+      r.which = 4 + (tile & 1);
+      if (!f(r)) return false;
+      if (r.is_v) {
+        ++tile;
+        r.kv_row += BN;
+        r.live -= BN;
+        r.first = false;
+      }
+      r.is_v = !r.is_v;
+    }
   }
+  int next0 = c.single0, next1 = c.single1;
+  RingTile t0{0, 0, 0, false, true, 0}, t1 = t0;  // the streams' last K tiles
+  for (int j = 0; j < 2 * steps; ++j) {
+    const bool is_v = j == 2 * steps - 1 || (j > 0 && !(j & 1));
+    const int n = j == 2 * steps - 1 ? steps - 1 : is_v ? (j - 2) >> 1 : (j + 1) >> 1;
+    RingTile r = n & 1 ? t1 : t0;
+    r.is_v = is_v;
+    if (!is_v) {
+      r.kv_row += BN;
+      r.live -= BN;
+      r.first = r.live <= 0;
+      if (r.first) {
+        const SharedPiece pc = load_piece(p, n & 1 ? next1++ : next0++);
+        r.kv_row = pc.kv_row;
+        r.kv_head = pc.kv_head;
+        r.live = pc.keys;
+      }
+      r.which = 2 * (n & 1) + ((n >> 1) & 1);
+      if (n & 1) t1 = r;
+      else t0 = r;
+    }
+    if (!f(r)) return false;
+  }
+  return true;
 }
 
-// Four e4m3 codes times a power of two, as bf16 (exact: the low halves of the
-// fp32 products are zero, so the upper halves are the bf16 values).
-__device__ __forceinline__ uint2 codes_to_bf16(uint32_t c, float scale) {
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// Four e4m3 codes as f16, times m (f16 in both halves).
+__device__ __forceinline__ uint2 codes_to_f16(uint32_t c, uint32_t m) {
   uint32_t h0, h1;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h0) : "h"((uint16_t)c));
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h1) : "h"((uint16_t)(c >> 16)));
-  float x[4];
-  asm("{\n\t.reg .f16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
-      "cvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}" : "=f"(x[0]), "=f"(x[1]) : "r"(h0));
-  asm("{\n\t.reg .f16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
-      "cvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}" : "=f"(x[2]), "=f"(x[3]) : "r"(h1));
+  return make_uint2(mul_f16x2(h0, m), mul_f16x2(h1, m));
+}
+__device__ __forceinline__ float exp2_int(int e) {  // e in [-126, 127]
+  return __uint_as_float((uint32_t)(e + 127) << 23);
+}
+// Exponent of a scale s >= 0, such that exp2_int takes it and its negative.
+__device__ __forceinline__ int exponent_of(float s) {
+  return min(max((int)(__float_as_uint(s) >> 23) - 127, -126), 126);
+}
+constexpr uint32_t idesc_16bit_f32(bool f16, int M, int N, int b_mn) {
+  return idesc_bf16_f32(M, N, 0, b_mn) & ~(f16 ? (1u << 7) | (1u << 10) : 0u);
+}
+
+// One KV tile for the rows of a warp (one per lane): keys [copy * W, (copy + 1) * W)
+// of the tile.  S from TMEM, masked to the `here` visible keys of the tile, online
+// softmax in base 2, P (16 bits, zero for the other copies' keys) back over S, and
+// where there is an O (`has_o`), O rescaled when the maximum moves or o_scale != 1.
+template <int W, int D, bool QUANT>
+__device__ __forceinline__ void softmax_tile(uint32_t s_addr, uint32_t o_addr, int copy, int here,
+                                             bool has_o, float o_scale, float sl2, float& m_run,
+                                             float& m_use, float& l_run) {
+  float x[W];
+  {
+    uint32_t v[W];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) x[i] *= scale;
-  return make_uint2(__byte_perm(__float_as_uint(x[0]), __float_as_uint(x[1]), 0x7632),
-                    __byte_perm(__float_as_uint(x[2]), __float_as_uint(x[3]), 0x7632));
+    for (int q = 0; q < W / 32; ++q) tmem_ld32p(s_addr + copy * W + q * 32, v + q * 32);
+    tmem_wait_ld();
+#pragma unroll
+    for (int c = 0; c < W; ++c) x[c] = __uint_as_float(v[c]);
+  }
+  here -= copy * W;
+  if (here < W) {
+#pragma unroll
+    for (int c = 0; c < W; ++c)
+      if (c >= here) x[c] = -INFINITY;
+  }
+  float mx0 = x[0], mx1 = x[1], mx2 = x[2], mx3 = x[3];
+#pragma unroll
+  for (int c = 4; c + 8 <= W; c += 8) {
+    mx0 = fmax3(mx0, x[c], x[c + 1]);
+    mx1 = fmax3(mx1, x[c + 2], x[c + 3]);
+    mx2 = fmax3(mx2, x[c + 4], x[c + 5]);
+    mx3 = fmax3(mx3, x[c + 6], x[c + 7]);
+  }
+  mx0 = fmax3(mx0, x[W - 4], x[W - 3]);
+  mx1 = fmax3(mx1, x[W - 2], x[W - 1]);
+  const float mx = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)) * sl2;
+  // The maximum moves only when a tile raises it by more than kMaxSlack (log2
+  // units): exponentials stay below 2^kMaxSlack, l uses the same maximum, and O in
+  // TMEM is rescaled only then.
+  const bool move = mx > m_run + kMaxSlack;
+  const float m_new = move ? mx : m_run;
+  const float m_new_use = (m_new == -INFINITY) ? 0.f : m_new;
+  const float alpha = move ? ex2_approx(m_run - m_new_use) : 1.f;
+  float sum0 = 0.f, sum1 = 0.f;
+#pragma unroll
+  for (int q = 0; q < W / 32; ++q) {
+    uint32_t pk[16];
+#pragma unroll
+    for (int c = 0; c < 32; c += 2) {
+      float a, b;
+      ffma2(a, b, x[q * 32 + c], x[q * 32 + c + 1], sl2, sl2, -m_new_use, -m_new_use);
+      a = ex2_approx(a);
+      b = ex2_approx(b);
+      fadd2(sum0, sum1, sum0, sum1, a, b);
+      // P in 16 bits, the second product's operand type: off by at most 2^-8 (bf16) or
+      // 2^-11 (f16) of each weight; l sums the unrounded values
+      pk[c >> 1] = QUANT ? pack_f16x2(a, b) : pack_bf16x2(a, b);
+    }
+    tmem_st16(s_addr + copy * (W / 2) + q * 16, pk);
+  }
+  if constexpr (W < BN) {
+    uint32_t zero[16];
+#pragma unroll
+    for (int c = 0; c < 16; ++c) zero[c] = 0u;
+#pragma unroll
+    for (int q = 0; q < BN / 32; ++q)
+      if (q / (W / 32) != copy) tmem_st16(s_addr + q * 16, zero);
+  }
+  l_run = l_run * alpha + (sum0 + sum1);
+  const bool need = has_o && (move || o_scale != 1.f);
+  if (__any_sync(0xffffffffu, need)) {
+    const float a = need ? alpha * o_scale : 1.f;
+    uint32_t v[32];
+#pragma unroll
+    for (int q = 0; q < D / 32; ++q) {
+      tmem_ld32(o_addr + q * 32, v);
+      tmem_wait_ld();
+#pragma unroll
+      for (int c = 0; c < 32; ++c) v[c] = __float_as_uint(__uint_as_float(v[c]) * a);
+      tmem_st32(o_addr + q * 32, v);
+    }
+  }
+  tmem_wait_st();
+  m_run = m_new;
+  m_use = m_new_use;
 }
 
 template <int D, bool QUANT>
 __global__ void __launch_bounds__(SharedCfg<D, QUANT>::kThreads, 1)
 attn_shared_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                   const SharedParams p) {
+                   const __grid_constant__ CUtensorMap tm_k_tail,
+                   const __grid_constant__ CUtensorMap tm_v_tail, const SharedParams p) {
   using C = SharedCfg<D, QUANT>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
-  uint64_t* empty = full + C::kStages;
+  uint64_t* empty = full + 3 * C::kStages;
   uint64_t* raw_full = empty + C::kStages;
   uint64_t* raw_empty = raw_full + C::kRawStages;
   uint64_t* q_full = raw_empty + C::kRawStages;
   uint64_t* s_full = q_full + 2;
   uint64_t* p_full = s_full + 2;
   uint64_t* o_full = p_full + 2;
-  uint64_t* fix_req = o_full + 2;
-  uint64_t* fix_done = fix_req + 1;
-  uint64_t* bar_drain = fix_done + 1;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_drain + 1);
+  uint64_t* bar_drain = o_full + 2;
+  uint16_t* raw_mul = reinterpret_cast<uint16_t*>(smem + C::kMulOff);
+  RawNote* raw_note = reinterpret_cast<RawNote*>(smem + C::kNoteOff);
+  int2* tile_exp = reinterpret_cast<int2*>(smem + C::kExpOff);  // (ek, ev) by RingTile::which
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kWordOff);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile int* issued_loads = reinterpret_cast<volatile int*>(tmem_slot + 2);  // for the abort drain
+  volatile int* issued_phases = issued_loads + 1;
+  int* stream_tiles = reinterpret_cast<int*>(tmem_slot + 4);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   grid_dep_trigger();  // the merge may be scheduled as blocks of this grid end
 
-  const int first = __ldg(p.table + blockIdx.x), last = __ldg(p.table + blockIdx.x + 1);
-  if (first < 0 || last > p.num_pieces) {
-    if (threadIdx.x == 0) set_status(p.status, CPATTN_ERR_RANGE);
-    return;
-  }
-  if (first >= last) return;
-
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kStages; ++i) {
-      mbar_init(full + i, QUANT ? 128 : 1);
-      mbar_init(empty + i, 1);
+      for (int u = 0; u < 3; ++u) mbar_init(full + u * C::kStages + i, QUANT ? 128 : 1);
+      mbar_init(empty + i, 2);  // a commit of each stream
     }
     for (int i = 0; i < C::kRawStages; ++i) {
-      mbar_init(raw_full + i, 1);
+      mbar_init(raw_full + i, 2);  // the TMA copy and the factors
       mbar_init(raw_empty + i, 128);
     }
     for (int s = 0; s < 2; ++s) {
@@ -188,15 +385,14 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
       mbar_init(s_full + s, 1);
       mbar_init(p_full + s, 128);
       mbar_init(o_full + s, 1);
+      mbar_init(bar_drain + s, 1);
+      stream_tiles[s] = 0;
     }
-    mbar_init(fix_req, 1);
-    mbar_init(fix_done, 32);
-    mbar_init(bar_drain, 1);
     *abort_flag = 0;
-    tmem_slot[2] = 0;
+    *issued_loads = *issued_phases = 0;
     fence_barrier_init();
   }
-  if (warp == C::kProducerWarp) {
+  if (warp == kProducerWarp) {
     tmem_alloc(tmem_slot, C::kTmemCols);
     tmem_relinquish();
   }
@@ -204,216 +400,295 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  volatile int* issued_loads = reinterpret_cast<volatile int*>(tmem_slot + 2);  // for the abort drain
   const uint32_t q_base = smem_u32(smem);
   const uint32_t ring_base = smem_u32(smem + C::kRingOff);
+  SharedCta list;
+  if (!load_list(p, list, stream_tiles)) {
+    if (warp == kProducerWarp) tmem_dealloc(tmem_base, C::kTmemCols);
+    return;
+  }
+  const int steps = stream_tiles[0] + stream_tiles[1];  // of the small units
+
+  // A ring slot has a full barrier for each user (stream 0, stream 1, both), so that
+  // every waiter sees all phases of the barriers it waits on; their parities are kept
+  // as bits of a word, `user * kStages + slot`.
+  auto full_bit = [](int user, int slot) { return user * C::kStages + slot; };
+  // Ring places of step n of the small units, behind dual_seq places of dual units.
+  auto k_place = [](int n) { return n == 0 ? 0 : 2 * n - 1; };
+  auto v_place = [&](int n) { return n == steps - 1 ? 2 * n + 1 : 2 * n + 2; };
 
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsOther));
-    if (warp == C::kProducerWarp) {
+    if (warp == kProducerWarp) {
       // ---------------------------------------------------------- producer --
+      // bf16: one lane.  e4m3: the whole warp, which also turns the scales of the
+      // tile's rows into f16 factors, one tile behind the copies it starts.
+      constexpr int kSt = QUANT ? C::kRawStages : C::kStages;
+      constexpr int kBytes = QUANT ? C::kRawTile : C::kTile;
+      constexpr int kChunks = QUANT ? 1 : D / 64;   // boxes across a row
+      constexpr int kLine = kBytes / BN / kChunks;  // bytes of a box row
+      uint64_t* const emptyb = QUANT ? raw_empty : empty;
+      uint8_t* const ring = smem + (QUANT ? C::kRawOff : C::kRingOff);
       if (lane == 0) {
         prefetch_tmap(&tm_k);
         prefetch_tmap(&tm_v);
-        constexpr int kSt = QUANT ? C::kRawStages : C::kStages;
-        constexpr int kBytes = QUANT ? C::kRawTile : C::kTile;
-        uint64_t* const fullb = QUANT ? raw_full : full;
-        uint64_t* const emptyb = QUANT ? raw_empty : empty;
-        uint8_t* const ring = smem + (QUANT ? C::kRawOff : C::kRingOff);
-        int seq = 0;
-        bool ok = true;
-        for (int i = first; i < last && ok; ++i) {
-          SharedPiece pc;
-          if (!load_piece(p, i, pc)) continue;
-          const bool dual = shared_dual(pc.rows);
-          const int T = (pc.keys + BN - 1) / BN;
-          for (int j = 0; j < 2 * T; ++j, ++seq) {
-            bool is_v;
-            int t;
-            tile_at(dual, j, T, is_v, t);
-            const int slot = seq % kSt;
-            ok = mbar_wait(emptyb + slot, ((seq / kSt) & 1) ^ 1, abort_flag, p.timeout_ns);
-            if (!ok) break;
-            mbar_arrive_expect_tx(fullb + slot, kBytes);
-            const CUtensorMap* tm = is_v ? &tm_v : &tm_k;
-            const int row = pc.kv_row + t * BN;
-            if (QUANT) {
-              tma_load_3d(ring + slot * kBytes, tm, fullb + slot, 0, pc.kv_head, row);
-            } else {
+        prefetch_tmap(&tm_k_tail);
+        prefetch_tmap(&tm_v_tail);
+      }
+      auto copy = [&](const RingTile& r, int slot, uint64_t* bar) {
+        uint8_t* dst = ring + slot * kBytes;
+        if (r.live > BN - kTailRows) {
+          mbar_arrive_expect_tx(bar, kBytes);
+          const CUtensorMap* tm = r.is_v ? &tm_v : &tm_k;
 #pragma unroll
-              for (int c = 0; c < D / 64; ++c)
-                tma_load_3d(ring + slot * kBytes + c * BN * 128, tm, fullb + slot, c * 64,
-                            pc.kv_head, row);
-            }
-          }
+          for (int c = 0; c < kChunks; ++c)
+            tma_load_3d(dst + c * BN * kLine, tm, bar, c * 64, r.kv_head, r.kv_row);
+        } else {
+          const int boxes = (r.live + kTailRows - 1) / kTailRows;
+          mbar_arrive_expect_tx(bar, boxes * kTailRows * kLine * kChunks);
+          const CUtensorMap* tm = r.is_v ? &tm_v_tail : &tm_k_tail;
+          for (int x = 0; x < boxes; ++x)
+#pragma unroll
+            for (int c = 0; c < kChunks; ++c)
+              tma_load_3d(dst + (c * BN + x * kTailRows) * kLine, tm, bar, c * 64, r.kv_head,
+                          r.kv_row + x * kTailRows);
         }
+      };
+      int seq = 0;
+      uint32_t phases = 0;  // (bf16) loads of each full barrier, mod 2
+      bool ok = true;
+      if constexpr (!QUANT) {
+        if (lane == 0)
+          ok = for_each_ring_tile(p, list, steps, [&](const RingTile& r) {
+            const int slot = seq % kSt;
+            if (!wait_one(emptyb + slot, ((seq / kSt) & 1) ^ 1, abort_flag, p.timeout_ns))
+              return false;
+            copy(r, slot, full + full_bit(r.user(), slot));
+            phases ^= 1u << full_bit(r.user(), slot);
+            ++seq;
+            return true;
+          });
+      } else {
+        RingTile last{};                       // the tile whose factors are still to be made
+        float sk[4] = {}, sv[4] = {};          // its rows' scales (and its V rows', of a K tile)
+        int ev0 = 0, ev1 = 0;                  // E of each stream's V rows
+        auto factors = [&]() {
+          const int slot = (seq - 1) % kSt;
+          const bool second = last.user() == 1;
+          int ev = second ? ev1 : ev0, e = ev;
+          if (!last.is_v) {
+            float mk = fmaxf(fmaxf(sk[0], sk[1]), fmaxf(sk[2], sk[3]));
+            float mv = fmaxf(fmaxf(sv[0], sv[1]), fmaxf(sv[2], sv[3]));
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) {
+              mk = fmaxf(mk, __shfl_xor_sync(0xffffffffu, mk, o));
+              mv = fmaxf(mv, __shfl_xor_sync(0xffffffffu, mv, o));
+            }
+            e = exponent_of(mk);
+            ev = last.first ? exponent_of(mv) : max(ev, exponent_of(mv));
+            if (second) ev1 = ev;
+            else ev0 = ev;
+          }
+          const float inv = exp2_int(-e);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            raw_mul[slot * BN + i * 32 + lane] = (uint16_t)pack_f16x2(sk[i] * inv, 0.f);
+          if (lane == 0) raw_note[slot] = RawNote{last.live, last.which | (last.is_v ? RawNote::kNoteV : 0), e, ev};
+          __syncwarp();
+          if (lane == 0) mbar_arrive(raw_full + slot);
+        };
+        ok = for_each_ring_tile(p, list, steps, [&](const RingTile& r) {
+          const int slot = seq % kSt;
+          if (!wait_warp(emptyb + slot, ((seq / kSt) & 1) ^ 1, abort_flag, p.timeout_ns)) return false;
+          if (lane == 0) copy(r, slot, raw_full + slot);
+          __syncwarp();
+          float a[4], b[4];
+          const long long at = (long long)r.kv_head * p.s_head + r.kv_row + lane;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const bool live = i * 32 + lane < r.live;
+            a[i] = live ? __ldg((r.is_v ? p.vs : p.ks) + at + i * 32) : 0.f;
+            b[i] = live && !r.is_v ? __ldg(p.vs + at + i * 32) : 0.f;
+          }
+          if (seq > 0) factors();
+          last = r;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            sk[i] = a[i];
+            sv[i] = b[i];
+          }
+          ++seq;
+          return true;
+        });
+        if (ok && seq > 0) factors();
+        // given up: the last copy's barrier still wants its second arrival
+        if (!ok && seq > 0 && lane == 0) mbar_arrive(raw_full + (seq - 1) % kSt);
+      }
+      if (lane == 0) {
         *issued_loads = seq;
+        *issued_phases = (int)phases;
         if (!ok) {
           set_status(p.status, CPATTN_ERR_TIMEOUT);
           *abort_flag = 1;
         }
       }
-    } else if (warp == C::kMmaWarp) {
-      // -------------------------------------------------------- MMA issuer --
-      // Step n of a piece is a (KV tile, stream) pair, the streams in turn; while
-      // stream s works on P of step n the tensor core has step n + 1.  S of step
-      // n + 2 overwrites P of step n, whose PV was issued before it.
+    } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
+      // ------------------------------------------- MMA issuer of one stream --
+      // Its steps in order: P V of a step, then Q K^T of its next, whose S overwrites
+      // the P that the former reads (the tensor core keeps their order).
+      const int s = warp - kMmaWarp;
       if (lane == 0) {
-        constexpr uint32_t kIdescQK = idesc_bf16_f32(BM, BN, 0, 0);
-        constexpr uint32_t kIdescPV = idesc_bf16_f32(BM, D, 0, 1);
-        const uint64_t dq0 = smem_desc_sw128(q_base, 16, 1024);
+        constexpr uint32_t kIdescQK = idesc_16bit_f32(QUANT, BM, BN, 0);
+        constexpr uint32_t kIdescPV = idesc_16bit_f32(QUANT, BM, D, 1);
+        const uint64_t qd = smem_desc_sw128(q_base, 16, 1024) + (uint64_t)((s * C::kQTile) >> 4);
         const uint64_t dk0 = smem_desc_sw128(ring_base, 16, 1024);
         const uint64_t dv0 = smem_desc_sw128(ring_base, BN * 128, 1024);
-        int seq0 = 0;                  // ring place of the piece's first tile
-        int steps[2] = {0, 0}, pieces[2] = {0, 0}, fixes = 0;
-        bool ok = true;
-        for (int i = first; i < last && ok; ++i) {
-          SharedPiece pc;
-          if (!load_piece(p, i, pc)) continue;
-          const bool dual = shared_dual(pc.rows);
-          const int T = (pc.keys + BN - 1) / BN;
-          const int N = dual ? 2 * T : T;
-          const bool ragged = !QUANT && pc.keys % BN != 0;
-          auto wait_tile = [&](int seq) {
-            const bool r = mbar_wait(full + seq % C::kStages, (seq / C::kStages) & 1, abort_flag,
-                                     p.timeout_ns);
-            tc_fence_after();
-            return r;
-          };
-          auto issue_qk = [&](int n) {
-            const int s = n & 1, t = dual ? n >> 1 : n;
-            const int seq = seq0 + k_place(dual, t), slot = seq % C::kStages;
-            if (n < 2) {
-              if (!mbar_wait(q_full + s, pieces[s] & 1, abort_flag, p.timeout_ns)) return false;
-              tc_fence_after();
-            }
-            if (!(dual && s == 1) && !wait_tile(seq)) return false;
-            const uint64_t qd = dq0 + (uint64_t)((s * C::kQTile) >> 4);
-            const uint64_t kd = dk0 + (uint64_t)((slot * C::kTile) >> 4);
+        const uint32_t s_tmem = tmem_base + s * BN, o_tmem = tmem_base + 2 * BN + s * D;
+        auto issue_qk = [&](int slot) {
+          const uint64_t kd = dk0 + (uint64_t)((slot * C::kTile) >> 4);
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-              constexpr int kChunk = (BM * 128) >> 4;
-              const uint64_t off = (uint64_t)((kk >> 2) * kChunk + (kk & 3) * 2);
-              mma_ss(tmem_base + s * BN, qd + off, kd + off, kIdescQK, kk > 0 ? 1u : 0u);
-            }
-            mma_commit(s_full + s);
-            if (!(dual && s == 0)) mma_commit(empty + slot);
-            return true;
-          };
-          ok = issue_qk(0);
-          if (ok && N > 1) ok = issue_qk(1);
-          for (int n = 0; n < N && ok; ++n) {
-            const int s = n & 1, t = dual ? n >> 1 : n;
-            const int seq = seq0 + v_place(dual, t, T), slot = seq % C::kStages;
-            const bool first_use = !(dual && s == 1);
-            const bool fix = ragged && t == T - 1 && first_use;
-            if (first_use) {
-              ok = wait_tile(seq);
-              if (ok && fix) mbar_arrive(fix_req);
-            }
-            if (ok) ok = mbar_wait(p_full + s, steps[s] & 1, abort_flag, p.timeout_ns);
-            if (ok && fix) ok = mbar_wait(fix_done, fixes++ & 1, abort_flag, p.timeout_ns);
-            if (!ok) break;
-            tc_fence_after();
-            ++steps[s];
-            const uint64_t vd = dv0 + (uint64_t)((slot * C::kTile) >> 4);
-            const uint32_t dt = tmem_base + 2 * BN + s * D, pt = tmem_base + s * BN;
-#pragma unroll
-            for (int kk = 0; kk < BN / 16; ++kk)
-              mma_ts(dt, pt + kk * 8, vd + (uint64_t)(kk * ((16 * 128) >> 4)), kIdescPV,
-                     (n >= 2 || kk > 0) ? 1u : 0u);
-            if (n + 2 >= N) mma_commit(o_full + s);
-            if (!(dual && s == 0)) mma_commit(empty + slot);
-            if (n + 2 < N) ok = issue_qk(n + 2);
+          for (int kk = 0; kk < D / 16; ++kk) {
+            constexpr int kChunk = (BM * 128) >> 4;
+            const uint64_t off = (uint64_t)((kk >> 2) * kChunk + (kk & 3) * 2);
+            mma_ss(s_tmem, qd + off, kd + off, kIdescQK, kk > 0 ? 1u : 0u);
           }
-          ++pieces[0];
-          if (N > 1) ++pieces[1];
-          seq0 += 2 * T;
+        };
+        auto issue_pv = [&](int slot, bool first) {
+          const uint64_t vd = dv0 + (uint64_t)((slot * C::kTile) >> 4);
+#pragma unroll
+          for (int kk = 0; kk < BN / 16; ++kk)
+            mma_ts(o_tmem, s_tmem + kk * 8, vd + (uint64_t)(kk * ((16 * 128) >> 4)), kIdescPV,
+                   (!first || kk > 0) ? 1u : 0u);
+        };
+        const int single_end = s ? list.single2 : list.single1;
+        int i = list.dual0;  // piece whose keys come next
+        bool dual = i < list.dual1;
+        if (!dual) i = s ? list.single1 : list.single0;
+        int dual_seq = 0;    // ring places of the dual tiles so far
+        int n = s;           // step of the small units
+        int step = 0, pieces = 0;
+        bool ok = true;
+        int left = 0;        // KV tiles of the current piece behind the one in S
+        uint32_t phases = 0;
+        auto wait_tile = [&](int user, int slot) {
+          const int b = full_bit(user, slot);
+          const uint32_t parity = (phases >> b) & 1;
+          phases ^= 1u << b;
+          return wait_one(full + b, parity, abort_flag, p.timeout_ns);
+        };
+        // Q K^T of the stream's next step (of a piece whose first tile it is: once the
+        // queries are there); false when there is none or a wait ran out
+        int v_seq = 0;       // ring place of the V tile of the step in S
+        bool shared_tile = false, head = false;  // of the step in S
+        auto next_qk = [&]() {
+          head = left == 0;
+          if (head) {
+            if (dual && i == list.dual1) {
+              dual = false;
+              i = s ? list.single1 : list.single0;
+            }
+            if (!dual && i >= single_end) return false;
+            left = num_tiles(load_piece(p, i++).keys);
+            ok = wait_one(q_full + s, pieces++ & 1, abort_flag, p.timeout_ns);
+          }
+          --left;
+          int k_seq;
+          shared_tile = dual;
+          if (dual) {
+            k_seq = dual_seq;
+            v_seq = dual_seq + 1;
+            dual_seq += 2;
+          } else {
+            k_seq = dual_seq + k_place(n);
+            v_seq = dual_seq + v_place(n);
+            n += 2;
+          }
+          const int slot = k_seq % C::kStages;
+          ok = ok && wait_tile(dual ? 2 : s, slot);
+          if (!ok) return false;
+          tc_fence_after();
+          issue_qk(slot);
+          mma_commit(s_full + s);
+          mma_commit(empty + slot);
+          if (!dual) mbar_arrive(empty + slot);  // the other stream does not use the tile
+          return true;
+        };
+        for (bool more = next_qk(); more; ++step) {
+          const int slot = v_seq % C::kStages;
+          const bool first = head, last = left == 0, mine = !shared_tile;
+          ok = wait_tile(mine ? s : 2, slot) && wait_one(p_full + s, step & 1, abort_flag, p.timeout_ns);
+          if (!ok) break;
+          tc_fence_after();
+          issue_pv(slot, first);
+          if (last) mma_commit(o_full + s);
+          mma_commit(empty + slot);
+          if (mine) mbar_arrive(empty + slot);
+          more = next_qk();
         }
         if (!ok) {
           set_status(p.status, CPATTN_ERR_TIMEOUT);
           *abort_flag = 1;
         }
         // every MMA and commit issued by this thread has completed
-        mma_commit(bar_drain);
-        mbar_wait(bar_drain, 0, nullptr, p.timeout_ns);
-      }
-    } else if (!QUANT && warp == C::kFixWarp) {
-      // ------------------------------------------ V rows behind the last key --
-      int seq0 = 0, fixes = 0;
-      for (int i = first; i < last; ++i) {
-        SharedPiece pc;
-        if (!load_piece(p, i, pc)) continue;
-        const int T = (pc.keys + BN - 1) / BN, live = pc.keys - (T - 1) * BN;
-        if (live < BN) {
-          const int seq = seq0 + 2 * T - 1, slot = seq % C::kStages;
-          if (!mbar_wait_warp(fix_req, fixes & 1, abort_flag, p.timeout_ns) ||
-              !mbar_wait_warp(full + slot, (seq / C::kStages) & 1, abort_flag, p.timeout_ns))
-            break;  // the MMA warp's own wait runs out as well and reports
-          ++fixes;
-          for (int c = 0; c < D / 64; ++c) {
-            uint4* tile = reinterpret_cast<uint4*>(smem + C::kRingOff + slot * C::kTile + c * BN * 128);
-            for (int at = live * 8 + lane; at < BN * 8; at += 32) tile[at] = make_uint4(0, 0, 0, 0);
-          }
-          fence_async_shared();
-          mbar_arrive(fix_done);
-        }
-        seq0 += 2 * T;
+        mma_commit(bar_drain + s);
+        wait_one(bar_drain + s, 0, nullptr, p.timeout_ns);
       }
     }
     if constexpr (QUANT) if (warp >= kConvertWarp) {
-      // ------------------------------------------------- codes to bf16 tiles --
-      // Warp w has rows 32w .. 32w+31 of every tile, D / 16 lanes to a row.
+      // --------------------------------------------------- codes to f16 tiles --
+      // Warp w has rows 32w .. 32w+31 of every tile, D / 16 lanes to a row.  Rows
+      // behind the last key become zeros (0 * NaN is NaN, so masking P alone would
+      // not keep stale rows out).
       const int w = warp - kConvertWarp;
       constexpr int kLanes = D / 16, kRowsPer = 32 / kLanes;
       const int rl = lane / kLanes, cl = lane % kLanes;  // row in the group, 16-code chunk
-      int seq = 0;
+      const int total = 2 * steps;  // + the dual tiles', counted below
+      int tiles = total;
+      for (int i = list.dual0; i < list.dual1; ++i) tiles += 2 * num_tiles(load_piece(p, i).keys);
       bool ok = true;
-      for (int i = first; i < last && ok; ++i) {
-        SharedPiece pc;
-        if (!load_piece(p, i, pc)) continue;
-        const bool dual = shared_dual(pc.rows);
-        const int T = (pc.keys + BN - 1) / BN;
-        const long long srow = (long long)pc.kv_head * p.s_head + pc.kv_row + w * 32 + lane;
-        auto load_scale = [&](int j) {
-          bool is_v;
-          int t;
-          tile_at(dual, j, T, is_v, t);
-          const bool live = t * BN + w * 32 + lane < pc.keys;
-          return live ? __ldg((is_v ? p.vs : p.ks) + srow + t * BN) : 0.f;
-        };
-        float next = load_scale(0);
-        for (int j = 0; j < 2 * T; ++j, ++seq) {
-          const float scale = next;
-          if (j + 1 < 2 * T) next = load_scale(j + 1);
-          bool is_v;
-          int t;
-          tile_at(dual, j, T, is_v, t);
-          const int live = pc.keys - t * BN;
-          const int raw = seq % C::kRawStages, slot = seq % C::kStages;
-          ok = mbar_wait_warp(raw_full + raw, (seq / C::kRawStages) & 1, abort_flag, p.timeout_ns) &&
-               mbar_wait_warp(empty + slot, ((seq / C::kStages) & 1) ^ 1, abort_flag, p.timeout_ns);
-          if (!ok) break;
-          const uint8_t* src = smem + C::kRawOff + raw * C::kRawTile;
-          uint8_t* dst = smem + C::kRingOff + slot * C::kTile;
+      for (int seq = 0; seq < tiles; ++seq) {
+        const int raw = seq % C::kRawStages, slot = seq % C::kStages;
+        ok = wait_warp(empty + slot, ((seq / C::kStages) & 1) ^ 1, abort_flag, p.timeout_ns) &&
+             wait_warp(raw_full + raw, (seq / C::kRawStages) & 1, abort_flag, p.timeout_ns);
+        if (!ok) break;
+        const RawNote note = raw_note[raw];
+        if (w == 0 && lane == 0 && note.which < RawNote::kNoteV)
+          tile_exp[note.which] = make_int2(note.ek, note.ev);
+        const uint8_t* src = smem + C::kRawOff + raw * C::kRawTile + (w * 32 + rl) * D + cl * 16;
+        const uint16_t* mul = raw_mul + raw * BN + w * 32 + rl;
+        uint8_t* dst = smem + C::kRingOff + slot * C::kTile + (cl >> 2) * (BN * 128);
+        const int live = note.live - w * 32 - rl;
+        // loads of a batch before its stores: the compiler cannot tell them apart
+        constexpr int kBatch = 4;
 #pragma unroll
-          for (int r0 = 0; r0 < 32; r0 += kRowsPer) {
-            const int row = w * 32 + r0 + rl;
-            const float sc = __shfl_sync(0xffffffffu, scale, r0 + rl);
-            uint4 a = *reinterpret_cast<const uint4*>(src + row * D + cl * 16);
-            if (row >= live) a = make_uint4(0, 0, 0, 0);
-            const uint2 x0 = codes_to_bf16(a.x, sc), x1 = codes_to_bf16(a.y, sc);
-            const uint2 x2 = codes_to_bf16(a.z, sc), x3 = codes_to_bf16(a.w, sc);
-            uint8_t* line = dst + (cl >> 2) * (BN * 128) + row * 128;
-            const int c0 = (cl & 3) * 2;  // 16-byte chunk of the row's 128 bytes
-            *reinterpret_cast<uint4*>(line + ((c0 ^ (row & 7)) << 4)) = make_uint4(x0.x, x0.y, x1.x, x1.y);
-            *reinterpret_cast<uint4*>(line + (((c0 + 1) ^ (row & 7)) << 4)) =
-                make_uint4(x2.x, x2.y, x3.x, x3.y);
+        for (int r0 = 0; r0 < 32; r0 += kBatch * kRowsPer) {
+          uint4 v[kBatch];
+          uint32_t m[kBatch];
+#pragma unroll
+          for (int x = 0; x < kBatch; ++x) {
+            const int r = r0 + x * kRowsPer;
+            v[x] = *reinterpret_cast<const uint4*>(src + r * D);
+            m[x] = mul[r];
+            if (r >= live) v[x] = make_uint4(0, 0, 0, 0);
           }
-          fence_async_shared();
-          mbar_arrive(full + slot);
-          mbar_arrive(raw_empty + raw);
+#pragma unroll
+          for (int x = 0; x < kBatch; ++x) {
+            const int row = w * 32 + r0 + x * kRowsPer + rl;
+            const uint32_t m2 = m[x] * 0x10001u;
+            const uint2 x0 = codes_to_f16(v[x].x, m2), x1 = codes_to_f16(v[x].y, m2);
+            const uint2 x2 = codes_to_f16(v[x].z, m2), x3 = codes_to_f16(v[x].w, m2);
+            // two 16-byte chunks of the row's line; the lanes of a row's second line
+            // store theirs the other way round, so that a quarter warp hits every bank
+            uint8_t* line = dst + row * 128;
+            const int c0 = (cl & 3) * 2, flip = cl >> 2;
+            const uint4 lo = make_uint4(x0.x, x0.y, x1.x, x1.y), hi = make_uint4(x2.x, x2.y, x3.x, x3.y);
+            *reinterpret_cast<uint4*>(line + (((c0 + flip) ^ (row & 7)) << 4)) = flip ? hi : lo;
+            *reinterpret_cast<uint4*>(line + (((c0 + 1 - flip) ^ (row & 7)) << 4)) = flip ? lo : hi;
+          }
         }
+        fence_async_shared();
+        mbar_arrive(full + full_bit((note.which & (RawNote::kNoteV - 1)) >> 1, slot));
+        mbar_arrive(raw_empty + raw);
       }
       if (!ok && lane == 0) {
         set_status(p.status, CPATTN_ERR_TIMEOUT);
@@ -428,135 +703,156 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     const int trow = wq * 32 + lane;  // row within the MMA tile
     const uint32_t s_addr = tmem_base + ((uint32_t)(wq * 32) << 16) + s * BN;
     const uint32_t o_addr = tmem_base + ((uint32_t)(wq * 32) << 16) + 2 * BN + s * D;
-    const float sl2 = p.scale_log2;
-    // The stream's next piece with KV tiles for it, from index i on; last if none.
-    SharedPiece np;
-    auto find = [&](int i) {
-      for (; i < last; ++i)
-        if (load_piece(p, i, np) && (s == 0 || shared_dual(np.rows) || np.keys > BN)) break;
-      return i;
+    uint8_t* const q_line = smem + s * C::kQTile + trow * 128;
+    auto q_chunk = [&](int c) {  // 16-byte chunk c of this thread's query row (128-byte swizzle)
+      return q_line + (c >> 3) * (BM * 128) + (((c & 7) ^ (trow & 7)) << 4);
     };
-    // This thread's query row of piece np to shared memory (128-byte swizzle).
-    auto load_q = [&]() {
-      const int r = shared_dual(np.rows) ? s * BM + trow : trow;
-      if (r < np.rows) {
-        const int packed = np.r0 + r, qi = packed / p.g;
-        const __nv_bfloat16* src = p.q + (long long)(np.q_row0 + qi) * p.q_row +
-                                   (long long)(np.kv_head * p.g + packed - qi * p.g) * p.q_head;
-        uint8_t* dst = smem + s * C::kQTile + trow * 128;
+    auto row_of = [&](const SharedPiece& pc) {
+      return shared_dual(pc.rows) ? s * BM + trow : trow & (BM / shared_reps(pc.rows) - 1);
+    };
+    // This thread's query row of a piece to shared memory, asynchronously; q_ready()
+    // publishes it, and returns the factor of its scores.
+    auto load_q = [&](const SharedPiece& pc) {
+      const int r = row_of(pc);
+      if (r < pc.rows) {
+        const int packed = pc.r0 + r, qi = packed / p.g;
+        const __nv_bfloat16* src = p.q + (long long)(pc.q_row0 + qi) * p.q_row +
+                                   (long long)(pc.kv_head * p.g + packed - qi * p.g) * p.q_head;
 #pragma unroll
         for (int c = 0; c < D / 8; ++c)
-          *reinterpret_cast<uint4*>(dst + (c >> 3) * (BM * 128) + (((c & 7) ^ (trow & 7)) << 4)) =
-              __ldg(reinterpret_cast<const uint4*>(src) + c);
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(q_chunk(c))),
+                       "l"(src + c * 8)
+                       : "memory");
+      }
+    };
+    auto q_ready = [&](const SharedPiece& pc) {
+      float factor = p.scale_log2;
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      if constexpr (QUANT) {
+        if (row_of(pc) < pc.rows) {
+          // bf16 to f16 in place, times 2^f with 2^f max|q| in [2^14, 2^15)
+          uint32_t mx = 0;
+#pragma unroll
+          for (int c = 0; c < D / 8; ++c) {
+            const uint4 v = *reinterpret_cast<const uint4*>(q_chunk(c));
+            mx = __vmaxu2(__vmaxu2(mx, __vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu)),
+                          __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu));
+          }
+          const int e = (int)(max(mx & 0xFFFFu, mx >> 16) >> 7) - 127;  // of max|q|
+          const int f = min(max(14 - e, -126), 126);
+          const float up = exp2_int(f);
+          factor *= exp2_int(-f);
+#pragma unroll
+          for (int c = 0; c < D / 8; ++c) {
+            uint4* const at = reinterpret_cast<uint4*>(q_chunk(c));
+            uint4 v = *at;
+            uint32_t* const x = &v.x;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              x[i] = pack_f16x2(__uint_as_float(x[i] << 16) * up,
+                                __uint_as_float(x[i] & 0xFFFF0000u) * up);
+            *at = v;
+          }
+        }
       }
       fence_async_shared();
       mbar_arrive(q_full + s);
+      return factor;
     };
-    int step = 0, done = 0;
+    // the stream's pieces: the dual ones, then its own
+    const int single0 = s ? list.single1 : list.single0, single1 = s ? list.single2 : list.single1;
+    const int duals = list.dual1 - list.dual0, pieces = duals + single1 - single0;
+    auto piece = [&](int i) {
+      return load_piece(p, i < duals ? list.dual0 + i : single0 + i - duals);
+    };
+    SharedPiece np{};
+    float factor = 0.f;
+    if (pieces > 0) {
+      np = piece(0);
+      load_q(np);
+      factor = q_ready(np);
+    }
+    int step = 0;      // of the stream
+    int dual_seq = 0;  // ring places of the dual tiles before this piece
+    uint32_t phases = 0;
     bool ok = true;
-    int i = find(first);
-    if (i < last) load_q();
-    while (i < last) {
+    for (int i = 0; i < pieces; ++i) {
       const SharedPiece pc = np;
-      const bool dual = shared_dual(pc.rows);
-      const int T = (pc.keys + BN - 1) / BN;
-      const int r = dual ? s * BM + trow : trow;
-      const bool warp_live = (dual ? s * BM : 0) + wq * 32 < pc.rows;
+      const bool more = i + 1 < pieces;
+      if (more) np = piece(i + 1);
+      const bool dual = i < duals;
+      const int T = num_tiles(pc.keys);
+      const int reps = shared_reps(pc.rows), r = row_of(pc);
+      const int copy = reps == 4 ? wq : reps == 2 ? wq >> 1 : 0;
+      const bool warp_live = (r & ~31) < pc.rows;
       int seen = 0;  // keys of the piece that this row sees
       if (r < pc.rows) {
         const long long pos = (long long)pc.q_pos0 + (long long)((pc.r0 + r) / p.g) * pc.q_pos_step;
         seen = (int)max(0LL, min((long long)pc.keys, pos + 1 - pc.key0));
       }
       float m_run = -INFINITY, l_run = 0.f, m_use = 0.f;
-      for (int t = dual ? 0 : s; t < T; t += dual ? 1 : 2, ++step) {
-        ok = mbar_wait_warp(s_full + s, step & 1, abort_flag, p.timeout_ns);
+      int ev = 0;  // exponent of O
+      for (int t = 0; t < T; ++t, ++step) {
+        ok = wait_warp(s_full + s, step & 1, abort_flag, p.timeout_ns);
         if (!ok) break;
         tc_fence_after();
+        // the piece's last S is done: its query tile is free for the next piece
+        if (t == T - 1 && more) load_q(np);
+        float sl2 = factor, o_scale = 1.f;
+        if constexpr (QUANT) {
+          // written before the K tile of this step went to the tensor core, and not
+          // again before this step's P has been used
+          const volatile int2* e =
+              tile_exp + (dual ? 4 + ((dual_seq / 2 + t) & 1) : 2 * s + ((step - dual_seq / 2) & 1));
+          const int ek = e->x, ev_now = e->y;
+          sl2 *= exp2_int(ek);
+          if (t > 0 && ev_now != ev) o_scale = exp2_int(max(ev - ev_now, -126));
+          ev = ev_now;
+        }
         if (warp_live) {
-          float x[BN];
-          {
-            uint32_t v[BN];
-#pragma unroll
-            for (int q = 0; q < BN / 32; ++q) tmem_ld32p(s_addr + q * 32, v + q * 32);
-            tmem_wait_ld();
-#pragma unroll
-            for (int c = 0; c < BN; ++c) x[c] = __uint_as_float(v[c]);
-          }
           const int here = seen - t * BN;  // visible keys of this tile
-          if (here < BN) {
+          if (reps == 1)
+            softmax_tile<BN, D, QUANT>(s_addr, o_addr, 0, here, t > 0, o_scale, sl2, m_run, m_use, l_run);
+          else if (reps == 2)
+            softmax_tile<BN / 2, D, QUANT>(s_addr, o_addr, copy, here, t > 0, o_scale, sl2, m_run, m_use,
+                                           l_run);
+          else
+            softmax_tile<BN / 4, D, QUANT>(s_addr, o_addr, copy, here, t > 0, o_scale, sl2, m_run, m_use,
+                                           l_run);
+        }
+        if constexpr (!QUANT) {
+          // V rows behind the last key become zeros (0 * NaN is NaN, so masking P
+          // alone would not keep stale rows out); both streams do it to a shared tile
+          const int user = dual ? 2 : s, n = 2 * (step - dual_seq / 2) + s;
+          const int k_bit = full_bit(user, (dual_seq + (dual ? 2 * t : k_place(n))) % C::kStages);
+          const int v_slot = (dual_seq + (dual ? 2 * t + 1 : v_place(n))) % C::kStages;
+          const int v_bit = full_bit(user, v_slot), live = pc.keys - t * BN;
+          phases ^= 1u << k_bit;
+          if (live < BN) {
+            ok = wait_warp(full + v_bit, (phases >> v_bit) & 1, abort_flag, p.timeout_ns);
+            if (!ok) break;
+            uint8_t* tile = smem + C::kRingOff + v_slot * C::kTile;
 #pragma unroll
-            for (int c = 0; c < BN; ++c)
-              if (c >= here) x[c] = -INFINITY;
+            for (int c = 0; c < D / 64; ++c)
+              for (int at = live * 8 + trow; at < BN * 8; at += 128)
+                *reinterpret_cast<uint4*>(tile + c * BN * 128 + at * 16) = make_uint4(0, 0, 0, 0);
+            fence_async_shared();
           }
-          float mx0 = x[0], mx1 = x[1], mx2 = x[2], mx3 = x[3];
-#pragma unroll
-          for (int c = 4; c + 8 <= BN; c += 8) {
-            mx0 = fmax3(mx0, x[c], x[c + 1]);
-            mx1 = fmax3(mx1, x[c + 2], x[c + 3]);
-            mx2 = fmax3(mx2, x[c + 4], x[c + 5]);
-            mx3 = fmax3(mx3, x[c + 6], x[c + 7]);
-          }
-          mx0 = fmax3(mx0, x[BN - 4], x[BN - 3]);
-          mx1 = fmax3(mx1, x[BN - 2], x[BN - 1]);
-          const float mx = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)) * sl2;
-          // The maximum moves only when a tile raises it by more than kMaxSlack
-          // (log2 units): exponentials stay below 2^kMaxSlack, l uses the same
-          // maximum, and O in TMEM is rescaled only then.
-          const bool move = mx > m_run + kMaxSlack;
-          const float m_new = move ? mx : m_run;
-          const float m_new_use = (m_new == -INFINITY) ? 0.f : m_new;
-          const float alpha = move ? ex2_approx(m_run - m_new_use) : 1.f;
-          float sum0 = 0.f, sum1 = 0.f;
-#pragma unroll
-          for (int q = 0; q < BN / 32; ++q) {
-            uint32_t pk[16];
-#pragma unroll
-            for (int c = 0; c < 32; c += 2) {
-              float a, b;
-              ffma2(a, b, x[q * 32 + c], x[q * 32 + c + 1], sl2, sl2, -m_new_use, -m_new_use);
-              a = ex2_approx(a);
-              b = ex2_approx(b);
-              fadd2(sum0, sum1, sum0, sum1, a, b);
-              // P in bf16 (half a step, 2^-8 of each weight; l sums the unrounded
-              // values): the second product's operand type
-              pk[c >> 1] = pack_bf16x2(a, b);
-            }
-            tmem_st16(s_addr + q * 16, pk);
-          }
-          l_run = l_run * alpha + (sum0 + sum1);
-          const bool need = t > (dual ? 0 : s) && move;
-          if (__any_sync(0xffffffffu, need)) {
-            const float a = need ? alpha : 1.f;
-            uint32_t v[32];
-#pragma unroll
-            for (int q = 0; q < D / 32; ++q) {
-              tmem_ld32(o_addr + q * 32, v);
-              tmem_wait_ld();
-#pragma unroll
-              for (int c = 0; c < 32; ++c) v[c] = __float_as_uint(__uint_as_float(v[c]) * a);
-              tmem_st32(o_addr + q * 32, v);
-            }
-          }
-          tmem_wait_st();
-          m_run = m_new;
-          m_use = m_new_use;
+          phases ^= 1u << v_bit;
         }
         tc_fence_before();
         mbar_arrive(p_full + s);
       }
-      if (ok) ok = mbar_wait_warp(o_full + s, done & 1, abort_flag, p.timeout_ns);
       if (!ok) break;
-      ++done;
+      if (more) factor = q_ready(np);
+      if (dual) dual_seq += 2 * T;
+      ok = wait_warp(o_full + s, i & 1, abort_flag, p.timeout_ns);
+      if (!ok) break;
       tc_fence_after();
-      // the query tile is free (its last product is done): the next piece's rows
-      // go in before this one's store, so that its first S overlaps the store
-      i = find(i + 1);
-      if (i < last) load_q();
       if (warp_live) {
         const bool none = l_run == 0.f;  // (a NaN sum is not none)
-        const float inv = none ? 0.f : 1.f / l_run;
-        const long long row = (long long)pc.ws_row + r +
-                              ((pc.flags & kPieceSplit) && s == 1 ? pc.rows : 0);
+        const float inv = none ? 0.f : exp2_int(ev) / l_run;
+        const long long row = (long long)pc.ws_row + copy * pc.rows + r;
         float* dst = p.ws_o + row * D;
 #pragma unroll
         for (int q = 0; q < D / 32; ++q) {
@@ -586,14 +882,20 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
   // ---- teardown ----
   tc_fence_before();
   __syncthreads();
-  if (warp == C::kProducerWarp) {
+  if (warp == kProducerWarp) {
     if (lane == 0 && *abort_flag) {
-      // let the copies in flight land before the shared memory goes
-      constexpr int kSt = QUANT ? C::kRawStages : C::kStages;
-      uint64_t* const fullb = QUANT ? raw_full : full;
-      const int n = *issued_loads;
-      for (int j = max(0, n - kSt); j < n; ++j)
-        mbar_wait(fullb + j % kSt, (j / kSt) & 1, nullptr, p.timeout_ns);
+      // let the copies in flight land before the shared memory goes: the last load of
+      // each barrier that had one (a barrier without loads passes: its phase before
+      // the first counts as done)
+      if constexpr (QUANT) {
+        const int n = *issued_loads;
+        for (int j = max(0, n - C::kRawStages); j < n; ++j)
+          wait_one(raw_full + j % C::kRawStages, (j / C::kRawStages) & 1, nullptr, p.timeout_ns);
+      } else {
+        const uint32_t phases = (uint32_t)*issued_phases;
+        for (int b = 0; b < 3 * C::kStages; ++b)
+          wait_one(full + b, ((phases >> b) & 1) ^ 1, nullptr, p.timeout_ns);
+      }
     }
     __syncwarp();
     tc_fence_after();
@@ -601,83 +903,158 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
   }
 }
 
-// One warp per (query row, head): its partials, in the order of its segments.
+// Merge of a row's partials, one warp per (query row, head).  Latency bound: a lane
+// finds one partial each (the plan's words, read before the wait for the attention
+// kernel), so that after the wait two dependent loads are left, the L of all
+// partials and their O.
+constexpr int kMergeThreads = 256;
 template <int D>
-__global__ void __launch_bounds__(256) shared_merge_kernel(const SharedParams p) {
-  constexpr int E = D / 32;
-  const int lane = threadIdx.x & 31;
-  grid_dep_wait();  // the attention kernel before this one wrote the partials
-  const long long u = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-  if (u >= (long long)p.num_q_rows * p.Hq) return;
+__device__ __forceinline__ void merge_row(const SharedParams& p, long long u, int lane) {
+  constexpr int E = D / 32;  // columns of a lane
+  const unsigned all = 0xffffffffu;
   const int n = (int)(u / p.Hq), h = (int)(u % p.Hq), kvh = h / p.g, j = h % p.g;
-  const int e0 = p.table[p.row_first + n], e1 = p.table[p.row_first + n + 1];
-  if (e0 == e1) return;
-  if (e0 < 0 || e1 > p.num_entries) {
+  const int e0 = __ldg(p.table + p.row_first + n), e1 = __ldg(p.table + p.row_first + n + 1);
+  if (e0 == e1) return;  // a row of no segment
+  if (e0 < 0 || e1 < e0 || e1 > p.num_entries) {
     if (lane == 0) set_status(p.status, CPATTN_ERR_RANGE);
     return;
   }
   float m = -INFINITY, sw = 0.f, acc[E];
 #pragma unroll
   for (int c = 0; c < E; ++c) acc[c] = 0.f;
-  for (int e = e0; e < e1; ++e) {
-    const long long packed = (long long)p.table[p.entries + 2 * e + 1] * p.g + j;
-    const long long unit = p.table[p.entries + 2 * e] + packed / kRows * p.Hkv + kvh;
-    if (packed < 0 || unit < 0 || unit >= p.num_units) {
+  bool waited = false;
+  for (int eb = e0; eb < e1; eb += 32) {
+    // lane e: the pieces of entry eb + e, and the row's place in their partials
+    int p0 = 0, count = 0, at = 0, reps = 1;
+    bool ok = true;
+    if (eb + lane < e1) {
+      const int2 en = __ldg(reinterpret_cast<const int2*>(p.table + p.entries) + eb + lane);
+      const long long packed = (long long)en.y * p.g + j;
+      const long long unit = en.x + packed / kRows * p.Hkv + kvh;
+      ok = en.x >= 0 && en.y >= 0 && unit < p.num_units;
+      if (ok) {
+        const int2 pr = __ldg(reinterpret_cast<const int2*>(p.table + p.units) + unit);
+        ok = pr.x >= 0 && pr.x <= pr.y && pr.y <= p.num_pieces;
+        p0 = pr.x;
+        at = (int)(packed % kRows);
+        if (pr.y > pr.x) reps = shared_reps(__ldg(p.table + p.pieces + 12LL * p0 + 4));  // rows
+        count = (pr.y - pr.x) * reps;
+      }
+    }
+    if (!__all_sync(all, ok)) {
       if (lane == 0) set_status(p.status, CPATTN_ERR_RANGE);
       return;
     }
-    const int p0 = p.table[p.unit_first + unit], p1 = p.table[p.unit_first + unit + 1];
-    if (p0 < 0 || p1 > p.num_pieces) {
-      if (lane == 0) set_status(p.status, CPATTN_ERR_RANGE);
-      return;
-    }
-    for (int i = p0; i < p1; ++i) {
-      const SharedPiece& pc = reinterpret_cast<const SharedPiece*>(p.table + p.pieces)[i];
-      for (int part = 0; part <= (pc.flags & kPieceSplit ? 1 : 0); ++part) {
-        const long long row = (long long)pc.ws_row + packed % kRows + part * pc.rows;
-        if (row < 0 || row >= p.ws_rows) {
-          if (lane == 0) set_status(p.status, CPATTN_ERR_RANGE);
-          return;
-        }
-        const float lj = p.ws_l[row];
-        const float mn = fmaxf(m, lj);
-        const float use = mn == -INFINITY ? 0.f : mn;  // a NaN partial stays one
-        const float a = exp2f(m - use), w = exp2f(lj - use);
-        sw = sw * a + w;
+    int upto = count;  // partials of this entry and those before it
 #pragma unroll
-        for (int c = 0; c < E; ++c) acc[c] = fmaf(acc[c], a, w * p.ws_o[row * D + lane * E + c]);
-        m = mn;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(all, upto, o);
+      if (lane >= o) upto += x;
+    }
+    const int total = __shfl_sync(all, upto, 31), entries = min(32, e1 - eb);
+    for (int b = 0; b < total; b += 32) {
+      // lane l: partial b + l
+      int piece = 0, off = 0, copy = 0;
+      for (int e = 0; e < entries; ++e) {
+        const int end = __shfl_sync(all, upto, e), cnt = __shfl_sync(all, count, e);
+        const int first = __shfl_sync(all, p0, e), a = __shfl_sync(all, at, e);
+        const int k = __shfl_sync(all, reps, e), i = b + lane - (end - cnt);
+        if (i >= 0 && b + lane < end) {
+          piece = first + i / k;  // k is 1, 2 or 4
+          copy = i % k;
+          off = a;
+        }
+      }
+      const bool mine = b + lane < total;
+      long long row = 0;
+      if (mine) {
+        const int32_t* pc = p.table + p.pieces + 12LL * piece;
+        row = (long long)__ldg(pc + 9) + (long long)copy * __ldg(pc + 4) + off;  // ws_row, rows
+      }
+      if (!__all_sync(all, row >= 0 && row < p.ws_rows)) {
+        if (lane == 0) set_status(p.status, CPATTN_ERR_RANGE);
+        return;
+      }
+      if (!waited) grid_dep_wait();  // the attention kernel before this one wrote the partials
+      waited = true;
+      const float l = mine ? __ldcg(p.ws_l + row) : -INFINITY;
+      float mx = l;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(all, mx, o));
+      const float mn = fmaxf(m, mx), use = mn == -INFINITY ? 0.f : mn;
+      const float w = exp2f(l - use);  // (a NaN partial stays one)
+      float ws = w;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) ws += __shfl_xor_sync(all, ws, o);
+      const float old = exp2f(m - use);
+      sw = sw * old + ws;
+#pragma unroll
+      for (int c = 0; c < E; ++c) acc[c] *= old;
+      m = mn;
+      const int cnt = min(32, total - b);
+#pragma unroll 8
+      for (int i = 0; i < cnt; ++i) {
+        const float wi = __shfl_sync(all, w, i);
+        const float* src = p.ws_o + __shfl_sync(all, row, i) * D + lane * E;
+        float x[E];
+        if constexpr (E == 4) {
+          const float4 f = __ldcg(reinterpret_cast<const float4*>(src));
+          x[0] = f.x; x[1] = f.y; x[2] = f.z; x[3] = f.w;
+        } else {
+          const float2 f = __ldcg(reinterpret_cast<const float2*>(src));
+          x[0] = f.x; x[1] = f.y;
+        }
+#pragma unroll
+        for (int c = 0; c < E; ++c) acc[c] = fmaf(wi, x[c], acc[c]);
       }
     }
   }
+  if (!waited) grid_dep_wait();
   const float inv = sw == 0.f ? 0.f : 1.f / sw;
-  const long long out = ((long long)n * p.Hq + h) * D + lane * E;
 #pragma unroll
-  for (int c = 0; c < E; ++c) {
-    if (p.o_f32) static_cast<float*>(p.o)[out + c] = acc[c] * inv;
-    else static_cast<__nv_bfloat16*>(p.o)[out + c] = __float2bfloat16_rn(acc[c] * inv);
+  for (int c = 0; c < E; ++c) acc[c] *= inv;
+  const long long out = u * D + lane * E;
+  if (p.o_f32) {
+    float* o = static_cast<float*>(p.o) + out;
+    if constexpr (E == 4) *reinterpret_cast<float4*>(o) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+    else *reinterpret_cast<float2*>(o) = make_float2(acc[0], acc[1]);
+  } else {
+    __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.o) + out;
+    if constexpr (E == 4)
+      *reinterpret_cast<uint2*>(o) = make_uint2(pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3]));
+    else
+      *reinterpret_cast<uint32_t*>(o) = pack_bf16x2(acc[0], acc[1]);
   }
-  if (lane == 0) p.lse[(long long)n * p.Hq + h] = sw == 0.f ? -INFINITY : (m + log2f(sw)) * kLn2;
+  if (lane == 0) p.lse[u] = sw == 0.f ? -INFINITY : (m + log2f(sw)) * kLn2;
+}
+template <int D>
+__global__ void __launch_bounds__(kMergeThreads) shared_merge_kernel(const SharedParams p) {
+  const long long u = ((long long)blockIdx.x * kMergeThreads + threadIdx.x) >> 5;
+  if (u < (long long)p.num_q_rows * p.Hq) merge_row<D>(p, u, threadIdx.x & 31);
+  grid_dep_wait();  // no block ends before the kernel that this launch may overlap
 }
 
-// 3-D map of a code buffer (cols, heads, rows) with a D-column x 1-head x 128-row
-// box, rows packed in shared memory; out-of-range rows read as zero.
+// 3-D map of a code buffer (cols, heads, rows) with a D-column x 1-head box, rows
+// packed in shared memory; out-of-range rows read as zero.
 bool make_code_map(CUtensorMap* m, const void* base, int cols, int heads, long long rows,
-                   long long head_stride, long long row_stride) {
+                   long long head_stride, long long row_stride, int box_rows) {
   auto enc = tensor_map_encoder();
   if (!enc) return false;
   cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)heads, (cuuint64_t)rows};
   cuuint64_t strides[2] = {(cuuint64_t)head_stride, (cuuint64_t)row_stride};
-  cuuint32_t box[3] = {(cuuint32_t)cols, 1, BN};
+  cuuint32_t box[3] = {(cuuint32_t)cols, 1, (cuuint32_t)box_rows};
   cuuint32_t estr[3] = {1, 1, 1};
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+struct SharedMaps {  // full tiles, then the tail boxes
+  CUtensorMap k, v, k_tail, v_tail;
+};
+
 template <int D, bool QUANT>
-int launch_shared(const CUtensorMap& mk, const CUtensorMap& mv, const SharedParams& p, int num_ctas,
-                  cudaStream_t stream) {
+int launch_shared(const SharedMaps& m, const SharedParams& p, int num_ctas, cudaStream_t stream) {
   using C = SharedCfg<D, QUANT>;
   auto kern = attn_shared_kernel<D, QUANT>;
   if (!allow_smem(kern, C::kSmemBytes)) return CPATTN_ERR_CUDA;
@@ -693,8 +1070,8 @@ int launch_shared(const CUtensorMap& mk, const CUtensorMap& mv, const SharedPara
                   : -1;
   }
   if (regs_ok < 0) return CPATTN_ERR_UNSUPPORTED;
-  return launch_kernel(kern, (unsigned)num_ctas, C::kThreads, C::kSmemBytes, stream, false, mk, mv,
-                       p) == cudaSuccess
+  return launch_kernel(kern, (unsigned)num_ctas, C::kThreads, C::kSmemBytes, stream, false, m.k, m.v,
+                       m.k_tail, m.v_tail, p) == cudaSuccess
              ? CPATTN_OK
              : CPATTN_ERR_CUDA;
 }
@@ -740,10 +1117,10 @@ extern "C" int cp_attn_shared(const cp_shared_plan_t* plan, const int32_t* table
   const SharedTable T = shared_table(*plan);
   SharedParams p{};
   p.table = table_dev;
-  p.unit_first = T.unit_first;
+  p.pieces = T.pieces;
+  p.units = T.units;
   p.row_first = T.row_first;
   p.entries = T.entries;
-  p.pieces = T.pieces;
   p.num_units = plan->num_units;
   p.num_pieces = plan->num_pieces;
   p.num_entries = plan->num_entries;
@@ -768,21 +1145,27 @@ extern "C" int cp_attn_shared(const cp_shared_plan_t* plan, const int32_t* table
   p.status = status_dev;
   p.timeout_ns = attn_debug().timeout_ns;
   if (plan->num_pieces > 0) {
-    CUtensorMap mk, mv;
-    if (quant ? !make_code_map(&mk, k, d, plan->Hkv, num_kv_rows, k_head_stride, k_row_stride) ||
-                    !make_code_map(&mv, v, dv, plan->Hkv, num_kv_rows, v_head_stride, v_row_stride)
-              : !make_map(&mk, k, d, plan->Hkv, num_kv_rows, k_head_stride, k_row_stride) ||
-                    !make_map(&mv, v, dv, plan->Hkv, num_kv_rows, v_head_stride, v_row_stride))
+    SharedMaps m;
+    auto map = [&](CUtensorMap* t, const void* base, int dim, int64_t hs, int64_t rs, int box_rows) {
+      return quant ? make_code_map(t, base, dim, plan->Hkv, num_kv_rows, hs, rs, box_rows)
+                   : make_map(t, base, dim, plan->Hkv, num_kv_rows, hs, rs, box_rows);
+    };
+    if (!map(&m.k, k, d, k_head_stride, k_row_stride, BN) ||
+        !map(&m.v, v, dv, v_head_stride, v_row_stride, BN) ||
+        !map(&m.k_tail, k, d, k_head_stride, k_row_stride, kTailRows) ||
+        !map(&m.v_tail, v, dv, v_head_stride, v_row_stride, kTailRows))
       return CPATTN_ERR_CUDA;
-    const int r = d == 128 ? (quant ? launch_shared<128, true>(mk, mv, p, plan->num_ctas, stream)
-                                    : launch_shared<128, false>(mk, mv, p, plan->num_ctas, stream))
-                           : (quant ? launch_shared<64, true>(mk, mv, p, plan->num_ctas, stream)
-                                    : launch_shared<64, false>(mk, mv, p, plan->num_ctas, stream));
+    const int n = plan->num_ctas;
+    const int r = d == 128 ? (quant ? launch_shared<128, true>(m, p, n, stream)
+                                    : launch_shared<128, false>(m, p, n, stream))
+                           : (quant ? launch_shared<64, true>(m, p, n, stream)
+                                    : launch_shared<64, false>(m, p, n, stream));
     if (r != CPATTN_OK) return r;
   }
-  const long long blocks = ((long long)plan->num_q_rows * plan->Hq + 7) / 8;
+  const long long warps = kMergeThreads / 32;
+  const long long blocks = ((long long)plan->num_q_rows * plan->Hq + warps - 1) / warps;
   if (blocks > 0x7fffffffLL) return CPATTN_ERR_TOO_LARGE;
   const cudaError_t e = launch_kernel(d == 128 ? shared_merge_kernel<128> : shared_merge_kernel<64>,
-                                      (unsigned)blocks, 256, 0, stream, true, p);
+                                      (unsigned)blocks, kMergeThreads, 0, stream, true, p);
   return e == cudaSuccess ? CPATTN_OK : CPATTN_ERR_CUDA;
 }

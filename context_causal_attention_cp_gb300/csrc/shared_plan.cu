@@ -1,13 +1,14 @@
 // Host plan of cp_attn_shared: units, their cut into pieces and the merge lists.
 //
-// The units (segment, packed-row tile, KV head) are walked in a fixed order and
-// their keys dealt to the thread blocks one after the other: each block is
-// filled up to a budget, so a unit is cut only where a block is full, and every
-// block's cost is within a tile of the others'.  The smallest budget that needs
-// no more than num_ctas blocks is found by bisection.  A piece costs its KV
+// The units (segment, packed-row tile, KV head), dual ones first, are walked in a
+// fixed order and their keys dealt to the thread blocks one after the other: each
+// block is filled up to a budget, so a unit is cut only where a block is full, and
+// every block's cost is within a KV tile of the others'.  The smallest budget that
+// needs no more than num_ctas blocks is found by bisection.  A piece costs its KV
 // tiles plus a fixed part (its queries' load and its partial's store), so that
-// short units are not shredded.  Nothing is allocated: each pass walks the
-// segment table again.
+// short units are not shredded.  A block's run of small units is cut once more, at
+// half its KV tiles, between the block's two streams.  Nothing is allocated: each
+// pass walks the segment table again.
 #include <algorithm>
 #include <cstdint>
 
@@ -17,74 +18,138 @@ namespace cpattn {
 namespace {
 
 constexpr int kKeys = kSharedTileKeys;
-constexpr int kTileCost = 16;       // one KV tile for one MMA tile of rows
-constexpr int kDualCost = 24;       // one KV tile for two
-constexpr int kPieceCost = 16;      // a piece's fixed part
-constexpr int tile_cost(int rows) { return shared_dual(rows) ? kDualCost : kTileCost; }
-// partial rows that a piece leaves
-constexpr bool split(int rows, long long keys) { return !shared_dual(rows) && keys > kKeys; }
-constexpr int parts(int rows, long long keys) { return split(rows, keys) ? 2 * rows : rows; }
+#ifndef CPATTN_SHARED_COSTS
+#define CPATTN_SHARED_COSTS 16, 24, 16
+#endif
+constexpr int kCosts[3] = {CPATTN_SHARED_COSTS};
+constexpr int kTileCost = kCosts[0];   // one KV tile for one MMA tile of rows
+constexpr int kDualCost = kCosts[1];   // one KV tile for two
+constexpr int kPieceCost = kCosts[2];  // a piece's fixed part
 constexpr long long kMaxUnits = 1LL << 22;
+constexpr int kMaxCtas = 4096;
 
 long long last_pos(const cp_segment_t& s) {
   return (long long)s.q_pos0 + (long long)(s.q_len - 1) * s.q_pos_step;
 }
+long long num_tiles(const cp_segment_t& s, int g) {
+  return ((long long)s.q_len * g + CPATTN_SHARED_ROWS - 1) / CPATTN_SHARED_ROWS;
+}
+long long kv_tiles(long long keys) { return (keys + kKeys - 1) / kKeys; }
 
-// Calls f(segment, tile, rows, keys) for every packed-row tile: `keys` that its
-// last row sees (its other rows see no more).
-template <class F>
-void for_each_tile(const cp_segment_t* segs, int num_segs, int g, F&& f) {
-  for (int i = 0; i < num_segs; ++i) {
-    const cp_segment_t& s = segs[i];
-    const long long packed = (long long)s.q_len * g;
-    for (long long r0 = 0; r0 < packed; r0 += CPATTN_SHARED_ROWS) {
-      const int rows = (int)std::min<long long>(CPATTN_SHARED_ROWS, packed - r0);
-      const long long pos = s.q_pos0 + ((r0 + rows - 1) / g) * s.q_pos_step;
-      f(s, r0, rows, std::max<long long>(0, pos + 1));
+// The line of all units' keys.
+struct Line {
+  const cp_segment_t* segs;
+  int num_segs, g, Hkv;
+};
+// A place in the line: the next key to deal is key0 of the unit (seg, tile, head).
+struct Place {
+  bool dual = true;      // dual units first, then the others
+  bool end = false;
+  int seg = 0, head = 0;
+  long long tile = 0, key0 = 0;
+  long long unit0 = 0;   // unit of (seg, tile 0, head 0)
+  int rows = 0;          // of the unit
+  long long keys = 0;    // that the unit's last row sees (its other rows no more)
+};
+struct Cut {
+  const cp_segment_t* seg;
+  long long unit, r0, key0, keys;
+  int rows, head;
+};
+
+void measure(const Line& L, Place& p) {
+  const cp_segment_t& s = L.segs[p.seg];
+  const long long packed = (long long)s.q_len * L.g, r0 = p.tile * CPATTN_SHARED_ROWS;
+  p.rows = (int)std::min<long long>(CPATTN_SHARED_ROWS, packed - r0);
+  const long long pos = s.q_pos0 + ((r0 + p.rows - 1) / L.g) * s.q_pos_step;
+  p.keys = std::max<long long>(0, pos + 1);
+}
+// Moves p on to the next key, if it is past the last of its unit (or at a unit of
+// the other kind or without keys).
+void settle(const Line& L, Place& p) {
+  while (!p.end) {
+    if (p.seg >= L.num_segs) {
+      if (!p.dual) {
+        p.end = true;
+        return;
+      }
+      p = Place{};
+      p.dual = false;
+      continue;
+    }
+    if (p.tile >= num_tiles(L.segs[p.seg], L.g)) {
+      p.unit0 += p.tile * L.Hkv;
+      ++p.seg;
+      p.tile = p.key0 = 0;
+      p.head = 0;
+      continue;
+    }
+    measure(L, p);
+    if (shared_dual(p.rows) != p.dual || p.keys == 0) {
+      ++p.tile;
+      p.head = 0;
+      p.key0 = 0;
+      continue;
+    }
+    if (p.key0 < p.keys) return;
+    p.key0 = 0;
+    if (++p.head >= L.Hkv) {
+      p.head = 0;
+      ++p.tile;
     }
   }
 }
-
-// Deals every unit's keys; calls f(cta, segment, r0, rows, head, key0, keys) for
-// each piece and u(segment, r0, rows, head) before a unit's first piece.
-// Returns the number of blocks used, or max_ctas + 1 as soon as they do not do.
-template <class U, class F>
-int deal(const cp_segment_t* segs, int num_segs, int g, int Hkv, long long budget, int max_ctas,
-         U&& u, F&& f) {
-  int cta = 0;
+// One thread block's share: calls f(cut) for each of its pieces.
+template <class F>
+void share(const Line& L, Place& p, long long budget, F&& f) {
   long long used = 0;
-  bool full = false;
-  for_each_tile(segs, num_segs, g, [&](const cp_segment_t& s, long long r0, int rows,
-                                       long long keys) {
-    for (int h = 0; h < Hkv && !full; ++h) {
-      u(s, r0, rows, h);
-      long long key0 = 0;
-      while (key0 < keys) {
-        const long long tiles = (keys - key0 + kKeys - 1) / kKeys;
-        long long fit = (budget - used - kPieceCost) / tile_cost(rows);
-        if (fit < 1) {
-          if (++cta >= max_ctas) {
-            full = true;
-            return;
-          }
-          used = 0;
-          continue;
-        }
-        fit = std::min(fit, tiles);
-        const long long n = std::min(keys - key0, fit * kKeys);
-        f(cta, s, r0, rows, h, key0, n);
-        key0 += n;
-        used += kPieceCost + fit * tile_cost(rows);
+  for (settle(L, p); !p.end; settle(L, p)) {
+    const long long cost = p.dual ? kDualCost : kTileCost;
+    const long long fit = std::min((budget - used - kPieceCost) / cost, kv_tiles(p.keys - p.key0));
+    if (fit < 1) return;
+    const long long n = std::min(p.keys - p.key0, fit * kKeys);
+    f(Cut{L.segs + p.seg, p.unit0 + p.tile * L.Hkv + p.head, p.tile * CPATTN_SHARED_ROWS, p.key0, n,
+          p.rows, p.head});
+    p.key0 += n;
+    used += kPieceCost + fit * cost;
+  }
+}
+bool fits(const Line& L, long long budget, int num_ctas) {
+  Place p;
+  for (int c = 0; c < num_ctas; ++c) share(L, p, budget, [](const Cut&) {});
+  settle(L, p);
+  return p.end;
+}
+// Calls f(cta, cut, stream) for every piece in the table's order of each kind:
+// stream -1 for dual pieces, else the stream that has it.
+template <class F>
+void deal(const Line& L, long long budget, int num_ctas, F&& f) {
+  Place p;
+  for (int c = 0; c < num_ctas; ++c) {
+    Place ahead = p;
+    long long tiles = 0;
+    share(L, ahead, budget, [&](const Cut& k) { if (!shared_dual(k.rows)) tiles += kv_tiles(k.keys); });
+    long long left = (tiles + 1) / 2;  // KV tiles that stream 0 still takes
+    share(L, p, budget, [&](const Cut& k) {
+      if (shared_dual(k.rows)) {
+        f(c, k, -1);
+        return;
       }
-    }
-  });
-  return full ? max_ctas + 1 : cta + 1;
+      Cut a = k, b = k;
+      a.keys = std::min(k.keys, left * kKeys);
+      b.key0 += a.keys;
+      b.keys -= a.keys;
+      left -= kv_tiles(a.keys);
+      if (a.keys > 0) f(c, a, 0);
+      if (b.keys > 0) f(c, b, 1);
+    });
+  }
 }
 
 bool plan_ok(const cp_shared_plan_t& p) {
   return p.num_q_rows >= 0 && p.Hq >= 1 && p.Hkv >= 1 && p.Hq % p.Hkv == 0 && p.num_ctas >= 1 &&
-         p.num_ctas <= 4096 && p.num_units >= 0 && p.num_pieces >= 0 && p.num_entries >= 0 &&
-         p.kv_rows >= 0 && p.ws_rows >= 0 && p.table_ints == shared_table(p).total;
+         p.num_ctas <= kMaxCtas && p.num_units >= 0 && p.num_pieces >= 0 && p.num_entries >= 0 &&
+         p.kv_rows >= 0 && p.budget >= 0 && p.ws_rows >= 0 && p.table_ints == shared_table(p).total;
 }
 
 int check_segments(const cp_segment_t* segs, int num_segs, int num_q_rows) {
@@ -107,43 +172,43 @@ using namespace cpattn;
 extern "C" int cp_shared_plan_size(const cp_segment_t* segs, int num_segs, int num_q_rows, int Hq,
                                    int Hkv, int num_ctas, cp_shared_plan_t* plan) {
   if (!plan || num_segs < 0 || (num_segs > 0 && !segs) || num_q_rows < 0 || Hq < 1 || Hkv < 1 ||
-      Hq % Hkv != 0 || num_ctas < 1 || num_ctas > 4096)
+      Hq % Hkv != 0 || num_ctas < 1 || num_ctas > kMaxCtas)
     return CPATTN_ERR_INVALID_ARG;
   if (num_segs > kMaxUnits) return CPATTN_ERR_TOO_LARGE;
   const int rc = check_segments(segs, num_segs, num_q_rows);
   if (rc != CPATTN_OK) return rc;
-  const int g = Hq / Hkv;
+  const Line L{segs, num_segs, Hq / Hkv, Hkv};
   long long tiles = 0, entries = 0, kv_rows = 0;
   for (int i = 0; i < num_segs; ++i) {
     const cp_segment_t& s = segs[i];
-    tiles += ((long long)s.q_len * g + CPATTN_SHARED_ROWS - 1) / CPATTN_SHARED_ROWS;
+    tiles += num_tiles(s, L.g);
     entries += s.q_len;
     if (s.q_len > 0)
       kv_rows = std::max(kv_rows, s.kv_row0 + std::max<long long>(0, last_pos(s) + 1));
   }
   if (tiles * Hkv > kMaxUnits || entries > 0x3fffffffLL) return CPATTN_ERR_TOO_LARGE;
   long long cost = 0;
-  for_each_tile(segs, num_segs, g, [&](const cp_segment_t&, long long, int rows, long long keys) {
-    if (keys > 0) cost += (kPieceCost + (keys + kKeys - 1) / kKeys * tile_cost(rows)) * Hkv;
-  });
-  // one block more than the average needs at most: the average, a whole piece
-  // and a cut on either side
-  long long lo = kPieceCost + kTileCost, hi = cost / num_ctas + 2 * (kPieceCost + kDualCost);
-  auto none = [](auto&&...) {};
-  while (deal(segs, num_segs, g, Hkv, hi, num_ctas, none, none) > num_ctas) hi *= 2;
+  {
+    Place p;
+    share(L, p, INT64_MAX / 4, [&](const Cut& k) {
+      cost += kPieceCost + kv_tiles(k.keys) * (shared_dual(k.rows) ? kDualCost : kTileCost);
+    });
+  }
+  long long lo = kPieceCost + std::min(kTileCost, kDualCost);
+  long long hi = std::max(lo, cost / num_ctas + 2 * (kPieceCost + kDualCost));
+  while (!fits(L, hi, num_ctas)) hi *= 2;
   while (lo < hi) {
     const long long mid = (lo + hi) / 2;
-    if (deal(segs, num_segs, g, Hkv, mid, num_ctas, none, none) <= num_ctas) hi = mid;
+    if (fits(L, mid, num_ctas)) hi = mid;
     else lo = mid + 1;
   }
   if (hi > 0x7fffffffLL) return CPATTN_ERR_TOO_LARGE;
   long long pieces = 0, ws_rows = 0;
-  deal(segs, num_segs, g, Hkv, hi, num_ctas, none,
-       [&](int, const cp_segment_t&, long long, int rows, int, long long, long long keys) {
-         ++pieces;
-         ws_rows += parts(rows, keys);
-       });
-  if (ws_rows > 0x7fffffffLL || pieces > 0x7fffffffLL) return CPATTN_ERR_TOO_LARGE;
+  deal(L, hi, num_ctas, [&](int, const Cut& k, int) {
+    ++pieces;
+    ws_rows += shared_reps(k.rows) * k.rows;
+  });
+  if (ws_rows > 0x7fffffffLL) return CPATTN_ERR_TOO_LARGE;
   plan->num_q_rows = num_q_rows;
   plan->Hq = Hq;
   plan->Hkv = Hkv;
@@ -165,32 +230,33 @@ extern "C" int cp_shared_plan(const cp_segment_t* segs, int num_segs, const cp_s
     return CPATTN_ERR_INVALID_ARG;
   const int rc = check_segments(segs, num_segs, plan->num_q_rows);
   if (rc != CPATTN_OK) return rc;
-  const int g = plan->Hq / plan->Hkv, Hkv = plan->Hkv, N = plan->num_q_rows;
-  const SharedTable T = shared_table(*plan);
-  int32_t* cta_first = table;
-  int32_t* unit_first = table + T.unit_first;
-  int32_t* row_first = table + T.row_first;
-  int32_t* entries = table + T.entries;
-  auto* pieces = reinterpret_cast<SharedPiece*>(table + T.pieces);
+  const Line L{segs, num_segs, plan->Hq / plan->Hkv, plan->Hkv};
+  const int N = plan->num_q_rows;
   // the table must be the one that was sized: check the counts before writing
-  long long tiles = 0, ents = 0, np = 0, ws = 0;
+  long long tiles = 0, ents = 0, np = 0, duals = 0, ws = 0;
   for (int i = 0; i < num_segs; ++i) {
-    tiles += ((long long)segs[i].q_len * g + CPATTN_SHARED_ROWS - 1) / CPATTN_SHARED_ROWS;
+    tiles += num_tiles(segs[i], L.g);
     ents += segs[i].q_len;
   }
-  if (tiles * Hkv != plan->num_units || ents != plan->num_entries) return CPATTN_ERR_INVALID_ARG;
-  auto none = [](auto&&...) {};
-  const int used =
-      deal(segs, num_segs, g, Hkv, plan->budget, plan->num_ctas, none,
-           [&](int, const cp_segment_t&, long long, int rows, int, long long, long long keys) {
-             ++np;
-             ws += parts(rows, keys);
-           });
-  if (used > plan->num_ctas || np != plan->num_pieces || ws != plan->ws_rows)
+  if (tiles * L.Hkv != plan->num_units || ents != plan->num_entries ||
+      !fits(L, plan->budget, plan->num_ctas))
     return CPATTN_ERR_INVALID_ARG;
-  for (long long i = T.entries + 2 * ents; i < T.pieces; ++i) table[i] = 0;  // padding
+  deal(L, plan->budget, plan->num_ctas, [&](int, const Cut& k, int stream) {
+    ++np;
+    duals += stream < 0;
+    ws += shared_reps(k.rows) * k.rows;
+  });
+  if (np != plan->num_pieces || ws != plan->ws_rows) return CPATTN_ERR_INVALID_ARG;
+
+  const SharedTable T = shared_table(*plan);
+  auto* ctas = reinterpret_cast<SharedCta*>(table);
+  auto* pieces = reinterpret_cast<SharedPiece*>(table + T.pieces);
+  int32_t* units = table + T.units;
+  int32_t* row_first = table + T.row_first;
+  int32_t* entries = table + T.entries;
 
   // entries of each query row, segment by segment
+  row_first[T.entries - T.row_first - 1] = 0;  // the padding
   for (int n = 0; n <= N; ++n) row_first[n] = 0;
   for (int i = 0; i < num_segs; ++i)
     for (int j = 0; j < segs[i].q_len; ++j) ++row_first[segs[i].q_row0 + j + 1];
@@ -203,34 +269,45 @@ extern "C" int cp_shared_plan(const cp_segment_t* segs, int num_segs, const cp_s
       entries[2 * e] = unit0;
       entries[2 * e + 1] = j;
     }
-    unit0 += (int32_t)(((long long)s.q_len * g + CPATTN_SHARED_ROWS - 1) / CPATTN_SHARED_ROWS) * Hkv;
+    unit0 += (int32_t)num_tiles(s, L.g) * L.Hkv;
   }
   for (int n = N; n > 0; --n) row_first[n] = row_first[n - 1];
   row_first[0] = 0;
 
-  int32_t unit = 0, piece = 0, cta_now = -1, ws_row = 0;
-  deal(segs, num_segs, g, Hkv, plan->budget, plan->num_ctas,
-       [&](const cp_segment_t&, long long, int, int) { unit_first[unit++] = piece; },
-       [&](int cta, const cp_segment_t& s, long long r0, int rows, int h, long long key0,
-           long long keys) {
-         while (cta_now < cta) cta_first[++cta_now] = piece;
-         SharedPiece p{};
-         p.q_row0 = s.q_row0;
-         p.q_pos0 = s.q_pos0;
-         p.q_pos_step = s.q_pos_step;
-         p.r0 = (int32_t)r0;
-         p.rows = rows;
-         p.kv_head = h;
-         p.kv_row = (int32_t)(s.kv_row0 + key0);
-         p.key0 = (int32_t)key0;
-         p.keys = (int32_t)keys;
-         p.ws_row = ws_row;
-         p.flags = split(rows, keys) ? kPieceSplit : 0;
-         ws_row += parts(rows, keys);
-         pieces[piece++] = p;
-       });
-  unit_first[unit] = piece;
-  while (cta_now < plan->num_ctas) cta_first[++cta_now] = piece;
+  for (int u = 0; u < 2 * plan->num_units; ++u) units[u] = 0;
+  for (int c = 0; c < plan->num_ctas; ++c) ctas[c] = SharedCta{};
+  int32_t next[2] = {0, (int32_t)duals}, ws_row = 0;  // next dual and next single piece
+  int cta = -1;
+  auto open = [&](int c) {  // empty ranges from here on
+    while (cta < c) {
+      ++cta;
+      ctas[cta].dual0 = ctas[cta].dual1 = next[0];
+      ctas[cta].single0 = ctas[cta].single1 = ctas[cta].single2 = next[1];
+    }
+  };
+  deal(L, plan->budget, plan->num_ctas, [&](int c, const Cut& k, int stream) {
+    open(c);
+    const int32_t at = next[stream >= 0]++;
+    if (stream < 0) ctas[c].dual1 = at + 1;
+    if (stream == 0) ctas[c].single1 = at + 1;
+    if (stream >= 0) ctas[c].single2 = at + 1;
+    SharedPiece p{};
+    p.q_row0 = k.seg->q_row0;
+    p.q_pos0 = k.seg->q_pos0;
+    p.q_pos_step = k.seg->q_pos_step;
+    p.r0 = (int32_t)k.r0;
+    p.rows = k.rows;
+    p.kv_head = k.head;
+    p.kv_row = (int32_t)(k.seg->kv_row0 + k.key0);
+    p.key0 = (int32_t)k.key0;
+    p.keys = (int32_t)k.keys;
+    p.ws_row = ws_row;
+    ws_row += shared_reps(k.rows) * k.rows;
+    pieces[at] = p;
+    if (units[2 * k.unit] == units[2 * k.unit + 1]) units[2 * k.unit] = at;
+    units[2 * k.unit + 1] = at + 1;
+  });
+  open(plan->num_ctas - 1);
   return CPATTN_OK;
 }
 

@@ -1,13 +1,12 @@
 // Plan table of cp_attn_shared: what the host lays out and the kernels read.
 //
 // Table (int32 words, see cp_shared_plan):
-//   cta_first  [num_ctas + 1]     pieces of thread block c: cta_first[c] .. cta_first[c+1]-1
-//   unit_first [num_units + 1]    pieces of unit u (consecutive)
-//   row_first  [num_q_rows + 1]   entries of query row n
+//   ctas       [num_ctas]         SharedCta: the pieces of each thread block
+//   pieces     [num_pieces]       SharedPiece, those of dual units first
+//   units      [num_units][2]     pieces [first, end) of a unit
+//   row_first  [num_q_rows + 1]   entries of query row n (padded to an even word)
 //   entries    [num_entries][2]   (unit of the row's segment's first tile and KV head 0,
 //                                  row index within the segment)
-//   (padded to 16 bytes)
-//   pieces     [num_pieces]       SharedPiece
 // Unit = (segment, tile of up to CPATTN_SHARED_ROWS packed rows, KV head), numbered
 // tile-major within a segment: unit0 + tile * Hkv + head.
 #pragma once
@@ -26,31 +25,42 @@ struct SharedPiece {
   int32_t kv_row;    // KV row of the piece's first key
   int32_t key0;      // its key number within the segment's run
   int32_t keys;      // keys of the piece, >= 1
-  int32_t ws_row;    // first partial row in the workspace
-  int32_t flags;     // kPieceSplit: two partials, the second at ws_row + rows
-  int32_t unused;
+  int32_t ws_row;    // first partial row in the workspace (reps * rows of them)
+  int32_t unused[2];
 };
 static_assert(sizeof(SharedPiece) == 48, "three 16-byte words");
-constexpr int kPieceSplit = 2;
+
+// The pieces of one thread block.  A unit of more than kSharedTileRows rows is two
+// MMA tiles that use every KV tile (dual); both of the block's softmax warpgroups
+// (streams) work on it.  The pieces of smaller units go to one stream each: stream
+// 0 has [single0, single1), stream 1 [single1, single2), and stream 0 has as many
+// KV tiles as stream 1 or one more.
+struct SharedCta {
+  int32_t dual0, dual1, single0, single1, single2;
+  int32_t unused[3];
+};
+static_assert(sizeof(SharedCta) == 32, "two 16-byte words");
+
 constexpr int kSharedTileRows = 128;  // packed rows of one MMA tile
 constexpr int kSharedTileKeys = 128;  // keys of one KV tile
+__host__ __device__ constexpr bool shared_dual(int rows) { return rows > kSharedTileRows; }
 
-// A unit of more than kSharedTileRows rows is two MMA tiles that use every KV
-// tile (dual).  A smaller one is a single MMA tile whose KV tiles are dealt
-// alternately to the two softmax warpgroups; each keeps its own sum, so a piece
-// of two or more KV tiles leaves two partials (split).
-__host__ __device__ __forceinline__ bool shared_dual(int rows) { return rows > kSharedTileRows; }
+// A unit of at most 64 (32) rows fills its MMA tile with 2 (4) copies of them, and
+// copy c works on the c-th half (quarter) of the keys of every KV tile: the MMAs
+// cost the same, and all four warps of a stream share the exponentials.  Each copy
+// leaves a partial result: a piece has reps * rows partial rows, copy-major.
+__host__ __device__ constexpr int shared_reps(int rows) { return rows <= 32 ? 4 : rows <= 64 ? 2 : 1; }
 
 struct SharedTable {
-  long long unit_first, row_first, entries, pieces, total;  // word offsets (cta_first at 0)
+  long long pieces, units, row_first, entries, total;  // word offsets (ctas at 0)
 };
 inline SharedTable shared_table(const cp_shared_plan_t& p) {
   SharedTable t;
-  t.unit_first = (long long)p.num_ctas + 1;
-  t.row_first = t.unit_first + p.num_units + 1;
-  t.entries = t.row_first + p.num_q_rows + 1;
-  t.pieces = (t.entries + 2LL * p.num_entries + 3) & ~3LL;
-  t.total = t.pieces + (long long)p.num_pieces * (long long)(sizeof(SharedPiece) / 4);
+  t.pieces = p.num_ctas * (long long)(sizeof(SharedCta) / 4);
+  t.units = t.pieces + p.num_pieces * (long long)(sizeof(SharedPiece) / 4);
+  t.row_first = t.units + 2LL * p.num_units;
+  t.entries = (t.row_first + p.num_q_rows + 2) & ~1LL;
+  t.total = t.entries + 2LL * p.num_entries;
   return t;
 }
 

@@ -283,12 +283,14 @@ def test_table_that_does_not_match_is_reported():
     q, k, v, _, _, _ = make(11, 4, 600, 8, 2, 128, False)
     plan = cpa.make_shared_plan([1] * 4, [10, 20, 30, 40], 300, 8, 2)
     i = plan.info
-    pieces = (i.num_ctas + 1 + i.num_units + 1 + i.num_q_rows + 1 + 2 * i.num_entries + 3) // 4 * 4
-    unit_first, entries = i.num_ctas + 1, i.num_ctas + 1 + i.num_units + 1 + i.num_q_rows + 1
-    for at, value in ((pieces + 0, 4), (pieces + 4, 257), (pieces + 5, 2), (pieces + 6, 590),
-                      (pieces + 8, 0), (pieces + 9, int(i.ws_rows)), (pieces + 6, -1),
-                      (i.num_ctas, i.num_pieces + 1), (0, -1), (unit_first + i.num_units, 1 << 30),
-                      (entries, i.num_units), (entries + 1, -1)):
+    pieces = 8 * i.num_ctas
+    units = pieces + 12 * i.num_pieces
+    entries = (units + 2 * i.num_units + i.num_q_rows + 2) // 2 * 2
+    for at, value in ((pieces + 0, 4), (pieces + 4, 257), (pieces + 4, 200), (pieces + 5, 2),
+                      (pieces + 6, 590), (pieces + 6, -1), (pieces + 8, 0),
+                      (pieces + 9, int(i.ws_rows)), (4, i.num_pieces + 1), (2, -1), (1, 1),
+                      (units + 2 * i.num_units - 1, 1 << 30), (entries, i.num_units),
+                      (entries + 1, -1)):
         table = plan.table.clone()
         table[at] = value
         bad = cpa.SharedPlan(i, table, plan.segs_host)

@@ -14,39 +14,54 @@ from context_causal_attention_cp_gb300 import _lib as L
 from oracle import shared as osh
 
 ROWS = 256  # CPATTN_SHARED_ROWS
+CTA = ("dual0", "dual1", "single0", "single1", "single2", "u0", "u1", "u2")
 PIECE = ("q_row0", "q_pos0", "q_pos_step", "r0", "rows", "kv_head", "kv_row", "key0", "keys",
-         "ws_row", "flags", "unused")
+         "ws_row", "u0", "u1")
 
 
 def read_table(plan):
     i, t = plan.info, plan.table.tolist()
     at, out = 0, {}
-    for name, n in (("cta_first", i.num_ctas + 1), ("unit_first", i.num_units + 1),
-                    ("row_first", i.num_q_rows + 1), ("entries", 2 * i.num_entries)):
+    for name, n, fields in (("ctas", i.num_ctas, CTA), ("pieces", i.num_pieces, PIECE)):
+        out[name] = [dict(zip(fields, t[at + len(fields) * j: at + len(fields) * (j + 1)]))
+                     for j in range(n)]
+        at += n * len(fields)
+    for name, n in (("units", 2 * i.num_units), ("row_first", i.num_q_rows + 1),
+                    ("entries", 2 * i.num_entries)):
+        at += at % 2 if name == "entries" else 0
         out[name] = t[at: at + n]
         at += n
-    at = (at + 3) // 4 * 4
-    out["pieces"] = [dict(zip(PIECE, t[at + 12 * j: at + 12 * j + 12]))
-                     for j in range(i.num_pieces)]
-    assert at + 12 * i.num_pieces == len(t) == i.table_ints
+    assert at == len(t) == i.table_ints
     return out
+
+
+def tiles_of(pieces):
+    return sum((p["keys"] + 127) // 128 for p in pieces)
 
 
 def check_plan(segs, N, Hq, Hkv, num_ctas):
     plan = cpa.make_shared_plan_segs(torch.tensor(segs, dtype=torch.int32).reshape(-1, 8), N, Hq,
                                      Hkv, num_ctas=num_ctas, device="cpu")
     T, g = read_table(plan), Hq // Hkv
-    assert T["cta_first"][0] == 0 and T["cta_first"][-1] == len(T["pieces"])
-    assert T["cta_first"] == sorted(T["cta_first"])
-    assert T["unit_first"][0] == 0 and T["unit_first"][-1] == len(T["pieces"])
-    # partial rows do not overlap and stay inside the workspace
+    # each piece belongs to one block; dual pieces first; the streams' tiles are even
+    duals = [p for p in T["pieces"] if p["rows"] > 128]
+    at = [0, len(duals)]
+    assert duals == T["pieces"][:len(duals)]
+    for c in T["ctas"]:
+        assert [c["dual0"], c["single0"]] == at
+        assert c["dual0"] <= c["dual1"] and c["single0"] <= c["single1"] <= c["single2"]
+        at = [c["dual1"], c["single2"]]
+        two = [tiles_of(T["pieces"][a:b]) for a, b in ((c["single0"], c["single1"]),
+                                                       (c["single1"], c["single2"]))]
+        assert two[0] - two[1] in (0, 1)
+    assert at == [len(duals), len(T["pieces"])]
+    # partial rows do not overlap and fill the workspace
     used = np.zeros(plan.info.ws_rows, dtype=np.int32)
     for p in T["pieces"]:
-        parts = p["rows"] * (2 if p["flags"] & 2 else 1)
         assert 1 <= p["rows"] <= ROWS and p["keys"] >= 1
-        if not p["flags"] & 1:
-            assert 0 <= p["ws_row"] and p["ws_row"] + parts <= plan.info.ws_rows
-            used[p["ws_row"]: p["ws_row"] + parts] += 1
+        parts = p["rows"] * (4 if p["rows"] <= 32 else 2 if p["rows"] <= 64 else 1)
+        assert 0 <= p["ws_row"] and p["ws_row"] + parts <= plan.info.ws_rows
+        used[p["ws_row"]: p["ws_row"] + parts] += 1
         assert p["kv_row"] + p["keys"] <= plan.info.kv_rows
     assert (used == 1).all()
     # every row's entries lead to pieces that cover its runs' keys once
@@ -59,7 +74,7 @@ def check_plan(segs, N, Hq, Hkv, num_ctas):
                 packed = i * g + h % g
                 unit = unit0 + packed // ROWS * Hkv + h // g
                 at = 0
-                for j in range(T["unit_first"][unit], T["unit_first"][unit + 1]):
+                for j in range(T["units"][2 * unit], T["units"][2 * unit + 1]):
                     p = T["pieces"][j]
                     assert p["kv_head"] == h // g and p["r0"] == packed // ROWS * ROWS
                     assert p["q_row0"] + (p["r0"] + packed % ROWS) // g == n
@@ -100,10 +115,10 @@ def test_plan_shares_are_even():
     own = [rng.randint(1, 2048) for _ in range(64)]
     segs = cpa.shared_segments([1] * 64, own, 65536).tolist()
     _, T = check_plan(segs, 64, 32, 8, 152)
-    tiles = [sum((p["keys"] + 127) // 128 * (1.5 if p["rows"] > 128 else 1) for p in T["pieces"][a:b])
-             for a, b in zip(T["cta_first"], T["cta_first"][1:])]
-    pieces = [b - a for a, b in zip(T["cta_first"], T["cta_first"][1:])]
-    cost = [t + n for t, n in zip(tiles, pieces)]
+    cost = []
+    for c in T["ctas"]:
+        dual, single = T["pieces"][c["dual0"]:c["dual1"]], T["pieces"][c["single0"]:c["single2"]]
+        cost.append(1.5 * tiles_of(dual) + tiles_of(single) + len(dual) + len(single))
     assert max(cost) <= sum(cost) / 152 + 4
 
 
