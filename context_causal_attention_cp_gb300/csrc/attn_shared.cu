@@ -55,6 +55,7 @@ struct SharedParams {
   const int32_t* table;
   long long pieces, units, row_first, entries;  // word offsets
   int num_units, num_pieces, num_entries, num_q_rows, Hq, Hkv, g;
+  uint32_t g_mul, g_shift;  // n / g = umulhi(n, g_mul) >> g_shift, see group_div
   long long ws_rows;
   const __nv_bfloat16* q;
   long long q_row, q_head;
@@ -91,7 +92,7 @@ struct SharedCfg {
   static constexpr int kNoteOff = kMulOff + kRawStages * BN * 2;   // RawNote of each raw tile
   static constexpr int kExpOff = kNoteOff + kRawStages * 16;       // exponents, see RawNote::which
   static constexpr int kBarOff = kExpOff + 48;
-  static constexpr int kNumBars = 4 * kStages + 2 * kRawStages + 8 + 2;
+  static constexpr int kNumBars = 4 * kStages + 2 * kRawStages + 8 + 4;
   static constexpr int kWordOff = kBarOff + kNumBars * 8;  // TMEM slot, abort, loads, phases, tiles[2]
   static constexpr int kSmemBytes = kWordOff + 32 + 1024;  // + align slack
   static_assert(kBarOff % 8 == 0 && kSmemBytes <= 232448, "shared memory budget");
@@ -132,10 +133,16 @@ __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, const 
   return true;
 }
 
+// n / g for 0 <= n < 2^31: with 2^s the power of two from g on, g_mul = floor(2^(31+s)
+// / g) + 1 and n g_mul 2^-(31+s) exceeds n / g by less than 1 / g.
+__device__ __forceinline__ int group_div(const SharedParams& p, int n) {
+  return p.g == 1 ? n : (int)(__umulhi((uint32_t)n, p.g_mul) >> p.g_shift);
+}
+
 __device__ __forceinline__ SharedPiece load_piece(const SharedParams& p, int i) {
   const int4* w = reinterpret_cast<const int4*>(p.table + p.pieces) + 3LL * i;
   const int4 a = __ldg(w), b = __ldg(w + 1), c = __ldg(w + 2);
-  return SharedPiece{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, c.x, c.y, {c.z, c.w}};
+  return SharedPiece{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, c.x, c.y, c.z, c.w};
 }
 __device__ __forceinline__ bool piece_ok(const SharedParams& p, const SharedPiece& pc, bool dual) {
   return pc.rows >= 1 && pc.rows <= kRows && shared_dual(pc.rows) == dual && pc.r0 >= 0 &&
@@ -143,7 +150,8 @@ __device__ __forceinline__ bool piece_ok(const SharedParams& p, const SharedPiec
          (long long)pc.q_row0 + ((long long)pc.r0 + pc.rows - 1) / p.g < p.num_q_rows &&
          pc.kv_head >= 0 && pc.kv_head < p.Hkv && pc.keys >= 1 && pc.key0 >= 0 && pc.kv_row >= 0 &&
          (long long)pc.kv_row + pc.keys <= p.num_kv_rows && pc.ws_row >= 0 &&
-         (long long)pc.ws_row + shared_reps(pc.rows) * pc.rows <= p.ws_rows;
+         (pc.reps == 1 || (pc.reps == 2 && pc.rows <= 64) || (pc.reps == 4 && pc.rows <= 32)) &&
+         (long long)pc.ws_row + pc.reps * pc.rows <= p.ws_rows;
 }
 __device__ __forceinline__ int num_tiles(int keys) { return (keys - 1) / BN + 1; }
 
@@ -170,6 +178,18 @@ __device__ __forceinline__ bool load_list(const SharedParams& p, SharedCta& c, i
   ok = ok && (tiles[0] == tiles[1] || tiles[0] == tiles[1] + 1);
   if (!ok && threadIdx.x == 0) set_status(p.status, CPATTN_ERR_RANGE);
   return ok;
+}
+
+// Two barriers at once (their polls overlap).
+__device__ __forceinline__ bool wait_warp2(uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb,
+                                           const volatile int* abort, uint64_t timeout) {
+  uint64_t t0 = 0;
+  for (uint32_t i = 1;; ++i) {
+    const bool x = mbar_try_wait(a, pa), y = mbar_try_wait(b, pb);
+    if (__all_sync(0xffffffffu, x && y)) return true;
+    if (i % kPollsPerCheck == 0 && __shfl_sync(0xffffffffu, (int)give_up(t0, abort, timeout), 0))
+      return false;
+  }
 }
 
 // One K or V tile of the ring.
@@ -341,6 +361,13 @@ __device__ __forceinline__ void softmax_tile(uint32_t s_addr, uint32_t o_addr, i
   m_use = m_new_use;
 }
 
+// 32 bytes, a whole sector.
+__device__ __forceinline__ void store8(float* at, const float (&f)[8]) {
+  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(at), "f"(f[0]), "f"(f[1]),
+               "f"(f[2]), "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7])
+               : "memory");
+}
+
 template <int D, bool QUANT>
 __global__ void __launch_bounds__(SharedCfg<D, QUANT>::kThreads, 1)
 attn_shared_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
@@ -358,7 +385,8 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
   uint64_t* s_full = q_full + 2;
   uint64_t* p_full = s_full + 2;
   uint64_t* o_full = p_full + 2;
-  uint64_t* bar_drain = o_full + 2;
+  uint64_t* turn = o_full + 2;
+  uint64_t* bar_drain = turn + 2;
   uint16_t* raw_mul = reinterpret_cast<uint16_t*>(smem + C::kMulOff);
   RawNote* raw_note = reinterpret_cast<RawNote*>(smem + C::kNoteOff);
   int2* tile_exp = reinterpret_cast<int2*>(smem + C::kExpOff);  // (ek, ev) by RingTile::which
@@ -385,6 +413,7 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
       mbar_init(s_full + s, 1);
       mbar_init(p_full + s, 128);
       mbar_init(o_full + s, 1);
+      mbar_init(turn + s, 1);
       mbar_init(bar_drain + s, 1);
       stream_tiles[s] = 0;
     }
@@ -576,13 +605,13 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
           phases ^= 1u << b;
           return wait_one(full + b, parity, abort_flag, p.timeout_ns);
         };
-        // Q K^T of the stream's next step (of a piece whose first tile it is: once the
-        // queries are there); false when there is none or a wait ran out
-        int v_seq = 0;       // ring place of the V tile of the step in S
-        bool shared_tile = false, head = false;  // of the step in S
-        auto next_qk = [&]() {
-          head = left == 0;
-          if (head) {
+        int k_slot = 0, v_slot = 0;                // of the stream's next step
+        bool next_dual = false, next_head = false;
+        // Finds the stream's next step; waits for its queries, at a piece's head, and
+        // its K tile.  False when there is none or a wait ran out.
+        auto prepare = [&]() {
+          next_head = left == 0;
+          if (next_head) {
             if (dual && i == list.dual1) {
               dual = false;
               i = s ? list.single1 : list.single0;
@@ -592,38 +621,54 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             ok = wait_one(q_full + s, pieces++ & 1, abort_flag, p.timeout_ns);
           }
           --left;
-          int k_seq;
-          shared_tile = dual;
+          next_dual = dual;
           if (dual) {
-            k_seq = dual_seq;
-            v_seq = dual_seq + 1;
+            k_slot = dual_seq % C::kStages;
+            v_slot = (dual_seq + 1) % C::kStages;
             dual_seq += 2;
           } else {
-            k_seq = dual_seq + k_place(n);
-            v_seq = dual_seq + v_place(n);
+            k_slot = (dual_seq + k_place(n)) % C::kStages;
+            v_slot = (dual_seq + v_place(n)) % C::kStages;
             n += 2;
           }
-          const int slot = k_seq % C::kStages;
-          ok = ok && wait_tile(dual ? 2 : s, slot);
-          if (!ok) return false;
-          tc_fence_after();
-          issue_qk(slot);
-          mma_commit(s_full + s);
-          mma_commit(empty + slot);
-          if (!dual) mbar_arrive(empty + slot);  // the other stream does not use the tile
-          return true;
+          ok = ok && wait_tile(dual ? 2 : s, k_slot);
+          return ok;
         };
-        for (bool more = next_qk(); more; ++step) {
-          const int slot = v_seq % C::kStages;
-          const bool first = head, last = left == 0, mine = !shared_tile;
-          ok = wait_tile(mine ? s : 2, slot) && wait_one(p_full + s, step & 1, abort_flag, p.timeout_ns);
+        auto begin_step = [&]() {
+          tc_fence_after();
+          issue_qk(k_slot);
+          mma_commit(s_full + s);
+          mma_commit(empty + k_slot);
+          if (!next_dual) mbar_arrive(empty + k_slot);  // the other stream does not use the tile
+        };
+        bool more = prepare();
+        if (more) begin_step();
+        while (more) {
+          const int slot = v_slot;
+          const bool first = next_head, last = left == 0, both = next_dual;
+          ok = wait_tile(both ? 2 : s, slot) && wait_one(p_full + s, step & 1, abort_flag, p.timeout_ns);
           if (!ok) break;
+          // Dual units: the streams' bursts of MMAs alternate, so that each stream's
+          // softmax runs under the other's MMAs; without the turns the two fall into
+          // step and the tensor core idles during both softmaxes.
+          if (both) {
+            if (!last) more = prepare();
+            if (ok && (s == 1 || step > 0))
+              ok = wait_one(turn + s, (s == 1 ? step : step - 1) & 1, abort_flag, p.timeout_ns);
+            if (!ok) break;
+          }
           tc_fence_after();
           issue_pv(slot, first);
           if (last) mma_commit(o_full + s);
           mma_commit(empty + slot);
-          if (mine) mbar_arrive(empty + slot);
-          more = next_qk();
+          if (!both) mbar_arrive(empty + slot);
+          if (both && !last) begin_step();
+          if (both) mbar_arrive(turn + (s ^ 1));
+          if (!both || last) {
+            more = prepare();
+            if (more) begin_step();
+          }
+          ++step;
         }
         if (!ok) {
           set_status(p.status, CPATTN_ERR_TIMEOUT);
@@ -636,55 +681,58 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     }
     if constexpr (QUANT) if (warp >= kConvertWarp) {
       // --------------------------------------------------- codes to f16 tiles --
-      // Warp w has rows 32w .. 32w+31 of every tile, D / 16 lanes to a row.  Rows
-      // behind the last key become zeros (0 * NaN is NaN, so masking P alone would
-      // not keep stale rows out).
+      // Warp w has rows 32w .. 32w+31 of every tile; of a row, lane l has 8 codes of
+      // each 64 (so that 8 lanes store 8 different banks' chunks).  Rows behind the
+      // last key become zeros (0 * NaN is NaN, so masking P alone would not keep stale
+      // rows out).
       const int w = warp - kConvertWarp;
-      constexpr int kLanes = D / 16, kRowsPer = 32 / kLanes;
-      const int rl = lane / kLanes, cl = lane % kLanes;  // row in the group, 16-code chunk
-      const int total = 2 * steps;  // + the dual tiles', counted below
-      int tiles = total;
+      const int rl = lane >> 3, cl = lane & 7;  // row of four, 8-code chunk
+      int tiles = 2 * steps;
       for (int i = list.dual0; i < list.dual1; ++i) tiles += 2 * num_tiles(load_piece(p, i).keys);
+      // chunk places of rows r and r + 4 of a row's 128-byte line
+      const uint32_t swz[2] = {(uint32_t)((cl ^ rl) << 4), (uint32_t)((cl ^ (rl + 4)) << 4)};
       bool ok = true;
       for (int seq = 0; seq < tiles; ++seq) {
         const int raw = seq % C::kRawStages, slot = seq % C::kStages;
-        ok = wait_warp(empty + slot, ((seq / C::kStages) & 1) ^ 1, abort_flag, p.timeout_ns) &&
-             wait_warp(raw_full + raw, (seq / C::kRawStages) & 1, abort_flag, p.timeout_ns);
+        ok = wait_warp2(empty + slot, ((seq / C::kStages) & 1) ^ 1, raw_full + raw,
+                        (seq / C::kRawStages) & 1, abort_flag, p.timeout_ns);
         if (!ok) break;
         const RawNote note = raw_note[raw];
         if (w == 0 && lane == 0 && note.which < RawNote::kNoteV)
           tile_exp[note.which] = make_int2(note.ek, note.ev);
-        const uint8_t* src = smem + C::kRawOff + raw * C::kRawTile + (w * 32 + rl) * D + cl * 16;
+        const uint8_t* src = smem + C::kRawOff + raw * C::kRawTile + (w * 32 + rl) * D + cl * 8;
         const uint16_t* mul = raw_mul + raw * BN + w * 32 + rl;
-        uint8_t* dst = smem + C::kRingOff + slot * C::kTile + (cl >> 2) * (BN * 128);
+        uint8_t* dst = smem + C::kRingOff + slot * C::kTile + (w * 32 + rl) * 128;
         const int live = note.live - w * 32 - rl;
         // loads of a batch before its stores: the compiler cannot tell them apart
-        constexpr int kBatch = 4;
+        constexpr int kBatch = 4, kHalves = D / 64;
 #pragma unroll
-        for (int r0 = 0; r0 < 32; r0 += kBatch * kRowsPer) {
-          uint4 v[kBatch];
+        for (int r0 = 0; r0 < 32; r0 += 4 * kBatch) {
+          uint2 v[kBatch][kHalves];
           uint32_t m[kBatch];
 #pragma unroll
           for (int x = 0; x < kBatch; ++x) {
-            const int r = r0 + x * kRowsPer;
-            v[x] = *reinterpret_cast<const uint4*>(src + r * D);
-            m[x] = mul[r];
-            if (r >= live) v[x] = make_uint4(0, 0, 0, 0);
+            m[x] = mul[r0 + 4 * x];
+#pragma unroll
+            for (int h = 0; h < kHalves; ++h)
+              v[x][h] = *reinterpret_cast<const uint2*>(src + (r0 + 4 * x) * D + h * 64);
+          }
+          if (live < 32) {
+#pragma unroll
+            for (int x = 0; x < kBatch; ++x)
+#pragma unroll
+              for (int h = 0; h < kHalves; ++h)
+                if (r0 + 4 * x >= live) v[x][h] = make_uint2(0, 0);
           }
 #pragma unroll
-          for (int x = 0; x < kBatch; ++x) {
-            const int row = w * 32 + r0 + x * kRowsPer + rl;
-            const uint32_t m2 = m[x] * 0x10001u;
-            const uint2 x0 = codes_to_f16(v[x].x, m2), x1 = codes_to_f16(v[x].y, m2);
-            const uint2 x2 = codes_to_f16(v[x].z, m2), x3 = codes_to_f16(v[x].w, m2);
-            // two 16-byte chunks of the row's line; the lanes of a row's second line
-            // store theirs the other way round, so that a quarter warp hits every bank
-            uint8_t* line = dst + row * 128;
-            const int c0 = (cl & 3) * 2, flip = cl >> 2;
-            const uint4 lo = make_uint4(x0.x, x0.y, x1.x, x1.y), hi = make_uint4(x2.x, x2.y, x3.x, x3.y);
-            *reinterpret_cast<uint4*>(line + (((c0 + flip) ^ (row & 7)) << 4)) = flip ? hi : lo;
-            *reinterpret_cast<uint4*>(line + (((c0 + 1 - flip) ^ (row & 7)) << 4)) = flip ? lo : hi;
-          }
+          for (int x = 0; x < kBatch; ++x)
+#pragma unroll
+            for (int h = 0; h < kHalves; ++h) {
+              const uint32_t m2 = m[x] * 0x10001u;
+              const uint2 a = codes_to_f16(v[x][h].x, m2), b = codes_to_f16(v[x][h].y, m2);
+              *reinterpret_cast<uint4*>(dst + h * (BN * 128) + (r0 + 4 * x) * 128 + swz[x & 1]) =
+                  make_uint4(a.x, a.y, b.x, b.y);
+            }
         }
         fence_async_shared();
         mbar_arrive(full + full_bit((note.which & (RawNote::kNoteV - 1)) >> 1, slot));
@@ -708,14 +756,15 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
       return q_line + (c >> 3) * (BM * 128) + (((c & 7) ^ (trow & 7)) << 4);
     };
     auto row_of = [&](const SharedPiece& pc) {
-      return shared_dual(pc.rows) ? s * BM + trow : trow & (BM / shared_reps(pc.rows) - 1);
+      // (a small unit's rows in the other half for stream 1: other schedulers' warps)
+      return shared_dual(pc.rows) ? s * BM + trow : (trow + s * (BM / 2)) & (BM / pc.reps - 1);
     };
     // This thread's query row of a piece to shared memory, asynchronously; q_ready()
     // publishes it, and returns the factor of its scores.
     auto load_q = [&](const SharedPiece& pc) {
       const int r = row_of(pc);
       if (r < pc.rows) {
-        const int packed = pc.r0 + r, qi = packed / p.g;
+        const int packed = pc.r0 + r, qi = group_div(p, packed);
         const __nv_bfloat16* src = p.q + (long long)(pc.q_row0 + qi) * p.q_row +
                                    (long long)(pc.kv_head * p.g + packed - qi * p.g) * p.q_head;
 #pragma unroll
@@ -782,12 +831,12 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
       if (more) np = piece(i + 1);
       const bool dual = i < duals;
       const int T = num_tiles(pc.keys);
-      const int reps = shared_reps(pc.rows), r = row_of(pc);
+      const int reps = pc.reps, r = row_of(pc);
       const int copy = reps == 4 ? wq : reps == 2 ? wq >> 1 : 0;
       const bool warp_live = (r & ~31) < pc.rows;
       int seen = 0;  // keys of the piece that this row sees
       if (r < pc.rows) {
-        const long long pos = (long long)pc.q_pos0 + (long long)((pc.r0 + r) / p.g) * pc.q_pos_step;
+        const long long pos = (long long)pc.q_pos0 + (long long)group_div(p, pc.r0 + r) * pc.q_pos_step;
         seen = (int)max(0LL, min((long long)pc.keys, pos + 1 - pc.key0));
       }
       float m_run = -INFINITY, l_run = 0.f, m_use = 0.f;
@@ -855,17 +904,18 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
         const long long row = (long long)pc.ws_row + copy * pc.rows + r;
         float* dst = p.ws_o + row * D;
 #pragma unroll
-        for (int q = 0; q < D / 32; ++q) {
-          uint32_t v[32];
-          tmem_ld32(o_addr + q * 32, v);
+        for (int q = 0; q < D / 64; ++q) {
+          uint32_t v[64];
+          tmem_ld32p(o_addr + q * 64, v);
+          tmem_ld32p(o_addr + q * 64 + 32, v + 32);
           tmem_wait_ld();
           if (r < pc.rows) {
 #pragma unroll
-            for (int c = 0; c < 32; c += 4) {
-              float4 f = make_float4(__uint_as_float(v[c]) * inv, __uint_as_float(v[c + 1]) * inv,
-                                     __uint_as_float(v[c + 2]) * inv, __uint_as_float(v[c + 3]) * inv);
-              if (none) f = make_float4(0.f, 0.f, 0.f, 0.f);
-              *reinterpret_cast<float4*>(dst + q * 32 + c) = f;
+            for (int c = 0; c < 64; c += 8) {
+              float f[8];
+#pragma unroll
+              for (int x = 0; x < 8; ++x) f[x] = none ? 0.f : __uint_as_float(v[c + x]) * inv;
+              store8(dst + q * 64 + c, f);
             }
           }
         }
@@ -903,29 +953,30 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
   }
 }
 
-// Merge of a row's partials, one warp per (query row, head).  Latency bound: a lane
-// finds one partial each (the plan's words, read before the wait for the attention
-// kernel), so that after the wait two dependent loads are left, the L of all
-// partials and their O.
-constexpr int kMergeThreads = 256;
+// Merge of a row's partials, `ways` warps per (query row, head), each an interleaved
+// share of them.  Latency bound: a lane finds one partial each (the plan's words,
+// read before the wait for the attention kernel), so that after the wait two
+// dependent loads are left, the L of all partials and their O.
+constexpr int kMergeThreads = 256, kMergeWarps = kMergeThreads / 32;
+constexpr int kMergeLoads = 8;  // partials of a warp whose O loads are in flight together
+
+template <int E>
+struct MergeSum {  // sum_j 2^(L_j - m) (1, O_j), this lane's E columns
+  float m, w, o[E];
+};
+
+// The share `way` of `ways` of a row's partials; false (and CPATTN_ERR_RANGE) when the
+// plan's words lead out of the buffers.
 template <int D>
-__device__ __forceinline__ void merge_row(const SharedParams& p, long long u, int lane) {
-  constexpr int E = D / 32;  // columns of a lane
+__device__ __forceinline__ bool merge_share(const SharedParams& p, int n, int h, int e0, int e1,
+                                            int way, int ways, int lane, MergeSum<D / 32>& sum) {
+  constexpr int E = D / 32;
   const unsigned all = 0xffffffffu;
-  const int n = (int)(u / p.Hq), h = (int)(u % p.Hq), kvh = h / p.g, j = h % p.g;
-  const int e0 = __ldg(p.table + p.row_first + n), e1 = __ldg(p.table + p.row_first + n + 1);
-  if (e0 == e1) return;  // a row of no segment
-  if (e0 < 0 || e1 < e0 || e1 > p.num_entries) {
-    if (lane == 0) set_status(p.status, CPATTN_ERR_RANGE);
-    return;
-  }
-  float m = -INFINITY, sw = 0.f, acc[E];
-#pragma unroll
-  for (int c = 0; c < E; ++c) acc[c] = 0.f;
+  const int kvh = h / p.g, j = h % p.g;
   bool waited = false;
   for (int eb = e0; eb < e1; eb += 32) {
-    // lane e: the pieces of entry eb + e, and the row's place in their partials
-    int p0 = 0, count = 0, at = 0, reps = 1;
+    // lane e: the partials of entry eb + e
+    SharedUnit un{0, 0, 1, 0};
     bool ok = true;
     if (eb + lane < e1) {
       const int2 en = __ldg(reinterpret_cast<const int2*>(p.table + p.entries) + eb + lane);
@@ -933,105 +984,144 @@ __device__ __forceinline__ void merge_row(const SharedParams& p, long long u, in
       const long long unit = en.x + packed / kRows * p.Hkv + kvh;
       ok = en.x >= 0 && en.y >= 0 && unit < p.num_units;
       if (ok) {
-        const int2 pr = __ldg(reinterpret_cast<const int2*>(p.table + p.units) + unit);
-        ok = pr.x >= 0 && pr.x <= pr.y && pr.y <= p.num_pieces;
-        p0 = pr.x;
-        at = (int)(packed % kRows);
-        if (pr.y > pr.x) reps = shared_reps(__ldg(p.table + p.pieces + 12LL * p0 + 4));  // rows
-        count = (pr.y - pr.x) * reps;
+        const int4 w = __ldg(reinterpret_cast<const int4*>(p.table + p.units) + unit);
+        un = SharedUnit{w.x, w.y, w.z, w.w};
+        const int at = (int)(packed % kRows);
+        ok = un.ws_row >= 0 && un.parts >= 0 &&
+             (un.parts == 0 || (at < un.rows && un.rows <= kRows &&
+                                un.ws_row + (long long)un.parts * un.rows <= p.ws_rows));
+        un.ws_row += at;
       }
     }
-    if (!__all_sync(all, ok)) {
-      if (lane == 0) set_status(p.status, CPATTN_ERR_RANGE);
-      return;
-    }
-    int upto = count;  // partials of this entry and those before it
+    if (!__all_sync(all, ok)) return false;
+    int upto = un.parts;  // partials of this entry and those before it
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int x = __shfl_up_sync(all, upto, o);
       if (lane >= o) upto += x;
     }
     const int total = __shfl_sync(all, upto, 31), entries = min(32, e1 - eb);
-    for (int b = 0; b < total; b += 32) {
-      // lane l: partial b + l
-      int piece = 0, off = 0, copy = 0;
-      for (int e = 0; e < entries; ++e) {
-        const int end = __shfl_sync(all, upto, e), cnt = __shfl_sync(all, count, e);
-        const int first = __shfl_sync(all, p0, e), a = __shfl_sync(all, at, e);
-        const int k = __shfl_sync(all, reps, e), i = b + lane - (end - cnt);
-        if (i >= 0 && b + lane < end) {
-          piece = first + i / k;  // k is 1, 2 or 4
-          copy = i % k;
-          off = a;
-        }
-      }
-      const bool mine = b + lane < total;
+    for (int b = way; b < total; b += 32 * ways) {
+      // lane l: partial b + l * ways
+      const int mine = b + lane * ways;
       long long row = 0;
-      if (mine) {
-        const int32_t* pc = p.table + p.pieces + 12LL * piece;
-        row = (long long)__ldg(pc + 9) + (long long)copy * __ldg(pc + 4) + off;  // ws_row, rows
-      }
-      if (!__all_sync(all, row >= 0 && row < p.ws_rows)) {
-        if (lane == 0) set_status(p.status, CPATTN_ERR_RANGE);
-        return;
+      for (int e = 0; e < entries; ++e) {
+        const int end = __shfl_sync(all, upto, e), cnt = __shfl_sync(all, un.parts, e);
+        const int first = __shfl_sync(all, un.ws_row, e), stride = __shfl_sync(all, un.rows, e);
+        if (mine >= end - cnt && mine < end) row = first + (long long)(mine - (end - cnt)) * stride;
       }
       if (!waited) grid_dep_wait();  // the attention kernel before this one wrote the partials
       waited = true;
-      const float l = mine ? __ldcg(p.ws_l + row) : -INFINITY;
+      const int cnt = min(32, (total - b + ways - 1) / ways);
+      const float l = mine < total ? __ldcg(p.ws_l + row) : -INFINITY;
+      float4 x[kMergeLoads];  // (two columns of each in x, y at D = 64)
+      auto load = [&](int i0) {
+#pragma unroll
+        for (int i = 0; i < kMergeLoads; ++i) {
+          const long long r = __shfl_sync(all, row, (i0 + i) & 31);
+          x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (i0 + i < cnt) {
+            const float* src = p.ws_o + r * D + lane * E;
+            if constexpr (E == 4) {
+              x[i] = __ldcg(reinterpret_cast<const float4*>(src));
+            } else {
+              const float2 f = __ldcg(reinterpret_cast<const float2*>(src));
+              x[i].x = f.x;
+              x[i].y = f.y;
+            }
+          }
+        }
+      };
+      load(0);
       float mx = l;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(all, mx, o));
-      const float mn = fmaxf(m, mx), use = mn == -INFINITY ? 0.f : mn;
+      const float mn = fmaxf(sum.m, mx), use = mn == -INFINITY ? 0.f : mn;
       const float w = exp2f(l - use);  // (a NaN partial stays one)
       float ws = w;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) ws += __shfl_xor_sync(all, ws, o);
-      const float old = exp2f(m - use);
-      sw = sw * old + ws;
+      const float old = exp2f(sum.m - use);
+      sum.w = sum.w * old + ws;
 #pragma unroll
-      for (int c = 0; c < E; ++c) acc[c] *= old;
-      m = mn;
-      const int cnt = min(32, total - b);
-#pragma unroll 8
-      for (int i = 0; i < cnt; ++i) {
-        const float wi = __shfl_sync(all, w, i);
-        const float* src = p.ws_o + __shfl_sync(all, row, i) * D + lane * E;
-        float x[E];
-        if constexpr (E == 4) {
-          const float4 f = __ldcg(reinterpret_cast<const float4*>(src));
-          x[0] = f.x; x[1] = f.y; x[2] = f.z; x[3] = f.w;
-        } else {
-          const float2 f = __ldcg(reinterpret_cast<const float2*>(src));
-          x[0] = f.x; x[1] = f.y;
+      for (int c = 0; c < E; ++c) sum.o[c] *= old;
+      sum.m = mn;
+      for (int i0 = 0; i0 < cnt; i0 += kMergeLoads) {
+        if (i0 > 0) load(i0);
+#pragma unroll
+        for (int i = 0; i < kMergeLoads; ++i) {
+          const float wi = __shfl_sync(all, w, (i0 + i) & 31);
+          if (i0 + i < cnt) {
+            sum.o[0] = fmaf(wi, x[i].x, sum.o[0]);
+            sum.o[1] = fmaf(wi, x[i].y, sum.o[1]);
+            if constexpr (E == 4) {
+              sum.o[2] = fmaf(wi, x[i].z, sum.o[2]);
+              sum.o[3] = fmaf(wi, x[i].w, sum.o[3]);
+            }
+          }
         }
-#pragma unroll
-        for (int c = 0; c < E; ++c) acc[c] = fmaf(wi, x[c], acc[c]);
       }
     }
   }
-  if (!waited) grid_dep_wait();
-  const float inv = sw == 0.f ? 0.f : 1.f / sw;
+  return true;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kMergeThreads) shared_merge_kernel(const SharedParams p, int ways) {
+  constexpr int E = D / 32;  // columns of a lane
+  __shared__ MergeSum<E> parts[kMergeWarps][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, way = warp % ways;
+  const long long u = (long long)blockIdx.x * (kMergeWarps / ways) + warp / ways;
+  MergeSum<E> sum;
+  sum.m = -INFINITY;
+  sum.w = 0.f;
 #pragma unroll
-  for (int c = 0; c < E; ++c) acc[c] *= inv;
+  for (int c = 0; c < E; ++c) sum.o[c] = 0.f;
+  bool write = false;
+  if (u < (long long)p.num_q_rows * p.Hq) {
+    const int n = (int)(u / p.Hq), h = (int)(u % p.Hq);
+    const int e0 = __ldg(p.table + p.row_first + n), e1 = __ldg(p.table + p.row_first + n + 1);
+    if (e0 != e1) {  // (a row of no segment is left as it is)
+      write = e0 >= 0 && e1 > e0 && e1 <= p.num_entries &&
+              merge_share<D>(p, n, h, e0, e1, way, ways, lane, sum);
+      if (!write && lane == 0) set_status(p.status, CPATTN_ERR_RANGE);
+    }
+  }
+  grid_dep_wait();  // no block ends before the kernel that this launch may overlap
+  if (ways > 1) {
+    parts[warp][lane] = sum;
+    __syncthreads();
+    if (way > 0) return;
+    for (int x = 1; x < ways; ++x) {
+      const MergeSum<E> other = parts[warp + x][lane];
+      const float mn = fmaxf(sum.m, other.m), use = mn == -INFINITY ? 0.f : mn;
+      const float a = exp2f(sum.m - use), b = exp2f(other.m - use);
+      sum.w = sum.w * a + other.w * b;
+#pragma unroll
+      for (int c = 0; c < E; ++c) sum.o[c] = sum.o[c] * a + other.o[c] * b;
+      sum.m = mn;
+    }
+  }
+  if (!write) return;
+  const float inv = sum.w == 0.f ? 0.f : 1.f / sum.w;
+#pragma unroll
+  for (int c = 0; c < E; ++c) sum.o[c] *= inv;
   const long long out = u * D + lane * E;
   if (p.o_f32) {
     float* o = static_cast<float*>(p.o) + out;
-    if constexpr (E == 4) *reinterpret_cast<float4*>(o) = make_float4(acc[0], acc[1], acc[2], acc[3]);
-    else *reinterpret_cast<float2*>(o) = make_float2(acc[0], acc[1]);
+    if constexpr (E == 4)
+      *reinterpret_cast<float4*>(o) = make_float4(sum.o[0], sum.o[1], sum.o[2], sum.o[3]);
+    else
+      *reinterpret_cast<float2*>(o) = make_float2(sum.o[0], sum.o[1]);
   } else {
     __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.o) + out;
     if constexpr (E == 4)
-      *reinterpret_cast<uint2*>(o) = make_uint2(pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3]));
+      *reinterpret_cast<uint2*>(o) =
+          make_uint2(pack_bf16x2(sum.o[0], sum.o[1]), pack_bf16x2(sum.o[2], sum.o[3]));
     else
-      *reinterpret_cast<uint32_t*>(o) = pack_bf16x2(acc[0], acc[1]);
+      *reinterpret_cast<uint32_t*>(o) = pack_bf16x2(sum.o[0], sum.o[1]);
   }
-  if (lane == 0) p.lse[u] = sw == 0.f ? -INFINITY : (m + log2f(sw)) * kLn2;
-}
-template <int D>
-__global__ void __launch_bounds__(kMergeThreads) shared_merge_kernel(const SharedParams p) {
-  const long long u = ((long long)blockIdx.x * kMergeThreads + threadIdx.x) >> 5;
-  if (u < (long long)p.num_q_rows * p.Hq) merge_row<D>(p, u, threadIdx.x & 31);
-  grid_dep_wait();  // no block ends before the kernel that this launch may overlap
+  if (lane == 0) p.lse[u] = sum.w == 0.f ? -INFINITY : (sum.m + log2f(sum.w)) * kLn2;
 }
 
 // 3-D map of a code buffer (cols, heads, rows) with a D-column x 1-head box, rows
@@ -1102,7 +1192,8 @@ extern "C" int cp_attn_shared(const cp_shared_plan_t* plan, const int32_t* table
     return CPATTN_ERR_INVALID_ARG;
   const bool quant = k_scales != nullptr;
   const int64_t per16 = quant ? 16 : 8;  // elements in 16 bytes
-  if (!a16(table_dev) || !a16(q) || !a16(k) || !a16(v) || !a16(o) || !a16(workspace) ||
+  if (!a16(table_dev) || !a16(q) || !a16(k) || !a16(v) || !a16(o) ||
+      (reinterpret_cast<uintptr_t>(workspace) & 31u) ||
       (reinterpret_cast<uintptr_t>(lse) & 3u) || (reinterpret_cast<uintptr_t>(k_scales) & 3u) ||
       (reinterpret_cast<uintptr_t>(v_scales) & 3u) || q_row_stride % 8 || q_head_stride % 8 ||
       k_row_stride % per16 || k_head_stride % per16 || v_row_stride % per16 ||
@@ -1128,6 +1219,8 @@ extern "C" int cp_attn_shared(const cp_shared_plan_t* plan, const int32_t* table
   p.Hq = plan->Hq;
   p.Hkv = plan->Hkv;
   p.g = plan->Hq / plan->Hkv;
+  for (p.g_shift = 0; (1LL << (p.g_shift + 1)) < p.g; ++p.g_shift) {}  // s - 1
+  p.g_mul = (uint32_t)((1ULL << (32 + p.g_shift)) / p.g + 1);
   p.ws_rows = plan->ws_rows;
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.q_row = q_row_stride;
@@ -1162,10 +1255,14 @@ extern "C" int cp_attn_shared(const cp_shared_plan_t* plan, const int32_t* table
                                     : launch_shared<64, false>(m, p, n, stream));
     if (r != CPATTN_OK) return r;
   }
-  const long long warps = kMergeThreads / 32;
-  const long long blocks = ((long long)plan->num_q_rows * plan->Hq + warps - 1) / warps;
+  // Warps per row: enough that a warp's partials are loaded in one go (the average is
+  // ws_rows / rows), e.g. 152 partials a row at one token on a 256K prefix.
+  const long long rows = (long long)plan->num_q_rows * plan->Hq;
+  int ways = 1;
+  while (ways < kMergeWarps && plan->ws_rows > rows * ways * kMergeLoads) ways *= 2;
+  const long long blocks = (rows * ways + kMergeWarps - 1) / kMergeWarps;
   if (blocks > 0x7fffffffLL) return CPATTN_ERR_TOO_LARGE;
   const cudaError_t e = launch_kernel(d == 128 ? shared_merge_kernel<128> : shared_merge_kernel<64>,
-                                      (unsigned)blocks, kMergeThreads, 0, stream, true, p);
+                                      (unsigned)blocks, kMergeThreads, 0, stream, true, p, ways);
   return e == cudaSuccess ? CPATTN_OK : CPATTN_ERR_CUDA;
 }

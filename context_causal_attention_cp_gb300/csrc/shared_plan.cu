@@ -54,7 +54,7 @@ struct Place {
 struct Cut {
   const cp_segment_t* seg;
   long long unit, r0, key0, keys;
-  int rows, head;
+  int rows, head, reps;
 };
 
 void measure(const Line& L, Place& p) {
@@ -109,7 +109,7 @@ void share(const Line& L, Place& p, long long budget, F&& f) {
     if (fit < 1) return;
     const long long n = std::min(p.keys - p.key0, fit * kKeys);
     f(Cut{L.segs + p.seg, p.unit0 + p.tile * L.Hkv + p.head, p.tile * CPATTN_SHARED_ROWS, p.key0, n,
-          p.rows, p.head});
+          p.rows, p.head, shared_reps(p.rows, p.keys)});
     p.key0 += n;
     used += kPieceCost + fit * cost;
   }
@@ -206,7 +206,7 @@ extern "C" int cp_shared_plan_size(const cp_segment_t* segs, int num_segs, int n
   long long pieces = 0, ws_rows = 0;
   deal(L, hi, num_ctas, [&](int, const Cut& k, int) {
     ++pieces;
-    ws_rows += shared_reps(k.rows) * k.rows;
+    ws_rows += k.reps * k.rows;
   });
   if (ws_rows > 0x7fffffffLL) return CPATTN_ERR_TOO_LARGE;
   plan->num_q_rows = num_q_rows;
@@ -244,14 +244,14 @@ extern "C" int cp_shared_plan(const cp_segment_t* segs, int num_segs, const cp_s
   deal(L, plan->budget, plan->num_ctas, [&](int, const Cut& k, int stream) {
     ++np;
     duals += stream < 0;
-    ws += shared_reps(k.rows) * k.rows;
+    ws += k.reps * k.rows;
   });
   if (np != plan->num_pieces || ws != plan->ws_rows) return CPATTN_ERR_INVALID_ARG;
 
   const SharedTable T = shared_table(*plan);
   auto* ctas = reinterpret_cast<SharedCta*>(table);
   auto* pieces = reinterpret_cast<SharedPiece*>(table + T.pieces);
-  int32_t* units = table + T.units;
+  auto* units = reinterpret_cast<SharedUnit*>(table + T.units);
   int32_t* row_first = table + T.row_first;
   int32_t* entries = table + T.entries;
 
@@ -274,7 +274,7 @@ extern "C" int cp_shared_plan(const cp_segment_t* segs, int num_segs, const cp_s
   for (int n = N; n > 0; --n) row_first[n] = row_first[n - 1];
   row_first[0] = 0;
 
-  for (int u = 0; u < 2 * plan->num_units; ++u) units[u] = 0;
+  for (int u = 0; u < plan->num_units; ++u) units[u] = SharedUnit{};
   for (int c = 0; c < plan->num_ctas; ++c) ctas[c] = SharedCta{};
   int32_t next[2] = {0, (int32_t)duals}, ws_row = 0;  // next dual and next single piece
   int cta = -1;
@@ -302,10 +302,13 @@ extern "C" int cp_shared_plan(const cp_segment_t* segs, int num_segs, const cp_s
     p.key0 = (int32_t)k.key0;
     p.keys = (int32_t)k.keys;
     p.ws_row = ws_row;
-    ws_row += shared_reps(k.rows) * k.rows;
+    p.reps = k.reps;
+    ws_row += k.reps * k.rows;
     pieces[at] = p;
-    if (units[2 * k.unit] == units[2 * k.unit + 1]) units[2 * k.unit] = at;
-    units[2 * k.unit + 1] = at + 1;
+    SharedUnit& u = units[k.unit];  // (its pieces come one after the other)
+    if (u.parts == 0) u.ws_row = p.ws_row;
+    u.parts += k.reps;
+    u.rows = k.rows;
   });
   open(plan->num_ctas - 1);
   return CPATTN_OK;

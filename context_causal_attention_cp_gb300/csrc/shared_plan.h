@@ -3,7 +3,7 @@
 // Table (int32 words, see cp_shared_plan):
 //   ctas       [num_ctas]         SharedCta: the pieces of each thread block
 //   pieces     [num_pieces]       SharedPiece, those of dual units first
-//   units      [num_units][2]     pieces [first, end) of a unit
+//   units      [num_units]        SharedUnit: the partial rows of a unit
 //   row_first  [num_q_rows + 1]   entries of query row n (padded to an even word)
 //   entries    [num_entries][2]   (unit of the row's segment's first tile and KV head 0,
 //                                  row index within the segment)
@@ -26,7 +26,8 @@ struct SharedPiece {
   int32_t key0;      // its key number within the segment's run
   int32_t keys;      // keys of the piece, >= 1
   int32_t ws_row;    // first partial row in the workspace (reps * rows of them)
-  int32_t unused[2];
+  int32_t reps;      // copies of the rows in the MMA tile, see shared_reps
+  int32_t unused;
 };
 static_assert(sizeof(SharedPiece) == 48, "three 16-byte words");
 
@@ -45,11 +46,21 @@ constexpr int kSharedTileRows = 128;  // packed rows of one MMA tile
 constexpr int kSharedTileKeys = 128;  // keys of one KV tile
 __host__ __device__ constexpr bool shared_dual(int rows) { return rows > kSharedTileRows; }
 
-// A unit of at most 64 (32) rows fills its MMA tile with 2 (4) copies of them, and
-// copy c works on the c-th half (quarter) of the keys of every KV tile: the MMAs
-// cost the same, and all four warps of a stream share the exponentials.  Each copy
-// leaves a partial result: a piece has reps * rows partial rows, copy-major.
-__host__ __device__ constexpr int shared_reps(int rows) { return rows <= 32 ? 4 : rows <= 64 ? 2 : 1; }
+// A unit of at most 64 (32) rows and enough keys fills its MMA tile with 2 (4) copies
+// of its rows, and copy c works on the c-th half (quarter) of the keys of every KV
+// tile: the MMAs cost the same, and all four warps of a stream share the exponentials.
+// Each copy leaves a partial result, which pays from kSharedRepKeys keys on: TODO.
+constexpr int kSharedRepKeys = 2048;
+__host__ __device__ constexpr int shared_reps(int rows, long long keys) {
+  return keys < kSharedRepKeys ? 1 : rows <= 32 ? 4 : rows <= 64 ? 2 : 1;
+}
+
+// The partials of a unit: part j of its packed row r is workspace row ws_row + j * rows
+// + r; the pieces' copies in the order of the keys.
+struct SharedUnit {
+  int32_t ws_row, parts, rows, unused;
+};
+static_assert(sizeof(SharedUnit) == 16, "one 16-byte word");
 
 struct SharedTable {
   long long pieces, units, row_first, entries, total;  // word offsets (ctas at 0)
@@ -58,7 +69,7 @@ inline SharedTable shared_table(const cp_shared_plan_t& p) {
   SharedTable t;
   t.pieces = p.num_ctas * (long long)(sizeof(SharedCta) / 4);
   t.units = t.pieces + p.num_pieces * (long long)(sizeof(SharedPiece) / 4);
-  t.row_first = t.units + 2LL * p.num_units;
+  t.row_first = t.units + p.num_units * (long long)(sizeof(SharedUnit) / 4);
   t.entries = (t.row_first + p.num_q_rows + 2) & ~1LL;
   t.total = t.entries + 2LL * p.num_entries;
   return t;

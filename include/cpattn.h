@@ -629,7 +629,7 @@ int cp_shared_workspace_size(const cp_shared_plan_t* plan, int dv, int64_t* byte
  *     anything; a value row that some row of a tile sees must be finite for the
  *     others.
  *   o: [num_q_rows, Hq, dv] contiguous, bf16 or fp32; lse: fp32 [num_q_rows, Hq].
- *   workspace: device, 16-byte aligned, at least cp_shared_workspace_size bytes;
+ *   workspace: device, 32-byte aligned, at least cp_shared_workspace_size bytes;
  *     overwritten; not to be shared by calls that may run at the same time.
  * P is rounded to bf16 for the second product, as in cp_attn_partial.  One or two
  * launches (the merge only where plan->needs_merge), no order of atomics: the

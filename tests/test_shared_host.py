@@ -16,18 +16,19 @@ from oracle import shared as osh
 ROWS = 256  # CPATTN_SHARED_ROWS
 CTA = ("dual0", "dual1", "single0", "single1", "single2", "u0", "u1", "u2")
 PIECE = ("q_row0", "q_pos0", "q_pos_step", "r0", "rows", "kv_head", "kv_row", "key0", "keys",
-         "ws_row", "u0", "u1")
+         "ws_row", "reps", "u1")
+UNIT = ("ws_row", "parts", "rows", "u0")
 
 
 def read_table(plan):
     i, t = plan.info, plan.table.tolist()
     at, out = 0, {}
-    for name, n, fields in (("ctas", i.num_ctas, CTA), ("pieces", i.num_pieces, PIECE)):
+    for name, n, fields in (("ctas", i.num_ctas, CTA), ("pieces", i.num_pieces, PIECE),
+                            ("units", i.num_units, UNIT)):
         out[name] = [dict(zip(fields, t[at + len(fields) * j: at + len(fields) * (j + 1)]))
                      for j in range(n)]
         at += n * len(fields)
-    for name, n in (("units", 2 * i.num_units), ("row_first", i.num_q_rows + 1),
-                    ("entries", 2 * i.num_entries)):
+    for name, n in (("row_first", i.num_q_rows + 1), ("entries", 2 * i.num_entries)):
         at += at % 2 if name == "entries" else 0
         out[name] = t[at: at + n]
         at += n
@@ -59,12 +60,14 @@ def check_plan(segs, N, Hq, Hkv, num_ctas):
     used = np.zeros(plan.info.ws_rows, dtype=np.int32)
     for p in T["pieces"]:
         assert 1 <= p["rows"] <= ROWS and p["keys"] >= 1
-        parts = p["rows"] * (4 if p["rows"] <= 32 else 2 if p["rows"] <= 64 else 1)
+        assert p["reps"] in (1, 2, 4) and p["reps"] * p["rows"] <= max(128, p["rows"])
+        parts = p["rows"] * p["reps"]
         assert 0 <= p["ws_row"] and p["ws_row"] + parts <= plan.info.ws_rows
         used[p["ws_row"]: p["ws_row"] + parts] += 1
         assert p["kv_row"] + p["keys"] <= plan.info.kv_rows
     assert (used == 1).all()
     # every row's entries lead to pieces that cover its runs' keys once
+    ends = {p["ws_row"]: p for p in T["pieces"]}
     for n, runs in enumerate(osh.row_runs(segs, N)):
         e0, e1 = T["row_first"][n], T["row_first"][n + 1]
         assert e1 - e0 == len(runs)
@@ -72,16 +75,17 @@ def check_plan(segs, N, Hq, Hkv, num_ctas):
             for e, (kv0, seen) in zip(range(e0, e1), runs):
                 unit0, i = T["entries"][2 * e], T["entries"][2 * e + 1]
                 packed = i * g + h % g
-                unit = unit0 + packed // ROWS * Hkv + h // g
-                at = 0
-                for j in range(T["units"][2 * unit], T["units"][2 * unit + 1]):
-                    p = T["pieces"][j]
+                u = T["units"][unit0 + packed // ROWS * Hkv + h // g]
+                at, part = 0, 0
+                while part < u["parts"]:
+                    p = ends[u["ws_row"] + part * u["rows"]]
                     assert p["kv_head"] == h // g and p["r0"] == packed // ROWS * ROWS
                     assert p["q_row0"] + (p["r0"] + packed % ROWS) // g == n
-                    assert packed % ROWS < p["rows"]
+                    assert packed % ROWS < p["rows"] == u["rows"]
                     assert p["key0"] == at and p["kv_row"] == kv0 + at
                     at += p["keys"]
-                assert at >= seen
+                    part += p["reps"]
+                assert part == u["parts"] and at >= seen
     return plan, T
 
 
