@@ -50,6 +50,7 @@ constexpr int BN = kSharedTileKeys;
 constexpr int kTailRows = 16;                   // box rows of the loads of a run's last tile
 constexpr int kProducerWarp = 8, kMmaWarp = 9;  // MMA: 9 and 10
 constexpr int kConvertWarp = 12;                // to 15
+constexpr int kConvertThreads = 128;
 
 struct SharedParams {
   const int32_t* table;
@@ -155,14 +156,16 @@ __device__ __forceinline__ bool piece_ok(const SharedParams& p, const SharedPiec
 }
 __device__ __forceinline__ int num_tiles(int keys) { return (keys - 1) / BN + 1; }
 
-// This block's list, and a check of every piece in it against the buffers: the
-// roles below walk the list on their own and rely on it.  tiles[s]: KV tiles of
-// stream s's small units (zeroed by the caller before a barrier).  All threads
-// call it; false (and CPATTN_ERR_RANGE) when the list cannot be run.
-__device__ __forceinline__ bool load_list(const SharedParams& p, SharedCta& c, int* tiles) {
+__device__ __forceinline__ SharedCta load_cta(const SharedParams& p) {
   const int4* w = reinterpret_cast<const int4*>(p.table) + 2LL * blockIdx.x;
   const int4 a = __ldg(w);
-  c = SharedCta{a.x, a.y, a.z, a.w, __ldg(&w[1].x), {0, 0, 0}};
+  return SharedCta{a.x, a.y, a.z, a.w, __ldg(&w[1].x), {0, 0, 0}};
+}
+// Checks every piece of this block's list against the buffers: the roles below walk
+// the list on their own and rely on it.  tiles[s]: KV tiles of stream s's small units
+// (zeroed by the caller before a barrier).  All threads call it; false (and
+// CPATTN_ERR_RANGE) when the list cannot be run.
+__device__ __forceinline__ bool check_list(const SharedParams& p, const SharedCta& c, int* tiles) {
   bool ok = c.dual0 >= 0 && c.dual0 <= c.dual1 && c.dual1 <= p.num_pieces && c.single0 >= 0 &&
             c.single0 <= c.single1 && c.single1 <= c.single2 && c.single2 <= p.num_pieces;
   if (ok) {
@@ -398,15 +401,22 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   grid_dep_trigger();  // the merge may be scheduled as blocks of this grid end
-
+  // the block's list and the tensor maps travel while the barriers are set up
+  SharedCta list = load_cta(p);
+  if (warp == kProducerWarp && lane == 0) {
+    prefetch_tmap(&tm_k);
+    prefetch_tmap(&tm_v);
+    prefetch_tmap(&tm_k_tail);
+    prefetch_tmap(&tm_v_tail);
+  }
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kStages; ++i) {
-      for (int u = 0; u < 3; ++u) mbar_init(full + u * C::kStages + i, QUANT ? 128 : 1);
+      for (int u = 0; u < 3; ++u) mbar_init(full + u * C::kStages + i, QUANT ? kConvertThreads : 1);
       mbar_init(empty + i, 2);  // a commit of each stream
     }
     for (int i = 0; i < C::kRawStages; ++i) {
       mbar_init(raw_full + i, 2);  // the TMA copy and the factors
-      mbar_init(raw_empty + i, 128);
+      mbar_init(raw_empty + i, kConvertThreads);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(q_full + s, 128);
@@ -431,8 +441,7 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
   const uint32_t tmem_base = *tmem_slot;
   const uint32_t q_base = smem_u32(smem);
   const uint32_t ring_base = smem_u32(smem + C::kRingOff);
-  SharedCta list;
-  if (!load_list(p, list, stream_tiles)) {
+  if (!check_list(p, list, stream_tiles)) {
     if (warp == kProducerWarp) tmem_dealloc(tmem_base, C::kTmemCols);
     return;
   }
@@ -458,12 +467,6 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
       constexpr int kLine = kBytes / BN / kChunks;  // bytes of a box row
       uint64_t* const emptyb = QUANT ? raw_empty : empty;
       uint8_t* const ring = smem + (QUANT ? C::kRawOff : C::kRingOff);
-      if (lane == 0) {
-        prefetch_tmap(&tm_k);
-        prefetch_tmap(&tm_v);
-        prefetch_tmap(&tm_k_tail);
-        prefetch_tmap(&tm_v_tail);
-      }
       auto copy = [&](const RingTile& r, int slot, uint64_t* bar) {
         uint8_t* dst = ring + slot * kBytes;
         if (r.live > BN - kTailRows) {
@@ -498,21 +501,31 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             return true;
           });
       } else {
-        RingTile last{};                       // the tile whose factors are still to be made
-        float sk[4] = {}, sv[4] = {};          // its rows' scales (and its V rows', of a K tile)
-        int ev0 = 0, ev1 = 0;                  // E of each stream's V rows
+        // The scales' lines are fetched to L1 when a tile's copy starts, and read a tile
+        // later (held in registers instead, the loop waited for them: 2000 cycles a tile).
+        RingTile last{};        // the tile whose factors are still to be made
+        int ev0 = 0, ev1 = 0;   // E of each stream's V rows
+        auto scale_at = [&](const float* scales, const RingTile& r) {
+          return scales + (long long)r.kv_head * p.s_head + r.kv_row;
+        };
         auto factors = [&]() {
           const int slot = (seq - 1) % kSt;
           const bool second = last.user() == 1;
+          const float* at = scale_at(last.is_v ? p.vs : p.ks, last) + lane;
+          const float* at_v = scale_at(p.vs, last) + lane;
+          float sc[4], mv = 0.f;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const bool live = i * 32 + lane < last.live;
+            sc[i] = live ? __ldg(at + i * 32) : 0.f;
+            if (!last.is_v && live) mv = fmaxf(mv, __ldg(at_v + i * 32));
+          }
           int ev = second ? ev1 : ev0, e = ev;
           if (!last.is_v) {
-            float mk = fmaxf(fmaxf(sk[0], sk[1]), fmaxf(sk[2], sk[3]));
-            float mv = fmaxf(fmaxf(sv[0], sv[1]), fmaxf(sv[2], sv[3]));
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) {
-              mk = fmaxf(mk, __shfl_xor_sync(0xffffffffu, mk, o));
-              mv = fmaxf(mv, __shfl_xor_sync(0xffffffffu, mv, o));
-            }
+            float mk = fmaxf(fmaxf(sc[0], sc[1]), fmaxf(sc[2], sc[3]));
+            // (scales are not negative: their bits order as integers)
+            mk = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mk)));
+            mv = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mv)));
             e = exponent_of(mk);
             ev = last.first ? exponent_of(mv) : max(ev, exponent_of(mv));
             if (second) ev1 = ev;
@@ -521,7 +534,7 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
           const float inv = exp2_int(-e);
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            raw_mul[slot * BN + i * 32 + lane] = (uint16_t)pack_f16x2(sk[i] * inv, 0.f);
+            raw_mul[slot * BN + i * 32 + lane] = (uint16_t)pack_f16x2(sc[i] * inv, 0.f);
           if (lane == 0) raw_note[slot] = RawNote{last.live, last.which | (last.is_v ? RawNote::kNoteV : 0), e, ev};
           __syncwarp();
           if (lane == 0) mbar_arrive(raw_full + slot);
@@ -531,21 +544,14 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
           if (!wait_warp(emptyb + slot, ((seq / kSt) & 1) ^ 1, abort_flag, p.timeout_ns)) return false;
           if (lane == 0) copy(r, slot, raw_full + slot);
           __syncwarp();
-          float a[4], b[4];
-          const long long at = (long long)r.kv_head * p.s_head + r.kv_row + lane;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const bool live = i * 32 + lane < r.live;
-            a[i] = live ? __ldg((r.is_v ? p.vs : p.ks) + at + i * 32) : 0.f;
-            b[i] = live && !r.is_v ? __ldg(p.vs + at + i * 32) : 0.f;
-          }
+          // lanes 0-15 the lines of this tile's scales, 16-31 those of a K tile's V
+          // (32-byte steps: a tile's 512 bytes start anywhere)
+          const int row = (lane & 15) * 8 + (lane & 1 ? 7 : 0);
+          if (row < r.live && (lane < 16 || !r.is_v))
+            asm volatile("prefetch.global.L1 [%0];" ::"l"(
+                scale_at(lane >= 16 || r.is_v ? p.vs : p.ks, r) + row));
           if (seq > 0) factors();
           last = r;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            sk[i] = a[i];
-            sv[i] = b[i];
-          }
           ++seq;
           return true;
         });
@@ -646,17 +652,15 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
         while (more) {
           const int slot = v_slot;
           const bool first = next_head, last = left == 0, both = next_dual;
-          ok = wait_tile(both ? 2 : s, slot) && wait_one(p_full + s, step & 1, abort_flag, p.timeout_ns);
-          if (!ok) break;
+          ok = wait_tile(both ? 2 : s, slot);
+          if (ok && both && !last) more = prepare();
+          ok = ok && wait_one(p_full + s, step & 1, abort_flag, p.timeout_ns);
           // Dual units: the streams' bursts of MMAs alternate, so that each stream's
           // softmax runs under the other's MMAs; without the turns the two fall into
           // step and the tensor core idles during both softmaxes.
-          if (both) {
-            if (!last) more = prepare();
-            if (ok && (s == 1 || step > 0))
-              ok = wait_one(turn + s, (s == 1 ? step : step - 1) & 1, abort_flag, p.timeout_ns);
-            if (!ok) break;
-          }
+          if (ok && both && (s == 1 || step > 0))
+            ok = wait_one(turn + s, (s == 1 ? step : step - 1) & 1, abort_flag, p.timeout_ns);
+          if (!ok) break;
           tc_fence_after();
           issue_pv(slot, first);
           if (last) mma_commit(o_full + s);
@@ -903,19 +907,20 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
         const float inv = none ? 0.f : exp2_int(ev) / l_run;
         const long long row = (long long)pc.ws_row + copy * pc.rows + r;
         float* dst = p.ws_o + row * D;
+        constexpr int kCols = QUANT ? 64 : D;  // (register budget)
 #pragma unroll
-        for (int q = 0; q < D / 64; ++q) {
-          uint32_t v[64];
-          tmem_ld32p(o_addr + q * 64, v);
-          tmem_ld32p(o_addr + q * 64 + 32, v + 32);
+        for (int q = 0; q < D / kCols; ++q) {
+          uint32_t v[kCols];
+#pragma unroll
+          for (int c = 0; c < kCols; c += 32) tmem_ld32p(o_addr + q * kCols + c, v + c);
           tmem_wait_ld();
           if (r < pc.rows) {
 #pragma unroll
-            for (int c = 0; c < 64; c += 8) {
+            for (int c = 0; c < kCols; c += 8) {
               float f[8];
 #pragma unroll
               for (int x = 0; x < 8; ++x) f[x] = none ? 0.f : __uint_as_float(v[c + x]) * inv;
-              store8(dst + q * 64 + c, f);
+              store8(dst + q * kCols + c, f);
             }
           }
         }
