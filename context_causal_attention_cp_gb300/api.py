@@ -718,19 +718,91 @@ def cp_select_pass_cost(new_tokens: int, cached_tokens: int, Hq: int, Hkv: int, 
 
 
 # --------------------------------------------------------- quantised KV cache --
-@dataclass
+# A decode step calls these once a layer, with kernels of a few microseconds: their
+# checks look at each tensor once and leave the messages to the failing path.
+def _bad(t, name, dtype, index):
+    """Raise for a tensor that is not of `dtype` (or one of them) on device `index`."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, the call runs on cuda:{index}")
+    raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+
+
+def _vector(t, name, dtype, n, index):
+    """Check an optional contiguous 1-D argument of at least n entries; its address."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype is not dtype or \
+            t.get_device() != index:
+        _bad(t, name, dtype, index)
+    if t.dim() != 1 or t.shape[0] < n or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous, 1-D, with at least {n} entries")
+    return t.data_ptr()
+
+
+def _call(index, stream, fn, where, *args):
+    """fn(*args, stream) with device `index` current; `stream` or its current one."""
+    if torch._C._cuda_getDevice() == index:
+        rc = fn(*args, torch._C._cuda_getCurrentRawStream(index) if stream is None
+                else stream.cuda_stream)
+    else:
+        with torch.cuda.device(index):
+            return _call(index, stream, fn, where, *args)
+    if rc:
+        L.check(rc, where)
+
+
+def _codes_of(codes, scales, name):
+    """cp_kv_codes_t of one side of a cache."""
+    if codes.dtype is not torch.float8_e4m3fn or scales.dtype is not torch.float32:
+        raise TypeError(f"{name} must be float8_e4m3fn with float32 scales, got {codes.dtype} "
+                        f"and {scales.dtype}")
+    if codes.device != scales.device:
+        raise ValueError(f"{name} is on {codes.device}, its scales on {scales.device}")
+    if codes.dim() != 3 or (codes.numel() and codes.stride(2) != 1):
+        raise ValueError(f"{name} must be [rows, Hkv, dim] with a contiguous last dim")
+    rows, Hkv, dim = codes.shape
+    if tuple(scales.shape) != (Hkv, rows) or (scales.numel() and scales.stride(1) != 1):
+        raise ValueError(f"the scales of {name} must be [{Hkv}, {rows}] with a contiguous last "
+                         f"dim")
+    # a tensor of one row or head may carry any stride for that dim
+    hs = codes.stride(1) if Hkv > 1 else dim
+    rs = codes.stride(0) if rows > 1 else (Hkv - 1) * hs + dim
+    ss = scales.stride(0) if Hkv > 1 else max(scales.stride(0), rows)
+    return L.KvCodes(codes.data_ptr(), scales.data_ptr(), rs, hs, ss)
+
+
+@dataclass(frozen=True)
 class KVCache:
     """Quantised KV rows (see cp_kv_codes_t in cpattn.h): codes float8_e4m3fn
     [rows, Hkv, d | dv] (last dim contiguous) and their scales fp32 [Hkv, rows]
-    (last dim contiguous).  ``v`` is None where V is part of K (absorbed MLA)."""
+    (last dim contiguous).  ``v`` is None where V is part of K (absorbed MLA).
+    Its tensors are checked once, when it is made."""
     k: torch.Tensor
     k_scale: torch.Tensor
     v: Optional[torch.Tensor] = None
     v_scale: Optional[torch.Tensor] = None
 
-    @property
-    def rows(self):
-        return self.k.shape[0]
+    def __post_init__(self):
+        if (self.v is None) != (self.v_scale is None):
+            raise ValueError("v and v_scale go together")
+        kc, vc = _codes_of(self.k, self.k_scale, "k"), None
+        if self.v is not None:
+            vc = _codes_of(self.v, self.v_scale, "v")
+            if self.v.shape[:2] != self.k.shape[:2] or self.v.device != self.k.device:
+                raise ValueError("k and v disagree on rows, heads or device")
+        rows, Hkv, d = self.k.shape
+        set_ = lambda name, x: object.__setattr__(self, name, x)  # noqa: E731 - frozen
+        set_("rows", rows)
+        set_("_sides", (kc, vc))
+        set_("_dims", (Hkv, d, 0 if self.v is None else self.v.shape[2]))
+        set_("_index", self.k.get_device())
+
+    def _device_index(self):
+        if self._index < 0:
+            raise ValueError("the cache must be on a CUDA device")
+        return self._index
 
 
 def alloc_kv_cache(rows, Hkv, d, dv=None, device="cuda") -> KVCache:
@@ -744,36 +816,16 @@ def alloc_kv_cache(rows, Hkv, d, dv=None, device="cuda") -> KVCache:
     return KVCache(k, ks, v, vs)
 
 
-def _check_codes(codes, scales, name, ref, rows, Hkv):
-    _dev(codes, name, torch.float8_e4m3fn, ref, contiguous=False)
-    _dev(scales, name + "_scale", torch.float32, ref, contiguous=False)
-    if codes.dim() != 3 or codes.shape[0] != rows or codes.shape[1] != Hkv or \
-            (codes.numel() and codes.stride(2) != 1):
-        raise ValueError(f"{name} must be [{rows}, {Hkv}, dim] with a contiguous last dim")
-    if tuple(scales.shape) != (Hkv, rows) or (scales.numel() and scales.stride(1) != 1):
-        raise ValueError(f"{name}_scale must be [{Hkv}, {rows}] with a contiguous last dim")
-
-
-def _codes(codes, scales):
-    # a tensor of one row or head may carry any stride for that dim
-    rows, Hkv, dim = codes.shape
-    hs = codes.stride(1) if Hkv > 1 else dim
-    rs = codes.stride(0) if rows > 1 else (Hkv - 1) * hs + dim
-    ss = scales.stride(0) if Hkv > 1 else max(scales.stride(0), rows)
-    return L.KvCodes(codes.data_ptr(), scales.data_ptr(), rs, hs, ss)
-
-
-def _cache_sides(cache, ref=None):
-    rows, Hkv = cache.k.shape[0], cache.k.shape[1]
-    if cache.k.dim() != 3:
-        raise ValueError("cache.k must be [rows, Hkv, d]")
-    if (cache.v is None) != (cache.v_scale is None):
-        raise ValueError("cache.v and cache.v_scale go together")
-    _check_codes(cache.k, cache.k_scale, "cache.k", ref, rows, Hkv)
-    if cache.v is not None:
-        _check_codes(cache.v, cache.v_scale, "cache.v", cache.k, rows, Hkv)
-    return (_codes(cache.k, cache.k_scale),
-            None if cache.v is None else _codes(cache.v, cache.v_scale))
+def _new_rows(x, name, dtype, n, Hkv, dim, index):
+    if not isinstance(x, torch.Tensor) or not x.is_cuda or x.dtype is not dtype or \
+            x.get_device() != index:
+        _bad(x, name, dtype, index)
+    if x.shape != (n, Hkv, dim):
+        raise ValueError(f"{name} must be [{n}, {Hkv}, {dim}], got {tuple(x.shape)}")
+    rs, hs, cs = x.stride()
+    if cs != 1 and x.numel():
+        raise ValueError(f"{name} needs a contiguous last dim")
+    return rs, hs
 
 
 def cp_kv_quantize(cache: KVCache, k, v=None, slots=None, *, status=None, stream=None) -> KVCache:
@@ -783,32 +835,19 @@ def cp_kv_quantize(cache: KVCache, k, v=None, slots=None, *, status=None, stream
     contiguous.  ``slots``: int32 [n], the cache row of each new row (negative:
     skipped); without it row i goes to cache row i.
     """
-    lib = L.load()
-    kc, vc = _cache_sides(cache)
+    index = cache._device_index()
+    Hkv, d, dv = cache._dims
     if (v is None) != (cache.v is None):
         raise ValueError("v goes with a cache that has V")
-    for x, c, name in ((k, cache.k, "k"), (v, cache.v, "v")):
-        if x is None and name == "v":
-            continue
-        _dev(x, name, (torch.bfloat16, torch.float32), cache.k, contiguous=False)
-        if x.dtype != k.dtype:
-            raise TypeError("k and v must have one dtype")
-        if x.dim() != 3 or x.shape[0] != k.shape[0] or tuple(x.shape[1:]) != tuple(c.shape[1:]):
-            raise ValueError(f"{name} must be [n, {c.shape[1]}, {c.shape[2]}]")
-        if x.numel() and x.stride(2) != 1:
-            raise ValueError(f"{name} needs a contiguous last dim")
+    dtype = torch.float32 if k.dtype is torch.float32 else torch.bfloat16
     n = k.shape[0]
-    if slots is not None:
-        _dev(slots, "slots", torch.int32, cache.k)
-        if slots.dim() != 1 or slots.shape[0] < n:
-            raise ValueError("slots must be int32 with one entry per row")
-    _status(status, cache.k)
-    vx = k if v is None else v
-    with torch.cuda.device(cache.k.device):
-        L.check(lib.cp_kv_quantize(
-            _p(k), k.stride(0), k.stride(1), _p(v), vx.stride(0), vx.stride(1),
-            1 if k.dtype == torch.float32 else 0, n, k.shape[1], k.shape[2], vx.shape[2],
-            _p(slots), kc, vc, cache.rows, _p(status), _stream(stream)), "cp_kv_quantize")
+    krs, khs = _new_rows(k, "k", dtype, n, Hkv, d, index)
+    vrs, vhs = (0, 0) if v is None else _new_rows(v, "v", dtype, n, Hkv, dv, index)
+    kc, vc = cache._sides
+    _call(index, stream, L.load().cp_kv_quantize, "cp_kv_quantize", k.data_ptr(), krs, khs,
+          None if v is None else v.data_ptr(), vrs, vhs, dtype is torch.float32, n, Hkv, d, dv,
+          _vector(slots, "slots", torch.int32, n, index), kc, vc, cache.rows,
+          _vector(status, "status", torch.int32, 1, index))
     return cache
 
 
@@ -818,46 +857,49 @@ def cp_kv_dequantize(cache: KVCache, idx=None, *, out_k=None, out_v=None, out_fp
     of row i), bf16 or fp32 (see cp_kv_dequantize in cpattn.h).  A negative
     index leaves its output row as it is.  Returns (k [n, Hkv, d], v [n, Hkv,
     dv] or None)."""
-    lib = L.load()
-    kc, vc = _cache_sides(cache)
-    n = cache.rows
+    index = cache._device_index()
+    Hkv, d, dv = cache._dims
+    n, at = cache.rows, None
     if idx is not None:
-        _dev(idx, "idx", torch.int32, cache.k)
-        if idx.dim() != 1:
-            raise ValueError("idx must be a 1-D int32 index")
+        at = _vector(idx, "idx", torch.int32, 0, index)
         n = idx.shape[0]
-    dtype = torch.float32 if out_fp32 else torch.bfloat16
-    if out_k is None:
-        out_k = torch.empty((n,) + tuple(cache.k.shape[1:]), dtype=dtype, device=cache.k.device)
     if out_v is not None and cache.v is None:
         raise ValueError("out_v goes with a cache that has V")
+    if out_k is None:
+        out_k = torch.empty((n, Hkv, d), device=cache.k.device,
+                            dtype=torch.float32 if out_fp32 else torch.bfloat16)
+    dtype = torch.float32 if out_k.dtype is torch.float32 else torch.bfloat16
     if out_v is None and cache.v is not None:
-        out_v = torch.empty((n,) + tuple(cache.v.shape[1:]), dtype=out_k.dtype,
-                            device=cache.k.device)
-    for out, c, name in ((out_k, cache.k, "out_k"), (out_v, cache.v, "out_v")):
-        if out is None:
-            continue
-        _dev(out, name, (torch.bfloat16, torch.float32), cache.k)
-        if out.dtype != out_k.dtype:
-            raise TypeError("out_k and out_v must have one dtype")
-        _shape(out, name, (n,) + tuple(c.shape[1:]))
-    _status(status, cache.k)
-    with torch.cuda.device(cache.k.device):
-        L.check(lib.cp_kv_dequantize(
-            kc, vc, cache.rows, cache.k.shape[1], cache.k.shape[2],
-            0 if cache.v is None else cache.v.shape[2], _p(idx), n, _p(out_k), _p(out_v),
-            1 if out_k.dtype == torch.float32 else 0, _p(status), _stream(stream)),
-            "cp_kv_dequantize")
+        out_v = torch.empty((n, Hkv, dv), dtype=dtype, device=cache.k.device)
+    _new_rows(out_k, "out_k", dtype, n, Hkv, d, index)
+    if out_v is not None:
+        _new_rows(out_v, "out_v", dtype, n, Hkv, dv, index)
+    if not out_k.is_contiguous() or (out_v is not None and not out_v.is_contiguous()):
+        raise ValueError("out_k and out_v must be contiguous")
+    kc, vc = cache._sides
+    _call(index, stream, L.load().cp_kv_dequantize, "cp_kv_dequantize", kc, vc, cache.rows, Hkv, d,
+          dv, at, n, out_k.data_ptr(), None if out_v is None else out_v.data_ptr(),
+          dtype is torch.float32, _vector(status, "status", torch.int32, 1, index))
     return out_k, out_v
 
 
 # ----------------------------------------------------------- shared prefix --
-@dataclass
+@dataclass(frozen=True)
 class SharedPlan:
     """The plan of cp_attn_shared for one set of lengths (see cpattn.h)."""
     info: L.SharedPlanInfo
     table: torch.Tensor          # int32 [table_ints], device
     segs_host: torch.Tensor      # int32 [S, 8], host: the segments it was made from
+
+    def __post_init__(self):
+        if self.table.dtype is not torch.int32 or not self.table.is_contiguous() or \
+                self.table.numel() < self.info.table_ints:
+            raise ValueError("table must be contiguous int32 with the plan's words")
+        i = self.info
+        set_ = lambda name, x: object.__setattr__(self, name, x)  # noqa: E731 - frozen
+        set_("_shape", (i.num_q_rows, i.Hq, i.Hkv))
+        set_("_index", self.table.get_device())
+        set_("_table", self.table.data_ptr())
 
     @property
     def num_q_rows(self):
@@ -946,46 +988,71 @@ def cp_attn_shared(plan: SharedPlan, q, k, v, scale, *, k_scale=None, v_scale=No
     ``workspace``: alloc_shared_workspace(plan, dv), allocated when omitted.
     Returns (O [N, Hq, dv], LSE [N, Hq], workspace).
     """
-    lib = L.load()
-    info = plan.info
-    _dev(q, "q", torch.bfloat16, plan.table, contiguous=False)
+    index = plan._index
+    if index < 0:
+        raise ValueError("the plan must be on a CUDA device")
+    N, Hq, Hkv = plan._shape
     quant = k_scale is not None
     if quant != (v_scale is not None):
         raise ValueError("k_scale and v_scale go together")
     kv_dtype = torch.float8_e4m3fn if quant else torch.bfloat16
-    _dev(k, "k", kv_dtype, q, contiguous=False)
-    _dev(v, "v", kv_dtype, q, contiguous=False)
+    for t, name, dtype in ((q, "q", torch.bfloat16), (k, "k", kv_dtype), (v, "v", kv_dtype)):
+        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype is not dtype or \
+                t.get_device() != index:
+            _bad(t, name, dtype, index)
     if q.dim() != 3 or k.dim() != 3 or v.dim() != 3:
         raise ValueError("q, k and v are [rows, heads, dim]")
-    N, Hq, d = q.shape
-    rows, Hkv, dv = v.shape
-    if k.shape[0] != rows or k.shape[1] != Hkv or k.shape[2] != d:
-        raise ValueError("k and v disagree on rows or heads, or k and q on the head dim")
-    if (N, Hq, Hkv) != (info.num_q_rows, info.Hq, info.Hkv):
-        raise ValueError(f"the plan is for {info.num_q_rows} query rows, {info.Hq} / {info.Hkv} "
-                         f"heads; got {N}, {Hq} / {Hkv}")
-    if (N and q.stride(2) != 1) or (rows and (k.stride(2) != 1 or v.stride(2) != 1)):
+    rows, d, dv = v.shape[0], q.shape[2], v.shape[2]
+    if q.shape != (N, Hq, d):
+        raise ValueError(f"the plan is for q [{N}, {Hq}, d], got {tuple(q.shape)}")
+    if k.shape != (rows, Hkv, d) or v.shape != (rows, Hkv, dv):
+        raise ValueError(f"k and v must be [rows, {Hkv}, dim] of equal rows and k's dim q's, got "
+                         f"{tuple(k.shape)} and {tuple(v.shape)}")
+    (qrs, qhs, qcs), (krs, khs, kcs), (vrs, vhs, vcs) = q.stride(), k.stride(), v.stride()
+    if (qcs != 1 and N) or ((kcs != 1 or vcs != 1) and rows):
         raise ValueError("q, k and v need a contiguous last dim")
-    kc, vc = _codes(k, k_scale if quant else k), _codes(v, v_scale if quant else v)
+    # a tensor of one row or head may carry any stride for that dim
+    if N <= 1:
+        qrs = Hq * d
+    if Hq == 1:
+        qhs = d
+    if Hkv == 1:
+        khs, vhs = d, dv
+    if rows <= 1:
+        krs, vrs = (Hkv - 1) * khs + d, (Hkv - 1) * vhs + dv
+    ks = vs = None
     scale_stride = 0
     if quant:
-        _check_codes(k, k_scale, "k", q, rows, Hkv)
-        _check_codes(v, v_scale, "v", q, rows, Hkv)
-        scale_stride = kc.scale_stride
-        if vc.scale_stride != scale_stride:
+        for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+            if not isinstance(t, torch.Tensor) or not t.is_cuda or \
+                    t.dtype is not torch.float32 or t.get_device() != index:
+                _bad(t, name, torch.float32, index)
+            if t.shape != (Hkv, rows) or (t.stride(1) != 1 and rows > 1):
+                raise ValueError(f"{name} must be [{Hkv}, {rows}] with a contiguous last dim")
+        scale_stride = k_scale.stride(0) if Hkv > 1 else rows
+        if Hkv > 1 and v_scale.stride(0) != scale_stride:
             raise ValueError("k_scale and v_scale must have one row stride")
-    out, lse = _attn_outputs(out, lse, N, Hq, dv, out_fp32, q)
-    if out.shape[0] != N:
-        raise ValueError("out needs one row per query row")
+        ks, vs = k_scale.data_ptr(), v_scale.data_ptr()
+    if out is None:
+        out = torch.empty((N, Hq, dv), dtype=torch.float32 if out_fp32 else torch.bfloat16,
+                          device=q.device)
+    if lse is None:
+        lse = torch.empty((N, Hq), dtype=torch.float32, device=q.device)
+    f32 = out.dtype is torch.float32
+    if not out.is_cuda or not (f32 or out.dtype is torch.bfloat16) or out.get_device() != index:
+        _bad(out, "out", (torch.bfloat16, torch.float32), index)
+    if not lse.is_cuda or lse.dtype is not torch.float32 or lse.get_device() != index:
+        _bad(lse, "lse", torch.float32, index)
+    if out.shape != (N, Hq, dv) or lse.shape != (N, Hq):
+        raise ValueError(f"out must be [{N}, {Hq}, {dv}] and lse [{N}, {Hq}]")
+    if not out.is_contiguous() or not lse.is_contiguous():
+        raise ValueError("out and lse must be contiguous")
     if workspace is None:
         workspace = alloc_shared_workspace(plan, dv)
-    _dev(workspace, "workspace", torch.uint8, q)
-    _status(status, q)
-    with torch.cuda.device(q.device):
-        L.check(lib.cp_attn_shared(
-            info, _p(plan.table), _p(q), q.stride(0) if N > 1 else Hq * d,
-            q.stride(1) if Hq > 1 else d, _p(k), kc.row_stride, kc.head_stride, _p(k_scale), _p(v),
-            vc.row_stride, vc.head_stride, _p(v_scale), scale_stride, rows, d, dv, float(scale),
-            _p(out), 1 if out.dtype == torch.float32 else 0, _p(lse), _p(workspace),
-            workspace.numel(), _p(status), _stream(stream)), "cp_attn_shared")
+    nbytes = workspace.numel()
+    _call(index, stream, L.load().cp_attn_shared, "cp_attn_shared", plan.info, plan._table,
+          q.data_ptr(), qrs, qhs, k.data_ptr(), krs, khs, ks, v.data_ptr(), vrs, vhs, vs,
+          scale_stride, rows, d, dv, scale, out.data_ptr(), f32, lse.data_ptr(),
+          _vector(workspace, "workspace", torch.uint8, 0, index), nbytes,
+          _vector(status, "status", torch.int32, 1, index))
     return out, lse, workspace

@@ -4,7 +4,10 @@
 // For one vector x: a = max finite |x_c|, e = clamp(ceil(log2(a/448)), -117,
 // 119), scale = 2^e, code_c = e4m3(x_c 2^-e), value = code_c 2^e.  Both kernels
 // are HBM streams: a vector is read once, kept in registers between the maximum
-// and the rounding, and its codes are written once.
+// and the rounding, and its codes are written once.  L = 2^k lanes share a vector,
+// 16 elements (16 bytes of codes) each and step, and a thread works on kUnroll
+// rows at once, so that their loads travel together; which row, side and head a
+// thread has is settled once, before its loop over rows.
 #include <algorithm>
 #include <cstdint>
 
@@ -56,119 +59,189 @@ struct KvSide {  // one of K and V
   int dim;
 };
 
-// 8 consecutive elements as fp32.
+constexpr int kChunk = 16;  // elements of a lane's step
+
+// 16 consecutive elements, as they lie in memory.
 template <bool F32>
-__device__ __forceinline__ void load8(const void* x, long long at, float (&v)[8]) {
-  if (F32) {
-    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(x) + at);
-    const float4 a = __ldg(p), b = __ldg(p + 1);
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-  } else {
-    const uint4 a = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(x) + at));
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+struct Raw16 {
+  uint4 w[F32 ? 4 : 2];
+  __device__ __forceinline__ void load(const void* x, long long at) {
+    const uint4* p = F32 ? reinterpret_cast<const uint4*>(static_cast<const float*>(x) + at)
+                         : reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(x) + at);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = __uint_as_float(w[i] << 16);
-      v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    }
+    for (int i = 0; i < (F32 ? 4 : 2); ++i) w[i] = __ldcs(p + i);
   }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < (F32 ? 4 : 2); ++i) w[i] = make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ float at(int c) const {  // c a constant
+    const uint4& v = w[c / (F32 ? 4 : 8)];
+    const int i = F32 ? c % 4 : c % 8 / 2;
+    const uint32_t u = i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+    return __uint_as_float(F32 ? u : c % 2 ? u & 0xFFFF0000u : u << 16);
+  }
+};
+
+// A thread's place: row `row` of the block's rows, vector (side, head) and lane.  A
+// block has kKvThreads / (vectors * L) rows, or one row in several passes.
+struct KvPlace {
+  int row, rows, first;  // first: its (vector, lane) number, the others follow by kKvThreads
+  bool on;
+};
+__device__ __forceinline__ KvPlace kv_place(int lanes_per_row) {
+  KvPlace p;
+  p.rows = max(1, kKvThreads / lanes_per_row);
+  p.row = (int)threadIdx.x / lanes_per_row;
+  p.on = p.row < p.rows || lanes_per_row > kKvThreads;
+  if (lanes_per_row > kKvThreads) p.row = 0;
+  p.first = (int)threadIdx.x - p.row * lanes_per_row;
+  return p;
 }
 
-// A warp per (row, K or V, head) vector; lane l holds elements 8l.. of each 256.
-template <bool F32>
+// NC: chunks of a lane (dim <= 16 * L * NC).
+template <bool F32, int NC>
 __global__ void __launch_bounds__(kKvThreads)
-kv_quantize_kernel(const KvSide k, const KvSide v, int sides, int num_rows, int Hkv,
+kv_quantize_kernel(const KvSide k, const KvSide v, int sides, int num_rows, int Hkv, int log_l,
                    const int32_t* __restrict__ slots, int cache_rows, int32_t* status) {
-  const int lane = threadIdx.x & 31;
-  const long long vectors = (long long)num_rows * sides * Hkv;
-  const long long nwarps = ((long long)gridDim.x * blockDim.x) >> 5;
-  for (long long u = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5; u < vectors;
-       u += nwarps) {
-    const int h = (int)(u % Hkv);
-    const long long rs = u / Hkv;
-    const KvSide& s = (rs % sides) ? v : k;
-    const long long row = rs / sides;
-    const int slot = slots ? __ldg(slots + row) : (int)row;
-    if (slot < 0 || slot >= cache_rows) {
-      if (slot >= 0 && lane == 0) set_status(status, CPATTN_ERR_RANGE);
-      continue;
-    }
-    const long long at = row * s.x_row + (long long)h * s.x_head;
-    float x[kMaxDim / 256][8];
-    float a = 0.f;
+  constexpr int kUnroll = NC == 1 && !F32 ? 2 : 1;
+  const int L = 1 << log_l, lpr = (sides * Hkv) << log_l;
+  const KvPlace pl = kv_place(lpr);
+  if (!pl.on) return;
+  const uint32_t group = (L == 32 ? 0xffffffffu : (1u << L) - 1u) << (threadIdx.x & 31 & ~(L - 1));
+  const int step = gridDim.x * pl.rows;
+  for (int x = pl.first; x < lpr; x += kKvThreads) {
+    const int vec = x >> log_l, lane = x & (L - 1);
+    const KvSide& s = vec >= Hkv ? v : k;
+    const int h = vec >= Hkv ? vec - Hkv : vec;
+    const int c0 = lane * kChunk;
+    for (long long r0 = (long long)blockIdx.x * pl.rows + pl.row; r0 < num_rows;
+         r0 += (long long)step * kUnroll) {
+      Raw16<F32> raw[kUnroll][NC];
+      int slot[kUnroll];
 #pragma unroll
-    for (int i = 0; i < kMaxDim / 256; ++i) {
-      const int c = i * 256 + lane * 8;
-      if (c < s.dim) {
-        load8<F32>(s.x, at + c, x[i]);
+      for (int u = 0; u < kUnroll; ++u) {
+        const long long row = r0 + (long long)u * step;
+        slot[u] = row < num_rows ? (slots ? __ldg(slots + row) : (int)row) : -1;
+      }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float m = fabsf(x[i][j]);
-          a = fmaxf(a, m < INFINITY ? m : 0.f);
+      for (int u = 0; u < kUnroll; ++u) {
+        const long long row = r0 + (long long)u * step;
+        if (slot[u] >= cache_rows) {
+          if (lane == 0) set_status(status, CPATTN_ERR_RANGE);
+          slot[u] = -1;
+        }
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+          const int c = c0 + i * L * kChunk;
+          if (slot[u] >= 0 && c < s.dim) raw[u][i].load(s.x, row * s.x_row + h * s.x_head + c);
+          else raw[u][i].zero();
         }
       }
-    }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-    const int e = scale_exponent(a);
-    const float inv = exp2_int(-e);
-    uint8_t* dst = s.codes + (long long)slot * s.c_row + (long long)h * s.c_head;
+      for (int u = 0; u < kUnroll; ++u) {
+        float a = 0.f;
 #pragma unroll
-    for (int i = 0; i < kMaxDim / 256; ++i) {
-      const int c = i * 256 + lane * 8;
-      if (c < s.dim) {
-        uint32_t w[2];
+        for (int i = 0; i < NC; ++i)
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-          w[j] = (uint32_t)e4m3x2(x[i][4 * j] * inv, x[i][4 * j + 1] * inv) |
-                 (uint32_t)e4m3x2(x[i][4 * j + 2] * inv, x[i][4 * j + 3] * inv) << 16;
-        *reinterpret_cast<uint2*>(dst + c) = make_uint2(w[0], w[1]);
+          for (int c = 0; c < kChunk; ++c) {
+            const float m = fabsf(raw[u][i].at(c));
+            a = fmaxf(a, m < INFINITY ? m : 0.f);
+          }
+        for (int o = L >> 1; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(group, a, o));
+        if (slot[u] < 0) continue;
+        const int e = scale_exponent(a);
+        const float inv = exp2_int(-e);
+        uint8_t* dst = s.codes + (long long)slot[u] * s.c_row + h * s.c_head;
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+          const int c = c0 + i * L * kChunk;
+          if (c >= s.dim) continue;
+          uint32_t w[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            w[j] = (uint32_t)e4m3x2(raw[u][i].at(4 * j) * inv, raw[u][i].at(4 * j + 1) * inv) |
+                   (uint32_t)e4m3x2(raw[u][i].at(4 * j + 2) * inv, raw[u][i].at(4 * j + 3) * inv) << 16;
+          *reinterpret_cast<uint4*>(dst + c) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        if (lane == 0) s.scales[h * s.s_head + slot[u]] = exp2_int(e);
       }
     }
-    if (lane == 0) s.scales[(long long)h * s.s_head + slot] = exp2_int(e);
   }
 }
 
-// A warp per (row, K or V, head) vector.
-template <bool F32>
+template <bool F32, int NC>
 __global__ void __launch_bounds__(kKvThreads)
-kv_dequantize_kernel(const KvSide k, const KvSide v, int sides, int num_rows, int Hkv,
+kv_dequantize_kernel(const KvSide k, const KvSide v, int sides, int num_rows, int Hkv, int log_l,
                      const int32_t* __restrict__ idx, int cache_rows, int32_t* status) {
-  const int lane = threadIdx.x & 31;
-  const long long vectors = (long long)num_rows * sides * Hkv;
-  const long long nwarps = ((long long)gridDim.x * blockDim.x) >> 5;
-  for (long long u = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5; u < vectors;
-       u += nwarps) {
-    const int h = (int)(u % Hkv);
-    const long long rs = u / Hkv;
-    const KvSide& s = (rs % sides) ? v : k;
-    const long long row = rs / sides;
-    const int src = idx ? __ldg(idx + row) : (int)row;
-    if (src < 0 || src >= cache_rows) {
-      if (src >= 0 && lane == 0) set_status(status, CPATTN_ERR_RANGE);
-      continue;
-    }
-    const float scale = __ldg(s.scales + (long long)h * s.s_head + src);
-    const uint8_t* p = s.codes + (long long)src * s.c_row + (long long)h * s.c_head;
-    const long long at = (row * Hkv + h) * s.dim;
-    for (int c = lane * 8; c < s.dim; c += 256) {
-      const uint2 w = __ldg(reinterpret_cast<const uint2*>(p + c));
-      float x[8];
-      e4m3x2_to_f32((uint16_t)w.x, x[0], x[1]);
-      e4m3x2_to_f32((uint16_t)(w.x >> 16), x[2], x[3]);
-      e4m3x2_to_f32((uint16_t)w.y, x[4], x[5]);
-      e4m3x2_to_f32((uint16_t)(w.y >> 16), x[6], x[7]);
+  constexpr int kUnroll = 4 / NC;
+  const int L = 1 << log_l, lpr = (sides * Hkv) << log_l;
+  const KvPlace pl = kv_place(lpr);
+  if (!pl.on) return;
+  const int step = gridDim.x * pl.rows;
+  for (int x = pl.first; x < lpr; x += kKvThreads) {
+    const int vec = x >> log_l, lane = x & (L - 1);
+    const KvSide& s = vec >= Hkv ? v : k;
+    const int h = vec >= Hkv ? vec - Hkv : vec;
+    const int c0 = lane * kChunk;
+    for (long long r0 = (long long)blockIdx.x * pl.rows + pl.row; r0 < num_rows;
+         r0 += (long long)step * kUnroll) {
+      int src[kUnroll];
+      float scale[kUnroll];
+      uint4 w[kUnroll][NC];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] *= scale;
-      if (F32) {
-        float4* o = reinterpret_cast<float4*>(static_cast<float*>(s.out) + at + c);
-        o[0] = make_float4(x[0], x[1], x[2], x[3]);
-        o[1] = make_float4(x[4], x[5], x[6], x[7]);
-      } else {
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(s.out) + at + c) =
-            make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
-                       pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+      for (int u = 0; u < kUnroll; ++u) {
+        const long long row = r0 + (long long)u * step;
+        src[u] = row < num_rows ? (idx ? __ldg(idx + row) : (int)row) : -1;
+      }
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        if (src[u] >= cache_rows) {
+          if (lane == 0) set_status(status, CPATTN_ERR_RANGE);
+          src[u] = -1;
+        }
+        if (src[u] < 0) continue;
+        scale[u] = __ldg(s.scales + h * s.s_head + src[u]);
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+          const int c = c0 + i * L * kChunk;
+          if (c < s.dim)
+            w[u][i] = __ldg(reinterpret_cast<const uint4*>(s.codes + (long long)src[u] * s.c_row +
+                                                           h * s.c_head + c));
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        if (src[u] < 0) continue;
+        const long long at = ((r0 + (long long)u * step) * Hkv + h) * s.dim;
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+          const int c = c0 + i * L * kChunk;
+          if (c >= s.dim) continue;
+          const uint32_t q[4] = {w[u][i].x, w[u][i].y, w[u][i].z, w[u][i].w};
+          float f[16];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            e4m3x2_to_f32((uint16_t)q[j], f[4 * j], f[4 * j + 1]);
+            e4m3x2_to_f32((uint16_t)(q[j] >> 16), f[4 * j + 2], f[4 * j + 3]);
+          }
+#pragma unroll
+          for (int j = 0; j < 16; ++j) f[j] *= scale[u];
+          if (F32) {
+            float4* o = reinterpret_cast<float4*>(static_cast<float*>(s.out) + at + c);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              __stcs(o + j, make_float4(f[4 * j], f[4 * j + 1], f[4 * j + 2], f[4 * j + 3]));
+          } else {
+            uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(s.out) + at + c);
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+              __stcs(o + j, make_uint4(pack_bf16x2(f[8 * j], f[8 * j + 1]),
+                                       pack_bf16x2(f[8 * j + 2], f[8 * j + 3]),
+                                       pack_bf16x2(f[8 * j + 4], f[8 * j + 5]),
+                                       pack_bf16x2(f[8 * j + 6], f[8 * j + 7])));
+          }
+        }
       }
     }
   }
@@ -195,9 +268,19 @@ int cache_side(const cp_kv_codes_t* c, int dim, int Hkv, int cache_rows, KvSide*
   return CPATTN_OK;
 }
 
-unsigned kv_grid(long long vectors) {
-  const long long blocks = (vectors * 32 + kKvThreads - 1) / kKvThreads;
-  return (unsigned)std::min<long long>(blocks, 1 << 20);
+// Lanes of a vector (log2) and blocks of a launch: enough for the rows, and at most
+// some blocks per SM, the rest of the rows being the loop's.
+struct KvShape {
+  int log_l, chunks;
+  unsigned grid;
+};
+KvShape kv_shape(int num_rows, int vectors, int dim) {
+  KvShape s;
+  for (s.log_l = 0; s.log_l < 5 && (kChunk << s.log_l) < dim; ++s.log_l) {}
+  s.chunks = (dim + (kChunk << s.log_l) - 1) / (kChunk << s.log_l);
+  const long long lpr = (long long)vectors << s.log_l, rows = std::max<long long>(1, kKvThreads / lpr);
+  s.grid = (unsigned)std::min<long long>((num_rows + rows - 1) / rows, 152 * 16);
+  return s;
 }
 
 }  // namespace
@@ -232,10 +315,11 @@ extern "C" int cp_kv_quantize(const void* k, int64_t k_row_stride, int64_t k_hea
   vs.x_row = v_row_stride;
   vs.x_head = v_head_stride;
   const int sides = v ? 2 : 1;
-  const unsigned grid = kv_grid((long long)num_rows * sides * Hkv);
-  auto kern = x_is_fp32 ? kv_quantize_kernel<true> : kv_quantize_kernel<false>;
-  kern<<<grid, kKvThreads, 0, stream>>>(ks, vs, sides, num_rows, Hkv, slots, cache_rows,
-                                        status_dev);
+  const KvShape sh = kv_shape(num_rows, sides * Hkv, std::max(d, v ? dv : 0));
+  auto kern = sh.chunks == 1 ? (x_is_fp32 ? kv_quantize_kernel<true, 1> : kv_quantize_kernel<false, 1>)
+                             : (x_is_fp32 ? kv_quantize_kernel<true, 2> : kv_quantize_kernel<false, 2>);
+  kern<<<sh.grid, kKvThreads, 0, stream>>>(ks, vs, sides, num_rows, Hkv, sh.log_l, slots, cache_rows,
+                                           status_dev);
   return cudaGetLastError() == cudaSuccess ? CPATTN_OK : CPATTN_ERR_CUDA;
 }
 
@@ -255,8 +339,11 @@ extern "C" int cp_kv_dequantize(const cp_kv_codes_t* k_cache, const cp_kv_codes_
   ks.out = k_out;
   vs.out = v_out;
   const int sides = v_cache ? 2 : 1;
-  const unsigned grid = kv_grid((long long)num_rows * sides * Hkv);
-  auto kern = out_is_fp32 ? kv_dequantize_kernel<true> : kv_dequantize_kernel<false>;
-  kern<<<grid, kKvThreads, 0, stream>>>(ks, vs, sides, num_rows, Hkv, idx, cache_rows, status_dev);
+  const KvShape sh = kv_shape(num_rows, sides * Hkv, std::max(d, v_cache ? dv : 0));
+  auto kern = sh.chunks == 1
+                  ? (out_is_fp32 ? kv_dequantize_kernel<true, 1> : kv_dequantize_kernel<false, 1>)
+                  : (out_is_fp32 ? kv_dequantize_kernel<true, 2> : kv_dequantize_kernel<false, 2>);
+  kern<<<sh.grid, kKvThreads, 0, stream>>>(ks, vs, sides, num_rows, Hkv, sh.log_l, idx, cache_rows,
+                                           status_dev);
   return cudaGetLastError() == cudaSuccess ? CPATTN_OK : CPATTN_ERR_CUDA;
 }

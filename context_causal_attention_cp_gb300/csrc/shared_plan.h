@@ -50,7 +50,7 @@ __host__ __device__ constexpr bool shared_dual(int rows) { return rows > kShared
 // of its rows, and copy c works on the c-th half (quarter) of the keys of every KV
 // tile: the MMAs cost the same, and all four warps of a stream share the exponentials.
 // Each copy leaves a partial result, which pays from kSharedRepKeys keys on: TODO.
-constexpr int kSharedRepKeys = 512;
+constexpr int kSharedRepKeys = 2048;
 __host__ __device__ constexpr int shared_reps(int rows, long long keys) {
   return keys < kSharedRepKeys ? 1 : rows <= 32 ? 4 : rows <= 64 ? 2 : 1;
 }
