@@ -145,8 +145,8 @@ __device__ __forceinline__ SharedPiece load_piece(const SharedParams& p, int i) 
   const int4 a = __ldg(w), b = __ldg(w + 1), c = __ldg(w + 2);
   return SharedPiece{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, c.x, c.y, c.z, c.w};
 }
-__device__ __forceinline__ bool piece_ok(const SharedParams& p, const SharedPiece& pc, bool dual) {
-  return pc.rows >= 1 && pc.rows <= kRows && shared_dual(pc.rows) == dual && pc.r0 >= 0 &&
+__device__ __forceinline__ bool piece_ok(const SharedParams& p, const SharedPiece& pc, int kind) {
+  return pc.rows >= 1 && pc.rows <= kRows && shared_kind(pc.rows) == kind && pc.r0 >= 0 &&
          pc.q_row0 >= 0 &&
          (long long)pc.q_row0 + ((long long)pc.r0 + pc.rows - 1) / p.g < p.num_q_rows &&
          pc.kv_head >= 0 && pc.kv_head < p.Hkv && pc.keys >= 1 && pc.key0 >= 0 && pc.kv_row >= 0 &&
@@ -159,7 +159,8 @@ __device__ __forceinline__ int num_tiles(int keys) { return (keys - 1) / BN + 1;
 __device__ __forceinline__ SharedCta load_cta(const SharedParams& p) {
   const int4* w = reinterpret_cast<const int4*>(p.table) + 2LL * blockIdx.x;
   const int4 a = __ldg(w);
-  return SharedCta{a.x, a.y, a.z, a.w, __ldg(&w[1].x), {0, 0, 0}};
+  const int4 b = __ldg(w + 1);
+  return SharedCta{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 }
 // Checks every piece of this block's list against the buffers: the roles below walk
 // the list on their own and rely on it.  tiles[s]: KV tiles of stream s's small units
@@ -167,13 +168,17 @@ __device__ __forceinline__ SharedCta load_cta(const SharedParams& p) {
 // CPATTN_ERR_RANGE) when the list cannot be run.
 __device__ __forceinline__ bool check_list(const SharedParams& p, const SharedCta& c, int* tiles) {
   bool ok = c.dual0 >= 0 && c.dual0 <= c.dual1 && c.dual1 <= p.num_pieces && c.single0 >= 0 &&
-            c.single0 <= c.single1 && c.single1 <= c.single2 && c.single2 <= p.num_pieces;
+            c.single0 <= c.single1 && c.single1 <= c.single2 && c.single2 <= p.num_pieces &&
+            c.small0 >= 0 && c.small0 <= c.small1 && c.small1 <= p.num_pieces &&
+            (c.small0 == c.small1 || (c.dual0 == c.dual1 && c.single0 == c.single2));
   if (ok) {
     for (int i = c.dual0 + threadIdx.x; i < c.dual1; i += blockDim.x)
-      ok = ok && piece_ok(p, load_piece(p, i), true);
+      ok = ok && piece_ok(p, load_piece(p, i), 0);
+    for (int i = c.small0 + threadIdx.x; i < c.small1; i += blockDim.x)
+      ok = ok && piece_ok(p, load_piece(p, i), 2);
     for (int i = c.single0 + threadIdx.x; i < c.single2; i += blockDim.x) {
       const SharedPiece pc = load_piece(p, i);
-      ok = ok && piece_ok(p, pc, false);
+      ok = ok && piece_ok(p, pc, 1);
       if (ok) atomicAdd(tiles + (i >= c.single1), num_tiles(pc.keys));
     }
   }
@@ -181,6 +186,13 @@ __device__ __forceinline__ bool check_list(const SharedParams& p, const SharedCt
   ok = ok && (tiles[0] == tiles[1] || tiles[0] == tiles[1] + 1);
   if (!ok && threadIdx.x == 0) set_status(p.status, CPATTN_ERR_RANGE);
   return ok;
+}
+
+// Byte offset of 16-code chunk `chunk` of row `row` in a raw e4m3 tile: rows of D bytes,
+// their chunks swizzled (128-byte swizzle at D = 128, 64-byte at D = 64).
+template <int D>
+__device__ __forceinline__ uint32_t code_at(int row, int chunk) {
+  return D == 128 ? row * 128 + ((chunk ^ (row & 7)) << 4) : row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4);
 }
 
 // Two barriers at once (their polls overlap).
@@ -371,6 +383,14 @@ __device__ __forceinline__ void store8(float* at, const float (&f)[8]) {
                : "memory");
 }
 
+}  // namespace
+}  // namespace cpattn
+
+#include "attn_shared_small.cuh"  // run_small, on the pieces above
+
+namespace cpattn {
+namespace {
+
 template <int D, bool QUANT>
 __global__ void __launch_bounds__(SharedCfg<D, QUANT>::kThreads, 1)
 attn_shared_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
@@ -409,6 +429,14 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     prefetch_tmap(&tm_k_tail);
     prefetch_tmap(&tm_v_tail);
   }
+  if (threadIdx.x < 2) stream_tiles[threadIdx.x] = 0;
+  __syncthreads();
+  if (!check_list(p, list, stream_tiles)) return;
+  if (list.small0 < list.small1) {
+    run_small<D, QUANT>(p, list, smem, &tm_k, &tm_v, &tm_k_tail, &tm_v_tail);
+    return;
+  }
+  const int steps = stream_tiles[0] + stream_tiles[1];  // of the single units
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kStages; ++i) {
       for (int u = 0; u < 3; ++u) mbar_init(full + u * C::kStages + i, QUANT ? kConvertThreads : 1);
@@ -425,7 +453,6 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
       mbar_init(o_full + s, 1);
       mbar_init(turn + s, 1);
       mbar_init(bar_drain + s, 1);
-      stream_tiles[s] = 0;
     }
     *abort_flag = 0;
     *issued_loads = *issued_phases = 0;
@@ -441,12 +468,6 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
   const uint32_t tmem_base = *tmem_slot;
   const uint32_t q_base = smem_u32(smem);
   const uint32_t ring_base = smem_u32(smem + C::kRingOff);
-  if (!check_list(p, list, stream_tiles)) {
-    if (warp == kProducerWarp) tmem_dealloc(tmem_base, C::kTmemCols);
-    return;
-  }
-  const int steps = stream_tiles[0] + stream_tiles[1];  // of the small units
-
   // A ring slot has a full barrier for each user (stream 0, stream 1, both), so that
   // every waiter sees all phases of the barriers it waits on; their parities are kept
   // as bits of a word, `user * kStages + slot`.
@@ -704,7 +725,7 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
         const RawNote note = raw_note[raw];
         if (w == 0 && lane == 0 && note.which < RawNote::kNoteV)
           tile_exp[note.which] = make_int2(note.ek, note.ev);
-        const uint8_t* src = smem + C::kRawOff + raw * C::kRawTile + (w * 32 + rl) * D + cl * 8;
+        const uint8_t* src = smem + C::kRawOff + raw * C::kRawTile + (cl & 1) * 8;
         const uint16_t* mul = raw_mul + raw * BN + w * 32 + rl;
         uint8_t* dst = smem + C::kRingOff + slot * C::kTile + (w * 32 + rl) * 128;
         const int live = note.live - w * 32 - rl;
@@ -719,7 +740,8 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             m[x] = mul[r0 + 4 * x];
 #pragma unroll
             for (int h = 0; h < kHalves; ++h)
-              v[x][h] = *reinterpret_cast<const uint2*>(src + (r0 + 4 * x) * D + h * 64);
+              v[x][h] = *reinterpret_cast<const uint2*>(
+                  src + code_at<D>(w * 32 + rl + r0 + 4 * x, h * 4 + (cl >> 1)));
           }
           if (live < 32) {
 #pragma unroll
@@ -1130,7 +1152,8 @@ __global__ void __launch_bounds__(kMergeThreads) shared_merge_kernel(const Share
 }
 
 // 3-D map of a code buffer (cols, heads, rows) with a D-column x 1-head box, rows
-// packed in shared memory; out-of-range rows read as zero.
+// packed in shared memory and swizzled over their length (see code_at); out-of-range
+// rows read as zero.
 bool make_code_map(CUtensorMap* m, const void* base, int cols, int heads, long long rows,
                    long long head_stride, long long row_stride, int box_rows) {
   auto enc = tensor_map_encoder();
@@ -1140,7 +1163,8 @@ bool make_code_map(CUtensorMap* m, const void* base, int cols, int heads, long l
   cuuint32_t box[3] = {(cuuint32_t)cols, 1, (cuuint32_t)box_rows};
   cuuint32_t estr[3] = {1, 1, 1};
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+             CU_TENSOR_MAP_INTERLEAVE_NONE,
+             cols == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -1151,8 +1175,9 @@ struct SharedMaps {  // full tiles, then the tail boxes
 template <int D, bool QUANT>
 int launch_shared(const SharedMaps& m, const SharedParams& p, int num_ctas, cudaStream_t stream) {
   using C = SharedCfg<D, QUANT>;
+  constexpr int kSmem = std::max(C::kSmemBytes, SmallCfg<D, QUANT>::kSmemBytes);
   auto kern = attn_shared_kernel<D, QUANT>;
-  if (!allow_smem(kern, C::kSmemBytes)) return CPATTN_ERR_CUDA;
+  if (!allow_smem(kern, kSmem)) return CPATTN_ERR_CUDA;
   // setmaxnreg.inc waits until the block's launch allocation covers the split;
   // refuse a build whose register count could not (a property of this binary).
   static int regs_ok = 0;  // 0 not checked yet, 1 ok, -1 refused
@@ -1165,7 +1190,7 @@ int launch_shared(const SharedMaps& m, const SharedParams& p, int num_ctas, cuda
                   : -1;
   }
   if (regs_ok < 0) return CPATTN_ERR_UNSUPPORTED;
-  return launch_kernel(kern, (unsigned)num_ctas, C::kThreads, C::kSmemBytes, stream, false, m.k, m.v,
+  return launch_kernel(kern, (unsigned)num_ctas, C::kThreads, kSmem, stream, false, m.k, m.v,
                        m.k_tail, m.v_tail, p) == cudaSuccess
              ? CPATTN_OK
              : CPATTN_ERR_CUDA;

@@ -1,14 +1,14 @@
 // Host plan of cp_attn_shared: units, their cut into pieces and the merge lists.
 //
-// The units (segment, packed-row tile, KV head), dual ones first, are walked in a
+// The units (segment, packed-row tile, KV head), kind by kind, are walked in a
 // fixed order and their keys dealt to the thread blocks one after the other: each
 // block is filled up to a budget, so a unit is cut only where a block is full, and
-// every block's cost is within a KV tile of the others'.  The smallest budget that
-// needs no more than num_ctas blocks is found by bisection.  A piece costs its KV
-// tiles plus a fixed part (its queries' load and its partial's store), so that
-// short units are not shredded.  A block's run of small units is cut once more, at
-// half its KV tiles, between the block's two streams.  Nothing is allocated: each
-// pass walks the segment table again.
+// every block's cost is within a KV tile of the others' (a block with small units has
+// no others).  The smallest budget that needs no more than num_ctas blocks is found by
+// bisection.  A piece costs its KV tiles plus a fixed part (its queries' load and its
+// partial's store), so that short units are not shredded.  A block's run of single
+// units is cut once more, at half its KV tiles, between the block's two streams.
+// Nothing is allocated: each pass walks the segment table again.
 #include <algorithm>
 #include <cstdint>
 
@@ -18,13 +18,18 @@ namespace cpattn {
 namespace {
 
 constexpr int kKeys = kSharedTileKeys;
+// Costs by the kind of unit (dual, single, small), of a KV tile and of a piece's fixed
+// part.
 #ifndef CPATTN_SHARED_COSTS
-#define CPATTN_SHARED_COSTS 16, 24, 16
+#define CPATTN_SHARED_COSTS {24, 16, 16}, {24, 16, 8}
 #endif
-constexpr int kCosts[3] = {CPATTN_SHARED_COSTS};
-constexpr int kTileCost = kCosts[0];   // one KV tile for one MMA tile of rows
-constexpr int kDualCost = kCosts[1];   // one KV tile for two
-constexpr int kPieceCost = kCosts[2];  // a piece's fixed part
+constexpr int kCosts[2][3] = {CPATTN_SHARED_COSTS};
+long long tile_cost(int rows) { return kCosts[0][shared_kind(rows)]; }
+long long piece_cost(int rows) { return kCosts[1][shared_kind(rows)]; }
+constexpr int kMinCost = std::min({kCosts[0][0] + kCosts[1][0], kCosts[0][1] + kCosts[1][1],
+                                   kCosts[0][2] + kCosts[1][2]});
+constexpr int kMaxCost = std::max({kCosts[0][0] + kCosts[1][0], kCosts[0][1] + kCosts[1][1],
+                                   kCosts[0][2] + kCosts[1][2]});
 constexpr long long kMaxUnits = 1LL << 22;
 constexpr int kMaxCtas = 4096;
 
@@ -43,7 +48,7 @@ struct Line {
 };
 // A place in the line: the next key to deal is key0 of the unit (seg, tile, head).
 struct Place {
-  bool dual = true;      // dual units first, then the others
+  int kind = 0;          // units of this kind, then those of the next
   bool end = false;
   int seg = 0, head = 0;
   long long tile = 0, key0 = 0;
@@ -69,12 +74,10 @@ void measure(const Line& L, Place& p) {
 void settle(const Line& L, Place& p) {
   while (!p.end) {
     if (p.seg >= L.num_segs) {
-      if (!p.dual) {
-        p.end = true;
-        return;
-      }
+      const int kind = p.kind + 1;
       p = Place{};
-      p.dual = false;
+      p.kind = kind;
+      p.end = kind > 2;
       continue;
     }
     if (p.tile >= num_tiles(L.segs[p.seg], L.g)) {
@@ -85,7 +88,7 @@ void settle(const Line& L, Place& p) {
       continue;
     }
     measure(L, p);
-    if (shared_dual(p.rows) != p.dual || p.keys == 0) {
+    if (shared_kind(p.rows) != p.kind || p.keys == 0) {
       ++p.tile;
       p.head = 0;
       p.key0 = 0;
@@ -103,15 +106,18 @@ void settle(const Line& L, Place& p) {
 template <class F>
 void share(const Line& L, Place& p, long long budget, F&& f) {
   long long used = 0;
-  for (settle(L, p); !p.end; settle(L, p)) {
-    const long long cost = p.dual ? kDualCost : kTileCost;
-    const long long fit = std::min((budget - used - kPieceCost) / cost, kv_tiles(p.keys - p.key0));
-    if (fit < 1) return;
+  settle(L, p);
+  const bool small = p.kind == 2;
+  for (; !p.end; settle(L, p)) {
+    if ((p.kind == 2) != small) return;
+    const long long cost = tile_cost(p.rows), fixed = piece_cost(p.rows);
+    const long long fit = std::min((budget - used - fixed) / cost, kv_tiles(p.keys - p.key0));
+    if (budget - used < fixed + cost) return;
     const long long n = std::min(p.keys - p.key0, fit * kKeys);
     f(Cut{L.segs + p.seg, p.unit0 + p.tile * L.Hkv + p.head, p.tile * CPATTN_SHARED_ROWS, p.key0, n,
           p.rows, p.head, shared_reps(p.rows, p.keys)});
     p.key0 += n;
-    used += kPieceCost + fit * cost;
+    used += fixed + fit * cost;
   }
 }
 bool fits(const Line& L, long long budget, int num_ctas) {
@@ -120,19 +126,19 @@ bool fits(const Line& L, long long budget, int num_ctas) {
   settle(L, p);
   return p.end;
 }
-// Calls f(cta, cut, stream) for every piece in the table's order of each kind:
-// stream -1 for dual pieces, else the stream that has it.
+// Calls f(cta, cut, stream) for every piece in the table's order of each kind (stream:
+// that has a single piece).
 template <class F>
 void deal(const Line& L, long long budget, int num_ctas, F&& f) {
   Place p;
   for (int c = 0; c < num_ctas; ++c) {
     Place ahead = p;
     long long tiles = 0;
-    share(L, ahead, budget, [&](const Cut& k) { if (!shared_dual(k.rows)) tiles += kv_tiles(k.keys); });
+    share(L, ahead, budget, [&](const Cut& k) { if (shared_kind(k.rows) == 1) tiles += kv_tiles(k.keys); });
     long long left = (tiles + 1) / 2;  // KV tiles that stream 0 still takes
     share(L, p, budget, [&](const Cut& k) {
-      if (shared_dual(k.rows)) {
-        f(c, k, -1);
+      if (shared_kind(k.rows) != 1) {
+        f(c, k, 0);
         return;
       }
       Cut a = k, b = k;
@@ -147,7 +153,7 @@ void deal(const Line& L, long long budget, int num_ctas, F&& f) {
 }
 
 bool plan_ok(const cp_shared_plan_t& p) {
-  return p.num_q_rows >= 0 && p.Hq >= 1 && p.Hkv >= 1 && p.Hq % p.Hkv == 0 && p.num_ctas >= 1 &&
+  return p.num_q_rows >= 0 && p.Hq >= 1 && p.Hkv >= 1 && p.Hq % p.Hkv == 0 && p.num_ctas >= 2 &&
          p.num_ctas <= kMaxCtas && p.num_units >= 0 && p.num_pieces >= 0 && p.num_entries >= 0 &&
          p.kv_rows >= 0 && p.budget >= 0 && p.ws_rows >= 0 && p.table_ints == shared_table(p).total;
 }
@@ -172,7 +178,7 @@ using namespace cpattn;
 extern "C" int cp_shared_plan_size(const cp_segment_t* segs, int num_segs, int num_q_rows, int Hq,
                                    int Hkv, int num_ctas, cp_shared_plan_t* plan) {
   if (!plan || num_segs < 0 || (num_segs > 0 && !segs) || num_q_rows < 0 || Hq < 1 || Hkv < 1 ||
-      Hq % Hkv != 0 || num_ctas < 1 || num_ctas > kMaxCtas)
+      Hq % Hkv != 0 || num_ctas < 2 || num_ctas > kMaxCtas)
     return CPATTN_ERR_INVALID_ARG;
   if (num_segs > kMaxUnits) return CPATTN_ERR_TOO_LARGE;
   const int rc = check_segments(segs, num_segs, num_q_rows);
@@ -190,13 +196,17 @@ extern "C" int cp_shared_plan_size(const cp_segment_t* segs, int num_segs, int n
   long long cost = 0;
   {
     Place p;
-    share(L, p, INT64_MAX / 4, [&](const Cut& k) {
-      cost += kPieceCost + kv_tiles(k.keys) * (shared_dual(k.rows) ? kDualCost : kTileCost);
-    });
+    for (int part = 0; part < 2; ++part)  // the small units are a share of their own
+      share(L, p, INT64_MAX / 4, [&](const Cut& k) {
+        cost += piece_cost(k.rows) + kv_tiles(k.keys) * tile_cost(k.rows);
+      });
   }
-  long long lo = kPieceCost + std::min(kTileCost, kDualCost);
-  long long hi = std::max(lo, cost / num_ctas + 2 * (kPieceCost + kDualCost));
-  while (!fits(L, hi, num_ctas)) hi *= 2;
+  long long lo = kMinCost, hi = std::max<long long>(lo, cost / num_ctas + 2 * kMaxCost);
+  while (!fits(L, hi, num_ctas)) {
+    // one block cannot hold small units and others: it takes two
+    if (hi > (1LL << 40)) return CPATTN_ERR_INVALID_ARG;
+    hi *= 2;
+  }
   while (lo < hi) {
     const long long mid = (lo + hi) / 2;
     if (fits(L, mid, num_ctas)) hi = mid;
@@ -233,7 +243,7 @@ extern "C" int cp_shared_plan(const cp_segment_t* segs, int num_segs, const cp_s
   const Line L{segs, num_segs, plan->Hq / plan->Hkv, plan->Hkv};
   const int N = plan->num_q_rows;
   // the table must be the one that was sized: check the counts before writing
-  long long tiles = 0, ents = 0, np = 0, duals = 0, ws = 0;
+  long long tiles = 0, ents = 0, np = 0, kinds[3] = {}, ws = 0;
   for (int i = 0; i < num_segs; ++i) {
     tiles += num_tiles(segs[i], L.g);
     ents += segs[i].q_len;
@@ -241,9 +251,9 @@ extern "C" int cp_shared_plan(const cp_segment_t* segs, int num_segs, const cp_s
   if (tiles * L.Hkv != plan->num_units || ents != plan->num_entries ||
       !fits(L, plan->budget, plan->num_ctas))
     return CPATTN_ERR_INVALID_ARG;
-  deal(L, plan->budget, plan->num_ctas, [&](int, const Cut& k, int stream) {
+  deal(L, plan->budget, plan->num_ctas, [&](int, const Cut& k, int) {
     ++np;
-    duals += stream < 0;
+    ++kinds[shared_kind(k.rows)];
     ws += k.reps * k.rows;
   });
   if (np != plan->num_pieces || ws != plan->ws_rows) return CPATTN_ERR_INVALID_ARG;
@@ -276,21 +286,25 @@ extern "C" int cp_shared_plan(const cp_segment_t* segs, int num_segs, const cp_s
 
   for (int u = 0; u < plan->num_units; ++u) units[u] = SharedUnit{};
   for (int c = 0; c < plan->num_ctas; ++c) ctas[c] = SharedCta{};
-  int32_t next[2] = {0, (int32_t)duals}, ws_row = 0;  // next dual and next single piece
+  // the next piece of each kind
+  int32_t next[3] = {0, (int32_t)kinds[0], (int32_t)(kinds[0] + kinds[1])}, ws_row = 0;
   int cta = -1;
   auto open = [&](int c) {  // empty ranges from here on
     while (cta < c) {
       ++cta;
       ctas[cta].dual0 = ctas[cta].dual1 = next[0];
       ctas[cta].single0 = ctas[cta].single1 = ctas[cta].single2 = next[1];
+      ctas[cta].small0 = ctas[cta].small1 = next[2];
     }
   };
   deal(L, plan->budget, plan->num_ctas, [&](int c, const Cut& k, int stream) {
     open(c);
-    const int32_t at = next[stream >= 0]++;
-    if (stream < 0) ctas[c].dual1 = at + 1;
-    if (stream == 0) ctas[c].single1 = at + 1;
-    if (stream >= 0) ctas[c].single2 = at + 1;
+    const int kind = shared_kind(k.rows);
+    const int32_t at = next[kind]++;
+    if (kind == 0) ctas[c].dual1 = at + 1;
+    if (kind == 1 && stream == 0) ctas[c].single1 = at + 1;
+    if (kind == 1) ctas[c].single2 = at + 1;
+    if (kind == 2) ctas[c].small1 = at + 1;
     SharedPiece p{};
     p.q_row0 = k.seg->q_row0;
     p.q_pos0 = k.seg->q_pos0;

@@ -2,7 +2,7 @@
 //
 // Table (int32 words, see cp_shared_plan):
 //   ctas       [num_ctas]         SharedCta: the pieces of each thread block
-//   pieces     [num_pieces]       SharedPiece, those of dual units first
+//   pieces     [num_pieces]       SharedPiece, by the kind of their units
 //   units      [num_units]        SharedUnit: the partial rows of a unit
 //   row_first  [num_q_rows + 1]   entries of query row n (padded to an even word)
 //   entries    [num_entries][2]   (unit of the row's segment's first tile and KV head 0,
@@ -31,20 +31,25 @@ struct SharedPiece {
 };
 static_assert(sizeof(SharedPiece) == 48, "three 16-byte words");
 
-// The pieces of one thread block.  A unit of more than kSharedTileRows rows is two
-// MMA tiles that use every KV tile (dual); both of the block's softmax warpgroups
-// (streams) work on it.  The pieces of smaller units go to one stream each: stream
-// 0 has [single0, single1), stream 1 [single1, single2), and stream 0 has as many
-// KV tiles as stream 1 or one more.
+// The pieces of one thread block.  Units come in three kinds, by their rows:
+//   dual    more than kSharedTileRows: two MMA tiles that use every KV tile; both of the
+//           block's softmax warpgroups (streams) work on it: [dual0, dual1);
+//   single  one MMA tile; a piece goes to one stream: stream 0 has [single0, single1),
+//           stream 1 [single1, single2), and stream 0 has as many KV tiles as stream 1
+//           or one more;
+//   small   at most kSharedSmallRows: [small0, small1), in blocks that have no others.
 struct SharedCta {
-  int32_t dual0, dual1, single0, single1, single2;
-  int32_t unused[3];
+  int32_t dual0, dual1, single0, single1, single2, small0, small1, unused;
 };
 static_assert(sizeof(SharedCta) == 32, "two 16-byte words");
 
 constexpr int kSharedTileRows = 128;  // packed rows of one MMA tile
 constexpr int kSharedTileKeys = 128;  // keys of one KV tile
+constexpr int kSharedSmallRows = 16;  // packed rows of one warp-level MMA
 __host__ __device__ constexpr bool shared_dual(int rows) { return rows > kSharedTileRows; }
+__host__ __device__ constexpr int shared_kind(int rows) {  // 0 dual, 1 single, 2 small
+  return shared_dual(rows) ? 0 : rows > kSharedSmallRows ? 1 : 2;
+}
 
 // A unit of at most 64 (32) rows and enough keys fills its MMA tile with 2 (4) copies
 // of its rows, and copy c works on the c-th half (quarter) of the keys of every KV
@@ -52,7 +57,7 @@ __host__ __device__ constexpr bool shared_dual(int rows) { return rows > kShared
 // Each copy leaves a partial result, which pays from kSharedRepKeys keys on: TODO.
 constexpr int kSharedRepKeys = 2048;
 __host__ __device__ constexpr int shared_reps(int rows, long long keys) {
-  return keys < kSharedRepKeys ? 1 : rows <= 32 ? 4 : rows <= 64 ? 2 : 1;
+  return keys < kSharedRepKeys || rows <= kSharedSmallRows ? 1 : rows <= 32 ? 4 : rows <= 64 ? 2 : 1;
 }
 
 // The partials of a unit: part j of its packed row r is workspace row ws_row + j * rows

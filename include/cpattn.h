@@ -596,7 +596,7 @@ int cp_kv_dequantize(const cp_kv_codes_t* k_cache, const cp_kv_codes_t* v_cache,
  * group at i*(Hq/Hkv) + j), and cuts the (tile, KV head, keys) work into
  * num_ctas shares of about equal cost, each a list of pieces.  It depends on the
  * lengths alone: one plan serves every layer of a step.
- *   num_ctas in [1, 4096]: thread blocks of the launch (the device's SM count).
+ *   num_ctas in [2, 4096]: thread blocks of the launch (the device's SM count).
  *   Hq % Hkv == 0; num_segs and the tiles times Hkv up to 2^22, query rows, KV
  *   rows and partial rows below 2^31 (CPATTN_ERR_TOO_LARGE).
  * cp_shared_plan_size fills *plan; cp_shared_plan then writes plan->table_ints

@@ -14,7 +14,7 @@ from context_causal_attention_cp_gb300 import _lib as L
 from oracle import shared as osh
 
 ROWS = 256  # CPATTN_SHARED_ROWS
-CTA = ("dual0", "dual1", "single0", "single1", "single2", "u0", "u1", "u2")
+CTA = ("dual0", "dual1", "single0", "single1", "single2", "small0", "small1", "u0")
 PIECE = ("q_row0", "q_pos0", "q_pos_step", "r0", "rows", "kv_head", "kv_row", "key0", "keys",
          "ws_row", "reps", "u1")
 UNIT = ("ws_row", "parts", "rows", "u0")
@@ -44,18 +44,22 @@ def check_plan(segs, N, Hq, Hkv, num_ctas):
     plan = cpa.make_shared_plan_segs(torch.tensor(segs, dtype=torch.int32).reshape(-1, 8), N, Hq,
                                      Hkv, num_ctas=num_ctas, device="cpu")
     T, g = read_table(plan), Hq // Hkv
-    # each piece belongs to one block; dual pieces first; the streams' tiles are even
-    duals = [p for p in T["pieces"] if p["rows"] > 128]
-    at = [0, len(duals)]
-    assert duals == T["pieces"][:len(duals)]
+    # each piece belongs to one block; dual pieces first, small ones last and in blocks of
+    # their own; the streams' tiles are even
+    kinds = [0 if p["rows"] > 128 else 1 if p["rows"] > 16 else 2 for p in T["pieces"]]
+    assert kinds == sorted(kinds)
+    at = [0, kinds.count(0), kinds.count(0) + kinds.count(1)]
+    ends = at[1:] + [len(kinds)]
     for c in T["ctas"]:
-        assert [c["dual0"], c["single0"]] == at
+        assert [c["dual0"], c["single0"], c["small0"]] == at
         assert c["dual0"] <= c["dual1"] and c["single0"] <= c["single1"] <= c["single2"]
-        at = [c["dual1"], c["single2"]]
+        at = [c["dual1"], c["single2"], c["small1"]]
+        assert c["small0"] == c["small1"] or (c["dual0"] == c["dual1"] and
+                                              c["single0"] == c["single2"])
         two = [tiles_of(T["pieces"][a:b]) for a, b in ((c["single0"], c["single1"]),
                                                        (c["single1"], c["single2"]))]
         assert two[0] - two[1] in (0, 1)
-    assert at == [len(duals), len(T["pieces"])]
+    assert at == ends
     # partial rows do not overlap and fill the workspace
     used = np.zeros(plan.info.ws_rows, dtype=np.int32)
     for p in T["pieces"]:
@@ -100,7 +104,7 @@ def test_plan_covers_every_key_once(seed):
     segs = cpa.shared_segments(q_lens, own, prefix, prefix_row0=rng.randint(0, 5)).tolist()
     if seed % 3 == 0 and sum(q_lens) > 2:  # a nested prefix over part of the batch
         segs.insert(1, [1, sum(q_lens) - 2, 299, 0, 7, 300, 0, -1])
-    check_plan(segs, sum(q_lens), Hq, Hkv, rng.choice([1, 3, 16, 152]))
+    check_plan(segs, sum(q_lens), Hq, Hkv, rng.choice([2, 3, 16, 152]))
 
 
 def test_plan_empty_batches():
@@ -119,11 +123,11 @@ def test_plan_shares_are_even():
     own = [rng.randint(1, 2048) for _ in range(64)]
     segs = cpa.shared_segments([1] * 64, own, 65536).tolist()
     _, T = check_plan(segs, 64, 32, 8, 152)
-    cost = []
-    for c in T["ctas"]:
-        dual, single = T["pieces"][c["dual0"]:c["dual1"]], T["pieces"][c["single0"]:c["single2"]]
-        cost.append(1.5 * tiles_of(dual) + tiles_of(single) + len(dual) + len(single))
-    assert max(cost) <= sum(cost) / 152 + 4
+    for kind in ("dual", "small"):
+        cost = [tiles_of(T["pieces"][c[kind + "0"]:c[kind + "1"]]) + c[kind + "1"] - c[kind + "0"]
+                for c in T["ctas"]]
+        cost = [x for x in cost if x]
+        assert len(cost) > 20 and sorted(cost)[-1] <= sum(cost) / len(cost) + 8
 
 
 def seg_ptr(rows):
@@ -148,6 +152,7 @@ def test_plan_refusals():
     assert size([good], Hq=6, Hkv=4) == L.ERR_INVALID_ARG
     assert size([good], Hkv=0) == L.ERR_INVALID_ARG
     assert size([good], ctas=0) == L.ERR_INVALID_ARG
+    assert size([good], ctas=1) == L.ERR_INVALID_ARG
     assert size([good], ctas=4097) == L.ERR_INVALID_ARG
     assert size([good], N=-1) == L.ERR_INVALID_ARG
     assert size([good], n=-1) == L.ERR_INVALID_ARG
