@@ -6,7 +6,11 @@
 // units works on registers: eight warps share each KV tile, 16 keys each, with warp-level
 // 16x8x16 MMAs, and each keeps its own maximum, sum and 16 x D output; at a piece's end
 // the eight are joined in shared memory.  What bounds it is HBM: a KV tile costs a warp
-// about 100 instructions (250 with codes) and the block 64 KB (33 KB).
+// about 100 instructions (250 with codes) and the block 64 KB (33 KB).  The ninth warp
+// loads: K and V tiles by TMA, the query rows and (e4m3) the scales by asynchronous
+// copies, all of them ahead across piece ends.  A warp's step issues the products of the
+// next tile's keys between the softmax and the second product of this one, so that their
+// latencies overlap.
 //
 // Fragments are loaded as they lie in memory.  Q K^T sums over d in any order, so lane
 // (key g = lane / 4, c = lane % 4) takes whole 16-byte chunks of a key row, and of a
@@ -32,15 +36,19 @@ template <int D, bool QUANT>
 struct SmallCfg {
   static constexpr int kTile = BN * D * (QUANT ? 1 : 2);
   static constexpr int kScales = QUANT ? BN * 4 : 0;  // the rows' scales, fp32
-  static constexpr int kJoin = kSmallWarps * kSharedSmallRows * D * 4;
-  static constexpr int kFixed = kJoin + kSmallWarps * kSharedSmallRows * 8 + 2 * kMaxSmallStages * 8 + 64 + 1024;
+  static constexpr int kQ = kSharedSmallRows * D * 2;  // two of them
+  static constexpr int kJoinRows = 8;                  // rows that are joined in one round
+  static constexpr int kJoin = kSmallWarps * kJoinRows * D * 4;
+  static constexpr int kMl = 2 * kSmallWarps * kJoinRows * 8;
+  static constexpr int kFixed = 2 * kQ + kJoin + kMl + (2 * kMaxSmallStages + 4) * 8 + 16 + 1024;
   static constexpr int kFit = (232448 - kFixed) / (kTile + kScales);
   static constexpr int kStages = kFit < kMaxSmallStages ? kFit : kMaxSmallStages;
   static constexpr int kScaleOff = kStages * kTile;
-  static constexpr int kJoinOff = kScaleOff + kStages * kScales;
-  static constexpr int kMlOff = kJoinOff + kJoin;  // (m, l) of each warp's rows
-  static constexpr int kBarOff = kMlOff + kSmallWarps * kSharedSmallRows * 8;
-  static constexpr int kWordOff = kBarOff + 2 * kStages * 8;
+  static constexpr int kQOff = kScaleOff + kStages * kScales;
+  static constexpr int kJoinOff = kQOff + 2 * kQ;
+  static constexpr int kMlOff = kJoinOff + kJoin;  // (m, l) of each warp's rows, two of them
+  static constexpr int kBarOff = kMlOff + kMl;
+  static constexpr int kWordOff = kBarOff + (2 * kStages + 4) * 8;
   static constexpr int kSmemBytes = kWordOff + 16 + 1024;  // + align slack
   static_assert(kSmemBytes <= 232448, "shared memory budget");
 };
@@ -100,6 +108,58 @@ __device__ __forceinline__ int join_at(int d, int r) {
   return d ^ (((d >> 5) & 3) << 2) ^ ((r & (D / 16 - 1)) << 4);
 }
 
+// One KV tile's K for a warp: the chunks of its keys (row = key0 + 8j + g), as they lie.
+template <int D, bool QUANT>
+struct SmallK {
+  static constexpr int kLoads = QUANT ? D / 64 : D / 32;
+  uint4 v[2][kLoads];
+  float2 scale[2];  // (e4m3) of the keys 8j + 2c, + 1
+  __device__ __forceinline__ void load(uint32_t tile, const float* scales, int key0, int g, int c) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int row = key0 + 8 * j + g;
+#pragma unroll
+      for (int x = 0; x < kLoads; ++x)
+        v[j][x] = QUANT ? lds128(tile + code_at<D>(row, D == 128 ? 2 * c + x : c))
+                        : lds128(tile + (x >> 1) * (BN * 128) + row * 128 +
+                                 (((2 * c + (x & 1)) ^ (row & 7)) << 4));
+      if (QUANT) scale[j] = *reinterpret_cast<const float2*>(scales + key0 + 8 * j + 2 * c);
+    }
+  }
+  // s[j]: keys 8j + 2c, + 1 of rows g, g + 8; two chains a product, for their latency
+  __device__ __forceinline__ void product(const uint32_t (&q)[D / 16][4], const float (&factor)[2],
+                                          float (&s)[2][4]) const {
+    float s2[2][4];
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int y = 0; y < 4; ++y) s[j][y] = s2[j][y] = 0.f;
+#pragma unroll
+    for (int x = 0; x < kLoads; ++x)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        if constexpr (!QUANT) {
+          mma_16816<false>(s[j], q[2 * x], v[j][x].x, v[j][x].y);
+          mma_16816<false>(s2[j], q[2 * x + 1], v[j][x].z, v[j][x].w);
+        } else {
+          const uint32_t w[4] = {v[j][x].x, v[j][x].y, v[j][x].z, v[j][x].w};
+#pragma unroll
+          for (int y = 0; y < 4; ++y)
+            mma_16816<true>(y & 1 ? s2[j] : s[j], q[4 * x + y], e4m3x2_to_f16x2(w[y]),
+                            e4m3x2_to_f16x2(w[y] >> 16));
+        }
+      }
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int hh = 0; hh < 2; ++hh) {
+        s[j][2 * hh] = (s[j][2 * hh] + s2[j][2 * hh]) * (QUANT ? factor[hh] * scale[j].x : factor[hh]);
+        s[j][2 * hh + 1] =
+            (s[j][2 * hh + 1] + s2[j][2 * hh + 1]) * (QUANT ? factor[hh] * scale[j].y : factor[hh]);
+      }
+  }
+};
+
 template <int D, bool QUANT>
 __device__ __forceinline__ void run_small(const SharedParams& p, const SharedCta& list, uint8_t* smem,
                                           const CUtensorMap* tm_k, const CUtensorMap* tm_v,
@@ -108,6 +168,8 @@ __device__ __forceinline__ void run_small(const SharedParams& p, const SharedCta
   constexpr int NS = C::kStages;
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
   uint64_t* empty = full + NS;
+  uint64_t* q_full = empty + NS;
+  uint64_t* q_empty = q_full + 2;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kWordOff);
   volatile int* issued_loads = abort_flag + 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -116,27 +178,46 @@ __device__ __forceinline__ void run_small(const SharedParams& p, const SharedCta
       mbar_init(full + i, QUANT ? 33 : 1);  // the TMA copy and each lane's scales
       mbar_init(empty + i, kSmallWarps);
     }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(q_full + i, 32);  // each lane's copies
+      mbar_init(q_empty + i, kSmallWarps);
+    }
     *abort_flag = 0;
     *issued_loads = 0;
     fence_barrier_init();
   }
   __syncthreads();
+  auto arrive_copies = [&](uint64_t* bar) {  // when this lane's copies so far have landed
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+  };
 
   if (warp >= kSmallWarps) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(SharedCfg<D, QUANT>::kRegsOther));
-    if (warp == kProducerWarp && (QUANT || lane == 0)) {
+    if (warp == kProducerWarp) {
       constexpr int kChunks = QUANT ? 1 : D / 64;      // boxes across a row
       constexpr int kLine = C::kTile / BN / kChunks;   // bytes of a box row
       int seq = 0;
       bool ok = true;
       for (int i = list.small0; i < list.small1 && ok; ++i) {
         const SharedPiece pc = load_piece(p, i);
+        const int n = i - list.small0, qb = n & 1;
+        ok = wait_warp(q_empty + qb, ((n >> 1) & 1) ^ 1, abort_flag, p.timeout_ns);
+        if (!ok) break;
+        // the query rows, 16-byte chunks swizzled over a row's length
+        for (int x = lane; x < pc.rows * (D / 8); x += 32) {
+          const int r = x / (D / 8), ch = x % (D / 8), packed = pc.r0 + r, qi = group_div(p, packed);
+          const __nv_bfloat16* src = p.q + (long long)(pc.q_row0 + qi) * p.q_row +
+                                     (long long)(pc.kv_head * p.g + packed - qi * p.g) * p.q_head + ch * 8;
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                           smem_u32(smem + C::kQOff + qb * C::kQ) + r * (D * 2) + ((ch ^ (r & 7)) << 4)),
+                       "l"(src)
+                       : "memory");
+        }
+        arrive_copies(q_full + qb);
         for (int u = 0; u < 2 * num_tiles(pc.keys); ++u, ++seq) {  // K0 V0 K1 V1 ...
           const int slot = seq % NS, t = u >> 1, row = pc.kv_row + t * BN, live = pc.keys - t * BN;
           const bool is_v = u & 1;
-          const uint32_t parity = ((seq / NS) & 1) ^ 1;
-          ok = QUANT ? wait_warp(empty + slot, parity, abort_flag, p.timeout_ns)
-                     : wait_one(empty + slot, parity, abort_flag, p.timeout_ns);
+          ok = wait_warp(empty + slot, ((seq / NS) & 1) ^ 1, abort_flag, p.timeout_ns);
           if (!ok) break;
           uint8_t* dst = smem + slot * C::kTile;
           if (lane == 0) {
@@ -151,8 +232,8 @@ __device__ __forceinline__ void run_small(const SharedParams& p, const SharedCta
                 tma_load_3d(dst + (c * BN + x * rows) * kLine, tm, full + slot, c * 64, pc.kv_head,
                             row + x * rows);
           }
+          __syncwarp();
           if constexpr (QUANT) {
-            __syncwarp();
             const float* src = (is_v ? p.vs : p.ks) + (long long)pc.kv_head * p.s_head + row + lane;
             const uint32_t at = smem_u32(smem + C::kScaleOff + slot * C::kScales) + lane * 4;
 #pragma unroll
@@ -161,12 +242,11 @@ __device__ __forceinline__ void run_small(const SharedParams& p, const SharedCta
                 asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(at + x * 128),
                              "l"(src + x * 32)
                              : "memory");
-            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(
-                             smem_u32(full + slot))
-                         : "memory");
+            arrive_copies(full + slot);
           }
         }
       }
+      asm volatile("cp.async.wait_all;" ::: "memory");
       if (lane == 0) {
         *issued_loads = seq;
         if (!ok) {
@@ -182,36 +262,43 @@ __device__ __forceinline__ void run_small(const SharedParams& p, const SharedCta
     const uint32_t smem_base = smem_u32(smem);
     constexpr int kSteps = D / 16;        // k-steps of Q K^T
     constexpr int kOut = D / 8;           // column blocks of O
-    float* const join = reinterpret_cast<float*>(smem + C::kJoinOff);
-    float2* const ml = reinterpret_cast<float2*>(smem + C::kMlOff);
+    auto scales_of = [&](int slot) {
+      return reinterpret_cast<const float*>(smem + C::kScaleOff + slot * C::kScales);
+    };
     int seq = 0;
-    bool ok = true;
+    bool ok = true, turns = true;  // turns: the last piece used a half of the join buffer
+    SharedPiece np = load_piece(p, list.small0);
     for (int i = list.small0; i < list.small1; ++i) {
-      const SharedPiece pc = load_piece(p, i);
-      // ---- queries: rows g and g + 8 ----
-      uint32_t q[kSteps][4];
-      float factor[2];
-      int seen[2];
+      const SharedPiece pc = np;
+      if (i + 1 < list.small1) np = load_piece(p, i + 1);
+      const int T = num_tiles(pc.keys), n = i - list.small0, qb = n & 1;
+      int seen[2], last_seen = 0, full_seen = pc.keys;  // keys that any, that all rows see
 #pragma unroll
       for (int hh = 0; hh < 2; ++hh) {
         const int r = g + 8 * hh;
         seen[hh] = 0;
-        factor[hh] = p.scale_log2;
-        uint4 v[D / 32];
         if (r < pc.rows) {
-          const int packed = pc.r0 + r, qi = group_div(p, packed);
-          const __nv_bfloat16* src = p.q + (long long)(pc.q_row0 + qi) * p.q_row +
-                                     (long long)(pc.kv_head * p.g + packed - qi * p.g) * p.q_head;
-          const long long pos = (long long)pc.q_pos0 + (long long)qi * pc.q_pos_step;
+          const long long pos = (long long)pc.q_pos0 + (long long)group_div(p, pc.r0 + r) * pc.q_pos_step;
           seen[hh] = (int)max(0LL, min((long long)pc.keys, pos + 1 - pc.key0));
-          // bf16: chunks 2c, 2c + 1 of each 128 bytes; e4m3: the 16-element chunks that
-          // the lane's code chunks stand for
+          last_seen = max(last_seen, seen[hh]);
+          full_seen = min(full_seen, seen[hh]);
+        }
+      }
+      last_seen = __reduce_max_sync(0xffffffffu, last_seen);
+      full_seen = __reduce_min_sync(0xffffffffu, full_seen);
+      // ---- queries: rows g and g + 8 ----
+      uint32_t q[kSteps][4];
+      float factor[2] = {p.scale_log2, p.scale_log2};
+      ok = wait_warp(q_full + qb, (n >> 1) & 1, abort_flag, p.timeout_ns);
 #pragma unroll
-          for (int x = 0; x < D / 32; ++x)
-            v[x] = __ldg(reinterpret_cast<const uint4*>(src + q_chunk<D, QUANT>(c, x)));
-        } else {
+      for (int hh = 0; hh < 2; ++hh) {
+        const int r = g + 8 * hh;
+        uint4 v[D / 32];
 #pragma unroll
-          for (int x = 0; x < D / 32; ++x) v[x] = make_uint4(0, 0, 0, 0);
+        for (int x = 0; x < D / 32; ++x) {
+          v[x] = lds128(smem_base + C::kQOff + qb * C::kQ + r * (D * 2) +
+                        (((q_chunk<D, QUANT>(c, x) >> 3) ^ (r & 7)) << 4));
+          if (r >= pc.rows) v[x] = make_uint4(0, 0, 0, 0);
         }
         if constexpr (QUANT) {
           // bf16 to f16 times 2^f with 2^f max|q| in [2^14, 2^15)
@@ -242,10 +329,8 @@ __device__ __forceinline__ void run_small(const SharedParams& p, const SharedCta
           q[2 * x + 1][hh + 2] = v[x].w;
         }
       }
-      const int seen_all = max(seen[0], seen[1]);
-      const int last_seen = __reduce_max_sync(0xffffffffu, seen_all);
-      const int first_seen = min(pc.rows > g ? seen[0] : pc.keys, pc.rows > g + 8 ? seen[1] : pc.keys);
-      const int full_seen = __reduce_min_sync(0xffffffffu, first_seen);  // keys that all rows see
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_empty + qb);
       float o[kOut][4];
 #pragma unroll
       for (int x = 0; x < kOut; ++x)
@@ -253,65 +338,58 @@ __device__ __forceinline__ void run_small(const SharedParams& p, const SharedCta
         for (int y = 0; y < 4; ++y) o[x][y] = 0.f;
       float m_run[2] = {-INFINITY, -INFINITY}, m_use[2] = {0.f, 0.f}, l_run[2] = {0.f, 0.f};
       int ev = -126;  // (e4m3) exponent of O
-      const int T = num_tiles(pc.keys);
-      for (int t = 0; t < T; ++t, seq += 2) {
-        const int ks = seq % NS, vs = (seq + 1) % NS;
-        const int at0 = t * BN + key0;           // the warp's first key
-        const bool work = at0 < last_seen;       // some row sees some of its keys
-        ok = wait_warp(full + ks, (seq / NS) & 1, abort_flag, p.timeout_ns);
+      // S of a tile; t the tile, seq_t its K tile's place
+      auto begin_s = [&](SmallK<D, QUANT>& k, int t, int seq_t) {
+        const int slot = seq_t % NS;
+        if (!wait_warp(full + slot, (seq_t / NS) & 1, abort_flag, p.timeout_ns)) return false;
+        if (t * BN + key0 < last_seen)  // (some row sees some of the warp's keys)
+          k.load(smem_base + slot * C::kTile, scales_of(slot), key0, g, c);
+        return true;
+      };
+      auto release = [&](int slot) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(empty + slot);
+      };
+      SmallK<D, QUANT> k;
+      float s[2][4];
+      ok = ok && begin_s(k, 0, seq);
+      if (ok) {
+        if (key0 < last_seen) k.product(q, factor, s);
+        release(seq % NS);
+      }
+      for (int t = 0; t < T && ok; ++t, seq += 2) {
+        const int v_slot = (seq + 1) % NS, at0 = t * BN + key0;
+        const bool work = at0 < last_seen, next = t + 1 < T, next_work = next && at0 + BN < last_seen;
+        ok = wait_warp(full + v_slot, ((seq + 1) / NS) & 1, abort_flag, p.timeout_ns);
+        if (ok && next) ok = begin_s(k, t + 1, seq + 2);
         if (!ok) break;
-        // ---- S = Q K^T: keys 8j + 2c, + 1 of rows g, g + 8 ----
-        float s[2][4];
-        if (work) {
-          float s2[2][4];
+        const uint32_t tile = smem_base + v_slot * C::kTile;
+        const int live = pc.keys - at0;  // of the warp's keys
+        // (e4m3) the lane's codes of the keys 2c, 2c + 1, 2c + 8, 2c + 9 and their scales
+        uint32_t w[4][D / 32];
+        float f[4];
+        if constexpr (QUANT) {
+          if (work) {
+            const float* sc = scales_of(v_slot) + key0;
 #pragma unroll
-          for (int j = 0; j < 2; ++j)
-#pragma unroll
-            for (int y = 0; y < 4; ++y) s[j][y] = s2[j][y] = 0.f;
-          const uint32_t tile = smem_base + ks * C::kTile;
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const int row = key0 + 8 * j + g;
-            if constexpr (!QUANT) {
-#pragma unroll
-              for (int x = 0; x < D / 32; ++x) {
-                const uint4 k = lds128(tile + (x >> 1) * (BN * 128) + row * 128 +
-                                       (((2 * c + (x & 1)) ^ (row & 7)) << 4));
-                mma_16816<false>(s[j], q[2 * x], k.x, k.y);
-                mma_16816<false>(s2[j], q[2 * x + 1], k.z, k.w);
+            for (int x = 0; x < 4; ++x) {
+              const int key = 2 * c + (x >> 1) * 8 + (x & 1), row = key0 + key;
+              f[x] = sc[key];
+              if constexpr (D == 128) {
+                const uint4 v = lds128(tile + code_at<D>(row, g));
+                w[x][0] = v.x; w[x][1] = v.y; w[x][2] = v.z; w[x][3] = v.w;
+              } else {
+                const uint2 v = lds64(tile + code_at<D>(row, g >> 1) + (g & 1) * 8);
+                w[x][0] = v.x; w[x][1] = v.y;
               }
-            } else {
+              if (key >= live) {  // rows behind the last key are zeros
+                f[x] = 0.f;
 #pragma unroll
-              for (int x = 0; x < D / 64; ++x) {
-                const uint4 k = lds128(tile + code_at<D>(row, D == 128 ? 2 * c + x : c));
-                const uint32_t w[4] = {k.x, k.y, k.z, k.w};
-#pragma unroll
-                for (int y = 0; y < 4; ++y) {
-                  const uint32_t b0 = e4m3x2_to_f16x2(w[y]), b1 = e4m3x2_to_f16x2(w[y] >> 16);
-                  if (y & 1) mma_16816<true>(s2[j], q[4 * x + y], b0, b1);
-                  else mma_16816<true>(s[j], q[4 * x + y], b0, b1);
-                }
+                for (int y = 0; y < D / 32; ++y) w[x][y] = 0u;
               }
-            }
-          }
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            float k0 = 1.f, k1 = 1.f;
-            if constexpr (QUANT) {
-              const float2 x = *reinterpret_cast<const float2*>(smem + C::kScaleOff + ks * C::kScales +
-                                                                (key0 + 8 * j + 2 * c) * 4);
-              k0 = x.x;
-              k1 = x.y;
-            }
-#pragma unroll
-            for (int hh = 0; hh < 2; ++hh) {
-              s[j][2 * hh] = (s[j][2 * hh] + s2[j][2 * hh]) * (factor[hh] * k0);
-              s[j][2 * hh + 1] = (s[j][2 * hh + 1] + s2[j][2 * hh + 1]) * (factor[hh] * k1);
             }
           }
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(empty + ks);
         // ---- softmax, base 2; the maximum moves as in softmax_tile ----
         uint32_t pa[4];
         if (work) {
@@ -353,11 +431,10 @@ __device__ __forceinline__ void run_small(const SharedParams& p, const SharedCta
               for (int y = 0; y < 4; ++y) o[x][y] *= alpha[y >> 1];
           }
         }
-        ok = wait_warp(full + vs, ((seq + 1) / NS) & 1, abort_flag, p.timeout_ns);
-        if (!ok) break;
+        // ---- the next tile's S, then O += P V ----
+        if (next_work) k.product(q, factor, s);
+        if (next) release((seq + 2) % NS);
         if (work) {
-          const uint32_t tile = smem_base + vs * C::kTile;
-          const int live = pc.keys - at0;  // of the warp's keys
           if constexpr (!QUANT) {
             // keys 2c, 2c + 1 (and + 8) of a column: rows behind the last key are zeros
             uint32_t mask[2] = {~0u, ~0u};
@@ -380,14 +457,7 @@ __device__ __forceinline__ void run_small(const SharedParams& p, const SharedCta
               mma_16816<false>(o[2 * x + 1], pa, v[2] & mask[0], v[3] & mask[1]);
             }
           } else {
-            // factors of the keys 2c, 2c + 1, 2c + 8, 2c + 9, relative to 2^ev
-            float f[4];
-            const float* sc = reinterpret_cast<const float*>(smem + C::kScaleOff + vs * C::kScales) + key0;
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              const int key = 2 * c + (x >> 1) * 8 + (x & 1);
-              f[x] = key < live ? sc[key] : 0.f;
-            }
+            // factors of the lane's keys, relative to 2^ev
             const uint32_t mx = __reduce_max_sync(
                 0xffffffffu, __float_as_uint(fmaxf(fmaxf(f[0], f[1]), fmaxf(f[2], f[3]))));
             const int e = exponent_of(__uint_as_float(mx));
@@ -401,21 +471,6 @@ __device__ __forceinline__ void run_small(const SharedParams& p, const SharedCta
             }
             const float inv = exp2_int(-ev);
             const uint32_t f0 = pack_f16x2(f[0] * inv, f[1] * inv), f1 = pack_f16x2(f[2] * inv, f[3] * inv);
-            uint32_t w[4][D / 32];  // the lane's codes of its four keys
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              const int key = 2 * c + (x >> 1) * 8 + (x & 1), row = key0 + key;
-              if constexpr (D == 128) {
-                const uint4 v = lds128(tile + code_at<D>(row, g));
-                w[x][0] = v.x; w[x][1] = v.y; w[x][2] = v.z; w[x][3] = v.w;
-              } else {
-                const uint2 v = lds64(tile + code_at<D>(row, g >> 1) + (g & 1) * 8);
-                w[x][0] = v.x; w[x][1] = v.y;
-              }
-              if (key >= live)
-#pragma unroll
-                for (int y = 0; y < D / 32; ++y) w[x][y] = 0u;
-            }
 #pragma unroll
             for (int y = 0; y < D / 32; ++y) {
 #pragma unroll
@@ -430,71 +485,79 @@ __device__ __forceinline__ void run_small(const SharedParams& p, const SharedCta
             }
           }
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(empty + vs);
+        release(v_slot);
       }
-      // ---- join the warps: O = sum_w f_w O_w / L, f_w = 2^(m_w - M), L = sum f_w l_w ----
+      // ---- join the warps: O = sum_w f_w O_w / L, f_w = 2^(m_w - M), L = sum f_w l_w,
+      // rows 0-7 and then 8-15; up to 4 rows in the halves of the buffer in turn, so that
+      // the next piece need not wait for this one's readers ----
       const float down = exp2_int(ev);
+      const bool halves = pc.rows <= C::kJoinRows / 2;
+      float* const join = reinterpret_cast<float*>(smem + C::kJoinOff + (halves && (n & 1) ? C::kJoin / 2 : 0));
+      const int stride = halves ? C::kJoinRows / 2 : C::kJoinRows;  // rows of a warp's part
+      float2* const ml = reinterpret_cast<float2*>(smem + C::kMlOff) + (n & 1) * (kSmallWarps * C::kJoinRows);
 #pragma unroll
       for (int hh = 0; hh < 2; ++hh) {
+        if (hh * C::kJoinRows >= pc.rows && hh > 0) break;
         const int r = g + 8 * hh;
         float l = l_run[hh];
         l += __shfl_xor_sync(0xffffffffu, l, 1);
         l += __shfl_xor_sync(0xffffffffu, l, 2);
+        // the buffer's last readers: only between pieces that take turns none are left
+        if (!halves || !turns || hh > 0) bar_small(false);
         if (r < pc.rows) {
-          if (c == 0) ml[warp * kSharedSmallRows + r] = make_float2(m_use[hh], l);
-          float* const dst = join + (warp * kSharedSmallRows + r) * D;
+          if (c == 0) ml[warp * C::kJoinRows + g] = make_float2(m_use[hh], l);
+          float* const dst = join + (warp * stride + g) * D;
 #pragma unroll
           for (int x = 0; x < kOut; ++x) {
             if constexpr (!QUANT) {  // columns 8x + 2c, + 1
-              *reinterpret_cast<float2*>(dst + join_at<D>(8 * x + 2 * c, r)) =
+              *reinterpret_cast<float2*>(dst + join_at<D>(8 * x + 2 * c, g)) =
                   make_float2(o[x][2 * hh], o[x][2 * hh + 1]);
-            } else if (x % 4 == 0) {  // column 8x + n of the MMAs is d = n (D / 8) + x, n = 2c, 2c + 1
+            } else if (x % 4 == 0) {  // column 8x + y of the MMAs is d = y (D / 8) + x, y = 2c, 2c + 1
 #pragma unroll
-              for (int n = 0; n < 2; ++n)
-                *reinterpret_cast<float4*>(dst + join_at<D>((2 * c + n) * (D / 8) + x, r)) =
-                    make_float4(o[x][2 * hh + n] * down, o[x + 1][2 * hh + n] * down,
-                                o[x + 2][2 * hh + n] * down, o[x + 3][2 * hh + n] * down);
+              for (int y = 0; y < 2; ++y)
+                *reinterpret_cast<float4*>(dst + join_at<D>((2 * c + y) * (D / 8) + x, g)) =
+                    make_float4(o[x][2 * hh + y] * down, o[x + 1][2 * hh + y] * down,
+                                o[x + 2][2 * hh + y] * down, o[x + 3][2 * hh + y] * down);
             }
           }
         }
-      }
-      // (a warp that gave up still comes here, so that none waits for it)
-      if (bar_small(!ok)) {
-        ok = false;
-        break;
-      }
-      for (int u = threadIdx.x; u < pc.rows * (D / 4); u += 32 * kSmallWarps) {
-        const int r = u / (D / 4), d = u % (D / 4) * 4;
-        float m[kSmallWarps], l[kSmallWarps], M = -INFINITY, L = 0.f;
+        // (a warp that gave up still comes here, so that none waits for it)
+        ok = !bar_small(!ok);
+        if (!ok) break;
+        const int rows = min(C::kJoinRows, pc.rows - hh * C::kJoinRows);
+        for (int u = threadIdx.x; u < rows * (D / 4); u += 32 * kSmallWarps) {
+          const int x = u / (D / 4), d = u % (D / 4) * 4;  // row of the round
+          float m[kSmallWarps], lw[kSmallWarps], M = -INFINITY, L = 0.f;
+          float4 part[kSmallWarps];
 #pragma unroll
-        for (int w = 0; w < kSmallWarps; ++w) {
-          const float2 x = ml[w * kSharedSmallRows + r];
-          m[w] = x.x;
-          l[w] = x.y;
-          if (l[w] != 0.f) M = fmaxf(M, m[w]);  // (m of a warp without keys means nothing)
-        }
-        if (M == -INFINITY) M = 0.f;
-        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int w = 0; w < kSmallWarps; ++w) {
-          const float f = l[w] == 0.f ? 0.f : ex2_approx(m[w] - M);
-          L += f * l[w];
-          const float4 x = *reinterpret_cast<const float4*>(join + (w * kSharedSmallRows + r) * D +
-                                                           join_at<D>(d, r));
-          if (l[w] != 0.f) {
-            sum.x = fmaf(f, x.x, sum.x);
-            sum.y = fmaf(f, x.y, sum.y);
-            sum.z = fmaf(f, x.z, sum.z);
-            sum.w = fmaf(f, x.w, sum.w);
+          for (int y = 0; y < kSmallWarps; ++y) {
+            const float2 v = ml[y * C::kJoinRows + x];
+            part[y] = *reinterpret_cast<const float4*>(join + (y * stride + x) * D + join_at<D>(d, x));
+            m[y] = v.x;
+            lw[y] = v.y;
+            if (lw[y] != 0.f) M = fmaxf(M, m[y]);  // (m of a warp without keys means nothing)
           }
+          if (M == -INFINITY) M = 0.f;
+          float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int y = 0; y < kSmallWarps; ++y) {
+            if (lw[y] == 0.f) continue;
+            const float fw = ex2_approx(m[y] - M);
+            L += fw * lw[y];
+            sum.x = fmaf(fw, part[y].x, sum.x);
+            sum.y = fmaf(fw, part[y].y, sum.y);
+            sum.z = fmaf(fw, part[y].z, sum.z);
+            sum.w = fmaf(fw, part[y].w, sum.w);
+          }
+          const float inv = L == 0.f ? 0.f : 1.f / L;
+          const long long row = (long long)pc.ws_row + hh * C::kJoinRows + x;
+          *reinterpret_cast<float4*>(p.ws_o + row * D + d) =
+              make_float4(sum.x * inv, sum.y * inv, sum.z * inv, sum.w * inv);
+          if (d == 0) p.ws_l[row] = L == 0.f ? -INFINITY : M + lg2_approx(L);
         }
-        const float inv = L == 0.f ? 0.f : 1.f / L;
-        *reinterpret_cast<float4*>(p.ws_o + ((long long)pc.ws_row + r) * D + d) =
-            make_float4(sum.x * inv, sum.y * inv, sum.z * inv, sum.w * inv);
-        if (d == 0) p.ws_l[(long long)pc.ws_row + r] = L == 0.f ? -INFINITY : M + lg2_approx(L);
       }
-      bar_small(false);
+      if (!ok) break;
+      turns = halves;
     }
     if (!ok && lane == 0) {
       set_status(p.status, CPATTN_ERR_TIMEOUT);
