@@ -376,6 +376,11 @@ __device__ __forceinline__ void softmax_tile(uint32_t s_addr, uint32_t o_addr, i
   m_use = m_new_use;
 }
 
+// Partial rows in the workspace: those of one piece (or copy) by chunks of 8 columns, so
+// that the lanes of a warp, a row each, store to one place.  Offset of column 8 c of row
+// r of `rows`, from the first row's place at D floats a row.
+__device__ __forceinline__ int partial_at(int c, int r, int rows) { return (c * rows + r) * 8; }
+
 // 32 bytes, a whole sector.
 __device__ __forceinline__ void store8(float* at, const float (&f)[8]) {
   asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(at), "f"(f[0]), "f"(f[1]),
@@ -785,17 +790,27 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
       // (a small unit's rows in the other half for stream 1: other schedulers' warps)
       return shared_dual(pc.rows) ? s * BM + trow : (trow + s * (BM / 2)) & (BM / pc.reps - 1);
     };
-    // This thread's query row of a piece to shared memory, asynchronously; q_ready()
-    // publishes it, and returns the factor of its scores.
+    // The warp's query rows of a piece to shared memory, asynchronously (D / 8 lanes to a
+    // row: a thread for each row would touch 32 lines with every instruction, 4000 cycles
+    // a piece); q_ready() publishes them, and returns the factor of this row's scores.
     auto load_q = [&](const SharedPiece& pc) {
+      constexpr int kLanes = D / 8;  // of a row
       const int r = row_of(pc);
+      const __nv_bfloat16* row = nullptr;
       if (r < pc.rows) {
         const int packed = pc.r0 + r, qi = group_div(p, packed);
-        const __nv_bfloat16* src = p.q + (long long)(pc.q_row0 + qi) * p.q_row +
-                                   (long long)(pc.kv_head * p.g + packed - qi * p.g) * p.q_head;
-#pragma unroll
-        for (int c = 0; c < D / 8; ++c)
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(q_chunk(c))),
+        row = p.q + (long long)(pc.q_row0 + qi) * p.q_row +
+              (long long)(pc.kv_head * p.g + packed - qi * p.g) * p.q_head;
+      }
+      const int c = lane % kLanes;
+      uint32_t dst = q_base + s * C::kQTile + (c >> 3) * (BM * 128) + wq * 32 * 128;
+#pragma unroll 4
+      for (int i = lane / kLanes; i < 32; i += 32 / kLanes) {
+        const __nv_bfloat16* src = reinterpret_cast<const __nv_bfloat16*>(
+            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(row), i));
+        if (src)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                           dst + i * 128 + (((c & 7) ^ (i & 7)) << 4)),
                        "l"(src + c * 8)
                        : "memory");
       }
@@ -804,6 +819,7 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
       float factor = p.scale_log2;
       asm volatile("cp.async.wait_all;" ::: "memory");
       if constexpr (QUANT) {
+        __syncwarp();  // (the row came by other lanes' copies)
         if (row_of(pc) < pc.rows) {
           // bf16 to f16 in place, times 2^f with 2^f max|q| in [2^14, 2^15)
           uint32_t mx = 0;
@@ -845,7 +861,6 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     if (pieces > 0) {
       np = piece(0);
       load_q(np);
-      factor = q_ready(np);
     }
     int step = 0;      // of the stream
     int dual_seq = 0;  // ring places of the dual tiles before this piece
@@ -867,14 +882,19 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
       }
       float m_run = -INFINITY, l_run = 0.f, m_use = 0.f;
       int ev = 0;  // exponent of O
-      for (int t = 0; t < T; ++t, ++step) {
-        ok = wait_warp(s_full + s, step & 1, abort_flag, p.timeout_ns);
-        if (!ok) break;
-        tc_fence_after();
-        // the piece's last S is done: its query tile is free for the next piece
-        if (t == T - 1 && more) load_q(np);
+      // The list's first tile is preceded by one that sees no key (and writes only P, over
+      // an S that is still to come): it brings the code in, which takes as long as three
+      // tiles (4000 cycles from L2, up to 9000 from HBM), while the queries travel.
+      for (int t = i > 0 ? 0 : -1; t < T; ++t) {
+        if (t >= 0) {
+          ok = wait_warp(s_full + s, step & 1, abort_flag, p.timeout_ns);
+          if (!ok) break;
+          tc_fence_after();
+          // the piece's last S is done: its query tile is free for the next piece
+          if (t == T - 1 && more) load_q(np);
+        }
         float sl2 = factor, o_scale = 1.f;
-        if constexpr (QUANT) {
+        if (QUANT && t >= 0) {
           // written before the K tile of this step went to the tensor core, and not
           // again before this step's P has been used
           const volatile int2* e =
@@ -885,7 +905,7 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
           ev = ev_now;
         }
         if (warp_live) {
-          const int here = seen - t * BN;  // visible keys of this tile
+          const int here = t < 0 ? 0 : seen - t * BN;  // visible keys of this tile
           if (reps == 1)
             softmax_tile<BN, D, QUANT>(s_addr, o_addr, 0, here, t > 0, o_scale, sl2, m_run, m_use, l_run);
           else if (reps == 2)
@@ -894,6 +914,11 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
           else
             softmax_tile<BN / 4, D, QUANT>(s_addr, o_addr, copy, here, t > 0, o_scale, sl2, m_run, m_use,
                                            l_run);
+        }
+        if (t < 0) {
+          tc_fence_before();
+          factor = q_ready(pc);
+          continue;
         }
         if constexpr (!QUANT) {
           // V rows behind the last key become zeros (0 * NaN is NaN, so masking P
@@ -917,6 +942,7 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
         }
         tc_fence_before();
         mbar_arrive(p_full + s);
+        ++step;
       }
       if (!ok) break;
       if (more) factor = q_ready(np);
@@ -927,8 +953,8 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
       if (warp_live) {
         const bool none = l_run == 0.f;  // (a NaN sum is not none)
         const float inv = none ? 0.f : exp2_int(ev) / l_run;
-        const long long row = (long long)pc.ws_row + copy * pc.rows + r;
-        float* dst = p.ws_o + row * D;
+        const long long row0 = (long long)pc.ws_row + copy * pc.rows;
+        float* dst = p.ws_o + row0 * D;
         constexpr int kCols = QUANT ? 64 : D;  // (register budget)
 #pragma unroll
         for (int q = 0; q < D / kCols; ++q) {
@@ -942,11 +968,11 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
               float f[8];
 #pragma unroll
               for (int x = 0; x < 8; ++x) f[x] = none ? 0.f : __uint_as_float(v[c + x]) * inv;
-              store8(dst + q * kCols + c, f);
+              store8(dst + partial_at((q * kCols + c) / 8, r, pc.rows), f);
             }
           }
         }
-        if (r < pc.rows) p.ws_l[row] = none ? -INFINITY : m_use + lg2_approx(l_run);
+        if (r < pc.rows) p.ws_l[row0 + r] = none ? -INFINITY : m_use + lg2_approx(l_run);
       }
       tc_fence_before();
     }
@@ -980,44 +1006,54 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
   }
 }
 
-// Merge of a row's partials, `ways` warps per (query row, head), each an interleaved
-// share of them.  Latency bound: a lane finds one partial each (the plan's words,
-// read before the wait for the attention kernel), so that after the wait two
-// dependent loads are left, the L of all partials and their O.
+// Merge of the partials of J heads of a query row (J = 1, 2, 4 dividing g, so that they
+// are J rows side by side of the same unit), `ways` warps for them, each an interleaved
+// share of the partials.  Bound by latency or, with many rows, by the partials' bytes:
+// the plan's words are read before the wait for the attention kernel, so that two
+// dependent loads are left after it, the L of up to 32 / J partials and their O.  A lane
+// has 4 columns of each of its chunks, all of one row (see partial_at: a chunk's J rows
+// are contiguous).
 constexpr int kMergeThreads = 256, kMergeWarps = kMergeThreads / 32;
-constexpr int kMergeLoads = 8;  // partials of a warp whose O loads are in flight together
-
-template <int E>
-struct MergeSum {  // sum_j 2^(L_j - m) (1, O_j), this lane's E columns
-  float m, w, o[E];
+template <int D, int J>
+struct MergeCfg {
+  static constexpr int kLanes = 2 * J;                                 // of a chunk's J rows
+  static constexpr int kVec = D * J / 128 > 0 ? D * J / 128 : 1;       // 16-byte loads of a partial
+  static constexpr int kLoads = 8 / kVec;  // partials of a warp whose O loads are in flight together
 };
 
-// The share `way` of `ways` of a row's partials; false (and CPATTN_ERR_RANGE) when the
-// plan's words lead out of the buffers.
-template <int D>
-__device__ __forceinline__ bool merge_share(const SharedParams& p, int n, int h, int e0, int e1,
-                                            int way, int ways, int lane, MergeSum<D / 32>& sum) {
-  constexpr int E = D / 32;
+template <int V>
+struct MergeSum {  // sum_j 2^(L_j - m) (1, O_j), this lane's row and columns
+  float m, w, o[V][4];
+};
+
+// The share `way` of `ways` of the partials of heads h0 .. h0 + J - 1; false (and
+// CPATTN_ERR_RANGE) when the plan's words lead out of the buffers.
+template <int D, int J>
+__device__ __forceinline__ bool merge_share(const SharedParams& p, int h0, int e0, int e1, int way, int ways,
+                                            int lane, MergeSum<MergeCfg<D, J>::kVec>& sum) {
+  using C = MergeCfg<D, J>;
   const unsigned all = 0xffffffffu;
-  const int kvh = h / p.g, j = h % p.g;
+  const int kvh = h0 / p.g, j0 = h0 - kvh * p.g;
+  const int mine = (lane >> 1) % J, chunk = lane / C::kLanes;  // the lane's row, first chunk
+  float m_l = -INFINITY;  // sum.m of row lane % J
   bool waited = false;
   for (int eb = e0; eb < e1; eb += 32) {
     // lane e: the partials of entry eb + e
     SharedUnit un{0, 0, 1, 0};
+    int at = 0;
     bool ok = true;
     if (eb + lane < e1) {
       const int2 en = __ldg(reinterpret_cast<const int2*>(p.table + p.entries) + eb + lane);
-      const long long packed = (long long)en.y * p.g + j;
+      const long long packed = (long long)en.y * p.g + j0;
       const long long unit = en.x + packed / kRows * p.Hkv + kvh;
       ok = en.x >= 0 && en.y >= 0 && unit < p.num_units;
       if (ok) {
         const int4 w = __ldg(reinterpret_cast<const int4*>(p.table + p.units) + unit);
         un = SharedUnit{w.x, w.y, w.z, w.w};
-        const int at = (int)(packed % kRows);
+        at = (int)(packed % kRows);
         ok = un.ws_row >= 0 && un.parts >= 0 &&
-             (un.parts == 0 || (at < un.rows && un.rows <= kRows &&
+             (un.parts == 0 || (at + J <= un.rows && un.rows <= kRows &&
                                 un.ws_row + (long long)un.parts * un.rows <= p.ws_rows));
-        un.ws_row += at;
       }
     }
     if (!__all_sync(all, ok)) return false;
@@ -1028,64 +1064,71 @@ __device__ __forceinline__ bool merge_share(const SharedParams& p, int n, int h,
       if (lane >= o) upto += x;
     }
     const int total = __shfl_sync(all, upto, 31), entries = min(32, e1 - eb);
-    for (int b = way; b < total; b += 32 * ways) {
-      // lane l: partial b + l * ways
-      const int mine = b + lane * ways;
-      long long row = 0;
+    for (int b = way; b < total; b += 32 / J * ways) {
+      // lane l: row l % J of partial b + (l / J) * ways
+      const int part = b + lane / J * ways;
+      long long first = 0;  // workspace row of the partial's first
+      int rows = 1, row = 0;
       for (int e = 0; e < entries; ++e) {
         const int end = __shfl_sync(all, upto, e), cnt = __shfl_sync(all, un.parts, e);
-        const int first = __shfl_sync(all, un.ws_row, e), stride = __shfl_sync(all, un.rows, e);
-        if (mine >= end - cnt && mine < end) row = first + (long long)(mine - (end - cnt)) * stride;
+        const int ws_row = __shfl_sync(all, un.ws_row, e), r = __shfl_sync(all, un.rows, e);
+        const int a = __shfl_sync(all, at, e);
+        if (part >= end - cnt && part < end) {
+          first = ws_row + (long long)(part - (end - cnt)) * r;
+          rows = r;
+          row = a;
+        }
       }
       if (!waited) grid_dep_wait();  // the attention kernel before this one wrote the partials
       waited = true;
-      const int cnt = min(32, (total - b + ways - 1) / ways);
-      const float l = mine < total ? __ldcg(p.ws_l + row) : -INFINITY;
-      float4 x[kMergeLoads];  // (two columns of each in x, y at D = 64)
+      const int cnt = min(32 / J, (total - b + ways - 1) / ways);
+      const float l = part < total ? __ldcg(p.ws_l + first + row + lane % J) : -INFINITY;
+      float4 x[C::kLoads][C::kVec];
       auto load = [&](int i0) {
 #pragma unroll
-        for (int i = 0; i < kMergeLoads; ++i) {
-          const long long r = __shfl_sync(all, row, (i0 + i) & 31);
-          x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (i0 + i < cnt) {
-            const float* src = p.ws_o + r * D + lane * E;
-            if constexpr (E == 4) {
-              x[i] = __ldcg(reinterpret_cast<const float4*>(src));
-            } else {
-              const float2 f = __ldcg(reinterpret_cast<const float2*>(src));
-              x[i].x = f.x;
-              x[i].y = f.y;
-            }
+        for (int i = 0; i < C::kLoads; ++i) {
+          const int from = (i0 + i) * J & 31;
+          const float* src = p.ws_o + __shfl_sync(all, first, from) * D;
+          const int r = __shfl_sync(all, rows, from), r0 = __shfl_sync(all, row, from);
+#pragma unroll
+          for (int v = 0; v < C::kVec; ++v) {
+            const int c = v * (32 / C::kLanes) + chunk;
+            x[i][v] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (i0 + i < cnt && c < D / 8)
+              x[i][v] = __ldcg(reinterpret_cast<const float4*>(src + partial_at(c, r0 + mine, r)) + (lane & 1));
           }
         }
       };
       load(0);
       float mx = l;
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(all, mx, o));
-      const float mn = fmaxf(sum.m, mx), use = mn == -INFINITY ? 0.f : mn;
+      for (int o = 16; o >= J; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(all, mx, o));
+      const float mn = fmaxf(m_l, mx), use = mn == -INFINITY ? 0.f : mn;
       const float w = exp2f(l - use);  // (a NaN partial stays one)
       float ws = w;
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) ws += __shfl_xor_sync(all, ws, o);
-      const float old = exp2f(sum.m - use);
-      sum.w = sum.w * old + ws;
+      for (int o = 16; o >= J; o >>= 1) ws += __shfl_xor_sync(all, ws, o);
+      const float old = __shfl_sync(all, exp2f(m_l - use), mine);
+      m_l = mn;
+      sum.w = sum.w * old + __shfl_sync(all, ws, mine);
 #pragma unroll
-      for (int c = 0; c < E; ++c) sum.o[c] *= old;
-      sum.m = mn;
-      for (int i0 = 0; i0 < cnt; i0 += kMergeLoads) {
+      for (int v = 0; v < C::kVec; ++v)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) sum.o[v][c] *= old;
+      sum.m = __shfl_sync(all, mn, mine);
+      for (int i0 = 0; i0 < cnt; i0 += C::kLoads) {
         if (i0 > 0) load(i0);
 #pragma unroll
-        for (int i = 0; i < kMergeLoads; ++i) {
-          const float wi = __shfl_sync(all, w, (i0 + i) & 31);
-          if (i0 + i < cnt) {
-            sum.o[0] = fmaf(wi, x[i].x, sum.o[0]);
-            sum.o[1] = fmaf(wi, x[i].y, sum.o[1]);
-            if constexpr (E == 4) {
-              sum.o[2] = fmaf(wi, x[i].z, sum.o[2]);
-              sum.o[3] = fmaf(wi, x[i].w, sum.o[3]);
+        for (int i = 0; i < C::kLoads; ++i) {
+          const float wi = __shfl_sync(all, w, ((i0 + i) * J & 31) + mine);
+          if (i0 + i < cnt)
+#pragma unroll
+            for (int v = 0; v < C::kVec; ++v) {
+              sum.o[v][0] = fmaf(wi, x[i][v].x, sum.o[v][0]);
+              sum.o[v][1] = fmaf(wi, x[i][v].y, sum.o[v][1]);
+              sum.o[v][2] = fmaf(wi, x[i][v].z, sum.o[v][2]);
+              sum.o[v][3] = fmaf(wi, x[i][v].w, sum.o[v][3]);
             }
-          }
         }
       }
     }
@@ -1093,24 +1136,30 @@ __device__ __forceinline__ bool merge_share(const SharedParams& p, int n, int h,
   return true;
 }
 
-template <int D>
+template <int D, int J>
 __global__ void __launch_bounds__(kMergeThreads) shared_merge_kernel(const SharedParams p, int ways) {
-  constexpr int E = D / 32;  // columns of a lane
-  __shared__ MergeSum<E> parts[kMergeWarps][32];
+  using C = MergeCfg<D, J>;
+  constexpr int V = C::kVec;
+  __shared__ MergeSum<V> parts[kMergeWarps][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, way = warp % ways;
   const long long u = (long long)blockIdx.x * (kMergeWarps / ways) + warp / ways;
-  MergeSum<E> sum;
+  const int groups = p.Hq / J;  // of heads
+  int n = 0, h0 = 0;
+  MergeSum<V> sum;
   sum.m = -INFINITY;
   sum.w = 0.f;
 #pragma unroll
-  for (int c = 0; c < E; ++c) sum.o[c] = 0.f;
+  for (int v = 0; v < V; ++v)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) sum.o[v][c] = 0.f;
   bool write = false;
-  if (u < (long long)p.num_q_rows * p.Hq) {
-    const int n = (int)(u / p.Hq), h = (int)(u % p.Hq);
+  if (u < (long long)p.num_q_rows * groups) {
+    n = (int)(u / groups);
+    h0 = (int)(u - (long long)n * groups) * J;
     const int e0 = __ldg(p.table + p.row_first + n), e1 = __ldg(p.table + p.row_first + n + 1);
     if (e0 != e1) {  // (a row of no segment is left as it is)
       write = e0 >= 0 && e1 > e0 && e1 <= p.num_entries &&
-              merge_share<D>(p, n, h, e0, e1, way, ways, lane, sum);
+              merge_share<D, J>(p, h0, e0, e1, way, ways, lane, sum);
       if (!write && lane == 0) set_status(p.status, CPATTN_ERR_RANGE);
     }
   }
@@ -1120,35 +1169,54 @@ __global__ void __launch_bounds__(kMergeThreads) shared_merge_kernel(const Share
     __syncthreads();
     if (way > 0) return;
     for (int x = 1; x < ways; ++x) {
-      const MergeSum<E> other = parts[warp + x][lane];
+      const MergeSum<V>& other = parts[warp + x][lane];
       const float mn = fmaxf(sum.m, other.m), use = mn == -INFINITY ? 0.f : mn;
       const float a = exp2f(sum.m - use), b = exp2f(other.m - use);
       sum.w = sum.w * a + other.w * b;
 #pragma unroll
-      for (int c = 0; c < E; ++c) sum.o[c] = sum.o[c] * a + other.o[c] * b;
+      for (int v = 0; v < V; ++v)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) sum.o[v][c] = sum.o[v][c] * a + other.o[v][c] * b;
       sum.m = mn;
     }
   }
   if (!write) return;
   const float inv = sum.w == 0.f ? 0.f : 1.f / sum.w;
+  const long long row = (long long)n * p.Hq + h0 + (lane >> 1) % J;
 #pragma unroll
-  for (int c = 0; c < E; ++c) sum.o[c] *= inv;
-  const long long out = u * D + lane * E;
-  if (p.o_f32) {
-    float* o = static_cast<float*>(p.o) + out;
-    if constexpr (E == 4)
-      *reinterpret_cast<float4*>(o) = make_float4(sum.o[0], sum.o[1], sum.o[2], sum.o[3]);
+  for (int v = 0; v < V; ++v) {
+    const int c = v * (32 / C::kLanes) + lane / C::kLanes;
+    if (c >= D / 8) break;
+    const long long out = row * D + c * 8 + (lane & 1) * 4;
+    const float4 f = make_float4(sum.o[v][0] * inv, sum.o[v][1] * inv, sum.o[v][2] * inv, sum.o[v][3] * inv);
+    if (p.o_f32)
+      *reinterpret_cast<float4*>(static_cast<float*>(p.o) + out) = f;
     else
-      *reinterpret_cast<float2*>(o) = make_float2(sum.o[0], sum.o[1]);
-  } else {
-    __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.o) + out;
-    if constexpr (E == 4)
-      *reinterpret_cast<uint2*>(o) =
-          make_uint2(pack_bf16x2(sum.o[0], sum.o[1]), pack_bf16x2(sum.o[2], sum.o[3]));
-    else
-      *reinterpret_cast<uint32_t*>(o) = pack_bf16x2(sum.o[0], sum.o[1]);
+      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + out) =
+          make_uint2(pack_bf16x2(f.x, f.y), pack_bf16x2(f.z, f.w));
   }
-  if (lane == 0) p.lse[u] = sum.w == 0.f ? -INFINITY : (sum.m + log2f(sum.w)) * kLn2;
+  if (lane < 2 * J && (lane & 1) == 0)
+    p.lse[row] = sum.w == 0.f ? -INFINITY : (sum.m + log2f(sum.w)) * kLn2;
+}
+
+// Warps for a row's J heads: enough that a warp's partials are loaded in one go (the
+// average is ws_rows / rows), e.g. 152 partials a row at one token on a 256K prefix.
+template <int D, int J>
+int launch_merge(const SharedParams& p, cudaStream_t stream) {
+  const long long rows = (long long)p.num_q_rows * p.Hq;
+  int ways = 1;
+  while (ways < kMergeWarps && p.ws_rows > rows * ways * MergeCfg<D, J>::kLoads) ways *= 2;
+  const long long blocks = (rows / J * ways + kMergeWarps - 1) / kMergeWarps;
+  if (blocks > 0x7fffffffLL) return CPATTN_ERR_TOO_LARGE;
+  const cudaError_t e = launch_kernel(shared_merge_kernel<D, J>, (unsigned)blocks, kMergeThreads, 0, stream,
+                                      true, p, ways);
+  return e == cudaSuccess ? CPATTN_OK : CPATTN_ERR_CUDA;
+}
+template <int D>
+int launch_merge(const SharedParams& p, cudaStream_t stream) {
+  return p.g % 4 == 0   ? launch_merge<D, 4>(p, stream)
+         : p.g % 2 == 0 ? launch_merge<D, 2>(p, stream)
+                        : launch_merge<D, 1>(p, stream);
 }
 
 // 3-D map of a code buffer (cols, heads, rows) with a D-column x 1-head box, rows
@@ -1285,14 +1353,5 @@ extern "C" int cp_attn_shared(const cp_shared_plan_t* plan, const int32_t* table
                                     : launch_shared<64, false>(m, p, n, stream));
     if (r != CPATTN_OK) return r;
   }
-  // Warps per row: enough that a warp's partials are loaded in one go (the average is
-  // ws_rows / rows), e.g. 152 partials a row at one token on a 256K prefix.
-  const long long rows = (long long)plan->num_q_rows * plan->Hq;
-  int ways = 1;
-  while (ways < kMergeWarps && plan->ws_rows > rows * ways * kMergeLoads) ways *= 2;
-  const long long blocks = (rows * ways + kMergeWarps - 1) / kMergeWarps;
-  if (blocks > 0x7fffffffLL) return CPATTN_ERR_TOO_LARGE;
-  const cudaError_t e = launch_kernel(d == 128 ? shared_merge_kernel<128> : shared_merge_kernel<64>,
-                                      (unsigned)blocks, kMergeThreads, 0, stream, true, p, ways);
-  return e == cudaSuccess ? CPATTN_OK : CPATTN_ERR_CUDA;
+  return d == 128 ? launch_merge<128>(p, stream) : launch_merge<64>(p, stream);
 }

@@ -550,10 +550,11 @@ __device__ __forceinline__ void run_small(const SharedParams& p, const SharedCta
             sum.w = fmaf(fw, part[y].w, sum.w);
           }
           const float inv = L == 0.f ? 0.f : 1.f / L;
-          const long long row = (long long)pc.ws_row + hh * C::kJoinRows + x;
-          *reinterpret_cast<float4*>(p.ws_o + row * D + d) =
+          const int row = hh * C::kJoinRows + x;
+          *reinterpret_cast<float4*>(p.ws_o + (long long)pc.ws_row * D + partial_at(d >> 3, row, pc.rows) +
+                                     (d & 4)) =
               make_float4(sum.x * inv, sum.y * inv, sum.z * inv, sum.w * inv);
-          if (d == 0) p.ws_l[row] = L == 0.f ? -INFINITY : M + lg2_approx(L);
+          if (d == 0) p.ws_l[(long long)pc.ws_row + row] = L == 0.f ? -INFINITY : M + lg2_approx(L);
         }
       }
       if (!ok) break;
