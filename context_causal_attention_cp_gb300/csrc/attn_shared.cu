@@ -857,7 +857,7 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
       return load_piece(p, i < duals ? list.dual0 + i : single0 + i - duals);
     };
     SharedPiece np{};
-    float factor = 0.f;
+    float factor = p.scale_log2;
     if (pieces > 0) {
       np = piece(0);
       load_q(np);
