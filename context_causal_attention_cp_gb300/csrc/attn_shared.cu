@@ -861,6 +861,7 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     if (pieces > 0) {
       np = piece(0);
       load_q(np);
+      factor = q_ready(np);
     }
     int step = 0;      // of the stream
     int dual_seq = 0;  // ring places of the dual tiles before this piece
@@ -885,8 +886,8 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
       // The list's first tile is preceded by one that sees no key (and writes only P, over
       // an S that is still to come): it brings the code in, which takes as long as three
       // tiles (4000 cycles from L2, up to 9000 from HBM), while the queries travel.
-      for (int t = i > 0 ? 0 : -1; t < T; ++t) {
-        if (t >= 0) {
+      for (int t = 0; t < T; ++t) {
+        {
           ok = wait_warp(s_full + s, step & 1, abort_flag, p.timeout_ns);
           if (!ok) break;
           tc_fence_after();
@@ -894,7 +895,7 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
           if (t == T - 1 && more) load_q(np);
         }
         float sl2 = factor, o_scale = 1.f;
-        if (QUANT && t >= 0) {
+        if constexpr (QUANT) {
           // written before the K tile of this step went to the tensor core, and not
           // again before this step's P has been used
           const volatile int2* e =
@@ -905,7 +906,7 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
           ev = ev_now;
         }
         if (warp_live) {
-          const int here = t < 0 ? 0 : seen - t * BN;  // visible keys of this tile
+          const int here = seen - t * BN;  // visible keys of this tile
           if (reps == 1)
             softmax_tile<BN, D, QUANT>(s_addr, o_addr, 0, here, t > 0, o_scale, sl2, m_run, m_use, l_run);
           else if (reps == 2)
@@ -914,11 +915,6 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
           else
             softmax_tile<BN / 4, D, QUANT>(s_addr, o_addr, copy, here, t > 0, o_scale, sl2, m_run, m_use,
                                            l_run);
-        }
-        if (t < 0) {
-          tc_fence_before();
-          factor = q_ready(pc);
-          continue;
         }
         if constexpr (!QUANT) {
           // V rows behind the last key become zeros (0 * NaN is NaN, so masking P

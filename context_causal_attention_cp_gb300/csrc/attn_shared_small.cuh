@@ -3,22 +3,23 @@
 //
 // A 128-row MMA tile would be nearly empty, and the trips through tensor memory (S out,
 // P in, O out) take longer than a KV tile's way from HBM.  So a block that has small
-// units works on registers: eight warps share each KV tile, 16 keys each, with warp-level
-// 16x8x16 MMAs, and each keeps its own maximum, sum and 16 x D output; at a piece's end
-// the eight are joined in shared memory.  What bounds it is HBM: a KV tile costs a warp
-// about 100 instructions (250 with codes) and the block 64 KB (33 KB).  The ninth warp
-// loads: K and V tiles by TMA, the query rows and (e4m3) the scales by asynchronous
-// copies, all of them ahead across piece ends.  A warp's step issues the products of the
-// next tile's keys between the softmax and the second product of this one, so that their
-// latencies overlap.
+// units works on registers, with warp-level 16x8x16 MMAs that have the keys (and then
+// the columns of V) as their 16 rows and the queries as their 8 columns:
+//     S^T = K Q^T,   O^T += V^T P^T.
+// Eight warps share each KV tile, 16 keys each, and each keeps its own maximum, sum and
+// output; at a piece's end the eight are joined in shared memory.  The ninth warp loads:
+// K and V tiles by TMA, the query rows and (e4m3) the scales by asynchronous copies, all
+// of them ahead across piece ends.  A warp's step issues the products of the next tile's
+// keys between the softmax and the second product of this one.
 //
-// Fragments are loaded as they lie in memory.  Q K^T sums over d in any order, so lane
-// (key g = lane / 4, c = lane % 4) takes whole 16-byte chunks of a key row, and of a
-// query row the same ones: a chunk's elements 4x .. 4x+3 are its share of one k-step.
+// Fragments are loaded as they lie in memory.  K Q^T sums over d in any order, so lane
+// (g = lane / 4, c = lane % 4) takes whole 16-byte chunks of key rows g and g + 8 and of
+// query row g the same ones: a chunk's elements 4x .. 4x+3 are its share of one k-step.
 // The chunks 2c and 2c + 1 of each 128 bytes meet no bank conflict under the 128-byte
-// swizzle.  V of a bf16 tile goes through the transposing matrix load.  V codes: lane
-// (d group g, c) reads 16 codes of each of its keys 2c, 2c+1, 2c+8, 2c+9, and joins two
-// rows' bytes into a pair for each d, so column 8j + g of the MMAs' output is d = 16g + j.
+// swizzle.  V of a bf16 tile goes through the transposing matrix load.  V codes: the lane
+// reads the g-th eighth of the columns of its keys 2c, 2c+1, 2c+8, 2c+9 and joins two
+// rows' bytes into a pair for each column, so rows g and g + 8 of product x are columns
+// g D/8 + 2x and + 1.
 #pragma once
 #include <cstdint>
 
@@ -29,17 +30,16 @@ namespace cpattn {
 namespace {
 
 constexpr int kSmallWarps = 8, kSmallKeys = BN / kSmallWarps;  // keys of a warp in a KV tile
-static_assert(kSmallKeys == 16, "one MMA k-step");
+static_assert(kSmallKeys == 16 && kSharedSmallRows == 8, "an MMA's rows (and one k-step), and its columns");
 constexpr int kMaxSmallStages = 12;
 
 template <int D, bool QUANT>
 struct SmallCfg {
   static constexpr int kTile = BN * D * (QUANT ? 1 : 2);
-  static constexpr int kScales = QUANT ? BN * 4 : 0;  // the rows' scales, fp32
+  static constexpr int kScales = QUANT ? BN * 4 : 0;   // the rows' scales, fp32
   static constexpr int kQ = kSharedSmallRows * D * 2;  // two of them
-  static constexpr int kJoinRows = 8;                  // rows that are joined in one round
-  static constexpr int kJoin = kSmallWarps * kJoinRows * D * 4;
-  static constexpr int kMl = 2 * kSmallWarps * kJoinRows * 8;
+  static constexpr int kJoin = kSmallWarps * kSharedSmallRows * D * 4;
+  static constexpr int kMl = 2 * kSmallWarps * kSharedSmallRows * 8;
   static constexpr int kFixed = 2 * kQ + kJoin + kMl + (2 * kMaxSmallStages + 4) * 8 + 16 + 1024;
   static constexpr int kFit = (232448 - kFixed) / (kTile + kScales);
   static constexpr int kStages = kFit < kMaxSmallStages ? kFit : kMaxSmallStages;
@@ -54,17 +54,18 @@ struct SmallCfg {
 };
 
 template <bool F16>
-__device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                          uint32_t a3, uint32_t b0, uint32_t b1) {
   if constexpr (F16)
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
         "{%8, %9}, {%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
   else
     asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
         "{%8, %9}, {%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ uint4 lds128(uint32_t at) {
   uint4 v;
@@ -77,10 +78,20 @@ __device__ __forceinline__ uint2 lds64(uint32_t at) {
   asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at));
   return v;
 }
+__device__ __forceinline__ float lds_f32(uint32_t at) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(at));
+  return v;
+}
 __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t c) {  // the low half
   uint32_t h;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)c));
   return h;
+}
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t v) {  // 16-bit elements
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
 }
 
 // The 256 threads of the eight warps; true when any of them says so.
@@ -102,63 +113,366 @@ __device__ __forceinline__ int q_chunk(int c, int x) {
   if (QUANT) return (D == 128 ? 2 * c + (x >> 1) : c) * 16 + (x & 1) * 8;
   return (x >> 1) * 64 + (2 * c + (x & 1)) * 8;
 }
-// Place of column d of row r in a warp's part of the join buffer (bank swizzle).
-template <int D>
+// Place of column d of row r of a warp's part of the join buffer (bank swizzle: a store's
+// lanes have 8 columns, or 8 groups of four, of the rows 2 c + e).
+template <bool QUANT>
 __device__ __forceinline__ int join_at(int d, int r) {
-  return d ^ (((d >> 5) & 3) << 2) ^ ((r & (D / 16 - 1)) << 4);
+  return d ^ (((r >> 1) & 3) << (QUANT ? 2 : 3));
 }
 
-// One KV tile's K for a warp: the chunks of its keys (row = key0 + 8j + g), as they lie.
+// What a warp needs to work on the pieces.
+template <int D, bool QUANT>
+struct SmallWarp {
+  uint32_t base;  // shared memory
+  uint8_t* mem;
+  uint64_t *full, *empty, *q_full, *q_empty;
+  const volatile int* abort;
+  int warp, g, c, lane;
+  __device__ __forceinline__ void release(uint64_t* bar) const {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
+  }
+  __device__ __forceinline__ uint32_t scale_at(int slot, int row) const {
+    using C = SmallCfg<D, QUANT>;
+    return base + C::kScaleOff + slot * C::kScales + row * 4;
+  }
+};
+
+// K of a warp's 16 keys: chunks of rows g and g + 8, as they lie.
 template <int D, bool QUANT>
 struct SmallK {
   static constexpr int kLoads = QUANT ? D / 64 : D / 32;
   uint4 v[2][kLoads];
-  float2 scale[2];  // (e4m3) of the keys 8j + 2c, + 1
-  __device__ __forceinline__ void load(uint32_t tile, const float* scales, int key0, int g, int c) {
+  float scale[2];
+  __device__ __forceinline__ void load(const SmallWarp<D, QUANT>& w, int slot) {
+    const uint32_t tile = w.base + slot * SmallCfg<D, QUANT>::kTile;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      const int row = key0 + 8 * j + g;
+      const int row = w.warp * kSmallKeys + 8 * j + w.g;
 #pragma unroll
       for (int x = 0; x < kLoads; ++x)
-        v[j][x] = QUANT ? lds128(tile + code_at<D>(row, D == 128 ? 2 * c + x : c))
+        v[j][x] = QUANT ? lds128(tile + code_at<D>(row, D == 128 ? 2 * w.c + x : w.c))
                         : lds128(tile + (x >> 1) * (BN * 128) + row * 128 +
-                                 (((2 * c + (x & 1)) ^ (row & 7)) << 4));
-      if (QUANT) scale[j] = *reinterpret_cast<const float2*>(scales + key0 + 8 * j + 2 * c);
+                                 (((2 * w.c + (x & 1)) ^ (row & 7)) << 4));
+      scale[j] = QUANT ? lds_f32(w.scale_at(slot, row)) : 1.f;
     }
   }
-  // s[j]: keys 8j + 2c, + 1 of rows g, g + 8; two chains a product, for their latency
-  __device__ __forceinline__ void product(const uint32_t (&q)[D / 16][4], const float (&factor)[2],
-                                          float (&s)[2][4]) const {
-    float s2[2][4];
+  // s: keys g (0, 1) and g + 8 (2, 3), queries 2c, 2c + 1; two chains, for their latency
+  __device__ __forceinline__ void product(const uint32_t (&q)[D / 16][2], const float (&factor)[2],
+                                          float (&s)[4]) const {
+    float s2[4];
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+    for (int y = 0; y < 4; ++y) s[y] = s2[y] = 0.f;
 #pragma unroll
-      for (int y = 0; y < 4; ++y) s[j][y] = s2[j][y] = 0.f;
+    for (int x = 0; x < kLoads; ++x) {
+      const uint32_t u0[4] = {v[0][x].x, v[0][x].y, v[0][x].z, v[0][x].w};
+      const uint32_t u1[4] = {v[1][x].x, v[1][x].y, v[1][x].z, v[1][x].w};
+      if constexpr (!QUANT) {
+        mma_16816<false>(s, u0[0], u1[0], u0[1], u1[1], q[2 * x][0], q[2 * x][1]);
+        mma_16816<false>(s2, u0[2], u1[2], u0[3], u1[3], q[2 * x + 1][0], q[2 * x + 1][1]);
+      } else {
 #pragma unroll
-    for (int x = 0; x < kLoads; ++x)
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        if constexpr (!QUANT) {
-          mma_16816<false>(s[j], q[2 * x], v[j][x].x, v[j][x].y);
-          mma_16816<false>(s2[j], q[2 * x + 1], v[j][x].z, v[j][x].w);
-        } else {
-          const uint32_t w[4] = {v[j][x].x, v[j][x].y, v[j][x].z, v[j][x].w};
-#pragma unroll
-          for (int y = 0; y < 4; ++y)
-            mma_16816<true>(y & 1 ? s2[j] : s[j], q[4 * x + y], e4m3x2_to_f16x2(w[y]),
-                            e4m3x2_to_f16x2(w[y] >> 16));
-        }
+        for (int y = 0; y < 4; ++y)
+          mma_16816<true>(y & 1 ? s2 : s, e4m3x2_to_f16x2(u0[y]), e4m3x2_to_f16x2(u1[y]),
+                          e4m3x2_to_f16x2(u0[y] >> 16), e4m3x2_to_f16x2(u1[y] >> 16), q[4 * x + y][0],
+                          q[4 * x + y][1]);
       }
+    }
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int hh = 0; hh < 2; ++hh) {
-        s[j][2 * hh] = (s[j][2 * hh] + s2[j][2 * hh]) * (QUANT ? factor[hh] * scale[j].x : factor[hh]);
-        s[j][2 * hh + 1] =
-            (s[j][2 * hh + 1] + s2[j][2 * hh + 1]) * (QUANT ? factor[hh] * scale[j].y : factor[hh]);
-      }
+    for (int y = 0; y < 4; ++y) s[y] = (s[y] + s2[y]) * (factor[y & 1] * scale[y >> 1]);
   }
 };
+
+// One piece; n its number in the list, seq the ring place of its first
+// tile; turns: the last piece used a half of the join buffer.
+template <int D, bool QUANT>
+__device__ __forceinline__ bool small_piece(const SharedParams& p, const SmallWarp<D, QUANT>& w,
+                                            const SharedPiece& pc, int n, int& seq, bool& turns) {
+  using C = SmallCfg<D, QUANT>;
+  constexpr int NS = C::kStages, kOut = D / 16;
+  const unsigned all = 0xffffffffu;
+  const int g = w.g, c = w.c, key0 = w.warp * kSmallKeys, T = num_tiles(pc.keys), qb = n & 1;
+  // keys of the piece that the rows 2c, 2c + 1 see, that any and that all rows see
+  int seen[2], last_seen = 0, full_seen = pc.keys;
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const int r = 2 * c + e;
+    seen[e] = 0;
+    if (r < pc.rows) {
+      const long long pos = (long long)pc.q_pos0 + (long long)group_div(p, pc.r0 + r) * pc.q_pos_step;
+      seen[e] = (int)max(0LL, min((long long)pc.keys, pos + 1 - pc.key0));
+      last_seen = max(last_seen, seen[e]);
+      full_seen = min(full_seen, seen[e]);
+    }
+  }
+  last_seen = __reduce_max_sync(all, last_seen);
+  full_seen = __reduce_min_sync(all, full_seen);
+  // ---- queries: row g ----
+  uint32_t q[D / 16][2];
+  float factor[2];
+  bool ok = wait_warp(w.q_full + qb, (n >> 1) & 1, w.abort, p.timeout_ns);
+  uint4 v[D / 32];
+#pragma unroll
+  for (int x = 0; x < D / 32; ++x) {
+    v[x] = lds128(w.base + C::kQOff + qb * C::kQ + g * (D * 2) +
+                  (((q_chunk<D, QUANT>(c, x) >> 3) ^ g) << 4));
+    if (g >= pc.rows) v[x] = make_uint4(0, 0, 0, 0);
+  }
+  float f_row = p.scale_log2;
+  if constexpr (QUANT) {
+    // bf16 to f16 times 2^f with 2^f max|q| in [2^14, 2^15)
+    uint32_t mx = 0;
+#pragma unroll
+    for (int x = 0; x < D / 32; ++x)
+      mx = __vmaxu2(__vmaxu2(mx, __vmaxu2(v[x].x & 0x7FFF7FFFu, v[x].y & 0x7FFF7FFFu)),
+                    __vmaxu2(v[x].z & 0x7FFF7FFFu, v[x].w & 0x7FFF7FFFu));
+    mx = max(mx & 0xFFFFu, mx >> 16);
+    mx = max(mx, __shfl_xor_sync(all, mx, 1));
+    mx = max(mx, __shfl_xor_sync(all, mx, 2));
+    const int f = min(max(14 - ((int)(mx >> 7) - 127), -126), 126);
+    const float up = exp2_int(f);
+    f_row *= exp2_int(-f);
+#pragma unroll
+    for (int x = 0; x < D / 32; ++x) {
+      uint32_t* const u = &v[x].x;
+#pragma unroll
+      for (int y = 0; y < 4; ++y)
+        u[y] = pack_f16x2(__uint_as_float(u[y] << 16) * up, __uint_as_float(u[y] & 0xFFFF0000u) * up);
+    }
+  }
+  factor[0] = __shfl_sync(all, f_row, 8 * c);      // of row 2c
+  factor[1] = __shfl_sync(all, f_row, 8 * c + 4);  // and the next
+#pragma unroll
+  for (int x = 0; x < D / 32; ++x) {
+    q[2 * x][0] = v[x].x;
+    q[2 * x][1] = v[x].y;
+    q[2 * x + 1][0] = v[x].z;
+    q[2 * x + 1][1] = v[x].w;
+  }
+  w.release(w.q_empty + qb);
+  float o[kOut][4];
+#pragma unroll
+  for (int x = 0; x < kOut; ++x)
+#pragma unroll
+    for (int y = 0; y < 4; ++y) o[x][y] = 0.f;
+  float m_run[2], m_use[2], l_run[2];
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    m_run[e] = -INFINITY;
+    m_use[e] = l_run[e] = 0.f;
+  }
+  int ev = -126;  // (e4m3) exponent of O
+  SmallK<D, QUANT> k;
+  float s[4];
+  ok = ok && wait_warp(w.full + seq % NS, (seq / NS) & 1, w.abort, p.timeout_ns);
+  if (ok) {
+    if (key0 < last_seen) {  // (some row sees some of the warp's keys)
+      k.load(w, seq % NS);
+      k.product(q, factor, s);
+    }
+    w.release(w.empty + seq % NS);
+  }
+  for (int t = 0; t < T && ok; ++t, seq += 2) {
+    const int at0 = t * BN + key0, v_slot = (seq + 1) % NS, k_slot = (seq + 2) % NS;
+    const bool work = at0 < last_seen, next = t + 1 < T, next_work = next && at0 + BN < last_seen;
+    ok = wait_warp(w.full + v_slot, ((seq + 1) / NS) & 1, w.abort, p.timeout_ns) &&
+         (!next || wait_warp(w.full + k_slot, ((seq + 2) / NS) & 1, w.abort, p.timeout_ns));
+    if (!ok) break;
+    if (next_work) k.load(w, k_slot);
+    const uint32_t tile = w.base + v_slot * C::kTile;
+    const int live = pc.keys - at0;  // of the warp's keys
+    // (e4m3) the lane's codes of the keys 2c, 2c + 1, 2c + 8, 2c + 9, and their scales
+    uint32_t u[4][D / 32];
+    float f[4];
+    if constexpr (QUANT) {
+      if (work) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const int row = key0 + 2 * c + (x >> 1) * 8 + (x & 1);
+          f[x] = lds_f32(w.scale_at(v_slot, row));
+          if constexpr (D == 128) {
+            const uint4 v = lds128(tile + code_at<D>(row, g));
+            u[x][0] = v.x; u[x][1] = v.y; u[x][2] = v.z; u[x][3] = v.w;
+          } else {
+            const uint2 v = lds64(tile + code_at<D>(row, g >> 1) + (g & 1) * 8);
+            u[x][0] = v.x; u[x][1] = v.y;
+          }
+        }
+        if (live < kSmallKeys) {  // rows behind the last key are zeros
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            if (2 * c + (x >> 1) * 8 + (x & 1) >= live) {
+              f[x] = 0.f;
+#pragma unroll
+              for (int y = 0; y < D / 32; ++y) u[x][y] = 0u;
+            }
+        }
+      }
+    }
+    // ---- softmax, base 2; the maximum moves as in softmax_tile ----
+    uint32_t pb[2];
+    if (work) {
+      if (at0 + kSmallKeys > full_seen) {
+#pragma unroll
+        for (int y = 0; y < 4; ++y)
+          if (at0 + g + (y >> 1) * 8 >= seen[y & 1]) s[y] = -INFINITY;
+      }
+      float alpha[2];
+      bool any = false;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float mx = fmaxf(s[e], s[e + 2]);
+        mx = fmaxf(mx, __shfl_xor_sync(all, mx, 4));
+        mx = fmaxf(mx, __shfl_xor_sync(all, mx, 8));
+        mx = fmaxf(mx, __shfl_xor_sync(all, mx, 16));
+        const bool move = mx > m_run[e] + kMaxSlack;
+        const float m_new = move ? mx : m_run[e];
+        const float use = m_new == -INFINITY ? 0.f : m_new;
+        alpha[e] = move ? ex2_approx(m_run[e] - use) : 1.f;
+        any = any || move;
+        m_run[e] = m_new;
+        m_use[e] = use;
+        const float a = ex2_approx(s[e] - use), z = ex2_approx(s[e + 2] - use);
+        l_run[e] = l_run[e] * alpha[e] + (a + z);
+        s[e] = a;
+        s[e + 2] = z;
+      }
+#pragma unroll
+      for (int hh = 0; hh < 2; ++hh)  // keys g, g + 8
+        // P in 16 bits, as in softmax_tile; queries by rows, keys by columns now
+        pb[hh] = transpose_8x8(QUANT ? pack_f16x2(s[2 * hh], s[2 * hh + 1])
+                                     : pack_bf16x2(s[2 * hh], s[2 * hh + 1]));
+      if (__any_sync(all, any)) {
+#pragma unroll
+        for (int x = 0; x < kOut; ++x)
+#pragma unroll
+          for (int y = 0; y < 4; ++y) o[x][y] *= alpha[y & 1];
+      }
+    }
+    // ---- the next tile's S, then O += P V ----
+    if (next_work) k.product(q, factor, s);
+    if (next) w.release(w.empty + k_slot);
+    if (work) {
+      if constexpr (!QUANT) {
+        // keys 2c, 2c + 1 (and + 8) of a column: rows behind the last key are zeros
+        uint32_t mask[2] = {~0u, ~0u};
+        if (live < kSmallKeys)
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+            mask[x] = (2 * c + 8 * x < live ? 0xFFFFu : 0u) | (2 * c + 8 * x + 1 < live ? 0xFFFF0000u : 0u);
+        // matrix x of the load: columns 8 (x & 1) of 16, keys 8 (x >> 1)
+        const int row = key0 + (w.lane & 7) + 8 * (w.lane >> 4), col = (w.lane >> 3) & 1;
+#pragma unroll
+        for (int x = 0; x < kOut; ++x) {
+          const int chunk = 2 * x + col;
+          const uint32_t at =
+              tile + (chunk >> 3) * (BN * 128) + row * 128 + (((chunk & 7) ^ (row & 7)) << 4);
+          uint32_t v[4];
+          asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                       : "r"(at));
+          mma_16816<false>(o[x], v[0] & mask[0], v[1] & mask[0], v[2] & mask[1], v[3] & mask[1], pb[0],
+                           pb[1]);
+        }
+      } else {
+        // factors of the lane's keys, relative to 2^ev
+        const int e = exponent_of(__uint_as_float(__reduce_max_sync(
+            all, __float_as_uint(fmaxf(fmaxf(f[0], f[1]), fmaxf(f[2], f[3]))))));
+        if (e > ev) {  // (the same for the warp)
+          const float down = exp2_int(max(ev - e, -126));
+#pragma unroll
+          for (int x = 0; x < kOut; ++x)
+#pragma unroll
+            for (int y = 0; y < 4; ++y) o[x][y] *= down;
+          ev = e;
+        }
+        const float inv = exp2_int(-ev);
+        const uint32_t f0 = pack_f16x2(f[0] * inv, f[1] * inv), f1 = pack_f16x2(f[2] * inv, f[3] * inv);
+#pragma unroll
+        for (int x = 0; x < kOut; ++x) {  // columns 2x, 2x + 1 of the lane's
+          const uint32_t a = __byte_perm(u[0][x >> 1], u[1][x >> 1], x & 1 ? 0x7362 : 0x5140);
+          const uint32_t z = __byte_perm(u[2][x >> 1], u[3][x >> 1], x & 1 ? 0x7362 : 0x5140);
+          const uint32_t a0 = mul_f16x2(e4m3x2_to_f16x2(a), f0), a1 = mul_f16x2(e4m3x2_to_f16x2(a >> 16), f0);
+          const uint32_t a2 = mul_f16x2(e4m3x2_to_f16x2(z), f1), a3 = mul_f16x2(e4m3x2_to_f16x2(z >> 16), f1);
+          mma_16816<true>(o[x], a0, a1, a2, a3, pb[0], pb[1]);
+        }
+      }
+    }
+    w.release(w.empty + v_slot);
+  }
+  // ---- join the warps: O = sum_w f_w O_w / L, f_w = 2^(m_w - M), L = sum f_w l_w; up to 4
+  // rows in the halves of the buffer in turn, so that the next piece need not wait for
+  // this one's readers ----
+  const float down = exp2_int(ev);
+  const bool halves = pc.rows <= kSharedSmallRows / 2;
+  float* const join = reinterpret_cast<float*>(w.mem + C::kJoinOff + (halves && (n & 1) ? C::kJoin / 2 : 0));
+  const int stride = halves ? kSharedSmallRows / 2 : kSharedSmallRows;  // rows of a warp's part
+  float2* const ml = reinterpret_cast<float2*>(w.mem + C::kMlOff) + (n & 1) * (kSmallWarps * kSharedSmallRows);
+  float l[2];
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    l[e] = l_run[e];
+    l[e] += __shfl_xor_sync(all, l[e], 4);
+    l[e] += __shfl_xor_sync(all, l[e], 8);
+    l[e] += __shfl_xor_sync(all, l[e], 16);
+  }
+  // the buffer's last readers: only between pieces that take turns none are left
+  if (!halves || !turns) bar_small(false);
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const int r = 2 * c + e;
+    if (r >= pc.rows) break;
+    if (g == 0) ml[w.warp * kSharedSmallRows + r] = make_float2(m_use[e], l[e]);
+    float* const dst = join + (w.warp * stride + r) * D;
+    if constexpr (!QUANT) {
+#pragma unroll
+      for (int x = 0; x < kOut; ++x) {
+        dst[join_at<QUANT>(16 * x + g, r)] = o[x][e];
+        dst[join_at<QUANT>(16 * x + 8 + g, r)] = o[x][e + 2];
+      }
+    } else {
+#pragma unroll
+      for (int x = 0; x < kOut; x += 2)
+        *reinterpret_cast<float4*>(dst + join_at<QUANT>(g * (D / 8) + 2 * x, r)) =
+            make_float4(o[x][e] * down, o[x][e + 2] * down, o[x + 1][e] * down,
+                        o[x + 1][e + 2] * down);
+    }
+  }
+  // (a warp that gave up still comes here, so that none waits for it)
+  ok = !bar_small(!ok);
+  if (!ok) return false;
+  for (int i = w.warp * 32 + w.lane; i < pc.rows * (D / 4); i += 32 * kSmallWarps) {
+    const int x = i / (D / 4), d = i % (D / 4) * 4;  // row, column
+    float m[kSmallWarps], lw[kSmallWarps], M = -INFINITY, L = 0.f;
+    float4 part[kSmallWarps];
+#pragma unroll
+    for (int y = 0; y < kSmallWarps; ++y) {
+      const float2 v = ml[y * kSharedSmallRows + x];
+      part[y] = *reinterpret_cast<const float4*>(join + (y * stride + x) * D + join_at<QUANT>(d, x));
+      m[y] = v.x;
+      lw[y] = v.y;
+      if (lw[y] != 0.f) M = fmaxf(M, m[y]);  // (m of a warp without keys means nothing)
+    }
+    if (M == -INFINITY) M = 0.f;
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int y = 0; y < kSmallWarps; ++y) {
+      if (lw[y] == 0.f) continue;
+      const float fw = ex2_approx(m[y] - M);
+      L += fw * lw[y];
+      sum.x = fmaf(fw, part[y].x, sum.x);
+      sum.y = fmaf(fw, part[y].y, sum.y);
+      sum.z = fmaf(fw, part[y].z, sum.z);
+      sum.w = fmaf(fw, part[y].w, sum.w);
+    }
+    const float inv = L == 0.f ? 0.f : 1.f / L;
+    *reinterpret_cast<float4*>(p.ws_o + (long long)pc.ws_row * D + partial_at(d >> 3, x, pc.rows) + (d & 4)) =
+        make_float4(sum.x * inv, sum.y * inv, sum.z * inv, sum.w * inv);
+    if (d == 0) p.ws_l[(long long)pc.ws_row + x] = L == 0.f ? -INFINITY : M + lg2_approx(L);
+  }
+  turns = halves;
+  return true;
+}
 
 template <int D, bool QUANT>
 __device__ __forceinline__ void run_small(const SharedParams& p, const SharedCta& list, uint8_t* smem,
@@ -257,308 +571,15 @@ __device__ __forceinline__ void run_small(const SharedParams& p, const SharedCta
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(SharedCfg<D, QUANT>::kRegsSoftmax));
-    const int g = lane >> 2, c = lane & 3;
-    const int key0 = warp * kSmallKeys;   // the warp's keys of a tile
-    const uint32_t smem_base = smem_u32(smem);
-    constexpr int kSteps = D / 16;        // k-steps of Q K^T
-    constexpr int kOut = D / 8;           // column blocks of O
-    auto scales_of = [&](int slot) {
-      return reinterpret_cast<const float*>(smem + C::kScaleOff + slot * C::kScales);
-    };
+    const SmallWarp<D, QUANT> w{smem_u32(smem), smem, full, empty, q_full, q_empty, abort_flag,
+                                warp, lane >> 2, lane & 3, lane};
     int seq = 0;
-    bool ok = true, turns = true;  // turns: the last piece used a half of the join buffer
+    bool ok = true, turns = true;
     SharedPiece np = load_piece(p, list.small0);
-    for (int i = list.small0; i < list.small1; ++i) {
+    for (int i = list.small0; i < list.small1 && ok; ++i) {
       const SharedPiece pc = np;
       if (i + 1 < list.small1) np = load_piece(p, i + 1);
-      const int T = num_tiles(pc.keys), n = i - list.small0, qb = n & 1;
-      int seen[2], last_seen = 0, full_seen = pc.keys;  // keys that any, that all rows see
-#pragma unroll
-      for (int hh = 0; hh < 2; ++hh) {
-        const int r = g + 8 * hh;
-        seen[hh] = 0;
-        if (r < pc.rows) {
-          const long long pos = (long long)pc.q_pos0 + (long long)group_div(p, pc.r0 + r) * pc.q_pos_step;
-          seen[hh] = (int)max(0LL, min((long long)pc.keys, pos + 1 - pc.key0));
-          last_seen = max(last_seen, seen[hh]);
-          full_seen = min(full_seen, seen[hh]);
-        }
-      }
-      last_seen = __reduce_max_sync(0xffffffffu, last_seen);
-      full_seen = __reduce_min_sync(0xffffffffu, full_seen);
-      // ---- queries: rows g and g + 8 ----
-      uint32_t q[kSteps][4];
-      float factor[2] = {p.scale_log2, p.scale_log2};
-      ok = wait_warp(q_full + qb, (n >> 1) & 1, abort_flag, p.timeout_ns);
-#pragma unroll
-      for (int hh = 0; hh < 2; ++hh) {
-        const int r = g + 8 * hh;
-        uint4 v[D / 32];
-#pragma unroll
-        for (int x = 0; x < D / 32; ++x) {
-          v[x] = lds128(smem_base + C::kQOff + qb * C::kQ + r * (D * 2) +
-                        (((q_chunk<D, QUANT>(c, x) >> 3) ^ (r & 7)) << 4));
-          if (r >= pc.rows) v[x] = make_uint4(0, 0, 0, 0);
-        }
-        if constexpr (QUANT) {
-          // bf16 to f16 times 2^f with 2^f max|q| in [2^14, 2^15)
-          uint32_t mx = 0;
-#pragma unroll
-          for (int x = 0; x < D / 32; ++x)
-            mx = __vmaxu2(__vmaxu2(mx, __vmaxu2(v[x].x & 0x7FFF7FFFu, v[x].y & 0x7FFF7FFFu)),
-                          __vmaxu2(v[x].z & 0x7FFF7FFFu, v[x].w & 0x7FFF7FFFu));
-          mx = max(mx & 0xFFFFu, mx >> 16);
-          mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-          mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-          const int f = min(max(14 - ((int)(mx >> 7) - 127), -126), 126);
-          const float up = exp2_int(f);
-          factor[hh] *= exp2_int(-f);
-#pragma unroll
-          for (int x = 0; x < D / 32; ++x) {
-            uint32_t* const w = &v[x].x;
-#pragma unroll
-            for (int y = 0; y < 4; ++y)
-              w[y] = pack_f16x2(__uint_as_float(w[y] << 16) * up, __uint_as_float(w[y] & 0xFFFF0000u) * up);
-          }
-        }
-#pragma unroll
-        for (int x = 0; x < D / 32; ++x) {
-          q[2 * x][hh] = v[x].x;
-          q[2 * x][hh + 2] = v[x].y;
-          q[2 * x + 1][hh] = v[x].z;
-          q[2 * x + 1][hh + 2] = v[x].w;
-        }
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(q_empty + qb);
-      float o[kOut][4];
-#pragma unroll
-      for (int x = 0; x < kOut; ++x)
-#pragma unroll
-        for (int y = 0; y < 4; ++y) o[x][y] = 0.f;
-      float m_run[2] = {-INFINITY, -INFINITY}, m_use[2] = {0.f, 0.f}, l_run[2] = {0.f, 0.f};
-      int ev = -126;  // (e4m3) exponent of O
-      // S of a tile; t the tile, seq_t its K tile's place
-      auto begin_s = [&](SmallK<D, QUANT>& k, int t, int seq_t) {
-        const int slot = seq_t % NS;
-        if (!wait_warp(full + slot, (seq_t / NS) & 1, abort_flag, p.timeout_ns)) return false;
-        if (t * BN + key0 < last_seen)  // (some row sees some of the warp's keys)
-          k.load(smem_base + slot * C::kTile, scales_of(slot), key0, g, c);
-        return true;
-      };
-      auto release = [&](int slot) {
-        __syncwarp();
-        if (lane == 0) mbar_arrive(empty + slot);
-      };
-      SmallK<D, QUANT> k;
-      float s[2][4];
-      ok = ok && begin_s(k, 0, seq);
-      if (ok) {
-        if (key0 < last_seen) k.product(q, factor, s);
-        release(seq % NS);
-      }
-      for (int t = 0; t < T && ok; ++t, seq += 2) {
-        const int v_slot = (seq + 1) % NS, at0 = t * BN + key0;
-        const bool work = at0 < last_seen, next = t + 1 < T, next_work = next && at0 + BN < last_seen;
-        ok = wait_warp(full + v_slot, ((seq + 1) / NS) & 1, abort_flag, p.timeout_ns);
-        if (ok && next) ok = begin_s(k, t + 1, seq + 2);
-        if (!ok) break;
-        const uint32_t tile = smem_base + v_slot * C::kTile;
-        const int live = pc.keys - at0;  // of the warp's keys
-        // (e4m3) the lane's codes of the keys 2c, 2c + 1, 2c + 8, 2c + 9 and their scales
-        uint32_t w[4][D / 32];
-        float f[4];
-        if constexpr (QUANT) {
-          if (work) {
-            const float* sc = scales_of(v_slot) + key0;
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              const int key = 2 * c + (x >> 1) * 8 + (x & 1), row = key0 + key;
-              f[x] = sc[key];
-              if constexpr (D == 128) {
-                const uint4 v = lds128(tile + code_at<D>(row, g));
-                w[x][0] = v.x; w[x][1] = v.y; w[x][2] = v.z; w[x][3] = v.w;
-              } else {
-                const uint2 v = lds64(tile + code_at<D>(row, g >> 1) + (g & 1) * 8);
-                w[x][0] = v.x; w[x][1] = v.y;
-              }
-              if (key >= live) {  // rows behind the last key are zeros
-                f[x] = 0.f;
-#pragma unroll
-                for (int y = 0; y < D / 32; ++y) w[x][y] = 0u;
-              }
-            }
-          }
-        }
-        // ---- softmax, base 2; the maximum moves as in softmax_tile ----
-        uint32_t pa[4];
-        if (work) {
-          if (at0 + kSmallKeys > full_seen) {
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-#pragma unroll
-              for (int y = 0; y < 4; ++y)
-                if (at0 + 8 * j + 2 * c + (y & 1) >= seen[y >> 1]) s[j][y] = -INFINITY;
-          }
-          float alpha[2];
-          bool any = false;
-#pragma unroll
-          for (int hh = 0; hh < 2; ++hh) {
-            float mx = fmaxf(fmaxf(s[0][2 * hh], s[0][2 * hh + 1]), fmaxf(s[1][2 * hh], s[1][2 * hh + 1]));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-            const bool move = mx > m_run[hh] + kMaxSlack;
-            const float m_new = move ? mx : m_run[hh];
-            const float use = m_new == -INFINITY ? 0.f : m_new;
-            alpha[hh] = move ? ex2_approx(m_run[hh] - use) : 1.f;
-            any = any || move;
-            m_run[hh] = m_new;
-            m_use[hh] = use;
-            float sum = 0.f;
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const float a = ex2_approx(s[j][2 * hh] - use), b = ex2_approx(s[j][2 * hh + 1] - use);
-              sum += a + b;
-              // P in 16 bits, as in softmax_tile
-              pa[2 * j + hh] = QUANT ? pack_f16x2(a, b) : pack_bf16x2(a, b);
-            }
-            l_run[hh] = l_run[hh] * alpha[hh] + sum;
-          }
-          if (__any_sync(0xffffffffu, any)) {
-#pragma unroll
-            for (int x = 0; x < kOut; ++x)
-#pragma unroll
-              for (int y = 0; y < 4; ++y) o[x][y] *= alpha[y >> 1];
-          }
-        }
-        // ---- the next tile's S, then O += P V ----
-        if (next_work) k.product(q, factor, s);
-        if (next) release((seq + 2) % NS);
-        if (work) {
-          if constexpr (!QUANT) {
-            // keys 2c, 2c + 1 (and + 8) of a column: rows behind the last key are zeros
-            uint32_t mask[2] = {~0u, ~0u};
-            if (live < kSmallKeys)
-#pragma unroll
-              for (int x = 0; x < 2; ++x)
-                mask[x] = (2 * c + 8 * x < live ? 0xFFFFu : 0u) | (2 * c + 8 * x + 1 < live ? 0xFFFF0000u : 0u);
-            // matrix x of the load: keys 8 (x & 1), columns 8 (x >> 1) of 16
-            const int row = key0 + (lane & 15);
-#pragma unroll
-            for (int x = 0; x < D / 16; ++x) {
-              const int chunk = 2 * x + (lane >> 4);
-              const uint32_t at = tile + (chunk >> 3) * (BN * 128) + row * 128 +
-                                  (((chunk & 7) ^ (row & 7)) << 4);
-              uint32_t v[4];
-              asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-                           : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
-                           : "r"(at));
-              mma_16816<false>(o[2 * x], pa, v[0] & mask[0], v[1] & mask[1]);
-              mma_16816<false>(o[2 * x + 1], pa, v[2] & mask[0], v[3] & mask[1]);
-            }
-          } else {
-            // factors of the lane's keys, relative to 2^ev
-            const uint32_t mx = __reduce_max_sync(
-                0xffffffffu, __float_as_uint(fmaxf(fmaxf(f[0], f[1]), fmaxf(f[2], f[3]))));
-            const int e = exponent_of(__uint_as_float(mx));
-            if (e > ev) {  // (the same for the warp)
-              const float down = exp2_int(max(ev - e, -126));
-#pragma unroll
-              for (int x = 0; x < kOut; ++x)
-#pragma unroll
-                for (int y = 0; y < 4; ++y) o[x][y] *= down;
-              ev = e;
-            }
-            const float inv = exp2_int(-ev);
-            const uint32_t f0 = pack_f16x2(f[0] * inv, f[1] * inv), f1 = pack_f16x2(f[2] * inv, f[3] * inv);
-#pragma unroll
-            for (int y = 0; y < D / 32; ++y) {
-#pragma unroll
-              for (int z = 0; z < 2; ++z) {  // two columns at a time
-                const uint32_t a = __byte_perm(w[0][y], w[1][y], z ? 0x7362 : 0x5140);
-                const uint32_t b = __byte_perm(w[2][y], w[3][y], z ? 0x7362 : 0x5140);
-                mma_16816<true>(o[4 * y + 2 * z], pa, mul_f16x2(e4m3x2_to_f16x2(a), f0),
-                                mul_f16x2(e4m3x2_to_f16x2(b), f1));
-                mma_16816<true>(o[4 * y + 2 * z + 1], pa, mul_f16x2(e4m3x2_to_f16x2(a >> 16), f0),
-                                mul_f16x2(e4m3x2_to_f16x2(b >> 16), f1));
-              }
-            }
-          }
-        }
-        release(v_slot);
-      }
-      // ---- join the warps: O = sum_w f_w O_w / L, f_w = 2^(m_w - M), L = sum f_w l_w,
-      // rows 0-7 and then 8-15; up to 4 rows in the halves of the buffer in turn, so that
-      // the next piece need not wait for this one's readers ----
-      const float down = exp2_int(ev);
-      const bool halves = pc.rows <= C::kJoinRows / 2;
-      float* const join = reinterpret_cast<float*>(smem + C::kJoinOff + (halves && (n & 1) ? C::kJoin / 2 : 0));
-      const int stride = halves ? C::kJoinRows / 2 : C::kJoinRows;  // rows of a warp's part
-      float2* const ml = reinterpret_cast<float2*>(smem + C::kMlOff) + (n & 1) * (kSmallWarps * C::kJoinRows);
-#pragma unroll
-      for (int hh = 0; hh < 2; ++hh) {
-        if (hh * C::kJoinRows >= pc.rows && hh > 0) break;
-        const int r = g + 8 * hh;
-        float l = l_run[hh];
-        l += __shfl_xor_sync(0xffffffffu, l, 1);
-        l += __shfl_xor_sync(0xffffffffu, l, 2);
-        // the buffer's last readers: only between pieces that take turns none are left
-        if (!halves || !turns || hh > 0) bar_small(false);
-        if (r < pc.rows) {
-          if (c == 0) ml[warp * C::kJoinRows + g] = make_float2(m_use[hh], l);
-          float* const dst = join + (warp * stride + g) * D;
-#pragma unroll
-          for (int x = 0; x < kOut; ++x) {
-            if constexpr (!QUANT) {  // columns 8x + 2c, + 1
-              *reinterpret_cast<float2*>(dst + join_at<D>(8 * x + 2 * c, g)) =
-                  make_float2(o[x][2 * hh], o[x][2 * hh + 1]);
-            } else if (x % 4 == 0) {  // column 8x + y of the MMAs is d = y (D / 8) + x, y = 2c, 2c + 1
-#pragma unroll
-              for (int y = 0; y < 2; ++y)
-                *reinterpret_cast<float4*>(dst + join_at<D>((2 * c + y) * (D / 8) + x, g)) =
-                    make_float4(o[x][2 * hh + y] * down, o[x + 1][2 * hh + y] * down,
-                                o[x + 2][2 * hh + y] * down, o[x + 3][2 * hh + y] * down);
-            }
-          }
-        }
-        // (a warp that gave up still comes here, so that none waits for it)
-        ok = !bar_small(!ok);
-        if (!ok) break;
-        const int rows = min(C::kJoinRows, pc.rows - hh * C::kJoinRows);
-        for (int u = threadIdx.x; u < rows * (D / 4); u += 32 * kSmallWarps) {
-          const int x = u / (D / 4), d = u % (D / 4) * 4;  // row of the round
-          float m[kSmallWarps], lw[kSmallWarps], M = -INFINITY, L = 0.f;
-          float4 part[kSmallWarps];
-#pragma unroll
-          for (int y = 0; y < kSmallWarps; ++y) {
-            const float2 v = ml[y * C::kJoinRows + x];
-            part[y] = *reinterpret_cast<const float4*>(join + (y * stride + x) * D + join_at<D>(d, x));
-            m[y] = v.x;
-            lw[y] = v.y;
-            if (lw[y] != 0.f) M = fmaxf(M, m[y]);  // (m of a warp without keys means nothing)
-          }
-          if (M == -INFINITY) M = 0.f;
-          float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-          for (int y = 0; y < kSmallWarps; ++y) {
-            if (lw[y] == 0.f) continue;
-            const float fw = ex2_approx(m[y] - M);
-            L += fw * lw[y];
-            sum.x = fmaf(fw, part[y].x, sum.x);
-            sum.y = fmaf(fw, part[y].y, sum.y);
-            sum.z = fmaf(fw, part[y].z, sum.z);
-            sum.w = fmaf(fw, part[y].w, sum.w);
-          }
-          const float inv = L == 0.f ? 0.f : 1.f / L;
-          const int row = hh * C::kJoinRows + x;
-          *reinterpret_cast<float4*>(p.ws_o + (long long)pc.ws_row * D + partial_at(d >> 3, row, pc.rows) +
-                                     (d & 4)) =
-              make_float4(sum.x * inv, sum.y * inv, sum.z * inv, sum.w * inv);
-          if (d == 0) p.ws_l[(long long)pc.ws_row + row] = L == 0.f ? -INFINITY : M + lg2_approx(L);
-        }
-      }
-      if (!ok) break;
-      turns = halves;
+      ok = small_piece<D, QUANT>(p, w, pc, i - list.small0, seq, turns);
     }
     if (!ok && lane == 0) {
       set_status(p.status, CPATTN_ERR_TIMEOUT);

@@ -46,7 +46,7 @@ def check_plan(segs, N, Hq, Hkv, num_ctas):
     T, g = read_table(plan), Hq // Hkv
     # each piece belongs to one block; dual pieces first, small ones last and in blocks of
     # their own; the streams' tiles are even
-    kinds = [0 if p["rows"] > 128 else 1 if p["rows"] > 16 else 2 for p in T["pieces"]]
+    kinds = [0 if p["rows"] > 128 else 1 if p["rows"] > 8 else 2 for p in T["pieces"]]
     assert kinds == sorted(kinds)
     at = [0, kinds.count(0), kinds.count(0) + kinds.count(1)]
     ends = at[1:] + [len(kinds)]
