@@ -721,6 +721,14 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
       for (int i = list.dual0; i < list.dual1; ++i) tiles += 2 * num_tiles(load_piece(p, i).keys);
       // chunk places of rows r and r + 4 of a row's 128-byte line
       const uint32_t swz[2] = {(uint32_t)((cl ^ rl) << 4), (uint32_t)((cl ^ (rl + 4)) << 4)};
+      // and of the codes of rows r and r + 4 (every eighth row is swizzled alike)
+      constexpr int kBatch = 4, kHalves = D / 64;
+      uint32_t from[2][kHalves];
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int h = 0; h < kHalves; ++h)
+          from[x][h] = code_at<D>(w * 32 + rl + 4 * x, h * 4 + (cl >> 1)) + (cl & 1) * 8;
       bool ok = true;
       for (int seq = 0; seq < tiles; ++seq) {
         const int raw = seq % C::kRawStages, slot = seq % C::kStages;
@@ -730,12 +738,11 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
         const RawNote note = raw_note[raw];
         if (w == 0 && lane == 0 && note.which < RawNote::kNoteV)
           tile_exp[note.which] = make_int2(note.ek, note.ev);
-        const uint8_t* src = smem + C::kRawOff + raw * C::kRawTile + (cl & 1) * 8;
+        const uint8_t* src = smem + C::kRawOff + raw * C::kRawTile;
         const uint16_t* mul = raw_mul + raw * BN + w * 32 + rl;
         uint8_t* dst = smem + C::kRingOff + slot * C::kTile + (w * 32 + rl) * 128;
         const int live = note.live - w * 32 - rl;
         // loads of a batch before its stores: the compiler cannot tell them apart
-        constexpr int kBatch = 4, kHalves = D / 64;
 #pragma unroll
         for (int r0 = 0; r0 < 32; r0 += 4 * kBatch) {
           uint2 v[kBatch][kHalves];
@@ -745,8 +752,7 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             m[x] = mul[r0 + 4 * x];
 #pragma unroll
             for (int h = 0; h < kHalves; ++h)
-              v[x][h] = *reinterpret_cast<const uint2*>(
-                  src + code_at<D>(w * 32 + rl + r0 + 4 * x, h * 4 + (cl >> 1)));
+              v[x][h] = *reinterpret_cast<const uint2*>(src + from[x & 1][h] + (r0 + 4 * (x & ~1)) * D);
           }
           if (live < 32) {
 #pragma unroll
@@ -1195,13 +1201,13 @@ __global__ void __launch_bounds__(kMergeThreads) shared_merge_kernel(const Share
     p.lse[row] = sum.w == 0.f ? -INFINITY : (sum.m + log2f(sum.w)) * kLn2;
 }
 
-// Warps for a row's J heads: enough that a warp's partials are loaded in one go (the
+// Warps for a row's J heads: enough that a warp loads its partials in two goes (their
 // average is ws_rows / rows), e.g. 152 partials a row at one token on a 256K prefix.
 template <int D, int J>
 int launch_merge(const SharedParams& p, cudaStream_t stream) {
   const long long rows = (long long)p.num_q_rows * p.Hq;
   int ways = 1;
-  while (ways < kMergeWarps && p.ws_rows > rows * ways * MergeCfg<D, J>::kLoads) ways *= 2;
+  while (ways < kMergeWarps && p.ws_rows > rows * ways * 2 * MergeCfg<D, J>::kLoads) ways *= 2;
   const long long blocks = (rows / J * ways + kMergeWarps - 1) / kMergeWarps;
   if (blocks > 0x7fffffffLL) return CPATTN_ERR_TOO_LARGE;
   const cudaError_t e = launch_kernel(shared_merge_kernel<D, J>, (unsigned)blocks, kMergeThreads, 0, stream,
