@@ -5,9 +5,13 @@
 // 119), scale = 2^e, code_c = e4m3(x_c 2^-e), value = code_c 2^e.  Both kernels
 // are HBM streams: a vector is read once, kept in registers between the maximum
 // and the rounding, and its codes are written once.  L = 2^k lanes share a vector,
-// 16 elements (16 bytes of codes) each and step, and a thread works on kUnroll
-// rows at once, so that their loads travel together; which row, side and head a
-// thread has is settled once, before its loop over rows.
+// 8 elements each and step, so that a load or store of a step has no gaps (16 elements
+// left every store two passes over its lines: 32768 rows read back in 45 us instead of
+// 38).  L is the smallest that leaves a lane at most four steps: with L twice or four
+// times that, the shuffles of the maximum and the walk over rows cost more (8192 rows
+// of 16 vectors of 128: 12 us, 15 and 21).  A thread works on kUnroll rows at once, so
+// that their loads travel together; which row, side and head it has is settled once,
+// before its loop over rows.
 #include <algorithm>
 #include <cstdint>
 
@@ -59,27 +63,52 @@ struct KvSide {  // one of K and V
   int dim;
 };
 
-constexpr int kChunk = 16;  // elements of a lane's step
+constexpr int kChunk = 8;  // elements of a lane's step: 16 bytes of bf16, 8 of codes
 
-// 16 consecutive elements, as they lie in memory.
+// 8 consecutive elements, as they lie in memory.
 template <bool F32>
-struct Raw16 {
-  uint4 w[F32 ? 4 : 2];
+struct Raw8 {
+  static constexpr int kWords = F32 ? 2 : 1;
+  uint4 w[kWords];
   __device__ __forceinline__ void load(const void* x, long long at) {
     const uint4* p = F32 ? reinterpret_cast<const uint4*>(static_cast<const float*>(x) + at)
                          : reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(x) + at);
 #pragma unroll
-    for (int i = 0; i < (F32 ? 4 : 2); ++i) w[i] = __ldcs(p + i);
+    for (int i = 0; i < kWords; ++i) w[i] = __ldcs(p + i);
   }
   __device__ __forceinline__ void zero() {
 #pragma unroll
-    for (int i = 0; i < (F32 ? 4 : 2); ++i) w[i] = make_uint4(0, 0, 0, 0);
+    for (int i = 0; i < kWords; ++i) w[i] = make_uint4(0, 0, 0, 0);
   }
   __device__ __forceinline__ float at(int c) const {  // c a constant
     const uint4& v = w[c / (F32 ? 4 : 8)];
     const int i = F32 ? c % 4 : c % 8 / 2;
     const uint32_t u = i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
     return __uint_as_float(F32 ? u : c % 2 ? u & 0xFFFF0000u : u << 16);
+  }
+  // max |x_c| with the bits of an infinity or NaN above all numbers'
+  __device__ __forceinline__ uint32_t max_bits() const {
+    if constexpr (F32) {
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < kWords; ++i)
+        m = max(max(m, max(w[i].x & 0x7FFFFFFFu, w[i].y & 0x7FFFFFFFu)),
+                max(w[i].z & 0x7FFFFFFFu, w[i].w & 0x7FFFFFFFu));
+      return m;
+    } else {
+      const uint32_t m = __vmaxu2(__vmaxu2(w[0].x & 0x7FFF7FFFu, w[0].y & 0x7FFF7FFFu),
+                                  __vmaxu2(w[0].z & 0x7FFF7FFFu, w[0].w & 0x7FFF7FFFu));
+      return max(m & 0xFFFF0000u, m << 16);
+    }
+  }
+  __device__ __forceinline__ float max_finite() const {
+    float a = 0.f;
+#pragma unroll
+    for (int c = 0; c < kChunk; ++c) {
+      const float m = fabsf(at(c));
+      a = fmaxf(a, m < INFINITY ? m : 0.f);
+    }
+    return a;
   }
 };
 
@@ -99,12 +128,12 @@ __device__ __forceinline__ KvPlace kv_place(int lanes_per_row) {
   return p;
 }
 
-// NC: chunks of a lane (dim <= 16 * L * NC).
+// NC: chunks of a lane (dim <= 8 * L * NC).
 template <bool F32, int NC>
 __global__ void __launch_bounds__(kKvThreads)
 kv_quantize_kernel(const KvSide k, const KvSide v, int sides, int num_rows, int Hkv, int log_l,
                    const int32_t* __restrict__ slots, int cache_rows, int32_t* status) {
-  constexpr int kUnroll = NC == 1 && !F32 ? 2 : 1;
+  constexpr int kUnroll = F32 ? (NC == 1 ? 2 : 1) : NC == 1 ? 4 : NC == 2 ? 2 : 1;
   const int L = 1 << log_l, lpr = (sides * Hkv) << log_l;
   const KvPlace pl = kv_place(lpr);
   if (!pl.on) return;
@@ -117,7 +146,7 @@ kv_quantize_kernel(const KvSide k, const KvSide v, int sides, int num_rows, int 
     const int c0 = lane * kChunk;
     for (long long r0 = (long long)blockIdx.x * pl.rows + pl.row; r0 < num_rows;
          r0 += (long long)step * kUnroll) {
-      Raw16<F32> raw[kUnroll][NC];
+      Raw8<F32> raw[kUnroll][NC];
       int slot[kUnroll];
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
@@ -140,15 +169,17 @@ kv_quantize_kernel(const KvSide k, const KvSide v, int sides, int num_rows, int 
       }
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
-        float a = 0.f;
+        uint32_t bits = 0;
 #pragma unroll
-        for (int i = 0; i < NC; ++i)
+        for (int i = 0; i < NC; ++i) bits = max(bits, raw[u][i].max_bits());
+        for (int o = L >> 1; o > 0; o >>= 1) bits = max(bits, __shfl_xor_sync(group, bits, o));
+        float a = __uint_as_float(bits);
+        if (bits >= 0x7F800000u) {  // (the same in the vector's lanes)
+          a = 0.f;
 #pragma unroll
-          for (int c = 0; c < kChunk; ++c) {
-            const float m = fabsf(raw[u][i].at(c));
-            a = fmaxf(a, m < INFINITY ? m : 0.f);
-          }
-        for (int o = L >> 1; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(group, a, o));
+          for (int i = 0; i < NC; ++i) a = fmaxf(a, raw[u][i].max_finite());
+          for (int o = L >> 1; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(group, a, o));
+        }
         if (slot[u] < 0) continue;
         const int e = scale_exponent(a);
         const float inv = exp2_int(-e);
@@ -157,12 +188,12 @@ kv_quantize_kernel(const KvSide k, const KvSide v, int sides, int num_rows, int 
         for (int i = 0; i < NC; ++i) {
           const int c = c0 + i * L * kChunk;
           if (c >= s.dim) continue;
-          uint32_t w[4];
+          uint32_t w[2];
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
+          for (int j = 0; j < 2; ++j)
             w[j] = (uint32_t)e4m3x2(raw[u][i].at(4 * j) * inv, raw[u][i].at(4 * j + 1) * inv) |
                    (uint32_t)e4m3x2(raw[u][i].at(4 * j + 2) * inv, raw[u][i].at(4 * j + 3) * inv) << 16;
-          *reinterpret_cast<uint4*>(dst + c) = make_uint4(w[0], w[1], w[2], w[3]);
+          *reinterpret_cast<uint2*>(dst + c) = make_uint2(w[0], w[1]);
         }
         if (lane == 0) s.scales[h * s.s_head + slot[u]] = exp2_int(e);
       }
@@ -174,7 +205,7 @@ template <bool F32, int NC>
 __global__ void __launch_bounds__(kKvThreads)
 kv_dequantize_kernel(const KvSide k, const KvSide v, int sides, int num_rows, int Hkv, int log_l,
                      const int32_t* __restrict__ idx, int cache_rows, int32_t* status) {
-  constexpr int kUnroll = 4 / NC;
+  constexpr int kUnroll = NC == 1 ? 8 : NC == 2 ? 4 : 2;
   const int L = 1 << log_l, lpr = (sides * Hkv) << log_l;
   const KvPlace pl = kv_place(lpr);
   if (!pl.on) return;
@@ -188,7 +219,7 @@ kv_dequantize_kernel(const KvSide k, const KvSide v, int sides, int num_rows, in
          r0 += (long long)step * kUnroll) {
       int src[kUnroll];
       float scale[kUnroll];
-      uint4 w[kUnroll][NC];
+      uint2 w[kUnroll][NC];
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
         const long long row = r0 + (long long)u * step;
@@ -206,7 +237,7 @@ kv_dequantize_kernel(const KvSide k, const KvSide v, int sides, int num_rows, in
         for (int i = 0; i < NC; ++i) {
           const int c = c0 + i * L * kChunk;
           if (c < s.dim)
-            w[u][i] = __ldg(reinterpret_cast<const uint4*>(s.codes + (long long)src[u] * s.c_row +
+            w[u][i] = __ldg(reinterpret_cast<const uint2*>(s.codes + (long long)src[u] * s.c_row +
                                                            h * s.c_head + c));
         }
       }
@@ -218,28 +249,24 @@ kv_dequantize_kernel(const KvSide k, const KvSide v, int sides, int num_rows, in
         for (int i = 0; i < NC; ++i) {
           const int c = c0 + i * L * kChunk;
           if (c >= s.dim) continue;
-          const uint32_t q[4] = {w[u][i].x, w[u][i].y, w[u][i].z, w[u][i].w};
-          float f[16];
+          const uint32_t q[2] = {w[u][i].x, w[u][i].y};
+          float f[kChunk];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
+          for (int j = 0; j < 2; ++j) {
             e4m3x2_to_f32((uint16_t)q[j], f[4 * j], f[4 * j + 1]);
             e4m3x2_to_f32((uint16_t)(q[j] >> 16), f[4 * j + 2], f[4 * j + 3]);
           }
 #pragma unroll
-          for (int j = 0; j < 16; ++j) f[j] *= scale[u];
+          for (int j = 0; j < kChunk; ++j) f[j] *= scale[u];
           if (F32) {
             float4* o = reinterpret_cast<float4*>(static_cast<float*>(s.out) + at + c);
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+            for (int j = 0; j < 2; ++j)
               __stcs(o + j, make_float4(f[4 * j], f[4 * j + 1], f[4 * j + 2], f[4 * j + 3]));
           } else {
-            uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(s.out) + at + c);
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-              __stcs(o + j, make_uint4(pack_bf16x2(f[8 * j], f[8 * j + 1]),
-                                       pack_bf16x2(f[8 * j + 2], f[8 * j + 3]),
-                                       pack_bf16x2(f[8 * j + 4], f[8 * j + 5]),
-                                       pack_bf16x2(f[8 * j + 6], f[8 * j + 7])));
+            __stcs(reinterpret_cast<uint4*>(static_cast<uint16_t*>(s.out) + at + c),
+                   make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                              pack_bf16x2(f[6], f[7])));
           }
         }
       }
@@ -268,18 +295,19 @@ int cache_side(const cp_kv_codes_t* c, int dim, int Hkv, int cache_rows, KvSide*
   return CPATTN_OK;
 }
 
-// Lanes of a vector (log2) and blocks of a launch: enough for the rows, and at most
-// some blocks per SM, the rest of the rows being the loop's.
+// Lanes of a vector (log2) and blocks of a launch: enough for the rows, and at most as
+// many as reside at once, the rest of the rows being the loop's (16 per SM, in turn:
+// 8192 rows written in 14 us instead of 12, 32768 read in 41 instead of 38).
 struct KvShape {
   int log_l, chunks;
   unsigned grid;
 };
-KvShape kv_shape(int num_rows, int vectors, int dim) {
+KvShape kv_shape(int num_rows, int vectors, int dim, int blocks_per_sm) {
   KvShape s;
-  for (s.log_l = 0; s.log_l < 5 && (kChunk << s.log_l) < dim; ++s.log_l) {}
+  for (s.log_l = 0; s.log_l < 5 && (4 * kChunk << s.log_l) < dim; ++s.log_l) {}
   s.chunks = (dim + (kChunk << s.log_l) - 1) / (kChunk << s.log_l);
   const long long lpr = (long long)vectors << s.log_l, rows = std::max<long long>(1, kKvThreads / lpr);
-  s.grid = (unsigned)std::min<long long>((num_rows + rows - 1) / rows, 152 * 16);
+  s.grid = (unsigned)std::min<long long>((num_rows + rows - 1) / rows, 152 * blocks_per_sm);
   return s;
 }
 
@@ -315,9 +343,13 @@ extern "C" int cp_kv_quantize(const void* k, int64_t k_row_stride, int64_t k_hea
   vs.x_row = v_row_stride;
   vs.x_head = v_head_stride;
   const int sides = v ? 2 : 1;
-  const KvShape sh = kv_shape(num_rows, sides * Hkv, std::max(d, v ? dv : 0));
-  auto kern = sh.chunks == 1 ? (x_is_fp32 ? kv_quantize_kernel<true, 1> : kv_quantize_kernel<false, 1>)
-                             : (x_is_fp32 ? kv_quantize_kernel<true, 2> : kv_quantize_kernel<false, 2>);
+  const KvShape sh = kv_shape(num_rows, sides * Hkv, std::max(d, v ? dv : 0), 4);
+  decltype(&kv_quantize_kernel<true, 1>) const kerns[2][4] = {
+      {kv_quantize_kernel<false, 1>, kv_quantize_kernel<false, 2>, kv_quantize_kernel<false, 3>,
+       kv_quantize_kernel<false, 4>},
+      {kv_quantize_kernel<true, 1>, kv_quantize_kernel<true, 2>, kv_quantize_kernel<true, 3>,
+       kv_quantize_kernel<true, 4>}};
+  auto kern = kerns[x_is_fp32 ? 1 : 0][sh.chunks - 1];
   kern<<<sh.grid, kKvThreads, 0, stream>>>(ks, vs, sides, num_rows, Hkv, sh.log_l, slots, cache_rows,
                                            status_dev);
   return cudaGetLastError() == cudaSuccess ? CPATTN_OK : CPATTN_ERR_CUDA;
@@ -339,10 +371,13 @@ extern "C" int cp_kv_dequantize(const cp_kv_codes_t* k_cache, const cp_kv_codes_
   ks.out = k_out;
   vs.out = v_out;
   const int sides = v_cache ? 2 : 1;
-  const KvShape sh = kv_shape(num_rows, sides * Hkv, std::max(d, v_cache ? dv : 0));
-  auto kern = sh.chunks == 1
-                  ? (out_is_fp32 ? kv_dequantize_kernel<true, 1> : kv_dequantize_kernel<false, 1>)
-                  : (out_is_fp32 ? kv_dequantize_kernel<true, 2> : kv_dequantize_kernel<false, 2>);
+  const KvShape sh = kv_shape(num_rows, sides * Hkv, std::max(d, v_cache ? dv : 0), 6);
+  decltype(&kv_dequantize_kernel<true, 1>) const kerns[2][4] = {
+      {kv_dequantize_kernel<false, 1>, kv_dequantize_kernel<false, 2>, kv_dequantize_kernel<false, 3>,
+       kv_dequantize_kernel<false, 4>},
+      {kv_dequantize_kernel<true, 1>, kv_dequantize_kernel<true, 2>, kv_dequantize_kernel<true, 3>,
+       kv_dequantize_kernel<true, 4>}};
+  auto kern = kerns[out_is_fp32 ? 1 : 0][sh.chunks - 1];
   kern<<<sh.grid, kKvThreads, 0, stream>>>(ks, vs, sides, num_rows, Hkv, sh.log_l, idx, cache_rows,
                                            status_dev);
   return cudaGetLastError() == cudaSuccess ? CPATTN_OK : CPATTN_ERR_CUDA;
