@@ -143,7 +143,7 @@ __device__ __forceinline__ int group_div(const SharedParams& p, int n) {
 __device__ __forceinline__ SharedPiece load_piece(const SharedParams& p, int i) {
   const int4* w = reinterpret_cast<const int4*>(p.table + p.pieces) + 3LL * i;
   const int4 a = __ldg(w), b = __ldg(w + 1), c = __ldg(w + 2);
-  return SharedPiece{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, c.x, c.y, c.z, c.w};
+  return SharedPiece{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, c.x, c.y, {c.z, c.w}};
 }
 __device__ __forceinline__ bool piece_ok(const SharedParams& p, const SharedPiece& pc, int kind) {
   return pc.rows >= 1 && pc.rows <= kRows && shared_kind(pc.rows) == kind && pc.r0 >= 0 &&
@@ -151,8 +151,7 @@ __device__ __forceinline__ bool piece_ok(const SharedParams& p, const SharedPiec
          (long long)pc.q_row0 + ((long long)pc.r0 + pc.rows - 1) / p.g < p.num_q_rows &&
          pc.kv_head >= 0 && pc.kv_head < p.Hkv && pc.keys >= 1 && pc.key0 >= 0 && pc.kv_row >= 0 &&
          (long long)pc.kv_row + pc.keys <= p.num_kv_rows && pc.ws_row >= 0 &&
-         (pc.reps == 1 || (pc.reps == 2 && pc.rows <= 64) || (pc.reps == 4 && pc.rows <= 32)) &&
-         (long long)pc.ws_row + pc.reps * pc.rows <= p.ws_rows;
+         (long long)pc.ws_row + pc.rows <= p.ws_rows;
 }
 __device__ __forceinline__ int num_tiles(int keys) { return (keys - 1) / BN + 1; }
 
@@ -291,39 +290,37 @@ constexpr uint32_t idesc_16bit_f32(bool f16, int M, int N, int b_mn) {
   return idesc_bf16_f32(M, N, 0, b_mn) & ~(f16 ? (1u << 7) | (1u << 10) : 0u);
 }
 
-// One KV tile for the rows of a warp (one per lane): keys [copy * W, (copy + 1) * W)
-// of the tile.  S from TMEM, masked to the `here` visible keys of the tile, online
-// softmax in base 2, P (16 bits, zero for the other copies' keys) back over S, and
-// where there is an O (`has_o`), O rescaled when the maximum moves or o_scale != 1.
-template <int W, int D, bool QUANT>
-__device__ __forceinline__ void softmax_tile(uint32_t s_addr, uint32_t o_addr, int copy, int here,
-                                             bool has_o, float o_scale, float sl2, float& m_run,
+// One KV tile for the rows of a warp (one per lane).  S from TMEM, masked to the `here`
+// visible keys of the tile, online softmax in base 2, P (16 bits) back over S, and where
+// there is an O (`has_o`), O rescaled when the maximum moves or o_scale != 1.
+template <int D, bool QUANT>
+__device__ __forceinline__ void softmax_tile(uint32_t s_addr, uint32_t o_addr, int here, bool has_o,
+                                             float o_scale, float sl2, float& m_run,
                                              float& m_use, float& l_run) {
-  float x[W];
+  float x[BN];
   {
-    uint32_t v[W];
+    uint32_t v[BN];
 #pragma unroll
-    for (int q = 0; q < W / 32; ++q) tmem_ld32p(s_addr + copy * W + q * 32, v + q * 32);
+    for (int q = 0; q < BN / 32; ++q) tmem_ld32p(s_addr + q * 32, v + q * 32);
     tmem_wait_ld();
 #pragma unroll
-    for (int c = 0; c < W; ++c) x[c] = __uint_as_float(v[c]);
+    for (int c = 0; c < BN; ++c) x[c] = __uint_as_float(v[c]);
   }
-  here -= copy * W;
-  if (here < W) {
+  if (here < BN) {
 #pragma unroll
-    for (int c = 0; c < W; ++c)
+    for (int c = 0; c < BN; ++c)
       if (c >= here) x[c] = -INFINITY;
   }
   float mx0 = x[0], mx1 = x[1], mx2 = x[2], mx3 = x[3];
 #pragma unroll
-  for (int c = 4; c + 8 <= W; c += 8) {
+  for (int c = 4; c + 8 <= BN; c += 8) {
     mx0 = fmax3(mx0, x[c], x[c + 1]);
     mx1 = fmax3(mx1, x[c + 2], x[c + 3]);
     mx2 = fmax3(mx2, x[c + 4], x[c + 5]);
     mx3 = fmax3(mx3, x[c + 6], x[c + 7]);
   }
-  mx0 = fmax3(mx0, x[W - 4], x[W - 3]);
-  mx1 = fmax3(mx1, x[W - 2], x[W - 1]);
+  mx0 = fmax3(mx0, x[BN - 4], x[BN - 3]);
+  mx1 = fmax3(mx1, x[BN - 2], x[BN - 1]);
   const float mx = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)) * sl2;
   // The maximum moves only when a tile raises it by more than kMaxSlack (log2
   // units): exponentials stay below 2^kMaxSlack, l uses the same maximum, and O in
@@ -334,7 +331,7 @@ __device__ __forceinline__ void softmax_tile(uint32_t s_addr, uint32_t o_addr, i
   const float alpha = move ? ex2_approx(m_run - m_new_use) : 1.f;
   float sum0 = 0.f, sum1 = 0.f;
 #pragma unroll
-  for (int q = 0; q < W / 32; ++q) {
+  for (int q = 0; q < BN / 32; ++q) {
     uint32_t pk[16];
 #pragma unroll
     for (int c = 0; c < 32; c += 2) {
@@ -347,15 +344,7 @@ __device__ __forceinline__ void softmax_tile(uint32_t s_addr, uint32_t o_addr, i
       // 2^-11 (f16) of each weight; l sums the unrounded values
       pk[c >> 1] = QUANT ? pack_f16x2(a, b) : pack_bf16x2(a, b);
     }
-    tmem_st16(s_addr + copy * (W / 2) + q * 16, pk);
-  }
-  if constexpr (W < BN) {
-    uint32_t zero[16];
-#pragma unroll
-    for (int c = 0; c < 16; ++c) zero[c] = 0u;
-#pragma unroll
-    for (int q = 0; q < BN / 32; ++q)
-      if (q / (W / 32) != copy) tmem_st16(s_addr + q * 16, zero);
+    tmem_st16(s_addr + q * 16, pk);
   }
   l_run = l_run * alpha + (sum0 + sum1);
   const bool need = has_o && (move || o_scale != 1.f);
@@ -376,7 +365,7 @@ __device__ __forceinline__ void softmax_tile(uint32_t s_addr, uint32_t o_addr, i
   m_use = m_new_use;
 }
 
-// Partial rows in the workspace: those of one piece (or copy) by chunks of 8 columns, so
+// Partial rows in the workspace: those of one piece by chunks of 8 columns, so
 // that the lanes of a warp, a row each, store to one place.  Offset of column 8 c of row
 // r of `rows`, from the first row's place at D floats a row.
 __device__ __forceinline__ int partial_at(int c, int r, int rows) { return (c * rows + r) * 8; }
@@ -793,8 +782,8 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
       return q_line + (c >> 3) * (BM * 128) + (((c & 7) ^ (trow & 7)) << 4);
     };
     auto row_of = [&](const SharedPiece& pc) {
-      // (a small unit's rows in the other half for stream 1: other schedulers' warps)
-      return shared_dual(pc.rows) ? s * BM + trow : (trow + s * (BM / 2)) & (BM / pc.reps - 1);
+      // (a single unit's rows in the other half for stream 1: other schedulers' warps)
+      return shared_dual(pc.rows) ? s * BM + trow : trow ^ (s * (BM / 2));
     };
     // The warp's query rows of a piece to shared memory, asynchronously (D / 8 lanes to a
     // row: a thread for each row would touch 32 lines with every instruction, 4000 cycles
@@ -879,8 +868,7 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
       if (more) np = piece(i + 1);
       const bool dual = i < duals;
       const int T = num_tiles(pc.keys);
-      const int reps = pc.reps, r = row_of(pc);
-      const int copy = reps == 4 ? wq : reps == 2 ? wq >> 1 : 0;
+      const int r = row_of(pc);
       const bool warp_live = (r & ~31) < pc.rows;
       int seen = 0;  // keys of the piece that this row sees
       if (r < pc.rows) {
@@ -913,14 +901,7 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
         }
         if (warp_live) {
           const int here = seen - t * BN;  // visible keys of this tile
-          if (reps == 1)
-            softmax_tile<BN, D, QUANT>(s_addr, o_addr, 0, here, t > 0, o_scale, sl2, m_run, m_use, l_run);
-          else if (reps == 2)
-            softmax_tile<BN / 2, D, QUANT>(s_addr, o_addr, copy, here, t > 0, o_scale, sl2, m_run, m_use,
-                                           l_run);
-          else
-            softmax_tile<BN / 4, D, QUANT>(s_addr, o_addr, copy, here, t > 0, o_scale, sl2, m_run, m_use,
-                                           l_run);
+          softmax_tile<D, QUANT>(s_addr, o_addr, here, t > 0, o_scale, sl2, m_run, m_use, l_run);
         }
         if constexpr (!QUANT) {
           // V rows behind the last key become zeros (0 * NaN is NaN, so masking P
@@ -955,8 +936,7 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
       if (warp_live) {
         const bool none = l_run == 0.f;  // (a NaN sum is not none)
         const float inv = none ? 0.f : exp2_int(ev) / l_run;
-        const long long row0 = (long long)pc.ws_row + copy * pc.rows;
-        float* dst = p.ws_o + row0 * D;
+        float* dst = p.ws_o + (long long)pc.ws_row * D;
         constexpr int kCols = QUANT ? 64 : D;  // (register budget)
 #pragma unroll
         for (int q = 0; q < D / kCols; ++q) {
@@ -974,7 +954,7 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             }
           }
         }
-        if (r < pc.rows) p.ws_l[row0 + r] = none ? -INFINITY : m_use + lg2_approx(l_run);
+        if (r < pc.rows) p.ws_l[(long long)pc.ws_row + r] = none ? -INFINITY : m_use + lg2_approx(l_run);
       }
       tc_fence_before();
     }

@@ -59,7 +59,7 @@ struct Place {
 struct Cut {
   const cp_segment_t* seg;
   long long unit, r0, key0, keys;
-  int rows, head, reps;
+  int rows, head;
 };
 
 void measure(const Line& L, Place& p) {
@@ -124,7 +124,7 @@ void share(const Line& L, Place& p, long long budget, F&& f) {
     if (budget - used < fixed + cost) return;
     const long long n = std::min(p.keys - p.key0, fit * kKeys);
     f(Cut{L.segs + p.seg, p.unit0 + p.tile * L.Hkv + p.head, p.tile * CPATTN_SHARED_ROWS, p.key0, n,
-          p.rows, p.head, shared_reps(p.rows, p.keys)});
+          p.rows, p.head});
     p.key0 += n;
     used += fixed + fit * cost;
   }
@@ -225,7 +225,7 @@ extern "C" int cp_shared_plan_size(const cp_segment_t* segs, int num_segs, int n
   long long pieces = 0, ws_rows = 0;
   deal(L, hi, num_ctas, [&](int, const Cut& k, int) {
     ++pieces;
-    ws_rows += k.reps * k.rows;
+    ws_rows += k.rows;
   });
   if (ws_rows > 0x7fffffffLL) return CPATTN_ERR_TOO_LARGE;
   plan->num_q_rows = num_q_rows;
@@ -263,7 +263,7 @@ extern "C" int cp_shared_plan(const cp_segment_t* segs, int num_segs, const cp_s
   deal(L, plan->budget, plan->num_ctas, [&](int, const Cut& k, int) {
     ++np;
     ++kinds[shared_kind(k.rows)];
-    ws += k.reps * k.rows;
+    ws += k.rows;
   });
   if (np != plan->num_pieces || ws != plan->ws_rows) return CPATTN_ERR_INVALID_ARG;
 
@@ -325,12 +325,11 @@ extern "C" int cp_shared_plan(const cp_segment_t* segs, int num_segs, const cp_s
     p.key0 = (int32_t)k.key0;
     p.keys = (int32_t)k.keys;
     p.ws_row = ws_row;
-    p.reps = k.reps;
-    ws_row += k.reps * k.rows;
+    ws_row += k.rows;
     pieces[at] = p;
     SharedUnit& u = units[k.unit];  // (its pieces come one after the other)
     if (u.parts == 0) u.ws_row = p.ws_row;
-    u.parts += k.reps;
+    ++u.parts;
     u.rows = k.rows;
   });
   open(plan->num_ctas - 1);

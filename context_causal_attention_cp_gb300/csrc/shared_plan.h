@@ -25,9 +25,8 @@ struct SharedPiece {
   int32_t kv_row;    // KV row of the piece's first key
   int32_t key0;      // its key number within the segment's run
   int32_t keys;      // keys of the piece, >= 1
-  int32_t ws_row;    // first partial row in the workspace (reps * rows of them)
-  int32_t reps;      // copies of the rows in the MMA tile, see shared_reps
-  int32_t unused;
+  int32_t ws_row;    // first partial row in the workspace (`rows` of them)
+  int32_t unused[2];
 };
 static_assert(sizeof(SharedPiece) == 48, "three 16-byte words");
 
@@ -51,17 +50,8 @@ __host__ __device__ constexpr int shared_kind(int rows) {  // 0 dual, 1 single, 
   return shared_dual(rows) ? 0 : rows > kSharedSmallRows ? 1 : 2;
 }
 
-// A unit of at most 64 (32) rows and enough keys fills its MMA tile with 2 (4) copies
-// of its rows, and copy c works on the c-th half (quarter) of the keys of every KV
-// tile: the MMAs cost the same, and all four warps of a stream share the exponentials.
-// Each copy leaves a partial result, which pays from kSharedRepKeys keys on: TODO.
-constexpr int kSharedRepKeys = 2048;
-__host__ __device__ constexpr int shared_reps(int rows, long long keys) {
-  return keys < kSharedRepKeys || rows <= kSharedSmallRows ? 1 : rows <= 32 ? 4 : rows <= 64 ? 2 : 1;
-}
-
 // The partials of a unit: part j of its packed row r is workspace row ws_row + j * rows
-// + r; the pieces' copies in the order of the keys.
+// + r; the pieces in the order of their keys.
 struct SharedUnit {
   int32_t ws_row, parts, rows, unused;
 };

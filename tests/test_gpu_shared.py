@@ -289,7 +289,7 @@ def test_table_that_does_not_match_is_reported():
     for at, value in ((pieces + 0, 4), (pieces + 4, 257), (pieces + 4, 200), (pieces + 5, 2),
                       (pieces + 6, 590), (pieces + 6, -1), (pieces + 8, 0),
                       (pieces + 9, int(i.ws_rows)), (6, i.num_pieces + 1), (5, -1), (1, 1),
-                      (pieces + 10, 3), (units + 1, 1 << 30), (units + 2, 257), (units, -1),
+                      (units + 1, 1 << 30), (units + 2, 257), (units, -1),
                       (entries, i.num_units), (entries + 1, -1)):
         table = plan.table.clone()
         table[at] = value

@@ -16,7 +16,7 @@ from oracle import shared as osh
 ROWS = 256  # CPATTN_SHARED_ROWS
 CTA = ("dual0", "dual1", "single0", "single1", "single2", "small0", "small1", "u0")
 PIECE = ("q_row0", "q_pos0", "q_pos_step", "r0", "rows", "kv_head", "kv_row", "key0", "keys",
-         "ws_row", "reps", "u1")
+         "ws_row", "u0", "u1")
 UNIT = ("ws_row", "parts", "rows", "u0")
 
 
@@ -64,8 +64,7 @@ def check_plan(segs, N, Hq, Hkv, num_ctas):
     used = np.zeros(plan.info.ws_rows, dtype=np.int32)
     for p in T["pieces"]:
         assert 1 <= p["rows"] <= ROWS and p["keys"] >= 1
-        assert p["reps"] in (1, 2, 4) and p["reps"] * p["rows"] <= max(128, p["rows"])
-        parts = p["rows"] * p["reps"]
+        parts = p["rows"]
         assert 0 <= p["ws_row"] and p["ws_row"] + parts <= plan.info.ws_rows
         used[p["ws_row"]: p["ws_row"] + parts] += 1
         assert p["kv_row"] + p["keys"] <= plan.info.kv_rows
@@ -88,7 +87,7 @@ def check_plan(segs, N, Hq, Hkv, num_ctas):
                     assert packed % ROWS < p["rows"] == u["rows"]
                     assert p["key0"] == at and p["kv_row"] == kv0 + at
                     at += p["keys"]
-                    part += p["reps"]
+                    part += 1
                 assert part == u["parts"] and at >= seen
     return plan, T
 
