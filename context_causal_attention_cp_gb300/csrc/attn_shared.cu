@@ -147,8 +147,8 @@ __device__ __forceinline__ SharedPiece load_piece(const SharedParams& p, int i) 
 }
 __device__ __forceinline__ bool piece_ok(const SharedParams& p, const SharedPiece& pc, int kind) {
   return pc.rows >= 1 && pc.rows <= kRows && shared_kind(pc.rows) == kind && pc.r0 >= 0 &&
-         pc.q_row0 >= 0 &&
-         (long long)pc.q_row0 + ((long long)pc.r0 + pc.rows - 1) / p.g < p.num_q_rows &&
+         pc.r0 <= 0x7fffffff - kRows && pc.q_row0 >= 0 &&
+         (long long)pc.q_row0 + group_div(p, pc.r0 + pc.rows - 1) < p.num_q_rows &&
          pc.kv_head >= 0 && pc.kv_head < p.Hkv && pc.keys >= 1 && pc.key0 >= 0 && pc.kv_row >= 0 &&
          (long long)pc.kv_row + pc.keys <= p.num_kv_rows && pc.ws_row >= 0 &&
          (long long)pc.ws_row + pc.rows <= p.ws_rows;
@@ -162,9 +162,9 @@ __device__ __forceinline__ SharedCta load_cta(const SharedParams& p) {
   return SharedCta{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 }
 // Checks every piece of this block's list against the buffers: the roles below walk
-// the list on their own and rely on it.  tiles[s]: KV tiles of stream s's small units
+// the list on their own and rely on it.  tiles[s]: KV tiles of stream s's single units
 // (zeroed by the caller before a barrier).  All threads call it; false (and
-// CPATTN_ERR_RANGE) when the list cannot be run.
+// CPATTN_ERR_RANGE) when the list cannot be run.  It is a barrier, too.
 __device__ __forceinline__ bool check_list(const SharedParams& p, const SharedCta& c, int* tiles) {
   bool ok = c.dual0 >= 0 && c.dual0 <= c.dual1 && c.dual1 <= p.num_pieces && c.single0 >= 0 &&
             c.single0 <= c.single1 && c.single1 <= c.single2 && c.single2 <= p.num_pieces &&
@@ -182,7 +182,8 @@ __device__ __forceinline__ bool check_list(const SharedParams& p, const SharedCt
     }
   }
   ok = __syncthreads_and(ok);
-  ok = ok && (tiles[0] == tiles[1] || tiles[0] == tiles[1] + 1);
+  // (a small list has no single units and no tiles)
+  if (ok && c.single0 < c.single2) ok = tiles[0] == tiles[1] || tiles[0] == tiles[1] + 1;
   if (!ok && threadIdx.x == 0) set_status(p.status, CPATTN_ERR_RANGE);
   return ok;
 }
@@ -425,12 +426,10 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
   }
   if (threadIdx.x < 2) stream_tiles[threadIdx.x] = 0;
   __syncthreads();
-  if (!check_list(p, list, stream_tiles)) return;
   if (list.small0 < list.small1) {
     run_small<D, QUANT>(p, list, smem, &tm_k, &tm_v, &tm_k_tail, &tm_v_tail);
     return;
   }
-  const int steps = stream_tiles[0] + stream_tiles[1];  // of the single units
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kStages; ++i) {
       for (int u = 0; u < 3; ++u) mbar_init(full + u * C::kStages + i, QUANT ? kConvertThreads : 1);
@@ -457,9 +456,15 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     tmem_relinquish();
   }
   tc_fence_before();
-  __syncthreads();
+  const bool runs = check_list(p, list, stream_tiles);
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
+  if (!runs) {
+    __syncthreads();
+    if (warp == kProducerWarp) tmem_dealloc(tmem_base, C::kTmemCols);
+    return;
+  }
+  const int steps = stream_tiles[0] + stream_tiles[1];  // of the single units
   const uint32_t q_base = smem_u32(smem);
   const uint32_t ring_base = smem_u32(smem + C::kRingOff);
   // A ring slot has a full barrier for each user (stream 0, stream 1, both), so that

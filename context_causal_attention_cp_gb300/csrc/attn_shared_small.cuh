@@ -500,7 +500,7 @@ __device__ __forceinline__ void run_small(const SharedParams& p, const SharedCta
     *issued_loads = 0;
     fence_barrier_init();
   }
-  __syncthreads();
+  if (!check_list(p, list, nullptr)) return;
   auto arrive_copies = [&](uint64_t* bar) {  // when this lane's copies so far have landed
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
   };
