@@ -37,7 +37,6 @@ i32 = ctypes.c_int
 i64 = ctypes.c_int64
 
 
-
 class KvCodes(ctypes.Structure):
     """cp_kv_codes_t"""
     _fields_ = [("codes", vp), ("scales", vp), ("row_stride", i64), ("head_stride", i64),
@@ -48,7 +47,7 @@ class SharedPlanInfo(ctypes.Structure):
     """cp_shared_plan_t"""
     _fields_ = [(n, ctypes.c_int32) for n in
                 ("num_q_rows", "Hq", "Hkv", "num_ctas", "num_units", "num_pieces", "num_entries",
-                 "kv_rows", "needs_merge", "budget")] + [("ws_rows", i64), ("table_ints", i64)]
+                 "kv_rows", "budget")] + [("ws_rows", i64), ("table_ints", i64)]
 
 
 # name -> (restype, argtypes); must match include/cpattn.h

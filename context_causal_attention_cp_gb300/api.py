@@ -825,7 +825,8 @@ def _new_rows(x, name, dtype, n, Hkv, dim, index):
     rs, hs, cs = x.stride()
     if cs != 1 and x.numel():
         raise ValueError(f"{name} needs a contiguous last dim")
-    return rs, hs
+    # a tensor of one row or head may carry any stride for that dim
+    return rs if n > 1 else 0, hs if Hkv > 1 else 0
 
 
 def cp_kv_quantize(cache: KVCache, k, v=None, slots=None, *, status=None, stream=None) -> KVCache:

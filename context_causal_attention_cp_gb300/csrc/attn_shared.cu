@@ -32,7 +32,8 @@
 // largest e that the stream has met in the piece; O is rescaled when that grows.  A
 // query row enters as f16 times the power of two that brings its largest element to
 // [2^14, 2^15), so that elements down to 2^-30 of it keep bf16's 8 bits.  P in f16 is
-// off by 2^-12 of a weight (bf16: 2^-9).
+// off by at most 2^-11 of a weight (bf16: 2^-8) down to 2^-21 of the largest weight, and
+// by 2^-32 of the largest below that.
 #include <algorithm>
 #include <cstdint>
 
@@ -291,6 +292,12 @@ constexpr uint32_t idesc_16bit_f32(bool f16, int M, int N, int b_mn) {
   return idesc_bf16_f32(M, N, 0, b_mn) & ~(f16 ? (1u << 7) | (1u << 10) : 0u);
 }
 
+// f16 weights are 2^kF16Lift times those of the maximum that they are taken by: an f16
+// below 2^-14 loses bits, which now begins at 2^-21 of the largest weight (and ends the
+// weight at 2^-32), and kF16Lift + kMaxSlack stays below 2^16.
+constexpr float kF16Lift = 7.f;
+static_assert(kF16Lift + kMaxSlack < 16.f, "f16 range");
+
 // One KV tile for the rows of a warp (one per lane).  S from TMEM, masked to the `here`
 // visible keys of the tile, online softmax in base 2, P (16 bits) back over S, and where
 // there is an O (`has_o`), O rescaled when the maximum moves or o_scale != 1.
@@ -328,8 +335,9 @@ __device__ __forceinline__ void softmax_tile(uint32_t s_addr, uint32_t o_addr, i
   // TMEM is rescaled only then.
   const bool move = mx > m_run + kMaxSlack;
   const float m_new = move ? mx : m_run;
-  const float m_new_use = (m_new == -INFINITY) ? 0.f : m_new;
-  const float alpha = move ? ex2_approx(m_run - m_new_use) : 1.f;
+  const float m_num = (m_new == -INFINITY) ? 0.f : m_new;
+  const float alpha = move ? ex2_approx(m_run - m_num) : 1.f;
+  const float m_new_use = QUANT ? m_num - kF16Lift : m_num;
   float sum0 = 0.f, sum1 = 0.f;
 #pragma unroll
   for (int q = 0; q < BN / 32; ++q) {
@@ -426,6 +434,7 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
   }
   if (threadIdx.x < 2) stream_tiles[threadIdx.x] = 0;
   __syncthreads();
+  if (list.dual0 == list.dual1 && list.single0 == list.single2 && list.small0 == list.small1) return;  // no work
   if (list.small0 < list.small1) {
     run_small<D, QUANT>(p, list, smem, &tm_k, &tm_v, &tm_k_tail, &tm_v_tail);
     return;
@@ -1189,21 +1198,23 @@ __global__ void __launch_bounds__(kMergeThreads) shared_merge_kernel(const Share
 // Warps for a row's J heads: enough that a warp loads its partials in two goes (their
 // average is ws_rows / rows), e.g. 152 partials a row at one token on a 256K prefix.
 template <int D, int J>
-int launch_merge(const SharedParams& p, cudaStream_t stream) {
+int launch_merge(const SharedParams& p, bool behind, cudaStream_t stream) {
   const long long rows = (long long)p.num_q_rows * p.Hq;
   int ways = 1;
   while (ways < kMergeWarps && p.ws_rows > rows * ways * 2 * MergeCfg<D, J>::kLoads) ways *= 2;
   const long long blocks = (rows / J * ways + kMergeWarps - 1) / kMergeWarps;
   if (blocks > 0x7fffffffLL) return CPATTN_ERR_TOO_LARGE;
   const cudaError_t e = launch_kernel(shared_merge_kernel<D, J>, (unsigned)blocks, kMergeThreads, 0, stream,
-                                      true, p, ways);
+                                      behind, p, ways);
   return e == cudaSuccess ? CPATTN_OK : CPATTN_ERR_CUDA;
 }
+// behind: the kernel before it on the stream is this call's, not one that may still
+// write the plan's table.
 template <int D>
-int launch_merge(const SharedParams& p, cudaStream_t stream) {
-  return p.g % 4 == 0   ? launch_merge<D, 4>(p, stream)
-         : p.g % 2 == 0 ? launch_merge<D, 2>(p, stream)
-                        : launch_merge<D, 1>(p, stream);
+int launch_merge(const SharedParams& p, bool behind, cudaStream_t stream) {
+  return p.g % 4 == 0   ? launch_merge<D, 4>(p, behind, stream)
+         : p.g % 2 == 0 ? launch_merge<D, 2>(p, behind, stream)
+                        : launch_merge<D, 1>(p, behind, stream);
 }
 
 // 3-D map of a code buffer (cols, heads, rows) with a D-column x 1-head box, rows
@@ -1340,5 +1351,6 @@ extern "C" int cp_attn_shared(const cp_shared_plan_t* plan, const int32_t* table
                                     : launch_shared<64, false>(m, p, n, stream));
     if (r != CPATTN_OK) return r;
   }
-  return d == 128 ? launch_merge<128>(p, stream) : launch_merge<64>(p, stream);
+  const bool behind = plan->num_pieces > 0;
+  return d == 128 ? launch_merge<128>(p, behind, stream) : launch_merge<64>(p, behind, stream);
 }

@@ -327,8 +327,9 @@ __device__ __forceinline__ bool small_piece(const SharedParams& p, const SmallWa
         mx = fmaxf(mx, __shfl_xor_sync(all, mx, 16));
         const bool move = mx > m_run[e] + kMaxSlack;
         const float m_new = move ? mx : m_run[e];
-        const float use = m_new == -INFINITY ? 0.f : m_new;
-        alpha[e] = move ? ex2_approx(m_run[e] - use) : 1.f;
+        const float m_num = m_new == -INFINITY ? 0.f : m_new;
+        const float use = QUANT ? m_num - kF16Lift : m_num;
+        alpha[e] = move ? ex2_approx(m_run[e] - m_num) : 1.f;
         any = any || move;
         m_run[e] = m_new;
         m_use[e] = use;

@@ -279,7 +279,7 @@ inline bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintp
 // Checks one side's cache and moves it into the kernels' form.
 int cache_side(const cp_kv_codes_t* c, int dim, int Hkv, int cache_rows, KvSide* s) {
   if (dim < 16 || dim > kMaxDim || dim % 16) return CPATTN_ERR_UNSUPPORTED;
-  if (!c->codes || !c->scales) return CPATTN_ERR_INVALID_ARG;
+  if ((!c->codes || !c->scales) && cache_rows > 0) return CPATTN_ERR_INVALID_ARG;
   if (!aligned(c->codes, 16) || !aligned(c->scales, 4) || c->row_stride % 16 ||
       c->head_stride % 16)
     return CPATTN_ERR_ALIGNMENT;

@@ -236,7 +236,6 @@ extern "C" int cp_shared_plan_size(const cp_segment_t* segs, int num_segs, int n
   plan->num_pieces = (int32_t)pieces;
   plan->num_entries = (int32_t)entries;
   plan->kv_rows = (int32_t)kv_rows;
-  plan->needs_merge = entries > 0;
   plan->budget = (int32_t)hi;
   plan->ws_rows = ws_rows;
   plan->table_ints = shared_table(*plan).total;

@@ -606,7 +606,6 @@ typedef struct {
   int32_t num_q_rows, Hq, Hkv, num_ctas;
   int32_t num_units, num_pieces, num_entries;
   int32_t kv_rows;     /* KV rows that the segments reach */
-  int32_t needs_merge; /* some row has more than one partial, or none */
   int32_t budget;      /* cost of the largest share */
   int64_t ws_rows;     /* partial rows in the workspace */
   int64_t table_ints;  /* size of the table, int32 words */
@@ -624,18 +623,22 @@ int cp_shared_workspace_size(const cp_shared_plan_t* plan, int dv, int64_t* byte
  *     c], num_q_rows rows (strides in elements, multiples of 16 bytes, >= 0).
  *   k, v: with k_scales NULL, bf16 rows as in cp_attn_partial.  Otherwise e4m3
  *     codes with the strides in bytes and the scales of cp_kv_codes_t (k_scales,
- *     v_scales; one scale_stride for both).  (d, dv): (64, 64) and (128, 128).
+ *     v_scales; one scale_stride for both; powers of two, as cp_kv_quantize writes).  (d, dv): (64, 64) and (128, 128).
  *     Key and value rows outside the segments' runs, or past num_kv_rows, may hold
  *     anything; a value row that some row of a tile sees must be finite for the
  *     others.
  *   o: [num_q_rows, Hq, dv] contiguous, bf16 or fp32; lse: fp32 [num_q_rows, Hq].
  *   workspace: device, 32-byte aligned, at least cp_shared_workspace_size bytes;
  *     overwritten; not to be shared by calls that may run at the same time.
- * P is rounded to bf16 for the second product, as in cp_attn_partial.  One or two
- * launches (the merge only where plan->needs_merge), no order of atomics: the
- * same call gives the same bits.  num_kv_rows < plan->kv_rows:
+ * P is rounded to bf16 for the second product, as in cp_attn_partial, and with codes
+ * to f16.  Codes enter the products exactly where the scales of 128 consecutive keys
+ * of a run (for V: of a run) are within 2^15 of the largest; what a row further below
+ * loses is under 2^-33 of the largest element.
+ * Two launches (the attention and the merge of the partial results), no order of
+ * atomics: the same call gives the same bits.  num_kv_rows < plan->kv_rows:
  * CPATTN_ERR_INVALID_ARG.  A table that does not match the plan sets
- * CPATTN_ERR_RANGE and what it spoils is skipped. */
+ * CPATTN_ERR_RANGE and what it spoils is skipped; a wait inside the attention that
+ * runs out sets CPATTN_ERR_TIMEOUT.  With either, o and lse are not to be used. */
 int cp_attn_shared(const cp_shared_plan_t* plan, const int32_t* table_dev, const void* q,
                    int64_t q_row_stride, int64_t q_head_stride, const void* k,
                    int64_t k_row_stride, int64_t k_head_stride, const float* k_scales,

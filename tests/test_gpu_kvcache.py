@@ -131,6 +131,35 @@ def test_strided_rows_and_cache():
     assert (scales[:, :, 64:] == 0).all()
 
 
+def test_one_row_or_head_of_any_stride():
+    """The stride of a dimension of one entry means nothing."""
+    x = draw(5, 3, 3, 64, torch.bfloat16).reshape(-1)
+    for shape, strides in (((1, 2, 64), (7, 64, 1)), ((3, 1, 64), (64, 3, 1)), ((1, 1, 64), (1, 1, 1))):
+        k = torch.as_strided(x, shape, strides)
+        cache = cpa.alloc_kv_cache(shape[0], shape[1], 64, 64)
+        cpa.cp_kv_quantize(cache, k, k)
+        want, want_s = osh.kv_quantize(f64(k))
+        assert (f64(cache.k) == want).all() and (f64(cache.v_scale) == want_s).all()
+
+
+def test_cache_without_rows():
+    cache = cpa.alloc_kv_cache(0, 2, 64, 64)
+    none = torch.empty((0, 2, 64), dtype=torch.bfloat16, device="cuda")
+    cpa.cp_kv_quantize(cache, none, none)
+    k, v = cpa.cp_kv_dequantize(cache)
+    assert k.shape == v.shape == (0, 2, 64)
+    status = cpa.new_status()
+    one = torch.ones((1, 2, 64), dtype=torch.bfloat16, device="cuda")
+    cpa.cp_kv_quantize(cache, one, one, status=status)
+    assert int(status.item()) == L.ERR_RANGE
+    skip = torch.full((1,), -1, dtype=torch.int32, device="cuda")
+    status = cpa.new_status()
+    cpa.cp_kv_quantize(cache, one, one, skip, status=status)
+    cpa.cp_kv_dequantize(cache, skip, out_k=one, out_v=one.clone(), status=status)
+    cpa.check_status(status)
+    assert (one == 1).all()
+
+
 def test_index_out_of_range_is_reported_and_skipped():
     cache = cpa.alloc_kv_cache(8, 2, 64, 64)
     x = draw(1, 3, 2, 64, torch.bfloat16)

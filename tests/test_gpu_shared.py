@@ -139,6 +139,53 @@ def test_rows_outside_the_runs_hold_anything(d, quant):
     check(o, lse, ref, d, 330)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_scales_of_many_sizes(d):
+    """Cache rows whose scales differ by up to 2^15 lose nothing in the products, in
+    units of every kind (4 to 256 packed rows)."""
+    Hq, Hkv = 8, 2
+    q_lens, own, prefix = [1, 3, 9, 30, 70], [50, 300, 129, 31, 190], 500
+    N, rows = sum(q_lens), 1200
+    g = torch.Generator(device="cuda").manual_seed(d)
+    q = torch.randn(N, Hq, d, generator=g, device="cuda").bfloat16()
+    cache = cpa.alloc_kv_cache(rows, Hkv, d, d)
+    x = [torch.randn(rows, Hkv, d, generator=g, device="cuda") *
+         torch.exp2(torch.randint(-12, 2, (rows, Hkv, 1), generator=g, device="cuda").float())
+         for _ in range(2)]
+    cpa.cp_kv_quantize(cache, *x)
+    for s in (cache.k_scale, cache.v_scale):
+        assert 2.0 ** 13 <= (s.max() / s.min()).item() <= 2.0 ** 15
+    kd, vd = cpa.cp_kv_dequantize(cache, out_fp32=True)
+    plan = cpa.make_shared_plan(q_lens, own, prefix, Hq, Hkv)
+    ref = osh.shared_attention(f64(q), f64(kd), f64(vd), plan.segs_host.tolist(), 0.3)
+    o, lse, _ = cpa.cp_attn_shared(plan, q, cache.k, cache.v, 0.3, k_scale=cache.k_scale,
+                                   v_scale=cache.v_scale, out_fp32=True)
+    check(o, lse, ref, d, prefix + max(own))
+
+
+@pytest.mark.parametrize("quant", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("tokens", [1, 9, 64])
+def test_many_small_weights(tokens, quant):
+    """One key has most of the weight and a value of zero; the others' weights, 2^-18.4
+    of it each, make the output (an f16 weight would be subnormal there).  One block to
+    a KV head, so that the run is not cut."""
+    Hq, Hkv, d, keys = 8, 2, 128, 20000
+    q = torch.ones(tokens, Hq, d, dtype=torch.bfloat16, device="cuda")
+    k = torch.zeros(keys, Hkv, d, dtype=torch.bfloat16, device="cuda")
+    v = torch.ones_like(k)
+    k[77], v[77] = 1.0, 0.0
+    kw, k64, v64 = {}, f64(k), f64(v)
+    if quant:
+        cache = cpa.alloc_kv_cache(keys, Hkv, d, d)
+        cpa.cp_kv_quantize(cache, k, v)
+        k, v, kw = cache.k, cache.v, dict(k_scale=cache.k_scale, v_scale=cache.v_scale)
+    scale = 18.4 * np.log(2.0) / d
+    plan = cpa.make_shared_plan([1] * tokens, [0] * tokens, keys, Hq, Hkv, num_ctas=2)
+    ref = osh.shared_attention(f64(q), k64, v64, plan.segs_host.tolist(), scale)
+    o, lse, _ = cpa.cp_attn_shared(plan, q, k, v, scale, **kw, out_fp32=True)
+    check(o, lse, ref, d, keys)
+
+
 def test_nan_in_a_visible_key_reaches_its_rows_only():
     """A NaN among one request's own keys spoils that request and no other."""
     for quant in (False, True):

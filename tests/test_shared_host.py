@@ -111,7 +111,6 @@ def test_plan_empty_batches():
                     ([[0, 2, -4, 1, 0, 0, 0, 0]], 2)):
         plan, T = check_plan(segs, N, 8, 2, 152)
         assert plan.info.num_pieces == 0
-    assert plan.info.needs_merge == 1  # rows without a key get O = 0, L = -inf
 
 
 def test_plan_shares_are_even():
