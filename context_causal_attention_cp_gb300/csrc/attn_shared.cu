@@ -101,6 +101,12 @@ struct SharedCfg {
   static constexpr int kTmemCols = 512;  // S of each stream, then O of each
 };
 
+// Orders this thread's shared-memory accesses before later ones of the async proxy (TMA,
+// tcgen05.mma reading shared memory).
+__device__ __forceinline__ void fence_async_shared() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
 // What the producer tells the converters about a raw tile.
 struct RawNote {
   static constexpr int kNoteV = 8;
