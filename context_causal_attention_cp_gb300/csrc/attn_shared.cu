@@ -171,7 +171,7 @@ __device__ __forceinline__ SharedCta load_cta(const SharedParams& p) {
 // Checks every piece of this block's list against the buffers: the roles below walk
 // the list on their own and rely on it.  tiles[s]: KV tiles of stream s's single units
 // (zeroed by the caller before a barrier).  All threads call it; false (and
-// CPATTN_ERR_RANGE) when the list cannot be run.  It is a barrier, too.
+// CPATTN_ERR_RANGE) when the list cannot be run.
 __device__ __forceinline__ bool check_list(const SharedParams& p, const SharedCta& c, int* tiles) {
   bool ok = c.dual0 >= 0 && c.dual0 <= c.dual1 && c.dual1 <= p.num_pieces && c.single0 >= 0 &&
             c.single0 <= c.single1 && c.single1 <= c.single2 && c.single2 <= p.num_pieces &&
@@ -189,7 +189,7 @@ __device__ __forceinline__ bool check_list(const SharedParams& p, const SharedCt
     }
   }
   ok = __syncthreads_and(ok);
-  // (a small list has no single units and no tiles)
+  // (not for a list of small units: their path goes on to lay out this memory otherwise)
   if (ok && c.single0 < c.single2) ok = tiles[0] == tiles[1] || tiles[0] == tiles[1] + 1;
   if (!ok && threadIdx.x == 0) set_status(p.status, CPATTN_ERR_RANGE);
   return ok;
@@ -298,9 +298,9 @@ constexpr uint32_t idesc_16bit_f32(bool f16, int M, int N, int b_mn) {
   return idesc_bf16_f32(M, N, 0, b_mn) & ~(f16 ? (1u << 7) | (1u << 10) : 0u);
 }
 
-// f16 weights are 2^kF16Lift times those of the maximum that they are taken by: an f16
-// below 2^-14 loses bits, which now begins at 2^-21 of the largest weight (and ends the
-// weight at 2^-32), and kF16Lift + kMaxSlack stays below 2^16.
+// f16 weights are taken by a maximum that is kF16Lift too small: an f16 below 2^-14 loses
+// bits, which now begins at 2^-21 of the largest weight (and ends the weight at 2^-32),
+// and the largest stays below 2^16.
 constexpr float kF16Lift = 7.f;
 static_assert(kF16Lift + kMaxSlack < 16.f, "f16 range");
 
@@ -335,15 +335,14 @@ __device__ __forceinline__ void softmax_tile(uint32_t s_addr, uint32_t o_addr, i
   }
   mx0 = fmax3(mx0, x[BN - 4], x[BN - 3]);
   mx1 = fmax3(mx1, x[BN - 2], x[BN - 1]);
-  const float mx = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)) * sl2;
+  const float mx = fmaf(fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)), sl2, QUANT ? -kF16Lift : 0.f);
   // The maximum moves only when a tile raises it by more than kMaxSlack (log2
   // units): exponentials stay below 2^kMaxSlack, l uses the same maximum, and O in
   // TMEM is rescaled only then.
   const bool move = mx > m_run + kMaxSlack;
   const float m_new = move ? mx : m_run;
-  const float m_num = (m_new == -INFINITY) ? 0.f : m_new;
-  const float alpha = move ? ex2_approx(m_run - m_num) : 1.f;
-  const float m_new_use = QUANT ? m_num - kF16Lift : m_num;
+  const float m_new_use = (m_new == -INFINITY) ? 0.f : m_new;
+  const float alpha = move ? ex2_approx(m_run - m_new_use) : 1.f;
   float sum0 = 0.f, sum1 = 0.f;
 #pragma unroll
   for (int q = 0; q < BN / 32; ++q) {
@@ -441,10 +440,12 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
   if (threadIdx.x < 2) stream_tiles[threadIdx.x] = 0;
   __syncthreads();
   if (list.dual0 == list.dual1 && list.single0 == list.single2 && list.small0 == list.small1) return;  // no work
+  if (!check_list(p, list, stream_tiles)) return;
   if (list.small0 < list.small1) {
     run_small<D, QUANT>(p, list, smem, &tm_k, &tm_v, &tm_k_tail, &tm_v_tail);
     return;
   }
+  const int steps = stream_tiles[0] + stream_tiles[1];  // of the single units
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kStages; ++i) {
       for (int u = 0; u < 3; ++u) mbar_init(full + u * C::kStages + i, QUANT ? kConvertThreads : 1);
@@ -471,15 +472,9 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     tmem_relinquish();
   }
   tc_fence_before();
-  const bool runs = check_list(p, list, stream_tiles);
+  __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  if (!runs) {
-    __syncthreads();
-    if (warp == kProducerWarp) tmem_dealloc(tmem_base, C::kTmemCols);
-    return;
-  }
-  const int steps = stream_tiles[0] + stream_tiles[1];  // of the single units
   const uint32_t q_base = smem_u32(smem);
   const uint32_t ring_base = smem_u32(smem + C::kRingOff);
   // A ring slot has a full barrier for each user (stream 0, stream 1, both), so that

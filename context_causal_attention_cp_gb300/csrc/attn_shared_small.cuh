@@ -325,11 +325,11 @@ __device__ __forceinline__ bool small_piece(const SharedParams& p, const SmallWa
         mx = fmaxf(mx, __shfl_xor_sync(all, mx, 4));
         mx = fmaxf(mx, __shfl_xor_sync(all, mx, 8));
         mx = fmaxf(mx, __shfl_xor_sync(all, mx, 16));
+        if (QUANT) mx -= kF16Lift;
         const bool move = mx > m_run[e] + kMaxSlack;
         const float m_new = move ? mx : m_run[e];
-        const float m_num = m_new == -INFINITY ? 0.f : m_new;
-        const float use = QUANT ? m_num - kF16Lift : m_num;
-        alpha[e] = move ? ex2_approx(m_run[e] - m_num) : 1.f;
+        const float use = m_new == -INFINITY ? 0.f : m_new;
+        alpha[e] = move ? ex2_approx(m_run[e] - use) : 1.f;
         any = any || move;
         m_run[e] = m_new;
         m_use[e] = use;
@@ -501,7 +501,7 @@ __device__ __forceinline__ void run_small(const SharedParams& p, const SharedCta
     *issued_loads = 0;
     fence_barrier_init();
   }
-  if (!check_list(p, list, nullptr)) return;
+  __syncthreads();
   auto arrive_copies = [&](uint64_t* bar) {  // when this lane's copies so far have landed
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
   };
