@@ -733,8 +733,7 @@ def _vector(t, name, dtype, n, index):
     """Check an optional contiguous 1-D argument of at least n entries; its address."""
     if t is None:
         return None
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype is not dtype or \
-            t.get_device() != index:
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != index:
         _bad(t, name, dtype, index)
     if t.dim() != 1 or t.shape[0] < n or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous, 1-D, with at least {n} entries")
@@ -817,8 +816,7 @@ def alloc_kv_cache(rows, Hkv, d, dv=None, device="cuda") -> KVCache:
 
 
 def _new_rows(x, name, dtype, n, Hkv, dim, index):
-    if not isinstance(x, torch.Tensor) or not x.is_cuda or x.dtype is not dtype or \
-            x.get_device() != index:
+    if not isinstance(x, torch.Tensor) or x.dtype is not dtype or x.get_device() != index:
         _bad(x, name, dtype, index)
     if x.shape != (n, Hkv, dim):
         raise ValueError(f"{name} must be [{n}, {Hkv}, {dim}], got {tuple(x.shape)}")
@@ -998,17 +996,17 @@ def cp_attn_shared(plan: SharedPlan, q, k, v, scale, *, k_scale=None, v_scale=No
         raise ValueError("k_scale and v_scale go together")
     kv_dtype = torch.float8_e4m3fn if quant else torch.bfloat16
     for t, name, dtype in ((q, "q", torch.bfloat16), (k, "k", kv_dtype), (v, "v", kv_dtype)):
-        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype is not dtype or \
-                t.get_device() != index:
+        if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != index:
             _bad(t, name, dtype, index)
-    if q.dim() != 3 or k.dim() != 3 or v.dim() != 3:
+    qs, kshape, vshape = q.shape, k.shape, v.shape
+    if len(qs) != 3 or len(kshape) != 3 or len(vshape) != 3:
         raise ValueError("q, k and v are [rows, heads, dim]")
-    rows, d, dv = v.shape[0], q.shape[2], v.shape[2]
-    if q.shape != (N, Hq, d):
-        raise ValueError(f"the plan is for q [{N}, {Hq}, d], got {tuple(q.shape)}")
-    if k.shape != (rows, Hkv, d) or v.shape != (rows, Hkv, dv):
+    rows, d, dv = vshape[0], qs[2], vshape[2]
+    if qs[0] != N or qs[1] != Hq:
+        raise ValueError(f"the plan is for q [{N}, {Hq}, d], got {tuple(qs)}")
+    if kshape != (rows, Hkv, d) or vshape[1] != Hkv:
         raise ValueError(f"k and v must be [rows, {Hkv}, dim] of equal rows and k's dim q's, got "
-                         f"{tuple(k.shape)} and {tuple(v.shape)}")
+                         f"{tuple(kshape)} and {tuple(vshape)}")
     (qrs, qhs, qcs), (krs, khs, kcs), (vrs, vhs, vcs) = q.stride(), k.stride(), v.stride()
     if (qcs != 1 and N) or ((kcs != 1 or vcs != 1) and rows):
         raise ValueError("q, k and v need a contiguous last dim")
@@ -1025,8 +1023,8 @@ def cp_attn_shared(plan: SharedPlan, q, k, v, scale, *, k_scale=None, v_scale=No
     scale_stride = 0
     if quant:
         for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-            if not isinstance(t, torch.Tensor) or not t.is_cuda or \
-                    t.dtype is not torch.float32 or t.get_device() != index:
+            if not isinstance(t, torch.Tensor) or t.dtype is not torch.float32 or \
+                    t.get_device() != index:
                 _bad(t, name, torch.float32, index)
             if t.shape != (Hkv, rows) or (t.stride(1) != 1 and rows > 1):
                 raise ValueError(f"{name} must be [{Hkv}, {rows}] with a contiguous last dim")
@@ -1040,9 +1038,9 @@ def cp_attn_shared(plan: SharedPlan, q, k, v, scale, *, k_scale=None, v_scale=No
     if lse is None:
         lse = torch.empty((N, Hq), dtype=torch.float32, device=q.device)
     f32 = out.dtype is torch.float32
-    if not out.is_cuda or not (f32 or out.dtype is torch.bfloat16) or out.get_device() != index:
+    if not (f32 or out.dtype is torch.bfloat16) or out.get_device() != index:
         _bad(out, "out", (torch.bfloat16, torch.float32), index)
-    if not lse.is_cuda or lse.dtype is not torch.float32 or lse.get_device() != index:
+    if lse.dtype is not torch.float32 or lse.get_device() != index:
         _bad(lse, "lse", torch.float32, index)
     if out.shape != (N, Hq, dv) or lse.shape != (N, Hq):
         raise ValueError(f"out must be [{N}, {Hq}, {dv}] and lse [{N}, {Hq}]")
