@@ -22,7 +22,15 @@
 //                of tensor work.
 //   warps 12-15  (e4m3 cache) codes to f16 tiles.
 // A unit of two MMA tiles (dual) gives both streams every KV tile; the pieces of
-// smaller units belong to one stream each, and the streams' KV tiles alternate.
+// units of one tile (single) belong to one stream each, and the streams' KV tiles
+// alternate.  Blocks with units of up to 8 rows (small) run attn_shared_small.cuh.
+//
+// What bounds it: dual units the chain S -> softmax -> P -> P V of a stream, 3600 cycles
+// a KV tile of which the two streams' MMAs hold 3000 (256 tokens of 32 heads on a 64K
+// prefix, d = 128: 216 us a call in bf16, 1.27 PFLOP/s, 0.65 of cuBLAS; 272 us over
+// codes, whose way through shared memory is half as long again).  Measured and not
+// kept: P in two halves, turns before the last MMA, MMAs issued by whole warps, eight
+// converter warps, a first tile over nothing that brings the code in.
 //
 // e4m3 cache: both products run in f16, which holds a code exactly and takes two
 // instructions for two codes (bf16 takes 6.5, more than a step has issue slots
@@ -73,6 +81,7 @@ struct SharedParams {
   float* ws_l;  // log2 units
   int32_t* status;
   unsigned long long timeout_ns;
+  int withhold_q;  // test hook: queries are never published (see cp_attn_debug)
 };
 
 template <int D, bool QUANT>
@@ -223,7 +232,7 @@ struct RingTile {
 };
 // Calls f(tile) for the K and V tiles of a list in the order in which the MMA warps
 // use them, until it returns false: K0 V0 K1 V1 ... for dual units, then K0 K1 V0
-// K2 V1 ... for the steps of the small units, step n being the next KV tile of
+// K2 V1 ... for the steps of the single units, step n being the next KV tile of
 // stream n & 1.
 template <class F>
 __device__ __forceinline__ bool for_each_ring_tile(const SharedParams& p, const SharedCta& c,
@@ -481,7 +490,7 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
   // every waiter sees all phases of the barriers it waits on; their parities are kept
   // as bits of a word, `user * kStages + slot`.
   auto full_bit = [](int user, int slot) { return user * C::kStages + slot; };
-  // Ring places of step n of the small units, behind dual_seq places of dual units.
+  // Ring places of step n of the single units, behind dual_seq places of dual units.
   auto k_place = [](int n) { return n == 0 ? 0 : 2 * n - 1; };
   auto v_place = [&](int n) { return n == steps - 1 ? 2 * n + 1 : 2 * n + 2; };
 
@@ -630,7 +639,7 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
         bool dual = i < list.dual1;
         if (!dual) i = s ? list.single1 : list.single0;
         int dual_seq = 0;    // ring places of the dual tiles so far
-        int n = s;           // step of the small units
+        int n = s;           // step of the single units
         int step = 0, pieces = 0;
         bool ok = true;
         int left = 0;        // KV tiles of the current piece behind the one in S
@@ -857,7 +866,7 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
         }
       }
       fence_async_shared();
-      mbar_arrive(q_full + s);
+      if (!p.withhold_q) mbar_arrive(q_full + s);
       return factor;
     };
     // the stream's pieces: the dual ones, then its own
@@ -1334,6 +1343,7 @@ extern "C" int cp_attn_shared(const cp_shared_plan_t* plan, const int32_t* table
   p.ws_l = p.ws_o + plan->ws_rows * dv;
   p.status = status_dev;
   p.timeout_ns = attn_debug().timeout_ns;
+  p.withhold_q = attn_debug().withhold_q;
   if (plan->num_pieces > 0) {
     SharedMaps m;
     auto map = [&](CUtensorMap* t, const void* base, int dim, int64_t hs, int64_t rs, int box_rows) {

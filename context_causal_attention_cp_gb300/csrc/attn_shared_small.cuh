@@ -12,6 +12,14 @@
 // of them ahead across piece ends.  A warp's step issues the products of the next tile's
 // keys between the softmax and the second product of this one.
 //
+// What bounds it: HBM in bf16 (256 tokens with 1024 keys each: 166 us, 6.5 TB/s, 0.96 of a
+// copy), the instructions that decode in e4m3 (133 us, 4.5 TB/s).  A piece costs 1.1 us
+// (e4m3 1.4) besides its tiles.  Queries as the MMAs' 16 rows take twice the MMAs and
+// registers: 1.0 -> 1.2 us a KV tile where HBM does not bind (e4m3 1.1 -> 1.4).  Two teams
+// of four warps on pieces of their own leave each half the ring (slower by a third), and
+// a next piece's queries and first product before the last step of this one help short
+// pieces (140 us for 1024 of 128 keys instead of 152) and cost long ones more.
+//
 // Fragments are loaded as they lie in memory.  K Q^T sums over d in any order, so lane
 // (g = lane / 4, c = lane % 4) takes whole 16-byte chunks of key rows g and g + 8 and of
 // query row g the same ones: a chunk's elements 4x .. 4x+3 are its share of one k-step.
@@ -528,7 +536,7 @@ __device__ __forceinline__ void run_small(const SharedParams& p, const SharedCta
                        "l"(src)
                        : "memory");
         }
-        arrive_copies(q_full + qb);
+        if (!p.withhold_q) arrive_copies(q_full + qb);
         for (int u = 0; u < 2 * num_tiles(pc.keys); ++u, ++seq) {  // K0 V0 K1 V1 ...
           const int slot = seq % NS, t = u >> 1, row = pc.kv_row + t * BN, live = pc.keys - t * BN;
           const bool is_v = u & 1;

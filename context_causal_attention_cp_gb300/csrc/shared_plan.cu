@@ -2,9 +2,8 @@
 //
 // The units (segment, packed-row tile, KV head), kind by kind, are walked in a
 // fixed order and their keys dealt to the thread blocks one after the other: each
-// block is filled up to a budget, so a unit is cut only where a block is full, and
-// every block's cost is within a KV tile of the others' (a block with small units has
-// no others).  The smallest budget that needs no more than num_ctas blocks is found by
+// block is filled up to a budget, so a unit is cut only where a block is full (a block
+// with small units has no others).  The smallest budget that needs no more than num_ctas blocks is found by
 // bisection.  A piece costs its KV tiles plus a fixed part (its queries' load and its
 // partial's store), so that short units are not shredded.  A block's run of single
 // units is cut once more, at half its KV tiles, between the block's two streams.
@@ -109,7 +108,7 @@ void settle(const Line& L, Place& p) {
 constexpr int kAlignBlocks = 8;
 bool begins_block(const Line& L, const Place& p, long long budget) {
   return p.kind == 0 && p.tile > 0 && p.head == 0 && p.key0 == 0 &&
-         L.Hkv * kv_tiles(p.keys) * tile_cost(p.rows) >= kAlignBlocks * budget;
+         L.Hkv * kv_tiles(p.keys) * tile_cost(p.rows) / kAlignBlocks >= budget;
 }
 // One thread block's share: calls f(cut) for each of its pieces.
 template <class F>

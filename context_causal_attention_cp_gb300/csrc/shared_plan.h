@@ -44,7 +44,7 @@ static_assert(sizeof(SharedCta) == 32, "two 16-byte words");
 
 constexpr int kSharedTileRows = 128;  // packed rows of one MMA tile
 constexpr int kSharedTileKeys = 128;  // keys of one KV tile
-constexpr int kSharedSmallRows = 8;   // packed rows of one warp-level MMA
+constexpr int kSharedSmallRows = 8;   // packed rows of one warp-level MMA's columns
 __host__ __device__ constexpr bool shared_dual(int rows) { return rows > kSharedTileRows; }
 __host__ __device__ constexpr int shared_kind(int rows) {  // 0 dual, 1 single, 2 small
   return shared_dual(rows) ? 0 : rows > kSharedSmallRows ? 1 : 2;

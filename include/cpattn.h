@@ -656,7 +656,8 @@ int cp_attn_shared(const cp_shared_plan_t* plan, const int32_t* table_dev, const
  *     load, so the MMA thread's wait on it runs out: the kernel then writes
  *     CPATTN_ERR_TIMEOUT to the status word, drains its own copies, frees its
  *     tensor memory and returns (outputs of the affected tiles are not
- *     written).  Nothing traps and no wait is unbounded.  Reset to 0 after use.
+ *     written).  Nothing traps and no wait is unbounded.  cp_attn_shared loads the
+ *     queries and never publishes them, to the same end.  Reset to 0 after use.
  *   CPATTN_DEBUG_NVTX: value != 0 turns on NVTX ranges named after each entry
  *     point that queues device work (pushed for the host call's duration, for
  *     timeline tools); 0 turns them off.  Off by default unless the

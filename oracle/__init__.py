@@ -27,6 +27,8 @@ Modules:
                   the pass-Q ring (hop-by-hop merge into a carried accumulator)
     select     -- the pass-KV / pass-Q choice (message sizes; fitted heuristic;
                   the roofline cost rule)
+    shared     -- the e4m3 cache's quantisation; attention over the union of the key
+                  runs of a segment table (shared prefixes)
 
 Readings where the pages are silent:
     R1 remainder tokens of a zigzag split go one each to blocks 0..rem-1;

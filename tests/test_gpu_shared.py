@@ -350,6 +350,34 @@ def test_table_that_does_not_match_is_reported():
         assert int(status.item()) == L.ERR_RANGE, (at, value)
 
 
+@pytest.mark.parametrize("quant", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("tokens", [1, 8, 64])
+def test_a_wait_that_runs_out_is_reported(tokens, quant):
+    """With the queries never published, the waits on them run out in units of every
+    kind: the kernel reports it and drains its copies, and the same call is right
+    afterwards."""
+    lib = L.load()
+    Hq, Hkv, d = 8, 2, 128
+    q, k, v, scales, k64, v64 = make(9, tokens, 3000, Hq, Hkv, d, quant)
+    plan = cpa.make_shared_plan([1] * tokens, [0] * tokens, 3000, Hq, Hkv, num_ctas=7)
+    status = cpa.new_status()
+    call = lambda: cpa.cp_attn_shared(plan, q, k, v, 0.1, status=status, **scales)  # noqa: E731
+    assert lib.cp_attn_debug(L.DEBUG_WAIT_LIMIT_NS, 20_000_000) == L.OK
+    assert lib.cp_attn_debug(L.DEBUG_WITHHOLD_Q, 1) == L.OK
+    try:
+        call()
+        torch.cuda.synchronize()
+        assert int(status.item()) == L.ERR_TIMEOUT
+    finally:
+        lib.cp_attn_debug(L.DEBUG_WITHHOLD_Q, 0)
+        lib.cp_attn_debug(L.DEBUG_WAIT_LIMIT_NS, 4_000_000_000)
+    status.zero_()
+    o, lse, _ = call()
+    cpa.check_status(status, "after the timeout")
+    ref = osh.shared_attention(f64(q), k64, v64, plan.segs_host.tolist(), 0.1)
+    check(o, lse, ref, d, 3000)
+
+
 def test_refusals_of_the_binding():
     q, k, v, scales, _, _ = make(12, 2, 300, 8, 2, 128, True)
     plan = cpa.make_shared_plan([1, 1], [10, 20], 200, 8, 2)
