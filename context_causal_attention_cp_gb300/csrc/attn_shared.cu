@@ -1024,7 +1024,9 @@ template <int D, int J>
 struct MergeCfg {
   static constexpr int kLanes = 2 * J;                                 // of a chunk's J rows
   static constexpr int kVec = D * J / 128 > 0 ? D * J / 128 : 1;       // 16-byte loads of a partial
-  static constexpr int kLoads = 8 / kVec;  // partials of a warp whose O loads are in flight together
+  // partials of a warp whose O loads are in flight together (12 or 16 vectors cost J = 4
+  // more in registers than they gain)
+  static constexpr int kLoads = (J == 1 ? 16 : 8) / kVec;
 };
 
 template <int V>
@@ -1206,12 +1208,16 @@ __global__ void __launch_bounds__(kMergeThreads) shared_merge_kernel(const Share
 }
 
 // Warps for a row's J heads: enough that a warp loads its partials in two goes (their
-// average is ws_rows / rows), e.g. 152 partials a row at one token on a 256K prefix.
+// average is ws_rows / rows), e.g. 152 partials a row at one token on a 256K prefix, but
+// no more than let all blocks reside at once (two to an SM): a block takes 5 us, mostly
+// for its chain of loads, and a second wave of them as much again.
+constexpr int kMergeResident = 2 * 152;
 template <int D, int J>
 int launch_merge(const SharedParams& p, bool behind, cudaStream_t stream) {
   const long long rows = (long long)p.num_q_rows * p.Hq;
   int ways = 1;
   while (ways < kMergeWarps && p.ws_rows > rows * ways * 2 * MergeCfg<D, J>::kLoads) ways *= 2;
+  while (ways > 1 && rows / J * ways > (long long)kMergeResident * kMergeWarps) ways /= 2;
   const long long blocks = (rows / J * ways + kMergeWarps - 1) / kMergeWarps;
   if (blocks > 0x7fffffffLL) return CPATTN_ERR_TOO_LARGE;
   const cudaError_t e = launch_kernel(shared_merge_kernel<D, J>, (unsigned)blocks, kMergeThreads, 0, stream,
