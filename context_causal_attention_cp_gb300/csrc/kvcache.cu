@@ -6,8 +6,8 @@
 // are HBM streams: a vector is read once, kept in registers between the maximum
 // and the rounding, and its codes are written once.  L = 2^k lanes share a vector,
 // 8 elements each and step, so that a load or store of a step has no gaps (16 elements
-// left every store two passes over its lines: 32768 rows read back in 45 us instead of
-// 38).  L is the smallest that leaves a lane at most four steps: with L twice or four
+// left every store two passes over its lines: 32768 rows of 16 vectors of 128 read back
+// in 45 us; now 36).  L is the smallest that leaves a lane at most four steps: with L twice or four
 // times that, the shuffles of the maximum and the walk over rows cost more (8192 rows
 // of 16 vectors of 128: 12 us, 15 and 21).  A thread works on kUnroll rows at once, so
 // that their loads travel together; which row, side and head it has is settled once,
@@ -25,6 +25,7 @@ namespace cpattn {
 namespace {
 
 constexpr int kKvThreads = 256;
+constexpr int kWriteBlocks = 4, kReadBlocks = 5;  // resident on an SM
 constexpr int kMaxDim = 1024;
 constexpr int kMinExp = -117, kMaxExp = 119;
 
@@ -202,10 +203,10 @@ kv_quantize_kernel(const KvSide k, const KvSide v, int sides, int num_rows, int 
 }
 
 template <bool F32, int NC>
-__global__ void __launch_bounds__(kKvThreads)
+__global__ void __launch_bounds__(kKvThreads, kReadBlocks)
 kv_dequantize_kernel(const KvSide k, const KvSide v, int sides, int num_rows, int Hkv, int log_l,
                      const int32_t* __restrict__ idx, int cache_rows, int32_t* status) {
-  constexpr int kUnroll = NC == 1 ? 8 : NC == 2 ? 4 : 2;
+  constexpr int kUnroll = NC == 1 ? 4 : NC == 2 ? 2 : 1;
   const int L = 1 << log_l, lpr = (sides * Hkv) << log_l;
   const KvPlace pl = kv_place(lpr);
   if (!pl.on) return;
@@ -297,7 +298,8 @@ int cache_side(const cp_kv_codes_t* c, int dim, int Hkv, int cache_rows, KvSide*
 
 // Lanes of a vector (log2) and blocks of a launch: enough for the rows, and at most as
 // many as reside at once, the rest of the rows being the loop's (16 per SM, in turn:
-// 8192 rows written in 14 us instead of 12, 32768 read in 41 instead of 38).
+// 8192 rows written in 14 us instead of 12).  Reading, five blocks that hold half as many
+// rows each in flight beat four (36.5 and 38 us for 32768 rows).
 struct KvShape {
   int log_l, chunks;
   unsigned grid;
@@ -343,7 +345,7 @@ extern "C" int cp_kv_quantize(const void* k, int64_t k_row_stride, int64_t k_hea
   vs.x_row = v_row_stride;
   vs.x_head = v_head_stride;
   const int sides = v ? 2 : 1;
-  const KvShape sh = kv_shape(num_rows, sides * Hkv, std::max(d, v ? dv : 0), 4);
+  const KvShape sh = kv_shape(num_rows, sides * Hkv, std::max(d, v ? dv : 0), kWriteBlocks);
   decltype(&kv_quantize_kernel<true, 1>) const kerns[2][4] = {
       {kv_quantize_kernel<false, 1>, kv_quantize_kernel<false, 2>, kv_quantize_kernel<false, 3>,
        kv_quantize_kernel<false, 4>},
@@ -371,7 +373,7 @@ extern "C" int cp_kv_dequantize(const cp_kv_codes_t* k_cache, const cp_kv_codes_
   ks.out = k_out;
   vs.out = v_out;
   const int sides = v_cache ? 2 : 1;
-  const KvShape sh = kv_shape(num_rows, sides * Hkv, std::max(d, v_cache ? dv : 0), 6);
+  const KvShape sh = kv_shape(num_rows, sides * Hkv, std::max(d, v_cache ? dv : 0), kReadBlocks);
   decltype(&kv_dequantize_kernel<true, 1>) const kerns[2][4] = {
       {kv_dequantize_kernel<false, 1>, kv_dequantize_kernel<false, 2>, kv_dequantize_kernel<false, 3>,
        kv_dequantize_kernel<false, 4>},
