@@ -36,7 +36,7 @@
 // instructions for two codes (bf16 takes 6.5, more than a step has issue slots
 // for).  K row r enters as code * 2^(e_r - E), E the tile's largest e, and 2^E goes
 // into the scores' factor: what a row far below the tile's largest loses is below
-// 2^-33 of that largest, less than an fp32 score resolves.  V the same with E the
+// 2^-32 of that largest, less than an fp32 score resolves.  V the same with E the
 // largest e that the stream has met in the piece; O is rescaled when that grows.  A
 // query row enters as f16 times the power of two that brings its largest element to
 // [2^14, 2^15), so that elements down to 2^-30 of it keep bf16's 8 bits.  P in f16 is
