@@ -686,18 +686,22 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
           mma_commit(empty + k_slot);
           if (!next_dual) mbar_arrive(empty + k_slot);  // the other stream does not use the tile
         };
+        // Bursts by turns: for dual units, and for single ones when each stream has one
+        // piece (they have as many KV tiles, or stream 0 one more; 8 tokens on a 128K
+        // prefix 112 -> 108 us).  With several, a stream would wait for the other's ends.
+        const bool one_each = list.single1 - list.single0 == 1 && list.single2 - list.single1 == 1;
         bool more = prepare();
         if (more) begin_step();
         while (more) {
           const int slot = v_slot;
-          const bool first = next_head, last = left == 0, both = next_dual;
+          const bool first = next_head, last = left == 0, both = next_dual, turns = both || one_each;
           ok = wait_tile(both ? 2 : s, slot);
-          if (ok && both && !last) more = prepare();
+          if (ok && turns && !last) more = prepare();
           ok = ok && wait_one(p_full + s, step & 1, abort_flag, p.timeout_ns);
-          // Dual units: the streams' bursts of MMAs alternate, so that each stream's
-          // softmax runs under the other's MMAs; without the turns the two fall into
-          // step and the tensor core idles during both softmaxes.
-          if (ok && both && (s == 1 || step > 0))
+          // The streams' bursts of MMAs alternate, so that each stream's softmax runs under
+          // the other's MMAs; without the turns the two fall into step and the tensor
+          // core idles during both softmaxes.
+          if (ok && turns && (s == 1 || step > 0))
             ok = wait_one(turn + s, (s == 1 ? step : step - 1) & 1, abort_flag, p.timeout_ns);
           if (!ok) break;
           tc_fence_after();
@@ -705,9 +709,9 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
           if (last) mma_commit(o_full + s);
           mma_commit(empty + slot);
           if (!both) mbar_arrive(empty + slot);
-          if (both && !last) begin_step();
-          if (both) mbar_arrive(turn + (s ^ 1));
-          if (!both || last) {
+          if (turns && !last) begin_step();
+          if (turns) mbar_arrive(turn + (s ^ 1));
+          if (!turns || last) {
             more = prepare();
             if (more) begin_step();
           }
