@@ -923,7 +923,10 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
           const volatile int2* e =
               tile_exp + (dual ? 4 + ((dual_seq / 2 + t) & 1) : 2 * s + ((step - dual_seq / 2) & 1));
           const int ek = e->x, ev_now = e->y;
-          sl2 *= exp2_int(ek);
+          // Not below a normal number: a zero row over zero keys would come to 0, and a
+          // masked -inf times 0 is NaN.  The raw scores are below 2^31 (2^15 448 d), so
+          // that a factor that is raised to 2^-126 still leaves scores of 0.
+          sl2 = fmaxf(sl2 * exp2_int(ek), 0x1p-126f);
           if (t > 0 && ev_now != ev) o_scale = exp2_int(max(ev - ev_now, -126));
           ev = ev_now;
         }
