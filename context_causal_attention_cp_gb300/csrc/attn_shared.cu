@@ -303,6 +303,13 @@ __device__ __forceinline__ float exp2_int(int e) {  // e in [-126, 127]
 __device__ __forceinline__ int exponent_of(float s) {
   return min(max((int)(__float_as_uint(s) >> 23) - 127, -126), 126);
 }
+// Factor f s of a raw e4m3 score, f > 0 of its query row and s of its key (or key tile).
+// Not below a normal number: a zero row over zero keys would come to 0, and a masked -inf
+// times 0 is NaN.  Not infinite: a score of 0 between orthogonal large rows stays 0.  A
+// raw score is below 2^31 (2^15 448 d), so that with a raised factor it is still nothing.
+__device__ __forceinline__ float score_factor(float f, float s) {
+  return fminf(fmaxf(f * s, 0x1p-126f), 0x1.fffffep127f);
+}
 constexpr uint32_t idesc_16bit_f32(bool f16, int M, int N, int b_mn) {
   return idesc_bf16_f32(M, N, 0, b_mn) & ~(f16 ? (1u << 7) | (1u << 10) : 0u);
 }
@@ -923,10 +930,7 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
           const volatile int2* e =
               tile_exp + (dual ? 4 + ((dual_seq / 2 + t) & 1) : 2 * s + ((step - dual_seq / 2) & 1));
           const int ek = e->x, ev_now = e->y;
-          // Not below a normal number: a zero row over zero keys would come to 0, and a
-          // masked -inf times 0 is NaN.  The raw scores are below 2^31 (2^15 448 d), so
-          // that a factor that is raised to 2^-126 still leaves scores of 0.
-          sl2 = fmaxf(sl2 * exp2_int(ek), 0x1p-126f);
+          sl2 = score_factor(sl2, exp2_int(ek));
           if (t > 0 && ev_now != ev) o_scale = exp2_int(max(ev - ev_now, -126));
           ev = ev_now;
         }

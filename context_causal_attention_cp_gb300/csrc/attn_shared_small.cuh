@@ -187,7 +187,8 @@ struct SmallK {
       }
     }
 #pragma unroll
-    for (int y = 0; y < 4; ++y) s[y] = (s[y] + s2[y]) * (factor[y & 1] * scale[y >> 1]);
+    for (int y = 0; y < 4; ++y)
+      s[y] = (s[y] + s2[y]) * (QUANT ? score_factor(factor[y & 1], scale[y >> 1]) : factor[y & 1]);
   }
 };
 

@@ -64,3 +64,17 @@ def test_zero_queries_and_zero_keys(d, quant, tokens):
         some[prefix:] = 0
         attend((q.float() * 2.0 ** -20).bfloat16(), some, v, quant, tokens, own, prefix, scale,
                "queries of 2^-20, a tile of zero keys")
+
+
+@KINDS
+@CACHES
+@DIMS
+def test_large_queries_orthogonal_to_large_keys(d, quant, tokens):
+    """Scores of 0 between queries of 2^100 and keys of 2^60, whose factor is above
+    fp32's range: the mean of V and L = ln n."""
+    prefix, own = 300, tokens + 37
+    q, k, v = draw(d, tokens, prefix + own, d)
+    q[:, :, : d // 2] = 0
+    k[:, :, d // 2:] = 0
+    attend((q.float() * 2.0 ** 100).bfloat16(), (k.float() * 2.0 ** 60).bfloat16(), v, quant,
+           tokens, own, prefix, d ** -0.5, "orthogonal")
