@@ -8,6 +8,10 @@ Layouts (see include/cpattn.h):
     q      bf16 [rows, Hq, d]          (cat rows: shard rows in rank order)
     k, v   bf16 [kv_rows, Hkv, d|dv]   (last dim contiguous; v may view k)
     o      bf16 or fp32 [rows, Hq, dv]; lse fp32 [rows, Hq] (natural log)
+
+``stream``: the call's work goes there (default: the current stream), and outputs and
+workspaces that the call makes come from that stream's memory, as inside
+``torch.cuda.stream(stream)``.
 """
 
 from dataclasses import dataclass
@@ -31,6 +35,16 @@ def _strategy(s):
 
 def _stream(stream):
     return ctypes.c_void_p((stream or torch.cuda.current_stream()).cuda_stream)
+
+
+def _empty(shape, dtype, device, stream):
+    """A new buffer for a call on ``stream`` (None: the current one), from that stream's
+    memory: a block that another stream freed may still be in use there, and one that is
+    freed goes back to the stream that works on it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
 def _p(t):
@@ -182,8 +196,9 @@ def cp_shard_plan(plan: ShardPlan, status=None, stream=None) -> ShardPlan:
 
 def make_plan(new_lens, prefix_lens, cp_size, strategy, device="cuda", status=None,
               stream=None) -> ShardPlan:
-    return cp_shard_plan(alloc_plan(new_lens, prefix_lens, cp_size, strategy, device), status,
-                         stream)
+    with torch.cuda.stream(stream):  # the plan's buffers from its memory, see _empty
+        plan = alloc_plan(new_lens, prefix_lens, cp_size, strategy, device)
+    return cp_shard_plan(plan, status, stream)
 
 
 # ---------------------------------------------------------------- attention --
@@ -201,16 +216,16 @@ def _check_qkv(q, k, v):
         raise ValueError("q must be contiguous; k and v need a contiguous last dim")
 
 
-def _attn_outputs(out, lse, n_out, Hq, dv, out_fp32, ref):
+def _attn_outputs(out, lse, n_out, Hq, dv, out_fp32, ref, stream):
     """Allocate or check the O [n, Hq, dv] (bf16 / fp32) and LSE [n, Hq] outputs."""
     if out is None:
-        out = torch.empty((n_out, Hq, dv), dtype=torch.float32 if out_fp32 else torch.bfloat16,
-                          device=ref.device)
+        out = _empty((n_out, Hq, dv), torch.float32 if out_fp32 else torch.bfloat16, ref.device,
+                     stream)
     _dev(out, "out", (torch.bfloat16, torch.float32), ref)
     if out.dim() != 3 or tuple(out.shape[1:]) != (Hq, dv):
         raise ValueError(f"out must be [rows, {Hq}, {dv}], got {tuple(out.shape)}")
     if lse is None:
-        lse = torch.empty((out.shape[0], Hq), dtype=torch.float32, device=ref.device)
+        lse = _empty((out.shape[0], Hq), torch.float32, ref.device, stream)
     _dev(lse, "lse", torch.float32, ref)
     _shape(lse, "lse", (out.shape[0], Hq))
     return out, lse
@@ -225,7 +240,7 @@ def cp_attn_partial(segs, q, k, v, scale, *, num_segs=None, tiles=None, num_tile
     rows, Hq, d = q.shape
     Hkv, dv = v.shape[1], v.shape[2]
     n_out = rows if num_out_rows is None else num_out_rows
-    out, lse = _attn_outputs(out, lse, n_out, Hq, dv, out_fp32, q)
+    out, lse = _attn_outputs(out, lse, n_out, Hq, dv, out_fp32, q, stream)
     ns, nt = _segments(segs, num_segs, tiles, num_tiles, q)
     _status(status, q)
     L.check(lib.cp_attn_partial(
@@ -246,7 +261,7 @@ def cp_attn_prefill(segs, q, k, v, scale, *, num_segs=None, tiles=None, num_tile
     _check_qkv(q, k, v)
     n, Hq, d = q.shape
     Hkv, dv = v.shape[1], v.shape[2]
-    out, lse = _attn_outputs(out, lse, n, Hq, dv, out_fp32, q)
+    out, lse = _attn_outputs(out, lse, n, Hq, dv, out_fp32, q, stream)
     if out.shape[0] != n:
         raise ValueError("out needs one row per token")
     ns, nt = _segments(segs, num_segs, tiles, num_tiles, q)
@@ -271,7 +286,7 @@ def cp_attn_partial_restore(segs, q, k, v, scale, dst_rows, *, num_out_rows=None
     if dst_rows.dim() != 1 or dst_rows.shape[0] < rows:
         raise ValueError("dst_rows must be int32 with one entry per query row")
     n_out = rows if num_out_rows is None else num_out_rows
-    out, lse = _attn_outputs(out, lse, n_out, Hq, dv, out_fp32, q)
+    out, lse = _attn_outputs(out, lse, n_out, Hq, dv, out_fp32, q, stream)
     ns, nt = _segments(segs, num_segs, tiles, num_tiles, q)
     _status(status, q)
     L.check(lib.cp_attn_partial_restore(
@@ -335,8 +350,8 @@ def cp_lse_merge(o_parts, lse_parts, *, dst_rows=None, out=None, lse_out=None, o
             raise ValueError("dst_rows needs one int32 per row")
     n_out = rows if num_out_rows is None else num_out_rows
     if out is None:
-        out = torch.empty((n_out, Hq, dv), dtype=torch.float32 if out_fp32 else torch.bfloat16,
-                          device=o_parts.device)
+        out = _empty((n_out, Hq, dv), torch.float32 if out_fp32 else torch.bfloat16,
+                     o_parts.device, stream)
     _dev(out, "out", (torch.bfloat16, torch.float32), o_parts)
     if out.dim() != 3 or tuple(out.shape[1:]) != (Hq, dv):
         raise ValueError("out must be [rows, Hq, dv]")
@@ -362,7 +377,7 @@ def cp_restore(src, idx, *, out=None, status=None, stream=None):
     rows = idx.shape[0]
     row_bytes = math.prod(src.shape[1:]) * src.element_size()
     if out is None:
-        out = torch.empty((rows,) + tuple(src.shape[1:]), dtype=src.dtype, device=src.device)
+        out = _empty((rows,) + tuple(src.shape[1:]), src.dtype, src.device, stream)
     _dev(out, "out", src.dtype, src)
     _shape(out, "out", (rows,) + tuple(src.shape[1:]))
     _status(status, src)
@@ -533,14 +548,14 @@ def cp_attn_partial_kv(plan: ShardPlan, q_cat, k, v, scale, kv_block, *, workspa
         plan.new_lens, plan.prefix_lens, plan.cp_size, plan.strategy, kv_block, Hq, dv)
     _check_qkv(q_cat, k, v)
     if workspace is None:
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=q_cat.device)
+        workspace = _empty(nbytes, torch.uint8, q_cat.device, stream)
     _dev(workspace, "workspace", torch.uint8, q_cat)
     idx = plan.gather_idx[:N] if isinstance(dst_rows, str) else dst_rows
     if idx is not None:
         _dev(idx, "dst_rows", torch.int32, q_cat)
         if idx.dim() != 1 or idx.shape[0] < N:
             raise ValueError("dst_rows needs one int32 per query row")
-    out, lse_out = _attn_outputs(out, lse_out, N, Hq, dv, out_fp32, q_cat)
+    out, lse_out = _attn_outputs(out, lse_out, N, Hq, dv, out_fp32, q_cat, stream)
     _segments(plan.segs, plan.total_segs, plan.tiles, plan.total_tiles, q_cat)
     _status(status, q_cat)
     L.check(lib.cp_attn_partial_kv(
@@ -577,14 +592,14 @@ def cp_attn_split_kv(segs, q, k, v, scale, kv_block, *, segs_host=None, num_out_
                                                                     dv)
     max_rows = longest if max_seg_rows is None else int(max_seg_rows)
     if workspace is None:
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+        workspace = _empty(nbytes, torch.uint8, q.device, stream)
     _dev(workspace, "workspace", torch.uint8, q)
     if dst_rows is not None:
         _dev(dst_rows, "dst_rows", torch.int32, q)
         if dst_rows.dim() != 1 or dst_rows.shape[0] < rows:
             raise ValueError("dst_rows needs one int32 per query row")
     n_out = rows if num_out_rows is None else num_out_rows
-    out, lse_out = _attn_outputs(out, lse_out, n_out, Hq, dv, out_fp32, q)
+    out, lse_out = _attn_outputs(out, lse_out, n_out, Hq, dv, out_fp32, q, stream)
     _status(status, q)
     L.check(lib.cp_attn_partial_kv(
         _p(segs), ns, None, 0, _p(q), rows, _p(k), k.stride(0), k.stride(1), _p(v), v.stride(0),
@@ -662,11 +677,13 @@ def cp_pass_q_attention(q_cat, k, v, plan: ShardPlan, scale, *, schedule=None, s
     N, Hq, d = q_cat.shape
     Hkv, dv = v.shape[1], v.shape[2]
     dev = q_cat.device
-    sched = pass_q_schedule(plan, dev) if schedule is None else schedule
+    if schedule is None:
+        with torch.cuda.stream(stream):  # its arrays from the call's memory, see _empty
+            schedule = pass_q_schedule(plan, dev)
+    sched = schedule
     if out is None:
-        out = (torch.empty((max(N, 1), Hq, dv), dtype=torch.float32, device=dev),
-               torch.empty((max(N, 1), Hq), dtype=torch.float32, device=dev),
-               torch.empty((max(N, 1), Hq), dtype=torch.float32, device=dev))
+        out = tuple(_empty(shape, torch.float32, dev, stream)
+                    for shape in ((max(N, 1), Hq, dv), (max(N, 1), Hq), (max(N, 1), Hq)))
     o_acc, lse, lse_b = out
     for t, name in ((o_acc, "o_acc"), (lse, "lse"), (lse_b, "lse_scratch")):
         _dev(t, name, torch.float32, q_cat)
@@ -865,11 +882,11 @@ def cp_kv_dequantize(cache: KVCache, idx=None, *, out_k=None, out_v=None, out_fp
     if out_v is not None and cache.v is None:
         raise ValueError("out_v goes with a cache that has V")
     if out_k is None:
-        out_k = torch.empty((n, Hkv, d), device=cache.k.device,
-                            dtype=torch.float32 if out_fp32 else torch.bfloat16)
+        out_k = _empty((n, Hkv, d), torch.float32 if out_fp32 else torch.bfloat16,
+                       cache.k.device, stream)
     dtype = torch.float32 if out_k.dtype is torch.float32 else torch.bfloat16
     if out_v is None and cache.v is not None:
-        out_v = torch.empty((n, Hkv, dv), dtype=dtype, device=cache.k.device)
+        out_v = _empty((n, Hkv, dv), dtype, cache.k.device, stream)
     _new_rows(out_k, "out_k", dtype, n, Hkv, d, index)
     if out_v is not None:
         _new_rows(out_v, "out_v", dtype, n, Hkv, dv, index)
@@ -1033,10 +1050,9 @@ def cp_attn_shared(plan: SharedPlan, q, k, v, scale, *, k_scale=None, v_scale=No
             raise ValueError("k_scale and v_scale must have one row stride")
         ks, vs = k_scale.data_ptr(), v_scale.data_ptr()
     if out is None:
-        out = torch.empty((N, Hq, dv), dtype=torch.float32 if out_fp32 else torch.bfloat16,
-                          device=q.device)
+        out = _empty((N, Hq, dv), torch.float32 if out_fp32 else torch.bfloat16, q.device, stream)
     if lse is None:
-        lse = torch.empty((N, Hq), dtype=torch.float32, device=q.device)
+        lse = _empty((N, Hq), torch.float32, q.device, stream)
     f32 = out.dtype is torch.float32
     if not (f32 or out.dtype is torch.bfloat16) or out.get_device() != index:
         _bad(out, "out", (torch.bfloat16, torch.float32), index)
@@ -1047,7 +1063,7 @@ def cp_attn_shared(plan: SharedPlan, q, k, v, scale, *, k_scale=None, v_scale=No
     if not out.is_contiguous() or not lse.is_contiguous():
         raise ValueError("out and lse must be contiguous")
     if workspace is None:
-        workspace = alloc_shared_workspace(plan, dv)
+        workspace = _empty(cp_shared_workspace_size(plan, dv), torch.uint8, q.device, stream)
     nbytes = workspace.numel()
     _call(index, stream, L.load().cp_attn_shared, "cp_attn_shared", plan.info, plan._table,
           q.data_ptr(), qrs, qhs, k.data_ptr(), krs, khs, ks, v.data_ptr(), vrs, vhs, vs,
