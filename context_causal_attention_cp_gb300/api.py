@@ -472,14 +472,17 @@ def cp_prefill_host(new_lens, prefix_lens, cp_size, strategy, Hq, Hkv, d, dv, sc
         _host(lse, f"lse[{i}]", torch.float32, (N, Hq))
     nbytes = cp_prefill_host_workspace_size(new_lens, prefix_lens, cp_size, strategy, Hq, Hkv,
                                             d, dv, v_is_k_prefix)
+    if streams is None:
+        streams = tuple(torch.cuda.Stream(dev) for _ in range(3))
     if workspace is None:
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        for s in streams:  # all three work on it
+            s.wait_stream(torch.cuda.current_stream(workspace.device))
+            workspace.record_stream(s)
     _dev(workspace, "workspace", torch.uint8)
     if workspace.numel() < nbytes:
         raise ValueError(f"workspace needs {nbytes} bytes")
     _status(status, workspace)
-    if streams is None:
-        streams = tuple(torch.cuda.Stream(dev) for _ in range(3))
     nb = len(batches)
     ptrs = lambda xs: (ctypes.c_void_p * max(1, nb))(  # noqa: E731
         *[x.data_ptr() if x is not None else None for x in xs])

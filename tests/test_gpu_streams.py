@@ -2,6 +2,8 @@
 block that the current stream has freed may still be in use there, and one that the call
 drops must not go back to a stream that does not wait for it."""
 
+import time
+
 import pytest
 import torch
 
@@ -86,3 +88,26 @@ def test_blocks_of_the_current_stream_are_not_taken():
     got = run(stream=torch.cuda.Stream())
     torch.cuda.synchronize()
     assert not blocks & {t.data_ptr() for t in got}
+
+
+def test_prefill_host_waits_for_the_stream_that_freed_its_workspace():
+    """A workspace that cp_prefill_host makes is a block of the current stream, whose work so
+    far comes first."""
+    g = torch.Generator().manual_seed(4)
+    r = lambda *s: torch.randn(s, generator=g).bfloat16().pin_memory()  # noqa: E731
+    N, KV = sum(NEW), sum(NEW) + sum(PRE)
+    o, lse = torch.empty((N, HQ, D), dtype=torch.bfloat16).pin_memory(), torch.empty((N, HQ)).pin_memory()
+    batch = (r(N, HQ, D), r(KV, HKV, D), r(KV, HKV, D), o, lse)
+    run = lambda **kw: cpa.cp_prefill_host(NEW, PRE, 2, "zigzag", HQ, HKV, D, D, 0.1, [batch],  # noqa: E731
+                                           **kw)
+    _, streams = run()
+    streams[2].synchronize()
+    want = o.clone()
+    o.zero_()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(1 << 29)  # about 0.3 s
+    _, streams = run(streams=streams)
+    time.sleep(0.05)
+    assert not streams[2].query()
+    streams[2].synchronize()
+    assert torch.equal(o, want)
