@@ -773,7 +773,7 @@ def _call(index, stream, fn, where, *args):
 
 
 def _codes_of(codes, scales, name):
-    """cp_kv_codes_t of one side of a cache."""
+    """Check one side of a cache; its cp_kv_codes_t."""
     if codes.dtype is not torch.float8_e4m3fn or scales.dtype is not torch.float32:
         raise TypeError(f"{name} must be float8_e4m3fn with float32 scales, got {codes.dtype} "
                         f"and {scales.dtype}")
@@ -797,7 +797,7 @@ class KVCache:
     """Quantised KV rows (see cp_kv_codes_t in cpattn.h): codes float8_e4m3fn
     [rows, Hkv, d | dv] (last dim contiguous) and their scales fp32 [Hkv, rows]
     (last dim contiguous).  ``v`` is None where V is part of K (absorbed MLA).
-    Its tensors are checked once, when it is made."""
+    Their layout is checked once, when it is made."""
     k: torch.Tensor
     k_scale: torch.Tensor
     v: Optional[torch.Tensor] = None
@@ -814,14 +814,21 @@ class KVCache:
         rows, Hkv, d = self.k.shape
         set_ = lambda name, x: object.__setattr__(self, name, x)  # noqa: E731 - frozen
         set_("rows", rows)
-        set_("_sides", (kc, vc))
+        set_("_codes", (kc, vc))
         set_("_dims", (Hkv, d, 0 if self.v is None else self.v.shape[2]))
-        set_("_index", self.k.get_device())
 
-    def _device_index(self):
-        if self._index < 0:
+    def __reduce__(self):  # a copy is made, and checked, from the copies of its tensors
+        return type(self), (self.k, self.k_scale, self.v, self.v_scale)
+
+    def _sides(self):
+        """(device index, cp_kv_codes_t of K, of V or None), where the tensors are now."""
+        index, (kc, vc) = self.k.get_device(), self._codes
+        if index < 0:
             raise ValueError("the cache must be on a CUDA device")
-        return self._index
+        kc.codes, kc.scales = self.k.data_ptr(), self.k_scale.data_ptr()
+        if vc is not None:
+            vc.codes, vc.scales = self.v.data_ptr(), self.v_scale.data_ptr()
+        return index, kc, vc
 
 
 def alloc_kv_cache(rows, Hkv, d, dv=None, device="cuda") -> KVCache:
@@ -835,16 +842,16 @@ def alloc_kv_cache(rows, Hkv, d, dv=None, device="cuda") -> KVCache:
     return KVCache(k, ks, v, vs)
 
 
-def _new_rows(x, name, dtype, n, Hkv, dim, index):
+def _new_rows(x, name, dtype, shape, index):
     if not isinstance(x, torch.Tensor) or x.dtype is not dtype or x.get_device() != index:
         _bad(x, name, dtype, index)
-    if x.shape != (n, Hkv, dim):
-        raise ValueError(f"{name} must be [{n}, {Hkv}, {dim}], got {tuple(x.shape)}")
+    if x.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {tuple(x.shape)}")
     rs, hs, cs = x.stride()
     if cs != 1 and x.numel():
         raise ValueError(f"{name} needs a contiguous last dim")
     # a tensor of one row or head may carry any stride for that dim
-    return rs if n > 1 else 0, hs if Hkv > 1 else 0
+    return rs if shape[0] > 1 else 0, hs if shape[1] > 1 else 0
 
 
 def cp_kv_quantize(cache: KVCache, k, v=None, slots=None, *, status=None, stream=None) -> KVCache:
@@ -854,15 +861,14 @@ def cp_kv_quantize(cache: KVCache, k, v=None, slots=None, *, status=None, stream
     contiguous.  ``slots``: int32 [n], the cache row of each new row (negative:
     skipped); without it row i goes to cache row i.
     """
-    index = cache._device_index()
+    index, kc, vc = cache._sides()
     Hkv, d, dv = cache._dims
     if (v is None) != (cache.v is None):
         raise ValueError("v goes with a cache that has V")
     dtype = torch.float32 if k.dtype is torch.float32 else torch.bfloat16
     n = k.shape[0]
-    krs, khs = _new_rows(k, "k", dtype, n, Hkv, d, index)
-    vrs, vhs = (0, 0) if v is None else _new_rows(v, "v", dtype, n, Hkv, dv, index)
-    kc, vc = cache._sides
+    krs, khs = _new_rows(k, "k", dtype, (n, Hkv, d), index)
+    vrs, vhs = (0, 0) if v is None else _new_rows(v, "v", dtype, (n, Hkv, dv), index)
     _call(index, stream, L.load().cp_kv_quantize, "cp_kv_quantize", k.data_ptr(), krs, khs,
           None if v is None else v.data_ptr(), vrs, vhs, dtype is torch.float32, n, Hkv, d, dv,
           _vector(slots, "slots", torch.int32, n, index), kc, vc, cache.rows,
@@ -876,7 +882,7 @@ def cp_kv_dequantize(cache: KVCache, idx=None, *, out_k=None, out_v=None, out_fp
     of row i), bf16 or fp32 (see cp_kv_dequantize in cpattn.h).  A negative
     index leaves its output row as it is.  Returns (k [n, Hkv, d], v [n, Hkv,
     dv] or None)."""
-    index = cache._device_index()
+    index, kc, vc = cache._sides()
     Hkv, d, dv = cache._dims
     n, at = cache.rows, None
     if idx is not None:
@@ -890,12 +896,11 @@ def cp_kv_dequantize(cache: KVCache, idx=None, *, out_k=None, out_v=None, out_fp
     dtype = torch.float32 if out_k.dtype is torch.float32 else torch.bfloat16
     if out_v is None and cache.v is not None:
         out_v = _empty((n, Hkv, dv), dtype, cache.k.device, stream)
-    _new_rows(out_k, "out_k", dtype, n, Hkv, d, index)
+    _new_rows(out_k, "out_k", dtype, (n, Hkv, d), index)
     if out_v is not None:
-        _new_rows(out_v, "out_v", dtype, n, Hkv, dv, index)
+        _new_rows(out_v, "out_v", dtype, (n, Hkv, dv), index)
     if not out_k.is_contiguous() or (out_v is not None and not out_v.is_contiguous()):
         raise ValueError("out_k and out_v must be contiguous")
-    kc, vc = cache._sides
     _call(index, stream, L.load().cp_kv_dequantize, "cp_kv_dequantize", kc, vc, cache.rows, Hkv, d,
           dv, at, n, out_k.data_ptr(), None if out_v is None else out_v.data_ptr(),
           dtype is torch.float32, _vector(status, "status", torch.int32, 1, index))
@@ -917,8 +922,6 @@ class SharedPlan:
         i = self.info
         set_ = lambda name, x: object.__setattr__(self, name, x)  # noqa: E731 - frozen
         set_("_shape", (i.num_q_rows, i.Hq, i.Hkv))
-        set_("_index", self.table.get_device())
-        set_("_table", self.table.data_ptr())
 
     @property
     def num_q_rows(self):
@@ -1007,7 +1010,7 @@ def cp_attn_shared(plan: SharedPlan, q, k, v, scale, *, k_scale=None, v_scale=No
     ``workspace``: alloc_shared_workspace(plan, dv), allocated when omitted.
     Returns (O [N, Hq, dv], LSE [N, Hq], workspace).
     """
-    index = plan._index
+    index = plan.table.get_device()
     if index < 0:
         raise ValueError("the plan must be on a CUDA device")
     N, Hq, Hkv = plan._shape
@@ -1068,7 +1071,7 @@ def cp_attn_shared(plan: SharedPlan, q, k, v, scale, *, k_scale=None, v_scale=No
     if workspace is None:
         workspace = _empty(cp_shared_workspace_size(plan, dv), torch.uint8, q.device, stream)
     nbytes = workspace.numel()
-    _call(index, stream, L.load().cp_attn_shared, "cp_attn_shared", plan.info, plan._table,
+    _call(index, stream, L.load().cp_attn_shared, "cp_attn_shared", plan.info, plan.table.data_ptr(),
           q.data_ptr(), qrs, qhs, k.data_ptr(), krs, khs, ks, v.data_ptr(), vrs, vhs, vs,
           scale_stride, rows, d, dv, scale, out.data_ptr(), f32, lse.data_ptr(),
           _vector(workspace, "workspace", torch.uint8, 0, index), nbytes,
