@@ -35,6 +35,8 @@ constexpr int kMaxCtas = 4096;
 long long last_pos(const cp_segment_t& s) {
   return (long long)s.q_pos0 + (long long)(s.q_len - 1) * s.q_pos_step;
 }
+// Whether some row of s sees a key (else its key run is not read and may lie anywhere).
+bool sees_keys(const cp_segment_t& s) { return s.q_len > 0 && last_pos(s) >= 0; }
 long long num_tiles(const cp_segment_t& s, int g) {
   return ((long long)s.q_len * g + CPATTN_SHARED_ROWS - 1) / CPATTN_SHARED_ROWS;
 }
@@ -170,9 +172,10 @@ int check_segments(const cp_segment_t* segs, int num_segs, int num_q_rows) {
   for (int i = 0; i < num_segs; ++i) {
     const cp_segment_t& s = segs[i];
     if (s.q_len < 0 || s.q_row0 < 0 || (long long)s.q_row0 + s.q_len > num_q_rows ||
-        s.q_pos_step < 0 || s.kv_row0 < 0 || s.kv_len < 0 ||
-        (s.q_len > 0 && last_pos(s) + 1 > s.kv_len))
+        s.q_pos_step < 0 || s.kv_len < 0)
       return CPATTN_ERR_INVALID_ARG;
+    if (!sees_keys(s)) continue;
+    if (s.kv_row0 < 0 || last_pos(s) + 1 > s.kv_len) return CPATTN_ERR_INVALID_ARG;
     if ((long long)s.kv_row0 + s.kv_len > 0x7fffffffLL) return CPATTN_ERR_TOO_LARGE;
   }
   return CPATTN_OK;
@@ -197,8 +200,7 @@ extern "C" int cp_shared_plan_size(const cp_segment_t* segs, int num_segs, int n
     const cp_segment_t& s = segs[i];
     tiles += num_tiles(s, L.g);
     entries += s.q_len;
-    if (s.q_len > 0)
-      kv_rows = std::max(kv_rows, s.kv_row0 + std::max<long long>(0, last_pos(s) + 1));
+    if (sees_keys(s)) kv_rows = std::max(kv_rows, s.kv_row0 + last_pos(s) + 1);
   }
   if (tiles * Hkv > kMaxUnits || entries > 0x3fffffffLL) return CPATTN_ERR_TOO_LARGE;
   long long cost = 0;

@@ -581,7 +581,8 @@ int cp_kv_dequantize(const cp_kv_codes_t* k_cache, const cp_kv_codes_t* v_cache,
  * runs.  Row i of a segment (query row q_row0 + i) has position q_pos0 +
  * i*q_pos_step within the segment's key run and sees its keys 0 .. position (KV
  * rows kv_row0 + key); a negative position sees none.  kv_len >= the last row's
- * position + 1 and >= 0; q_pos_step >= 0; tok0 and req are not used.  Segments
+ * position + 1 and >= 0; q_pos_step >= 0; tok0 and req are not used.  kv_row0 >= 0
+ * where some row sees a key, and anything otherwise (an empty slot).  Segments
  * may share query rows: a row attends to the union of the runs of all the
  * segments that hold it (a key that two of them give is counted twice).  A
  * shared prefix of P keys is one segment over all rows of the batch with q_pos0
