@@ -35,9 +35,12 @@
 // e4m3 cache: both products run in f16, which holds a code exactly and takes two
 // instructions for two codes (bf16 takes 6.5, more than a step has issue slots
 // for).  K row r enters as code * 2^(e_r - E), E the tile's largest e, and 2^E goes
-// into the scores' factor: what a row far below the tile's largest loses is below
-// 2^-32 of that largest, less than an fp32 score resolves.  V the same with E the
-// largest e that the stream has met in the piece; O is rescaled when that grows.  A
+// into the scores' factor.  An f16 ends at 2^-24: a row within 2^15 of the largest scale
+// loses nothing, one down to 2^-24 of it less than 2^-32 of the tile's largest element
+// (the rounding of code times factor; less than an fp32 score resolves), and one below
+// that has a factor of 0 and counts as zeros, up to 2^-24 of that element.  V the same
+// with E the largest e that the stream has met in the piece; O is rescaled when that
+// grows, and a V row below 2^-24 adds nothing even where it has all of the weight.  A
 // query row enters as f16 times the power of two that brings its largest element to
 // [2^14, 2^15), so that elements down to 2^-30 of it keep bf16's 8 bits.  P in f16 is
 // off by at most 2^-11 of a weight (bf16: 2^-8) down to 2^-21 of the largest weight, and

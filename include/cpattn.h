@@ -633,8 +633,11 @@ int cp_shared_workspace_size(const cp_shared_plan_t* plan, int dv, int64_t* byte
  *     overwritten; not to be shared by calls that may run at the same time.
  * P is rounded to bf16 for the second product, as in cp_attn_partial, and with codes
  * to f16.  Codes enter the products exactly where the scales of 128 consecutive keys
- * of a run (for V: of a run) are within 2^15 of the largest; what a row further below
- * loses is under 2^-32 of the largest element.
+ * of a run (for V: of a run) are within 2^15 of the largest.  Further below, an element
+ * is off by less than 2^-32 of the largest element, down to scales of 2^-24 of the
+ * largest; a row below that may count as zeros, which is up to 2^-24 of the largest
+ * element: its key then scores 0, and its value adds nothing even where it has all of
+ * the weight.
  * Two launches (the attention and the merge of the partial results), no order of
  * atomics: the same call gives the same bits.  num_kv_rows < plan->kv_rows:
  * CPATTN_ERR_INVALID_ARG.  A table that does not match the plan sets
