@@ -80,3 +80,48 @@ def test_scales_far_below_the_largest(below, d, tokens):
     scale = 60.0 / d
     ref = osh.shared_attention(f64(q), k64, v64, segs, scale)
     check_f16(*run(cache, q, scale), ref, d, keys, q, k64, v64, scale, lost, "V")
+
+
+@KINDS
+@DIMS
+@pytest.mark.parametrize("ctas", [2, 6])
+@pytest.mark.parametrize("steps", [(3,), (-3,), (5, -4), (0, 7, 0, -6), (1, 1, 1, -8)], ids=str)
+def test_values_whose_scales_step_along_the_run(steps, ctas, d, tokens):
+    """V of a KV tile is 2^steps[t] times the tile's before it, so that the exponent of O moves
+    inside a piece (2 blocks: about 9 tiles a piece and several pieces a stream), and starts
+    again with the next.  Uniform weights: what any tile adds, and a missing or wrong
+    rescale of it, is far above f16's 2^-11 of a weight."""
+    Hq, Hkv, prefix = 16, 4, 8 * 128 + 61
+    own = tokens + 300
+    rows = prefix + own
+    q, k, v = draw(sum(steps) + d, tokens, rows, d, Hq, Hkv)
+    e, exps = 0, []
+    for t in range(-(-rows // 128)):
+        exps.append(e)
+        e += steps[t % len(steps)]
+    # (within 2^12 of the run's largest, where f16 loses nothing)
+    x = torch.tensor(exps, device="cuda").float()
+    x = torch.maximum(x, x.max() - 12).repeat_interleave(128)[:rows]
+    v = v.float() * torch.exp2(x)[:, None, None]
+    cache, k64, v64 = cached(k.float(), v)
+    plan = cpa.make_shared_plan([tokens], [own], prefix, Hq, Hkv, num_ctas=ctas)
+    scale = 0.02
+    ref = osh.shared_attention(f64(q), k64, v64, plan.segs_host.tolist(), scale)
+    o, lse, _ = cpa.cp_attn_shared(plan, q, cache.k, cache.v, scale, k_scale=cache.k_scale,
+                                   v_scale=cache.v_scale, out_fp32=True)
+    check_f16(o, lse, ref, d, rows, q, k64, v64, scale, 2.0 ** -32, f"{steps}")
+
+
+@KINDS
+@DIMS
+def test_weights_of_the_e4m3_path_in_f16(d, tokens):
+    """Ordinary values at f16's own tolerance, in the order of the oracle's terms."""
+    own, prefix = tokens + 200, 1500
+    q, k, v = draw(d + 1, tokens, prefix + own, d)
+    cache, k64, v64 = cached(k, v)
+    for ctas in (2, None):
+        plan = cpa.make_shared_plan([tokens], [own], prefix, 8, 2, num_ctas=ctas)
+        ref = osh.shared_attention(f64(q), k64, v64, plan.segs_host.tolist(), d ** -0.5)
+        o, lse, _ = cpa.cp_attn_shared(plan, q, cache.k, cache.v, d ** -0.5, k_scale=cache.k_scale,
+                                       v_scale=cache.v_scale, out_fp32=True)
+        check_f16(o, lse, ref, d, prefix + own, q, k64, v64, d ** -0.5, 2.0 ** -32, f"{ctas} blocks")
