@@ -915,17 +915,12 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
       }
       float m_run = -INFINITY, l_run = 0.f, m_use = 0.f;
       int ev = 0;  // exponent of O
-      // The list's first tile is preceded by one that sees no key (and writes only P, over
-      // an S that is still to come): it brings the code in, which takes as long as three
-      // tiles (4000 cycles from L2, up to 9000 from HBM), while the queries travel.
       for (int t = 0; t < T; ++t) {
-        {
-          ok = wait_warp(s_full + s, step & 1, abort_flag, p.timeout_ns);
-          if (!ok) break;
-          tc_fence_after();
-          // the piece's last S is done: its query tile is free for the next piece
-          if (t == T - 1 && more) load_q(np);
-        }
+        ok = wait_warp(s_full + s, step & 1, abort_flag, p.timeout_ns);
+        if (!ok) break;
+        tc_fence_after();
+        // the piece's last S is done: its query tile is free for the next piece
+        if (t == T - 1 && more) load_q(np);
         float sl2 = factor, o_scale = 1.f;
         if constexpr (QUANT) {
           // written before the K tile of this step went to the tensor core, and not

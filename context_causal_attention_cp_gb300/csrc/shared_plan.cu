@@ -3,8 +3,8 @@
 // The units (segment, packed-row tile, KV head), kind by kind, are walked in a
 // fixed order and their keys dealt to the thread blocks one after the other: each
 // block is filled up to a budget, so a unit is cut only where a block is full (a block
-// with small units has no others).  The smallest budget that needs no more than num_ctas blocks is found by
-// bisection.  A piece costs its KV tiles plus a fixed part (its queries' load and its
+// with small units has no others).  The smallest budget that needs no more than num_ctas
+// blocks is found by bisection.  A piece costs its KV tiles plus a fixed part (its queries' load and its
 // partial's store), so that short units are not shredded.  A block's run of single
 // units is cut once more, at half its KV tiles, between the block's two streams.
 // Nothing is allocated: each pass walks the segment table again.
@@ -18,8 +18,10 @@ namespace {
 
 constexpr int kKeys = kSharedTileKeys;
 // Costs by the kind of unit (dual, single, small), of a KV tile and of a piece's fixed
-// part, in about 80 ns.  Fitted to whole calls: a block's dual tile takes 1.9 us (bf16)
-// or 2.6 us (e4m3), a small tile 1.0 and 1.1 us, a small piece 1.1 and 1.4 us besides.
+// part, in about 80 ns.  Fitted to whole calls in bf16 at d = 128: a block's dual tile
+// takes 1.9 us, a small tile 1.0, a small piece 1.1 besides.  The one table serves e4m3
+// and d = 64, too: in e4m3 (2.6, 1.1 and 1.4 us) blocks with dual units end about a tenth
+// later than an even deal would let them.
 // The fixed part of a dual or single piece (its queries, 128 KB of partial rows, their
 // merge) is 3 to 4 us, and its cost is above that, which keeps units in few pieces.
 constexpr int kCosts[2][3] = {{24, 16, 12}, {90, 50, 20}};
