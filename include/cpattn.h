@@ -532,8 +532,9 @@ int cp_restore(const void* src, int num_src_rows, const int32_t* idx_dev, int ro
  * (or feeding it to the tensor cores as bf16) adds no second rounding.
  *
  * cp_kv_codes_t: one of K and V.  Row r, head h, column c has its code at
- * codes[r*row_stride + h*head_stride + c] (strides in bytes, multiples of 16,
- * heads and rows not overlapping; codes 16-byte aligned) and its scale at
+ * codes[r*row_stride + h*head_stride + c] (strides in bytes, multiples of 16; a row's
+ * heads in one place, head_stride >= dim and row_stride >= (Hkv-1)*head_stride + dim;
+ * codes 16-byte aligned) and its scale at
  * scales[h*scale_stride + r] (4-byte aligned, scale_stride >= the cache's
  * rows): a run of rows has its scales in consecutive words. */
 typedef struct {
@@ -596,7 +597,11 @@ int cp_kv_dequantize(const cp_kv_codes_t* k_cache, const cp_kv_codes_t* v_cache,
  * the same run into tiles of up to CPATTN_SHARED_ROWS rows (row i, head j of the
  * group at i*(Hq/Hkv) + j), and cuts the (tile, KV head, keys) work into
  * num_ctas shares of about equal cost, each a list of pieces.  It depends on the
- * lengths alone: one plan serves every layer of a step.
+ * lengths and on where the runs lie, so that one plan serves every layer of a step.  A
+ * launch takes the plan's counts by value: a captured graph replays the plan that it
+ * was captured with, and a step of other lengths needs its own plan and launch.
+ *   A run is consecutive KV rows.  Keys kept in pages are a segment for each page, and
+ *   a KV tile is up to 128 keys of one run, so that short pages leave most of it empty.
  *   num_ctas in [2, 4096]: thread blocks of the launch (the device's SM count).
  *   Hq % Hkv == 0; num_segs and the tiles times Hkv up to 2^22, query rows, KV
  *   rows and partial rows below 2^31 (CPATTN_ERR_TOO_LARGE).
