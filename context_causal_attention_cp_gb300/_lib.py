@@ -30,6 +30,7 @@ DEBUG_NVTX = 3
 ZIGZAG = 0
 INTERLEAVE = 1
 TILE_ROWS = 128
+MAX_ROPE_AXES = 8
 
 c_i32p = ctypes.POINTER(ctypes.c_int32)
 vp = ctypes.c_void_p
@@ -41,6 +42,12 @@ class KvCodes(ctypes.Structure):
     """cp_kv_codes_t"""
     _fields_ = [("codes", vp), ("scales", vp), ("row_stride", i64), ("head_stride", i64),
                 ("scale_stride", i64)]
+
+
+class RopeInfo(ctypes.Structure):
+    """cp_rope_t"""
+    _fields_ = [("table", vp)] + [(n, ctypes.c_int32) for n in ("pairs", "first", "interleaved",
+                                                               "axes")]
 
 
 class SharedPlanInfo(ctypes.Structure):
@@ -105,6 +112,17 @@ SIGNATURES = {
     "cp_attn_shared": (i32, [ctypes.POINTER(SharedPlanInfo), vp, vp, i64, i64, vp, i64, i64, vp,
                              vp, i64, i64, vp, i64, i32, i32, i32, ctypes.c_float, vp, i32, vp,
                              vp, i64, vp, vp]),
+    "cp_rope_table": (i32, [vp, vp, i32, vp]),
+    "cp_rope": (i32, [ctypes.POINTER(RopeInfo), vp, i64, i32, vp, i64, i64, i32, vp, i64, i64, vp,
+                      i64, i64, i32, vp, i64, i64, i32, i32, i32, vp, vp]),
+    "cp_kv_append": (i32, [ctypes.POINTER(RopeInfo), vp, i64, vp, i64, i64, vp, i64, i64, i32, i32,
+                           i32, i32, i32, vp, ctypes.POINTER(KvCodes), ctypes.POINTER(KvCodes),
+                           i32, vp, i64, i64, i32, vp, i64, i64, vp, vp]),
+    "cp_tree_layout": (i32, [vp, vp, i32, vp, i64, i32, i32, vp, i32, i32, vp, vp, vp, vp, vp]),
+    "cp_tree_workspace_size": (i32, [i32, i32, i32, i32, i32, ctypes.POINTER(i64)]),
+    "cp_attn_tree": (i32, [vp, i64, i64, i32, vp, i64, i64, vp, vp, i64, i64, vp, i64, i32, vp,
+                           i64, i32, i32, vp, vp, i32, vp, i32, i32, i32, i32, i32,
+                           ctypes.c_float, i32, i32, vp, i32, vp, vp, i64, vp, vp]),
     "cp_attn_debug": (i32, [i32, ctypes.c_longlong]),
     "cp_status_string": (ctypes.c_char_p, [i32]),
 }

@@ -1077,3 +1077,342 @@ def cp_attn_shared(plan: SharedPlan, q, k, v, scale, *, k_scale=None, v_scale=No
           _vector(workspace, "workspace", torch.uint8, 0, index), nbytes,
           _vector(status, "status", torch.int32, 1, index))
     return out, lse, workspace
+
+
+# -------------------------------------------------------- rotary positions --
+@dataclass(frozen=True)
+class Rope:
+    """A rotation's frequencies and which columns it turns (see cp_rope_t in cpattn.h)."""
+    table: torch.Tensor          # int32 [pairs, 4], device
+    first: int = 0
+    interleaved: bool = False
+    axes: int = 1                # rows of positions
+
+    def __post_init__(self):
+        t = self.table
+        if t.dtype is not torch.int32 or t.dim() != 2 or t.shape[1] != 4 or not t.is_contiguous():
+            raise ValueError("table must be contiguous int32 [pairs, 4]")
+        object.__setattr__(self, "_info", L.RopeInfo(None, t.shape[0], int(self.first),
+                                                     bool(self.interleaved), int(self.axes)))
+
+    def __reduce__(self):
+        return type(self), (self.table, self.first, self.interleaved, self.axes)
+
+    @property
+    def pairs(self):
+        return self.table.shape[0]
+
+    def _of(self, index):
+        """cp_rope_t, with the table where it is now."""
+        if self.table.get_device() != index:
+            _bad(self.table, "the rotation's table", torch.int32, index)
+        self._info.table = self.table.data_ptr()
+        return self._info
+
+
+def make_rope(inv_freq, *, axes=None, first=0, interleaved=False, device="cuda") -> Rope:
+    """The rotation of pairs by positions times ``inv_freq`` (radians a position, float64).
+
+    ``axes``: for each pair the row of positions that it follows (default: all the
+    first), e.g. time, height or width.  Pairs are columns (first + c, first + pairs + c),
+    or (first + 2c, first + 2c + 1) with ``interleaved``.
+    """
+    f = torch.as_tensor(inv_freq).detach().to("cpu", torch.float64).contiguous()
+    if f.dim() != 1 or f.numel() == 0:
+        raise ValueError("inv_freq must be 1-D, with an entry for each pair")
+    ax = None
+    if axes is not None:
+        ax = torch.as_tensor(axes).detach().to("cpu", torch.int32).contiguous()
+        if ax.shape != f.shape:
+            raise ValueError("axes needs an entry for each pair")
+    table = torch.empty((f.numel(), 4), dtype=torch.int32)
+    L.check(L.load().cp_rope_table(f.data_ptr(), None if ax is None else ax.data_ptr(), f.numel(),
+                                   table.data_ptr()), "cp_rope_table")
+    return Rope(table.to(device), first=int(first), interleaved=bool(interleaved),
+                axes=1 if ax is None else int(ax.max()) + 1)
+
+
+def _positions(rope, positions, n, index):
+    """Check the positions of n rows; their address and axis stride."""
+    if not isinstance(positions, torch.Tensor) or positions.dtype is not torch.int32 or \
+            positions.get_device() != index:
+        _bad(positions, "positions", torch.int32, index)
+    shape = positions.shape
+    if shape != (rope.axes, n) and not (rope.axes == 1 and shape == (n,)):
+        raise ValueError(f"positions must be [{rope.axes}, {n}], got {tuple(shape)}")
+    if n > 1 and positions.stride(-1) != 1:
+        raise ValueError("positions needs a contiguous last dim")
+    return positions.data_ptr(), max(positions.stride(0), n) if rope.axes > 1 else n
+
+
+def _rotated(x, out, name, dtype, n, d, index, stream):
+    """Check rows that are rotated, and their output (made when None); (output, arguments)."""
+    if not isinstance(x, torch.Tensor) or x.dim() != 3:
+        raise ValueError(f"{name} must be a CUDA tensor [rows, heads, dim]")
+    shape = (n, x.shape[1], d)
+    rs, hs = _new_rows(x, name, dtype, shape, index)
+    if out is None:
+        out = _empty(shape, dtype, x.device, stream)
+    ors, ohs = _new_rows(out, "out_" + name, dtype, shape, index)
+    if out.numel() and ((n > 1 and ors == 0) or (shape[1] > 1 and ohs == 0)):
+        raise ValueError(f"out_{name} needs a place for each element")
+    return out, (x.data_ptr(), rs, hs, shape[1], out.data_ptr(), ors, ohs)
+
+
+def cp_rope(rope: Rope, q, k=None, positions=None, *, inverse=False, out_q=None, out_k=None,
+            status=None, stream=None):
+    """Rotate q [n, Hq, d] and k [n, Hk, d] (bf16 or fp32, the same) by the rows' positions,
+    int32 [axes, n] or [n] (see cp_rope in cpattn.h).
+
+    ``inverse``: turn back, which takes the gradient of the outputs to that of the
+    inputs.  ``out_q`` / ``out_k`` may be q / k.  Returns (q, k or None), rotated.
+    """
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("q must be a CUDA tensor [rows, heads, dim]")
+    index, (n, Hq, d) = q.get_device(), q.shape
+    if index < 0:
+        raise ValueError("q must be a CUDA tensor")
+    if k is None and out_k is not None:
+        raise ValueError("out_k goes with k")
+    if Hq < 1:
+        raise ValueError("q needs at least one head")
+    dtype = torch.float32 if q.dtype is torch.float32 else torch.bfloat16
+    at, axis_stride = _positions(rope, positions, n, index)
+    out_q, qa = _rotated(q, out_q, "q", dtype, n, d, index, stream)
+    ka = (None, 0, 0, 0, None, 0, 0)
+    if k is not None:
+        out_k, ka = _rotated(k, out_k, "k", dtype, n, d, index, stream)
+    _call(index, stream, L.load().cp_rope, "cp_rope", rope._of(index), at, axis_stride, bool(inverse),
+          *qa, *ka, dtype is torch.float32, n, d, _vector(status, "status", torch.int32, 1, index))
+    return out_q, out_k
+
+
+# ------------------------------------------------------------- paged cache --
+def _row_side(t, name, index, shape):
+    """One side of a bf16 cache [rows, Hkv, dim] as a cp_kv_codes_t (strides in bytes)."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.bfloat16 or t.get_device() != index:
+        _bad(t, name, torch.bfloat16, index)
+    if t.dim() != 3 or t.shape[:2] != shape or (t.stride(2) != 1 and t.numel()):
+        raise ValueError(f"{name} must be [rows, Hkv, dim] with a contiguous last dim, of the "
+                         f"cache's {shape[0]} rows and {shape[1]} heads")
+    rows, Hkv, dim = t.shape
+    hs = t.stride(1) if Hkv > 1 else dim
+    rs = t.stride(0) if rows > 1 else (Hkv - 1) * hs + dim
+    return L.KvCodes(t.data_ptr(), None, 2 * rs, 2 * hs, 0)
+
+
+def cp_kv_append(cache, k, v=None, slots=None, *, rope: Optional[Rope] = None, positions=None,
+                 q=None, out_q=None, status=None, stream=None):
+    """Append new rows to a cache, K and q rotated on the way (see cp_kv_append in cpattn.h).
+
+    ``cache``: a KVCache, or a pair (k, v) of bf16 tensors [rows, Hkv, dim] (v None: K
+    alone).  k, v, slots: as in cp_kv_quantize.  With ``rope`` and ``positions`` (as in
+    cp_rope) K is rotated before it is rounded, and ``q`` [n, Hq, d] to ``out_q`` (made
+    when omitted; it may be q).  Returns out_q, or None without q.
+    """
+    if isinstance(cache, KVCache):
+        index, kc, vc = cache._sides()
+        rows, (Hkv, d, dv) = cache.rows, cache._dims
+    else:
+        ck, cv = cache
+        if not isinstance(ck, torch.Tensor) or ck.dim() != 3 or ck.get_device() < 0:
+            raise ValueError("the cache must be CUDA tensors [rows, Hkv, dim]")
+        index, (rows, Hkv, d) = ck.get_device(), ck.shape
+        kc = _row_side(ck, "the cache's k", index, (rows, Hkv))
+        vc, dv = (None, 0) if cv is None else (_row_side(cv, "the cache's v", index, (rows, Hkv)),
+                                               cv.shape[2])
+    if (v is None) != (vc is None):
+        raise ValueError("v goes with a cache that has V")
+    if (rope is None) != (positions is None):
+        raise ValueError("rope and positions go together")
+    if not isinstance(k, torch.Tensor) or k.dim() != 3:
+        raise ValueError("k must be a CUDA tensor [rows, Hkv, dim]")
+    dtype = torch.float32 if k.dtype is torch.float32 else torch.bfloat16
+    n = k.shape[0]
+    krs, khs = _new_rows(k, "k", dtype, (n, Hkv, d), index)
+    vrs, vhs = (0, 0) if v is None else _new_rows(v, "v", dtype, (n, Hkv, dv), index)
+    at, axis_stride = (None, 0) if rope is None else _positions(rope, positions, n, index)
+    qa = (None, 0, 0, 0, None, 0, 0)
+    if q is not None:
+        out_q, qa = _rotated(q, out_q, "q", dtype, n, d, index, stream)
+    elif out_q is not None:
+        raise ValueError("out_q goes with q")
+    _call(index, stream, L.load().cp_kv_append, "cp_kv_append",
+          None if rope is None else rope._of(index), at, axis_stride, k.data_ptr(), krs, khs,
+          None if v is None else v.data_ptr(), vrs, vhs, dtype is torch.float32, n, Hkv, d, dv,
+          _vector(slots, "slots", torch.int32, n, index), kc, vc, rows, *qa,
+          _vector(status, "status", torch.int32, 1, index))
+    return out_q
+
+
+def _batch(q_start, kv_lens, page_table, index):
+    """Check a paged batch's arrays; their arguments up to the table's width."""
+    if not isinstance(kv_lens, torch.Tensor) or kv_lens.dim() != 1:
+        raise ValueError("kv_lens must be a CUDA int32 tensor [requests]")
+    B = kv_lens.shape[0]
+    if not isinstance(page_table, torch.Tensor) or page_table.dtype is not torch.int32 or \
+            page_table.get_device() != index:
+        _bad(page_table, "page_table", torch.int32, index)
+    if page_table.dim() != 2 or page_table.shape[0] != B or \
+            (page_table.shape[1] > 1 and B and page_table.stride(1) != 1):
+        raise ValueError(f"page_table must be [{B}, pages] with a contiguous last dim")
+    width = page_table.shape[1]
+    if not isinstance(q_start, torch.Tensor) or q_start.dim() != 1 or q_start.shape[0] != B + 1:
+        raise ValueError(f"q_start must be a CUDA int32 tensor [{B + 1}]")
+    return (_vector(q_start, "q_start", torch.int32, B + 1, index),
+            _vector(kv_lens, "kv_lens", torch.int32, B, index), B, page_table.data_ptr(),
+            page_table.stride(0) if B > 1 else width, width)
+
+
+def cp_tree_layout(q_start, kv_lens, page_table, page_size, num_rows, *, parents=None,
+                   max_nodes=None, slots=None, positions=None, mask=None, status=None,
+                   stream=None):
+    """Cache rows, positions and masks of a step's new rows (see cp_tree_layout in cpattn.h).
+
+    int32 tensors on the device: q_start [B + 1], kv_lens [B], page_table [B, pages].
+    ``parents`` int32 [num_rows]: each node's parent within its request, -1 for a root;
+    without it the rows are chains and there is no mask.  Outputs that are not given are
+    made, the mask with bits for ``max_nodes`` rows a request.  Returns (slots [num_rows],
+    positions [num_rows], mask [num_rows, words] or None).
+    """
+    if not isinstance(q_start, torch.Tensor) or not q_start.is_cuda:
+        raise ValueError("q_start must be a CUDA int32 tensor")
+    index, n = q_start.get_device(), int(num_rows)
+    batch = _batch(q_start, kv_lens, page_table, index)
+    if n < 0:
+        raise ValueError("num_rows must not be negative")
+    if parents is None and mask is not None:
+        raise ValueError("a mask goes with parents")
+    if parents is not None and mask is None:
+        if max_nodes is None or max_nodes < 1:
+            raise ValueError("parents need a mask, or max_nodes to make one")
+        mask = _empty((n, -(-int(max_nodes) // 32)), torch.int32, q_start.device, stream)
+    if slots is None:
+        slots = _empty(n, torch.int32, q_start.device, stream)
+    if positions is None:
+        positions = _empty(n, torch.int32, q_start.device, stream)
+    words = 0
+    if mask is not None:
+        words = _mask_words(mask, n, index)
+    _call(index, stream, L.load().cp_tree_layout, "cp_tree_layout", *batch, int(page_size),
+          _vector(parents, "parents", torch.int32, n, index), n, words,
+          _vector(slots, "slots", torch.int32, n, index),
+          _vector(positions, "positions", torch.int32, n, index),
+          None if mask is None else mask.data_ptr(),
+          _vector(status, "status", torch.int32, 1, index))
+    return slots, positions, mask
+
+
+def _mask_words(mask, n, index):
+    if not isinstance(mask, torch.Tensor) or mask.dtype is not torch.int32 or mask.get_device() != index:
+        _bad(mask, "mask", torch.int32, index)
+    if mask.dim() != 2 or mask.shape[0] != n or mask.shape[1] < 1 or not mask.is_contiguous():
+        raise ValueError(f"mask must be contiguous [{n}, words]")
+    return mask.shape[1]
+
+
+def _tree_ctas(index):
+    return torch.cuda.get_device_properties(index).multi_processor_count
+
+
+def cp_tree_workspace_size(Hq, Hkv, dv, max_nodes, num_ctas) -> int:
+    """Workspace bytes of cp_attn_tree."""
+    nbytes = ctypes.c_int64()
+    L.check(L.load().cp_tree_workspace_size(int(Hq), int(Hkv), int(dv), int(max_nodes),
+                                            int(num_ctas), ctypes.byref(nbytes)),
+            "cp_tree_workspace_size")
+    return nbytes.value
+
+
+def alloc_tree_workspace(Hq, Hkv, dv, max_nodes=1, *, num_ctas=None, device="cuda") -> torch.Tensor:
+    """A workspace of cp_attn_tree, for batches of any lengths."""
+    if num_ctas is None:
+        num_ctas = _tree_ctas(device)
+    return torch.empty(cp_tree_workspace_size(Hq, Hkv, dv, max_nodes, num_ctas), dtype=torch.uint8,
+                       device=device)
+
+
+def cp_attn_tree(q, k, v, page_table, page_size, q_start, kv_lens, scale, *, mask=None,
+                 max_nodes=1, k_scale=None, v_scale=None, out=None, lse=None, out_fp32=False,
+                 num_ctas=None, workspace=None, status=None, stream=None):
+    """Attention of new rows over a paged cache (see cp_attn_tree in cpattn.h).
+
+    q bf16 [N, Hq, d]; k, v bf16 [cache rows, Hkv, d], or with ``k_scale`` and ``v_scale``
+    the float8_e4m3fn codes of a KVCache.  page_table, q_start, kv_lens, ``mask``: as
+    cp_tree_layout takes and gives them; without a mask a request's rows are a chain.
+    ``max_nodes``: the rows of a request to tune for (a longer request is right, and
+    slower).  Rows behind the last request are left as they are in ``out`` and ``lse``
+    (and are undefined in new ones).  ``workspace``: alloc_tree_workspace for the same
+    heads and max_nodes, allocated when omitted.  Returns (O [N, Hq, d], LSE [N, Hq],
+    workspace).
+    """
+    if not isinstance(q, torch.Tensor) or not q.is_cuda or q.dim() != 3:
+        raise ValueError("q must be a CUDA tensor [rows, Hq, d]")
+    index = q.get_device()
+    quant = k_scale is not None
+    if quant != (v_scale is not None):
+        raise ValueError("k_scale and v_scale go together")
+    kv_dtype = torch.float8_e4m3fn if quant else torch.bfloat16
+    for t, name, dtype in ((q, "q", torch.bfloat16), (k, "k", kv_dtype), (v, "v", kv_dtype)):
+        if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != index:
+            _bad(t, name, dtype, index)
+    N, Hq, d = q.shape
+    kshape, vshape = k.shape, v.shape
+    if len(kshape) != 3 or len(vshape) != 3 or kshape[:2] != vshape[:2] or kshape[2] != d:
+        raise ValueError(f"k and v must be [rows, Hkv, dim] of equal rows and heads and k's dim q's, "
+                         f"got {tuple(kshape)} and {tuple(vshape)}")
+    rows, Hkv, dv = vshape
+    (qrs, qhs, qcs), (krs, khs, kcs), (vrs, vhs, vcs) = q.stride(), k.stride(), v.stride()
+    if (qcs != 1 and N) or ((kcs != 1 or vcs != 1) and rows):
+        raise ValueError("q, k and v need a contiguous last dim")
+    # a tensor of one row or head may carry any stride for that dim
+    if N <= 1:
+        qrs = Hq * d
+    if Hq == 1:
+        qhs = d
+    if Hkv == 1:
+        khs, vhs = d, dv
+    if rows <= 1:
+        krs, vrs = (Hkv - 1) * khs + d, (Hkv - 1) * vhs + dv
+    ks = vs = None
+    scale_stride = 0
+    if quant:
+        for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+            if not isinstance(t, torch.Tensor) or t.dtype is not torch.float32 or \
+                    t.get_device() != index:
+                _bad(t, name, torch.float32, index)
+            if t.shape != (Hkv, rows) or (t.stride(1) != 1 and rows > 1):
+                raise ValueError(f"{name} must be [{Hkv}, {rows}] with a contiguous last dim")
+        scale_stride = k_scale.stride(0) if Hkv > 1 else rows
+        if Hkv > 1 and v_scale.stride(0) != scale_stride:
+            raise ValueError("k_scale and v_scale must have one row stride")
+        ks, vs = k_scale.data_ptr(), v_scale.data_ptr()
+    at_q, at_len, B, at_table, table_stride, width = _batch(q_start, kv_lens, page_table, index)
+    words = 0 if mask is None else _mask_words(mask, N, index)
+    if num_ctas is None:
+        num_ctas = _tree_ctas(index)
+    if out is None:
+        out = _empty((N, Hq, dv), torch.float32 if out_fp32 else torch.bfloat16, q.device, stream)
+    if lse is None:
+        lse = _empty((N, Hq), torch.float32, q.device, stream)
+    f32 = out.dtype is torch.float32
+    if not (f32 or out.dtype is torch.bfloat16) or out.get_device() != index:
+        _bad(out, "out", (torch.bfloat16, torch.float32), index)
+    if lse.dtype is not torch.float32 or lse.get_device() != index:
+        _bad(lse, "lse", torch.float32, index)
+    if out.shape != (N, Hq, dv) or lse.shape != (N, Hq):
+        raise ValueError(f"out must be [{N}, {Hq}, {dv}] and lse [{N}, {Hq}]")
+    if not out.is_contiguous() or not lse.is_contiguous():
+        raise ValueError("out and lse must be contiguous")
+    if workspace is None:
+        workspace = _empty(cp_tree_workspace_size(Hq, Hkv, dv, max_nodes, num_ctas), torch.uint8,
+                           q.device, stream)
+    nbytes = workspace.numel()
+    _call(index, stream, L.load().cp_attn_tree, "cp_attn_tree", q.data_ptr(), qrs, qhs, N,
+          k.data_ptr(), krs, khs, ks, v.data_ptr(), vrs, vhs, vs, scale_stride, rows, at_table,
+          table_stride, width, int(page_size), at_q, at_len, B,
+          None if mask is None else mask.data_ptr(), words, Hq, Hkv, d, dv, scale, int(max_nodes),
+          int(num_ctas), out.data_ptr(), f32, lse.data_ptr(),
+          _vector(workspace, "workspace", torch.uint8, 0, index), nbytes,
+          _vector(status, "status", torch.int32, 1, index))
+    return out, lse, workspace

@@ -50,15 +50,13 @@
 
 #include <cuda_bf16.h>
 
-#include "attn_common.cuh"
-#include "shared_plan.h"
+#include "attn_tiles.cuh"
 #include "trace.h"
 
 namespace cpattn {
 namespace {
 
 constexpr int kRows = CPATTN_SHARED_ROWS;
-constexpr int BN = kSharedTileKeys;
 constexpr int kTailRows = 16;                   // box rows of the loads of a run's last tile
 constexpr int kProducerWarp = 8, kMmaWarp = 9;  // MMA: 9 and 10
 constexpr int kConvertWarp = 12;                // to 15
@@ -113,12 +111,6 @@ struct SharedCfg {
   static constexpr int kTmemCols = 512;  // S of each stream, then O of each
 };
 
-// Orders this thread's shared-memory accesses before later ones of the async proxy (TMA,
-// tcgen05.mma reading shared memory).
-__device__ __forceinline__ void fence_async_shared() {
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-}
-
 // What the producer tells the converters about a raw tile.
 struct RawNote {
   static constexpr int kNoteV = 8;
@@ -126,38 +118,6 @@ struct RawNote {
   int which;    // RingTile::which, | kNoteV of a V tile
   int ek, ev;   // of a K tile: E of it, and E of its V tile
 };
-
-// Bounded waits, of one thread and of a whole warp (uniform).  They read the timer
-// only after a few hundred polls: it is far from the SM, and a read at every wait
-// that does not succeed at once costs more than the wait.
-constexpr uint32_t kPollsPerCheck = 256;
-__device__ __forceinline__ bool give_up(uint64_t& t0, const volatile int* abort, uint64_t timeout) {
-  const uint64_t now = global_timer_ns();
-  if (t0 == 0) t0 = now;
-  return (abort && *abort != 0) || now - t0 > timeout;
-}
-__device__ __forceinline__ bool wait_one(uint64_t* bar, uint32_t parity, const volatile int* abort,
-                                         uint64_t timeout) {
-  uint64_t t0 = 0;
-  for (uint32_t i = 1; !mbar_try_wait(bar, parity); ++i)
-    if (i % kPollsPerCheck == 0 && give_up(t0, abort, timeout)) return false;
-  return true;
-}
-__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, const volatile int* abort,
-                                          uint64_t timeout) {
-  uint64_t t0 = 0;
-  for (uint32_t i = 1; !__all_sync(0xffffffffu, mbar_try_wait(bar, parity)); ++i)
-    if (i % kPollsPerCheck == 0 &&
-        __shfl_sync(0xffffffffu, (int)give_up(t0, abort, timeout), 0))
-      return false;
-  return true;
-}
-
-// n / g for 0 <= n < 2^31: with 2^s the power of two from g on, g_mul = floor(2^(31+s)
-// / g) + 1 and n g_mul 2^-(31+s) exceeds n / g by less than 1 / g.
-__device__ __forceinline__ int group_div(const SharedParams& p, int n) {
-  return p.g == 1 ? n : (int)(__umulhi((uint32_t)n, p.g_mul) >> p.g_shift);
-}
 
 __device__ __forceinline__ SharedPiece load_piece(const SharedParams& p, int i) {
   const int4* w = reinterpret_cast<const int4*>(p.table + p.pieces) + 3LL * i;
@@ -172,8 +132,6 @@ __device__ __forceinline__ bool piece_ok(const SharedParams& p, const SharedPiec
          (long long)pc.kv_row + pc.keys <= p.num_kv_rows && pc.ws_row >= 0 &&
          (long long)pc.ws_row + pc.rows <= p.ws_rows;
 }
-__device__ __forceinline__ int num_tiles(int keys) { return (keys - 1) / BN + 1; }
-
 __device__ __forceinline__ SharedCta load_cta(const SharedParams& p) {
   const int4* w = reinterpret_cast<const int4*>(p.table) + 2LL * blockIdx.x;
   const int4 a = __ldg(w);
@@ -205,25 +163,6 @@ __device__ __forceinline__ bool check_list(const SharedParams& p, const SharedCt
   if (ok && c.single0 < c.single2) ok = tiles[0] == tiles[1] || tiles[0] == tiles[1] + 1;
   if (!ok && threadIdx.x == 0) set_status(p.status, CPATTN_ERR_RANGE);
   return ok;
-}
-
-// Byte offset of 16-code chunk `chunk` of row `row` in a raw e4m3 tile: rows of D bytes,
-// their chunks swizzled (128-byte swizzle at D = 128, 64-byte at D = 64).
-template <int D>
-__device__ __forceinline__ uint32_t code_at(int row, int chunk) {
-  return D == 128 ? row * 128 + ((chunk ^ (row & 7)) << 4) : row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4);
-}
-
-// Two barriers at once (their polls overlap).
-__device__ __forceinline__ bool wait_warp2(uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb,
-                                           const volatile int* abort, uint64_t timeout) {
-  uint64_t t0 = 0;
-  for (uint32_t i = 1;; ++i) {
-    const bool x = mbar_try_wait(a, pa), y = mbar_try_wait(b, pb);
-    if (__all_sync(0xffffffffu, x && y)) return true;
-    if (i % kPollsPerCheck == 0 && __shfl_sync(0xffffffffu, (int)give_up(t0, abort, timeout), 0))
-      return false;
-  }
 }
 
 // One K or V tile of the ring.
@@ -281,47 +220,6 @@ __device__ __forceinline__ bool for_each_ring_tile(const SharedParams& p, const 
   }
   return true;
 }
-
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-// Four e4m3 codes as f16, times m (f16 in both halves).
-__device__ __forceinline__ uint2 codes_to_f16(uint32_t c, uint32_t m) {
-  uint32_t h0, h1;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h0) : "h"((uint16_t)c));
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h1) : "h"((uint16_t)(c >> 16)));
-  return make_uint2(mul_f16x2(h0, m), mul_f16x2(h1, m));
-}
-__device__ __forceinline__ float exp2_int(int e) {  // e in [-126, 127]
-  return __uint_as_float((uint32_t)(e + 127) << 23);
-}
-// Exponent of a scale s >= 0, such that exp2_int takes it and its negative.
-__device__ __forceinline__ int exponent_of(float s) {
-  return min(max((int)(__float_as_uint(s) >> 23) - 127, -126), 126);
-}
-// Factor f s of a raw e4m3 score, f > 0 of its query row and s of its key (or key tile).
-// Not below a normal number: a zero row over zero keys would come to 0, and a masked -inf
-// times 0 is NaN.  Not infinite: a score of 0 between orthogonal large rows stays 0.  A
-// raw score is below 2^31 (2^15 448 d), so that with a raised factor it is still nothing.
-__device__ __forceinline__ float score_factor(float f, float s) {
-  return fminf(fmaxf(f * s, 0x1p-126f), 0x1.fffffep127f);
-}
-constexpr uint32_t idesc_16bit_f32(bool f16, int M, int N, int b_mn) {
-  return idesc_bf16_f32(M, N, 0, b_mn) & ~(f16 ? (1u << 7) | (1u << 10) : 0u);
-}
-
-// f16 weights are taken by a maximum that is kF16Lift too small: an f16 below 2^-14 loses
-// bits, which now begins at 2^-21 of the largest weight (and ends the weight at 2^-32),
-// and the largest stays below 2^16.
-constexpr float kF16Lift = 7.f;
-static_assert(kF16Lift + kMaxSlack < 16.f, "f16 range");
 
 // One KV tile for the rows of a warp (one per lane).  S from TMEM, masked to the `here`
 // visible keys of the tile, online softmax in base 2, P (16 bits) back over S, and where
@@ -396,18 +294,6 @@ __device__ __forceinline__ void softmax_tile(uint32_t s_addr, uint32_t o_addr, i
   tmem_wait_st();
   m_run = m_new;
   m_use = m_new_use;
-}
-
-// Partial rows in the workspace: those of one piece by chunks of 8 columns, so
-// that the lanes of a warp, a row each, store to one place.  Offset of column 8 c of row
-// r of `rows`, from the first row's place at D floats a row.
-__device__ __forceinline__ int partial_at(int c, int r, int rows) { return (c * rows + r) * 8; }
-
-// 32 bytes, a whole sector.
-__device__ __forceinline__ void store8(float* at, const float (&f)[8]) {
-  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(at), "f"(f[0]), "f"(f[1]),
-               "f"(f[2]), "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7])
-               : "memory");
 }
 
 }  // namespace
@@ -1240,23 +1126,6 @@ int launch_merge(const SharedParams& p, bool behind, cudaStream_t stream) {
   return p.g % 4 == 0   ? launch_merge<D, 4>(p, behind, stream)
          : p.g % 2 == 0 ? launch_merge<D, 2>(p, behind, stream)
                         : launch_merge<D, 1>(p, behind, stream);
-}
-
-// 3-D map of a code buffer (cols, heads, rows) with a D-column x 1-head box, rows
-// packed in shared memory and swizzled over their length (see code_at); out-of-range
-// rows read as zero.
-bool make_code_map(CUtensorMap* m, const void* base, int cols, int heads, long long rows,
-                   long long head_stride, long long row_stride, int box_rows) {
-  auto enc = tensor_map_encoder();
-  if (!enc) return false;
-  cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)heads, (cuuint64_t)rows};
-  cuuint64_t strides[2] = {(cuuint64_t)head_stride, (cuuint64_t)row_stride};
-  cuuint32_t box[3] = {(cuuint32_t)cols, 1, (cuuint32_t)box_rows};
-  cuuint32_t estr[3] = {1, 1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
-             CU_TENSOR_MAP_INTERLEAVE_NONE,
-             cols == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 struct SharedMaps {  // full tiles, then the tail boxes

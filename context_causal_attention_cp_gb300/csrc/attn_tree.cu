@@ -1,0 +1,188 @@
+// Attention of new rows (single tokens, chains, trees of drafted tokens) over a paged cache
+// (cp_attn_tree): the merge of cut units, and the host's part.
+#include <algorithm>
+#include <cstdint>
+
+#include <cuda_bf16.h>
+
+#include "attn_tree.cuh"
+#include "trace.h"
+
+namespace cpattn {
+namespace {
+
+// Merge of the units that the blocks' shares cut: block (x, y) takes the unit that is cut
+// behind attention block x, y a part of its values.  A row's partials (O_j, L_j) combine as
+//     m = max L_j, w_j = exp(L_j - m), O = sum w_j O_j / sum w_j, L = m + ln sum w_j.
+constexpr int kMergeThreads = 256;
+template <int D>
+__global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const TreeParams p) {
+  grid_dep_wait();
+  const int4 a = __ldcg(p.cut + 2 * blockIdx.x);
+  const int blocks = __ldcg(p.cut + 2 * blockIdx.x + 1).x;
+  if (blocks < 2 || blocks > (int)(gridDim.x - blockIdx.x)) return;
+  const int R = p.unit_rows, rows = a.z;
+  // half a chunk of 8 columns of a row
+  const int i = blockIdx.y * kMergeThreads + threadIdx.x, half = i & 1, r = (i >> 1) % R, c = (i >> 1) / R;
+  if (r >= rows || c >= D / 8) return;
+  auto slot_of = [&](int j) { return 2 * (int)blockIdx.x + (j == 0 ? 1 : 2 * j); };
+  float m = -INFINITY;
+#pragma unroll 8
+  for (int j = 0; j < blocks; ++j) m = fmaxf(m, __ldcg(p.ws_l + (long long)slot_of(j) * R + r));
+  const float use = m == -INFINITY ? 0.f : m;
+  float w = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+  for (int j = 0; j < blocks; ++j) {
+    const long long slot = (long long)slot_of(j) * R;
+    const float l = __ldcg(p.ws_l + slot + r);
+    const float4 x = __ldcg(reinterpret_cast<const float4*>(p.ws_o + slot * D + partial_at(c, r, R)) + half);
+    const float f = exp2f(l - use);
+    w += f;
+    if (f == 0.f) continue;
+    o.x = fmaf(f, x.x, o.x);
+    o.y = fmaf(f, x.y, o.y);
+    o.z = fmaf(f, x.z, o.z);
+    o.w = fmaf(f, x.w, o.w);
+  }
+  const float inv = w == 0.f ? 0.f : 1.f / w;
+  o = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+  const int packed = a.y + r, node = group_div(p, packed);
+  const long long at = (long long)(a.x + node) * p.Hq + a.w * p.g + packed - node * p.g;
+  const int col = c * 8 + half * 4;
+  if (p.o_f32)
+    *reinterpret_cast<float4*>(static_cast<float*>(p.o) + at * D + col) = o;
+  else
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + at * D + col) =
+        make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
+  if (col == 0) p.lse[at] = w == 0.f ? -INFINITY : (use + log2f(w)) * kLn2;
+}
+
+// Packed rows of a unit, by the rows that a request is expected to have.
+int unit_rows_of(int g, int max_nodes) {
+  (void)g;
+  (void)max_nodes;
+  return 8;
+}
+
+bool plan_sizes(int Hq, int Hkv, int dv, int max_nodes, int num_ctas, int* unit_rows, int64_t* o_at, int64_t* l_at,
+                int64_t* bytes) {
+  *unit_rows = unit_rows_of(Hq / Hkv, max_nodes);
+  const int64_t rows = 2LL * num_ctas * *unit_rows;
+  *o_at = 32LL * num_ctas;  // behind the cut units
+  *l_at = *o_at + rows * dv * 4;
+  *bytes = (*l_at + rows * 4 + 31) & ~31LL;
+  return true;
+}
+
+}  // namespace
+}  // namespace cpattn
+
+using namespace cpattn;
+
+extern "C" int cp_tree_workspace_size(int Hq, int Hkv, int dv, int max_nodes, int num_ctas, int64_t* bytes) {
+  if (!bytes || Hkv < 1 || Hq < Hkv || Hq % Hkv || Hq > 1 << 20 || max_nodes < 1 || num_ctas < 1 || num_ctas > 4096)
+    return CPATTN_ERR_INVALID_ARG;
+  if (dv != 64 && dv != 128) return CPATTN_ERR_UNSUPPORTED;
+  int rows;
+  int64_t o_at, l_at;
+  plan_sizes(Hq, Hkv, dv, max_nodes, num_ctas, &rows, &o_at, &l_at, bytes);
+  return CPATTN_OK;
+}
+
+extern "C" int cp_attn_tree(const void* q, int64_t q_row_stride, int64_t q_head_stride, int num_rows, const void* k,
+                            int64_t k_row_stride, int64_t k_head_stride, const float* k_scales, const void* v,
+                            int64_t v_row_stride, int64_t v_head_stride, const float* v_scales, int64_t scale_stride,
+                            int num_kv_rows, const int32_t* page_table, int64_t table_stride, int max_pages,
+                            int page_size, const int32_t* q_start, const int32_t* kv_lens, int num_reqs,
+                            const int32_t* mask, int mask_words, int Hq, int Hkv, int d, int dv, float scale,
+                            int max_nodes, int num_ctas, void* o, int o_is_fp32, float* lse, void* workspace,
+                            int64_t workspace_bytes, int32_t* status_dev, cudaStream_t stream) {
+  CPATTN_TRACE("cp_attn_tree");
+  int64_t need = 0;
+  const int rc = cp_tree_workspace_size(Hq, Hkv, dv, max_nodes, num_ctas, &need);
+  if (rc != CPATTN_OK) return rc;
+  if (d != dv) return CPATTN_ERR_UNSUPPORTED;
+  if (page_size < 16 || page_size > 65536 || (page_size & (page_size - 1))) return CPATTN_ERR_UNSUPPORTED;
+  if (!(scale > 0.f) || num_rows < 0 || num_kv_rows < 0 || num_reqs < 0 || num_reqs > CPATTN_MAX_REQS ||
+      max_pages < 0 || mask_words < 0 || (mask != nullptr) != (mask_words > 0) ||
+      (k_scales != nullptr) != (v_scales != nullptr) || (num_reqs > 1 && table_stride < max_pages))
+    return CPATTN_ERR_INVALID_ARG;
+  if ((long long)num_rows * (Hq / Hkv) > 0x7fffffffLL - CPATTN_SHARED_ROWS) return CPATTN_ERR_TOO_LARGE;
+  if (num_rows == 0 || num_reqs == 0) return CPATTN_OK;  // nothing to write
+  if (!q || !k || !v || !page_table || !q_start || !kv_lens || !o || !lse || !workspace || workspace_bytes < need ||
+      num_kv_rows < page_size || max_pages < 1)
+    return CPATTN_ERR_INVALID_ARG;
+  const bool quant = k_scales != nullptr;
+  const int64_t per16 = quant ? 16 : 8;  // elements in 16 bytes
+  if (!a16(q) || !a16(k) || !a16(v) || !a16(o) || (reinterpret_cast<uintptr_t>(workspace) & 31u) || q_row_stride % 8 ||
+      q_head_stride % 8 || k_row_stride % per16 || k_head_stride % per16 || v_row_stride % per16 ||
+      v_head_stride % per16)
+    return CPATTN_ERR_ALIGNMENT;
+  for (const void* at : {(const void*)k_scales, (const void*)v_scales, (const void*)page_table, (const void*)q_start,
+                         (const void*)kv_lens, (const void*)mask, (const void*)lse, (const void*)status_dev})
+    if (reinterpret_cast<uintptr_t>(at) & 3u) return CPATTN_ERR_ALIGNMENT;
+  if (q_row_stride < 0 || q_head_stride < 0 || k_head_stride < d || v_head_stride < dv ||
+      k_row_stride < (int64_t)(Hkv - 1) * k_head_stride + d || v_row_stride < (int64_t)(Hkv - 1) * v_head_stride + dv ||
+      (quant && scale_stride < num_kv_rows))
+    return CPATTN_ERR_INVALID_ARG;
+
+  TreeParams p{};
+  p.q_start = q_start;
+  p.kv_lens = kv_lens;
+  p.page_table = page_table;
+  p.mask = mask;
+  p.table_stride = table_stride;
+  p.num_reqs = num_reqs;
+  p.num_rows = num_rows;
+  p.max_pages = max_pages;
+  for (p.log_page = 4; (1 << p.log_page) < page_size; ++p.log_page) {}
+  p.words = mask_words;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.g = Hq / Hkv;
+  for (p.g_shift = 0; (1LL << (p.g_shift + 1)) < p.g; ++p.g_shift) {}  // see group_div
+  p.g_mul = (uint32_t)((1ULL << (32 + p.g_shift)) / p.g + 1);
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.q_row = q_row_stride;
+  p.q_head = q_head_stride;
+  p.ks = k_scales;
+  p.vs = v_scales;
+  p.s_head = scale_stride;
+  p.num_kv_rows = num_kv_rows;
+  p.scale_log2 = scale * kLog2e;
+  p.o = o;
+  p.o_f32 = o_is_fp32 ? 1 : 0;
+  p.lse = lse;
+  int64_t o_at, l_at, bytes;
+  plan_sizes(Hq, Hkv, dv, max_nodes, num_ctas, &p.unit_rows, &o_at, &l_at, &bytes);
+  p.cut = static_cast<int4*>(workspace);
+  p.ws_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + o_at);
+  p.ws_l = reinterpret_cast<float*>(static_cast<char*>(workspace) + l_at);
+  p.status = status_dev;
+  p.timeout_ns = attn_debug().timeout_ns;
+  p.withhold_q = attn_debug().withhold_q;
+  TreeMaps m;
+  const int whole = std::min(BN, page_size);
+  auto map = [&](CUtensorMap* t, const void* base, int64_t hs, int64_t rs, int box_rows) {
+    return quant ? make_code_map(t, base, d, Hkv, num_kv_rows, hs, rs, box_rows)
+                 : make_map(t, base, d, Hkv, num_kv_rows, hs, rs, box_rows);
+  };
+  if (!map(&m.k, k, k_head_stride, k_row_stride, whole) || !map(&m.v, v, v_head_stride, v_row_stride, whole) ||
+      !map(&m.k_tail, k, k_head_stride, k_row_stride, 16) || !map(&m.v_tail, v, v_head_stride, v_row_stride, 16))
+    return CPATTN_ERR_CUDA;
+  const int r = launch_tree_small(m, p, d, quant, num_ctas, stream);
+  if (r != CPATTN_OK) return r;
+  auto merge = d == 128 ? tree_merge_kernel<128> : tree_merge_kernel<64>;
+  const dim3 grid(num_ctas, (p.unit_rows * (d / 8) * 2 + kMergeThreads - 1) / kMergeThreads);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(kMergeThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, merge, p) == cudaSuccess ? CPATTN_OK : CPATTN_ERR_CUDA;
+}

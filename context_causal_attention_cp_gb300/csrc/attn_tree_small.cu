@@ -1,0 +1,678 @@
+// cp_attn_tree for few rows a request and KV head (a decode step, a short draft): warp-level
+// MMAs in registers.
+//
+// A 128-row MMA tile would be nearly empty, and HBM gives a block a KV tile of 128 keys every
+// 1.4 us (bf16, d = 128): so eight warps work on registers, with 16x8x16 MMAs that have keys
+// (and then the columns of V) as their 16 rows and queries as their 8 columns:
+//     S^T = K Q^T,   O^T += V^T P^T.
+// QW groups of warps share a KV tile's keys, 8 / QW warps to a group, and a group has NQ
+// columns of 8 rows: 8 * NQ * QW rows a unit.  Each warp keeps its own maximum, sum and
+// output; at a piece's end the 8 / QW of a row are joined in shared memory.  The ninth warp
+// loads: a tile's K and V pages by TMA, one lane a page, the query rows and (e4m3) the
+// scales by asynchronous copies, all of them ahead across piece ends.  A warp's step issues
+// the products of the next 16 keys between the softmax and the second product of these.
+//
+// Fragments are loaded as they lie in memory.  K Q^T sums over d in any order, so lane
+// (g = lane / 4, c = lane % 4) takes whole 16-byte chunks of key rows g and g + 8 and of
+// query row g the same ones: a chunk's elements 4x .. 4x+3 are its share of one k-step.
+// V of a bf16 tile goes through the transposing matrix load.  V codes: the lane reads the
+// g-th eighth of the columns of its keys 2c, 2c+1, 2c+8, 2c+9 and joins two rows' bytes into
+// a pair for each column, so rows g and g + 8 of product x are columns g D/8 + 2x and + 1.
+// Codes enter as f16, exact; K's scale multiplies the score, V's is taken relative to the
+// largest that the warp has met (O is rescaled when that grows).
+#include <algorithm>
+
+#include "attn_tree.cuh"
+
+namespace cpattn {
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kThreads = 384;  // a third warpgroup: the loading warp and three that idle
+constexpr int kRegsLaunch = 168, kRegsWork = 208, kRegsOther = 88;
+static_assert(kRegsWork * 256 + kRegsOther * 128 <= kRegsLaunch * kThreads, "register split exceeds the launch's");
+constexpr int kMaxStages = 12;
+
+template <int D, bool QUANT, int NQ, int QW>
+struct TreeCfg {
+  static constexpr int kRows = 8 * NQ * QW;  // of a unit
+  static constexpr int kKeyWarps = kWarps / QW;
+  static constexpr int kTile = BN * D * (QUANT ? 1 : 2);
+  static constexpr int kScales = QUANT ? BN * 4 : 0;  // the rows' scales, fp32
+  static constexpr int kQ = kRows * D * 2;            // two of them
+  static constexpr int kJoin = kWarps * 8 * NQ * D * 4;
+  static constexpr int kMl = kWarps * 8 * NQ * 8;
+  static constexpr int kFixed = 2 * kQ + kJoin + kMl + (2 * kMaxStages + 4) * 8 + 64 + 256 + 1024;
+  static constexpr int kFit = (232448 - kFixed) / (kTile + kScales);
+  static constexpr int kStages = kFit < kMaxStages ? kFit : kMaxStages;
+  static constexpr int kScaleOff = kStages * kTile;
+  static constexpr int kQOff = kScaleOff + kStages * kScales;
+  static constexpr int kJoinOff = kQOff + 2 * kQ;
+  static constexpr int kMlOff = kJoinOff + kJoin;  // (m, l) of each warp's rows
+  static constexpr int kBarOff = kMlOff + kMl;
+  static constexpr int kWordOff = kBarOff + (2 * kStages + 4) * 8;
+  static constexpr int kSumOff = kWordOff + 64;  // of tree_start
+  static constexpr int kSmemBytes = kSumOff + 256 + 1024;  // + align slack
+  static_assert(kStages >= 4 && kSmemBytes <= 232448, "shared memory budget");
+};
+
+// The 256 threads of the eight warps; true when any of them says so.
+__device__ __forceinline__ bool bar_warps(bool any) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+      "bar.red.or.pred q, 1, 256, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)any)
+      : "memory");
+  return r != 0;
+}
+
+// First element of the lane's 16-byte query chunk x: bf16, chunks 2c and 2c + 1 of each
+// 128 bytes; e4m3, the two halves of its code chunks (2c, 2c + 1 of a row of 128, c of 64).
+template <int D, bool QUANT>
+__device__ __forceinline__ int q_chunk(int c, int x) {
+  if (QUANT) return (D == 128 ? 2 * c + (x >> 1) : c) * 16 + (x & 1) * 8;
+  return (x >> 1) * 64 + (2 * c + (x & 1)) * 8;
+}
+// Place of column d of row r of a warp's part of the join buffer (bank swizzle: a store's
+// lanes have 8 columns, or 8 groups of four, of the rows 2 c + e).
+template <bool QUANT>
+__device__ __forceinline__ int join_at(int d, int r) {
+  return d ^ (((r >> 1) & 3) << (QUANT ? 2 : 3));
+}
+
+template <int D, bool QUANT, int NQ, int QW>
+struct Warp {
+  using C = TreeCfg<D, QUANT, NQ, QW>;
+  static constexpr int kOut = D / 16, kLoads = QUANT ? D / 64 : D / 32;
+  uint32_t base;  // shared memory
+  uint8_t* mem;
+  uint64_t *full, *empty, *q_full, *q_empty;
+  const volatile int* abort;
+  int warp, lane, g, c, row0, key0;  // row0: the warp's first row; key0: its first key of a tile
+
+  __device__ __forceinline__ void release(uint64_t* bar) const {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
+  }
+  __device__ __forceinline__ uint32_t scale_at(int slot, int row) const {
+    return base + C::kScaleOff + slot * C::kScales + row * 4;
+  }
+
+  // K of 16 keys from `key` on: chunks of rows g and g + 8, as they lie.
+  struct Keys {
+    uint4 v[2][kLoads];
+    float scale[2];
+  };
+  __device__ __forceinline__ void load_k(Keys& k, int slot, int key) const {
+    const uint32_t tile = base + slot * C::kTile;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int row = key + 8 * j + g;
+#pragma unroll
+      for (int x = 0; x < kLoads; ++x)
+        k.v[j][x] = QUANT ? lds128(tile + code_at<D>(row, D == 128 ? 2 * c + x : c))
+                          : lds128(tile + (x >> 1) * (BN * 128) + row * 128 +
+                                   (((2 * c + (x & 1)) ^ (row & 7)) << 4));
+      k.scale[j] = QUANT ? lds_f32(scale_at(slot, row)) : 1.f;
+    }
+  }
+  // s[n]: keys g (0, 1) and g + 8 (2, 3), rows 8n + 2c and 8n + 2c + 1; for one column of
+  // rows two chains, for their latency
+  __device__ __forceinline__ void product(const Keys& k, const uint32_t (&q)[NQ][kOut][2],
+                                          const float (&factor)[NQ][2], float (&s)[NQ][4]) const {
+    float s2[NQ][4];
+#pragma unroll
+    for (int n = 0; n < NQ; ++n)
+#pragma unroll
+      for (int y = 0; y < 4; ++y) s[n][y] = s2[n][y] = 0.f;
+#pragma unroll
+    for (int x = 0; x < kLoads; ++x) {
+      const uint32_t u0[4] = {k.v[0][x].x, k.v[0][x].y, k.v[0][x].z, k.v[0][x].w};
+      const uint32_t u1[4] = {k.v[1][x].x, k.v[1][x].y, k.v[1][x].z, k.v[1][x].w};
+      if constexpr (!QUANT) {
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) {
+          mma_16816<false>(s[n], u0[0], u1[0], u0[1], u1[1], q[n][2 * x][0], q[n][2 * x][1]);
+          mma_16816<false>(s2[n], u0[2], u1[2], u0[3], u1[3], q[n][2 * x + 1][0], q[n][2 * x + 1][1]);
+        }
+      } else {
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          const uint32_t a0 = e4m3x2_to_f16x2(u0[y]), a1 = e4m3x2_to_f16x2(u1[y]);
+          const uint32_t a2 = e4m3x2_to_f16x2(u0[y] >> 16), a3 = e4m3x2_to_f16x2(u1[y] >> 16);
+#pragma unroll
+          for (int n = 0; n < NQ; ++n)
+            mma_16816<true>(y & 1 ? s2[n] : s[n], a0, a1, a2, a3, q[n][4 * x + y][0], q[n][4 * x + y][1]);
+        }
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < NQ; ++n)
+#pragma unroll
+      for (int y = 0; y < 4; ++y)
+        s[n][y] = (s[n][y] + s2[n][y]) *
+                  (QUANT ? score_factor(factor[n][y & 1], k.scale[y >> 1]) : factor[n][y & 1]);
+  }
+
+  // Which of the 16 value rows from `key` of a tile on hold an infinity or NaN.
+  __device__ __forceinline__ uint32_t bad_rows(int slot, int key) const {
+    const uint32_t tile = base + slot * C::kTile;
+    const int row = key + (lane >> 1), half = lane & 1;
+    constexpr int kN = D * (QUANT ? 1 : 2) / 32;  // chunks of half a row
+    bool bad = false;
+#pragma unroll
+    for (int x = 0; x < kN; ++x) {
+      const int ch = half * kN + x;
+      const uint4 v = lds128(QUANT ? tile + code_at<D>(row, ch)
+                                   : tile + (ch >> 3) * (BN * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4));
+      const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int y = 0; y < 4; ++y)
+        if constexpr (QUANT)
+          bad = bad || __vcmpeq4(u[y] & 0x7F7F7F7Fu, 0x7F7F7F7Fu) != 0;
+        else
+          bad = bad || __vcmpgeu2(u[y] & 0x7FFF7FFFu, 0x7F807F80u) != 0;
+    }
+    return __reduce_or_sync(0xffffffffu, bad ? 1u << (lane >> 1) : 0u);
+  }
+
+  __device__ bool piece(const TreeParams& p, const TreePiece& pc, int n_piece, int& seq) const;
+};
+
+template <int D, bool QUANT, int NQ, int QW>
+__device__ __forceinline__ bool Warp<D, QUANT, NQ, QW>::piece(const TreeParams& p, const TreePiece& pc, int n_piece,
+                                                              int& seq) const {
+  constexpr int NS = C::kStages;
+  const unsigned all = 0xffffffffu;
+  const int T = pc.tiles, qb = n_piece & 1;
+  const int tile0 = pc.t0 * BN;  // first key
+  // ---- queries: row g of each column ----
+  uint32_t q[NQ][kOut][2];
+  float factor[NQ][2];
+  bool ok = wait_warp(q_full + qb, (n_piece >> 1) & 1, abort, p.timeout_ns);
+#pragma unroll
+  for (int n = 0; n < NQ; ++n) {
+    uint4 v[D / 32];
+    const int row = row0 + 8 * n + g;
+#pragma unroll
+    for (int x = 0; x < D / 32; ++x) {
+      v[x] = lds128(base + C::kQOff + qb * C::kQ + row * (D * 2) +
+                    (((q_chunk<D, QUANT>(c, x) >> 3) ^ (row & 7)) << 4));
+      if (row >= pc.rows) v[x] = make_uint4(0, 0, 0, 0);
+    }
+    float f_row = p.scale_log2;
+    if constexpr (QUANT) {
+      // bf16 to f16 times 2^f with 2^f max|q| in [2^14, 2^15)
+      uint32_t mx = 0;
+#pragma unroll
+      for (int x = 0; x < D / 32; ++x)
+        mx = __vmaxu2(__vmaxu2(mx, __vmaxu2(v[x].x & 0x7FFF7FFFu, v[x].y & 0x7FFF7FFFu)),
+                      __vmaxu2(v[x].z & 0x7FFF7FFFu, v[x].w & 0x7FFF7FFFu));
+      mx = max(mx & 0xFFFFu, mx >> 16);
+      mx = max(mx, __shfl_xor_sync(all, mx, 1));
+      mx = max(mx, __shfl_xor_sync(all, mx, 2));
+      const int f = min(max(14 - ((int)(mx >> 7) - 127), -126), 126);
+      const float up = exp2_int(f);
+      f_row *= exp2_int(-f);
+#pragma unroll
+      for (int x = 0; x < D / 32; ++x) {
+        uint32_t* const u = &v[x].x;
+#pragma unroll
+        for (int y = 0; y < 4; ++y)
+          u[y] = pack_f16x2(__uint_as_float(u[y] << 16) * up, __uint_as_float(u[y] & 0xFFFF0000u) * up);
+      }
+    }
+    factor[n][0] = __shfl_sync(all, f_row, 8 * c);      // of row 2c
+    factor[n][1] = __shfl_sync(all, f_row, 8 * c + 4);  // and the next
+#pragma unroll
+    for (int x = 0; x < D / 32; ++x) {
+      q[n][2 * x][0] = v[x].x;
+      q[n][2 * x][1] = v[x].y;
+      q[n][2 * x + 1][0] = v[x].z;
+      q[n][2 * x + 1][1] = v[x].w;
+    }
+  }
+  release(q_empty + qb);
+  float o[NQ][kOut][4], m_run[NQ][2], m_use[NQ][2], l_run[NQ][2];
+#pragma unroll
+  for (int n = 0; n < NQ; ++n) {
+#pragma unroll
+    for (int x = 0; x < kOut; ++x)
+#pragma unroll
+      for (int y = 0; y < 4; ++y) o[n][x][y] = 0.f;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      m_run[n][e] = -INFINITY;
+      m_use[n][e] = l_run[n][e] = 0.f;
+    }
+  }
+  const bool rows_live = row0 < pc.rows;  // (the warp has rows)
+  int ev = -126;  // (e4m3) exponent of O
+  Keys k;
+  float s[NQ][4];
+  ok = ok && wait_warp(full + seq % NS, (seq / NS) & 1, abort, p.timeout_ns);
+  if (ok) {
+    if (rows_live && tile0 + key0 < pc.keys) {
+      load_k(k, seq % NS, key0);
+      product(k, q, factor, s);
+    }
+    if (QW == 1) release(empty + seq % NS);
+  }
+  for (int t = 0; t < T && ok; ++t, seq += 2) {
+    const int k_now = seq % NS, v_slot = (seq + 1) % NS, k_next = (seq + 2) % NS;
+    const bool more = t + 1 < T;
+    ok = wait_warp(full + v_slot, ((seq + 1) / NS) & 1, abort, p.timeout_ns) &&
+         (!more || wait_warp(full + k_next, ((seq + 2) / NS) & 1, abort, p.timeout_ns));
+    if (!ok) break;
+    const uint32_t tile = base + v_slot * C::kTile;
+#pragma unroll 1
+    for (int step = 0; step < QW; ++step) {
+      const bool last_step = step == QW - 1;
+      const int key = key0 + 16 * step, at = tile0 + t * BN + key;  // in the tile, of the request
+      const bool work = rows_live && at < pc.keys;
+      const int at_next = last_step ? tile0 + (t + 1) * BN + key0 : at + 16;
+      const bool next_work = rows_live && (last_step ? more : true) && at_next < pc.keys;
+      if (next_work) load_k(k, last_step ? k_next : k_now, last_step ? key0 : key + 16);
+      // value rows that count: up to the last key, and (new keys) finite
+      uint32_t alive = 0xFFFFu;
+      // (e4m3) the lane's codes of the keys 2c, 2c + 1, 2c + 8, 2c + 9, and their scales
+      uint32_t u[4][D / 32];
+      float f[4];
+      uint32_t pb[NQ][2];
+      if (work) {
+        if (pc.keys - at < 16) alive >>= 16 - (pc.keys - at);
+        if (at + 16 > pc.req.L) {  // new keys among them: who sees which
+          const uint32_t bad = bad_rows(v_slot, key) & alive & ~((1u << min(16, max(0, pc.req.L - at))) - 1u);
+          alive &= ~bad;
+#pragma unroll
+          for (int n = 0; n < NQ; ++n)
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              const int kk = g + (y >> 1) * 8, node = at + kk - pc.req.L;
+              const int r = row0 + 8 * n + 2 * c + (y & 1);
+              if (node < 0 || r >= pc.rows) continue;
+              if (node >= pc.req.T || !sees(p, pc.req, group_div(p, pc.r0 + r), node)) s[n][y] = -INFINITY;
+              else if ((bad >> kk) & 1u) s[n][y] = __uint_as_float(0x7FC00000u);  // the row becomes NaN
+            }
+        }
+        if constexpr (QUANT) {
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const int row = key + 2 * c + (x >> 1) * 8 + (x & 1);
+            f[x] = lds_f32(scale_at(v_slot, row));
+            if constexpr (D == 128) {
+              const uint4 v = lds128(tile + code_at<D>(row, g));
+              u[x][0] = v.x; u[x][1] = v.y; u[x][2] = v.z; u[x][3] = v.w;
+            } else {
+              const uint2 v = lds64(tile + code_at<D>(row, g >> 1) + (g & 1) * 8);
+              u[x][0] = v.x; u[x][1] = v.y;
+            }
+          }
+          if (alive != 0xFFFFu) {
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              if (!((alive >> (2 * c + (x >> 1) * 8 + (x & 1))) & 1u)) {
+                f[x] = 0.f;
+#pragma unroll
+                for (int y = 0; y < D / 32; ++y) u[x][y] = 0u;
+              }
+          }
+        }
+        // ---- softmax, base 2; the maximum moves only when a step raises it by more than
+        // kMaxSlack, so that O is seldom rescaled ----
+        bool any = false;
+        float alpha[NQ][2];
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            // keys behind the last
+            if (pc.keys - at < 16) {
+              if (at + g >= pc.keys) s[n][e] = -INFINITY;
+              if (at + g + 8 >= pc.keys) s[n][e + 2] = -INFINITY;
+            }
+            float mx = fmaxf(s[n][e], s[n][e + 2]);
+            mx = fmaxf(mx, __shfl_xor_sync(all, mx, 4));
+            mx = fmaxf(mx, __shfl_xor_sync(all, mx, 8));
+            mx = fmaxf(mx, __shfl_xor_sync(all, mx, 16));
+            if (QUANT) mx -= kF16Lift;
+            const bool move = mx > m_run[n][e] + kMaxSlack;
+            const float m_new = move ? mx : m_run[n][e];
+            const float use = m_new == -INFINITY ? 0.f : m_new;
+            alpha[n][e] = move ? ex2_approx(m_run[n][e] - use) : 1.f;
+            any = any || move;
+            m_run[n][e] = m_new;
+            m_use[n][e] = use;
+            const float a = ex2_approx(s[n][e] - use), z = ex2_approx(s[n][e + 2] - use);
+            l_run[n][e] = l_run[n][e] * alpha[n][e] + (a + z);
+            s[n][e] = a;
+            s[n][e + 2] = z;
+          }
+          // P in 16 bits, the second product's operand type: off by at most 2^-8 (bf16) or
+          // 2^-11 (f16) of each weight; l sums the unrounded values.  Queries by rows, keys
+          // by columns now
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh)
+            pb[n][hh] = transpose_8x8(QUANT ? pack_f16x2(s[n][2 * hh], s[n][2 * hh + 1])
+                                            : pack_bf16x2(s[n][2 * hh], s[n][2 * hh + 1]));
+        }
+        if (__any_sync(all, any)) {
+#pragma unroll
+          for (int n = 0; n < NQ; ++n)
+#pragma unroll
+            for (int x = 0; x < kOut; ++x)
+#pragma unroll
+              for (int y = 0; y < 4; ++y) o[n][x][y] *= alpha[n][y & 1];
+        }
+      }
+      // ---- the next keys' S, then O += P V ----
+      if (next_work) product(k, q, factor, s);
+      if (last_step) {
+        if (QW > 1) release(empty + k_now);
+        else if (more) release(empty + k_next);
+      }
+      if (work) {
+        if constexpr (!QUANT) {
+          // keys 2c, 2c + 1 (and + 8) of a column
+          uint32_t mask[2] = {~0u, ~0u};
+          if (alive != 0xFFFFu)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const uint32_t two = alive >> (2 * c + 8 * x);
+              mask[x] = (two & 1u ? 0xFFFFu : 0u) | (two & 2u ? 0xFFFF0000u : 0u);
+            }
+          // matrix x of the load: columns 8 (x & 1) of 16, keys 8 (x >> 1)
+          const int row = key + (lane & 7) + 8 * (lane >> 4), col = (lane >> 3) & 1;
+#pragma unroll
+          for (int x = 0; x < kOut; ++x) {
+            const int chunk = 2 * x + col;
+            const uint32_t from = tile + (chunk >> 3) * (BN * 128) + row * 128 + (((chunk & 7) ^ (row & 7)) << 4);
+            uint32_t v[4];
+            asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                         : "r"(from));
+#pragma unroll
+            for (int n = 0; n < NQ; ++n)
+              mma_16816<false>(o[n][x], v[0] & mask[0], v[1] & mask[0], v[2] & mask[1], v[3] & mask[1], pb[n][0],
+                               pb[n][1]);
+          }
+        } else {
+          // factors of the lane's keys, relative to 2^ev
+          const int e = exponent_of(__uint_as_float(
+              __reduce_max_sync(all, __float_as_uint(fmaxf(fmaxf(f[0], f[1]), fmaxf(f[2], f[3]))))));
+          if (e > ev) {  // (the same for the warp)
+            const float down = exp2_int(max(ev - e, -126));
+#pragma unroll
+            for (int n = 0; n < NQ; ++n)
+#pragma unroll
+              for (int x = 0; x < kOut; ++x)
+#pragma unroll
+                for (int y = 0; y < 4; ++y) o[n][x][y] *= down;
+            ev = e;
+          }
+          const float inv = exp2_int(-ev);
+          const uint32_t f0 = pack_f16x2(f[0] * inv, f[1] * inv), f1 = pack_f16x2(f[2] * inv, f[3] * inv);
+#pragma unroll
+          for (int x = 0; x < kOut; ++x) {  // columns 2x, 2x + 1 of the lane's
+            const uint32_t a = __byte_perm(u[0][x >> 1], u[1][x >> 1], x & 1 ? 0x7362 : 0x5140);
+            const uint32_t z = __byte_perm(u[2][x >> 1], u[3][x >> 1], x & 1 ? 0x7362 : 0x5140);
+            const uint32_t a0 = mul_f16x2(e4m3x2_to_f16x2(a), f0), a1 = mul_f16x2(e4m3x2_to_f16x2(a >> 16), f0);
+            const uint32_t a2 = mul_f16x2(e4m3x2_to_f16x2(z), f1), a3 = mul_f16x2(e4m3x2_to_f16x2(z >> 16), f1);
+#pragma unroll
+            for (int n = 0; n < NQ; ++n) mma_16816<true>(o[n][x], a0, a1, a2, a3, pb[n][0], pb[n][1]);
+          }
+        }
+      }
+    }
+    release(empty + v_slot);
+  }
+  // ---- join the warps of a row: O = sum_w f_w O_w / L, f_w = 2^(m_w - M), L = sum f_w l_w ----
+  const float down = exp2_int(ev);
+  float* const join = reinterpret_cast<float*>(mem + C::kJoinOff);
+  float2* const ml = reinterpret_cast<float2*>(mem + C::kMlOff);
+  bar_warps(false);  // the buffer's last readers
+#pragma unroll
+  for (int n = 0; n < NQ; ++n)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float l = l_run[n][e];
+      l += __shfl_xor_sync(all, l, 4);
+      l += __shfl_xor_sync(all, l, 8);
+      l += __shfl_xor_sync(all, l, 16);
+      const int r = 8 * n + 2 * c + e;  // of the warp's
+      if (g == 0) ml[warp * (8 * NQ) + r] = make_float2(m_use[n][e], l);
+      float* const dst = join + (warp * (8 * NQ) + r) * D;
+      if constexpr (!QUANT) {
+#pragma unroll
+        for (int x = 0; x < kOut; ++x) {
+          dst[join_at<QUANT>(16 * x + g, r)] = o[n][x][e];
+          dst[join_at<QUANT>(16 * x + 8 + g, r)] = o[n][x][e + 2];
+        }
+      } else {
+#pragma unroll
+        for (int x = 0; x < kOut; x += 2)
+          *reinterpret_cast<float4*>(dst + join_at<QUANT>(g * (D / 8) + 2 * x, r)) =
+              make_float4(o[n][x][e] * down, o[n][x][e + 2] * down, o[n][x + 1][e] * down, o[n][x + 1][e + 2] * down);
+      }
+    }
+  // (a warp that gave up still comes here, so that none waits for it)
+  ok = !bar_warps(!ok);
+  if (!ok) return false;
+  for (int i = warp * 32 + lane; i < pc.rows * (D / 4); i += 32 * kWarps) {
+    const int r = i / (D / 4), d = i % (D / 4) * 4;  // row, column
+    const int first = r / (8 * NQ), in = r % (8 * NQ);  // its first warp (every QW-th after), row of the warp's
+    float M = -INFINITY, Lsum = 0.f;
+    float2 v[C::kKeyWarps];
+#pragma unroll
+    for (int y = 0; y < C::kKeyWarps; ++y) {
+      v[y] = ml[(first + y * QW) * (8 * NQ) + in];
+      if (v[y].y != 0.f) M = fmaxf(M, v[y].x);  // (m of a warp without keys means nothing)
+    }
+    if (M == -INFINITY) M = 0.f;
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int y = 0; y < C::kKeyWarps; ++y) {
+      const float4 part =
+          *reinterpret_cast<const float4*>(join + ((first + y * QW) * (8 * NQ) + in) * D + join_at<QUANT>(d, in));
+      if (v[y].y == 0.f) continue;
+      const float fw = ex2_approx(v[y].x - M);
+      Lsum += fw * v[y].y;
+      sum.x = fmaf(fw, part.x, sum.x);
+      sum.y = fmaf(fw, part.y, sum.y);
+      sum.z = fmaf(fw, part.z, sum.z);
+      sum.w = fmaf(fw, part.w, sum.w);
+    }
+    const float inv = Lsum == 0.f ? 0.f : 1.f / Lsum;
+    const float4 out = make_float4(sum.x * inv, sum.y * inv, sum.z * inv, sum.w * inv);
+    const float lse2 = Lsum == 0.f ? -INFINITY : M + lg2_approx(Lsum);
+    if (pc.slot >= 0) {
+      const long long slot = (long long)pc.slot * C::kRows;
+      *reinterpret_cast<float4*>(p.ws_o + slot * D + partial_at(d >> 3, r, C::kRows) + (d & 4)) = out;
+      if (d == 0) p.ws_l[slot + r] = lse2;
+    } else {
+      const int packed = pc.r0 + r, node = group_div(p, packed);
+      const long long at = (long long)(pc.req.row0 + node) * p.Hq + pc.kv_head * p.g + packed - node * p.g;
+      if (p.o_f32)
+        *reinterpret_cast<float4*>(static_cast<float*>(p.o) + at * D + d) = out;
+      else
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + at * D + d) =
+            make_uint2(pack_bf16x2(out.x, out.y), pack_bf16x2(out.z, out.w));
+      if (d == 0) p.lse[at] = lse2 * kLn2;
+    }
+  }
+  return true;
+}
+
+template <int D, bool QUANT, int NQ, int QW>
+__global__ void __launch_bounds__(kThreads, 1)
+attn_tree_small_kernel(const __grid_constant__ TreeMaps maps, const TreeParams p) {
+  using C = TreeCfg<D, QUANT, NQ, QW>;
+  constexpr int NS = C::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
+  uint64_t* empty = full + NS;
+  uint64_t* q_full = empty + NS;
+  uint64_t* q_empty = q_full + 2;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kWordOff);
+  volatile int* issued_loads = abort_flag + 1;
+  long long* found = reinterpret_cast<long long*>(smem + C::kWordOff + 16);
+  long long* sums = reinterpret_cast<long long*>(smem + C::kSumOff);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  grid_dep_trigger();  // the merge may be scheduled as blocks of this grid end
+  if (threadIdx.x == 0) {
+    prefetch_tmap(&maps.k);
+    prefetch_tmap(&maps.v);
+    prefetch_tmap(&maps.k_tail);
+    prefetch_tmap(&maps.v_tail);
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(full + i, QUANT ? 33 : 1);  // the TMA copies and each lane's scales
+      mbar_init(empty + i, kWarps);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(q_full + i, 32);  // each lane's copies
+      mbar_init(q_empty + i, kWarps);
+    }
+    *abort_flag = 0;
+    *issued_loads = 0;
+    fence_barrier_init();
+  }
+  TreeWalk walk{tree_start(p, sums, found)};  // (its barriers publish those above)
+  TreePiece pc;
+  auto arrive_copies = [&](uint64_t* bar) {  // when this lane's copies so far have landed
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+  };
+  if (warp >= kWarps) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
+  else asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsWork));
+  if (warp == kWarps) {
+    constexpr int kChunks = QUANT ? 1 : D / 64;     // boxes across a row
+    constexpr int kLine = C::kTile / BN / kChunks;  // bytes of a box row
+    const int whole = min(BN, 1 << p.log_page);     // rows of a whole box
+    int seq = 0, cut = 0;
+    bool ok = true;
+    for (int n = 0; ok && walk.next(p, pc); ++n) {
+      const int qb = n & 1;
+      if (pc.blocks) {
+        cut = pc.blocks;
+        if (lane == 0) put_cut(p, pc, cut);
+      }
+      ok = wait_warp(q_empty + qb, ((n >> 1) & 1) ^ 1, abort_flag, p.timeout_ns);
+      if (!ok) break;
+      // the query rows, 16-byte chunks swizzled over a row's length
+      for (int x = lane; x < pc.rows * (D / 8); x += 32) {
+        const int r = x / (D / 8), ch = x % (D / 8), packed = pc.r0 + r, node = group_div(p, packed);
+        const __nv_bfloat16* src = p.q + (long long)(pc.req.row0 + node) * p.q_row +
+                                   (long long)(pc.kv_head * p.g + packed - node * p.g) * p.q_head + ch * 8;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                         smem_u32(smem + C::kQOff + qb * C::kQ) + r * (D * 2) + ((ch ^ (r & 7)) << 4)),
+                     "l"(src)
+                     : "memory");
+      }
+      if (!p.withhold_q) arrive_copies(q_full + qb);
+      for (int t = 0; t < pc.tiles && ok; ++t) {
+        const int key0 = (pc.t0 + t) * BN, live = min(BN, pc.keys - key0);
+        // a lane's box: whole pages, or 16 rows of the tile's end
+        const int box = live > BN - 16 ? whole : 16, boxes = (live + box - 1) / box;
+        const int mine = lane < boxes ? cache_row(p, pc.b, key0 + lane * box) : 0;
+        // (e4m3) the cache rows of the lane's scales, keys x * 32 + lane
+        int srow[4] = {0, 0, 0, 0};
+        if constexpr (QUANT) {
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const int key = x * 32 + lane;
+            srow[x] = __shfl_sync(0xffffffffu, mine, (key / box) & 31) + key % box;
+          }
+        }
+        for (int kv = 0; kv < 2; ++kv, ++seq) {
+          const int slot = seq % NS;
+          ok = wait_warp(empty + slot, ((seq / NS) & 1) ^ 1, abort_flag, p.timeout_ns);
+          if (!ok) break;
+          uint8_t* dst = smem + slot * C::kTile;
+          if (lane == 0) mbar_arrive_expect_tx(full + slot, boxes * box * kLine * kChunks);
+          __syncwarp();
+          if (lane < boxes) {
+            const CUtensorMap* tm = box == whole ? (kv ? &maps.v : &maps.k) : (kv ? &maps.v_tail : &maps.k_tail);
+#pragma unroll
+            for (int c = 0; c < kChunks; ++c)
+              tma_load_3d(dst + (c * BN + lane * box) * kLine, tm, full + slot, c * 64, pc.kv_head, mine);
+          }
+          if constexpr (QUANT) {
+            const float* src = (kv ? p.vs : p.ks) + (long long)pc.kv_head * p.s_head;
+            const uint32_t at = smem_u32(smem + C::kScaleOff + slot * C::kScales) + lane * 4;
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              if (x * 32 + lane < live && srow[x] < p.num_kv_rows)
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(at + x * 128), "l"(src + srow[x])
+                             : "memory");
+            arrive_copies(full + slot);
+          }
+        }
+      }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    if (lane == 0) {
+      if (!cut) p.cut[2 * blockIdx.x + 1] = make_int4(0, 0, 0, 0);
+      *issued_loads = seq;
+      if (!ok) {
+        set_status(p.status, CPATTN_ERR_TIMEOUT);
+        *abort_flag = 1;
+      }
+    }
+  } else if (warp < kWarps) {
+    Warp<D, QUANT, NQ, QW> w;
+    w.base = smem_u32(smem);
+    w.mem = smem;
+    w.full = full;
+    w.empty = empty;
+    w.q_full = q_full;
+    w.q_empty = q_empty;
+    w.abort = abort_flag;
+    w.warp = warp;
+    w.lane = lane;
+    w.g = lane >> 2;
+    w.c = lane & 3;
+    w.row0 = warp % QW * (8 * NQ);
+    w.key0 = warp / QW * (16 * QW);
+    int seq = 0;
+    bool ok = true;
+    for (int n = 0; ok && walk.next(p, pc); ++n) ok = w.piece(p, pc, n, seq);
+    if (!ok && lane == 0) {
+      set_status(p.status, CPATTN_ERR_TIMEOUT);
+      *abort_flag = 1;
+    }
+  }
+  __syncthreads();
+  if (warp == kWarps && lane == 0 && *abort_flag) {
+    // let the copies in flight land before the shared memory goes
+    const int n = *issued_loads;
+    for (int j = max(0, n - NS); j < n; ++j) wait_one(full + j % NS, (j / NS) & 1, nullptr, p.timeout_ns);
+  }
+}
+
+template <int D, bool QUANT, int NQ, int QW>
+int launch(const TreeMaps& m, const TreeParams& p, int num_ctas, cudaStream_t stream) {
+  using C = TreeCfg<D, QUANT, NQ, QW>;
+  auto kern = attn_tree_small_kernel<D, QUANT, NQ, QW>;
+  if (!allow_smem(kern, C::kSmemBytes)) return CPATTN_ERR_CUDA;
+  if (!split_covered(kern, kThreads, kRegsWork * 256 + kRegsOther * 128)) return CPATTN_ERR_UNSUPPORTED;
+  return launch_kernel(kern, (unsigned)num_ctas, kThreads, C::kSmemBytes, stream, false, m, p) == cudaSuccess
+             ? CPATTN_OK
+             : CPATTN_ERR_CUDA;
+}
+template <int NQ, int QW>
+int launch(const TreeMaps& m, const TreeParams& p, int d, bool quant, int num_ctas, cudaStream_t stream) {
+  return d == 128 ? (quant ? launch<128, true, NQ, QW>(m, p, num_ctas, stream)
+                           : launch<128, false, NQ, QW>(m, p, num_ctas, stream))
+                  : (quant ? launch<64, true, NQ, QW>(m, p, num_ctas, stream)
+                           : launch<64, false, NQ, QW>(m, p, num_ctas, stream));
+}
+
+}  // namespace
+
+int launch_tree_small(const TreeMaps& m, const TreeParams& p, int d, bool quant, int num_ctas, cudaStream_t stream) {
+  return launch<1, 1>(m, p, d, quant, num_ctas, stream);
+}
+
+}  // namespace cpattn

@@ -1,0 +1,442 @@
+// Rotary positions, alone (cp_rope) and on the way into a KV cache (cp_kv_append).
+//
+// Pair c of a vector, (a, b), becomes (a cos t - b sin t, b cos t + a sin t) with the angle
+// t = p f_c, p the row's position on the pair's axis; the inverse takes -t.  A position
+// times a frequency is up to 2^31 turns, of which fp32 would keep none of the fraction.
+// So a frequency is held in turns as a 64-bit fraction F (f / 2 pi mod 1, times 2^64), and
+// p F mod 2^64 is the phase, exact but for F's rounding: off by |p| 2^-65 turns, two integer
+// multiplications for its upper 32 bits.  The quarter turn next to it is split off before
+// the rest goes to fp32, so that cos and sin are good to fp32 at any position.
+//
+// One kernel for both calls, an HBM stream: a block takes a few rows, computes their cos and
+// sin once into shared memory (they serve all heads) and then rotates, rounds or quantises
+// the rows' vectors.  L = 2^k lanes share a vector; a lane's item is two 16-byte chunks (of
+// bf16) that hold 8 pairs, or 16 columns that are not rotated.
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include <cuda_bf16.h>
+
+#include "../../include/cpattn.h"
+#include "kv_codes.cuh"
+#include "ptx.cuh"
+#include "trace.h"
+
+namespace cpattn {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMaxDim = 1024;
+constexpr int kMaxCs = 2048;  // cos and sin values of a block's rows
+constexpr int kItem = 16;     // columns of an item
+
+struct RopeSide {  // Q, K or V
+  const void* x;
+  long long x_row, x_head;  // elements
+  uint8_t* y;               // codes, or values
+  long long y_row, y_head;  // bytes
+  float* scales;            // codes' scales, or null
+  long long s_head;
+  int heads, dim;
+  int rotated;  // items that hold pairs (0: none)
+  int cached;   // rows go to their slots, as bf16 or codes; else to their own place, in x's type
+};
+
+struct RopeParams {
+  RopeSide side[3];
+  const int4* table;  // (F low, F high, axis, 0) of each pair
+  const int32_t* positions;
+  long long axis_stride;
+  int pairs, first, axes, inverse;
+  const int32_t* slots;
+  int num_rows, cache_rows, vectors, rows, log_l;  // rows: of a block
+  int32_t* status;
+};
+
+// cos and sin of position p (sign-extended to 64 bits) times frequency F.
+__device__ __forceinline__ float2 cos_sin(int p, uint32_t f_lo, uint32_t f_hi) {
+  const uint32_t u = (uint32_t)p;
+  const uint32_t phase = __umulhi(u, f_lo) + u * f_hi - (p < 0 ? f_lo : 0u);  // 2^-32 turns
+  const uint32_t quarter = (phase + 0x20000000u) >> 30;  // nearest, mod 4
+  const float rest = (float)(int)(phase - (quarter << 30)) * 0x1p-31f;  // half turns, |rest| <= 1/4
+  float s, c;
+  sincospif(rest, &s, &c);
+  const float a = quarter & 1 ? s : c, b = quarter & 1 ? c : s;
+  // quarters 0..3: (c, s), (-s, c), (-c, -s), (s, -c)
+  return make_float2(quarter == 1 || quarter == 2 ? -a : a, quarter >= 2 ? -b : b);
+}
+
+// 8 consecutive elements.
+template <bool F32>
+__device__ __forceinline__ void load8(const void* x, long long at, float* f) {
+  if constexpr (F32) {
+    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(x) + at);
+    const float4 a = __ldcs(p), b = __ldcs(p + 1);
+    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+  } else {
+    const uint4 v = __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(x) + at));
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = __uint_as_float(w[i] << 16);
+      f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+  }
+}
+__device__ __forceinline__ void store8_bf16(uint8_t* at, const float* f) {
+  *reinterpret_cast<uint4*>(at) = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
+                                             pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+}
+__device__ __forceinline__ void store8_f32(uint8_t* at, const float* f) {
+  reinterpret_cast<float4*>(at)[0] = make_float4(f[0], f[1], f[2], f[3]);
+  reinterpret_cast<float4*>(at)[1] = make_float4(f[4], f[5], f[6], f[7]);
+}
+__device__ __forceinline__ void store8_codes(uint8_t* at, const float* f, float inv) {
+  uint32_t w[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+    w[j] = (uint32_t)e4m3x2(f[4 * j] * inv, f[4 * j + 1] * inv) |
+           (uint32_t)e4m3x2(f[4 * j + 2] * inv, f[4 * j + 3] * inv) << 16;
+  *reinterpret_cast<uint2*>(at) = make_uint2(w[0], w[1]);
+}
+
+// NI: items of a lane.  INTER: pairs are neighbours (a rotated item's chunks then lie
+// side by side); else (c, c + pairs).
+template <bool F32, bool INTER, int NI>
+__global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p) {
+  __shared__ __align__(16) float2 cs[2][kMaxCs];
+  const int L = 1 << p.log_l, lane = threadIdx.x & (L - 1), group = threadIdx.x >> p.log_l;
+  const uint32_t mask = (L == 32 ? 0xffffffffu : (1u << L) - 1u) << (threadIdx.x & 31 & ~(L - 1));
+  const int c_rot = INTER ? 8 : p.pairs;  // columns from an item's first chunk to its second
+  int buf = 0;
+  for (long long r0 = (long long)blockIdx.x * p.rows; r0 < p.num_rows; r0 += (long long)gridDim.x * p.rows) {
+    const int rows = (int)min((long long)p.rows, p.num_rows - r0);
+    if (p.pairs > 0) {
+      for (int r = 0; r < rows; ++r)
+        for (int c = threadIdx.x; c < p.pairs; c += kThreads) {
+          const int4 f = __ldg(p.table + c);
+          const bool ok = f.z >= 0 && f.z < p.axes;
+          if (!ok) set_status(p.status, CPATTN_ERR_RANGE);
+          const int at = ok ? __ldg(p.positions + f.z * p.axis_stride + r0 + r) : 0;
+          float2 v = cos_sin(at, (uint32_t)f.x, (uint32_t)f.y);
+          if (p.inverse) v.y = -v.y;
+          cs[buf][r * p.pairs + c] = v;
+        }
+      __syncthreads();
+    }
+    for (int u = group; u < rows * p.vectors; u += kThreads >> p.log_l) {
+      const int r = u / p.vectors, vec = u - r * p.vectors;
+      const long long row = r0 + r;
+      const int h0 = p.side[0].heads, h1 = h0 + p.side[1].heads;
+      const RopeSide& s = vec < h0 ? p.side[0] : vec < h1 ? p.side[1] : p.side[2];
+      const int h = vec < h0 ? vec : vec < h1 ? vec - h0 : vec - h1;
+      long long to = row;
+      if (s.cached) {
+        if (p.slots) to = __ldg(p.slots + row);
+        if (to >= p.cache_rows) {
+          if (lane == 0) set_status(p.status, CPATTN_ERR_RANGE);
+          to = -1;
+        }
+        if (to < 0) continue;  // (the same in the vector's lanes)
+      }
+      const int skip = s.rotated ? 2 * s.rotated : 0, head = p.first / 8;  // chunks rotated, and before them
+      float f[NI][kItem];
+      int c0[NI], c1[NI];
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        const int j = lane + i * L;
+        c0[i] = c1[i] = -1;
+        if (j * kItem >= s.dim) continue;
+        if (j < s.rotated) {
+          c0[i] = p.first + j * (INTER ? 16 : 8);
+          c1[i] = c0[i] + c_rot;
+        } else {
+          const int n = 2 * (j - s.rotated);
+          c0[i] = 8 * (n < head ? n : n + skip);
+          c1[i] = 8 * (n + 1 < head ? n + 1 : n + 1 + skip);
+        }
+        const long long at = row * s.x_row + h * s.x_head;
+        load8<F32>(s.x, at + c0[i], f[i]);
+        load8<F32>(s.x, at + c1[i], f[i] + 8);
+      }
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        const int j = lane + i * L;
+        if (j >= s.rotated || c0[i] < 0) continue;
+        const float4* t = reinterpret_cast<const float4*>(&cs[buf][r * p.pairs + 8 * j]);
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) {
+          const float4 v = t[e / 2];
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const float c = x ? v.z : v.x, sn = x ? v.w : v.y;
+            float& a = f[i][INTER ? 2 * (e + x) : e + x];
+            float& b = f[i][INTER ? 2 * (e + x) + 1 : e + x + 8];
+            const float a0 = a, b0 = b;
+            a = a0 * c - b0 * sn;
+            b = b0 * c + a0 * sn;
+          }
+        }
+      }
+      uint8_t* const y = s.y + to * s.y_row + h * s.y_head;
+      if (!s.cached) {
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+          if (c0[i] < 0) continue;
+          if constexpr (F32) {
+            store8_f32(y + 4 * c0[i], f[i]);
+            store8_f32(y + 4 * c1[i], f[i] + 8);
+          } else {
+            store8_bf16(y + 2 * c0[i], f[i]);
+            store8_bf16(y + 2 * c1[i], f[i] + 8);
+          }
+        }
+      } else if (!s.scales) {
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+          if (c0[i] < 0) continue;
+          store8_bf16(y + 2 * c0[i], f[i]);
+          store8_bf16(y + 2 * c1[i], f[i] + 8);
+        }
+      } else {
+        // the largest finite element; the rotated value is rounded once, to its code
+        float a = 0.f;
+#pragma unroll
+        for (int i = 0; i < NI; ++i)
+          if (c0[i] >= 0)
+#pragma unroll
+            for (int e = 0; e < kItem; ++e) {
+              const float m = fabsf(f[i][e]);
+              a = fmaxf(a, m < INFINITY ? m : 0.f);
+            }
+        for (int o = L >> 1; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(mask, a, o));
+        const int e = scale_exponent(a);
+        const float inv = exp2_int(-e);
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+          if (c0[i] < 0) continue;
+          store8_codes(y + c0[i], f[i], inv);
+          store8_codes(y + c1[i], f[i] + 8, inv);
+        }
+        if (lane == 0) s.scales[h * s.s_head + to] = exp2_int(e);
+      }
+    }
+    buf ^= 1;  // (the next rows' values go to the other half: one barrier a round is enough)
+  }
+}
+
+inline bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+// Rows [n, heads, dim] with strides in elements of `size` bytes, 16-byte aligned.
+int check_rows(const void* x, int64_t row, int64_t head, int size) {
+  if (!aligned(x, 16) || row % (16 / size) || head % (16 / size)) return CPATTN_ERR_ALIGNMENT;
+  return row < 0 || head < 0 ? CPATTN_ERR_INVALID_ARG : CPATTN_OK;
+}
+// ... that are written: no element has two places.
+int check_out_rows(const void* x, int64_t row, int64_t head, int size, int64_t n, int heads, int dim) {
+  const int rc = check_rows(x, row, head, size);
+  if (rc != CPATTN_OK) return rc;
+  const bool by_row = (heads == 1 || head >= dim) && (n == 1 || row >= (heads - 1) * head + dim);
+  const bool by_head = (n == 1 || row >= dim) && (heads == 1 || head >= (n - 1) * row + dim);
+  return by_row || by_head ? CPATTN_OK : CPATTN_ERR_INVALID_ARG;
+}
+// Whether an output lies apart from its input, or on it with equal strides (each lane
+// reads what it writes).  Side by side in the rows of one buffer counts as apart.
+bool apart(const void* x, int64_t xr, int64_t xh, const void* y, int64_t yr, int64_t yh, int size, int64_t n,
+           int heads, int dim) {
+  if (n == 1) xr = yr = 0;
+  if (heads == 1) xh = yh = 0;
+  if (x == y && xr == yr && xh == yh) return true;
+  const intptr_t a = reinterpret_cast<intptr_t>(x), b = reinterpret_cast<intptr_t>(y);
+  const int64_t wx = ((heads - 1) * xh + dim) * size, wy = ((heads - 1) * yh + dim) * size;  // of a row
+  if (a + (n - 1) * xr * size + wx <= b || b + (n - 1) * yr * size + wy <= a) return true;
+  const int64_t row = xr * size;
+  if (xr != yr || row <= 0) return false;
+  const int64_t at = ((b - a) % row + row) % row;
+  return at >= wx && at + wy <= row;
+}
+
+int check_rope(const cp_rope_t* r, int d, const int32_t* positions, int64_t axis_stride, int num_rows) {
+  if (r->pairs < 1 || r->first < 0 || r->axes < 1 || r->axes > CPATTN_MAX_ROPE_AXES) return CPATTN_ERR_INVALID_ARG;
+  if (r->pairs % 8 || r->first % 8) return CPATTN_ERR_UNSUPPORTED;
+  if ((long long)r->first + 2LL * r->pairs > d) return CPATTN_ERR_INVALID_ARG;
+  if (!aligned(r->table, 16) || !aligned(positions, 4)) return CPATTN_ERR_ALIGNMENT;
+  if (num_rows > 0 && (!r->table || !positions)) return CPATTN_ERR_INVALID_ARG;
+  return r->axes > 1 && axis_stride < num_rows ? CPATTN_ERR_INVALID_ARG : CPATTN_OK;
+}
+
+int launch_rope(RopeParams& p, const cp_rope_t* rope, bool f32, cudaStream_t stream) {
+  const bool inter = rope && rope->interleaved;
+  int dim = 0;
+  p.vectors = 0;
+  for (int i = 0; i < 3; ++i) {
+    if (!p.side[i].heads) continue;
+    p.vectors += p.side[i].heads;
+    dim = std::max(dim, p.side[i].dim);
+  }
+  if (p.vectors == 0) return CPATTN_OK;
+  if (rope) {
+    p.table = reinterpret_cast<const int4*>(rope->table);
+    p.pairs = rope->pairs;
+    p.first = rope->first;
+    p.axes = rope->axes;
+  }
+  // Lanes of a vector: one item each where 32 are enough; 33 to 48 items (576 columns: 36)
+  // in three rounds of 16 lanes leave fewer idle than two of 32.
+  const int items = dim / kItem;
+  int ni = 1;
+  if (items > 48) p.log_l = 5, ni = 2;
+  else if (items > 32) p.log_l = 4, ni = 3;
+  else
+    for (p.log_l = 0; (1 << p.log_l) < items; ++p.log_l) {}
+  // Rows of a block: enough that its threads have a few vectors each, unless the blocks
+  // would be too few for the SMs.
+  const int groups = kThreads >> p.log_l;
+  int rows = std::max(1, 4 * groups / p.vectors);
+  rows = std::min(rows, std::max(1, p.num_rows / (152 * 4)));
+  if (p.pairs > 0) rows = std::max(1, std::min(rows, kMaxCs / p.pairs));
+  p.rows = rows;
+  const unsigned grid = (unsigned)std::min<long long>(((long long)p.num_rows + rows - 1) / rows, 152 * 8);
+  decltype(&rope_kernel<true, true, 1>) const kerns[2][2][3] = {
+      {{rope_kernel<false, false, 1>, rope_kernel<false, false, 2>, rope_kernel<false, false, 3>},
+       {rope_kernel<false, true, 1>, rope_kernel<false, true, 2>, rope_kernel<false, true, 3>}},
+      {{rope_kernel<true, false, 1>, rope_kernel<true, false, 2>, rope_kernel<true, false, 3>},
+       {rope_kernel<true, true, 1>, rope_kernel<true, true, 2>, rope_kernel<true, true, 3>}}};
+  kerns[f32 ? 1 : 0][inter ? 1 : 0][ni - 1]<<<grid, kThreads, 0, stream>>>(p);
+  return cudaGetLastError() == cudaSuccess ? CPATTN_OK : CPATTN_ERR_CUDA;
+}
+
+// One rotated tensor of cp_rope, or Q of cp_kv_append.
+int rotated_side(RopeSide* s, const void* x, int64_t xr, int64_t xh, int heads, void* y, int64_t yr, int64_t yh,
+                 bool f32, int num_rows, int d, const cp_rope_t* rope) {
+  const int size = f32 ? 4 : 2;
+  int rc = check_rows(x, xr, xh, size);
+  if (rc == CPATTN_OK) rc = check_out_rows(y, yr, yh, size, num_rows, heads, d);
+  if (rc != CPATTN_OK) return rc;
+  if (num_rows > 0 && (!x || !y)) return CPATTN_ERR_INVALID_ARG;
+  if (num_rows > 0 && !apart(x, xr, xh, y, yr, yh, size, num_rows, heads, d)) return CPATTN_ERR_INVALID_ARG;
+  s->x = x;
+  s->x_row = xr;
+  s->x_head = xh;
+  s->y = static_cast<uint8_t*>(y);
+  s->y_row = yr * size;
+  s->y_head = yh * size;
+  s->heads = heads;
+  s->dim = d;
+  s->rotated = rope ? rope->pairs / 8 : 0;
+  return CPATTN_OK;
+}
+
+// K or V of cp_kv_append.
+int cached_side(RopeSide* s, const void* x, int64_t xr, int64_t xh, bool f32, int heads, int dim,
+                const cp_kv_codes_t* c, int num_rows, int cache_rows, const cp_rope_t* rope) {
+  const int rc = check_rows(x, xr, xh, f32 ? 4 : 2);
+  if (rc != CPATTN_OK) return rc;
+  if (dim < 16 || dim > kMaxDim || dim % 16) return CPATTN_ERR_UNSUPPORTED;
+  const int size = c->scales ? 1 : 2;
+  if ((num_rows > 0 && !x) || (cache_rows > 0 && !c->codes)) return CPATTN_ERR_INVALID_ARG;
+  if (!aligned(c->codes, 16) || !aligned(c->scales, 4) || c->row_stride % 16 || c->head_stride % 16)
+    return CPATTN_ERR_ALIGNMENT;
+  if (c->head_stride < (int64_t)dim * size || c->row_stride < (int64_t)(heads - 1) * c->head_stride + dim * size ||
+      (c->scales && c->scale_stride < cache_rows))
+    return CPATTN_ERR_INVALID_ARG;
+  s->x = x;
+  s->x_row = xr;
+  s->x_head = xh;
+  s->y = static_cast<uint8_t*>(c->codes);
+  s->y_row = c->row_stride;
+  s->y_head = c->head_stride;
+  s->scales = c->scales;
+  s->s_head = c->scale_stride;
+  s->heads = heads;
+  s->dim = dim;
+  s->rotated = rope ? rope->pairs / 8 : 0;
+  s->cached = 1;
+  return CPATTN_OK;
+}
+
+}  // namespace
+}  // namespace cpattn
+
+using namespace cpattn;
+
+extern "C" int cp_rope_table(const double* inv_freq, const int32_t* axis, int pairs, int32_t* table) {
+  if (!inv_freq || !table || pairs < 1 || pairs > kMaxDim / 2) return CPATTN_ERR_INVALID_ARG;
+  // 1 / (2 pi) in two parts, so that the product keeps 2^-64 of a turn
+  const double hi = 0x1.45f306dc9c883p-3, lo = -0x1.6b01ec5417056p-57;
+  for (int c = 0; c < pairs; ++c) {
+    const double f = inv_freq[c];
+    const int a = axis ? axis[c] : 0;
+    if (!(std::fabs(f) <= 0x1p20) || a < 0 || a >= CPATTN_MAX_ROPE_AXES) return CPATTN_ERR_INVALID_ARG;
+    const double turns = f * hi, rest = std::fma(f, hi, -turns) + f * lo;
+    const uint64_t F = (uint64_t)std::ldexp(turns - std::floor(turns), 64) + (uint64_t)std::llrint(std::ldexp(rest, 64));
+    table[4 * c] = (int32_t)(uint32_t)F;
+    table[4 * c + 1] = (int32_t)(uint32_t)(F >> 32);
+    table[4 * c + 2] = a;
+    table[4 * c + 3] = 0;
+  }
+  return CPATTN_OK;
+}
+
+extern "C" int cp_rope(const cp_rope_t* rope, const int32_t* positions, int64_t axis_stride, int inverse,
+                       const void* q, int64_t q_row_stride, int64_t q_head_stride, int Hq, void* q_out,
+                       int64_t qo_row_stride, int64_t qo_head_stride, const void* k, int64_t k_row_stride,
+                       int64_t k_head_stride, int Hk, void* k_out, int64_t ko_row_stride,
+                       int64_t ko_head_stride, int x_is_fp32, int num_rows, int d, int32_t* status_dev,
+                       cudaStream_t stream) {
+  CPATTN_TRACE("cp_rope");
+  if (!rope || num_rows < 0 || Hq < 1 || Hk < 0 || Hq > 1 << 20 || Hk > 1 << 20 || (Hk > 0 && num_rows > 0 && !k))
+    return CPATTN_ERR_INVALID_ARG;
+  if (d < 16 || d > kMaxDim || d % 16) return CPATTN_ERR_UNSUPPORTED;
+  if (!aligned(status_dev, 4)) return CPATTN_ERR_ALIGNMENT;
+  int rc = check_rope(rope, d, positions, axis_stride, num_rows);
+  if (rc != CPATTN_OK) return rc;
+  RopeParams p{};
+  const bool f32 = x_is_fp32 != 0;
+  rc = rotated_side(&p.side[0], q, q_row_stride, q_head_stride, Hq, q_out, qo_row_stride, qo_head_stride, f32,
+                    num_rows, d, rope);
+  if (rc == CPATTN_OK && Hk > 0)
+    rc = rotated_side(&p.side[1], k, k_row_stride, k_head_stride, Hk, k_out, ko_row_stride, ko_head_stride, f32,
+                      num_rows, d, rope);
+  if (rc != CPATTN_OK || num_rows == 0) return rc;
+  p.positions = positions;
+  p.axis_stride = axis_stride;
+  p.inverse = inverse ? 1 : 0;
+  p.num_rows = num_rows;
+  p.status = status_dev;
+  return launch_rope(p, rope, f32, stream);
+}
+
+extern "C" int cp_kv_append(const cp_rope_t* rope, const int32_t* positions, int64_t axis_stride, const void* k,
+                            int64_t k_row_stride, int64_t k_head_stride, const void* v, int64_t v_row_stride,
+                            int64_t v_head_stride, int x_is_fp32, int num_rows, int Hkv, int d, int dv,
+                            const int32_t* slots, const cp_kv_codes_t* k_cache, const cp_kv_codes_t* v_cache,
+                            int cache_rows, const void* q, int64_t q_row_stride, int64_t q_head_stride, int Hq,
+                            void* q_out, int64_t qo_row_stride, int64_t qo_head_stride, int32_t* status_dev,
+                            cudaStream_t stream) {
+  CPATTN_TRACE("cp_kv_append");
+  if (num_rows < 0 || cache_rows < 0 || Hkv < 1 || Hkv > 1 << 20 || Hq < 0 || Hq > 1 << 20 || !k_cache ||
+      (v != nullptr && !v_cache) || (num_rows > 0 && !v && v_cache) || (v_cache && !v_cache->scales != !k_cache->scales))
+    return CPATTN_ERR_INVALID_ARG;
+  if (!aligned(slots, 4) || !aligned(status_dev, 4)) return CPATTN_ERR_ALIGNMENT;
+  int rc = rope ? check_rope(rope, d, positions, axis_stride, num_rows) : CPATTN_OK;
+  if (rc != CPATTN_OK) return rc;
+  RopeParams p{};
+  const bool f32 = x_is_fp32 != 0;
+  rc = cached_side(&p.side[1], k, k_row_stride, k_head_stride, f32, Hkv, d, k_cache, num_rows, cache_rows, rope);
+  if (rc == CPATTN_OK && v_cache)
+    rc = cached_side(&p.side[2], v, v_row_stride, v_head_stride, f32, Hkv, dv, v_cache, num_rows, cache_rows, nullptr);
+  if (rc == CPATTN_OK && Hq > 0)
+    rc = rotated_side(&p.side[0], q, q_row_stride, q_head_stride, Hq, q_out, qo_row_stride, qo_head_stride, f32,
+                      num_rows, d, rope);
+  if (rc != CPATTN_OK || num_rows == 0) return rc;
+  p.positions = positions;
+  p.axis_stride = axis_stride;
+  p.slots = slots;
+  p.num_rows = num_rows;
+  p.cache_rows = cache_rows;
+  p.status = status_dev;
+  return launch_rope(p, rope, f32, stream);
+}

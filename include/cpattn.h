@@ -657,6 +657,134 @@ int cp_attn_shared(const cp_shared_plan_t* plan, const int32_t* table_dev, const
                    int64_t workspace_bytes, int32_t* status_dev, cudaStream_t stream);
 
 /* ------------------------------------------------------------------------ */
+/* Rotary positions.  (No counterpart on the source pages, which rotate Q and K
+ * before attention without saying how.)
+ *
+ * A vector's columns first .. first + 2*pairs - 1 are pairs of columns: (first + c,
+ * first + pairs + c), or with `interleaved` (first + 2c, first + 2c + 1).  Pair c of a
+ * row turns by the angle t = positions[axis_c][row] * inv_freq_c:
+ *     (a, b) -> (a cos t - b sin t, b cos t + a sin t)
+ * and the other columns stay.  With one axis that is the position in the sequence, with
+ * several those of an image or video (time, height, width), each pair following the
+ * axis that the table gives it.  The phase is computed in 64-bit fractions of a turn: the
+ * angle is off by at most |position| * 2^-64 turns at any position, and cos and sin by fp32's
+ * rounding.  The rotation is computed in fp32 and rounded once.
+ *
+ * cp_rope_table (host): inv_freq [pairs] (radians a position, |inv_freq| <= 2^20) and
+ * axis [pairs] (0 .. CPATTN_MAX_ROPE_AXES - 1; NULL: all 0) to table [pairs][4] (host),
+ * which the caller copies to the device (16-byte aligned).
+ * cp_rope_t: its pairs, first (both multiples of 8) and axes (the rows of positions; a
+ * pair whose axis is not below it sets CPATTN_ERR_RANGE and turns by nothing). */
+#define CPATTN_MAX_ROPE_AXES 8
+typedef struct {
+  const int32_t* table; /* device */
+  int32_t pairs, first, interleaved, axes;
+} cp_rope_t;
+int cp_rope_table(const double* inv_freq, const int32_t* axis, int pairs, int32_t* table);
+
+/* Rotate the rows of q [num_rows, Hq, d], and of k [num_rows, Hk, d] (Hk = 0: q alone).
+ *   positions: device int32, axis a's position of row i at positions[a*axis_stride + i]
+ *     (axis_stride >= num_rows where axes > 1); any values.
+ *   inverse: turn by -t.  The rotation is orthogonal, so that this is the gradient: dq
+ *     from dq_out.
+ *   q, k, q_out, k_out: bf16, or fp32 (x_is_fp32); strides in elements, multiples of 16
+ *     bytes, >= 0.  An output may be its input (same pointer and strides); otherwise the
+ *     two must not overlap (rows side by side in one buffer of equal row strides do not).
+ *     No element of an output may have two places.
+ *   d: a multiple of 16, at most 1024, >= first + 2*pairs. */
+int cp_rope(const cp_rope_t* rope, const int32_t* positions, int64_t axis_stride, int inverse,
+            const void* q, int64_t q_row_stride, int64_t q_head_stride, int Hq, void* q_out,
+            int64_t qo_row_stride, int64_t qo_head_stride, const void* k, int64_t k_row_stride,
+            int64_t k_head_stride, int Hk, void* k_out, int64_t ko_row_stride,
+            int64_t ko_head_stride, int x_is_fp32, int num_rows, int d, int32_t* status_dev,
+            cudaStream_t stream);
+
+/* Append new rows to a KV cache, K (and Q) rotated on the way.
+ *   rope, positions, axis_stride: as in cp_rope; rope NULL: nothing is rotated.
+ *   k, v, x_is_fp32, num_rows, Hkv, d, dv, slots: as in cp_kv_quantize (v and v_cache
+ *     NULL: K alone).  Rows of slots < 0 are padding and skipped.
+ *   k_cache, v_cache: codes and scales, written as cp_kv_quantize writes them (from the
+ *     rotated fp32 values: K is rounded once); or, with scales NULL (both), bf16 rows at
+ *     `codes`, the strides in bytes all the same.
+ *   q: NULL with Hq = 0, or rows [num_rows, Hq, d] of k's type, rotated to q_out as in
+ *     cp_rope (padding rows among them).
+ * q_out, the caches and the inputs must not overlap (q_out may be q). */
+int cp_kv_append(const cp_rope_t* rope, const int32_t* positions, int64_t axis_stride,
+                 const void* k, int64_t k_row_stride, int64_t k_head_stride, const void* v,
+                 int64_t v_row_stride, int64_t v_head_stride, int x_is_fp32, int num_rows,
+                 int Hkv, int d, int dv, const int32_t* slots, const cp_kv_codes_t* k_cache,
+                 const cp_kv_codes_t* v_cache, int cache_rows, const void* q,
+                 int64_t q_row_stride, int64_t q_head_stride, int Hq, void* q_out,
+                 int64_t qo_row_stride, int64_t qo_head_stride, int32_t* status_dev,
+                 cudaStream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* A decode step over a paged cache.  (No counterpart on the source pages: their
+ * queries of a few tokens over a cached KV [CPB-PQ, decode] with the cache in pages and
+ * with trees of drafted tokens.)
+ *
+ * Key j of request b lies at cache row page_table[b*table_stride + j/page_size] *
+ * page_size + j % page_size (max_pages entries a request; page_size a power of two, 16 ..
+ * 65536).  Request b has kv_lens[b] >= 0 cached keys.  Its new tokens are the rows
+ * q_start[b] .. q_start[b+1]-1 (q_start [num_reqs+1], rising from 0) and follow as the
+ * keys kv_lens[b], kv_lens[b]+1, ...  All of these are device int32 arrays, read by the
+ * kernels: a captured graph replays on whatever lengths they hold.  Rows from
+ * q_start[num_reqs] on are padding.
+ *
+ * cp_tree_layout: once a step, where the new rows go and what they see.
+ *   parents: NULL (a chain), or [num_rows]: the number, within the request, of the node
+ *     that node i continues (-1: none, it follows the cached keys; otherwise below i).
+ *   slots [num_rows]: the cache row of each (for cp_kv_append); padding rows -1.
+ *   positions [num_rows]: kv_lens[b] + the node's depth (a chain's: kv_lens[b] + i);
+ *     padding rows 0.
+ *   mask (NULL without parents): int32 [num_rows][mask_words], bit j % 32 of word j / 32
+ *     set for the node itself and its ancestors; padding rows 0.
+ * A request whose rows, length or pages lie outside their arrays, a page that is not one
+ * (< 0), a parent that is not below its node and a node without a bit (>= 32 *
+ * mask_words) set CPATTN_ERR_RANGE; such a request's or node's slot is -1, such a parent
+ * counts as none. */
+int cp_tree_layout(const int32_t* q_start, const int32_t* kv_lens, int num_reqs,
+                   const int32_t* page_table, int64_t table_stride, int max_pages, int page_size,
+                   const int32_t* parents, int num_rows, int mask_words, int32_t* slots,
+                   int32_t* positions, int32_t* mask, int32_t* status_dev, cudaStream_t stream);
+
+/* Attention of the new rows over the paged cache.  Row i of request b sees the cached keys
+ * 0 .. kv_lens[b]-1 and the new keys kv_lens[b]+j of the nodes j that its mask names (mask
+ * NULL: j <= i).  With S_k as in cp_attn_partial
+ *     L = ln(sum over those keys of exp(S_k)),  O = sum exp(S_k - L) V_k;
+ * a row that sees nothing has O = 0 and L = -inf; padding rows are left as they are.  The
+ * new keys must be in the cache (cp_kv_append on the same stream before).
+ *   mask: int32 [num_rows][mask_words] as cp_tree_layout writes it, or any other bits (bits
+ *     at or past the request's rows are not looked at; a request of more than 32*mask_words
+ *     rows sets CPATTN_ERR_RANGE and is skipped).  NULL with mask_words = 0.
+ *   q, k, v, k_scales, v_scales, scale_stride, o, lse: as in cp_attn_shared, num_rows query
+ *     rows, num_kv_rows cache rows (whole pages).  (d, dv): (64, 64) and (128, 128).
+ *   max_nodes: the rows of a request that the call is tuned for, >= 1 (a longer one is
+ *     right, and slower).  num_ctas in [1, 4096]: thread blocks (the device's SM count).
+ *   workspace: device, 32-byte aligned, cp_tree_workspace_size bytes for the same Hq, Hkv,
+ *     dv, max_nodes and num_ctas (lengths play no part); overwritten, nothing in it needs
+ *     clearing; not to be shared by calls that may run at the same time.
+ * Keys outside what a request's rows see may hold anything, infinities and NaN among
+ * them; so may, for the other rows of its request, a new key that only some see.  A row that
+ * sees a new key whose value row holds an infinity or a NaN is NaN in all columns.  Weights
+ * are rounded as in cp_attn_shared; codes enter the products as described there.
+ * Two launches (the attention, and the merge of what was cut), no order of atomics: the same
+ * call gives the same bits.  A request whose rows, length or pages lie outside their
+ * arrays sets CPATTN_ERR_RANGE and is skipped; so does a page outside the cache, whose keys
+ * count as zeros; a wait that runs out sets CPATTN_ERR_TIMEOUT.  With any of them, o and lse
+ * are not to be used. */
+int cp_tree_workspace_size(int Hq, int Hkv, int dv, int max_nodes, int num_ctas, int64_t* bytes);
+int cp_attn_tree(const void* q, int64_t q_row_stride, int64_t q_head_stride, int num_rows,
+                 const void* k, int64_t k_row_stride, int64_t k_head_stride,
+                 const float* k_scales, const void* v, int64_t v_row_stride,
+                 int64_t v_head_stride, const float* v_scales, int64_t scale_stride,
+                 int num_kv_rows, const int32_t* page_table, int64_t table_stride, int max_pages,
+                 int page_size, const int32_t* q_start, const int32_t* kv_lens, int num_reqs,
+                 const int32_t* mask, int mask_words, int Hq, int Hkv, int d, int dv, float scale,
+                 int max_nodes, int num_ctas, void* o, int o_is_fp32, float* lse, void* workspace,
+                 int64_t workspace_bytes, int32_t* status_dev, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------ */
 /* Test hook for the failure path of the attention pipeline (no counterpart on
  * the source pages).  Process-wide; affects launches made after the call.
  *   CPATTN_DEBUG_WAIT_LIMIT_NS: time limit of every mbarrier wait inside the
