@@ -19,7 +19,7 @@ LIB = os.path.join(PKG, "libcpattn.so")
 SOURCES = ["plan.cu", "merge.cu", "attn.cu", "attn_mla.cu", "partial_kv.cu",
            "partial_kv_noalloc.cu", "select.cu", "ring.cu", "pipeline.cu", "attn_mla2.cu",
            "kvcache.cu", "shared_plan.cu", "attn_shared.cu", "rope.cu", "tree_layout.cu",
-           "attn_tree.cu", "attn_tree_small.cu"]
+           "attn_tree.cu", "attn_tree_small.cu", "attn_tree_mma.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -60,9 +60,8 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const TreePar
 
 // Packed rows of a unit, by the rows that a request is expected to have.
 int unit_rows_of(int g, int max_nodes) {
-  (void)g;
-  (void)max_nodes;
-  return 8;
+  const long long rows = (long long)g * max_nodes;
+  return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= BM ? BM : 2 * BM;
 }
 
 bool plan_sizes(int Hq, int Hkv, int dv, int max_nodes, int num_ctas, int* unit_rows, int64_t* o_at, int64_t* l_at,
@@ -171,7 +170,8 @@ extern "C" int cp_attn_tree(const void* q, int64_t q_row_stride, int64_t q_head_
   if (!map(&m.k, k, k_head_stride, k_row_stride, whole) || !map(&m.v, v, v_head_stride, v_row_stride, whole) ||
       !map(&m.k_tail, k, k_head_stride, k_row_stride, 16) || !map(&m.v_tail, v, v_head_stride, v_row_stride, 16))
     return CPATTN_ERR_CUDA;
-  const int r = launch_tree_small(m, p, d, quant, num_ctas, stream);
+  const int r = p.unit_rows < BM ? launch_tree_small(m, p, d, quant, num_ctas, stream)
+                                 : launch_tree_mma(m, p, d, quant, num_ctas, stream);
   if (r != CPATTN_OK) return r;
   auto merge = d == 128 ? tree_merge_kernel<128> : tree_merge_kernel<64>;
   const dim3 grid(num_ctas, (p.unit_rows * (d / 8) * 2 + kMergeThreads - 1) / kMergeThreads);

@@ -60,6 +60,8 @@ inline bool split_covered(void (*kern)(Params...), int threads, int regs) {
   return cudaFuncGetAttributes(&fa, kern) == cudaSuccess && fa.numRegs * threads >= regs;
 }
 int launch_tree_small(const TreeMaps& m, const TreeParams& p, int d, bool quant, int num_ctas, cudaStream_t stream);
+// ... and the one on tcgen05 (attn_tree_mma.cu): 128 or 256 rows.
+int launch_tree_mma(const TreeMaps& m, const TreeParams& p, int d, bool quant, int num_ctas, cudaStream_t stream);
 
 namespace {
 

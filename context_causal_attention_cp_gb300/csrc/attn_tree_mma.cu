@@ -1,0 +1,854 @@
+// cp_attn_tree for many rows a request and KV head (trees, longer drafts, chunks): tcgen05.
+//
+// A unit is one MMA tile of 128 packed rows (single), or two (dual).  Two softmax
+// warpgroups (streams) work at a time: of a dual unit each has one tile's rows and both use
+// every KV tile of 128 keys; of a single unit both have all rows, and the KV tiles alternate
+// between them, so that one stream's softmax runs under the other's products, too.
+//   warps 0-7    softmax, one row a thread: S from TMEM, mask (tiles with new keys only),
+//                online softmax in base 2 with a lazily moved maximum, P back to TMEM in 16
+//                bits; at a piece's end O / l from TMEM to the output, or to the workspace
+//                where the unit is cut.  A single unit's two halves are joined there, each
+//                stream half of the columns.
+//   warps 8, 9   producers of the K and the V tiles: a lane looks up a page, a tile ahead,
+//                and starts its TMA copies; one ring of tiles in the order of use that runs
+//                across piece ends.
+//   warp 10      MMA issuer (one thread): O += P V and the next S = Q K^T of one stream, then
+//                of the other.
+//   warp 11      query rows to shared memory.
+//   warps 12-15  (e4m3 cache) codes to f16 tiles, as in attn_shared.cu.
+// Every wait is bounded; all roles walk the block's share on their own (see attn_tree.cuh).
+//
+// Value rows behind the last key, and (among new keys) rows with an infinity or a NaN, become
+// zeros in shared memory before their product: 0 * NaN is NaN, so that masking P alone
+// would not keep them from the rows that do not see them.  A row that does see one becomes
+// NaN by its sum.
+#include <algorithm>
+
+#include "attn_tree.cuh"
+
+namespace cpattn {
+namespace {
+
+constexpr int kKWarp = 8, kVWarp = 9, kMmaWarp = 10, kQWarp = 11, kConvertWarp = 12;
+constexpr int kConvertThreads = 128;
+
+template <int D, bool QUANT, bool DUAL>
+struct MmaCfg {
+  static constexpr int kThreads = QUANT ? 512 : 384;
+  static constexpr int kRegsLaunch = QUANT ? 128 : 168;
+  static constexpr int kRegsSoftmax = 200, kRegsOther = QUANT ? 56 : 104;
+  static_assert(kRegsSoftmax * 256 + kRegsOther * (kThreads - 256) <= kRegsLaunch * kThreads,
+                "register split exceeds the launch allocation");
+  static constexpr int kQTile = BM * D * 2;
+  static constexpr int kTile = BN * D * 2;  // a K or V tile of 16-bit elements
+  static constexpr int kRawTile = BN * D;   // an e4m3 K or V tile
+  static constexpr int kStages = QUANT ? (D == 128 ? 3 : 6) : D == 128 ? 5 : 10;
+  static constexpr int kRawStages = !QUANT ? 0 : D == 64 ? 8 : DUAL ? 4 : 3;
+  static constexpr int kRingOff = 2 * kQTile;
+  static constexpr int kRawOff = kRingOff + kStages * kTile;
+  static constexpr int kMulOff = kRawOff + kRawStages * kRawTile;    // f16 factor of each raw row
+  static constexpr int kNoteOff = kMulOff + kRawStages * BN * 2;     // RawNote of each raw tile
+  static constexpr int kExpOff = kNoteOff + kRawStages * 16;         // (ek, ev) of tiles n mod 8
+  static constexpr int kLiftOff = kExpOff + 64;                      // exponents of query rows, [2][2][BM]
+  static constexpr int kMlOff = kLiftOff + (QUANT ? 4 * BM : 0);     // single: (m, l) of each stream's rows
+  static constexpr int kEvOff = kMlOff + (DUAL ? 0 : 2 * BM * 8);    // and O's exponent
+  static constexpr int kBadOff = kEvOff + (QUANT && !DUAL ? 2 * BM : 0);  // value rows that are not finite
+  static constexpr int kBarOff = kBadOff + 2 * 2 * 16 + kStages * 16;
+  static constexpr int kNumBars = 2 * kStages + 2 * kRawStages + 2 * 5 + 1;
+  static constexpr int kWordOff = kBarOff + kNumBars * 8;
+  static constexpr int kSumOff = (kWordOff + 64 + 7) & ~7;
+  static constexpr int kSmemBytes = kSumOff + 16 * 8;
+  static_assert(kBarOff % 8 == 0 && kSmemBytes <= 232448, "shared memory budget");
+  static constexpr int kTmemCols = 4 * 128;  // S of each stream, then O of each
+};
+
+// What a producer tells the converters about a raw tile.
+struct RawNote {
+  int live;         // rows up to the unit's end
+  int fresh;        // first row that is a new key
+  int ek, ev;       // of a K tile: its exponent, and V's
+};
+
+// Ring place of K and V of the block's n-th KV tile, in the order of use.  (A single list's
+// place behind its last V is left out: 2n + 2 of the last n.)
+template <bool DUAL>
+__device__ __forceinline__ int k_place(int n) { return DUAL ? 2 * n : n == 0 ? 0 : 2 * n - 1; }
+template <bool DUAL>
+__device__ __forceinline__ int v_place(int n) { return DUAL ? 2 * n + 1 : 2 * n + 2; }
+
+// Steps through the KV tiles of a share.
+struct TileWalk {
+  TreeWalk w;
+  TreePiece pc;
+  int t = -1, piece = -1;  // tile of the piece, number of the piece
+  __device__ __forceinline__ bool next(const TreeParams& p) {
+    if (piece < 0 || ++t >= pc.tiles) {
+      if (!w.next(p, pc)) return false;
+      t = 0;
+      ++piece;
+    }
+    return true;
+  }
+  __device__ __forceinline__ int left() const { return pc.tiles - 1 - t; }  // behind this one
+};
+
+// The bits of the keys that new row `node` sees of the 32 from key0 on.
+__device__ __forceinline__ uint32_t seen_bits(const TreeParams& p, const TreeReq& r, int node, int key0) {
+  const int n = key0 - r.L;  // new key of the first bit
+  if (n >= r.T) return 0u;
+  if (n <= -32) return ~0u;
+  uint32_t bits;
+  int count;  // bits that are keys
+  if (p.mask) {
+    const int32_t* row = p.mask + (long long)(r.row0 + node) * p.words;
+    if (n >= 0) {
+      const int w = n >> 5;
+      const uint32_t lo = (uint32_t)__ldg(row + w), hi = w + 1 < p.words ? (uint32_t)__ldg(row + w + 1) : 0u;
+      bits = __funnelshift_r(lo, hi, n & 31);
+    } else {
+      bits = ((uint32_t)__ldg(row) << -n) | ((1u << -n) - 1u);
+    }
+    count = r.T - n;
+  } else {
+    bits = ~0u;
+    count = node + 1 - n;
+  }
+  return count >= 32 ? bits : count <= 0 ? 0u : bits & ((1u << count) - 1u);
+}
+
+__device__ __forceinline__ void bar_named(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+// S of a tile to P, for the rows of a warp (one a lane): see softmax_tile in attn_shared.cu.
+// vis: the keys that the row sees (masked: not all); o_scale: what O is multiplied by besides.
+template <int D, bool QUANT>
+__device__ __forceinline__ void softmax_row(uint32_t s_addr, uint32_t o_addr, bool masked, const uint32_t (&vis)[4],
+                                            bool has_o, float o_scale, float sl2, float& m_run, float& m_use,
+                                            float& l_run) {
+  float x[BN];
+  {
+    uint32_t v[BN];
+#pragma unroll
+    for (int q = 0; q < BN / 32; ++q) tmem_ld32p(s_addr + q * 32, v + q * 32);
+    tmem_wait_ld();
+#pragma unroll
+    for (int c = 0; c < BN; ++c) x[c] = __uint_as_float(v[c]);
+  }
+  if (masked) {
+#pragma unroll
+    for (int c = 0; c < BN; ++c)
+      if (!((vis[c >> 5] >> (c & 31)) & 1u)) x[c] = -INFINITY;
+  }
+  float mx0 = x[0], mx1 = x[1], mx2 = x[2], mx3 = x[3];
+#pragma unroll
+  for (int c = 4; c + 8 <= BN; c += 8) {
+    mx0 = fmax3(mx0, x[c], x[c + 1]);
+    mx1 = fmax3(mx1, x[c + 2], x[c + 3]);
+    mx2 = fmax3(mx2, x[c + 4], x[c + 5]);
+    mx3 = fmax3(mx3, x[c + 6], x[c + 7]);
+  }
+  mx0 = fmax3(mx0, x[BN - 4], x[BN - 3]);
+  mx1 = fmax3(mx1, x[BN - 2], x[BN - 1]);
+  const float mx = fmaf(fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)), sl2, QUANT ? -kF16Lift : 0.f);
+  const bool move = mx > m_run + kMaxSlack;
+  const float m_new = move ? mx : m_run;
+  const float m_new_use = (m_new == -INFINITY) ? 0.f : m_new;
+  const float alpha = move ? ex2_approx(m_run - m_new_use) : 1.f;
+  float sum0 = 0.f, sum1 = 0.f;
+#pragma unroll
+  for (int q = 0; q < BN / 32; ++q) {
+    uint32_t pk[16];
+#pragma unroll
+    for (int c = 0; c < 32; c += 2) {
+      float a, b;
+      ffma2(a, b, x[q * 32 + c], x[q * 32 + c + 1], sl2, sl2, -m_new_use, -m_new_use);
+      a = ex2_approx(a);
+      b = ex2_approx(b);
+      fadd2(sum0, sum1, sum0, sum1, a, b);
+      // P in 16 bits, the second product's operand type: off by at most 2^-8 (bf16) or
+      // 2^-11 (f16) of each weight; l sums the unrounded values
+      pk[c >> 1] = QUANT ? pack_f16x2(a, b) : pack_bf16x2(a, b);
+    }
+    tmem_st16(s_addr + q * 16, pk);
+  }
+  l_run = l_run * alpha + (sum0 + sum1);
+  const bool need = has_o && (move || o_scale != 1.f);
+  if (__any_sync(0xffffffffu, need)) {
+    const float a = need ? alpha * o_scale : 1.f;
+    uint32_t v[32];
+#pragma unroll
+    for (int q = 0; q < D / 32; ++q) {
+      tmem_ld32(o_addr + q * 32, v);
+      tmem_wait_ld();
+#pragma unroll
+      for (int c = 0; c < 32; ++c) v[c] = __float_as_uint(__uint_as_float(v[c]) * a);
+      tmem_st32(o_addr + q * 32, v);
+    }
+  }
+  tmem_wait_st();
+  m_run = m_new;
+  m_use = m_new_use;
+}
+
+// 8 columns from column 8 c on of row r of a piece: to the output, or to its partial.
+__device__ __forceinline__ void put8(const TreeParams& p, const TreePiece& pc, int D, int r, int c, long long at,
+                                     const float (&f)[8]) {
+  if (pc.slot >= 0) {
+    store8(p.ws_o + (long long)pc.slot * p.unit_rows * D + partial_at(c, r, p.unit_rows), f);
+  } else if (p.o_f32) {  // (16-byte aligned)
+    float4* o = reinterpret_cast<float4*>(static_cast<float*>(p.o) + at * D + c * 8);
+    o[0] = make_float4(f[0], f[1], f[2], f[3]);
+    o[1] = make_float4(f[4], f[5], f[6], f[7]);
+  } else {
+    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.o) + at * D + c * 8) =
+        make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+  }
+}
+
+template <int D, bool QUANT, bool DUAL>
+__global__ void __launch_bounds__(MmaCfg<D, QUANT, DUAL>::kThreads, 1)
+attn_tree_mma_kernel(const __grid_constant__ TreeMaps maps, const TreeParams p) {
+  using C = MmaCfg<D, QUANT, DUAL>;
+  constexpr int NS = C::kStages;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
+  uint64_t* empty = full + NS;
+  uint64_t* raw_full = empty + NS;
+  uint64_t* raw_empty = raw_full + C::kRawStages;
+  uint64_t* q_full = raw_empty + C::kRawStages;
+  uint64_t* q_empty = q_full + 2;
+  uint64_t* s_full = q_empty + 2;
+  uint64_t* p_full = s_full + 2;
+  uint64_t* o_full = p_full + 2;
+  uint64_t* bar_drain = o_full + 2;
+  uint16_t* raw_mul = reinterpret_cast<uint16_t*>(smem + C::kMulOff);
+  RawNote* raw_note = reinterpret_cast<RawNote*>(smem + C::kNoteOff);
+  int2* tile_exp = reinterpret_cast<int2*>(smem + C::kExpOff);
+  int8_t* q_lift = reinterpret_cast<int8_t*>(smem + C::kLiftOff);
+  float2* ml = reinterpret_cast<float2*>(smem + C::kMlOff);
+  int8_t* o_exp = reinterpret_cast<int8_t*>(smem + C::kEvOff);
+  uint32_t* bad_scan = reinterpret_cast<uint32_t*>(smem + C::kBadOff);  // [2 streams][2][4]
+  uint32_t* bad_slot = bad_scan + 16;                                   // [kStages][4] (e4m3)
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kWordOff);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile int* issued = reinterpret_cast<volatile int*>(tmem_slot + 2);  // K and V tiles, for the abort drain
+  long long* found = reinterpret_cast<long long*>(tmem_slot + 4);
+  long long* sums = reinterpret_cast<long long*>(smem + C::kSumOff);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if ((smem_u32(smem) & 1023u) != 0) {  // the swizzled tiles need it (no static shared memory: it holds)
+    if (threadIdx.x == 0) {
+      set_status(p.status, CPATTN_ERR_ALIGNMENT);
+      p.cut[2 * blockIdx.x + 1] = make_int4(0, 0, 0, 0);
+    }
+    return;
+  }
+  grid_dep_trigger();  // the merge may be scheduled as blocks of this grid end
+  if (threadIdx.x == 0) {
+    prefetch_tmap(&maps.k);
+    prefetch_tmap(&maps.v);
+    prefetch_tmap(&maps.k_tail);
+    prefetch_tmap(&maps.v_tail);
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(full + i, QUANT ? kConvertThreads : 1);
+      mbar_init(empty + i, 1);
+    }
+    for (int i = 0; i < C::kRawStages; ++i) {
+      mbar_init(raw_full + i, 2);  // the TMA copies and the factors
+      mbar_init(raw_empty + i, kConvertThreads);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(q_full + s, 32);
+      mbar_init(q_empty + s, 1);
+      mbar_init(s_full + s, 1);
+      mbar_init(p_full + s, 128);
+      mbar_init(o_full + s, 1);
+    }
+    mbar_init(bar_drain, 1);
+    *abort_flag = 0;
+    issued[0] = issued[1] = 0;
+    fence_barrier_init();
+  }
+  if (warp == kKWarp) {
+    tmem_alloc(tmem_slot, C::kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  const TreeStart start = tree_start(p, sums, found);  // (its barriers publish those above)
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  const uint32_t q_base = smem_u32(smem);
+  const uint32_t ring_base = smem_u32(smem + C::kRingOff);
+
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsOther));
+    if (warp == kKWarp || warp == kVWarp) {
+      // ---------------------------------------------------------- producers --
+      constexpr int kSt = QUANT ? C::kRawStages : NS;
+      constexpr int kBytes = QUANT ? C::kRawTile : C::kTile;
+      constexpr int kChunks = QUANT ? 1 : D / 64;   // boxes across a row
+      constexpr int kLine = kBytes / BN / kChunks;  // bytes of a box row
+      const bool is_v = warp == kVWarp;
+      uint64_t* const fullb = QUANT ? raw_full : full;
+      uint64_t* const emptyb = QUANT ? raw_empty : empty;
+      uint8_t* const ring = smem + (QUANT ? C::kRawOff : C::kRingOff);
+      const int whole_log = min(7, p.log_page);
+      TileWalk w{{start}};
+      int n = 0, cut = 0;
+      int ev0 = 0, ev1 = 0;  // (e4m3) exponent of each stream's V rows
+      bool ok = true;
+      // The lane's box of the tile: whole pages, or 16 rows of the unit's end; looked up a tile
+      // ahead, so that the page table's latency is not waited for.
+      auto key_of = [&]() { return (w.pc.t0 + w.t) * BN; };
+      auto log_of = [&]() { return min(BN, w.pc.keys - key_of()) > BN - 16 ? whole_log : 4; };
+      bool more = w.next(p);
+      int row_next = 0;
+      auto lookup = [&]() {
+        const int live = min(BN, w.pc.keys - key_of()), log = log_of();
+        return (lane << log) < live ? cache_row(p, w.pc.b, key_of() + (lane << log)) : 0;
+      };
+      if (more) row_next = lookup();
+      while (more && ok) {
+        const int live = min(BN, w.pc.keys - key_of()), log = log_of(), boxes = (live + (1 << log) - 1) >> log;
+        const int mine = row_next, kvh = w.pc.kv_head, fresh = w.pc.req.L - key_of();
+        const bool first = w.t <= (DUAL ? 0 : 1);  // of its piece and stream
+        if (is_v && w.t == 0 && w.pc.blocks) {
+          cut = w.pc.blocks;
+          if (lane == 0) put_cut(p, w.pc, cut);
+        }
+        const int place = is_v ? v_place<DUAL>(n) : k_place<DUAL>(n), slot = place % kSt;
+        ok = wait_warp(emptyb + slot, ((place / kSt) & 1) ^ 1, abort_flag, p.timeout_ns);
+        if (!ok) break;
+        uint8_t* dst = ring + slot * kBytes;
+        if (lane == 0) mbar_arrive_expect_tx(fullb + slot, (boxes << log) * kLine * kChunks);
+        __syncwarp();
+        if (lane < boxes) {
+          const CUtensorMap* tm = log == whole_log ? (is_v ? &maps.v : &maps.k) : (is_v ? &maps.v_tail : &maps.k_tail);
+#pragma unroll
+          for (int c = 0; c < kChunks; ++c)
+            tma_load_3d(dst + (c * BN + (lane << log)) * kLine, tm, fullb + slot, c * 64, kvh, mine);
+        }
+        __syncwarp();
+        if constexpr (QUANT) {
+          // the rows' scales as f16 factors relative to the tile's largest (K), or to the
+          // largest that the stream has met in the piece (V)
+          float sc[4], mv = 0.f;
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const int key = x * 32 + lane;
+            const int row = __shfl_sync(0xffffffffu, mine, key >> log) + (key & ((1 << log) - 1));
+            const bool in = key < live && row < p.num_kv_rows;
+            const long long at = (long long)kvh * p.s_head + row;
+            sc[x] = in ? __ldg((is_v ? p.vs : p.ks) + at) : 0.f;
+            mv = fmaxf(mv, is_v ? sc[x] : in ? __ldg(p.vs + at) : 0.f);
+          }
+          float mk = fmaxf(fmaxf(sc[0], sc[1]), fmaxf(sc[2], sc[3]));
+          // (scales are not negative: their bits order as integers)
+          mk = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mk)));
+          mv = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mv)));
+          const bool second = !DUAL && (n & 1);
+          int ev = second ? ev1 : ev0;
+          ev = first ? exponent_of(mv) : max(ev, exponent_of(mv));
+          if (second) ev1 = ev;
+          else ev0 = ev;
+          const int e = is_v ? ev : exponent_of(mk);
+          const float inv = exp2_int(-e);
+#pragma unroll
+          for (int x = 0; x < 4; ++x) raw_mul[slot * BN + x * 32 + lane] = (uint16_t)pack_f16x2(sc[x] * inv, 0.f);
+          if (lane == 0) raw_note[slot] = RawNote{live, fresh, e, ev};
+          __syncwarp();
+          if (lane == 0) mbar_arrive(fullb + slot);
+        }
+        ++n;
+        more = w.next(p);
+        if (more) row_next = lookup();
+      }
+      if (lane == 0) {
+        if (is_v && !cut) p.cut[2 * blockIdx.x + 1] = make_int4(0, 0, 0, 0);
+        issued[is_v ? 1 : 0] = n;
+        if (!ok) {
+          set_status(p.status, CPATTN_ERR_TIMEOUT);
+          *abort_flag = 1;
+        }
+      }
+    } else if (warp == kMmaWarp) {
+      // ---------------------------------------------------------- MMA issuer --
+      if (lane == 0) {
+        constexpr uint32_t kIdescQK = idesc_16bit_f32(QUANT, BM, BN, 0);
+        constexpr uint32_t kIdescPV = idesc_16bit_f32(QUANT, BM, D, 1);
+        const uint64_t dq0 = smem_desc_sw128(q_base, 16, 1024);
+        const uint64_t dk0 = smem_desc_sw128(ring_base, 16, 1024);
+        const uint64_t dv0 = smem_desc_sw128(ring_base, BN * 128, 1024);
+        auto issue_qk = [&](int s, int buf, int slot) {
+          const uint64_t qd = dq0 + (uint64_t)((buf * C::kQTile) >> 4), kd = dk0 + (uint64_t)((slot * C::kTile) >> 4);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            constexpr int kChunk = (BM * 128) >> 4;
+            const uint64_t off = (uint64_t)((kk >> 2) * kChunk + (kk & 3) * 2);
+            mma_ss(tmem_base + s * BN, qd + off, kd + off, kIdescQK, kk > 0 ? 1u : 0u);
+          }
+        };
+        auto issue_pv = [&](int s, int slot, bool first) {
+          const uint64_t vd = dv0 + (uint64_t)((slot * C::kTile) >> 4);
+#pragma unroll
+          for (int kk = 0; kk < BN / 16; ++kk)
+            mma_ts(tmem_base + 2 * BN + s * D, tmem_base + s * BN + kk * 8, vd + (uint64_t)(kk * ((16 * 128) >> 4)),
+                   kIdescPV, (!first || kk > 0) ? 1u : 0u);
+        };
+        auto wait_place = [&](int place) {
+          return wait_one(full + place % NS, (place / NS) & 1, abort_flag, p.timeout_ns);
+        };
+        TileWalk wq{{start}}, wv{{start}};
+        bool ok = true;
+        if constexpr (DUAL) {
+          // S of tile n for both streams, each behind its own P V of tile n - 1
+          auto begin = [&](int n, int s) {
+            if (s == 0) ok = ok && wait_place(k_place<DUAL>(n));
+            if (wq.t == 0) ok = ok && wait_one(q_full + s, wq.piece & 1, abort_flag, p.timeout_ns);
+            if (!ok) return;
+            tc_fence_after();
+            issue_qk(s, s, k_place<DUAL>(n) % NS);
+            mma_commit(s_full + s);
+            if (wq.left() == 0) mma_commit(q_empty + s);
+            if (s == 1) mma_commit(empty + k_place<DUAL>(n) % NS);
+          };
+          if (wq.next(p)) {
+            begin(0, 0);
+            begin(0, 1);
+          }
+          for (int n = 0; ok && wv.next(p); ++n) {
+            const int slot = v_place<DUAL>(n) % NS;
+            const bool more = wq.next(p);
+            ok = wait_place(v_place<DUAL>(n));
+            for (int s = 0; s < 2 && ok; ++s) {
+              ok = wait_one(p_full + s, n & 1, abort_flag, p.timeout_ns);
+              if (!ok) break;
+              tc_fence_after();
+              issue_pv(s, slot, wv.t == 0);
+              if (wv.left() == 0) mma_commit(o_full + s);
+              if (s == 1) mma_commit(empty + slot);
+              if (more) begin(n + 1, s);
+            }
+          }
+        } else {
+          auto begin = [&](int n) {
+            const int buf = wq.piece & 1, slot = k_place<DUAL>(n) % NS;
+            ok = ok && wait_place(k_place<DUAL>(n));
+            if (wq.t == 0) ok = ok && wait_one(q_full + buf, (wq.piece >> 1) & 1, abort_flag, p.timeout_ns);
+            if (!ok) return;
+            tc_fence_after();
+            issue_qk(n & 1, buf, slot);
+            mma_commit(s_full + (n & 1));
+            mma_commit(empty + slot);
+            if (wq.left() == 0) mma_commit(q_empty + buf);
+          };
+          for (int n = 0; n < 2; ++n)
+            if (wq.next(p)) begin(n);
+          for (int n = 0; ok && wv.next(p); ++n) {
+            const int s = n & 1, slot = v_place<DUAL>(n) % NS;
+            ok = wait_place(v_place<DUAL>(n)) && wait_one(p_full + s, (n >> 1) & 1, abort_flag, p.timeout_ns);
+            if (!ok) break;
+            tc_fence_after();
+            issue_pv(s, slot, wv.t < 2);
+            if (wv.left() < 2) mma_commit(o_full + s);
+            mma_commit(empty + slot);
+            if (wq.next(p)) begin(n + 2);
+          }
+        }
+        if (!ok) {
+          set_status(p.status, CPATTN_ERR_TIMEOUT);
+          *abort_flag = 1;
+        }
+        // every MMA and commit issued by this thread has completed
+        mma_commit(bar_drain);
+        wait_one(bar_drain, 0, nullptr, p.timeout_ns);
+      }
+    } else if (warp == kQWarp) {
+      // -------------------------------------------------------------- queries --
+      // D / 8 lanes to a row.  Dual: tile s of a piece in buffer s, when the piece before has
+      // no product left; single: the pieces' tiles take turns, one ahead.
+      constexpr int kLanes = D / 8, kRows = 32 / kLanes;
+      TreeWalk w{start};
+      TreePiece pc;
+      bool ok = true;
+      const int c = lane % kLanes;
+      for (int i = 0; ok && w.next(p, pc); ++i) {
+        for (int s = 0; s < (DUAL ? 2 : 1) && ok; ++s) {
+          const int buf = DUAL ? s : i & 1, use = DUAL ? i : i >> 1;
+          ok = wait_warp(q_empty + buf, (use & 1) ^ 1, abort_flag, p.timeout_ns);
+          if (!ok) break;
+          const uint32_t tile = q_base + buf * C::kQTile + (c >> 3) * (BM * 128);
+          const int rows = min(BM, pc.rows - s * BM);
+#pragma unroll 4
+          for (int r = lane / kLanes; r < rows; r += kRows) {
+            const int packed = pc.r0 + s * BM + r, node = group_div(p, packed);
+            const __nv_bfloat16* src = p.q + (long long)(pc.req.row0 + node) * p.q_row +
+                                       (long long)(pc.kv_head * p.g + packed - node * p.g) * p.q_head + c * 8;
+            const uint32_t at = tile + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+            if constexpr (!QUANT) {
+              asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at), "l"(src) : "memory");
+            } else {
+              // bf16 to f16 times 2^f with 2^f max|q| in [2^14, 2^15)
+              const uint4 v = __ldg(reinterpret_cast<const uint4*>(src));
+              uint32_t x[4] = {v.x, v.y, v.z, v.w};
+              uint32_t mx = __vmaxu2(__vmaxu2(x[0] & 0x7FFF7FFFu, x[1] & 0x7FFF7FFFu),
+                                     __vmaxu2(x[2] & 0x7FFF7FFFu, x[3] & 0x7FFF7FFFu));
+              mx = max(mx & 0xFFFFu, mx >> 16);
+              const uint32_t group = (kLanes == 32 ? 0u : ((1u << kLanes) - 1u)) << (lane & ~(kLanes - 1));
+#pragma unroll
+              for (int o = kLanes / 2; o > 0; o >>= 1) mx = max(mx, __shfl_xor_sync(group, mx, o));
+              const int f = min(max(14 - ((int)(mx >> 7) - 127), -126), 126);
+              const float up = exp2_int(f);
+#pragma unroll
+              for (int y = 0; y < 4; ++y)
+                x[y] = pack_f16x2(__uint_as_float(x[y] << 16) * up, __uint_as_float(x[y] & 0xFFFF0000u) * up);
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x[0]), "r"(x[1]), "r"(x[2]),
+                           "r"(x[3])
+                           : "memory");
+              if (c == 0) q_lift[((i & 1) * 2 + s) * BM + r] = (int8_t)f;
+            }
+          }
+          if constexpr (!QUANT) asm volatile("cp.async.wait_all;" ::: "memory");
+          fence_async_shared();
+          if (!p.withhold_q) mbar_arrive(q_full + buf);
+        }
+      }
+      if (!ok && lane == 0) {
+        set_status(p.status, CPATTN_ERR_TIMEOUT);
+        *abort_flag = 1;
+      }
+    }
+    if constexpr (QUANT) if (warp >= kConvertWarp) {
+      // --------------------------------------------------- codes to f16 tiles --
+      // Warp w has rows 32w .. 32w+31 of every tile; of a row, lane l has 8 codes of each 64.
+      const int w = warp - kConvertWarp;
+      const int rl = lane >> 3, cl = lane & 7;  // row of four, 8-code chunk
+      int tiles = 0;
+      {
+        TreeWalk walk{start};
+        TreePiece pc;
+        while (walk.next(p, pc)) tiles += pc.tiles;
+      }
+      const uint32_t swz[2] = {(uint32_t)((cl ^ rl) << 4), (uint32_t)((cl ^ (rl + 4)) << 4)};
+      constexpr int kBatch = 4, kHalves = D / 64;
+      uint32_t from[2][kHalves];
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int h = 0; h < kHalves; ++h)
+          from[x][h] = code_at<D>(w * 32 + rl + 4 * x, h * 4 + (cl >> 1)) + (cl & 1) * 8;
+      bool ok = true;
+      const int places = tiles == 0 ? 0 : v_place<DUAL>(tiles - 1) + 1;
+      for (int place = 0; place < places; ++place) {
+        bool is_v;
+        int n;
+        if (DUAL) {
+          is_v = place & 1;
+          n = place >> 1;
+        } else {
+          is_v = place > 0 && !(place & 1);
+          n = is_v ? (place - 2) >> 1 : (place + 1) >> 1;
+        }
+        if (!is_v && n >= tiles) continue;
+        const int raw = place % C::kRawStages, slot = place % NS;
+        ok = wait_warp2(empty + slot, ((place / NS) & 1) ^ 1, raw_full + raw, (place / C::kRawStages) & 1, abort_flag,
+                        p.timeout_ns);
+        if (!ok) break;
+        const RawNote note = raw_note[raw];
+        const uint8_t* src = smem + C::kRawOff + raw * C::kRawTile;
+        // rows of this warp that become zeros
+        uint32_t dead = note.live >= w * 32 + 32 ? 0u : note.live <= w * 32 ? ~0u : ~0u << (note.live - w * 32);
+        if (!is_v) {
+          if (w == 0 && lane == 0) tile_exp[n & 7] = make_int2(note.ek, note.ev);
+        } else if (note.fresh < BN) {  // new keys: a NaN's row
+          bool bad = false;
+#pragma unroll
+          for (int ch = 0; ch < D / 16; ++ch) {
+            const uint4 v = *reinterpret_cast<const uint4*>(src + code_at<D>(w * 32 + lane, ch));
+            bad = bad || __vcmpeq4(v.x & 0x7F7F7F7Fu, 0x7F7F7F7Fu) || __vcmpeq4(v.y & 0x7F7F7F7Fu, 0x7F7F7F7Fu) ||
+                  __vcmpeq4(v.z & 0x7F7F7F7Fu, 0x7F7F7F7Fu) || __vcmpeq4(v.w & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+          }
+          const uint32_t word = __ballot_sync(0xffffffffu, bad && w * 32 + lane >= note.fresh) & ~dead;
+          if (lane == 0) bad_slot[slot * 4 + w] = word;
+          dead |= word;
+        }
+        dead >>= rl;
+        const uint16_t* mul = raw_mul + raw * BN + w * 32 + rl;
+        uint8_t* dst = smem + C::kRingOff + slot * C::kTile + (w * 32 + rl) * 128;
+        // loads of a batch before its stores: the compiler cannot tell them apart
+#pragma unroll
+        for (int r0 = 0; r0 < 32; r0 += 4 * kBatch) {
+          uint2 v[kBatch][kHalves];
+          uint32_t m[kBatch];
+#pragma unroll
+          for (int x = 0; x < kBatch; ++x) {
+            m[x] = mul[r0 + 4 * x];
+#pragma unroll
+            for (int h = 0; h < kHalves; ++h)
+              v[x][h] = *reinterpret_cast<const uint2*>(src + from[x & 1][h] + (r0 + 4 * (x & ~1)) * D);
+          }
+          if (dead) {
+#pragma unroll
+            for (int x = 0; x < kBatch; ++x)
+#pragma unroll
+              for (int h = 0; h < kHalves; ++h)
+                if ((dead >> (r0 + 4 * x)) & 1u) v[x][h] = make_uint2(0, 0);
+          }
+#pragma unroll
+          for (int x = 0; x < kBatch; ++x)
+#pragma unroll
+            for (int h = 0; h < kHalves; ++h) {
+              const uint32_t m2 = m[x] * 0x10001u;
+              const uint2 a = codes_to_f16(v[x][h].x, m2), b = codes_to_f16(v[x][h].y, m2);
+              *reinterpret_cast<uint4*>(dst + h * (BN * 128) + (r0 + 4 * x) * 128 + swz[x & 1]) =
+                  make_uint4(a.x, a.y, b.x, b.y);
+            }
+        }
+        fence_async_shared();
+        mbar_arrive(full + slot);
+        mbar_arrive(raw_empty + raw);
+      }
+      if (!ok && lane == 0) {
+        set_status(p.status, CPATTN_ERR_TIMEOUT);
+        *abort_flag = 1;
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegsSoftmax));
+    // ----------------------------------------------------------- softmax --
+    // A wait that runs out leaves ok false for good: no more waits, but every barrier of the
+    // warps still comes, so that none is left behind in one.
+    const int s = warp >> 2;          // stream
+    const int wq = warp & 3;          // TMEM lane quarter
+    const int trow = wq * 32 + lane;  // row within the MMA tile
+    const int r = DUAL ? s * BM + trow : trow;  // within the unit
+    const uint32_t lanes = tmem_base + ((uint32_t)(wq * 32) << 16);
+    const uint32_t s_addr = lanes + s * BN, o_addr = lanes + 2 * BN + s * D;
+    TreeWalk w{start};
+    TreePiece pc;
+    bool ok = true, pending = false;  // pending: the other stream may still read this one's O
+    int n0 = 0;                       // KV tiles before the piece
+    int tails = 0;                    // of the stream, with new keys
+    int had[2] = {0, 0};              // pieces in which a stream had tiles
+    for (int i = 0; w.next(p, pc); ++i) {
+      const bool warp_live = (r & ~31) < pc.rows;
+      const int node = r < pc.rows ? group_div(p, pc.r0 + r) : 0;
+      float m_run = -INFINITY, l_run = 0.f, m_use = 0.f, factor = p.scale_log2;
+      int ev = 0;  // exponent of O
+      bool first = true;
+      for (int t = DUAL ? 0 : (n0 ^ s) & 1; t < pc.tiles; t += DUAL ? 1 : 2) {
+        const int n = n0 + t, key0 = (pc.t0 + t) * BN;
+        ok = ok && wait_warp(s_full + s, (DUAL ? n : n >> 1) & 1, abort_flag, p.timeout_ns);
+        tc_fence_after();
+        float sl2 = factor, o_scale = 1.f;
+        if constexpr (QUANT) {
+          if (first && r < pc.rows) factor = p.scale_log2 * exp2_int(-q_lift[((i & 1) * 2 + (DUAL ? s : 0)) * BM + trow]);
+          // written before the K tile went to the tensor core, and not again before this
+          // step's P has been used
+          const volatile int2* e = tile_exp + (n & 7);
+          const int ek = e->x, ev_now = e->y;
+          sl2 = score_factor(factor, exp2_int(ek));
+          if (!first && ev_now != ev) o_scale = exp2_int(max(ev - ev_now, -126));
+          ev = ev_now;
+        }
+        // tiles with new keys, or keys behind the last
+        uint32_t vis[4] = {~0u, ~0u, ~0u, ~0u};
+        const bool tail = key0 + BN > pc.req.L;
+        float poison = 0.f;
+        if (tail) {
+          const int slot = v_place<DUAL>(n) % NS;
+          if (warp_live) {
+#pragma unroll
+            for (int x = 0; x < 4; ++x) vis[x] = r < pc.rows ? seen_bits(p, pc.req, node, key0 + 32 * x) : 0u;
+          }
+          ok = ok && wait_warp(full + slot, (v_place<DUAL>(n) / NS) & 1, abort_flag, p.timeout_ns);
+          const uint32_t* words;
+          if constexpr (!QUANT) {
+            // value row trow of the tile: one of no key, or one that is not finite
+            uint8_t* const line = smem + C::kRingOff + slot * C::kTile + trow * 128;
+            auto chunk_at = [&](int c) { return (c >> 3) * (BN * 128) + ((c ^ trow) & 7) * 16; };
+            const int key = key0 + trow;
+            bool bad = false;
+            if (key >= pc.req.L && key < pc.keys) {
+#pragma unroll
+              for (int c = 0; c < D / 8; ++c) {
+                const uint4 v = *reinterpret_cast<const uint4*>(line + chunk_at(c));
+                bad = bad || __vcmpgeu2(v.x & 0x7FFF7FFFu, 0x7F807F80u) || __vcmpgeu2(v.y & 0x7FFF7FFFu, 0x7F807F80u) ||
+                      __vcmpgeu2(v.z & 0x7FFF7FFFu, 0x7F807F80u) || __vcmpgeu2(v.w & 0x7FFF7FFFu, 0x7F807F80u);
+              }
+            }
+            uint32_t* const mine = bad_scan + (s * 2 + (tails & 1)) * 4;
+            const uint32_t word = __ballot_sync(0xffffffffu, bad);
+            if (lane == 0) mine[wq] = word;
+            words = mine;
+            ++tails;
+            if (DUAL) bar_named(2, 256);  // both streams have looked at the tile
+            else bar_named(2 + s, 128);
+            if (bad || key >= pc.keys) {
+#pragma unroll
+              for (int c = 0; c < D / 8; ++c)
+                *reinterpret_cast<uint4*>(line + chunk_at(c)) = make_uint4(0, 0, 0, 0);
+            }
+            fence_async_shared();
+          } else {
+            words = bad_slot + slot * 4;
+          }
+          uint32_t hit = 0;
+#pragma unroll
+          for (int x = 0; x < 4; ++x) hit |= vis[x] & words[x];
+          if (r < pc.rows && hit) poison = __uint_as_float(0x7FC00000u);
+        }
+        if (warp_live && ok)
+          softmax_row<D, QUANT>(s_addr, o_addr, tail, vis, !first, o_scale, sl2, m_run, m_use, l_run);
+        l_run += poison;
+        first = false;
+        if (!DUAL && pending) {
+          bar_named(5, 256);
+          pending = false;
+        }
+        tc_fence_before();
+        mbar_arrive(p_full + s);
+      }
+      // ---- the piece's end ----
+      const int packed = pc.r0 + r;
+      const long long at = (long long)(pc.req.row0 + node) * p.Hq + pc.kv_head * p.g + packed - node * p.g;
+      if constexpr (DUAL) {
+        ok = ok && wait_warp(o_full + s, i & 1, abort_flag, p.timeout_ns);
+        tc_fence_after();
+        if (warp_live && ok) {
+          const bool none = l_run == 0.f;  // (a NaN sum is not none)
+          const float inv = none ? 0.f : exp2_int(ev) / l_run;
+#pragma unroll
+          for (int q = 0; q < D / 32; ++q) {
+            uint32_t v[32];
+            tmem_ld32(o_addr + q * 32, v);
+            tmem_wait_ld();
+            if (r < pc.rows) {
+#pragma unroll
+              for (int c = 0; c < 32; c += 8) {
+                float f[8];
+#pragma unroll
+                for (int x = 0; x < 8; ++x) f[x] = none ? 0.f : __uint_as_float(v[c + x]) * inv;
+                put8(p, pc, D, r, q * 4 + c / 8, at, f);
+              }
+            }
+          }
+          if (r < pc.rows) {
+            const float lse2 = none ? -INFINITY : m_use + lg2_approx(l_run);
+            if (pc.slot >= 0) p.ws_l[(long long)pc.slot * p.unit_rows + r] = lse2;
+            else p.lse[at] = lse2 * kLn2;
+          }
+        }
+        tc_fence_before();
+      } else {
+        if (pending) bar_named(5, 256);
+        ml[s * BM + trow] = make_float2(m_use, l_run);
+        if constexpr (QUANT) o_exp[s * BM + trow] = (int8_t)ev;
+        bar_named(4, 256);
+        // the streams that had tiles (an O of none is not looked at)
+        bool live[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          live[x] = pc.tiles > 1 || (n0 & 1) == x;
+          if (live[x]) ok = ok && wait_warp(o_full + x, had[x]++ & 1, abort_flag, p.timeout_ns);
+        }
+        tc_fence_after();
+        if (warp_live && ok) {
+          const float2 a = ml[trow], b = ml[BM + trow];
+          const float ua = QUANT ? exp2_int(o_exp[trow]) : 1.f, ub = QUANT ? exp2_int(o_exp[BM + trow]) : 1.f;
+          // (m of a stream without keys means nothing)
+          float M = fmaxf(a.y != 0.f ? a.x : -INFINITY, b.y != 0.f ? b.x : -INFINITY);
+          if (M == -INFINITY) M = 0.f;
+          const float fa = a.y != 0.f ? ex2_approx(a.x - M) : 0.f, fb = b.y != 0.f ? ex2_approx(b.x - M) : 0.f;
+          const float sum = (a.y != 0.f ? fa * a.y : 0.f) + (b.y != 0.f ? fb * b.y : 0.f);
+          const bool none = sum == 0.f;
+          const float inv = none ? 0.f : 1.f / sum;
+          const float ca = live[0] ? fa * inv * ua : 0.f, cb = live[1] ? fb * inv * ub : 0.f;
+          const uint32_t from = lanes + 2 * BN + s * (D / 2);  // this stream's half of the columns
+#pragma unroll
+          for (int q = 0; q < D / 64; ++q) {
+            uint32_t u[32], v[32];
+            tmem_ld32(from + q * 32, u);
+            tmem_ld32(from + D + q * 32, v);
+            tmem_wait_ld();
+            if (r < pc.rows) {
+#pragma unroll
+              for (int c = 0; c < 32; c += 8) {
+                float f[8];
+#pragma unroll
+                for (int x = 0; x < 8; ++x) {
+                  const float y = ca == 0.f ? 0.f : __uint_as_float(u[c + x]) * ca;
+                  f[x] = cb == 0.f ? y : fmaf(__uint_as_float(v[c + x]), cb, y);
+                }
+                put8(p, pc, D, r, s * (D / 16) + q * 4 + c / 8, at, f);
+              }
+            }
+          }
+          if (r < pc.rows && s == 0) {
+            const float lse2 = none ? -INFINITY : M + lg2_approx(sum);
+            if (pc.slot >= 0) p.ws_l[(long long)pc.slot * p.unit_rows + r] = lse2;
+            else p.lse[at] = lse2 * kLn2;
+          }
+        }
+        tc_fence_before();
+        pending = true;
+      }
+      n0 += pc.tiles;
+    }
+    if (!ok && lane == 0) {
+      set_status(p.status, CPATTN_ERR_TIMEOUT);
+      *abort_flag = 1;
+    }
+  }
+
+  // ---- teardown ----
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kKWarp) {
+    if (lane == 0 && *abort_flag) {
+      // let the copies in flight land before the shared memory goes: the last of each slot
+      constexpr int kSt = QUANT ? C::kRawStages : NS;
+      const int nk = issued[0], nv = issued[1];
+      for (int slot = 0; slot < kSt; ++slot) {
+        int last = -1;
+        for (int n = max(0, nk - kSt - 1); n < nk; ++n)
+          if (k_place<DUAL>(n) % kSt == slot) last = max(last, k_place<DUAL>(n));
+        for (int n = max(0, nv - kSt - 1); n < nv; ++n)
+          if (v_place<DUAL>(n) % kSt == slot) last = max(last, v_place<DUAL>(n));
+        if (last >= 0) wait_one((QUANT ? raw_full : full) + slot, (last / kSt) & 1, nullptr, p.timeout_ns);
+      }
+    }
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem_base, C::kTmemCols);
+  }
+}
+
+template <int D, bool QUANT, bool DUAL>
+int launch(const TreeMaps& m, const TreeParams& p, int num_ctas, cudaStream_t stream) {
+  using C = MmaCfg<D, QUANT, DUAL>;
+  auto kern = attn_tree_mma_kernel<D, QUANT, DUAL>;
+  if (!allow_smem(kern, C::kSmemBytes)) return CPATTN_ERR_CUDA;
+  if (!split_covered(kern, C::kThreads, C::kRegsSoftmax * 256 + C::kRegsOther * (C::kThreads - 256)))
+    return CPATTN_ERR_UNSUPPORTED;
+  return launch_kernel(kern, (unsigned)num_ctas, C::kThreads, C::kSmemBytes, stream, false, m, p) == cudaSuccess
+             ? CPATTN_OK
+             : CPATTN_ERR_CUDA;
+}
+template <bool DUAL>
+int launch(const TreeMaps& m, const TreeParams& p, int d, bool quant, int num_ctas, cudaStream_t stream) {
+  return d == 128 ? (quant ? launch<128, true, DUAL>(m, p, num_ctas, stream)
+                           : launch<128, false, DUAL>(m, p, num_ctas, stream))
+                  : (quant ? launch<64, true, DUAL>(m, p, num_ctas, stream)
+                           : launch<64, false, DUAL>(m, p, num_ctas, stream));
+}
+
+}  // namespace
+
+int launch_tree_mma(const TreeMaps& m, const TreeParams& p, int d, bool quant, int num_ctas, cudaStream_t stream) {
+  return p.unit_rows == BM ? launch<false>(m, p, d, quant, num_ctas, stream)
+                           : launch<true>(m, p, d, quant, num_ctas, stream);
+}
+
+}  // namespace cpattn

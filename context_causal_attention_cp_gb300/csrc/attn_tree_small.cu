@@ -544,83 +544,92 @@ attn_tree_small_kernel(const __grid_constant__ TreeMaps maps, const TreeParams p
   auto arrive_copies = [&](uint64_t* bar) {  // when this lane's copies so far have landed
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
   };
-  if (warp >= kWarps) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
-  else asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsWork));
-  if (warp == kWarps) {
-    constexpr int kChunks = QUANT ? 1 : D / 64;     // boxes across a row
-    constexpr int kLine = C::kTile / BN / kChunks;  // bytes of a box row
-    const int whole = min(BN, 1 << p.log_page);     // rows of a whole box
-    int seq = 0, cut = 0;
-    bool ok = true;
-    for (int n = 0; ok && walk.next(p, pc); ++n) {
-      const int qb = n & 1;
-      if (pc.blocks) {
-        cut = pc.blocks;
-        if (lane == 0) put_cut(p, pc, cut);
-      }
-      ok = wait_warp(q_empty + qb, ((n >> 1) & 1) ^ 1, abort_flag, p.timeout_ns);
-      if (!ok) break;
-      // the query rows, 16-byte chunks swizzled over a row's length
-      for (int x = lane; x < pc.rows * (D / 8); x += 32) {
-        const int r = x / (D / 8), ch = x % (D / 8), packed = pc.r0 + r, node = group_div(p, packed);
-        const __nv_bfloat16* src = p.q + (long long)(pc.req.row0 + node) * p.q_row +
-                                   (long long)(pc.kv_head * p.g + packed - node * p.g) * p.q_head + ch * 8;
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
-                         smem_u32(smem + C::kQOff + qb * C::kQ) + r * (D * 2) + ((ch ^ (r & 7)) << 4)),
-                     "l"(src)
-                     : "memory");
-      }
-      if (!p.withhold_q) arrive_copies(q_full + qb);
-      for (int t = 0; t < pc.tiles && ok; ++t) {
-        const int key0 = (pc.t0 + t) * BN, live = min(BN, pc.keys - key0);
-        // a lane's box: whole pages, or 16 rows of the tile's end
-        const int box = live > BN - 16 ? whole : 16, boxes = (live + box - 1) / box;
-        const int mine = lane < boxes ? cache_row(p, pc.b, key0 + lane * box) : 0;
-        // (e4m3) the cache rows of the lane's scales, keys x * 32 + lane
-        int srow[4] = {0, 0, 0, 0};
-        if constexpr (QUANT) {
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const int key = x * 32 + lane;
-            srow[x] = __shfl_sync(0xffffffffu, mine, (key / box) & 31) + key % box;
-          }
+  if (warp >= kWarps) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
+    if (warp == kWarps) {
+      constexpr int kChunks = QUANT ? 1 : D / 64;     // boxes across a row
+      constexpr int kLine = C::kTile / BN / kChunks;  // bytes of a box row
+      const int whole_log = min(7, p.log_page);       // rows of a whole box
+      int seq = 0, cut = 0;
+      bool ok = true;
+      for (int n = 0; ok && walk.next(p, pc); ++n) {
+        const int qb = n & 1;
+        if (pc.blocks) {
+          cut = pc.blocks;
+          if (lane == 0) put_cut(p, pc, cut);
         }
-        for (int kv = 0; kv < 2; ++kv, ++seq) {
-          const int slot = seq % NS;
-          ok = wait_warp(empty + slot, ((seq / NS) & 1) ^ 1, abort_flag, p.timeout_ns);
-          if (!ok) break;
-          uint8_t* dst = smem + slot * C::kTile;
-          if (lane == 0) mbar_arrive_expect_tx(full + slot, boxes * box * kLine * kChunks);
-          __syncwarp();
-          if (lane < boxes) {
-            const CUtensorMap* tm = box == whole ? (kv ? &maps.v : &maps.k) : (kv ? &maps.v_tail : &maps.k_tail);
-#pragma unroll
-            for (int c = 0; c < kChunks; ++c)
-              tma_load_3d(dst + (c * BN + lane * box) * kLine, tm, full + slot, c * 64, pc.kv_head, mine);
-          }
+        ok = wait_warp(q_empty + qb, ((n >> 1) & 1) ^ 1, abort_flag, p.timeout_ns);
+        if (!ok) break;
+        // the query rows, 16-byte chunks swizzled over a row's length
+        for (int x = lane; x < pc.rows * (D / 8); x += 32) {
+          const int r = x / (D / 8), ch = x % (D / 8), packed = pc.r0 + r, node = group_div(p, packed);
+          const __nv_bfloat16* src = p.q + (long long)(pc.req.row0 + node) * p.q_row +
+                                     (long long)(pc.kv_head * p.g + packed - node * p.g) * p.q_head + ch * 8;
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                           smem_u32(smem + C::kQOff + qb * C::kQ) + r * (D * 2) + ((ch ^ (r & 7)) << 4)),
+                       "l"(src)
+                       : "memory");
+        }
+        if (!p.withhold_q) arrive_copies(q_full + qb);
+        // Cache row of the lane's box of tile t: whole pages, or 16 rows of the unit's end.
+        // Looked up a tile ahead, so that the page table's latency is not waited for.
+        auto box_log = [&](int t) { return min(BN, pc.keys - (pc.t0 + t) * BN) > BN - 16 ? whole_log : 4; };
+        auto lookup = [&](int t) {
+          const int key0 = (pc.t0 + t) * BN, live = min(BN, pc.keys - key0), log = box_log(t);
+          return t < pc.tiles && (lane << log) < live ? cache_row(p, pc.b, key0 + (lane << log)) : 0;
+        };
+        int next = lookup(0);
+        for (int t = 0; t < pc.tiles && ok; ++t) {
+          const int mine = next, live = min(BN, pc.keys - (pc.t0 + t) * BN);
+          const int log = box_log(t), boxes = (live + (1 << log) - 1) >> log;
+          next = lookup(t + 1);
+          // (e4m3) the cache rows of the lane's scales, keys x * 32 + lane
+          int srow[4] = {0, 0, 0, 0};
           if constexpr (QUANT) {
-            const float* src = (kv ? p.vs : p.ks) + (long long)pc.kv_head * p.s_head;
-            const uint32_t at = smem_u32(smem + C::kScaleOff + slot * C::kScales) + lane * 4;
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-              if (x * 32 + lane < live && srow[x] < p.num_kv_rows)
-                asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(at + x * 128), "l"(src + srow[x])
-                             : "memory");
-            arrive_copies(full + slot);
+  #pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const int key = x * 32 + lane;
+              srow[x] = __shfl_sync(0xffffffffu, mine, key >> log) + (key & ((1 << log) - 1));
+            }
+          }
+          for (int kv = 0; kv < 2; ++kv, ++seq) {
+            const int slot = seq % NS;
+            ok = wait_warp(empty + slot, ((seq / NS) & 1) ^ 1, abort_flag, p.timeout_ns);
+            if (!ok) break;
+            uint8_t* dst = smem + slot * C::kTile;
+            if (lane == 0) mbar_arrive_expect_tx(full + slot, (boxes << log) * kLine * kChunks);
+            __syncwarp();
+            if (lane < boxes) {
+              const CUtensorMap* tm = log == whole_log ? (kv ? &maps.v : &maps.k) : (kv ? &maps.v_tail : &maps.k_tail);
+  #pragma unroll
+              for (int c = 0; c < kChunks; ++c)
+                tma_load_3d(dst + (c * BN + (lane << log)) * kLine, tm, full + slot, c * 64, pc.kv_head, mine);
+            }
+            if constexpr (QUANT) {
+              const float* src = (kv ? p.vs : p.ks) + (long long)pc.kv_head * p.s_head;
+              const uint32_t at = smem_u32(smem + C::kScaleOff + slot * C::kScales) + lane * 4;
+  #pragma unroll
+              for (int x = 0; x < 4; ++x)
+                if (x * 32 + lane < live && srow[x] < p.num_kv_rows)
+                  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(at + x * 128), "l"(src + srow[x])
+                               : "memory");
+              arrive_copies(full + slot);
+            }
           }
         }
       }
-    }
-    asm volatile("cp.async.wait_all;" ::: "memory");
-    if (lane == 0) {
-      if (!cut) p.cut[2 * blockIdx.x + 1] = make_int4(0, 0, 0, 0);
-      *issued_loads = seq;
-      if (!ok) {
-        set_status(p.status, CPATTN_ERR_TIMEOUT);
-        *abort_flag = 1;
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      if (lane == 0) {
+        if (!cut) p.cut[2 * blockIdx.x + 1] = make_int4(0, 0, 0, 0);
+        *issued_loads = seq;
+        if (!ok) {
+          set_status(p.status, CPATTN_ERR_TIMEOUT);
+          *abort_flag = 1;
+        }
       }
     }
-  } else if (warp < kWarps) {
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsWork));
     Warp<D, QUANT, NQ, QW> w;
     w.base = smem_u32(smem);
     w.mem = smem;
@@ -672,7 +681,9 @@ int launch(const TreeMaps& m, const TreeParams& p, int d, bool quant, int num_ct
 }  // namespace
 
 int launch_tree_small(const TreeMaps& m, const TreeParams& p, int d, bool quant, int num_ctas, cudaStream_t stream) {
-  return launch<1, 1>(m, p, d, quant, num_ctas, stream);
+  return p.unit_rows == 8    ? launch<1, 1>(m, p, d, quant, num_ctas, stream)
+         : p.unit_rows == 16 ? launch<2, 1>(m, p, d, quant, num_ctas, stream)
+                             : launch<2, 2>(m, p, d, quant, num_ctas, stream);
 }
 
 }  // namespace cpattn
