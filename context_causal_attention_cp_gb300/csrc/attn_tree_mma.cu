@@ -23,6 +23,7 @@
 // would not keep them from the rows that do not see them.  A row that does see one becomes
 // NaN by its sum.
 #include <algorithm>
+#include <type_traits>
 
 #include "attn_tree.cuh"
 
@@ -53,7 +54,8 @@ struct MmaCfg {
   static constexpr int kMlOff = kLiftOff + (QUANT ? 4 * BM : 0);     // single: (m, l) of each stream's rows
   static constexpr int kEvOff = kMlOff + (DUAL ? 0 : 2 * BM * 8);    // and O's exponent
   static constexpr int kBadOff = kEvOff + (QUANT && !DUAL ? 2 * BM : 0);  // value rows that are not finite
-  static constexpr int kBarOff = kBadOff + 2 * 2 * 16 + kStages * 16;
+  static constexpr int kTilesOff = kBadOff + 2 * 2 * 16 + kStages * 16;  // KV tiles of pieces i mod 8
+  static constexpr int kBarOff = kTilesOff + 32;
   static constexpr int kNumBars = 2 * kStages + 2 * kRawStages + 2 * 5 + 1;
   static constexpr int kWordOff = kBarOff + kNumBars * 8;
   static constexpr int kSumOff = (kWordOff + 64 + 7) & ~7;
@@ -89,8 +91,32 @@ struct TileWalk {
     }
     return true;
   }
-  __device__ __forceinline__ int left() const { return pc.tiles - 1 - t; }  // behind this one
 };
+
+// The MMAs and commits of ptx.cuh, by the lane with `lead` of a whole warp.
+__device__ __forceinline__ void mma_ss_lead(uint32_t lead, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                            uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 q, %5, 0;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(lead)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts_lead(uint32_t lead, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                            uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 q, %5, 0;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(lead)
+      : "memory");
+}
+__device__ __forceinline__ void mma_commit_lead(uint32_t lead, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+      "r"(lead)
+      : "memory");
+}
 
 // The bits of the keys that new row `node` sees of the 32 from key0 on.
 __device__ __forceinline__ uint32_t seen_bits(const TreeParams& p, const TreeReq& r, int node, int key0) {
@@ -230,6 +256,7 @@ attn_tree_mma_kernel(const __grid_constant__ TreeMaps maps, const TreeParams p) 
   int8_t* o_exp = reinterpret_cast<int8_t*>(smem + C::kEvOff);
   uint32_t* bad_scan = reinterpret_cast<uint32_t*>(smem + C::kBadOff);  // [2 streams][2][4]
   uint32_t* bad_slot = bad_scan + 16;                                   // [kStages][4] (e4m3)
+  volatile int* piece_tiles = reinterpret_cast<volatile int*>(smem + C::kTilesOff);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kWordOff);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* issued = reinterpret_cast<volatile int*>(tmem_slot + 2);  // K and V tiles, for the abort drain
@@ -374,93 +401,158 @@ attn_tree_mma_kernel(const __grid_constant__ TreeMaps maps, const TreeParams p) 
       }
     } else if (warp == kMmaWarp) {
       // ---------------------------------------------------------- MMA issuer --
-      if (lane == 0) {
-        constexpr uint32_t kIdescQK = idesc_16bit_f32(QUANT, BM, BN, 0);
-        constexpr uint32_t kIdescPV = idesc_16bit_f32(QUANT, BM, D, 1);
-        const uint64_t dq0 = smem_desc_sw128(q_base, 16, 1024);
-        const uint64_t dk0 = smem_desc_sw128(ring_base, 16, 1024);
-        const uint64_t dv0 = smem_desc_sw128(ring_base, BN * 128, 1024);
-        auto issue_qk = [&](int s, int buf, int slot) {
-          const uint64_t qd = dq0 + (uint64_t)((buf * C::kQTile) >> 4), kd = dk0 + (uint64_t)((slot * C::kTile) >> 4);
+      // The whole warp runs it and one lane issues: what the MMAs' descriptors are made of is
+      // then uniform.  The pieces' tile counts come with their queries (0: no more).
+      const uint32_t lead = lane == 0;
+      constexpr uint32_t kIdescQK = idesc_16bit_f32(QUANT, BM, BN, 0);
+      constexpr uint32_t kIdescPV = idesc_16bit_f32(QUANT, BM, D, 1);
+      const uint64_t dq0 = smem_desc_sw128(q_base, 16, 1024);
+      const uint64_t dk0 = smem_desc_sw128(ring_base, 16, 1024);
+      const uint64_t dv0 = smem_desc_sw128(ring_base, BN * 128, 1024);
+      auto issue_qk = [&](int s, int buf, int slot) {
+        const uint64_t qd = dq0 + (uint32_t)(buf * (C::kQTile >> 4)), kd = dk0 + (uint32_t)(slot * (C::kTile >> 4));
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            constexpr int kChunk = (BM * 128) >> 4;
-            const uint64_t off = (uint64_t)((kk >> 2) * kChunk + (kk & 3) * 2);
-            mma_ss(tmem_base + s * BN, qd + off, kd + off, kIdescQK, kk > 0 ? 1u : 0u);
-          }
-        };
-        auto issue_pv = [&](int s, int slot, bool first) {
-          const uint64_t vd = dv0 + (uint64_t)((slot * C::kTile) >> 4);
+        for (int kk = 0; kk < D / 16; ++kk) {
+          constexpr int kChunk = (BM * 128) >> 4;
+          const uint64_t off = (uint64_t)((kk >> 2) * kChunk + (kk & 3) * 2);
+          mma_ss_lead(lead, tmem_base + s * BN, qd + off, kd + off, kIdescQK, kk > 0 ? 1u : 0u);
+        }
+      };
+      auto issue_pv = [&](int s, int slot, bool first) {
+        const uint64_t vd = dv0 + (uint32_t)(slot * (C::kTile >> 4));
 #pragma unroll
-          for (int kk = 0; kk < BN / 16; ++kk)
-            mma_ts(tmem_base + 2 * BN + s * D, tmem_base + s * BN + kk * 8, vd + (uint64_t)(kk * ((16 * 128) >> 4)),
-                   kIdescPV, (!first || kk > 0) ? 1u : 0u);
+        for (int kk = 0; kk < BN / 16; ++kk)
+          mma_ts_lead(lead, tmem_base + 2 * BN + s * D, tmem_base + s * BN + kk * 8,
+                      vd + (uint64_t)(kk * ((16 * 128) >> 4)), kIdescPV, (!first || kk > 0) ? 1u : 0u);
+      };
+      auto commit = [&](uint64_t* bar) { mma_commit_lead(lead, bar); };
+      auto wait = [&](uint64_t* bar, int parity) { return wait_warp(bar, parity, abort_flag, p.timeout_ns); };
+      // Tiles of the pieces for the products Q K^T, which run ahead, and P V.
+      int left_q = 0, left_v = 0;  // tiles of the piece behind the one at hand
+      int piece_q = -1, piece_v = -1;
+      uint32_t k_at = 0, v_at = DUAL ? 1 : 2;  // ring slots, and their phases
+      uint32_t k_phase = 0, v_phase = 0;
+      bool head_q = false, ok = true;
+      bool head_v[2] = {false, false};
+      auto advance = [&](uint32_t& slot, uint32_t& phase, uint32_t by) {
+        slot += by;
+        if (slot >= NS) {
+          slot -= NS;
+          phase ^= 1;
+        }
+      };
+      // The next tile's queries and K; false when there is none, or a wait ran out.
+      auto next_q = [&]() {
+        head_q = left_q == 0;
+        if (head_q) {
+          ++piece_q;
+          const int buf = DUAL ? 0 : piece_q & 1;
+          ok = wait(q_full + buf, (DUAL ? piece_q : piece_q >> 1) & 1);
+          if (!ok) return false;
+          left_q = __shfl_sync(0xffffffffu, piece_tiles[piece_q & 7], 0);
+          if (left_q == 0) return false;
+          if (DUAL) ok = wait(q_full + 1, piece_q & 1);
+        }
+        --left_q;
+        ok = ok && wait(full + k_at, k_phase);
+        return ok;
+      };
+      // (there is one wherever there was a next_q that has not been followed)
+      auto next_v = [&]() {
+        if (left_v == 0) {
+          ++piece_v;
+          left_v = __shfl_sync(0xffffffffu, piece_tiles[piece_v & 7], 0);
+          head_v[0] = head_v[1] = true;
+        }
+        --left_v;
+        return wait(full + v_at, v_phase);
+      };
+      if constexpr (DUAL) {
+        auto begin = [&](int s) {
+          tc_fence_after();
+          issue_qk(s, s, k_at);
+          commit(s_full + s);
+          if (left_q == 0) commit(q_empty + s);
         };
-        auto wait_place = [&](int place) {
-          return wait_one(full + place % NS, (place / NS) & 1, abort_flag, p.timeout_ns);
+        auto begun = [&]() {
+          commit(empty + k_at);
+          advance(k_at, k_phase, 2);
         };
-        TileWalk wq{{start}}, wv{{start}};
-        bool ok = true;
-        if constexpr (DUAL) {
-          // S of tile n for both streams, each behind its own P V of tile n - 1
-          auto begin = [&](int n, int s) {
-            if (s == 0) ok = ok && wait_place(k_place<DUAL>(n));
-            if (wq.t == 0) ok = ok && wait_one(q_full + s, wq.piece & 1, abort_flag, p.timeout_ns);
-            if (!ok) return;
-            tc_fence_after();
-            issue_qk(s, s, k_place<DUAL>(n) % NS);
-            mma_commit(s_full + s);
-            if (wq.left() == 0) mma_commit(q_empty + s);
-            if (s == 1) mma_commit(empty + k_place<DUAL>(n) % NS);
-          };
-          if (wq.next(p)) {
-            begin(0, 0);
-            begin(0, 1);
-          }
-          for (int n = 0; ok && wv.next(p); ++n) {
-            const int slot = v_place<DUAL>(n) % NS;
-            const bool more = wq.next(p);
-            ok = wait_place(v_place<DUAL>(n));
-            for (int s = 0; s < 2 && ok; ++s) {
-              ok = wait_one(p_full + s, n & 1, abort_flag, p.timeout_ns);
-              if (!ok) break;
-              tc_fence_after();
-              issue_pv(s, slot, wv.t == 0);
-              if (wv.left() == 0) mma_commit(o_full + s);
-              if (s == 1) mma_commit(empty + slot);
-              if (more) begin(n + 1, s);
-            }
-          }
-        } else {
-          auto begin = [&](int n) {
-            const int buf = wq.piece & 1, slot = k_place<DUAL>(n) % NS;
-            ok = ok && wait_place(k_place<DUAL>(n));
-            if (wq.t == 0) ok = ok && wait_one(q_full + buf, (wq.piece >> 1) & 1, abort_flag, p.timeout_ns);
-            if (!ok) return;
-            tc_fence_after();
-            issue_qk(n & 1, buf, slot);
-            mma_commit(s_full + (n & 1));
-            mma_commit(empty + slot);
-            if (wq.left() == 0) mma_commit(q_empty + buf);
-          };
-          for (int n = 0; n < 2; ++n)
-            if (wq.next(p)) begin(n);
-          for (int n = 0; ok && wv.next(p); ++n) {
-            const int s = n & 1, slot = v_place<DUAL>(n) % NS;
-            ok = wait_place(v_place<DUAL>(n)) && wait_one(p_full + s, (n >> 1) & 1, abort_flag, p.timeout_ns);
+        bool more = next_q();
+        if (more) {
+          begin(0);
+          begin(1);
+          begun();
+        }
+        for (int n = 0; more && ok; ++n) {
+          ok = next_v();
+          const bool last = left_v == 0;
+          ok = ok && wait(p_full, n & 1);
+          if (!ok) break;
+          tc_fence_after();
+          issue_pv(0, v_at, head_v[0]);
+          if (last) commit(o_full);
+          // (a next piece's queries may still be on their way: they do not hold up stream 1)
+          const bool turn = left_q > 0;
+          if (turn) {
+            more = next_q();
             if (!ok) break;
-            tc_fence_after();
-            issue_pv(s, slot, wv.t < 2);
-            if (wv.left() < 2) mma_commit(o_full + s);
-            mma_commit(empty + slot);
-            if (wq.next(p)) begin(n + 2);
+            begin(0);
+          }
+          ok = wait(p_full + 1, n & 1);
+          if (!ok) break;
+          tc_fence_after();
+          issue_pv(1, v_at, head_v[0]);
+          head_v[0] = false;
+          if (last) commit(o_full + 1);
+          commit(empty + v_at);
+          advance(v_at, v_phase, 2);
+          if (!turn) {
+            more = next_q();
+            if (!more) break;
+            begin(0);
+          }
+          begin(1);
+          begun();
+        }
+      } else {
+        int ahead = 0;  // tiles begun
+        auto begin = [&](int s) {
+          tc_fence_after();
+          issue_qk(s, piece_q & 1, k_at);
+          commit(s_full + s);
+          commit(empty + k_at);
+          if (left_q == 0) commit(q_empty + (piece_q & 1));
+          advance(k_at, k_phase, ahead == 0 ? 1 : 2);
+          ++ahead;
+        };
+        bool more = true;
+        for (int s = 0; s < 2 && more; ++s) {
+          more = next_q();
+          if (more) begin(s);
+        }
+        for (int n = 0; n < ahead && ok; ++n) {
+          const int s = n & 1;
+          ok = next_v() && wait(p_full + s, (n >> 1) & 1);
+          if (!ok) break;
+          tc_fence_after();
+          issue_pv(s, v_at, head_v[s]);
+          head_v[s] = false;
+          if (left_v < 2) commit(o_full + s);
+          commit(empty + v_at);
+          advance(v_at, v_phase, 2);
+          if (more) {
+            more = next_q();
+            if (more) begin(s);
           }
         }
-        if (!ok) {
-          set_status(p.status, CPATTN_ERR_TIMEOUT);
-          *abort_flag = 1;
-        }
-        // every MMA and commit issued by this thread has completed
+      }
+      if (!ok && lane == 0) {
+        set_status(p.status, CPATTN_ERR_TIMEOUT);
+        *abort_flag = 1;
+      }
+      // every MMA and commit issued by this thread has completed
+      if (lane == 0) {
         mma_commit(bar_drain);
         wait_one(bar_drain, 0, nullptr, p.timeout_ns);
       }
@@ -473,11 +565,15 @@ attn_tree_mma_kernel(const __grid_constant__ TreeMaps maps, const TreeParams p) 
       TreePiece pc;
       bool ok = true;
       const int c = lane % kLanes;
-      for (int i = 0; ok && w.next(p, pc); ++i) {
+      bool more = true;
+      for (int i = 0; ok && more; ++i) {
+        more = w.next(p, pc);
+        if (!more) pc.rows = 0;
         for (int s = 0; s < (DUAL ? 2 : 1) && ok; ++s) {
           const int buf = DUAL ? s : i & 1, use = DUAL ? i : i >> 1;
           ok = wait_warp(q_empty + buf, (use & 1) ^ 1, abort_flag, p.timeout_ns);
           if (!ok) break;
+          if (lane == 0 && s == 0) piece_tiles[i & 7] = more ? pc.tiles : 0;
           const uint32_t tile = q_base + buf * C::kQTile + (c >> 3) * (BM * 128);
           const int rows = min(BM, pc.rows - s * BM);
 #pragma unroll 4
