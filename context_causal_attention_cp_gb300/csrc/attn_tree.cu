@@ -58,6 +58,21 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const TreePar
   if (col == 0) p.lse[at] = w == 0.f ? -INFINITY : (use + log2f(w)) * kLn2;
 }
 
+// 3-D map of the queries (cols, heads, rows) whose box is 64 columns of the g heads of a KV
+// head and of BM / g rows.
+bool make_q_map(CUtensorMap* m, const void* q, int cols, int heads, int rows, int64_t head_stride,
+                int64_t row_stride, int g) {
+  auto enc = tensor_map_encoder();
+  if (!enc) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)heads, (cuuint64_t)rows};
+  cuuint64_t strides[2] = {(cuuint64_t)(head_stride * 2), (cuuint64_t)(row_stride * 2)};
+  cuuint32_t box[3] = {64, (cuuint32_t)g, (cuuint32_t)(BM / g)};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(q), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Packed rows of a unit, by the rows that a request is expected to have.
 int unit_rows_of(int g, int max_nodes) {
   const long long rows = (long long)g * max_nodes;
@@ -152,6 +167,7 @@ extern "C" int cp_attn_tree(const void* q, int64_t q_row_stride, int64_t q_head_
   p.scale_log2 = scale * kLog2e;
   p.o = o;
   p.o_f32 = o_is_fp32 ? 1 : 0;
+  p.o_32 = (reinterpret_cast<uintptr_t>(o) & 31u) == 0;
   p.lse = lse;
   int64_t o_at, l_at, bytes;
   plan_sizes(Hq, Hkv, dv, max_nodes, num_ctas, &p.unit_rows, &o_at, &l_at, &bytes);
@@ -170,6 +186,9 @@ extern "C" int cp_attn_tree(const void* q, int64_t q_row_stride, int64_t q_head_
   if (!map(&m.k, k, k_head_stride, k_row_stride, whole) || !map(&m.v, v, v_head_stride, v_row_stride, whole) ||
       !map(&m.k_tail, k, k_head_stride, k_row_stride, 16) || !map(&m.v_tail, v, v_head_stride, v_row_stride, 16))
     return CPATTN_ERR_CUDA;
+  // (a map wants strides; the slow way takes any)
+  p.q_boxes = !quant && p.unit_rows >= BM && BM % p.g == 0 && q_row_stride > 0 && q_head_stride > 0 &&
+              make_q_map(&m.q, q, d, Hq, num_rows, q_head_stride, q_row_stride, p.g);
   const int r = p.unit_rows < BM ? launch_tree_small(m, p, d, quant, num_ctas, stream)
                                  : launch_tree_mma(m, p, d, quant, num_ctas, stream);
   if (r != CPATTN_OK) return r;

@@ -32,7 +32,8 @@ struct TreeParams {
   int num_kv_rows;
   float scale_log2;
   void* o;
-  int o_f32;
+  int o_f32, o_32;  // fp32; 32-byte aligned
+  int q_boxes;      // a tile's 128 packed rows are a box of the queries: all heads of 128 / g rows
   float* lse;
   float* ws_o;  // [slots][dv / 8][unit_rows][8]
   float* ws_l;  // [slots][unit_rows], log2 units
@@ -51,6 +52,7 @@ struct TreeCut {
 // 8, 16 or 32 rows; pages: boxes of whole pages (at most 128 rows) and of 16 rows.
 struct TreeMaps {
   CUtensorMap k, v, k_tail, v_tail;
+  CUtensorMap q;  // with TreeParams::q_boxes
 };
 // Whether a launch of `kern` has the registers that its warps share out (setmaxnreg.inc waits
 // for them): a property of this binary.
@@ -139,53 +141,115 @@ __device__ __forceinline__ TreeStart tree_start(const TreeParams& p, long long* 
 }
 
 struct TreePiece {
-  TreeReq req;
-  int b, kv_head;
-  int r0, rows;    // first packed row of the unit and its rows
-  int t0, tiles;   // KV tiles
-  int keys;        // of the unit
-  int slot;        // of the partial, -1: the unit is whole
-  int blocks;      // that the unit is cut over, when it begins here and is cut; else 0
+  int row0, T, L, b;       // the request
+  int kv_head, r0, rows;   // first packed row of the unit and its rows
+  int t0, tiles, keys;     // KV tiles of the piece (0: there is none), keys of the unit
+  int slot;                // of the partial, -1: the unit is whole
+  int blocks;              // that the unit is cut over, when it begins here and is cut; else 0
 };
+static_assert(sizeof(TreePiece) == 48, "three 16-byte words");
 
-// Steps through a share; every role of a block walks on its own.
+// Steps through a share.  The next request's words are loaded while the one at hand is walked:
+// under load they are a few thousand cycles away.
 struct TreeWalk {
   TreeStart s;
+  TreeReq r, ahead;
+  long long w0;  // place of the unit at hand
+  int tiles, rts, kv_head, rt;
+  __device__ __forceinline__ TreeReq load(const TreeParams& p, int b) const {
+    bool bad;
+    return b < p.num_reqs ? load_req(p, b, bad) : TreeReq{0, 0, 0};
+  }
+  __device__ __forceinline__ void take(const TreeParams& p) {
+    tiles = num_tiles(max(1, r.L + r.T));
+    rts = row_tiles(p, r);
+  }
+  __device__ __forceinline__ TreeWalk(const TreeParams& p, const TreeStart& start) : s(start) {
+    tiles = rts = 1;
+    kv_head = rt = 0;
+    w0 = 0;
+    if (s.at >= s.end) return;
+    r = load(p, s.b);
+    ahead = load(p, s.b + 1);
+    take(p);
+    const long long unit = (s.at - s.b0) / tiles;
+    w0 = s.b0 + unit * tiles;
+    kv_head = (int)(unit / rts);
+    rt = (int)(unit - (long long)kv_head * rts);
+  }
   __device__ __forceinline__ bool next(const TreeParams& p, TreePiece& pc) {
     while (s.at < s.end) {
-      bool bad;
-      const TreeReq r = load_req(p, s.b, bad);
-      const int tiles = num_tiles(max(1, r.L + r.T)), rts = row_tiles(p, r);
-      const long long cost = r.T == 0 ? 0 : (long long)rts * p.Hkv * tiles;
-      if (s.at >= s.b0 + cost) {
-        s.b0 += cost;
-        ++s.b;
-        continue;
-      }
-      const long long unit = (s.at - s.b0) / tiles, w0 = s.b0 + unit * tiles;
-      const int t0 = (int)(s.at - w0), t1 = (int)min((long long)tiles, s.end - w0);
-      s.at = w0 + t1;
-      pc.req = r;
+      pc.row0 = r.row0;
+      pc.T = r.T;
+      pc.L = r.L;
       pc.b = s.b;
-      pc.kv_head = (int)(unit / rts);
-      pc.r0 = (int)(unit - (long long)pc.kv_head * rts) * p.unit_rows;
+      pc.kv_head = kv_head;
+      pc.r0 = rt * p.unit_rows;
       pc.rows = (int)min((long long)p.unit_rows, (long long)r.T * p.g - pc.r0);
       pc.keys = p.mask ? r.L + r.T : r.L + group_div(p, pc.r0 + pc.rows - 1) + 1;
       const int nt = num_tiles(pc.keys);
-      pc.t0 = t0;
-      pc.tiles = min(nt, t1) - t0;
-      if (pc.tiles <= 0) continue;  // (keys that only the request's later rows see)
-      const long long c0 = w0 / s.share, c1 = (w0 + nt - 1) / s.share;
-      pc.slot = c0 == c1 ? -1 : 2 * (int)blockIdx.x + (c0 == blockIdx.x ? 1 : 0);
-      pc.blocks = c0 == blockIdx.x && c1 > c0 ? (int)(c1 - c0) + 1 : 0;
-      return true;
+      pc.t0 = (int)(s.at - w0);
+      pc.tiles = (int)min((long long)nt, s.end - w0) - pc.t0;
+      const long long first = s.share * blockIdx.x;  // of the share
+      const bool here = w0 >= first, cut = w0 + nt > s.end;
+      pc.slot = here && !cut ? -1 : 2 * (int)blockIdx.x + (here ? 1 : 0);
+      pc.blocks = here && cut ? (int)((w0 + nt - 1) / s.share) - (int)blockIdx.x + 1 : 0;
+      // on to the next unit
+      s.at = min(s.end, w0 + tiles);
+      w0 += tiles;
+      if (++rt == rts) {
+        rt = 0;
+        if (++kv_head == p.Hkv && s.at < s.end) {
+          kv_head = 0;
+          do {
+            ++s.b;
+            r = ahead;
+            ahead = load(p, s.b + 1);
+          } while (r.T == 0 && s.b < p.num_reqs);
+          take(p);
+        }
+      }
+      if (pc.tiles > 0) return true;  // (else keys that only the request's later rows see)
     }
     return false;
   }
 };
 
+// The block's pieces, walked by one warp and read by the others; the last has no tiles.
+template <int N>
+struct PieceRing {
+  TreePiece at[N];
+  uint64_t full[N], empty[N];
+  __device__ __forceinline__ void init(int readers) {
+    for (int i = 0; i < N; ++i) {
+      mbar_init(full + i, 1);
+      mbar_init(empty + i, readers);
+    }
+  }
+  // Piece i, by a whole warp; false when a wait ran out.
+  __device__ __forceinline__ bool put(int i, const TreePiece& pc, const volatile int* abort, uint64_t timeout) {
+    if (!wait_warp(empty + i % N, ((i / N) & 1) ^ 1, abort, timeout)) return false;
+    if ((threadIdx.x & 31) == 0) {
+      at[i % N] = pc;
+      mbar_arrive(full + i % N);
+    }
+    return true;
+  }
+  // ... read; without tiles when there is none or a wait ran out.
+  __device__ __forceinline__ bool get(int i, TreePiece& pc, const volatile int* abort, uint64_t timeout) {
+    pc.tiles = 0;
+    if (!wait_warp(full + i % N, (i / N) & 1, abort, timeout)) return false;
+    const int4* w = reinterpret_cast<const int4*>(at + i % N);
+    const int4 a = w[0], b = w[1], c = w[2];
+    pc = TreePiece{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, c.x, c.y, c.z, c.w};
+    return true;
+  }
+  // A reader is done with piece i (one of a warp).
+  __device__ __forceinline__ void done(int i) { mbar_arrive(empty + i % N); }
+};
+
 __device__ __forceinline__ void put_cut(const TreeParams& p, const TreePiece& pc, int blocks) {
-  p.cut[2 * blockIdx.x] = make_int4(pc.req.row0, pc.r0, pc.rows, pc.kv_head);
+  p.cut[2 * blockIdx.x] = make_int4(pc.row0, pc.r0, pc.rows, pc.kv_head);
   p.cut[2 * blockIdx.x + 1] = make_int4(blocks, 0, 0, 0);
 }
 
@@ -200,10 +264,83 @@ __device__ __forceinline__ int cache_row(const TreeParams& p, int b, int key) {
   return (page << p.log_page) + (key & ((1 << p.log_page) - 1));
 }
 
+// The KV tiles of a list of pieces as their loader goes through them: the lane's box of a tile is
+// whole pages, or 16 rows of a unit's end, and is looked up a tile ahead, so that the page
+// table's latency is not waited for.
+template <int N>
+struct TileLoader {
+  PieceRing<N>& ring;
+  TreePiece pc;
+  int i = -1, t = 0, row = 0;  // piece, its tile, cache row of the lane's box
+  bool ok = true;
+  __device__ __forceinline__ explicit TileLoader(PieceRing<N>& r) : ring(r) { pc.tiles = 0; }
+  __device__ __forceinline__ int key0() const { return (pc.t0 + t) * BN; }
+  __device__ __forceinline__ int live() const { return min(BN, pc.keys - key0()); }
+  __device__ __forceinline__ int log_box(const TreeParams& p) const {
+    return live() > BN - 16 ? min(7, p.log_page) : 4;
+  }
+  // The next tile; false when there is none (or a wait ran out: ok).
+  __device__ __forceinline__ bool next(const TreeParams& p, const volatile int* abort) {
+    if (++t >= pc.tiles) {
+      ok = ring.get(++i, pc, abort, p.timeout_ns);
+      if (pc.tiles == 0) return false;
+      t = 0;
+    }
+    const int at = (threadIdx.x & 31) << log_box(p);
+    row = at < live() ? cache_row(p, pc.b, key0() + at) : 0;
+    return true;
+  }
+};
+// Starts the copies of a tile: kChunks boxes of 64 columns across, by the lanes that hold the
+// rows (one lane that starts them all takes 2900 cycles for 8 pages, these 2200).
+template <int kChunks, int kLine>
+__device__ __forceinline__ void copy_tile(const CUtensorMap* whole, const CUtensorMap* tail, uint8_t* dst, uint64_t* bar,
+                                          int kv_head, int row, int live, int log, int whole_log) {
+  const int lane = threadIdx.x & 31, boxes = (live + (1 << log) - 1) >> log;
+  if (lane == 0) mbar_arrive_expect_tx(bar, (boxes << log) * kLine * kChunks);
+  __syncwarp();
+  if (lane < boxes) {
+    const CUtensorMap* tm = log == whole_log ? whole : tail;
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c)
+      tma_load_3d(dst + (c * BN + (lane << log)) * kLine, tm, bar, c * 64, kv_head, row);
+  }
+  __syncwarp();
+}
+// Ring place of K and V of a list's n-th KV tile, in the order of use: K0 V0 K1 V1 ..., or
+// (AHEAD: two streams take turns) K0 K1 V0 K2 V1 ..., where the place behind the last V but
+// one is left out.
+template <bool AHEAD>
+__device__ __forceinline__ int k_place(int n) { return !AHEAD ? 2 * n : n == 0 ? 0 : 2 * n - 1; }
+template <bool AHEAD>
+__device__ __forceinline__ int v_place(int n) { return !AHEAD ? 2 * n + 1 : 2 * n + 2; }
+// Waits for the copies in flight, of nk K and nv V tiles, after an abort: the last of each slot.
+template <bool AHEAD>
+__device__ __forceinline__ void drain_tiles(uint64_t* full, int stages, int nk, int nv, uint64_t timeout) {
+  for (int slot = 0; slot < stages; ++slot) {
+    int last = -1;
+    for (int n = max(0, nk - stages - 1); n < nk; ++n)
+      if (k_place<AHEAD>(n) % stages == slot) last = max(last, k_place<AHEAD>(n));
+    for (int n = max(0, nv - stages - 1); n < nv; ++n)
+      if (v_place<AHEAD>(n) % stages == slot) last = max(last, v_place<AHEAD>(n));
+    if (last >= 0) wait_one(full + slot, (last / stages) & 1, nullptr, timeout);
+  }
+}
+
 // Whether new row `node` of a request sees new key `n` (0 <= n < T).
-__device__ __forceinline__ bool sees(const TreeParams& p, const TreeReq& r, int node, int n) {
+__device__ __forceinline__ bool sees(const TreeParams& p, const TreePiece& pc, int node, int n) {
   if (!p.mask) return n <= node;
-  return ((uint32_t)__ldg(p.mask + (long long)(r.row0 + node) * p.words + (n >> 5)) >> (n & 31)) & 1u;
+  return ((uint32_t)__ldg(p.mask + (long long)(pc.row0 + node) * p.words + (n >> 5)) >> (n & 31)) & 1u;
+}
+
+// Brings the masks of a piece's rows to L1, by a whole warp (up to 8 KB).
+__device__ __forceinline__ void fetch_masks(const TreeParams& p, const TreePiece& pc) {
+  if (!p.mask) return;
+  const int n0 = group_div(p, pc.r0), n1 = group_div(p, pc.r0 + pc.rows - 1);
+  const char* at = reinterpret_cast<const char*>(p.mask + (long long)(pc.row0 + n0) * p.words);
+  const long long bytes = min(8192LL, (long long)(n1 - n0 + 1) * p.words * 4);
+  for (long long x = (threadIdx.x & 31) * 32; x < bytes; x += 32 * 32)
+    asm volatile("prefetch.global.L1 [%0];" ::"l"(at + x));
 }
 
 }  // namespace

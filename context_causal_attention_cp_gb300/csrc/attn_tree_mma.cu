@@ -23,6 +23,7 @@
 // would not keep them from the rows that do not see them.  A row that does see one becomes
 // NaN by its sum.
 #include <algorithm>
+#include <climits>
 #include <type_traits>
 
 #include "attn_tree.cuh"
@@ -32,6 +33,9 @@ namespace {
 
 constexpr int kKWarp = 8, kVWarp = 9, kMmaWarp = 10, kQWarp = 11, kConvertWarp = 12;
 constexpr int kConvertThreads = 128;
+
+constexpr int kPieces = 4;  // in the ring
+using Pieces = PieceRing<kPieces>;
 
 template <int D, bool QUANT, bool DUAL>
 struct MmaCfg {
@@ -54,8 +58,8 @@ struct MmaCfg {
   static constexpr int kMlOff = kLiftOff + (QUANT ? 4 * BM : 0);     // single: (m, l) of each stream's rows
   static constexpr int kEvOff = kMlOff + (DUAL ? 0 : 2 * BM * 8);    // and O's exponent
   static constexpr int kBadOff = kEvOff + (QUANT && !DUAL ? 2 * BM : 0);  // value rows that are not finite
-  static constexpr int kTilesOff = kBadOff + 2 * 2 * 16 + kStages * 16;  // KV tiles of pieces i mod 8
-  static constexpr int kBarOff = kTilesOff + 32;
+  static constexpr int kPiecesOff = kBadOff + 2 * 2 * 16 + (QUANT ? kStages * 16 : 0);
+  static constexpr int kBarOff = kPiecesOff + (int)sizeof(Pieces);
   static constexpr int kNumBars = 2 * kStages + 2 * kRawStages + 2 * 5 + 1;
   static constexpr int kWordOff = kBarOff + kNumBars * 8;
   static constexpr int kSumOff = (kWordOff + 64 + 7) & ~7;
@@ -68,30 +72,11 @@ struct MmaCfg {
 struct RawNote {
   int live;         // rows up to the unit's end
   int fresh;        // first row that is a new key
-  int ek, ev;       // of a K tile: its exponent, and V's
+  int ek;           // of a K tile: its exponent
+  int16_t ev;       // and V's
+  int16_t last;     // of a K tile: the block has no other behind it
 };
-
-// Ring place of K and V of the block's n-th KV tile, in the order of use.  (A single list's
-// place behind its last V is left out: 2n + 2 of the last n.)
-template <bool DUAL>
-__device__ __forceinline__ int k_place(int n) { return DUAL ? 2 * n : n == 0 ? 0 : 2 * n - 1; }
-template <bool DUAL>
-__device__ __forceinline__ int v_place(int n) { return DUAL ? 2 * n + 1 : 2 * n + 2; }
-
-// Steps through the KV tiles of a share.
-struct TileWalk {
-  TreeWalk w;
-  TreePiece pc;
-  int t = -1, piece = -1;  // tile of the piece, number of the piece
-  __device__ __forceinline__ bool next(const TreeParams& p) {
-    if (piece < 0 || ++t >= pc.tiles) {
-      if (!w.next(p, pc)) return false;
-      t = 0;
-      ++piece;
-    }
-    return true;
-  }
-};
+static_assert(sizeof(RawNote) == 16, "");
 
 // The MMAs and commits of ptx.cuh, by the lane with `lead` of a whole warp.
 __device__ __forceinline__ void mma_ss_lead(uint32_t lead, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
@@ -118,30 +103,44 @@ __device__ __forceinline__ void mma_commit_lead(uint32_t lead, uint64_t* bar) {
       : "memory");
 }
 
-// The bits of the keys that new row `node` sees of the 32 from key0 on.
-__device__ __forceinline__ uint32_t seen_bits(const TreeParams& p, const TreeReq& r, int node, int key0) {
-  const int n = key0 - r.L;  // new key of the first bit
-  if (n >= r.T) return 0u;
-  if (n <= -32) return ~0u;
-  uint32_t bits;
-  int count;  // bits that are keys
-  if (p.mask) {
-    const int32_t* row = p.mask + (long long)(r.row0 + node) * p.words;
-    if (n >= 0) {
-      const int w = n >> 5;
-      const uint32_t lo = (uint32_t)__ldg(row + w), hi = w + 1 < p.words ? (uint32_t)__ldg(row + w + 1) : 0u;
-      bits = __funnelshift_r(lo, hi, n & 31);
-    } else {
-      bits = ((uint32_t)__ldg(row) << -n) | ((1u << -n) - 1u);
+// The words of a row's mask that hold the bits of a tile's 128 keys, the first of which is new
+// key n (negative: cached keys before it).  Fetched before they are needed.
+struct MaskWords {
+  uint32_t w[5];
+  __device__ __forceinline__ void load(const TreeParams& p, const TreePiece& pc, int node, int n) {
+    const int first = n >> 5;  // (rounds down)
+#pragma unroll
+    for (int x = 0; x < 5; ++x) {
+      const int at = first + x;
+      w[x] = !p.mask ? ~0u
+             : at >= 0 && at < p.words ? (uint32_t)__ldg(p.mask + (long long)(pc.row0 + node) * p.words + at)
+                                       : 0u;
     }
-    count = r.T - n;
-  } else {
-    bits = ~0u;
-    count = node + 1 - n;
   }
-  return count >= 32 ? bits : count <= 0 ? 0u : bits & ((1u << count) - 1u);
-}
+  // The keys of the tile that the row sees; limit: the new keys that it may see.
+  __device__ __forceinline__ void seen(int n, int limit, uint32_t (&vis)[4]) const {
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const int m = n + 32 * x;  // new key of the word's first bit
+      uint32_t bits = __funnelshift_r(w[x], w[x + 1], n & 31);
+      if (m < 0) bits |= m <= -32 ? ~0u : (1u << -m) - 1u;  // cached keys
+      const int count = limit - m;
+      vis[x] = count >= 32 ? bits : count <= 0 ? 0u : bits & ((1u << count) - 1u);
+    }
+  }
+};
 
+// A barrier of 256 threads; true when all of them say so.
+__device__ __forceinline__ bool bar_all(int id, bool all) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %2, 0;\n\t"
+      "bar.red.and.pred q, %1, 256, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"((uint32_t)all)
+      : "memory");
+  return r != 0;
+}
 __device__ __forceinline__ void bar_named(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
@@ -217,18 +216,34 @@ __device__ __forceinline__ void softmax_row(uint32_t s_addr, uint32_t o_addr, bo
   m_use = m_new_use;
 }
 
-// 8 columns from column 8 c on of row r of a piece: to the output, or to its partial.
-__device__ __forceinline__ void put8(const TreeParams& p, const TreePiece& pc, int D, int r, int c, long long at,
-                                     const float (&f)[8]) {
+// 16 columns from column 16 c on of row r of a piece: to the output, or to its partial.
+__device__ __forceinline__ void put16(const TreeParams& p, const TreePiece& pc, int D, int r, int c, long long at,
+                                      const float* f) {
   if (pc.slot >= 0) {
-    store8(p.ws_o + (long long)pc.slot * p.unit_rows * D + partial_at(c, r, p.unit_rows), f);
-  } else if (p.o_f32) {  // (16-byte aligned)
-    float4* o = reinterpret_cast<float4*>(static_cast<float*>(p.o) + at * D + c * 8);
-    o[0] = make_float4(f[0], f[1], f[2], f[3]);
-    o[1] = make_float4(f[4], f[5], f[6], f[7]);
+    float* dst = p.ws_o + (long long)pc.slot * p.unit_rows * D;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float x[8] = {f[8 * h], f[8 * h + 1], f[8 * h + 2], f[8 * h + 3],
+                          f[8 * h + 4], f[8 * h + 5], f[8 * h + 6], f[8 * h + 7]};
+      store8(dst + partial_at(2 * c + h, r, p.unit_rows), x);
+    }
+  } else if (p.o_f32) {
+    float4* o = reinterpret_cast<float4*>(static_cast<float*>(p.o) + at * D + c * 16);
+#pragma unroll
+    for (int x = 0; x < 4; ++x) o[x] = make_float4(f[4 * x], f[4 * x + 1], f[4 * x + 2], f[4 * x + 3]);
   } else {
-    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.o) + at * D + c * 8) =
-        make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+    uint32_t w[8];
+#pragma unroll
+    for (int x = 0; x < 8; ++x) w[x] = pack_bf16x2(f[2 * x], f[2 * x + 1]);
+    __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.o) + at * D + c * 16;
+    if (p.o_32)  // whole sectors
+      asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(o), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                   "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                   : "memory");
+    else {
+      reinterpret_cast<uint4*>(o)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+      reinterpret_cast<uint4*>(o)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
   }
 }
 
@@ -256,7 +271,7 @@ attn_tree_mma_kernel(const __grid_constant__ TreeMaps maps, const TreeParams p) 
   int8_t* o_exp = reinterpret_cast<int8_t*>(smem + C::kEvOff);
   uint32_t* bad_scan = reinterpret_cast<uint32_t*>(smem + C::kBadOff);  // [2 streams][2][4]
   uint32_t* bad_slot = bad_scan + 16;                                   // [kStages][4] (e4m3)
-  volatile int* piece_tiles = reinterpret_cast<volatile int*>(smem + C::kTilesOff);
+  Pieces& pieces = *reinterpret_cast<Pieces*>(smem + C::kPiecesOff);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kWordOff);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* issued = reinterpret_cast<volatile int*>(tmem_slot + 2);  // K and V tiles, for the abort drain
@@ -286,13 +301,14 @@ attn_tree_mma_kernel(const __grid_constant__ TreeMaps maps, const TreeParams p) 
       mbar_init(raw_empty + i, kConvertThreads);
     }
     for (int s = 0; s < 2; ++s) {
-      mbar_init(q_full + s, 32);
+      mbar_init(q_full + s, 1);
       mbar_init(q_empty + s, 1);
       mbar_init(s_full + s, 1);
       mbar_init(p_full + s, 128);
       mbar_init(o_full + s, 1);
     }
     mbar_init(bar_drain, 1);
+    pieces.init(8);  // the softmax warps, whose end of a piece is the last
     *abort_flag = 0;
     issued[0] = issued[1] = 0;
     fence_barrier_init();
@@ -321,42 +337,19 @@ attn_tree_mma_kernel(const __grid_constant__ TreeMaps maps, const TreeParams p) 
       uint64_t* const emptyb = QUANT ? raw_empty : empty;
       uint8_t* const ring = smem + (QUANT ? C::kRawOff : C::kRingOff);
       const int whole_log = min(7, p.log_page);
-      TileWalk w{{start}};
-      int n = 0, cut = 0;
+      TileLoader<kPieces> w(pieces);
+      int n = 0;
       int ev0 = 0, ev1 = 0;  // (e4m3) exponent of each stream's V rows
       bool ok = true;
-      // The lane's box of the tile: whole pages, or 16 rows of the unit's end; looked up a tile
-      // ahead, so that the page table's latency is not waited for.
-      auto key_of = [&]() { return (w.pc.t0 + w.t) * BN; };
-      auto log_of = [&]() { return min(BN, w.pc.keys - key_of()) > BN - 16 ? whole_log : 4; };
-      bool more = w.next(p);
-      int row_next = 0;
-      auto lookup = [&]() {
-        const int live = min(BN, w.pc.keys - key_of()), log = log_of();
-        return (lane << log) < live ? cache_row(p, w.pc.b, key_of() + (lane << log)) : 0;
-      };
-      if (more) row_next = lookup();
-      while (more && ok) {
-        const int live = min(BN, w.pc.keys - key_of()), log = log_of(), boxes = (live + (1 << log) - 1) >> log;
-        const int mine = row_next, kvh = w.pc.kv_head, fresh = w.pc.req.L - key_of();
+      for (bool more = w.next(p, abort_flag); more;) {
+        const int live = w.live(), log = w.log_box(p), mine = w.row, kvh = w.pc.kv_head, fresh = w.pc.L - w.key0();
         const bool first = w.t <= (DUAL ? 0 : 1);  // of its piece and stream
-        if (is_v && w.t == 0 && w.pc.blocks) {
-          cut = w.pc.blocks;
-          if (lane == 0) put_cut(p, w.pc, cut);
-        }
-        const int place = is_v ? v_place<DUAL>(n) : k_place<DUAL>(n), slot = place % kSt;
+        const int place = is_v ? v_place<!DUAL>(n) : k_place<!DUAL>(n), slot = place % kSt;
         ok = wait_warp(emptyb + slot, ((place / kSt) & 1) ^ 1, abort_flag, p.timeout_ns);
         if (!ok) break;
-        uint8_t* dst = ring + slot * kBytes;
-        if (lane == 0) mbar_arrive_expect_tx(fullb + slot, (boxes << log) * kLine * kChunks);
-        __syncwarp();
-        if (lane < boxes) {
-          const CUtensorMap* tm = log == whole_log ? (is_v ? &maps.v : &maps.k) : (is_v ? &maps.v_tail : &maps.k_tail);
-#pragma unroll
-          for (int c = 0; c < kChunks; ++c)
-            tma_load_3d(dst + (c * BN + (lane << log)) * kLine, tm, fullb + slot, c * 64, kvh, mine);
-        }
-        __syncwarp();
+        copy_tile<kChunks, kLine>(is_v ? &maps.v : &maps.k, is_v ? &maps.v_tail : &maps.k_tail, ring + slot * kBytes,
+                                  fullb + slot, kvh, mine, live, log, whole_log);
+        more = w.next(p, abort_flag);
         if constexpr (QUANT) {
           // the rows' scales as f16 factors relative to the tile's largest (K), or to the
           // largest that the stream has met in the piece (V)
@@ -383,16 +376,14 @@ attn_tree_mma_kernel(const __grid_constant__ TreeMaps maps, const TreeParams p) 
           const float inv = exp2_int(-e);
 #pragma unroll
           for (int x = 0; x < 4; ++x) raw_mul[slot * BN + x * 32 + lane] = (uint16_t)pack_f16x2(sc[x] * inv, 0.f);
-          if (lane == 0) raw_note[slot] = RawNote{live, fresh, e, ev};
+          if (lane == 0) raw_note[slot] = RawNote{live, fresh, e, (int16_t)ev, (int16_t)!more};
           __syncwarp();
           if (lane == 0) mbar_arrive(fullb + slot);
         }
         ++n;
-        more = w.next(p);
-        if (more) row_next = lookup();
       }
+      ok = ok && w.ok;
       if (lane == 0) {
-        if (is_v && !cut) p.cut[2 * blockIdx.x + 1] = make_int4(0, 0, 0, 0);
         issued[is_v ? 1 : 0] = n;
         if (!ok) {
           set_status(p.status, CPATTN_ERR_TIMEOUT);
@@ -441,6 +432,8 @@ attn_tree_mma_kernel(const __grid_constant__ TreeMaps maps, const TreeParams p) 
           phase ^= 1;
         }
       };
+      // (the queries of a piece come after its place in the ring, which lasts until its end)
+      auto tiles_of = [&](int i) { return __shfl_sync(0xffffffffu, pieces.at[i % kPieces].tiles, 0); };
       // The next tile's queries and K; false when there is none, or a wait ran out.
       auto next_q = [&]() {
         head_q = left_q == 0;
@@ -449,7 +442,7 @@ attn_tree_mma_kernel(const __grid_constant__ TreeMaps maps, const TreeParams p) 
           const int buf = DUAL ? 0 : piece_q & 1;
           ok = wait(q_full + buf, (DUAL ? piece_q : piece_q >> 1) & 1);
           if (!ok) return false;
-          left_q = __shfl_sync(0xffffffffu, piece_tiles[piece_q & 7], 0);
+          left_q = tiles_of(piece_q);
           if (left_q == 0) return false;
           if (DUAL) ok = wait(q_full + 1, piece_q & 1);
         }
@@ -461,7 +454,7 @@ attn_tree_mma_kernel(const __grid_constant__ TreeMaps maps, const TreeParams p) 
       auto next_v = [&]() {
         if (left_v == 0) {
           ++piece_v;
-          left_v = __shfl_sync(0xffffffffu, piece_tiles[piece_v & 7], 0);
+          left_v = tiles_of(piece_v);
           head_v[0] = head_v[1] = true;
         }
         --left_v;
@@ -561,25 +554,60 @@ attn_tree_mma_kernel(const __grid_constant__ TreeMaps maps, const TreeParams p) 
       // D / 8 lanes to a row.  Dual: tile s of a piece in buffer s, when the piece before has
       // no product left; single: the pieces' tiles take turns, one ahead.
       constexpr int kLanes = D / 8, kRows = 32 / kLanes;
-      TreeWalk w{start};
-      TreePiece pc;
-      bool ok = true;
+      // It also walks the share, two pieces ahead of the queries.
+      TreeWalk w(p, start);
+      TreePiece pc, ahead[2];
+      bool ok = true, cut = false;
       const int c = lane % kLanes;
+      int last[2] = {-1, -1};  // use of each buffer, where a box was its last
+      auto walk = [&](int i) {  // piece i
+        TreePiece x;
+        if (!w.next(p, x)) x.tiles = x.rows = x.blocks = 0;
+        if (x.blocks) {
+          cut = true;
+          if (lane == 0) put_cut(p, x, x.blocks);
+        }
+        ok = ok && pieces.put(i, x, abort_flag, p.timeout_ns);
+        return x;
+      };
+      ahead[0] = walk(0);
+      if (ahead[0].tiles) ahead[1] = walk(1);
       bool more = true;
       for (int i = 0; ok && more; ++i) {
-        more = w.next(p, pc);
-        if (!more) pc.rows = 0;
+        pc = ahead[0];
+        more = pc.tiles > 0;
+        if (more) {
+          fetch_masks(p, pc);
+          ahead[0] = ahead[1];
+          if (ahead[0].tiles) ahead[1] = walk(i + 2);
+        }
         for (int s = 0; s < (DUAL ? 2 : 1) && ok; ++s) {
           const int buf = DUAL ? s : i & 1, use = DUAL ? i : i >> 1;
           ok = wait_warp(q_empty + buf, (use & 1) ^ 1, abort_flag, p.timeout_ns);
           if (!ok) break;
-          if (lane == 0 && s == 0) piece_tiles[i & 7] = more ? pc.tiles : 0;
-          const uint32_t tile = q_base + buf * C::kQTile + (c >> 3) * (BM * 128);
           const int rows = min(BM, pc.rows - s * BM);
+          if (!QUANT && p.q_boxes) {  // a box holds all the heads of the tile's rows, packed as they are
+            if (lane == 0 && !p.withhold_q) {
+              if (rows > 0) {
+                const int row = pc.row0 + group_div(p, pc.r0 + s * BM);
+                mbar_arrive_expect_tx(q_full + buf, C::kQTile);
+#pragma unroll
+                for (int x = 0; x < D / 64; ++x)
+                  tma_load_3d(smem + buf * C::kQTile + x * (BM * 128), &maps.q, q_full + buf, x * 64, pc.kv_head * p.g,
+                              row);
+                last[buf] = use;
+              } else {
+                mbar_arrive(q_full + buf);
+                last[buf] = -1;  // (the box before has been used)
+              }
+            }
+            continue;
+          }
+          const uint32_t tile = q_base + buf * C::kQTile + (c >> 3) * (BM * 128);
 #pragma unroll 4
           for (int r = lane / kLanes; r < rows; r += kRows) {
             const int packed = pc.r0 + s * BM + r, node = group_div(p, packed);
-            const __nv_bfloat16* src = p.q + (long long)(pc.req.row0 + node) * p.q_row +
+            const __nv_bfloat16* src = p.q + (long long)(pc.row0 + node) * p.q_row +
                                        (long long)(pc.kv_head * p.g + packed - node * p.g) * p.q_head + c * 8;
             const uint32_t at = tile + r * 128 + (((c & 7) ^ (r & 7)) << 4);
             if constexpr (!QUANT) {
@@ -607,12 +635,19 @@ attn_tree_mma_kernel(const __grid_constant__ TreeMaps maps, const TreeParams p) 
           }
           if constexpr (!QUANT) asm volatile("cp.async.wait_all;" ::: "memory");
           fence_async_shared();
-          if (!p.withhold_q) mbar_arrive(q_full + buf);
+          __syncwarp();
+          if (lane == 0 && !p.withhold_q) mbar_arrive(q_full + buf);
         }
       }
-      if (!ok && lane == 0) {
-        set_status(p.status, CPATTN_ERR_TIMEOUT);
-        *abort_flag = 1;
+      if (lane == 0) {
+        if (!cut) p.cut[2 * blockIdx.x + 1] = make_int4(0, 0, 0, 0);
+        if (!ok) {
+          set_status(p.status, CPATTN_ERR_TIMEOUT);
+          *abort_flag = 1;
+        }
+        // no copy in flight when the shared memory goes
+        for (int buf = 0; buf < 2; ++buf)
+          if (last[buf] >= 0) wait_one(q_full + buf, last[buf] & 1, nullptr, p.timeout_ns);
       }
     }
     if constexpr (QUANT) if (warp >= kConvertWarp) {
@@ -620,12 +655,6 @@ attn_tree_mma_kernel(const __grid_constant__ TreeMaps maps, const TreeParams p) 
       // Warp w has rows 32w .. 32w+31 of every tile; of a row, lane l has 8 codes of each 64.
       const int w = warp - kConvertWarp;
       const int rl = lane >> 3, cl = lane & 7;  // row of four, 8-code chunk
-      int tiles = 0;
-      {
-        TreeWalk walk{start};
-        TreePiece pc;
-        while (walk.next(p, pc)) tiles += pc.tiles;
-      }
       const uint32_t swz[2] = {(uint32_t)((cl ^ rl) << 4), (uint32_t)((cl ^ (rl + 4)) << 4)};
       constexpr int kBatch = 4, kHalves = D / 64;
       uint32_t from[2][kHalves];
@@ -635,8 +664,13 @@ attn_tree_mma_kernel(const __grid_constant__ TreeMaps maps, const TreeParams p) 
         for (int h = 0; h < kHalves; ++h)
           from[x][h] = code_at<D>(w * 32 + rl + 4 * x, h * 4 + (cl >> 1)) + (cl & 1) * 8;
       bool ok = true;
-      const int places = tiles == 0 ? 0 : v_place<DUAL>(tiles - 1) + 1;
-      for (int place = 0; place < places; ++place) {
+      int tiles = INT_MAX;  // known when the last K tile has come
+      {
+        TreePiece pc;
+        ok = pieces.get(0, pc, abort_flag, p.timeout_ns);
+        if (pc.tiles == 0) tiles = 0;
+      }
+      for (int place = 0; ok && (tiles == INT_MAX || (tiles > 0 && place <= v_place<!DUAL>(tiles - 1))); ++place) {
         bool is_v;
         int n;
         if (DUAL) {
@@ -656,6 +690,7 @@ attn_tree_mma_kernel(const __grid_constant__ TreeMaps maps, const TreeParams p) 
         // rows of this warp that become zeros
         uint32_t dead = note.live >= w * 32 + 32 ? 0u : note.live <= w * 32 ? ~0u : ~0u << (note.live - w * 32);
         if (!is_v) {
+          if (note.last) tiles = n + 1;
           if (w == 0 && lane == 0) tile_exp[n & 7] = make_int2(note.ek, note.ev);
         } else if (note.fresh < BN) {  // new keys: a NaN's row
           bool bad = false;
@@ -721,13 +756,14 @@ attn_tree_mma_kernel(const __grid_constant__ TreeMaps maps, const TreeParams p) 
     const int r = DUAL ? s * BM + trow : trow;  // within the unit
     const uint32_t lanes = tmem_base + ((uint32_t)(wq * 32) << 16);
     const uint32_t s_addr = lanes + s * BN, o_addr = lanes + 2 * BN + s * D;
-    TreeWalk w{start};
     TreePiece pc;
     bool ok = true, pending = false;  // pending: the other stream may still read this one's O
     int n0 = 0;                       // KV tiles before the piece
     int tails = 0;                    // of the stream, with new keys
     int had[2] = {0, 0};              // pieces in which a stream had tiles
-    for (int i = 0; w.next(p, pc); ++i) {
+    for (int i = 0;; ++i) {
+      ok = ok && pieces.get(i, pc, abort_flag, p.timeout_ns);
+      if (!bar_all(6, ok && pc.tiles > 0)) break;  // (all eight warps go on, or none)
       const bool warp_live = (r & ~31) < pc.rows;
       const int node = r < pc.rows ? group_div(p, pc.r0 + r) : 0;
       float m_run = -INFINITY, l_run = 0.f, m_use = 0.f, factor = p.scale_log2;
@@ -735,6 +771,10 @@ attn_tree_mma_kernel(const __grid_constant__ TreeMaps maps, const TreeParams p) 
       bool first = true;
       for (int t = DUAL ? 0 : (n0 ^ s) & 1; t < pc.tiles; t += DUAL ? 1 : 2) {
         const int n = n0 + t, key0 = (pc.t0 + t) * BN;
+        // tiles with new keys, or keys behind the last
+        const bool tail = key0 + BN > pc.L;
+        MaskWords words;
+        if (tail && warp_live) words.load(p, pc, node, key0 - pc.L);
         ok = ok && wait_warp(s_full + s, (DUAL ? n : n >> 1) & 1, abort_flag, p.timeout_ns);
         tc_fence_after();
         float sl2 = factor, o_scale = 1.f;
@@ -748,25 +788,20 @@ attn_tree_mma_kernel(const __grid_constant__ TreeMaps maps, const TreeParams p) 
           if (!first && ev_now != ev) o_scale = exp2_int(max(ev - ev_now, -126));
           ev = ev_now;
         }
-        // tiles with new keys, or keys behind the last
         uint32_t vis[4] = {~0u, ~0u, ~0u, ~0u};
-        const bool tail = key0 + BN > pc.req.L;
         float poison = 0.f;
         if (tail) {
-          const int slot = v_place<DUAL>(n) % NS;
-          if (warp_live) {
-#pragma unroll
-            for (int x = 0; x < 4; ++x) vis[x] = r < pc.rows ? seen_bits(p, pc.req, node, key0 + 32 * x) : 0u;
-          }
-          ok = ok && wait_warp(full + slot, (v_place<DUAL>(n) / NS) & 1, abort_flag, p.timeout_ns);
-          const uint32_t* words;
+          const int slot = v_place<!DUAL>(n) % NS;
+          if (warp_live) words.seen(key0 - pc.L, p.mask ? pc.T : node + 1, vis);
+          ok = ok && wait_warp(full + slot, (v_place<!DUAL>(n) / NS) & 1, abort_flag, p.timeout_ns);
+          const uint32_t* bad_words;
           if constexpr (!QUANT) {
             // value row trow of the tile: one of no key, or one that is not finite
             uint8_t* const line = smem + C::kRingOff + slot * C::kTile + trow * 128;
             auto chunk_at = [&](int c) { return (c >> 3) * (BN * 128) + ((c ^ trow) & 7) * 16; };
             const int key = key0 + trow;
             bool bad = false;
-            if (key >= pc.req.L && key < pc.keys) {
+            if (key >= pc.L && key < pc.keys) {
 #pragma unroll
               for (int c = 0; c < D / 8; ++c) {
                 const uint4 v = *reinterpret_cast<const uint4*>(line + chunk_at(c));
@@ -777,7 +812,7 @@ attn_tree_mma_kernel(const __grid_constant__ TreeMaps maps, const TreeParams p) 
             uint32_t* const mine = bad_scan + (s * 2 + (tails & 1)) * 4;
             const uint32_t word = __ballot_sync(0xffffffffu, bad);
             if (lane == 0) mine[wq] = word;
-            words = mine;
+            bad_words = mine;
             ++tails;
             if (DUAL) bar_named(2, 256);  // both streams have looked at the tile
             else bar_named(2 + s, 128);
@@ -788,11 +823,11 @@ attn_tree_mma_kernel(const __grid_constant__ TreeMaps maps, const TreeParams p) 
             }
             fence_async_shared();
           } else {
-            words = bad_slot + slot * 4;
+            bad_words = bad_slot + slot * 4;
           }
           uint32_t hit = 0;
 #pragma unroll
-          for (int x = 0; x < 4; ++x) hit |= vis[x] & words[x];
+          for (int x = 0; x < 4; ++x) hit |= vis[x] & bad_words[x];
           if (r < pc.rows && hit) poison = __uint_as_float(0x7FC00000u);
         }
         if (warp_live && ok)
@@ -808,7 +843,7 @@ attn_tree_mma_kernel(const __grid_constant__ TreeMaps maps, const TreeParams p) 
       }
       // ---- the piece's end ----
       const int packed = pc.r0 + r;
-      const long long at = (long long)(pc.req.row0 + node) * p.Hq + pc.kv_head * p.g + packed - node * p.g;
+      const long long at = (long long)(pc.row0 + node) * p.Hq + pc.kv_head * p.g + packed - node * p.g;
       if constexpr (DUAL) {
         ok = ok && wait_warp(o_full + s, i & 1, abort_flag, p.timeout_ns);
         tc_fence_after();
@@ -816,17 +851,18 @@ attn_tree_mma_kernel(const __grid_constant__ TreeMaps maps, const TreeParams p) 
           const bool none = l_run == 0.f;  // (a NaN sum is not none)
           const float inv = none ? 0.f : exp2_int(ev) / l_run;
 #pragma unroll
-          for (int q = 0; q < D / 32; ++q) {
-            uint32_t v[32];
-            tmem_ld32(o_addr + q * 32, v);
+          for (int q = 0; q < D / 64; ++q) {
+            uint32_t v[64];
+            tmem_ld32p(o_addr + q * 64, v);
+            tmem_ld32p(o_addr + q * 64 + 32, v + 32);
             tmem_wait_ld();
             if (r < pc.rows) {
 #pragma unroll
-              for (int c = 0; c < 32; c += 8) {
-                float f[8];
+              for (int c = 0; c < 64; c += 16) {
+                float f[16];
 #pragma unroll
-                for (int x = 0; x < 8; ++x) f[x] = none ? 0.f : __uint_as_float(v[c + x]) * inv;
-                put8(p, pc, D, r, q * 4 + c / 8, at, f);
+                for (int x = 0; x < 16; ++x) f[x] = none ? 0.f : __uint_as_float(v[c + x]) * inv;
+                put16(p, pc, D, r, q * 4 + c / 16, at, f);
               }
             }
           }
@@ -870,14 +906,14 @@ attn_tree_mma_kernel(const __grid_constant__ TreeMaps maps, const TreeParams p) 
             tmem_wait_ld();
             if (r < pc.rows) {
 #pragma unroll
-              for (int c = 0; c < 32; c += 8) {
-                float f[8];
+              for (int c = 0; c < 32; c += 16) {
+                float f[16];
 #pragma unroll
-                for (int x = 0; x < 8; ++x) {
+                for (int x = 0; x < 16; ++x) {
                   const float y = ca == 0.f ? 0.f : __uint_as_float(u[c + x]) * ca;
                   f[x] = cb == 0.f ? y : fmaf(__uint_as_float(v[c + x]), cb, y);
                 }
-                put8(p, pc, D, r, s * (D / 16) + q * 4 + c / 8, at, f);
+                put16(p, pc, D, r, s * (D / 32) + q * 2 + c / 16, at, f);
               }
             }
           }
@@ -891,6 +927,8 @@ attn_tree_mma_kernel(const __grid_constant__ TreeMaps maps, const TreeParams p) 
         pending = true;
       }
       n0 += pc.tiles;
+      __syncwarp();
+      if (lane == 0) pieces.done(i);
     }
     if (!ok && lane == 0) {
       set_status(p.status, CPATTN_ERR_TIMEOUT);
@@ -902,19 +940,9 @@ attn_tree_mma_kernel(const __grid_constant__ TreeMaps maps, const TreeParams p) 
   tc_fence_before();
   __syncthreads();
   if (warp == kKWarp) {
-    if (lane == 0 && *abort_flag) {
-      // let the copies in flight land before the shared memory goes: the last of each slot
-      constexpr int kSt = QUANT ? C::kRawStages : NS;
-      const int nk = issued[0], nv = issued[1];
-      for (int slot = 0; slot < kSt; ++slot) {
-        int last = -1;
-        for (int n = max(0, nk - kSt - 1); n < nk; ++n)
-          if (k_place<DUAL>(n) % kSt == slot) last = max(last, k_place<DUAL>(n));
-        for (int n = max(0, nv - kSt - 1); n < nv; ++n)
-          if (v_place<DUAL>(n) % kSt == slot) last = max(last, v_place<DUAL>(n));
-        if (last >= 0) wait_one((QUANT ? raw_full : full) + slot, (last / kSt) & 1, nullptr, p.timeout_ns);
-      }
-    }
+    // (after an abort) let the copies in flight land before the shared memory goes
+    if (lane == 0 && *abort_flag)
+      drain_tiles<!DUAL>(QUANT ? raw_full : full, QUANT ? C::kRawStages : NS, issued[0], issued[1], p.timeout_ns);
     __syncwarp();
     tc_fence_after();
     tmem_dealloc(tmem_base, C::kTmemCols);

@@ -32,6 +32,8 @@ constexpr int kThreads = 384;  // a third warpgroup: the loading warp and three 
 constexpr int kRegsLaunch = 168, kRegsWork = 208, kRegsOther = 88;
 static_assert(kRegsWork * 256 + kRegsOther * 128 <= kRegsLaunch * kThreads, "register split exceeds the launch's");
 constexpr int kMaxStages = 12;
+constexpr int kPieces = 4;  // in the ring
+using Pieces = PieceRing<kPieces>;
 
 template <int D, bool QUANT, int NQ, int QW>
 struct TreeCfg {
@@ -42,14 +44,15 @@ struct TreeCfg {
   static constexpr int kQ = kRows * D * 2;            // two of them
   static constexpr int kJoin = kWarps * 8 * NQ * D * 4;
   static constexpr int kMl = kWarps * 8 * NQ * 8;
-  static constexpr int kFixed = 2 * kQ + kJoin + kMl + (2 * kMaxStages + 4) * 8 + 64 + 256 + 1024;
+  static constexpr int kFixed = 2 * kQ + kJoin + kMl + (int)sizeof(Pieces) + (2 * kMaxStages + 4) * 8 + 64 + 256 + 1024;
   static constexpr int kFit = (232448 - kFixed) / (kTile + kScales);
   static constexpr int kStages = kFit < kMaxStages ? kFit : kMaxStages;
   static constexpr int kScaleOff = kStages * kTile;
   static constexpr int kQOff = kScaleOff + kStages * kScales;
   static constexpr int kJoinOff = kQOff + 2 * kQ;
   static constexpr int kMlOff = kJoinOff + kJoin;  // (m, l) of each warp's rows
-  static constexpr int kBarOff = kMlOff + kMl;
+  static constexpr int kPiecesOff = kMlOff + kMl;
+  static constexpr int kBarOff = kPiecesOff + (int)sizeof(Pieces);
   static constexpr int kWordOff = kBarOff + (2 * kStages + 4) * 8;
   static constexpr int kSumOff = kWordOff + 64;  // of tree_start
   static constexpr int kSmemBytes = kSumOff + 256 + 1024;  // + align slack
@@ -283,17 +286,17 @@ __device__ __forceinline__ bool Warp<D, QUANT, NQ, QW>::piece(const TreeParams& 
       uint32_t pb[NQ][2];
       if (work) {
         if (pc.keys - at < 16) alive >>= 16 - (pc.keys - at);
-        if (at + 16 > pc.req.L) {  // new keys among them: who sees which
-          const uint32_t bad = bad_rows(v_slot, key) & alive & ~((1u << min(16, max(0, pc.req.L - at))) - 1u);
+        if (at + 16 > pc.L) {  // new keys among them: who sees which
+          const uint32_t bad = bad_rows(v_slot, key) & alive & ~((1u << min(16, max(0, pc.L - at))) - 1u);
           alive &= ~bad;
 #pragma unroll
           for (int n = 0; n < NQ; ++n)
 #pragma unroll
             for (int y = 0; y < 4; ++y) {
-              const int kk = g + (y >> 1) * 8, node = at + kk - pc.req.L;
+              const int kk = g + (y >> 1) * 8, node = at + kk - pc.L;
               const int r = row0 + 8 * n + 2 * c + (y & 1);
               if (node < 0 || r >= pc.rows) continue;
-              if (node >= pc.req.T || !sees(p, pc.req, group_div(p, pc.r0 + r), node)) s[n][y] = -INFINITY;
+              if (node >= pc.T || !sees(p, pc, group_div(p, pc.r0 + r), node)) s[n][y] = -INFINITY;
               else if ((bad >> kk) & 1u) s[n][y] = __uint_as_float(0x7FC00000u);  // the row becomes NaN
             }
         }
@@ -432,7 +435,6 @@ __device__ __forceinline__ bool Warp<D, QUANT, NQ, QW>::piece(const TreeParams& 
   const float down = exp2_int(ev);
   float* const join = reinterpret_cast<float*>(mem + C::kJoinOff);
   float2* const ml = reinterpret_cast<float2*>(mem + C::kMlOff);
-  bar_warps(false);  // the buffer's last readers
 #pragma unroll
   for (int n = 0; n < NQ; ++n)
 #pragma unroll
@@ -493,7 +495,7 @@ __device__ __forceinline__ bool Warp<D, QUANT, NQ, QW>::piece(const TreeParams& 
       if (d == 0) p.ws_l[slot + r] = lse2;
     } else {
       const int packed = pc.r0 + r, node = group_div(p, packed);
-      const long long at = (long long)(pc.req.row0 + node) * p.Hq + pc.kv_head * p.g + packed - node * p.g;
+      const long long at = (long long)(pc.row0 + node) * p.Hq + pc.kv_head * p.g + packed - node * p.g;
       if (p.o_f32)
         *reinterpret_cast<float4*>(static_cast<float*>(p.o) + at * D + d) = out;
       else
@@ -517,7 +519,8 @@ attn_tree_small_kernel(const __grid_constant__ TreeMaps maps, const TreeParams p
   uint64_t* q_full = empty + NS;
   uint64_t* q_empty = q_full + 2;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kWordOff);
-  volatile int* issued_loads = abort_flag + 1;
+  volatile int* issued = abort_flag + 1;  // K and V tiles, for the abort drain
+  Pieces& pieces = *reinterpret_cast<Pieces*>(smem + C::kPiecesOff);
   long long* found = reinterpret_cast<long long*>(smem + C::kWordOff + 16);
   long long* sums = reinterpret_cast<long long*>(smem + C::kSumOff);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -535,35 +538,84 @@ attn_tree_small_kernel(const __grid_constant__ TreeMaps maps, const TreeParams p
       mbar_init(q_full + i, 32);  // each lane's copies
       mbar_init(q_empty + i, kWarps);
     }
+    pieces.init(kWarps);
     *abort_flag = 0;
-    *issued_loads = 0;
+    issued[0] = issued[1] = 0;
     fence_barrier_init();
   }
-  TreeWalk walk{tree_start(p, sums, found)};  // (its barriers publish those above)
+  const TreeStart start = tree_start(p, sums, found);  // (its barriers publish those above)
   TreePiece pc;
   auto arrive_copies = [&](uint64_t* bar) {  // when this lane's copies so far have landed
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
   };
   if (warp >= kWarps) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
-    if (warp == kWarps) {
+    if (warp == kWarps || warp == kWarps + 1) {  // K, V
       constexpr int kChunks = QUANT ? 1 : D / 64;     // boxes across a row
       constexpr int kLine = C::kTile / BN / kChunks;  // bytes of a box row
-      const int whole_log = min(7, p.log_page);       // rows of a whole box
-      int seq = 0, cut = 0;
+      const bool is_v = warp > kWarps;
+      const int whole_log = min(7, p.log_page);
+      TileLoader<kPieces> w(pieces);
+      int n = 0;
       bool ok = true;
-      for (int n = 0; ok && walk.next(p, pc); ++n) {
-        const int qb = n & 1;
-        if (pc.blocks) {
-          cut = pc.blocks;
-          if (lane == 0) put_cut(p, pc, cut);
+      for (bool more = w.next(p, abort_flag); more; ++n) {
+        const int live = w.live(), log = w.log_box(p), mine = w.row, kvh = w.pc.kv_head;
+        const int place = is_v ? v_place<false>(n) : k_place<false>(n), slot = place % NS;
+        ok = wait_warp(empty + slot, ((place / NS) & 1) ^ 1, abort_flag, p.timeout_ns);
+        if (!ok) break;
+        copy_tile<kChunks, kLine>(is_v ? &maps.v : &maps.k, is_v ? &maps.v_tail : &maps.k_tail, smem + slot * C::kTile,
+                                  full + slot, kvh, mine, live, log, whole_log);
+        more = w.next(p, abort_flag);
+        if constexpr (QUANT) {
+          const float* src = (is_v ? p.vs : p.ks) + (long long)kvh * p.s_head;
+          const uint32_t at = smem_u32(smem + C::kScaleOff + slot * C::kScales) + lane * 4;
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const int key = x * 32 + lane;
+            const int row = __shfl_sync(0xffffffffu, mine, key >> log) + (key & ((1 << log) - 1));
+            if (key < live && row < p.num_kv_rows)
+              asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(at + x * 128), "l"(src + row) : "memory");
+          }
+          arrive_copies(full + slot);
         }
-        ok = wait_warp(q_empty + qb, ((n >> 1) & 1) ^ 1, abort_flag, p.timeout_ns);
+      }
+      ok = ok && w.ok;
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      if (lane == 0) {
+        issued[is_v ? 1 : 0] = n;
+        if (!ok) {
+          set_status(p.status, CPATTN_ERR_TIMEOUT);
+          *abort_flag = 1;
+        }
+      }
+    } else if (warp == kWarps + 2) {  // walks the share, two pieces ahead of the queries that it loads
+      TreeWalk w(p, start);
+      TreePiece ahead[2];
+      bool ok = true, cut = false;
+      auto walk = [&](int i) {  // piece i
+        TreePiece x;
+        if (!w.next(p, x)) x.tiles = x.rows = x.blocks = 0;
+        if (x.blocks) {
+          cut = true;
+          if (lane == 0) put_cut(p, x, x.blocks);
+        }
+        ok = ok && pieces.put(i, x, abort_flag, p.timeout_ns);
+        return x;
+      };
+      ahead[0] = walk(0);
+      if (ahead[0].tiles) ahead[1] = walk(1);
+      for (int i = 0; ok && ahead[0].tiles; ++i) {
+        const TreePiece pc = ahead[0];
+        const int qb = i & 1;
+        fetch_masks(p, pc);
+        ahead[0] = ahead[1];
+        if (ahead[0].tiles) ahead[1] = walk(i + 2);
+        ok = ok && wait_warp(q_empty + qb, ((i >> 1) & 1) ^ 1, abort_flag, p.timeout_ns);
         if (!ok) break;
         // the query rows, 16-byte chunks swizzled over a row's length
         for (int x = lane; x < pc.rows * (D / 8); x += 32) {
           const int r = x / (D / 8), ch = x % (D / 8), packed = pc.r0 + r, node = group_div(p, packed);
-          const __nv_bfloat16* src = p.q + (long long)(pc.req.row0 + node) * p.q_row +
+          const __nv_bfloat16* src = p.q + (long long)(pc.row0 + node) * p.q_row +
                                      (long long)(pc.kv_head * p.g + packed - node * p.g) * p.q_head + ch * 8;
           asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
                            smem_u32(smem + C::kQOff + qb * C::kQ) + r * (D * 2) + ((ch ^ (r & 7)) << 4)),
@@ -571,57 +623,10 @@ attn_tree_small_kernel(const __grid_constant__ TreeMaps maps, const TreeParams p
                        : "memory");
         }
         if (!p.withhold_q) arrive_copies(q_full + qb);
-        // Cache row of the lane's box of tile t: whole pages, or 16 rows of the unit's end.
-        // Looked up a tile ahead, so that the page table's latency is not waited for.
-        auto box_log = [&](int t) { return min(BN, pc.keys - (pc.t0 + t) * BN) > BN - 16 ? whole_log : 4; };
-        auto lookup = [&](int t) {
-          const int key0 = (pc.t0 + t) * BN, live = min(BN, pc.keys - key0), log = box_log(t);
-          return t < pc.tiles && (lane << log) < live ? cache_row(p, pc.b, key0 + (lane << log)) : 0;
-        };
-        int next = lookup(0);
-        for (int t = 0; t < pc.tiles && ok; ++t) {
-          const int mine = next, live = min(BN, pc.keys - (pc.t0 + t) * BN);
-          const int log = box_log(t), boxes = (live + (1 << log) - 1) >> log;
-          next = lookup(t + 1);
-          // (e4m3) the cache rows of the lane's scales, keys x * 32 + lane
-          int srow[4] = {0, 0, 0, 0};
-          if constexpr (QUANT) {
-  #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              const int key = x * 32 + lane;
-              srow[x] = __shfl_sync(0xffffffffu, mine, key >> log) + (key & ((1 << log) - 1));
-            }
-          }
-          for (int kv = 0; kv < 2; ++kv, ++seq) {
-            const int slot = seq % NS;
-            ok = wait_warp(empty + slot, ((seq / NS) & 1) ^ 1, abort_flag, p.timeout_ns);
-            if (!ok) break;
-            uint8_t* dst = smem + slot * C::kTile;
-            if (lane == 0) mbar_arrive_expect_tx(full + slot, (boxes << log) * kLine * kChunks);
-            __syncwarp();
-            if (lane < boxes) {
-              const CUtensorMap* tm = log == whole_log ? (kv ? &maps.v : &maps.k) : (kv ? &maps.v_tail : &maps.k_tail);
-  #pragma unroll
-              for (int c = 0; c < kChunks; ++c)
-                tma_load_3d(dst + (c * BN + (lane << log)) * kLine, tm, full + slot, c * 64, pc.kv_head, mine);
-            }
-            if constexpr (QUANT) {
-              const float* src = (kv ? p.vs : p.ks) + (long long)pc.kv_head * p.s_head;
-              const uint32_t at = smem_u32(smem + C::kScaleOff + slot * C::kScales) + lane * 4;
-  #pragma unroll
-              for (int x = 0; x < 4; ++x)
-                if (x * 32 + lane < live && srow[x] < p.num_kv_rows)
-                  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(at + x * 128), "l"(src + srow[x])
-                               : "memory");
-              arrive_copies(full + slot);
-            }
-          }
-        }
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
       if (lane == 0) {
         if (!cut) p.cut[2 * blockIdx.x + 1] = make_int4(0, 0, 0, 0);
-        *issued_loads = seq;
         if (!ok) {
           set_status(p.status, CPATTN_ERR_TIMEOUT);
           *abort_flag = 1;
@@ -646,18 +651,22 @@ attn_tree_small_kernel(const __grid_constant__ TreeMaps maps, const TreeParams p
     w.key0 = warp / QW * (16 * QW);
     int seq = 0;
     bool ok = true;
-    for (int n = 0; ok && walk.next(p, pc); ++n) ok = w.piece(p, pc, n, seq);
+    for (int n = 0;; ++n) {
+      ok = pieces.get(n, pc, abort_flag, p.timeout_ns);
+      // (all eight warps go on, or none)
+      if (bar_warps(!ok || pc.tiles == 0)) break;
+      ok = w.piece(p, pc, n, seq);
+      if (!ok) break;
+      if (lane == 0) pieces.done(n);
+    }
     if (!ok && lane == 0) {
       set_status(p.status, CPATTN_ERR_TIMEOUT);
       *abort_flag = 1;
     }
   }
   __syncthreads();
-  if (warp == kWarps && lane == 0 && *abort_flag) {
-    // let the copies in flight land before the shared memory goes
-    const int n = *issued_loads;
-    for (int j = max(0, n - NS); j < n; ++j) wait_one(full + j % NS, (j / NS) & 1, nullptr, p.timeout_ns);
-  }
+  // (after an abort) let the copies in flight land before the shared memory goes
+  if (warp == kWarps && lane == 0 && *abort_flag) drain_tiles<false>(full, NS, issued[0], issued[1], p.timeout_ns);
 }
 
 template <int D, bool QUANT, int NQ, int QW>
