@@ -11,51 +11,102 @@
 namespace cpattn {
 namespace {
 
-// Merge of the units that the blocks' shares cut: block (x, y) takes the unit that is cut
-// behind attention block x, y a part of its values.  A row's partials (O_j, L_j) combine as
+// Merge of the units that the blocks' shares cut: blocks (x, y) take the unit that is cut behind
+// attention block x.  A row's partials (O_j, L_j) combine as
 //     m = max L_j, w_j = exp(L_j - m), O = sum w_j O_j / sum w_j, L = m + ln sum w_j.
-constexpr int kMergeThreads = 256;
-template <int D>
-__global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const TreeParams p) {
+// Bound by latency, two dependent loads: the unit's description, and then L and O of up to
+// `LOADS` partials at once.  A thread has 4 columns of a row; where a unit has fewer values
+// than the block threads, several share a value's partials and are joined in shared memory.
+// Units of 8 and 16 rows: 512 threads, 8 loads; those of 128 and 256, of which most are cut
+// once, 256 and 4, for their bytes.
+struct MergeValue {  // sum_j 2^(L_j - m) (1, O_j)
+  float m, w;
+  float4 o;
+};
+__device__ __forceinline__ void merge_add(MergeValue& a, float m, float w, const float4& o) {
+  const float mn = fmaxf(a.m, m), use = mn == -INFINITY ? 0.f : mn;
+  const float fa = exp2f(a.m - use), fb = exp2f(m - use);
+  a.m = mn;
+  a.w = a.w * fa + w * fb;  // (a NaN partial stays one)
+  // (nothing of a partial without keys, whose O is zeros)
+  a.o = make_float4(a.o.x * fa + o.x * fb, a.o.y * fa + o.y * fb, a.o.z * fa + o.z * fb, a.o.w * fa + o.w * fb);
+}
+template <int D, int THREADS, int LOADS>
+__global__ void __launch_bounds__(THREADS) tree_merge_kernel(const TreeParams p) {
+  __shared__ MergeValue part[THREADS];
   grid_dep_wait();
   const int4 a = __ldcg(p.cut + 2 * blockIdx.x);
   const int blocks = __ldcg(p.cut + 2 * blockIdx.x + 1).x;
   if (blocks < 2 || blocks > (int)(gridDim.x - blockIdx.x)) return;
-  const int R = p.unit_rows, rows = a.z;
-  // half a chunk of 8 columns of a row
-  const int i = blockIdx.y * kMergeThreads + threadIdx.x, half = i & 1, r = (i >> 1) % R, c = (i >> 1) / R;
-  if (r >= rows || c >= D / 8) return;
+  const int R = p.unit_rows, rows = a.z, values = rows * (D / 4);
+  int ways = 1;
+  while (ways < blocks && 2 * ways * values <= THREADS) ways *= 2;
+  const int way = ways == 1 ? 0 : (int)threadIdx.x / values;
   auto slot_of = [&](int j) { return 2 * (int)blockIdx.x + (j == 0 ? 1 : 2 * j); };
-  float m = -INFINITY;
-#pragma unroll 8
-  for (int j = 0; j < blocks; ++j) m = fmaxf(m, __ldcg(p.ws_l + (long long)slot_of(j) * R + r));
-  const float use = m == -INFINITY ? 0.f : m;
-  float w = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-  for (int j = 0; j < blocks; ++j) {
-    const long long slot = (long long)slot_of(j) * R;
-    const float l = __ldcg(p.ws_l + slot + r);
-    const float4 x = __ldcg(reinterpret_cast<const float4*>(p.ws_o + slot * D + partial_at(c, r, R)) + half);
-    const float f = exp2f(l - use);
-    w += f;
-    if (f == 0.f) continue;
-    o.x = fmaf(f, x.x, o.x);
-    o.y = fmaf(f, x.y, o.y);
-    o.z = fmaf(f, x.z, o.z);
-    o.w = fmaf(f, x.w, o.w);
+  for (int i0 = blockIdx.y * THREADS; i0 < values; i0 += gridDim.y * THREADS) {
+    // half a chunk of 8 columns of a row
+    const int i = ways == 1 ? i0 + (int)threadIdx.x : (int)threadIdx.x - way * values;
+    const bool on = i < values && way < ways;
+    const int half = i & 1, c = (i >> 1) / rows, r = (i >> 1) - c * rows;
+    MergeValue v{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+    for (int j0 = way; on && j0 < blocks; j0 += ways * LOADS) {
+      float l[LOADS];
+      float4 o[LOADS];
+#pragma unroll
+      for (int x = 0; x < LOADS; ++x) {
+        const int j = j0 + x * ways;
+        l[x] = -INFINITY;
+        o[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (j < blocks) {
+          const long long slot = (long long)slot_of(j) * R;
+          l[x] = __ldcg(p.ws_l + slot + r);
+          o[x] = __ldcg(reinterpret_cast<const float4*>(p.ws_o + slot * D + partial_at(c, r, R)) + half);
+        }
+      }
+#pragma unroll
+      for (int x = 0; x < LOADS; ++x)
+        if (j0 + x * ways < blocks) merge_add(v, l[x], l[x] == -INFINITY ? 0.f : 1.f, o[x]);
+    }
+    if (ways > 1) {  // (one round)
+      part[threadIdx.x] = v;
+      __syncthreads();
+      if (way > 0 || !on) return;
+      for (int y = 1; y < ways; ++y) {
+        const MergeValue& other = part[threadIdx.x + y * values];
+        merge_add(v, other.m, other.w, other.o);
+      }
+    }
+    if (!on) continue;
+    const float inv = v.w == 0.f ? 0.f : 1.f / v.w;
+    const float4 out = make_float4(v.o.x * inv, v.o.y * inv, v.o.z * inv, v.o.w * inv);
+    const int packed = a.y + r, node = group_div(p, packed);
+    const long long at = (long long)(a.x + node) * p.Hq + a.w * p.g + packed - node * p.g;
+    const int col = c * 8 + half * 4;
+    if (p.o_f32)
+      *reinterpret_cast<float4*>(static_cast<float*>(p.o) + at * D + col) = out;
+    else
+      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + at * D + col) =
+          make_uint2(pack_bf16x2(out.x, out.y), pack_bf16x2(out.z, out.w));
+    if (col == 0) p.lse[at] = v.w == 0.f ? -INFINITY : (v.m + log2f(v.w)) * kLn2;
   }
-  const float inv = w == 0.f ? 0.f : 1.f / w;
-  o = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
-  const int packed = a.y + r, node = group_div(p, packed);
-  const long long at = (long long)(a.x + node) * p.Hq + a.w * p.g + packed - node * p.g;
-  const int col = c * 8 + half * 4;
-  if (p.o_f32)
-    *reinterpret_cast<float4*>(static_cast<float*>(p.o) + at * D + col) = o;
-  else
-    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + at * D + col) =
-        make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
-  if (col == 0) p.lse[at] = w == 0.f ? -INFINITY : (use + log2f(w)) * kLn2;
+}
+
+template <int D, int THREADS, int LOADS>
+cudaError_t launch_merge(const TreeParams& p, int num_ctas, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(num_ctas, (p.unit_rows * (D / 4) + THREADS - 1) / THREADS);
+  cfg.blockDim = dim3(THREADS);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, tree_merge_kernel<D, THREADS, LOADS>, p);
+}
+template <int D>
+cudaError_t launch_merge(const TreeParams& p, int num_ctas, cudaStream_t stream) {
+  return p.unit_rows < BM ? launch_merge<D, 512, 8>(p, num_ctas, stream) : launch_merge<D, 256, 4>(p, num_ctas, stream);
 }
 
 // 3-D map of the queries (cols, heads, rows) whose box is 64 columns of the g heads of a KV
@@ -192,16 +243,7 @@ extern "C" int cp_attn_tree(const void* q, int64_t q_row_stride, int64_t q_head_
   const int r = p.unit_rows < BM ? launch_tree_small(m, p, d, quant, num_ctas, stream)
                                  : launch_tree_mma(m, p, d, quant, num_ctas, stream);
   if (r != CPATTN_OK) return r;
-  auto merge = d == 128 ? tree_merge_kernel<128> : tree_merge_kernel<64>;
-  const dim3 grid(num_ctas, (p.unit_rows * (d / 8) * 2 + kMergeThreads - 1) / kMergeThreads);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(kMergeThreads);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, merge, p) == cudaSuccess ? CPATTN_OK : CPATTN_ERR_CUDA;
+  return (d == 128 ? launch_merge<128>(p, num_ctas, stream) : launch_merge<64>(p, num_ctas, stream)) == cudaSuccess
+             ? CPATTN_OK
+             : CPATTN_ERR_CUDA;
 }

@@ -5,12 +5,13 @@
 // 1.4 us (bf16, d = 128): so eight warps work on registers, with 16x8x16 MMAs that have keys
 // (and then the columns of V) as their 16 rows and queries as their 8 columns:
 //     S^T = K Q^T,   O^T += V^T P^T.
-// QW groups of warps share a KV tile's keys, 8 / QW warps to a group, and a group has NQ
-// columns of 8 rows: 8 * NQ * QW rows a unit.  Each warp keeps its own maximum, sum and
-// output; at a piece's end the 8 / QW of a row are joined in shared memory.  The ninth warp
-// loads: a tile's K and V pages by TMA, one lane a page, the query rows and (e4m3) the
-// scales by asynchronous copies, all of them ahead across piece ends.  A warp's step issues
-// the products of the next 16 keys between the softmax and the second product of these.
+// A unit has NQ columns of 8 rows, and the warps share its KV tiles' keys: 16 each, or (e4m3,
+// where the decoding's latency counts) in two teams that take turns at the tiles, 32 each.
+// Each warp keeps its own maximum, sum and output; at a piece's end the eight are joined in
+// shared memory.  Three more warps feed them: K and V pages by TMA, one lane a page, (e4m3)
+// with their scales by asynchronous copies; and the query rows, by the warp that walks the
+// block's share.  A warp's step issues the products of its next keys between the softmax and
+// the second product of these.
 //
 // Fragments are loaded as they lie in memory.  K Q^T sums over d in any order, so lane
 // (g = lane / 4, c = lane % 4) takes whole 16-byte chunks of key rows g and g + 8 and of
@@ -35,10 +36,11 @@ constexpr int kMaxStages = 12;
 constexpr int kPieces = 4;  // in the ring
 using Pieces = PieceRing<kPieces>;
 
-template <int D, bool QUANT, int NQ, int QW>
+template <int D, bool QUANT, int NQ>
 struct TreeCfg {
-  static constexpr int kRows = 8 * NQ * QW;  // of a unit
-  static constexpr int kKeyWarps = kWarps / QW;
+  static constexpr int kRows = 8 * NQ;  // of a unit
+  static constexpr int kTeams = QUANT ? 2 : 1;
+  static constexpr int kKeys = BN * kTeams / kWarps;  // of a warp in its team's tiles
   static constexpr int kTile = BN * D * (QUANT ? 1 : 2);
   static constexpr int kScales = QUANT ? BN * 4 : 0;  // the rows' scales, fp32
   static constexpr int kQ = kRows * D * 2;            // two of them
@@ -85,15 +87,16 @@ __device__ __forceinline__ int join_at(int d, int r) {
   return d ^ (((r >> 1) & 3) << (QUANT ? 2 : 3));
 }
 
-template <int D, bool QUANT, int NQ, int QW>
+template <int D, bool QUANT, int NQ>
 struct Warp {
-  using C = TreeCfg<D, QUANT, NQ, QW>;
+  using C = TreeCfg<D, QUANT, NQ>;
   static constexpr int kOut = D / 16, kLoads = QUANT ? D / 64 : D / 32;
+  static constexpr int kTeams = C::kTeams, kKeys = C::kKeys, kBlocks = kKeys / 16;
   uint32_t base;  // shared memory
   uint8_t* mem;
   uint64_t *full, *empty, *q_full, *q_empty;
   const volatile int* abort;
-  int warp, lane, g, c, row0, key0;  // row0: the warp's first row; key0: its first key of a tile
+  int warp, lane, g, c, team, key0;  // key0: the warp's first key of its team's tiles
 
   __device__ __forceinline__ void release(uint64_t* bar) const {
     __syncwarp();
@@ -159,15 +162,16 @@ struct Warp {
                   (QUANT ? score_factor(factor[n][y & 1], k.scale[y >> 1]) : factor[n][y & 1]);
   }
 
-  // Which of the 16 value rows from `key` of a tile on hold an infinity or NaN.
-  __device__ __forceinline__ uint32_t bad_rows(int slot, int key) const {
+  // Which of the warp's value rows of a tile hold an infinity or NaN.
+  __device__ __forceinline__ uint32_t bad_rows(int slot) const {
+    constexpr int kParts = 32 / kKeys;                          // lanes of a row
+    constexpr int kN = D * (QUANT ? 1 : 2) / 16 / kParts;       // chunks of a lane
     const uint32_t tile = base + slot * C::kTile;
-    const int row = key + (lane >> 1), half = lane & 1;
-    constexpr int kN = D * (QUANT ? 1 : 2) / 32;  // chunks of half a row
+    const int row = key0 + lane / kParts;
     bool bad = false;
 #pragma unroll
     for (int x = 0; x < kN; ++x) {
-      const int ch = half * kN + x;
+      const int ch = lane % kParts * kN + x;
       const uint4 v = lds128(QUANT ? tile + code_at<D>(row, ch)
                                    : tile + (ch >> 3) * (BN * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4));
       const uint32_t u[4] = {v.x, v.y, v.z, v.w};
@@ -178,18 +182,18 @@ struct Warp {
         else
           bad = bad || __vcmpgeu2(u[y] & 0x7FFF7FFFu, 0x7F807F80u) != 0;
     }
-    return __reduce_or_sync(0xffffffffu, bad ? 1u << (lane >> 1) : 0u);
+    return __reduce_or_sync(0xffffffffu, bad ? 1u << (lane / kParts) : 0u);
   }
 
-  __device__ bool piece(const TreeParams& p, const TreePiece& pc, int n_piece, int& seq) const;
+  __device__ bool piece(const TreeParams& p, const TreePiece& pc, int n_piece, int n0) const;
 };
 
-template <int D, bool QUANT, int NQ, int QW>
-__device__ __forceinline__ bool Warp<D, QUANT, NQ, QW>::piece(const TreeParams& p, const TreePiece& pc, int n_piece,
-                                                              int& seq) const {
+template <int D, bool QUANT, int NQ>
+__device__ __forceinline__ bool Warp<D, QUANT, NQ>::piece(const TreeParams& p, const TreePiece& pc, int n_piece,
+                                                          int n0) const {
   constexpr int NS = C::kStages;
   const unsigned all = 0xffffffffu;
-  const int T = pc.tiles, qb = n_piece & 1;
+  const int qb = n_piece & 1;
   const int tile0 = pc.t0 * BN;  // first key
   // ---- queries: row g of each column ----
   uint32_t q[NQ][kOut][2];
@@ -198,7 +202,7 @@ __device__ __forceinline__ bool Warp<D, QUANT, NQ, QW>::piece(const TreeParams& 
 #pragma unroll
   for (int n = 0; n < NQ; ++n) {
     uint4 v[D / 32];
-    const int row = row0 + 8 * n + g;
+    const int row = 8 * n + g;
 #pragma unroll
     for (int x = 0; x < D / 32; ++x) {
       v[x] = lds128(base + C::kQOff + qb * C::kQ + row * (D * 2) +
@@ -251,143 +255,139 @@ __device__ __forceinline__ bool Warp<D, QUANT, NQ, QW>::piece(const TreeParams& 
       m_use[n][e] = l_run[n][e] = 0.f;
     }
   }
-  const bool rows_live = row0 < pc.rows;  // (the warp has rows)
   int ev = -126;  // (e4m3) exponent of O
-  Keys k;
-  float s[NQ][4];
-  ok = ok && wait_warp(full + seq % NS, (seq / NS) & 1, abort, p.timeout_ns);
-  if (ok) {
-    if (rows_live && tile0 + key0 < pc.keys) {
-      load_k(k, seq % NS, key0);
-      product(k, q, factor, s);
-    }
-    if (QW == 1) release(empty + seq % NS);
-  }
-  for (int t = 0; t < T && ok; ++t, seq += 2) {
-    const int k_now = seq % NS, v_slot = (seq + 1) % NS, k_next = (seq + 2) % NS;
-    const bool more = t + 1 < T;
-    ok = wait_warp(full + v_slot, ((seq + 1) / NS) & 1, abort, p.timeout_ns) &&
-         (!more || wait_warp(full + k_next, ((seq + 2) / NS) & 1, abort, p.timeout_ns));
-    if (!ok) break;
-    const uint32_t tile = base + v_slot * C::kTile;
-#pragma unroll 1
-    for (int step = 0; step < QW; ++step) {
-      const bool last_step = step == QW - 1;
-      const int key = key0 + 16 * step, at = tile0 + t * BN + key;  // in the tile, of the request
-      const bool work = rows_live && at < pc.keys;
-      const int at_next = last_step ? tile0 + (t + 1) * BN + key0 : at + 16;
-      const bool next_work = rows_live && (last_step ? more : true) && at_next < pc.keys;
-      if (next_work) load_k(k, last_step ? k_next : k_now, last_step ? key0 : key + 16);
-      // value rows that count: up to the last key, and (new keys) finite
-      uint32_t alive = 0xFFFFu;
-      // (e4m3) the lane's codes of the keys 2c, 2c + 1, 2c + 8, 2c + 9, and their scales
-      uint32_t u[4][D / 32];
-      float f[4];
-      uint32_t pb[NQ][2];
-      if (work) {
-        if (pc.keys - at < 16) alive >>= 16 - (pc.keys - at);
-        if (at + 16 > pc.L) {  // new keys among them: who sees which
-          const uint32_t bad = bad_rows(v_slot, key) & alive & ~((1u << min(16, max(0, pc.L - at))) - 1u);
-          alive &= ~bad;
+  // A warp waits for every place of the ring in its order, the other team's, too, so that it
+  // sees all phases of the barriers.
+  auto wait_k = [&](int n) {
+    const int place = k_place<false>(n);
+    return wait_warp(full + place % NS, (place / NS) & 1, abort, p.timeout_ns);
+  };
+  auto wait_v = [&](int n) {
+    const int place = v_place<false>(n);
+    return wait_warp(full + place % NS, (place / NS) & 1, abort, p.timeout_ns);
+  };
+  float s[kBlocks][NQ][4];
+  auto scores = [&](int n) {  // of the block's n-th tile
+    const int slot = k_place<false>(n) % NS;
 #pragma unroll
-          for (int n = 0; n < NQ; ++n)
+    for (int b = 0; b < kBlocks; ++b) {
+      Keys k;
+      load_k(k, slot, key0 + 16 * b);
+      product(k, q, factor, s[b]);
+    }
+  };
+  int t = kTeams == 1 ? 0 : (n0 ^ team) & 1;  // the team's first tile
+  if (t == 1) ok = ok && wait_k(n0) && wait_v(n0);
+  if (t < pc.tiles) {
+    ok = ok && wait_k(n0 + t);
+    if (ok) {
+      if (tile0 + t * BN + key0 < pc.keys) scores(n0 + t);
+      release(empty + k_place<false>(n0 + t) % NS);
+    }
+  }
+  for (; t < pc.tiles && ok; t += kTeams) {
+    const int n = n0 + t, v_slot = v_place<false>(n) % NS, at = tile0 + t * BN + key0;
+    const bool more = t + kTeams < pc.tiles;
+    ok = wait_v(n);
+    if (kTeams == 2 && t + 1 < pc.tiles) ok = ok && wait_k(n + 1) && wait_v(n + 1);
+    if (more) ok = ok && wait_k(n + kTeams);
+    if (!ok) break;
+    const bool work = at < pc.keys, next_work = more && at + kTeams * BN < pc.keys;
+    const uint32_t tile = base + v_slot * C::kTile;
+    uint32_t alive = ~0u;  // value rows that count: up to the last key, and (new keys) finite
+    uint32_t pb[kBlocks][NQ][2];
+    if (work) {
+      const bool masked = at + kKeys > pc.L;  // new keys among them, or keys behind the last
+      if (masked) {
+        if (pc.keys - at < kKeys) alive = (1u << (pc.keys - at)) - 1u;
+        const uint32_t fresh = at >= pc.L ? ~0u : ~0u << min(31, pc.L - at);
+        const uint32_t bad = bad_rows(v_slot) & alive & fresh;
+        alive &= ~bad;
+#pragma unroll
+        for (int b = 0; b < kBlocks; ++b)
+#pragma unroll
+          for (int x = 0; x < NQ; ++x)
 #pragma unroll
             for (int y = 0; y < 4; ++y) {
-              const int kk = g + (y >> 1) * 8, node = at + kk - pc.L;
-              const int r = row0 + 8 * n + 2 * c + (y & 1);
-              if (node < 0 || r >= pc.rows) continue;
-              if (node >= pc.T || !sees(p, pc, group_div(p, pc.r0 + r), node)) s[n][y] = -INFINITY;
-              else if ((bad >> kk) & 1u) s[n][y] = __uint_as_float(0x7FC00000u);  // the row becomes NaN
+              const int kk = 16 * b + g + (y >> 1) * 8, node = at + kk - pc.L;
+              const int r = 8 * x + 2 * c + (y & 1);
+              if (at + kk >= pc.keys) s[b][x][y] = -INFINITY;
+              else if (node < 0 || r >= pc.rows) continue;
+              else if (!sees(p, pc, group_div(p, pc.r0 + r), node)) s[b][x][y] = -INFINITY;
+              else if ((bad >> kk) & 1u) s[b][x][y] = __uint_as_float(0x7FC00000u);  // the row becomes NaN
             }
+      }
+      // ---- softmax, base 2; the maximum moves only when a step raises it by more than
+      // kMaxSlack, so that O is seldom rescaled ----
+      bool any = false;
+      float alpha[NQ][2];
+#pragma unroll
+      for (int x = 0; x < NQ; ++x) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float mx = -INFINITY;
+#pragma unroll
+          for (int b = 0; b < kBlocks; ++b) mx = fmaxf(mx, fmaxf(s[b][x][e], s[b][x][e + 2]));
+          mx = fmaxf(mx, __shfl_xor_sync(all, mx, 4));
+          mx = fmaxf(mx, __shfl_xor_sync(all, mx, 8));
+          mx = fmaxf(mx, __shfl_xor_sync(all, mx, 16));
+          if (QUANT) mx -= kF16Lift;
+          const bool move = mx > m_run[x][e] + kMaxSlack;
+          const float m_new = move ? mx : m_run[x][e];
+          const float use = m_new == -INFINITY ? 0.f : m_new;
+          alpha[x][e] = move ? ex2_approx(m_run[x][e] - use) : 1.f;
+          any = any || move;
+          m_run[x][e] = m_new;
+          m_use[x][e] = use;
+          float sum = 0.f;
+#pragma unroll
+          for (int b = 0; b < kBlocks; ++b) {
+            const float a = ex2_approx(s[b][x][e] - use), z = ex2_approx(s[b][x][e + 2] - use);
+            sum += a + z;
+            s[b][x][e] = a;
+            s[b][x][e + 2] = z;
+          }
+          l_run[x][e] = l_run[x][e] * alpha[x][e] + sum;
         }
-        if constexpr (QUANT) {
+        // P in 16 bits, the second product's operand type: off by at most 2^-8 (bf16) or
+        // 2^-11 (f16) of each weight; l sums the unrounded values.  Queries by rows, keys
+        // by columns now
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const int row = key + 2 * c + (x >> 1) * 8 + (x & 1);
-            f[x] = lds_f32(scale_at(v_slot, row));
-            if constexpr (D == 128) {
-              const uint4 v = lds128(tile + code_at<D>(row, g));
-              u[x][0] = v.x; u[x][1] = v.y; u[x][2] = v.z; u[x][3] = v.w;
-            } else {
-              const uint2 v = lds64(tile + code_at<D>(row, g >> 1) + (g & 1) * 8);
-              u[x][0] = v.x; u[x][1] = v.y;
-            }
-          }
-          if (alive != 0xFFFFu) {
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-              if (!((alive >> (2 * c + (x >> 1) * 8 + (x & 1))) & 1u)) {
-                f[x] = 0.f;
-#pragma unroll
-                for (int y = 0; y < D / 32; ++y) u[x][y] = 0u;
-              }
-          }
-        }
-        // ---- softmax, base 2; the maximum moves only when a step raises it by more than
-        // kMaxSlack, so that O is seldom rescaled ----
-        bool any = false;
-        float alpha[NQ][2];
-#pragma unroll
-        for (int n = 0; n < NQ; ++n) {
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            // keys behind the last
-            if (pc.keys - at < 16) {
-              if (at + g >= pc.keys) s[n][e] = -INFINITY;
-              if (at + g + 8 >= pc.keys) s[n][e + 2] = -INFINITY;
-            }
-            float mx = fmaxf(s[n][e], s[n][e + 2]);
-            mx = fmaxf(mx, __shfl_xor_sync(all, mx, 4));
-            mx = fmaxf(mx, __shfl_xor_sync(all, mx, 8));
-            mx = fmaxf(mx, __shfl_xor_sync(all, mx, 16));
-            if (QUANT) mx -= kF16Lift;
-            const bool move = mx > m_run[n][e] + kMaxSlack;
-            const float m_new = move ? mx : m_run[n][e];
-            const float use = m_new == -INFINITY ? 0.f : m_new;
-            alpha[n][e] = move ? ex2_approx(m_run[n][e] - use) : 1.f;
-            any = any || move;
-            m_run[n][e] = m_new;
-            m_use[n][e] = use;
-            const float a = ex2_approx(s[n][e] - use), z = ex2_approx(s[n][e + 2] - use);
-            l_run[n][e] = l_run[n][e] * alpha[n][e] + (a + z);
-            s[n][e] = a;
-            s[n][e + 2] = z;
-          }
-          // P in 16 bits, the second product's operand type: off by at most 2^-8 (bf16) or
-          // 2^-11 (f16) of each weight; l sums the unrounded values.  Queries by rows, keys
-          // by columns now
+        for (int b = 0; b < kBlocks; ++b)
 #pragma unroll
           for (int hh = 0; hh < 2; ++hh)
-            pb[n][hh] = transpose_8x8(QUANT ? pack_f16x2(s[n][2 * hh], s[n][2 * hh + 1])
-                                            : pack_bf16x2(s[n][2 * hh], s[n][2 * hh + 1]));
-        }
-        if (__any_sync(all, any)) {
-#pragma unroll
-          for (int n = 0; n < NQ; ++n)
-#pragma unroll
-            for (int x = 0; x < kOut; ++x)
-#pragma unroll
-              for (int y = 0; y < 4; ++y) o[n][x][y] *= alpha[n][y & 1];
-        }
+            pb[b][x][hh] = transpose_8x8(QUANT ? pack_f16x2(s[b][x][2 * hh], s[b][x][2 * hh + 1])
+                                               : pack_bf16x2(s[b][x][2 * hh], s[b][x][2 * hh + 1]));
       }
-      // ---- the next keys' S, then O += P V ----
-      if (next_work) product(k, q, factor, s);
-      if (last_step) {
-        if (QW > 1) release(empty + k_now);
-        else if (more) release(empty + k_next);
+      if (__any_sync(all, any)) {
+#pragma unroll
+        for (int x = 0; x < NQ; ++x)
+#pragma unroll
+          for (int y = 0; y < kOut; ++y)
+#pragma unroll
+            for (int z = 0; z < 4; ++z) o[x][y][z] *= alpha[x][z & 1];
       }
-      if (work) {
+    }
+    // ---- the next tile's S, then O += P V ----
+    if (more) {
+      if (next_work) scores(n + kTeams);
+      release(empty + k_place<false>(n + kTeams) % NS);
+    }
+    if (work) {
+#pragma unroll
+      for (int b = 0; b < kBlocks; ++b) {
+        const uint32_t live = alive >> (16 * b);
         if constexpr (!QUANT) {
           // keys 2c, 2c + 1 (and + 8) of a column
           uint32_t mask[2] = {~0u, ~0u};
-          if (alive != 0xFFFFu)
+          if (alive != ~0u)
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-              const uint32_t two = alive >> (2 * c + 8 * x);
+              const uint32_t two = live >> (2 * c + 8 * x);
               mask[x] = (two & 1u ? 0xFFFFu : 0u) | (two & 2u ? 0xFFFF0000u : 0u);
             }
           // matrix x of the load: columns 8 (x & 1) of 16, keys 8 (x >> 1)
-          const int row = key + (lane & 7) + 8 * (lane >> 4), col = (lane >> 3) & 1;
+          const int row = key0 + 16 * b + (lane & 7) + 8 * (lane >> 4), col = (lane >> 3) & 1;
 #pragma unroll
           for (int x = 0; x < kOut; ++x) {
             const int chunk = 2 * x + col;
@@ -397,22 +397,46 @@ __device__ __forceinline__ bool Warp<D, QUANT, NQ, QW>::piece(const TreeParams& 
                          : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
                          : "r"(from));
 #pragma unroll
-            for (int n = 0; n < NQ; ++n)
-              mma_16816<false>(o[n][x], v[0] & mask[0], v[1] & mask[0], v[2] & mask[1], v[3] & mask[1], pb[n][0],
-                               pb[n][1]);
+            for (int y = 0; y < NQ; ++y)
+              mma_16816<false>(o[y][x], v[0] & mask[0], v[1] & mask[0], v[2] & mask[1], v[3] & mask[1], pb[b][y][0],
+                               pb[b][y][1]);
           }
         } else {
+          // the lane's codes of the keys 2c, 2c + 1, 2c + 8, 2c + 9, and their scales
+          uint32_t u[4][D / 32];
+          float f[4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const int row = key0 + 16 * b + 2 * c + (x >> 1) * 8 + (x & 1);
+            f[x] = lds_f32(scale_at(v_slot, row));
+            if constexpr (D == 128) {
+              const uint4 v = lds128(tile + code_at<D>(row, g));
+              u[x][0] = v.x; u[x][1] = v.y; u[x][2] = v.z; u[x][3] = v.w;
+            } else {
+              const uint2 v = lds64(tile + code_at<D>(row, g >> 1) + (g & 1) * 8);
+              u[x][0] = v.x; u[x][1] = v.y;
+            }
+          }
+          if (alive != ~0u) {
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              if (!((live >> (2 * c + (x >> 1) * 8 + (x & 1))) & 1u)) {
+                f[x] = 0.f;
+#pragma unroll
+                for (int y = 0; y < D / 32; ++y) u[x][y] = 0u;
+              }
+          }
           // factors of the lane's keys, relative to 2^ev
           const int e = exponent_of(__uint_as_float(
               __reduce_max_sync(all, __float_as_uint(fmaxf(fmaxf(f[0], f[1]), fmaxf(f[2], f[3]))))));
           if (e > ev) {  // (the same for the warp)
             const float down = exp2_int(max(ev - e, -126));
 #pragma unroll
-            for (int n = 0; n < NQ; ++n)
+            for (int y = 0; y < NQ; ++y)
 #pragma unroll
               for (int x = 0; x < kOut; ++x)
 #pragma unroll
-                for (int y = 0; y < 4; ++y) o[n][x][y] *= down;
+                for (int z = 0; z < 4; ++z) o[y][x][z] *= down;
             ev = e;
           }
           const float inv = exp2_int(-ev);
@@ -424,7 +448,7 @@ __device__ __forceinline__ bool Warp<D, QUANT, NQ, QW>::piece(const TreeParams& 
             const uint32_t a0 = mul_f16x2(e4m3x2_to_f16x2(a), f0), a1 = mul_f16x2(e4m3x2_to_f16x2(a >> 16), f0);
             const uint32_t a2 = mul_f16x2(e4m3x2_to_f16x2(z), f1), a3 = mul_f16x2(e4m3x2_to_f16x2(z >> 16), f1);
 #pragma unroll
-            for (int n = 0; n < NQ; ++n) mma_16816<true>(o[n][x], a0, a1, a2, a3, pb[n][0], pb[n][1]);
+            for (int y = 0; y < NQ; ++y) mma_16816<true>(o[y][x], a0, a1, a2, a3, pb[b][y][0], pb[b][y][1]);
           }
         }
       }
@@ -464,20 +488,18 @@ __device__ __forceinline__ bool Warp<D, QUANT, NQ, QW>::piece(const TreeParams& 
   if (!ok) return false;
   for (int i = warp * 32 + lane; i < pc.rows * (D / 4); i += 32 * kWarps) {
     const int r = i / (D / 4), d = i % (D / 4) * 4;  // row, column
-    const int first = r / (8 * NQ), in = r % (8 * NQ);  // its first warp (every QW-th after), row of the warp's
     float M = -INFINITY, Lsum = 0.f;
-    float2 v[C::kKeyWarps];
+    float2 v[kWarps];
 #pragma unroll
-    for (int y = 0; y < C::kKeyWarps; ++y) {
-      v[y] = ml[(first + y * QW) * (8 * NQ) + in];
+    for (int y = 0; y < kWarps; ++y) {
+      v[y] = ml[y * (8 * NQ) + r];
       if (v[y].y != 0.f) M = fmaxf(M, v[y].x);  // (m of a warp without keys means nothing)
     }
     if (M == -INFINITY) M = 0.f;
     float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int y = 0; y < C::kKeyWarps; ++y) {
-      const float4 part =
-          *reinterpret_cast<const float4*>(join + ((first + y * QW) * (8 * NQ) + in) * D + join_at<QUANT>(d, in));
+    for (int y = 0; y < kWarps; ++y) {
+      const float4 part = *reinterpret_cast<const float4*>(join + (y * (8 * NQ) + r) * D + join_at<QUANT>(d, r));
       if (v[y].y == 0.f) continue;
       const float fw = ex2_approx(v[y].x - M);
       Lsum += fw * v[y].y;
@@ -507,10 +529,10 @@ __device__ __forceinline__ bool Warp<D, QUANT, NQ, QW>::piece(const TreeParams& 
   return true;
 }
 
-template <int D, bool QUANT, int NQ, int QW>
+template <int D, bool QUANT, int NQ>
 __global__ void __launch_bounds__(kThreads, 1)
 attn_tree_small_kernel(const __grid_constant__ TreeMaps maps, const TreeParams p) {
-  using C = TreeCfg<D, QUANT, NQ, QW>;
+  using C = TreeCfg<D, QUANT, NQ>;
   constexpr int NS = C::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -532,7 +554,7 @@ attn_tree_small_kernel(const __grid_constant__ TreeMaps maps, const TreeParams p
     prefetch_tmap(&maps.v_tail);
     for (int i = 0; i < NS; ++i) {
       mbar_init(full + i, QUANT ? 33 : 1);  // the TMA copies and each lane's scales
-      mbar_init(empty + i, kWarps);
+      mbar_init(empty + i, kWarps / C::kTeams);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(q_full + i, 32);  // each lane's copies
@@ -635,7 +657,7 @@ attn_tree_small_kernel(const __grid_constant__ TreeMaps maps, const TreeParams p
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsWork));
-    Warp<D, QUANT, NQ, QW> w;
+    Warp<D, QUANT, NQ> w;
     w.base = smem_u32(smem);
     w.mem = smem;
     w.full = full;
@@ -647,16 +669,17 @@ attn_tree_small_kernel(const __grid_constant__ TreeMaps maps, const TreeParams p
     w.lane = lane;
     w.g = lane >> 2;
     w.c = lane & 3;
-    w.row0 = warp % QW * (8 * NQ);
-    w.key0 = warp / QW * (16 * QW);
-    int seq = 0;
+    w.team = warp * C::kTeams / kWarps;
+    w.key0 = warp % (kWarps / C::kTeams) * C::kKeys;
+    int n0 = 0;  // KV tiles before the piece
     bool ok = true;
     for (int n = 0;; ++n) {
       ok = pieces.get(n, pc, abort_flag, p.timeout_ns);
       // (all eight warps go on, or none)
       if (bar_warps(!ok || pc.tiles == 0)) break;
-      ok = w.piece(p, pc, n, seq);
+      ok = w.piece(p, pc, n, n0);
       if (!ok) break;
+      n0 += pc.tiles;
       if (lane == 0) pieces.done(n);
     }
     if (!ok && lane == 0) {
@@ -669,30 +692,28 @@ attn_tree_small_kernel(const __grid_constant__ TreeMaps maps, const TreeParams p
   if (warp == kWarps && lane == 0 && *abort_flag) drain_tiles<false>(full, NS, issued[0], issued[1], p.timeout_ns);
 }
 
-template <int D, bool QUANT, int NQ, int QW>
+template <int D, bool QUANT, int NQ>
 int launch(const TreeMaps& m, const TreeParams& p, int num_ctas, cudaStream_t stream) {
-  using C = TreeCfg<D, QUANT, NQ, QW>;
-  auto kern = attn_tree_small_kernel<D, QUANT, NQ, QW>;
+  using C = TreeCfg<D, QUANT, NQ>;
+  auto kern = attn_tree_small_kernel<D, QUANT, NQ>;
   if (!allow_smem(kern, C::kSmemBytes)) return CPATTN_ERR_CUDA;
   if (!split_covered(kern, kThreads, kRegsWork * 256 + kRegsOther * 128)) return CPATTN_ERR_UNSUPPORTED;
   return launch_kernel(kern, (unsigned)num_ctas, kThreads, C::kSmemBytes, stream, false, m, p) == cudaSuccess
              ? CPATTN_OK
              : CPATTN_ERR_CUDA;
 }
-template <int NQ, int QW>
+template <int NQ>
 int launch(const TreeMaps& m, const TreeParams& p, int d, bool quant, int num_ctas, cudaStream_t stream) {
-  return d == 128 ? (quant ? launch<128, true, NQ, QW>(m, p, num_ctas, stream)
-                           : launch<128, false, NQ, QW>(m, p, num_ctas, stream))
-                  : (quant ? launch<64, true, NQ, QW>(m, p, num_ctas, stream)
-                           : launch<64, false, NQ, QW>(m, p, num_ctas, stream));
+  return d == 128 ? (quant ? launch<128, true, NQ>(m, p, num_ctas, stream)
+                           : launch<128, false, NQ>(m, p, num_ctas, stream))
+                  : (quant ? launch<64, true, NQ>(m, p, num_ctas, stream)
+                           : launch<64, false, NQ>(m, p, num_ctas, stream));
 }
 
 }  // namespace
 
 int launch_tree_small(const TreeMaps& m, const TreeParams& p, int d, bool quant, int num_ctas, cudaStream_t stream) {
-  return p.unit_rows == 8    ? launch<1, 1>(m, p, d, quant, num_ctas, stream)
-         : p.unit_rows == 16 ? launch<2, 1>(m, p, d, quant, num_ctas, stream)
-                             : launch<2, 2>(m, p, d, quant, num_ctas, stream);
+  return p.unit_rows == 8 ? launch<1>(m, p, d, quant, num_ctas, stream) : launch<2>(m, p, d, quant, num_ctas, stream);
 }
 
 }  // namespace cpattn
