@@ -109,6 +109,27 @@ cudaError_t launch_merge(const TreeParams& p, int num_ctas, cudaStream_t stream)
   return p.unit_rows < BM ? launch_merge<D, 512, 8>(p, num_ctas, stream) : launch_merge<D, 256, 4>(p, num_ctas, stream);
 }
 
+// 3-D map of a cache (cols, heads, rows) with a box of one head and 64 columns (codes: all). A
+// head's row is all that a block reads of a cache row, so that L2 must not fetch more of it:
+// with 256 bytes at a time, the 128 of a head's codes brought another head's along.
+bool make_rows_map(CUtensorMap* m, const void* base, int cols, bool codes, int heads, long long rows,
+                   int64_t head_stride, int64_t row_stride, int box_rows) {
+  auto enc = tensor_map_encoder();
+  if (!enc) return false;
+  const int size = codes ? 1 : 2, bytes = cols * size;
+  cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)heads, (cuuint64_t)rows};
+  cuuint64_t strides[2] = {(cuuint64_t)(head_stride * size), (cuuint64_t)(row_stride * size)};
+  cuuint32_t box[3] = {(cuuint32_t)(codes ? cols : 64), 1, (cuuint32_t)box_rows};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return enc(m, codes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base),
+             dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+             bytes == 64    ? CU_TENSOR_MAP_L2_PROMOTION_L2_64B
+             : bytes == 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B
+                            : CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // 3-D map of the queries (cols, heads, rows) whose box is 64 columns of the g heads of a KV
 // head and of BM / g rows.
 bool make_q_map(CUtensorMap* m, const void* q, int cols, int heads, int rows, int64_t head_stride,
@@ -231,8 +252,7 @@ extern "C" int cp_attn_tree(const void* q, int64_t q_row_stride, int64_t q_head_
   TreeMaps m;
   const int whole = std::min(BN, page_size);
   auto map = [&](CUtensorMap* t, const void* base, int64_t hs, int64_t rs, int box_rows) {
-    return quant ? make_code_map(t, base, d, Hkv, num_kv_rows, hs, rs, box_rows)
-                 : make_map(t, base, d, Hkv, num_kv_rows, hs, rs, box_rows);
+    return make_rows_map(t, base, d, quant, Hkv, num_kv_rows, hs, rs, box_rows);
   };
   if (!map(&m.k, k, k_head_stride, k_row_stride, whole) || !map(&m.v, v, v_head_stride, v_row_stride, whole) ||
       !map(&m.k_tail, k, k_head_stride, k_row_stride, 16) || !map(&m.v_tail, v, v_head_stride, v_row_stride, 16))
