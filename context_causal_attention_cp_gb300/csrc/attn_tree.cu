@@ -37,12 +37,12 @@ __global__ void __launch_bounds__(THREADS) tree_merge_kernel(const TreeParams p)
   grid_dep_wait();
   const int4 a = __ldcg(p.cut + 2 * blockIdx.x);
   const int blocks = __ldcg(p.cut + 2 * blockIdx.x + 1).x;
-  if (blocks < 2 || blocks > (int)(gridDim.x - blockIdx.x)) return;
+  if (blocks < 2 || (long long)blockIdx.x + (blocks - 1LL) * p.team >= gridDim.x) return;
   const int R = p.unit_rows, rows = a.z, values = rows * (D / 4);
   int ways = 1;
   while (ways < blocks && 2 * ways * values <= THREADS) ways *= 2;
   const int way = ways == 1 ? 0 : (int)threadIdx.x / values;
-  auto slot_of = [&](int j) { return 2 * (int)blockIdx.x + (j == 0 ? 1 : 2 * j); };
+  auto slot_of = [&](int j) { return 2 * ((int)blockIdx.x + j * p.team) + (j == 0 ? 1 : 0); };
   for (int i0 = blockIdx.y * THREADS; i0 < values; i0 += gridDim.y * THREADS) {
     // half a chunk of 8 columns of a row
     const int i = ways == 1 ? i0 + (int)threadIdx.x : (int)threadIdx.x - way * values;
@@ -145,6 +145,15 @@ bool make_q_map(CUtensorMap* m, const void* q, int cols, int heads, int rows, in
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Blocks of a team: a divisor of the KV heads, the largest up to 8 that leaves few blocks (a
+// fiftieth) without a team.
+int team_of(int Hkv, int num_ctas) {
+  int team = 1;
+  for (int t = 2; t <= 8; ++t)
+    if (Hkv % t == 0 && t <= num_ctas && num_ctas % t <= num_ctas / 50) team = t;
+  return team;
+}
+
 // Packed rows of a unit, by the rows that a request is expected to have.
 int unit_rows_of(int g, int max_nodes) {
   const long long rows = (long long)g * max_nodes;
@@ -243,6 +252,8 @@ extern "C" int cp_attn_tree(const void* q, int64_t q_row_stride, int64_t q_head_
   p.lse = lse;
   int64_t o_at, l_at, bytes;
   plan_sizes(Hq, Hkv, dv, max_nodes, num_ctas, &p.unit_rows, &o_at, &l_at, &bytes);
+  p.team = team_of(Hkv, num_ctas);
+  p.teams = num_ctas / p.team;
   p.cut = static_cast<int4*>(workspace);
   p.ws_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + o_at);
   p.ws_l = reinterpret_cast<float*>(static_cast<char*>(workspace) + l_at);

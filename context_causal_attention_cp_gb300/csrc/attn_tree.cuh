@@ -1,16 +1,18 @@
 // Attention over a paged cache (cp_attn_tree): its work list and launch parameters.
 //
 // A unit is a KV head of a request and up to `unit_rows` of its packed rows (new row i, head
-// j of the KV head's group, at i*g + j).  The units' KV tiles of 128 keys, by request, head,
-// row tile and key, form one line, which is cut into equal shares, one a thread block.  The
-// blocks find their shares themselves, from the lengths on the device: a scan over the requests
-// in each block, then a walk.  So a launch depends on no length, and a captured graph serves
-// every step.
+// j of the KV head's group, at i*g + j).  A team of blocks takes one unit each of as many KV
+// heads that lie side by side, and walks the same keys: a cache row holds all heads' parts, and
+// so what DRAM opens for one head is read for the others while it is open.  The units' KV tiles
+// of 128 keys, by request, heads, row tile and key, form one line, which is cut into equal
+// shares, one a team.  The blocks find their shares themselves, from the lengths on the
+// device: a scan over the requests in each block, then a walk.  So a launch depends on no
+// length, and a captured graph serves every step.
 //
 // A unit inside one share is finished by its block.  One that is cut leaves a partial (O, L)
-// in the workspace for each of its blocks: a block has at most two, its first piece (slot 2c,
-// when the unit began in an earlier block) and its last (slot 2c + 1, when it began here and
-// goes on).  The block where a cut unit begins describes it for the merge.
+// in the workspace for each of its blocks, c, c + team, ...: a block has at most two, its first
+// piece (slot 2c, when the unit began in an earlier share) and its last (slot 2c + 1, when it
+// began here and goes on).  The block where a cut unit begins describes it for the merge.
 #pragma once
 #include <cstdint>
 
@@ -25,6 +27,7 @@ struct TreeParams {
   int Hq, Hkv, g;
   uint32_t g_mul, g_shift;  // see group_div
   int unit_rows;
+  int team, teams;  // blocks of a team, teams
   const __nv_bfloat16* q;
   long long q_row, q_head;
   const float *ks, *vs;
@@ -82,12 +85,12 @@ __device__ __forceinline__ int row_tiles(const TreeParams& p, const TreeReq& r) 
   return (int)(((long long)r.T * p.g + p.unit_rows - 1) / p.unit_rows);
 }
 __device__ __forceinline__ long long req_cost(const TreeParams& p, const TreeReq& r) {
-  return r.T == 0 ? 0 : (long long)row_tiles(p, r) * p.Hkv * num_tiles(r.L + r.T);
+  return r.T == 0 ? 0 : (long long)row_tiles(p, r) * (p.Hkv / p.team) * num_tiles(r.L + r.T);
 }
 
 // Where a block's share begins.
 struct TreeStart {
-  long long at, end, b0;  // the share, and the place of request b's first tile
+  long long first, at, end, b0;  // the share, and the place of request b's first tile
   long long share;
   int b;
 };
@@ -119,8 +122,9 @@ __device__ __forceinline__ TreeStart tree_start(const TreeParams& p, long long* 
     total += sums[w];
   }
   TreeStart s;
-  s.share = max(1LL, (total + gridDim.x - 1) / gridDim.x);
-  s.at = s.share * blockIdx.x;
+  s.share = max(1LL, (total + p.teams - 1) / p.teams);
+  s.first = s.share * (blockIdx.x / p.team);
+  s.at = s.first;
   s.end = min(total, s.at + s.share);
   before += upto - sum;
   if (s.at >= before && s.at < before + sum)
@@ -155,7 +159,7 @@ struct TreeWalk {
   TreeStart s;
   TreeReq r, ahead;
   long long w0;  // place of the unit at hand
-  int tiles, rts, kv_head, rt;
+  int tiles, rts, heads, rt;  // heads: of the team, their number
   __device__ __forceinline__ TreeReq load(const TreeParams& p, int b) const {
     bool bad;
     return b < p.num_reqs ? load_req(p, b, bad) : TreeReq{0, 0, 0};
@@ -166,7 +170,7 @@ struct TreeWalk {
   }
   __device__ __forceinline__ TreeWalk(const TreeParams& p, const TreeStart& start) : s(start) {
     tiles = rts = 1;
-    kv_head = rt = 0;
+    heads = rt = 0;
     w0 = 0;
     if (s.at >= s.end) return;
     r = load(p, s.b);
@@ -174,8 +178,8 @@ struct TreeWalk {
     take(p);
     const long long unit = (s.at - s.b0) / tiles;
     w0 = s.b0 + unit * tiles;
-    kv_head = (int)(unit / rts);
-    rt = (int)(unit - (long long)kv_head * rts);
+    heads = (int)(unit / rts);
+    rt = (int)(unit - (long long)heads * rts);
   }
   __device__ __forceinline__ bool next(const TreeParams& p, TreePiece& pc) {
     while (s.at < s.end) {
@@ -183,24 +187,23 @@ struct TreeWalk {
       pc.T = r.T;
       pc.L = r.L;
       pc.b = s.b;
-      pc.kv_head = kv_head;
+      pc.kv_head = heads * p.team + (int)blockIdx.x % p.team;
       pc.r0 = rt * p.unit_rows;
       pc.rows = (int)min((long long)p.unit_rows, (long long)r.T * p.g - pc.r0);
       pc.keys = p.mask ? r.L + r.T : r.L + group_div(p, pc.r0 + pc.rows - 1) + 1;
       const int nt = num_tiles(pc.keys);
       pc.t0 = (int)(s.at - w0);
       pc.tiles = (int)min((long long)nt, s.end - w0) - pc.t0;
-      const long long first = s.share * blockIdx.x;  // of the share
-      const bool here = w0 >= first, cut = w0 + nt > s.end;
+      const bool here = w0 >= s.first, cut = w0 + nt > s.end;
       pc.slot = here && !cut ? -1 : 2 * (int)blockIdx.x + (here ? 1 : 0);
-      pc.blocks = here && cut ? (int)((w0 + nt - 1) / s.share) - (int)blockIdx.x + 1 : 0;
+      pc.blocks = here && cut ? (int)((w0 + nt - 1) / s.share - s.first / s.share) + 1 : 0;
       // on to the next unit
       s.at = min(s.end, w0 + tiles);
       w0 += tiles;
       if (++rt == rts) {
         rt = 0;
-        if (++kv_head == p.Hkv && s.at < s.end) {
-          kv_head = 0;
+        if (++heads == p.Hkv / p.team && s.at < s.end) {
+          heads = 0;
           do {
             ++s.b;
             r = ahead;

@@ -48,7 +48,10 @@ struct TreeCfg {
   static constexpr int kMl = kWarps * 8 * NQ * 8;
   static constexpr int kFixed = 2 * kQ + kJoin + kMl + (int)sizeof(Pieces) + (2 * kMaxStages + 4) * 8 + 64 + 256 + 1024;
   static constexpr int kFit = (232448 - kFixed) / (kTile + kScales);
-  static constexpr int kStages = kFit < kMaxStages ? kFit : kMaxStages;
+  // With two teams a multiple of 4: K and V of the tiles n, n + kStages / 2, ... share slots, and
+  // then one team has them all, so that its warps see every phase of their barriers.
+  static constexpr int kMost = kFit < kMaxStages ? kFit : kMaxStages;
+  static constexpr int kStages = kTeams == 2 ? kMost / 4 * 4 : kMost;
   static constexpr int kScaleOff = kStages * kTile;
   static constexpr int kQOff = kScaleOff + kStages * kScales;
   static constexpr int kJoinOff = kQOff + 2 * kQ;
@@ -256,8 +259,6 @@ __device__ __forceinline__ bool Warp<D, QUANT, NQ>::piece(const TreeParams& p, c
     }
   }
   int ev = -126;  // (e4m3) exponent of O
-  // A warp waits for every place of the ring in its order, the other team's, too, so that it
-  // sees all phases of the barriers.
   auto wait_k = [&](int n) {
     const int place = k_place<false>(n);
     return wait_warp(full + place % NS, (place / NS) & 1, abort, p.timeout_ns);
@@ -277,7 +278,6 @@ __device__ __forceinline__ bool Warp<D, QUANT, NQ>::piece(const TreeParams& p, c
     }
   };
   int t = kTeams == 1 ? 0 : (n0 ^ team) & 1;  // the team's first tile
-  if (t == 1) ok = ok && wait_k(n0) && wait_v(n0);
   if (t < pc.tiles) {
     ok = ok && wait_k(n0 + t);
     if (ok) {
@@ -289,7 +289,6 @@ __device__ __forceinline__ bool Warp<D, QUANT, NQ>::piece(const TreeParams& p, c
     const int n = n0 + t, v_slot = v_place<false>(n) % NS, at = tile0 + t * BN + key0;
     const bool more = t + kTeams < pc.tiles;
     ok = wait_v(n);
-    if (kTeams == 2 && t + 1 < pc.tiles) ok = ok && wait_k(n + 1) && wait_v(n + 1);
     if (more) ok = ok && wait_k(n + kTeams);
     if (!ok) break;
     const bool work = at < pc.keys, next_work = more && at + kTeams * BN < pc.keys;

@@ -528,3 +528,27 @@ def test_refusals_of_the_binding():
     s.page = 24
     with pytest.raises(L.CpAttnError):
         s.call(q, kb, kb, 0.1)
+
+
+@KINDS
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("nodes", [1, 3, 12, 40])
+def test_long_batches_again_and_again(nodes, d, quant):
+    """Many pieces and tiles a block, all of its warps and rings going round many times, at
+    rates that memory sets: no wait runs out, and every call gives the same bits."""
+    B, Hq, Hkv = 40, 32, 32 if nodes == 1 else 8
+    rng = random.Random(20)
+    kv = [rng.randint(0, 4000) for _ in range(B)]
+    s = Step(20, [nodes] * B, kv, 16)
+    q, k, v, scales, _, _ = make(20, s.N, 64, Hq, Hkv, d, quant)
+    big = lambda t: t.repeat(-(-s.rows // 64), 1, 1)[: s.rows].contiguous()  # noqa: E731
+    k, v = (big(t.view(torch.uint8)).view(t.dtype) if quant else big(t) for t in (k, v))
+    scales = {n: x.repeat(1, -(-s.rows // 64))[:, : s.rows].contiguous() for n, x in scales.items()}
+    status = cpa.new_status()
+    ws = cpa.alloc_tree_workspace(Hq, Hkv, d, nodes)
+    first = None
+    for _ in range(12):
+        o, lse, _ = s.call(q, k, v, 0.1, workspace=ws, status=status, **scales)
+        first = (o, lse) if first is None else first
+        assert torch.equal(o, first[0]) and torch.equal(lse, first[1])
+    cpa.check_status(status)
