@@ -6,6 +6,7 @@ shared object is missing or does not export a symbol, loading raises.
 
 import ctypes
 import os
+import struct
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libcpattn.so")
 
@@ -56,6 +57,11 @@ class SharedPlanInfo(ctypes.Structure):
                 ("num_q_rows", "Hq", "Hkv", "num_ctas", "num_units", "num_pieces", "num_entries",
                  "kv_rows", "budget")] + [("ws_rows", i64), ("table_ints", i64)]
 
+
+# Arguments that go as one structure, packed in its order (which leaves no padding inside).
+ROPE_ARGS = struct.Struct("@6P9q6i")            # cp_rope_args_t
+KV_APPEND_ARGS = struct.Struct("@7P9q7i")       # cp_kv_append_args_t
+ATTN_TREE_ARGS = struct.Struct("@13P9q13if")    # cp_attn_tree_args_t
 
 # name -> (restype, argtypes); must match include/cpattn.h
 SIGNATURES = {
@@ -113,16 +119,12 @@ SIGNATURES = {
                              vp, i64, i64, vp, i64, i32, i32, i32, ctypes.c_float, vp, i32, vp,
                              vp, i64, vp, vp]),
     "cp_rope_table": (i32, [vp, vp, i32, vp]),
-    "cp_rope": (i32, [ctypes.POINTER(RopeInfo), vp, i64, i32, vp, i64, i64, i32, vp, i64, i64, vp,
-                      i64, i64, i32, vp, i64, i64, i32, i32, i32, vp, vp]),
-    "cp_kv_append": (i32, [ctypes.POINTER(RopeInfo), vp, i64, vp, i64, i64, vp, i64, i64, i32, i32,
-                           i32, i32, i32, vp, ctypes.POINTER(KvCodes), ctypes.POINTER(KvCodes),
-                           i32, vp, i64, i64, i32, vp, i64, i64, vp, vp]),
+    "cp_rope": (i32, [ctypes.POINTER(RopeInfo), ctypes.c_char_p, vp]),
+    "cp_kv_append": (i32, [ctypes.POINTER(RopeInfo), ctypes.POINTER(KvCodes),
+                           ctypes.POINTER(KvCodes), ctypes.c_char_p, vp]),
     "cp_tree_layout": (i32, [vp, vp, i32, vp, i64, i32, i32, vp, i32, i32, vp, vp, vp, vp, vp]),
     "cp_tree_workspace_size": (i32, [i32, i32, i32, i32, i32, ctypes.POINTER(i64)]),
-    "cp_attn_tree": (i32, [vp, i64, i64, i32, vp, i64, i64, vp, vp, i64, i64, vp, i64, i32, vp,
-                           i64, i32, i32, vp, vp, i32, vp, i32, i32, i32, i32, i32,
-                           ctypes.c_float, i32, i32, vp, i32, vp, vp, i64, vp, vp]),
+    "cp_attn_tree": (i32, [ctypes.c_char_p, vp]),
     "cp_attn_debug": (i32, [i32, ctypes.c_longlong]),
     "cp_status_string": (ctypes.c_char_p, [i32]),
 }

@@ -755,7 +755,8 @@ def _vector(t, name, dtype, n, index):
         return None
     if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != index:
         _bad(t, name, dtype, index)
-    if t.dim() != 1 or t.shape[0] < n or not t.is_contiguous():
+    shape = t.shape
+    if len(shape) != 1 or shape[0] < n or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous, 1-D, with at least {n} entries")
     return t.data_ptr()
 
@@ -1137,26 +1138,29 @@ def _positions(rope, positions, n, index):
     if not isinstance(positions, torch.Tensor) or positions.dtype is not torch.int32 or \
             positions.get_device() != index:
         _bad(positions, "positions", torch.int32, index)
-    shape = positions.shape
-    if shape != (rope.axes, n) and not (rope.axes == 1 and shape == (n,)):
-        raise ValueError(f"positions must be [{rope.axes}, {n}], got {tuple(shape)}")
-    if n > 1 and positions.stride(-1) != 1:
+    shape, axes = positions.shape, rope.axes
+    if shape != (axes, n) and not (axes == 1 and shape == (n,)):
+        raise ValueError(f"positions must be [{axes}, {n}], got {tuple(shape)}")
+    strides = positions.stride()
+    if strides[-1] != 1 and n > 1:
         raise ValueError("positions needs a contiguous last dim")
-    return positions.data_ptr(), max(positions.stride(0), n) if rope.axes > 1 else n
+    return positions.data_ptr(), max(strides[0], n) if axes > 1 else n
 
 
 def _rotated(x, out, name, dtype, n, d, index, stream):
-    """Check rows that are rotated, and their output (made when None); (output, arguments)."""
+    """Check rows that are rotated, and their output (made when None); the output, and both's
+    heads, address and strides."""
     if not isinstance(x, torch.Tensor) or x.dim() != 3:
         raise ValueError(f"{name} must be a CUDA tensor [rows, heads, dim]")
-    shape = (n, x.shape[1], d)
+    H = x.shape[1]
+    shape = (n, H, d)
     rs, hs = _new_rows(x, name, dtype, shape, index)
     if out is None:
         out = _empty(shape, dtype, x.device, stream)
     ors, ohs = _new_rows(out, "out_" + name, dtype, shape, index)
-    if out.numel() and ((n > 1 and ors == 0) or (shape[1] > 1 and ohs == 0)):
+    if (n > 1 and ors == 0 and H) or (H > 1 and ohs == 0 and n):
         raise ValueError(f"out_{name} needs a place for each element")
-    return out, (x.data_ptr(), rs, hs, shape[1], out.data_ptr(), ors, ohs)
+    return out, H, x.data_ptr(), rs, hs, out.data_ptr(), ors, ohs
 
 
 def cp_rope(rope: Rope, q, k=None, positions=None, *, inverse=False, out_q=None, out_k=None,
@@ -1178,12 +1182,13 @@ def cp_rope(rope: Rope, q, k=None, positions=None, *, inverse=False, out_q=None,
         raise ValueError("q needs at least one head")
     dtype = torch.float32 if q.dtype is torch.float32 else torch.bfloat16
     at, axis_stride = _positions(rope, positions, n, index)
-    out_q, qa = _rotated(q, out_q, "q", dtype, n, d, index, stream)
-    ka = (None, 0, 0, 0, None, 0, 0)
+    out_q, _, qp, qrs, qhs, op, ors, ohs = _rotated(q, out_q, "q", dtype, n, d, index, stream)
+    Hk = kp = krs = khs = okp = okrs = okhs = 0
     if k is not None:
-        out_k, ka = _rotated(k, out_k, "k", dtype, n, d, index, stream)
-    _call(index, stream, L.load().cp_rope, "cp_rope", rope._of(index), at, axis_stride, bool(inverse),
-          *qa, *ka, dtype is torch.float32, n, d, _vector(status, "status", torch.int32, 1, index))
+        out_k, Hk, kp, krs, khs, okp, okrs, okhs = _rotated(k, out_k, "k", dtype, n, d, index, stream)
+    _call(index, stream, L.load().cp_rope, "cp_rope", rope._of(index), L.ROPE_ARGS.pack(
+        qp, kp, op, okp, at, _vector(status, "status", torch.int32, 1, index) or 0, qrs, qhs, krs, khs,
+        ors, ohs, okrs, okhs, axis_stride, n, Hq, Hk, d, dtype is torch.float32, bool(inverse)))
     return out_q, out_k
 
 
@@ -1230,38 +1235,39 @@ def cp_kv_append(cache, k, v=None, slots=None, *, rope: Optional[Rope] = None, p
     dtype = torch.float32 if k.dtype is torch.float32 else torch.bfloat16
     n = k.shape[0]
     krs, khs = _new_rows(k, "k", dtype, (n, Hkv, d), index)
-    vrs, vhs = (0, 0) if v is None else _new_rows(v, "v", dtype, (n, Hkv, dv), index)
-    at, axis_stride = (None, 0) if rope is None else _positions(rope, positions, n, index)
-    qa = (None, 0, 0, 0, None, 0, 0)
+    vp = vrs = vhs = at = axis_stride = Hq = qp = qrs = qhs = op = ors = ohs = 0
+    if v is not None:
+        vrs, vhs = _new_rows(v, "v", dtype, (n, Hkv, dv), index)
+        vp = v.data_ptr()
+    if rope is not None:
+        at, axis_stride = _positions(rope, positions, n, index)
     if q is not None:
-        out_q, qa = _rotated(q, out_q, "q", dtype, n, d, index, stream)
+        out_q, Hq, qp, qrs, qhs, op, ors, ohs = _rotated(q, out_q, "q", dtype, n, d, index, stream)
     elif out_q is not None:
         raise ValueError("out_q goes with q")
     _call(index, stream, L.load().cp_kv_append, "cp_kv_append",
-          None if rope is None else rope._of(index), at, axis_stride, k.data_ptr(), krs, khs,
-          None if v is None else v.data_ptr(), vrs, vhs, dtype is torch.float32, n, Hkv, d, dv,
-          _vector(slots, "slots", torch.int32, n, index), kc, vc, rows, *qa,
-          _vector(status, "status", torch.int32, 1, index))
+          None if rope is None else rope._of(index), kc, vc, L.KV_APPEND_ARGS.pack(
+              k.data_ptr(), vp, qp, op, at, _vector(slots, "slots", torch.int32, n, index) or 0,
+              _vector(status, "status", torch.int32, 1, index) or 0, krs, khs, vrs, vhs, qrs, qhs, ors,
+              ohs, axis_stride, n, Hkv, d, dv, Hq, rows, dtype is torch.float32))
     return out_q
 
 
 def _batch(q_start, kv_lens, page_table, index):
-    """Check a paged batch's arrays; their arguments up to the table's width."""
-    if not isinstance(kv_lens, torch.Tensor) or kv_lens.dim() != 1:
-        raise ValueError("kv_lens must be a CUDA int32 tensor [requests]")
-    B = kv_lens.shape[0]
-    if not isinstance(page_table, torch.Tensor) or page_table.dtype is not torch.int32 or \
-            page_table.get_device() != index:
-        _bad(page_table, "page_table", torch.int32, index)
-    if page_table.dim() != 2 or page_table.shape[0] != B or \
-            (page_table.shape[1] > 1 and B and page_table.stride(1) != 1):
-        raise ValueError(f"page_table must be [{B}, pages] with a contiguous last dim")
-    width = page_table.shape[1]
-    if not isinstance(q_start, torch.Tensor) or q_start.dim() != 1 or q_start.shape[0] != B + 1:
-        raise ValueError(f"q_start must be a CUDA int32 tensor [{B + 1}]")
-    return (_vector(q_start, "q_start", torch.int32, B + 1, index),
-            _vector(kv_lens, "kv_lens", torch.int32, B, index), B, page_table.data_ptr(),
-            page_table.stride(0) if B > 1 else width, width)
+    """Check a paged batch's arrays; their addresses, and the batch's and table's sizes."""
+    for t, name in ((q_start, "q_start"), (kv_lens, "kv_lens"), (page_table, "page_table")):
+        if not isinstance(t, torch.Tensor) or t.dtype is not torch.int32 or t.get_device() != index:
+            _bad(t, name, torch.int32, index)
+    B, width = page_table.shape if page_table.dim() == 2 else (-1, 0)
+    if kv_lens.shape != (B,) or q_start.shape != (B + 1,):
+        raise ValueError("page_table must be [requests, pages], kv_lens [requests] and q_start "
+                         f"[requests + 1], got {tuple(page_table.shape)}, {tuple(kv_lens.shape)} "
+                         f"and {tuple(q_start.shape)}")
+    stride, step = page_table.stride()
+    if (step != 1 and width > 1 and B) or not kv_lens.is_contiguous() or not q_start.is_contiguous():
+        raise ValueError("page_table needs a contiguous last dim, kv_lens and q_start to be contiguous")
+    return (q_start.data_ptr(), kv_lens.data_ptr(), B, page_table.data_ptr(),
+            stride if B > 1 else width, width)
 
 
 def cp_tree_layout(q_start, kv_lens, page_table, page_size, num_rows, *, parents=None,
@@ -1311,8 +1317,14 @@ def _mask_words(mask, n, index):
     return mask.shape[1]
 
 
+_SMS = {}  # of a device, by its index
+
+
 def _tree_ctas(index):
-    return torch.cuda.get_device_properties(index).multi_processor_count
+    n = _SMS.get(index)
+    if n is None:
+        n = _SMS[index] = torch.cuda.get_device_properties(index).multi_processor_count
+    return n
 
 
 def cp_tree_workspace_size(Hq, Hkv, dv, max_nodes, num_ctas) -> int:
@@ -1327,7 +1339,7 @@ def cp_tree_workspace_size(Hq, Hkv, dv, max_nodes, num_ctas) -> int:
 def alloc_tree_workspace(Hq, Hkv, dv, max_nodes=1, *, num_ctas=None, device="cuda") -> torch.Tensor:
     """A workspace of cp_attn_tree, for batches of any lengths."""
     if num_ctas is None:
-        num_ctas = _tree_ctas(device)
+        num_ctas = torch.cuda.get_device_properties(device).multi_processor_count
     return torch.empty(cp_tree_workspace_size(Hq, Hkv, dv, max_nodes, num_ctas), dtype=torch.uint8,
                        device=device)
 
@@ -1374,8 +1386,7 @@ def cp_attn_tree(q, k, v, page_table, page_size, q_start, kv_lens, scale, *, mas
         khs, vhs = d, dv
     if rows <= 1:
         krs, vrs = (Hkv - 1) * khs + d, (Hkv - 1) * vhs + dv
-    ks = vs = None
-    scale_stride = 0
+    ks = vs = scale_stride = 0
     if quant:
         for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
             if not isinstance(t, torch.Tensor) or t.dtype is not torch.float32 or \
@@ -1388,7 +1399,9 @@ def cp_attn_tree(q, k, v, page_table, page_size, q_start, kv_lens, scale, *, mas
             raise ValueError("k_scale and v_scale must have one row stride")
         ks, vs = k_scale.data_ptr(), v_scale.data_ptr()
     at_q, at_len, B, at_table, table_stride, width = _batch(q_start, kv_lens, page_table, index)
-    words = 0 if mask is None else _mask_words(mask, N, index)
+    words = at_mask = 0
+    if mask is not None:
+        words, at_mask = _mask_words(mask, N, index), mask.data_ptr()
     if num_ctas is None:
         num_ctas = _tree_ctas(index)
     if out is None:
@@ -1408,11 +1421,10 @@ def cp_attn_tree(q, k, v, page_table, page_size, q_start, kv_lens, scale, *, mas
         workspace = _empty(cp_tree_workspace_size(Hq, Hkv, dv, max_nodes, num_ctas), torch.uint8,
                            q.device, stream)
     nbytes = workspace.numel()
-    _call(index, stream, L.load().cp_attn_tree, "cp_attn_tree", q.data_ptr(), qrs, qhs, N,
-          k.data_ptr(), krs, khs, ks, v.data_ptr(), vrs, vhs, vs, scale_stride, rows, at_table,
-          table_stride, width, int(page_size), at_q, at_len, B,
-          None if mask is None else mask.data_ptr(), words, Hq, Hkv, d, dv, scale, int(max_nodes),
-          int(num_ctas), out.data_ptr(), f32, lse.data_ptr(),
-          _vector(workspace, "workspace", torch.uint8, 0, index), nbytes,
-          _vector(status, "status", torch.int32, 1, index))
+    _call(index, stream, L.load().cp_attn_tree, "cp_attn_tree", L.ATTN_TREE_ARGS.pack(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), ks, vs, at_table, at_q, at_len, at_mask,
+        out.data_ptr(), lse.data_ptr(), _vector(workspace, "workspace", torch.uint8, 0, index),
+        _vector(status, "status", torch.int32, 1, index) or 0, qrs, qhs, krs, khs, vrs, vhs,
+        scale_stride, table_stride, nbytes, N, rows, width, page_size, B, words, Hq, Hkv, d, dv,
+        max_nodes, num_ctas, f32, scale))
     return out, lse, workspace

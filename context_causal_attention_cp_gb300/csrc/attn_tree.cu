@@ -185,96 +185,102 @@ extern "C" int cp_tree_workspace_size(int Hq, int Hkv, int dv, int max_nodes, in
   return CPATTN_OK;
 }
 
-extern "C" int cp_attn_tree(const void* q, int64_t q_row_stride, int64_t q_head_stride, int num_rows, const void* k,
-                            int64_t k_row_stride, int64_t k_head_stride, const float* k_scales, const void* v,
-                            int64_t v_row_stride, int64_t v_head_stride, const float* v_scales, int64_t scale_stride,
-                            int num_kv_rows, const int32_t* page_table, int64_t table_stride, int max_pages,
-                            int page_size, const int32_t* q_start, const int32_t* kv_lens, int num_reqs,
-                            const int32_t* mask, int mask_words, int Hq, int Hkv, int d, int dv, float scale,
-                            int max_nodes, int num_ctas, void* o, int o_is_fp32, float* lse, void* workspace,
-                            int64_t workspace_bytes, int32_t* status_dev, cudaStream_t stream) {
+extern "C" int cp_attn_tree(const cp_attn_tree_args_t* a, cudaStream_t stream) {
   CPATTN_TRACE("cp_attn_tree");
+  if (!a) return CPATTN_ERR_INVALID_ARG;
   int64_t need = 0;
-  const int rc = cp_tree_workspace_size(Hq, Hkv, dv, max_nodes, num_ctas, &need);
+  const int rc = cp_tree_workspace_size(a->Hq, a->Hkv, a->dv, a->max_nodes, a->num_ctas, &need);
   if (rc != CPATTN_OK) return rc;
-  if (d != dv) return CPATTN_ERR_UNSUPPORTED;
-  if (page_size < 16 || page_size > 65536 || (page_size & (page_size - 1))) return CPATTN_ERR_UNSUPPORTED;
-  if (!(scale > 0.f) || num_rows < 0 || num_kv_rows < 0 || num_reqs < 0 || num_reqs > CPATTN_MAX_REQS ||
-      max_pages < 0 || mask_words < 0 || (mask != nullptr) != (mask_words > 0) ||
-      (k_scales != nullptr) != (v_scales != nullptr) || (num_reqs > 1 && table_stride < max_pages))
+  const int d = a->d, Hkv = a->Hkv, page = a->page_size;
+  if (d != a->dv) return CPATTN_ERR_UNSUPPORTED;
+  if (page < 16 || page > 65536 || (page & (page - 1))) return CPATTN_ERR_UNSUPPORTED;
+  if (!(a->scale > 0.f) || a->num_rows < 0 || a->num_kv_rows < 0 || a->num_reqs < 0 ||
+      a->num_reqs > CPATTN_MAX_REQS || a->max_pages < 0 || a->mask_words < 0 ||
+      (a->mask != nullptr) != (a->mask_words > 0) || (a->k_scales != nullptr) != (a->v_scales != nullptr) ||
+      (a->num_reqs > 1 && a->table_stride < a->max_pages))
     return CPATTN_ERR_INVALID_ARG;
-  if ((long long)num_rows * (Hq / Hkv) > 0x7fffffffLL - CPATTN_SHARED_ROWS) return CPATTN_ERR_TOO_LARGE;
-  if (num_rows == 0 || num_reqs == 0) return CPATTN_OK;  // nothing to write
-  if (!q || !k || !v || !page_table || !q_start || !kv_lens || !o || !lse || !workspace || workspace_bytes < need ||
-      num_kv_rows < page_size || max_pages < 1)
+  if ((long long)a->num_rows * (a->Hq / Hkv) > 0x7fffffffLL - CPATTN_SHARED_ROWS) return CPATTN_ERR_TOO_LARGE;
+  if (a->num_rows == 0 || a->num_reqs == 0) return CPATTN_OK;  // nothing to write
+  if (!a->q || !a->k || !a->v || !a->page_table || !a->q_start || !a->kv_lens || !a->o || !a->lse || !a->workspace ||
+      a->workspace_bytes < need || a->num_kv_rows < page || a->max_pages < 1)
     return CPATTN_ERR_INVALID_ARG;
-  const bool quant = k_scales != nullptr;
+  const bool quant = a->k_scales != nullptr;
   const int64_t per16 = quant ? 16 : 8;  // elements in 16 bytes
-  if (!a16(q) || !a16(k) || !a16(v) || !a16(o) || (reinterpret_cast<uintptr_t>(workspace) & 31u) || q_row_stride % 8 ||
-      q_head_stride % 8 || k_row_stride % per16 || k_head_stride % per16 || v_row_stride % per16 ||
-      v_head_stride % per16)
+  if (!a16(a->q) || !a16(a->k) || !a16(a->v) || !a16(a->o) || (reinterpret_cast<uintptr_t>(a->workspace) & 31u) ||
+      a->q_row_stride % 8 || a->q_head_stride % 8 || a->k_row_stride % per16 || a->k_head_stride % per16 ||
+      a->v_row_stride % per16 || a->v_head_stride % per16)
     return CPATTN_ERR_ALIGNMENT;
-  for (const void* at : {(const void*)k_scales, (const void*)v_scales, (const void*)page_table, (const void*)q_start,
-                         (const void*)kv_lens, (const void*)mask, (const void*)lse, (const void*)status_dev})
+  for (const void* at : {(const void*)a->k_scales, (const void*)a->v_scales, (const void*)a->page_table,
+                         (const void*)a->q_start, (const void*)a->kv_lens, (const void*)a->mask, (const void*)a->lse,
+                         (const void*)a->status_dev})
     if (reinterpret_cast<uintptr_t>(at) & 3u) return CPATTN_ERR_ALIGNMENT;
-  if (q_row_stride < 0 || q_head_stride < 0 || k_head_stride < d || v_head_stride < dv ||
-      k_row_stride < (int64_t)(Hkv - 1) * k_head_stride + d || v_row_stride < (int64_t)(Hkv - 1) * v_head_stride + dv ||
-      (quant && scale_stride < num_kv_rows))
+  if (a->q_row_stride < 0 || a->q_head_stride < 0 || a->k_head_stride < d || a->v_head_stride < d ||
+      a->k_row_stride < (int64_t)(Hkv - 1) * a->k_head_stride + d ||
+      a->v_row_stride < (int64_t)(Hkv - 1) * a->v_head_stride + d || (quant && a->scale_stride < a->num_kv_rows))
     return CPATTN_ERR_INVALID_ARG;
 
   TreeParams p{};
-  p.q_start = q_start;
-  p.kv_lens = kv_lens;
-  p.page_table = page_table;
-  p.mask = mask;
-  p.table_stride = table_stride;
-  p.num_reqs = num_reqs;
-  p.num_rows = num_rows;
-  p.max_pages = max_pages;
-  for (p.log_page = 4; (1 << p.log_page) < page_size; ++p.log_page) {}
-  p.words = mask_words;
-  p.Hq = Hq;
+  p.q_start = a->q_start;
+  p.kv_lens = a->kv_lens;
+  p.page_table = a->page_table;
+  p.mask = a->mask;
+  p.table_stride = a->table_stride;
+  p.num_reqs = a->num_reqs;
+  p.num_rows = a->num_rows;
+  p.max_pages = a->max_pages;
+  for (p.log_page = 4; (1 << p.log_page) < page; ++p.log_page) {}
+  p.words = a->mask_words;
+  p.Hq = a->Hq;
   p.Hkv = Hkv;
-  p.g = Hq / Hkv;
+  p.g = a->Hq / Hkv;
   for (p.g_shift = 0; (1LL << (p.g_shift + 1)) < p.g; ++p.g_shift) {}  // see group_div
   p.g_mul = (uint32_t)((1ULL << (32 + p.g_shift)) / p.g + 1);
-  p.q = static_cast<const __nv_bfloat16*>(q);
-  p.q_row = q_row_stride;
-  p.q_head = q_head_stride;
-  p.ks = k_scales;
-  p.vs = v_scales;
-  p.s_head = scale_stride;
-  p.num_kv_rows = num_kv_rows;
-  p.scale_log2 = scale * kLog2e;
-  p.o = o;
-  p.o_f32 = o_is_fp32 ? 1 : 0;
-  p.o_32 = (reinterpret_cast<uintptr_t>(o) & 31u) == 0;
-  p.lse = lse;
+  p.q = static_cast<const __nv_bfloat16*>(a->q);
+  p.q_row = a->q_row_stride;
+  p.q_head = a->q_head_stride;
+  p.ks = a->k_scales;
+  p.vs = a->v_scales;
+  p.s_head = a->scale_stride;
+  p.num_kv_rows = a->num_kv_rows;
+  p.scale_log2 = a->scale * kLog2e;
+  p.o = a->o;
+  p.o_f32 = a->o_is_fp32 ? 1 : 0;
+  p.o_32 = (reinterpret_cast<uintptr_t>(a->o) & 31u) == 0;
+  p.lse = a->lse;
   int64_t o_at, l_at, bytes;
-  plan_sizes(Hq, Hkv, dv, max_nodes, num_ctas, &p.unit_rows, &o_at, &l_at, &bytes);
-  p.team = team_of(Hkv, num_ctas);
-  p.teams = num_ctas / p.team;
-  p.cut = static_cast<int4*>(workspace);
-  p.ws_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + o_at);
-  p.ws_l = reinterpret_cast<float*>(static_cast<char*>(workspace) + l_at);
-  p.status = status_dev;
+  plan_sizes(a->Hq, Hkv, d, a->max_nodes, a->num_ctas, &p.unit_rows, &o_at, &l_at, &bytes);
+  p.team = team_of(Hkv, a->num_ctas);
+  p.teams = a->num_ctas / p.team;
+  p.cut = static_cast<int4*>(a->workspace);
+  p.ws_o = reinterpret_cast<float*>(static_cast<char*>(a->workspace) + o_at);
+  p.ws_l = reinterpret_cast<float*>(static_cast<char*>(a->workspace) + l_at);
+  p.status = a->status_dev;
   p.timeout_ns = attn_debug().timeout_ns;
   p.withhold_q = attn_debug().withhold_q;
   TreeMaps m;
-  const int whole = std::min(BN, page_size);
   auto map = [&](CUtensorMap* t, const void* base, int64_t hs, int64_t rs, int box_rows) {
-    return make_rows_map(t, base, d, quant, Hkv, num_kv_rows, hs, rs, box_rows);
+    return make_rows_map(t, base, d, quant, Hkv, a->num_kv_rows, hs, rs, box_rows);
   };
-  if (!map(&m.k, k, k_head_stride, k_row_stride, whole) || !map(&m.v, v, v_head_stride, v_row_stride, whole) ||
-      !map(&m.k_tail, k, k_head_stride, k_row_stride, 16) || !map(&m.v_tail, v, v_head_stride, v_row_stride, 16))
+  const int whole = std::min(BN, page);
+  if (!map(&m.k, a->k, a->k_head_stride, a->k_row_stride, whole) ||
+      !map(&m.v, a->v, a->v_head_stride, a->v_row_stride, whole))
     return CPATTN_ERR_CUDA;
+  if (whole > 16) {
+    if (!map(&m.k_tail, a->k, a->k_head_stride, a->k_row_stride, 16) ||
+        !map(&m.v_tail, a->v, a->v_head_stride, a->v_row_stride, 16))
+      return CPATTN_ERR_CUDA;
+  } else {
+    m.k_tail = m.k;
+    m.v_tail = m.v;
+  }
   // (a map wants strides; the slow way takes any)
-  p.q_boxes = !quant && p.unit_rows >= BM && BM % p.g == 0 && q_row_stride > 0 && q_head_stride > 0 &&
-              make_q_map(&m.q, q, d, Hq, num_rows, q_head_stride, q_row_stride, p.g);
-  const int r = p.unit_rows < BM ? launch_tree_small(m, p, d, quant, num_ctas, stream)
-                                 : launch_tree_mma(m, p, d, quant, num_ctas, stream);
+  p.q_boxes = !quant && p.unit_rows >= BM && BM % p.g == 0 && p.q_row > 0 && p.q_head > 0 &&
+              make_q_map(&m.q, a->q, d, a->Hq, a->num_rows, p.q_head, p.q_row, p.g);
+  const int r = p.unit_rows < BM ? launch_tree_small(m, p, d, quant, a->num_ctas, stream)
+                                 : launch_tree_mma(m, p, d, quant, a->num_ctas, stream);
   if (r != CPATTN_OK) return r;
-  return (d == 128 ? launch_merge<128>(p, num_ctas, stream) : launch_merge<64>(p, num_ctas, stream)) == cudaSuccess
+  return (d == 128 ? launch_merge<128>(p, a->num_ctas, stream) : launch_merge<64>(p, a->num_ctas, stream)) ==
+                 cudaSuccess
              ? CPATTN_OK
              : CPATTN_ERR_CUDA;
 }

@@ -14,6 +14,7 @@
 // piece (slot 2c, when the unit began in an earlier share) and its last (slot 2c + 1, when it
 // began here and goes on).  The block where a cut unit begins describes it for the merge.
 #pragma once
+#include <atomic>
 #include <cstdint>
 
 #include "attn_tiles.cuh"
@@ -58,12 +59,19 @@ struct TreeMaps {
   CUtensorMap q;  // with TreeParams::q_boxes
 };
 // Whether a launch of `kern` has the registers that its warps share out (setmaxnreg.inc waits
-// for them): a property of this binary.
+// for them): a property of this binary, kept in `known` (0: not asked, 1: yes, -1: no).
 template <typename... Params>
-inline bool split_covered(void (*kern)(Params...), int threads, int regs) {
-  cudaFuncAttributes fa;
-  return cudaFuncGetAttributes(&fa, kern) == cudaSuccess && fa.numRegs * threads >= regs;
+inline bool split_covered(void (*kern)(Params...), int threads, int regs, std::atomic<int>& known) {
+  int k = known.load(std::memory_order_relaxed);
+  if (k == 0) {
+    cudaFuncAttributes fa;
+    if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess) return false;
+    k = fa.numRegs * threads >= regs ? 1 : -1;
+    known.store(k, std::memory_order_relaxed);
+  }
+  return k > 0;
 }
+
 int launch_tree_small(const TreeMaps& m, const TreeParams& p, int d, bool quant, int num_ctas, cudaStream_t stream);
 // ... and the one on tcgen05 (attn_tree_mma.cu): 128 or 256 rows.
 int launch_tree_mma(const TreeMaps& m, const TreeParams& p, int d, bool quant, int num_ctas, cudaStream_t stream);

@@ -23,6 +23,7 @@
 // would not keep them from the rows that do not see them.  A row that does see one becomes
 // NaN by its sum.
 #include <algorithm>
+#include <atomic>
 #include <climits>
 #include <type_traits>
 
@@ -954,8 +955,8 @@ int launch(const TreeMaps& m, const TreeParams& p, int num_ctas, cudaStream_t st
   using C = MmaCfg<D, QUANT, DUAL>;
   auto kern = attn_tree_mma_kernel<D, QUANT, DUAL>;
   if (!allow_smem(kern, C::kSmemBytes)) return CPATTN_ERR_CUDA;
-  if (!split_covered(kern, C::kThreads, C::kRegsSoftmax * 256 + C::kRegsOther * (C::kThreads - 256)))
-    return CPATTN_ERR_UNSUPPORTED;
+  static std::atomic<int> covered{0};
+  if (!split_covered(kern, C::kThreads, C::kRegsSoftmax * 256 + C::kRegsOther * (C::kThreads - 256), covered)) return CPATTN_ERR_UNSUPPORTED;
   return launch_kernel(kern, (unsigned)num_ctas, C::kThreads, C::kSmemBytes, stream, false, m, p) == cudaSuccess
              ? CPATTN_OK
              : CPATTN_ERR_CUDA;

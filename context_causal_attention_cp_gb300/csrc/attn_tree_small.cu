@@ -22,6 +22,7 @@
 // Codes enter as f16, exact; K's scale multiplies the score, V's is taken relative to the
 // largest that the warp has met (O is rescaled when that grows).
 #include <algorithm>
+#include <atomic>
 
 #include "attn_tree.cuh"
 
@@ -696,7 +697,8 @@ int launch(const TreeMaps& m, const TreeParams& p, int num_ctas, cudaStream_t st
   using C = TreeCfg<D, QUANT, NQ>;
   auto kern = attn_tree_small_kernel<D, QUANT, NQ>;
   if (!allow_smem(kern, C::kSmemBytes)) return CPATTN_ERR_CUDA;
-  if (!split_covered(kern, kThreads, kRegsWork * 256 + kRegsOther * 128)) return CPATTN_ERR_UNSUPPORTED;
+  static std::atomic<int> covered{0};
+  if (!split_covered(kern, kThreads, kRegsWork * 256 + kRegsOther * 128, covered)) return CPATTN_ERR_UNSUPPORTED;
   return launch_kernel(kern, (unsigned)num_ctas, kThreads, C::kSmemBytes, stream, false, m, p) == cudaSuccess
              ? CPATTN_OK
              : CPATTN_ERR_CUDA;

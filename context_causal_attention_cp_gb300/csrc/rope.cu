@@ -380,63 +380,56 @@ extern "C" int cp_rope_table(const double* inv_freq, const int32_t* axis, int pa
   return CPATTN_OK;
 }
 
-extern "C" int cp_rope(const cp_rope_t* rope, const int32_t* positions, int64_t axis_stride, int inverse,
-                       const void* q, int64_t q_row_stride, int64_t q_head_stride, int Hq, void* q_out,
-                       int64_t qo_row_stride, int64_t qo_head_stride, const void* k, int64_t k_row_stride,
-                       int64_t k_head_stride, int Hk, void* k_out, int64_t ko_row_stride,
-                       int64_t ko_head_stride, int x_is_fp32, int num_rows, int d, int32_t* status_dev,
-                       cudaStream_t stream) {
+extern "C" int cp_rope(const cp_rope_t* rope, const cp_rope_args_t* a, cudaStream_t stream) {
   CPATTN_TRACE("cp_rope");
-  if (!rope || num_rows < 0 || Hq < 1 || Hk < 0 || Hq > 1 << 20 || Hk > 1 << 20 || (Hk > 0 && num_rows > 0 && !k))
+  if (!rope || !a || a->num_rows < 0 || a->Hq < 1 || a->Hk < 0 || a->Hq > 1 << 20 || a->Hk > 1 << 20)
     return CPATTN_ERR_INVALID_ARG;
-  if (d < 16 || d > kMaxDim || d % 16) return CPATTN_ERR_UNSUPPORTED;
-  if (!aligned(status_dev, 4)) return CPATTN_ERR_ALIGNMENT;
-  int rc = check_rope(rope, d, positions, axis_stride, num_rows);
+  if (a->d < 16 || a->d > kMaxDim || a->d % 16) return CPATTN_ERR_UNSUPPORTED;
+  if (!aligned(a->status_dev, 4)) return CPATTN_ERR_ALIGNMENT;
+  int rc = check_rope(rope, a->d, a->positions, a->axis_stride, a->num_rows);
   if (rc != CPATTN_OK) return rc;
   RopeParams p{};
-  const bool f32 = x_is_fp32 != 0;
-  rc = rotated_side(&p.side[0], q, q_row_stride, q_head_stride, Hq, q_out, qo_row_stride, qo_head_stride, f32,
-                    num_rows, d, rope);
-  if (rc == CPATTN_OK && Hk > 0)
-    rc = rotated_side(&p.side[1], k, k_row_stride, k_head_stride, Hk, k_out, ko_row_stride, ko_head_stride, f32,
-                      num_rows, d, rope);
-  if (rc != CPATTN_OK || num_rows == 0) return rc;
-  p.positions = positions;
-  p.axis_stride = axis_stride;
-  p.inverse = inverse ? 1 : 0;
-  p.num_rows = num_rows;
-  p.status = status_dev;
+  const bool f32 = a->x_is_fp32 != 0;
+  rc = rotated_side(&p.side[0], a->q, a->q_row_stride, a->q_head_stride, a->Hq, a->q_out, a->qo_row_stride,
+                    a->qo_head_stride, f32, a->num_rows, a->d, rope);
+  if (rc == CPATTN_OK && a->Hk > 0)
+    rc = rotated_side(&p.side[1], a->k, a->k_row_stride, a->k_head_stride, a->Hk, a->k_out, a->ko_row_stride,
+                      a->ko_head_stride, f32, a->num_rows, a->d, rope);
+  if (rc != CPATTN_OK || a->num_rows == 0) return rc;
+  p.positions = a->positions;
+  p.axis_stride = a->axis_stride;
+  p.inverse = a->inverse ? 1 : 0;
+  p.num_rows = a->num_rows;
+  p.status = a->status_dev;
   return launch_rope(p, rope, f32, stream);
 }
 
-extern "C" int cp_kv_append(const cp_rope_t* rope, const int32_t* positions, int64_t axis_stride, const void* k,
-                            int64_t k_row_stride, int64_t k_head_stride, const void* v, int64_t v_row_stride,
-                            int64_t v_head_stride, int x_is_fp32, int num_rows, int Hkv, int d, int dv,
-                            const int32_t* slots, const cp_kv_codes_t* k_cache, const cp_kv_codes_t* v_cache,
-                            int cache_rows, const void* q, int64_t q_row_stride, int64_t q_head_stride, int Hq,
-                            void* q_out, int64_t qo_row_stride, int64_t qo_head_stride, int32_t* status_dev,
-                            cudaStream_t stream) {
+extern "C" int cp_kv_append(const cp_rope_t* rope, const cp_kv_codes_t* k_cache, const cp_kv_codes_t* v_cache,
+                            const cp_kv_append_args_t* a, cudaStream_t stream) {
   CPATTN_TRACE("cp_kv_append");
-  if (num_rows < 0 || cache_rows < 0 || Hkv < 1 || Hkv > 1 << 20 || Hq < 0 || Hq > 1 << 20 || !k_cache ||
-      (v != nullptr && !v_cache) || (num_rows > 0 && !v && v_cache) || (v_cache && !v_cache->scales != !k_cache->scales))
+  if (!a || a->num_rows < 0 || a->cache_rows < 0 || a->Hkv < 1 || a->Hkv > 1 << 20 || a->Hq < 0 || a->Hq > 1 << 20 ||
+      !k_cache || (a->v && !v_cache) || (a->num_rows > 0 && !a->v && v_cache) ||
+      (v_cache && !v_cache->scales != !k_cache->scales))
     return CPATTN_ERR_INVALID_ARG;
-  if (!aligned(slots, 4) || !aligned(status_dev, 4)) return CPATTN_ERR_ALIGNMENT;
-  int rc = rope ? check_rope(rope, d, positions, axis_stride, num_rows) : CPATTN_OK;
+  if (!aligned(a->slots, 4) || !aligned(a->status_dev, 4)) return CPATTN_ERR_ALIGNMENT;
+  int rc = rope ? check_rope(rope, a->d, a->positions, a->axis_stride, a->num_rows) : CPATTN_OK;
   if (rc != CPATTN_OK) return rc;
   RopeParams p{};
-  const bool f32 = x_is_fp32 != 0;
-  rc = cached_side(&p.side[1], k, k_row_stride, k_head_stride, f32, Hkv, d, k_cache, num_rows, cache_rows, rope);
+  const bool f32 = a->x_is_fp32 != 0;
+  rc = cached_side(&p.side[1], a->k, a->k_row_stride, a->k_head_stride, f32, a->Hkv, a->d, k_cache, a->num_rows,
+                   a->cache_rows, rope);
   if (rc == CPATTN_OK && v_cache)
-    rc = cached_side(&p.side[2], v, v_row_stride, v_head_stride, f32, Hkv, dv, v_cache, num_rows, cache_rows, nullptr);
-  if (rc == CPATTN_OK && Hq > 0)
-    rc = rotated_side(&p.side[0], q, q_row_stride, q_head_stride, Hq, q_out, qo_row_stride, qo_head_stride, f32,
-                      num_rows, d, rope);
-  if (rc != CPATTN_OK || num_rows == 0) return rc;
-  p.positions = positions;
-  p.axis_stride = axis_stride;
-  p.slots = slots;
-  p.num_rows = num_rows;
-  p.cache_rows = cache_rows;
-  p.status = status_dev;
+    rc = cached_side(&p.side[2], a->v, a->v_row_stride, a->v_head_stride, f32, a->Hkv, a->dv, v_cache, a->num_rows,
+                     a->cache_rows, nullptr);
+  if (rc == CPATTN_OK && a->Hq > 0)
+    rc = rotated_side(&p.side[0], a->q, a->q_row_stride, a->q_head_stride, a->Hq, a->q_out, a->qo_row_stride,
+                      a->qo_head_stride, f32, a->num_rows, a->d, rope);
+  if (rc != CPATTN_OK || a->num_rows == 0) return rc;
+  p.positions = a->positions;
+  p.axis_stride = a->axis_stride;
+  p.slots = a->slots;
+  p.num_rows = a->num_rows;
+  p.cache_rows = a->cache_rows;
+  p.status = a->status_dev;
   return launch_rope(p, rope, f32, stream);
 }

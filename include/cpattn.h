@@ -692,16 +692,21 @@ int cp_rope_table(const double* inv_freq, const int32_t* axis, int pairs, int32_
  *     two must not overlap (rows side by side in one buffer of equal row strides do not).
  *     No element of an output may have two places.
  *   d: a multiple of 16, at most 1024, >= first + 2*pairs. */
-int cp_rope(const cp_rope_t* rope, const int32_t* positions, int64_t axis_stride, int inverse,
-            const void* q, int64_t q_row_stride, int64_t q_head_stride, int Hq, void* q_out,
-            int64_t qo_row_stride, int64_t qo_head_stride, const void* k, int64_t k_row_stride,
-            int64_t k_head_stride, int Hk, void* k_out, int64_t ko_row_stride,
-            int64_t ko_head_stride, int x_is_fp32, int num_rows, int d, int32_t* status_dev,
-            cudaStream_t stream);
+typedef struct {
+  const void *q, *k;
+  void *q_out, *k_out;
+  const int32_t* positions;
+  int32_t* status_dev;
+  int64_t q_row_stride, q_head_stride, k_row_stride, k_head_stride;
+  int64_t qo_row_stride, qo_head_stride, ko_row_stride, ko_head_stride;
+  int64_t axis_stride;
+  int32_t num_rows, Hq, Hk, d, x_is_fp32, inverse;
+} cp_rope_args_t;
+int cp_rope(const cp_rope_t* rope, const cp_rope_args_t* args, cudaStream_t stream);
 
 /* Append new rows to a KV cache, K (and Q) rotated on the way.
  *   rope, positions, axis_stride: as in cp_rope; rope NULL: nothing is rotated.
- *   k, v, x_is_fp32, num_rows, Hkv, d, dv, slots: as in cp_kv_quantize (v and v_cache
+ *   k, v, x_is_fp32, num_rows, Hkv, d, dv, slots, cache_rows: as in cp_kv_quantize (v and v_cache
  *     NULL: K alone).  Rows of slots < 0 are padding and skipped.
  *   k_cache, v_cache: codes and scales, written as cp_kv_quantize writes them (from the
  *     rotated fp32 values: K is rounded once); or, with scales NULL (both), bf16 rows at
@@ -709,14 +714,18 @@ int cp_rope(const cp_rope_t* rope, const int32_t* positions, int64_t axis_stride
  *   q: NULL with Hq = 0, or rows [num_rows, Hq, d] of k's type, rotated to q_out as in
  *     cp_rope (padding rows among them).
  * q_out, the caches and the inputs must not overlap (q_out may be q). */
-int cp_kv_append(const cp_rope_t* rope, const int32_t* positions, int64_t axis_stride,
-                 const void* k, int64_t k_row_stride, int64_t k_head_stride, const void* v,
-                 int64_t v_row_stride, int64_t v_head_stride, int x_is_fp32, int num_rows,
-                 int Hkv, int d, int dv, const int32_t* slots, const cp_kv_codes_t* k_cache,
-                 const cp_kv_codes_t* v_cache, int cache_rows, const void* q,
-                 int64_t q_row_stride, int64_t q_head_stride, int Hq, void* q_out,
-                 int64_t qo_row_stride, int64_t qo_head_stride, int32_t* status_dev,
-                 cudaStream_t stream);
+typedef struct {
+  const void *k, *v, *q;
+  void* q_out;
+  const int32_t *positions, *slots;
+  int32_t* status_dev;
+  int64_t k_row_stride, k_head_stride, v_row_stride, v_head_stride;
+  int64_t q_row_stride, q_head_stride, qo_row_stride, qo_head_stride;
+  int64_t axis_stride;
+  int32_t num_rows, Hkv, d, dv, Hq, cache_rows, x_is_fp32;
+} cp_kv_append_args_t;
+int cp_kv_append(const cp_rope_t* rope, const cp_kv_codes_t* k_cache, const cp_kv_codes_t* v_cache,
+                 const cp_kv_append_args_t* args, cudaStream_t stream);
 
 /* ------------------------------------------------------------------------ */
 /* A decode step over a paged cache.  (No counterpart on the source pages: their
@@ -774,15 +783,21 @@ int cp_tree_layout(const int32_t* q_start, const int32_t* kv_lens, int num_reqs,
  * count as zeros; a wait that runs out sets CPATTN_ERR_TIMEOUT.  With any of them, o and lse
  * are not to be used. */
 int cp_tree_workspace_size(int Hq, int Hkv, int dv, int max_nodes, int num_ctas, int64_t* bytes);
-int cp_attn_tree(const void* q, int64_t q_row_stride, int64_t q_head_stride, int num_rows,
-                 const void* k, int64_t k_row_stride, int64_t k_head_stride,
-                 const float* k_scales, const void* v, int64_t v_row_stride,
-                 int64_t v_head_stride, const float* v_scales, int64_t scale_stride,
-                 int num_kv_rows, const int32_t* page_table, int64_t table_stride, int max_pages,
-                 int page_size, const int32_t* q_start, const int32_t* kv_lens, int num_reqs,
-                 const int32_t* mask, int mask_words, int Hq, int Hkv, int d, int dv, float scale,
-                 int max_nodes, int num_ctas, void* o, int o_is_fp32, float* lse, void* workspace,
-                 int64_t workspace_bytes, int32_t* status_dev, cudaStream_t stream);
+typedef struct {
+  const void *q, *k, *v;
+  const float *k_scales, *v_scales;
+  const int32_t *page_table, *q_start, *kv_lens, *mask;
+  void* o;
+  float* lse;
+  void* workspace;
+  int32_t* status_dev;
+  int64_t q_row_stride, q_head_stride, k_row_stride, k_head_stride, v_row_stride, v_head_stride;
+  int64_t scale_stride, table_stride, workspace_bytes;
+  int32_t num_rows, num_kv_rows, max_pages, page_size, num_reqs, mask_words;
+  int32_t Hq, Hkv, d, dv, max_nodes, num_ctas, o_is_fp32;
+  float scale;
+} cp_attn_tree_args_t;
+int cp_attn_tree(const cp_attn_tree_args_t* args, cudaStream_t stream);
 
 /* ------------------------------------------------------------------------ */
 /* Test hook for the failure path of the attention pipeline (no counterpart on
