@@ -15,7 +15,7 @@
 //   warp 10      MMA issuer (one thread): O += P V and the next S = Q K^T of one stream, then
 //                of the other.
 //   warp 11      query rows to shared memory.
-//   warps 12-15  (e4m3 cache) codes to f16 tiles, as in attn_shared.cu.
+//   warps 12-19  (e4m3 cache) codes to f16 tiles, as in attn_shared.cu.
 // Every wait is bounded; all roles walk the block's share on their own (see attn_tree.cuh).
 //
 // Value rows behind the last key, and (among new keys) rows with an infinity or a NaN, become
@@ -24,7 +24,6 @@
 // NaN by its sum.
 #include <algorithm>
 #include <atomic>
-#include <climits>
 #include <type_traits>
 
 #include "attn_tree.cuh"
@@ -33,27 +32,27 @@ namespace cpattn {
 namespace {
 
 constexpr int kKWarp = 8, kVWarp = 9, kMmaWarp = 10, kQWarp = 11, kConvertWarp = 12;
-constexpr int kConvertThreads = 128;
+constexpr int kConvertWarps = 8, kConvertThreads = 32 * kConvertWarps;
 
 constexpr int kPieces = 4;  // in the ring
 using Pieces = PieceRing<kPieces>;
 
 template <int D, bool QUANT, bool DUAL>
 struct MmaCfg {
-  static constexpr int kThreads = QUANT ? 512 : 384;
-  static constexpr int kRegsLaunch = QUANT ? 128 : 168;
-  static constexpr int kRegsSoftmax = 200, kRegsOther = QUANT ? 56 : 104;
+  static constexpr int kThreads = QUANT ? 640 : 384;
+  static constexpr int kRegsLaunch = QUANT ? 96 : 168;
+  static constexpr int kRegsSoftmax = QUANT ? 128 : 200, kRegsOther = QUANT ? 72 : 104;
   static_assert(kRegsSoftmax * 256 + kRegsOther * (kThreads - 256) <= kRegsLaunch * kThreads,
                 "register split exceeds the launch allocation");
   static constexpr int kQTile = BM * D * 2;
   static constexpr int kTile = BN * D * 2;  // a K or V tile of 16-bit elements
   static constexpr int kRawTile = BN * D;   // an e4m3 K or V tile
   static constexpr int kStages = QUANT ? (D == 128 ? 3 : 6) : D == 128 ? 5 : 10;
-  static constexpr int kRawStages = !QUANT ? 0 : D == 64 ? 8 : DUAL ? 4 : 3;
+  static constexpr int kRawStages = !QUANT ? 0 : D == 64 ? 8 : 3;
   static constexpr int kRingOff = 2 * kQTile;
   static constexpr int kRawOff = kRingOff + kStages * kTile;
-  static constexpr int kMulOff = kRawOff + kRawStages * kRawTile;    // f16 factor of each raw row
-  static constexpr int kNoteOff = kMulOff + kRawStages * BN * 2;     // RawNote of each raw tile
+  static constexpr int kScaleOff = kRawOff + kRawStages * kRawTile;  // of each raw row, and (K) of V's
+  static constexpr int kNoteOff = kScaleOff + kRawStages * BN * 8;   // RawNote of each raw tile
   static constexpr int kExpOff = kNoteOff + kRawStages * 16;         // (ek, ev) of tiles n mod 8
   static constexpr int kLiftOff = kExpOff + 64;                      // exponents of query rows, [2][2][BM]
   static constexpr int kMlOff = kLiftOff + (QUANT ? 4 * BM : 0);     // single: (m, l) of each stream's rows
@@ -71,13 +70,20 @@ struct MmaCfg {
 
 // What a producer tells the converters about a raw tile.
 struct RawNote {
-  int live;         // rows up to the unit's end
-  int fresh;        // first row that is a new key
-  int ek;           // of a K tile: its exponent
-  int16_t ev;       // and V's
-  int16_t last;     // of a K tile: the block has no other behind it
+  int live;   // rows up to the unit's end
+  int fresh;  // first row that is a new key
+  int first;  // of its piece and stream
+  int unused;
 };
 static_assert(sizeof(RawNote) == 16, "");
+
+__device__ __forceinline__ void copy_word(uint32_t at, const float* from) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(at), "l"(from) : "memory");
+}
+// Arrives when this lane's copies so far have landed.
+__device__ __forceinline__ void arrive_copies(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
 
 // The MMAs and commits of ptx.cuh, by the lane with `lead` of a whole warp.
 __device__ __forceinline__ void mma_ss_lead(uint32_t lead, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
@@ -148,55 +154,69 @@ __device__ __forceinline__ void bar_named(int id, int threads) {
 
 // S of a tile to P, for the rows of a warp (one a lane): see softmax_tile in attn_shared.cu.
 // vis: the keys that the row sees (masked: not all); o_scale: what O is multiplied by besides.
+// Over codes S goes through the registers twice, by halves, for its maximum and for P: the
+// converters have the registers that a whole row would take.  (P lies over columns of S that
+// are done.)
 template <int D, bool QUANT>
 __device__ __forceinline__ void softmax_row(uint32_t s_addr, uint32_t o_addr, bool masked, const uint32_t (&vis)[4],
                                             bool has_o, float o_scale, float sl2, float& m_run, float& m_use,
                                             float& l_run) {
-  float x[BN];
-  {
-    uint32_t v[BN];
+  constexpr int kParts = QUANT ? 2 : 1, kCols = BN / kParts;
+  float x[kCols];
+  auto load = [&](int part) {
+    uint32_t v[kCols];
 #pragma unroll
-    for (int q = 0; q < BN / 32; ++q) tmem_ld32p(s_addr + q * 32, v + q * 32);
+    for (int q = 0; q < kCols / 32; ++q) tmem_ld32p(s_addr + part * kCols + q * 32, v + q * 32);
     tmem_wait_ld();
 #pragma unroll
-    for (int c = 0; c < BN; ++c) x[c] = __uint_as_float(v[c]);
-  }
-  if (masked) {
+    for (int c = 0; c < kCols; ++c) x[c] = __uint_as_float(v[c]);
+    if (masked) {
 #pragma unroll
-    for (int c = 0; c < BN; ++c)
-      if (!((vis[c >> 5] >> (c & 31)) & 1u)) x[c] = -INFINITY;
-  }
-  float mx0 = x[0], mx1 = x[1], mx2 = x[2], mx3 = x[3];
+      for (int c = 0; c < kCols; ++c)
+        if (!((vis[(part * kCols + c) >> 5] >> (c & 31)) & 1u)) x[c] = -INFINITY;
+    }
+  };
+  float top = -INFINITY;
 #pragma unroll
-  for (int c = 4; c + 8 <= BN; c += 8) {
-    mx0 = fmax3(mx0, x[c], x[c + 1]);
-    mx1 = fmax3(mx1, x[c + 2], x[c + 3]);
-    mx2 = fmax3(mx2, x[c + 4], x[c + 5]);
-    mx3 = fmax3(mx3, x[c + 6], x[c + 7]);
+  for (int part = 0; part < kParts; ++part) {
+    load(part);
+    float mx0 = x[0], mx1 = x[1], mx2 = x[2], mx3 = x[3];
+#pragma unroll
+    for (int c = 4; c + 8 <= kCols; c += 8) {
+      mx0 = fmax3(mx0, x[c], x[c + 1]);
+      mx1 = fmax3(mx1, x[c + 2], x[c + 3]);
+      mx2 = fmax3(mx2, x[c + 4], x[c + 5]);
+      mx3 = fmax3(mx3, x[c + 6], x[c + 7]);
+    }
+    mx0 = fmax3(mx0, x[kCols - 4], x[kCols - 3]);
+    mx1 = fmax3(mx1, x[kCols - 2], x[kCols - 1]);
+    top = fmaxf(top, fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)));
   }
-  mx0 = fmax3(mx0, x[BN - 4], x[BN - 3]);
-  mx1 = fmax3(mx1, x[BN - 2], x[BN - 1]);
-  const float mx = fmaf(fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)), sl2, QUANT ? -kF16Lift : 0.f);
+  const float mx = fmaf(top, sl2, QUANT ? -kF16Lift : 0.f);
   const bool move = mx > m_run + kMaxSlack;
   const float m_new = move ? mx : m_run;
   const float m_new_use = (m_new == -INFINITY) ? 0.f : m_new;
   const float alpha = move ? ex2_approx(m_run - m_new_use) : 1.f;
   float sum0 = 0.f, sum1 = 0.f;
 #pragma unroll
-  for (int q = 0; q < BN / 32; ++q) {
-    uint32_t pk[16];
+  for (int part = 0; part < kParts; ++part) {
+    if (kParts > 1) load(part);
 #pragma unroll
-    for (int c = 0; c < 32; c += 2) {
-      float a, b;
-      ffma2(a, b, x[q * 32 + c], x[q * 32 + c + 1], sl2, sl2, -m_new_use, -m_new_use);
-      a = ex2_approx(a);
-      b = ex2_approx(b);
-      fadd2(sum0, sum1, sum0, sum1, a, b);
-      // P in 16 bits, the second product's operand type: off by at most 2^-8 (bf16) or
-      // 2^-11 (f16) of each weight; l sums the unrounded values
-      pk[c >> 1] = QUANT ? pack_f16x2(a, b) : pack_bf16x2(a, b);
+    for (int q = 0; q < kCols / 32; ++q) {
+      uint32_t pk[16];
+#pragma unroll
+      for (int c = 0; c < 32; c += 2) {
+        float a, b;
+        ffma2(a, b, x[q * 32 + c], x[q * 32 + c + 1], sl2, sl2, -m_new_use, -m_new_use);
+        a = ex2_approx(a);
+        b = ex2_approx(b);
+        fadd2(sum0, sum1, sum0, sum1, a, b);
+        // P in 16 bits, the second product's operand type: off by at most 2^-8 (bf16) or
+        // 2^-11 (f16) of each weight; l sums the unrounded values
+        pk[c >> 1] = QUANT ? pack_f16x2(a, b) : pack_bf16x2(a, b);
+      }
+      tmem_st16(s_addr + part * (kCols / 2) + q * 16, pk);
     }
-    tmem_st16(s_addr + q * 16, pk);
   }
   l_run = l_run * alpha + (sum0 + sum1);
   const bool need = has_o && (move || o_scale != 1.f);
@@ -264,7 +284,6 @@ attn_tree_mma_kernel(const __grid_constant__ TreeMaps maps, const TreeParams p) 
   uint64_t* p_full = s_full + 2;
   uint64_t* o_full = p_full + 2;
   uint64_t* bar_drain = o_full + 2;
-  uint16_t* raw_mul = reinterpret_cast<uint16_t*>(smem + C::kMulOff);
   RawNote* raw_note = reinterpret_cast<RawNote*>(smem + C::kNoteOff);
   int2* tile_exp = reinterpret_cast<int2*>(smem + C::kExpOff);
   int8_t* q_lift = reinterpret_cast<int8_t*>(smem + C::kLiftOff);
@@ -298,7 +317,7 @@ attn_tree_mma_kernel(const __grid_constant__ TreeMaps maps, const TreeParams p) 
       mbar_init(empty + i, 1);
     }
     for (int i = 0; i < C::kRawStages; ++i) {
-      mbar_init(raw_full + i, 2);  // the TMA copies and the factors
+      mbar_init(raw_full + i, 33);  // the TMA copies, with the note, and each lane's scales
       mbar_init(raw_empty + i, kConvertThreads);
     }
     for (int s = 0; s < 2; ++s) {
@@ -340,49 +359,32 @@ attn_tree_mma_kernel(const __grid_constant__ TreeMaps maps, const TreeParams p) 
       const int whole_log = min(7, p.log_page);
       TileLoader<kPieces> w(pieces);
       int n = 0;
-      int ev0 = 0, ev1 = 0;  // (e4m3) exponent of each stream's V rows
       bool ok = true;
-      for (bool more = w.next(p, abort_flag); more;) {
-        const int live = w.live(), log = w.log_box(p), mine = w.row, kvh = w.pc.kv_head, fresh = w.pc.L - w.key0();
-        const bool first = w.t <= (DUAL ? 0 : 1);  // of its piece and stream
+      for (bool more = w.next(p, abort_flag); more; ++n) {
+        const int live = w.live(), log = w.log_box(p), mine = w.row, kvh = w.pc.kv_head;
         const int place = is_v ? v_place<!DUAL>(n) : k_place<!DUAL>(n), slot = place % kSt;
         ok = wait_warp(emptyb + slot, ((place / kSt) & 1) ^ 1, abort_flag, p.timeout_ns);
         if (!ok) break;
+        if (QUANT && lane == 0) raw_note[slot] = RawNote{live, w.pc.L - w.key0(), w.t <= (DUAL ? 0 : 1), 0};
         copy_tile<kChunks, kLine>(is_v ? &maps.v : &maps.k, is_v ? &maps.v_tail : &maps.k_tail, ring + slot * kBytes,
                                   fullb + slot, kvh, mine, live, log, whole_log);
-        more = w.next(p, abort_flag);
         if constexpr (QUANT) {
-          // the rows' scales as f16 factors relative to the tile's largest (K), or to the
-          // largest that the stream has met in the piece (V)
-          float sc[4], mv = 0.f;
+          const uint32_t at = smem_u32(smem + C::kScaleOff + slot * BN * 8) + lane * 4;
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
             const int key = x * 32 + lane;
             const int row = __shfl_sync(0xffffffffu, mine, key >> log) + (key & ((1 << log) - 1));
-            const bool in = key < live && row < p.num_kv_rows;
-            const long long at = (long long)kvh * p.s_head + row;
-            sc[x] = in ? __ldg((is_v ? p.vs : p.ks) + at) : 0.f;
-            mv = fmaxf(mv, is_v ? sc[x] : in ? __ldg(p.vs + at) : 0.f);
+            if (key < live && row < p.num_kv_rows) {
+              const long long from = (long long)kvh * p.s_head + row;
+              copy_word(at + x * 128, (is_v ? p.vs : p.ks) + from);
+              if (!is_v) copy_word(at + BN * 4 + x * 128, p.vs + from);
+            }
           }
-          float mk = fmaxf(fmaxf(sc[0], sc[1]), fmaxf(sc[2], sc[3]));
-          // (scales are not negative: their bits order as integers)
-          mk = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mk)));
-          mv = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mv)));
-          const bool second = !DUAL && (n & 1);
-          int ev = second ? ev1 : ev0;
-          ev = first ? exponent_of(mv) : max(ev, exponent_of(mv));
-          if (second) ev1 = ev;
-          else ev0 = ev;
-          const int e = is_v ? ev : exponent_of(mk);
-          const float inv = exp2_int(-e);
-#pragma unroll
-          for (int x = 0; x < 4; ++x) raw_mul[slot * BN + x * 32 + lane] = (uint16_t)pack_f16x2(sc[x] * inv, 0.f);
-          if (lane == 0) raw_note[slot] = RawNote{live, fresh, e, (int16_t)ev, (int16_t)!more};
-          __syncwarp();
-          if (lane == 0) mbar_arrive(fullb + slot);
+          arrive_copies(fullb + slot);
         }
-        ++n;
+        more = w.next(p, abort_flag);
       }
+      if (QUANT) asm volatile("cp.async.wait_all;" ::: "memory");
       ok = ok && w.ok;
       if (lane == 0) {
         issued[is_v ? 1 : 0] = n;
@@ -653,7 +655,8 @@ attn_tree_mma_kernel(const __grid_constant__ TreeMaps maps, const TreeParams p) 
     }
     if constexpr (QUANT) if (warp >= kConvertWarp) {
       // --------------------------------------------------- codes to f16 tiles --
-      // Warp w has rows 32w .. 32w+31 of every tile; of a row, lane l has 8 codes of each 64.
+      // Warp w has rows 16w .. 16w+15 of every tile; of a row, lane l has 8 codes of each 64.
+      constexpr int kMine = BN / kConvertWarps;  // rows of a warp
       const int w = warp - kConvertWarp;
       const int rl = lane >> 3, cl = lane & 7;  // row of four, 8-code chunk
       const uint32_t swz[2] = {(uint32_t)((cl ^ rl) << 4), (uint32_t)((cl ^ (rl + 4)) << 4)};
@@ -663,15 +666,12 @@ attn_tree_mma_kernel(const __grid_constant__ TreeMaps maps, const TreeParams p) 
       for (int x = 0; x < 2; ++x)
 #pragma unroll
         for (int h = 0; h < kHalves; ++h)
-          from[x][h] = code_at<D>(w * 32 + rl + 4 * x, h * 4 + (cl >> 1)) + (cl & 1) * 8;
+          from[x][h] = code_at<D>(w * kMine + rl + 4 * x, h * 4 + (cl >> 1)) + (cl & 1) * 8;
       bool ok = true;
-      int tiles = INT_MAX;  // known when the last K tile has come
-      {
-        TreePiece pc;
-        ok = pieces.get(0, pc, abort_flag, p.timeout_ns);
-        if (pc.tiles == 0) tiles = 0;
-      }
-      for (int place = 0; ok && (tiles == INT_MAX || (tiles > 0 && place <= v_place<!DUAL>(tiles - 1))); ++place) {
+      // The KV tiles of the pieces so far; all: there are no more.
+      int tiles = 0, piece = 0, ev_k[2] = {0, 0}, ev_v[2] = {0, 0};
+      bool all = false;
+      for (int place = 0; ok; ++place) {
         bool is_v;
         int n;
         if (DUAL) {
@@ -681,41 +681,75 @@ attn_tree_mma_kernel(const __grid_constant__ TreeMaps maps, const TreeParams p) 
           is_v = place > 0 && !(place & 1);
           n = is_v ? (place - 2) >> 1 : (place + 1) >> 1;
         }
-        if (!is_v && n >= tiles) continue;
+        while (!all && n >= tiles && ok) {
+          TreePiece pc;
+          ok = pieces.get(piece++, pc, abort_flag, p.timeout_ns);
+          tiles += pc.tiles;
+          all = pc.tiles == 0;
+        }
+        if (!ok || (n >= tiles && (is_v || DUAL))) break;
+        if (n >= tiles) {  // (the place behind the last V but one)
+          if (tiles == 0) break;
+          continue;
+        }
         const int raw = place % C::kRawStages, slot = place % NS;
         ok = wait_warp2(empty + slot, ((place / NS) & 1) ^ 1, raw_full + raw, (place / C::kRawStages) & 1, abort_flag,
                         p.timeout_ns);
         if (!ok) break;
         const RawNote note = raw_note[raw];
         const uint8_t* src = smem + C::kRawOff + raw * C::kRawTile;
-        // rows of this warp that become zeros
-        uint32_t dead = note.live >= w * 32 + 32 ? 0u : note.live <= w * 32 ? ~0u : ~0u << (note.live - w * 32);
-        if (!is_v) {
-          if (note.last) tiles = n + 1;
-          if (w == 0 && lane == 0) tile_exp[n & 7] = make_int2(note.ek, note.ev);
-        } else if (note.fresh < BN) {  // new keys: a NaN's row
-          bool bad = false;
+        const float* scales = reinterpret_cast<const float*>(smem + C::kScaleOff + raw * BN * 8);
+        // Exponents: K's factors are relative to the tile's largest scale, V's to the largest
+        // that the stream has met in the piece (scales are not negative: their bits order as
+        // integers)
+        float mx = 0.f, mv = 0.f;
 #pragma unroll
-          for (int ch = 0; ch < D / 16; ++ch) {
-            const uint4 v = *reinterpret_cast<const uint4*>(src + code_at<D>(w * 32 + lane, ch));
-            bad = bad || __vcmpeq4(v.x & 0x7F7F7F7Fu, 0x7F7F7F7Fu) || __vcmpeq4(v.y & 0x7F7F7F7Fu, 0x7F7F7F7Fu) ||
-                  __vcmpeq4(v.z & 0x7F7F7F7Fu, 0x7F7F7F7Fu) || __vcmpeq4(v.w & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+        for (int x = 0; x < 4; ++x)
+          if (x * 32 + lane < note.live) {
+            mx = fmaxf(mx, scales[x * 32 + lane]);
+            if (!is_v) mv = fmaxf(mv, scales[BN + x * 32 + lane]);
           }
-          const uint32_t word = __ballot_sync(0xffffffffu, bad && w * 32 + lane >= note.fresh) & ~dead;
-          if (lane == 0) bad_slot[slot * 4 + w] = word;
-          dead |= word;
+        const int most = exponent_of(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mx))));
+        const int strm = DUAL ? 0 : n & 1;
+        int e = most;
+        // rows of this warp that become zeros
+        uint32_t dead = note.live >= (w + 1) * kMine ? 0u : note.live <= w * kMine ? ~0u : ~0u << (note.live - w * kMine);
+        if (!is_v) {
+          const int v = exponent_of(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mv))));
+          int& ev = strm ? ev_k[1] : ev_k[0];
+          ev = note.first ? v : max(ev, v);
+          if (w == 0 && lane == 0) tile_exp[n & 7] = make_int2(e, ev);
+        } else {
+          int& ev = strm ? ev_v[1] : ev_v[0];
+          ev = note.first ? most : max(ev, most);
+          e = ev;
+          if (note.fresh < BN) {  // new keys: a NaN's row
+            bool bad = false;
+            const int row = w * kMine + lane / 2;  // two lanes to a row
+#pragma unroll
+            for (int ch = 0; ch < D / 32; ++ch) {
+              const uint4 v = *reinterpret_cast<const uint4*>(src + code_at<D>(row, (lane & 1) * (D / 32) + ch));
+              bad = bad || __vcmpeq4(v.x & 0x7F7F7F7Fu, 0x7F7F7F7Fu) || __vcmpeq4(v.y & 0x7F7F7F7Fu, 0x7F7F7F7Fu) ||
+                    __vcmpeq4(v.z & 0x7F7F7F7Fu, 0x7F7F7F7Fu) || __vcmpeq4(v.w & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+            }
+            const uint32_t word =
+                __reduce_or_sync(0xffffffffu, bad && row >= note.fresh ? 1u << (lane / 2) : 0u) & ~dead;
+            if (lane == 0) reinterpret_cast<uint16_t*>(bad_slot)[slot * kConvertWarps + w] = (uint16_t)word;
+            dead |= word;
+          }
         }
+        const float inv = exp2_int(-e);
         dead >>= rl;
-        const uint16_t* mul = raw_mul + raw * BN + w * 32 + rl;
-        uint8_t* dst = smem + C::kRingOff + slot * C::kTile + (w * 32 + rl) * 128;
+        const float* mul = scales + w * kMine + rl;
+        uint8_t* dst = smem + C::kRingOff + slot * C::kTile + (w * kMine + rl) * 128;
         // loads of a batch before its stores: the compiler cannot tell them apart
 #pragma unroll
-        for (int r0 = 0; r0 < 32; r0 += 4 * kBatch) {
+        for (int r0 = 0; r0 < kMine; r0 += 4 * kBatch) {
           uint2 v[kBatch][kHalves];
           uint32_t m[kBatch];
 #pragma unroll
           for (int x = 0; x < kBatch; ++x) {
-            m[x] = mul[r0 + 4 * x];
+            m[x] = pack_f16x2(mul[r0 + 4 * x] * inv, 0.f);
 #pragma unroll
             for (int h = 0; h < kHalves; ++h)
               v[x][h] = *reinterpret_cast<const uint2*>(src + from[x & 1][h] + (r0 + 4 * (x & ~1)) * D);
@@ -725,7 +759,10 @@ attn_tree_mma_kernel(const __grid_constant__ TreeMaps maps, const TreeParams p) 
             for (int x = 0; x < kBatch; ++x)
 #pragma unroll
               for (int h = 0; h < kHalves; ++h)
-                if ((dead >> (r0 + 4 * x)) & 1u) v[x][h] = make_uint2(0, 0);
+                if ((dead >> (r0 + 4 * x)) & 1u) {
+                  v[x][h] = make_uint2(0, 0);
+                  m[x] = 0;
+                }
           }
 #pragma unroll
           for (int x = 0; x < kBatch; ++x)
