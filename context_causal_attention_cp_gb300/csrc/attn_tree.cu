@@ -241,6 +241,7 @@ extern "C" int cp_attn_tree(const cp_attn_tree_args_t* a, cudaStream_t stream) {
   p.ks = a->k_scales;
   p.vs = a->v_scales;
   p.s_head = a->scale_stride;
+  p.scales_16 = a16(a->k_scales) && a16(a->v_scales) && (a->scale_stride % 4 == 0 || Hkv == 1);
   p.num_kv_rows = a->num_kv_rows;
   p.scale_log2 = a->scale * kLog2e;
   p.o = a->o;

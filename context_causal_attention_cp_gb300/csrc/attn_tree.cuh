@@ -33,6 +33,7 @@ struct TreeParams {
   long long q_row, q_head;
   const float *ks, *vs;
   long long s_head;
+  int scales_16;  // 16 keys' scales begin at 16-byte boundaries
   int num_kv_rows;
   float scale_log2;
   void* o;
@@ -264,60 +265,92 @@ __device__ __forceinline__ void put_cut(const TreeParams& p, const TreePiece& pc
   p.cut[2 * blockIdx.x + 1] = make_int4(blocks, 0, 0, 0);
 }
 
-// Cache row of key `key` of request b (key within the request's pages).  A page outside the
-// cache gives a row behind it, which the TMA reads as zeros.
-__device__ __forceinline__ int cache_row(const TreeParams& p, int b, int key) {
-  const int page = __ldg(p.page_table + b * p.table_stride + (key >> p.log_page));
-  if ((uint32_t)page >= (uint32_t)(p.num_kv_rows >> p.log_page)) {
-    set_status(p.status, CPATTN_ERR_RANGE);
-    return p.num_kv_rows;
+// A KV tile for its loader.  The lane's box is whole pages, or 16 rows of a unit's end.
+struct LoadTile {
+  int live;          // keys of the unit from the tile's first on, at most BN; 0: no tile
+  int log;           // rows of a box (log2)
+  int page, at;      // of the lane's box: entry of the page table, row in the page
+  int kv_head, fresh, t;  // fresh: the first row that is a new key; t: number in the piece
+  // Cache row of the lane's box; of a page outside the cache a row behind it, which TMA reads
+  // as zeros.
+  __device__ __forceinline__ int row(const TreeParams& p) const {
+    return (uint32_t)page < (uint32_t)(p.num_kv_rows >> p.log_page) ? (page << p.log_page) + at : p.num_kv_rows;
   }
-  return (page << p.log_page) + (key & ((1 << p.log_page) - 1));
-}
-
-// The KV tiles of a list of pieces as their loader goes through them: the lane's box of a tile is
-// whole pages, or 16 rows of a unit's end, and is looked up a tile ahead, so that the page
-// table's latency is not waited for.
+};
+// The KV tiles of the block's pieces.  A loader takes a tile ahead of the one that it copies,
+// and looks at its page table's words only then: under load they are a thousand cycles away
+// (e4m3 tiles of 16-row pages: 142 -> 123 us a decode step of 64).
 template <int N>
 struct TileLoader {
   PieceRing<N>& ring;
   TreePiece pc;
-  int i = -1, t = 0, row = 0;  // piece, its tile, cache row of the lane's box
-  bool ok = true;
+  int i = -1, t = 0;  // piece, its tile
+  bool ok = true, end = false;
   __device__ __forceinline__ explicit TileLoader(PieceRing<N>& r) : ring(r) { pc.tiles = 0; }
-  __device__ __forceinline__ int key0() const { return (pc.t0 + t) * BN; }
-  __device__ __forceinline__ int live() const { return min(BN, pc.keys - key0()); }
-  __device__ __forceinline__ int log_box(const TreeParams& p) const {
-    return live() > BN - 16 ? min(7, p.log_page) : 4;
-  }
-  // The next tile; false when there is none (or a wait ran out: ok).
-  __device__ __forceinline__ bool next(const TreeParams& p, const volatile int* abort) {
+  __device__ __forceinline__ LoadTile next(const TreeParams& p, const volatile int* abort) {
+    LoadTile x;
+    x.live = x.log = x.page = x.at = x.kv_head = x.fresh = x.t = 0;
+    if (end) return x;
     if (++t >= pc.tiles) {
       ok = ring.get(++i, pc, abort, p.timeout_ns);
-      if (pc.tiles == 0) return false;
+      end = pc.tiles == 0;
+      if (end) return x;
       t = 0;
     }
-    const int at = (threadIdx.x & 31) << log_box(p);
-    row = at < live() ? cache_row(p, pc.b, key0() + at) : 0;
-    return true;
+    const int key0 = (pc.t0 + t) * BN, mine = threadIdx.x & 31;
+    x.live = min(BN, pc.keys - key0);
+    x.log = x.live > BN - 16 ? min(7, p.log_page) : 4;
+    const int key = key0 + (mine << x.log);
+    if ((mine << x.log) < x.live) x.page = __ldg(p.page_table + pc.b * p.table_stride + (key >> p.log_page));
+    x.at = key & ((1 << p.log_page) - 1);
+    x.kv_head = pc.kv_head;
+    x.fresh = pc.L - key0;
+    x.t = t;
+    return x;
   }
 };
-// Starts the copies of a tile: kChunks boxes of 64 columns across, by the lanes that hold the
+// Starts the copies of a tile, kChunks boxes of 64 columns across, by the lanes that hold the
 // rows (one lane that starts them all takes 2900 cycles for 8 pages, these 2200).
 template <int kChunks, int kLine>
-__device__ __forceinline__ void copy_tile(const CUtensorMap* whole, const CUtensorMap* tail, uint8_t* dst, uint64_t* bar,
-                                          int kv_head, int row, int live, int log, int whole_log) {
-  const int lane = threadIdx.x & 31, boxes = (live + (1 << log) - 1) >> log;
-  if (lane == 0) mbar_arrive_expect_tx(bar, (boxes << log) * kLine * kChunks);
+__device__ __forceinline__ void copy_tile(const TreeParams& p, const CUtensorMap* whole, const CUtensorMap* tail,
+                                          uint8_t* dst, uint64_t* bar, const LoadTile& x, int row, int whole_log) {
+  const int lane = threadIdx.x & 31, boxes = (x.live + (1 << x.log) - 1) >> x.log;
+  if (lane == 0) mbar_arrive_expect_tx(bar, (boxes << x.log) * kLine * kChunks);
   __syncwarp();
   if (lane < boxes) {
-    const CUtensorMap* tm = log == whole_log ? whole : tail;
+    const CUtensorMap* tm = x.log == whole_log ? whole : tail;
 #pragma unroll
     for (int c = 0; c < kChunks; ++c)
-      tma_load_3d(dst + (c * BN + (lane << log)) * kLine, tm, bar, c * 64, kv_head, row);
+      tma_load_3d(dst + (c * BN + (lane << x.log)) * kLine, tm, bar, c * 64, x.kv_head, row);
+    if (row == p.num_kv_rows) set_status(p.status, CPATTN_ERR_RANGE);
   }
   __syncwarp();
 }
+// The scales of a tile's rows to `at` in shared memory, asynchronously: whole blocks of 16 keys,
+// which lie in a page, or a word a key where their addresses are not aligned.
+__device__ __forceinline__ void copy_scales(const TreeParams& p, const float* scales, const LoadTile& x, int row,
+                                            uint32_t at) {
+  const int lane = threadIdx.x & 31;
+  const float* from = scales + (long long)x.kv_head * p.s_head;
+  if (p.scales_16) {
+    const int key = 16 * (lane >> 2), r = __shfl_sync(0xffffffffu, row, key >> x.log) + (key & ((1 << x.log) - 1));
+    if (key < x.live && r < p.num_kv_rows)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at + lane * 16), "l"(from + r + 4 * (lane & 3))
+                   : "memory");
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int key = i * 32 + lane, r = __shfl_sync(0xffffffffu, row, key >> x.log) + (key & ((1 << x.log) - 1));
+    if (key < x.live && r < p.num_kv_rows)
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(at + key * 4), "l"(from + r) : "memory");
+  }
+}
+// Arrives when this lane's copies so far have landed.
+__device__ __forceinline__ void arrive_copies(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
 // Ring place of K and V of a list's n-th KV tile, in the order of use: K0 V0 K1 V1 ..., or
 // (AHEAD: two streams take turns) K0 K1 V0 K2 V1 ..., where the place behind the last V but
 // one is left out.

@@ -77,14 +77,6 @@ struct RawNote {
 };
 static_assert(sizeof(RawNote) == 16, "");
 
-__device__ __forceinline__ void copy_word(uint32_t at, const float* from) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(at), "l"(from) : "memory");
-}
-// Arrives when this lane's copies so far have landed.
-__device__ __forceinline__ void arrive_copies(uint64_t* bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
-}
-
 // The MMAs and commits of ptx.cuh, by the lane with `lead` of a whole warp.
 __device__ __forceinline__ void mma_ss_lead(uint32_t lead, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
                                             uint32_t accumulate) {
@@ -360,29 +352,25 @@ attn_tree_mma_kernel(const __grid_constant__ TreeMaps maps, const TreeParams p) 
       TileLoader<kPieces> w(pieces);
       int n = 0;
       bool ok = true;
-      for (bool more = w.next(p, abort_flag); more; ++n) {
-        const int live = w.live(), log = w.log_box(p), mine = w.row, kvh = w.pc.kv_head;
-        const int place = is_v ? v_place<!DUAL>(n) : k_place<!DUAL>(n), slot = place % kSt;
+      // (e4m3: a tile two ahead; bf16, where a tile takes longer: one)
+      LoadTile cur = w.next(p, abort_flag), next{}, later{};
+      if (QUANT) next = w.next(p, abort_flag);
+      for (; cur.live; ++n) {
+        if (QUANT) later = w.next(p, abort_flag);
+        const int place = is_v ? v_place<!DUAL>(n) : k_place<!DUAL>(n), slot = place % kSt, row = cur.row(p);
         ok = wait_warp(emptyb + slot, ((place / kSt) & 1) ^ 1, abort_flag, p.timeout_ns);
         if (!ok) break;
-        if (QUANT && lane == 0) raw_note[slot] = RawNote{live, w.pc.L - w.key0(), w.t <= (DUAL ? 0 : 1), 0};
-        copy_tile<kChunks, kLine>(is_v ? &maps.v : &maps.k, is_v ? &maps.v_tail : &maps.k_tail, ring + slot * kBytes,
-                                  fullb + slot, kvh, mine, live, log, whole_log);
+        if (QUANT && lane == 0) raw_note[slot] = RawNote{cur.live, cur.fresh, cur.t <= (DUAL ? 0 : 1), 0};
+        copy_tile<kChunks, kLine>(p, is_v ? &maps.v : &maps.k, is_v ? &maps.v_tail : &maps.k_tail,
+                                  ring + slot * kBytes, fullb + slot, cur, row, whole_log);
         if constexpr (QUANT) {
-          const uint32_t at = smem_u32(smem + C::kScaleOff + slot * BN * 8) + lane * 4;
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const int key = x * 32 + lane;
-            const int row = __shfl_sync(0xffffffffu, mine, key >> log) + (key & ((1 << log) - 1));
-            if (key < live && row < p.num_kv_rows) {
-              const long long from = (long long)kvh * p.s_head + row;
-              copy_word(at + x * 128, (is_v ? p.vs : p.ks) + from);
-              if (!is_v) copy_word(at + BN * 4 + x * 128, p.vs + from);
-            }
-          }
+          const uint32_t at = smem_u32(smem + C::kScaleOff + slot * BN * 8);
+          copy_scales(p, is_v ? p.vs : p.ks, cur, row, at);
+          if (!is_v) copy_scales(p, p.vs, cur, row, at + BN * 4);
           arrive_copies(fullb + slot);
         }
-        more = w.next(p, abort_flag);
+        cur = QUANT ? next : w.next(p, abort_flag);
+        next = later;
       }
       if (QUANT) asm volatile("cp.async.wait_all;" ::: "memory");
       ok = ok && w.ok;

@@ -567,9 +567,6 @@ attn_tree_small_kernel(const __grid_constant__ TreeMaps maps, const TreeParams p
   }
   const TreeStart start = tree_start(p, sums, found);  // (its barriers publish those above)
   TreePiece pc;
-  auto arrive_copies = [&](uint64_t* bar) {  // when this lane's copies so far have landed
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
-  };
   if (warp >= kWarps) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
     if (warp == kWarps || warp == kWarps + 1) {  // K, V
@@ -580,26 +577,22 @@ attn_tree_small_kernel(const __grid_constant__ TreeMaps maps, const TreeParams p
       TileLoader<kPieces> w(pieces);
       int n = 0;
       bool ok = true;
-      for (bool more = w.next(p, abort_flag); more; ++n) {
-        const int live = w.live(), log = w.log_box(p), mine = w.row, kvh = w.pc.kv_head;
-        const int place = is_v ? v_place<false>(n) : k_place<false>(n), slot = place % NS;
+      // (e4m3: a tile two ahead; bf16, where a tile takes longer: one)
+      LoadTile cur = w.next(p, abort_flag), next{}, later{};
+      if (QUANT) next = w.next(p, abort_flag);
+      for (; cur.live; ++n) {
+        if (QUANT) later = w.next(p, abort_flag);
+        const int place = is_v ? v_place<false>(n) : k_place<false>(n), slot = place % NS, row = cur.row(p);
         ok = wait_warp(empty + slot, ((place / NS) & 1) ^ 1, abort_flag, p.timeout_ns);
         if (!ok) break;
-        copy_tile<kChunks, kLine>(is_v ? &maps.v : &maps.k, is_v ? &maps.v_tail : &maps.k_tail, smem + slot * C::kTile,
-                                  full + slot, kvh, mine, live, log, whole_log);
-        more = w.next(p, abort_flag);
+        copy_tile<kChunks, kLine>(p, is_v ? &maps.v : &maps.k, is_v ? &maps.v_tail : &maps.k_tail,
+                                  smem + slot * C::kTile, full + slot, cur, row, whole_log);
         if constexpr (QUANT) {
-          const float* src = (is_v ? p.vs : p.ks) + (long long)kvh * p.s_head;
-          const uint32_t at = smem_u32(smem + C::kScaleOff + slot * C::kScales) + lane * 4;
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const int key = x * 32 + lane;
-            const int row = __shfl_sync(0xffffffffu, mine, key >> log) + (key & ((1 << log) - 1));
-            if (key < live && row < p.num_kv_rows)
-              asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(at + x * 128), "l"(src + row) : "memory");
-          }
+          copy_scales(p, is_v ? p.vs : p.ks, cur, row, smem_u32(smem + C::kScaleOff + slot * C::kScales));
           arrive_copies(full + slot);
         }
+        cur = QUANT ? next : w.next(p, abort_flag);
+        next = later;
       }
       ok = ok && w.ok;
       asm volatile("cp.async.wait_all;" ::: "memory");
