@@ -8,10 +8,11 @@
 // multiplications for its upper 32 bits.  The quarter turn next to it is split off before
 // the rest goes to fp32, so that cos and sin are good to fp32 at any position.
 //
-// One kernel for both calls, an HBM stream: a block takes a few rows, computes their cos and
-// sin once into shared memory (they serve all heads) and then rotates, rounds or quantises
-// the rows' vectors.  L = 2^k lanes share a vector; a lane's item is two 16-byte chunks (of
-// bf16) that hold 8 pairs, or 16 columns that are not rotated.
+// One kernel for both calls, an HBM stream.  L = 2^k lanes share a vector; a lane's item is
+// two 16-byte chunks (of bf16) that hold 8 pairs, or 16 columns that are not rotated.  A
+// group of lanes has U vectors of the block's rows at a time: it starts all their loads,
+// computes its part of the rows' cos and sin (into shared memory: they serve all heads)
+// while these are on their way, and then rotates, rounds or quantises.
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
@@ -30,6 +31,9 @@ constexpr int kThreads = 256;
 constexpr int kMaxDim = 1024;
 constexpr int kMaxCs = 2048;  // cos and sin values of a block's rows
 constexpr int kItem = 16;     // columns of an item
+
+// Vectors that a group of lanes has at a time, as many as 32 to 48 registers hold.
+constexpr int units_at_once(bool f32, int items) { return f32 ? (items == 1 ? 2 : 1) : items == 1 ? 4 : 2; }
 
 struct RopeSide {  // Q, K or V
   const void* x;
@@ -67,24 +71,31 @@ __device__ __forceinline__ float2 cos_sin(int p, uint32_t f_lo, uint32_t f_hi) {
   return make_float2(quarter == 1 || quarter == 2 ? -a : a, quarter >= 2 ? -b : b);
 }
 
-// 8 consecutive elements.
+// 8 consecutive elements as they lie in memory, and in fp32.
 template <bool F32>
-__device__ __forceinline__ void load8(const void* x, long long at, float* f) {
-  if constexpr (F32) {
-    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(x) + at);
-    const float4 a = __ldcs(p), b = __ldcs(p + 1);
-    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
-  } else {
-    const uint4 v = __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(x) + at));
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+struct Raw8 {
+  uint4 v[F32 ? 2 : 1];
+  __device__ __forceinline__ void load(const void* x, long long at) {
+    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(x) + at * (F32 ? 4 : 2));
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      f[2 * i] = __uint_as_float(w[i] << 16);
-      f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    for (int i = 0; i < (F32 ? 2 : 1); ++i) v[i] = __ldcs(p + i);
+  }
+  __device__ __forceinline__ void values(float* f) const {
+#pragma unroll
+    for (int i = 0; i < (F32 ? 2 : 1); ++i) {
+      const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if constexpr (F32) {
+          f[4 * i + j] = __uint_as_float(w[j]);
+        } else {
+          f[2 * j] = __uint_as_float(w[j] << 16);
+          f[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+        }
+      }
     }
   }
-}
+};
 __device__ __forceinline__ void store8_bf16(uint8_t* at, const float* f) {
   *reinterpret_cast<uint4*>(at) = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
                                              pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
@@ -106,106 +117,110 @@ __device__ __forceinline__ void store8_codes(uint8_t* at, const float* f, float 
 // side by side); else (c, c + pairs).
 template <bool F32, bool INTER, int NI>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p) {
-  __shared__ __align__(16) float2 cs[2][kMaxCs];
-  const int L = 1 << p.log_l, lane = threadIdx.x & (L - 1), group = threadIdx.x >> p.log_l;
+  constexpr int U = units_at_once(F32, NI);
+  // cos and sin of pairs 8 j + 2 k, 8 j + 2 k + 1 of row r at [r][k][j]: lanes j side by side
+  __shared__ float4 cs[kMaxCs / 2];
+  const int L = 1 << p.log_l, groups = kThreads >> p.log_l;
+  const int lane = threadIdx.x & (L - 1), group = threadIdx.x >> p.log_l;
   const uint32_t mask = (L == 32 ? 0xffffffffu : (1u << L) - 1u) << (threadIdx.x & 31 & ~(L - 1));
   const int c_rot = INTER ? 8 : p.pairs;  // columns from an item's first chunk to its second
-  int buf = 0;
-  for (long long r0 = (long long)blockIdx.x * p.rows; r0 < p.num_rows; r0 += (long long)gridDim.x * p.rows) {
-    const int rows = (int)min((long long)p.rows, p.num_rows - r0);
-    if (p.pairs > 0) {
-      for (int r = 0; r < rows; ++r)
-        for (int c = threadIdx.x; c < p.pairs; c += kThreads) {
-          const int4 f = __ldg(p.table + c);
-          const bool ok = f.z >= 0 && f.z < p.axes;
-          if (!ok) set_status(p.status, CPATTN_ERR_RANGE);
-          const int at = ok ? __ldg(p.positions + f.z * p.axis_stride + r0 + r) : 0;
-          float2 v = cos_sin(at, (uint32_t)f.x, (uint32_t)f.y);
-          if (p.inverse) v.y = -v.y;
-          cs[buf][r * p.pairs + c] = v;
-        }
+  const int h0 = p.side[0].heads, h1 = h0 + p.side[1].heads, eighths = p.pairs / 8;
+  const long long r0 = (long long)blockIdx.x * p.rows;
+  const int rows = (int)min((long long)p.rows, p.num_rows - r0), units = rows * p.vectors;
+  // unit u: a row, and a head of one of the sides
+  auto side_of = [&](int u, int& r, int& h) -> const RopeSide& {
+    r = u / p.vectors;
+    const int vec = u - r * p.vectors;
+    h = vec < h0 ? vec : vec < h1 ? vec - h0 : vec - h1;
+    return vec < h0 ? p.side[0] : vec < h1 ? p.side[1] : p.side[2];
+  };
+  // the columns of item j's chunks
+  auto columns = [&](const RopeSide& s, int j, int& c0, int& c1) {
+    if (j < s.rotated) {
+      c0 = p.first + j * (INTER ? 16 : 8);
+      c1 = c0 + c_rot;
+    } else {
+      const int n = 2 * (j - s.rotated), skip = 2 * s.rotated, head = p.first / 8;  // chunks rotated, and before them
+      c0 = 8 * (s.rotated == 0 || n < head ? n : n + skip);
+      c1 = 8 * (s.rotated == 0 || n + 1 < head ? n + 1 : n + 1 + skip);
+    }
+  };
+  for (int base = group; base - group < units; base += U * groups) {  // (the same rounds in all threads)
+    Raw8<F32> raw[U][NI][2];
+    int to[U];
+#pragma unroll
+    for (int x = 0; x < U; ++x) {
+      const int u = base + x * groups;
+      to[x] = -1;
+      if (u >= units) continue;
+      int r, h;
+      const RopeSide& s = side_of(u, r, h);
+      const long long row = r0 + r, at = row * s.x_row + h * s.x_head;
+      to[x] = s.cached && p.slots ? __ldg(p.slots + row) : (int)row;
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        const int j = lane + i * L;
+        if (j * kItem >= s.dim) continue;
+        int c0, c1;
+        columns(s, j, c0, c1);
+        raw[x][i][0].load(s.x, at + c0);
+        raw[x][i][1].load(s.x, at + c1);
+      }
+    }
+    if (base == group && p.pairs > 0) {
+      for (int i = threadIdx.x; i < rows * p.pairs; i += kThreads) {
+        const int r = i / p.pairs, c = i - r * p.pairs;
+        const int4 f = __ldg(p.table + c);
+        const bool ok = f.z >= 0 && f.z < p.axes;
+        if (!ok) set_status(p.status, CPATTN_ERR_RANGE);
+        const int at = ok ? __ldg(p.positions + f.z * p.axis_stride + r0 + r) : 0;
+        float2 v = cos_sin(at, (uint32_t)f.x, (uint32_t)f.y);
+        if (p.inverse) v.y = -v.y;
+        reinterpret_cast<float2*>(cs)[(((r * 4 + ((c >> 1) & 3)) * eighths + (c >> 3)) << 1) + (c & 1)] = v;
+      }
       __syncthreads();
     }
-    for (int u = group; u < rows * p.vectors; u += kThreads >> p.log_l) {
-      const int r = u / p.vectors, vec = u - r * p.vectors;
-      const long long row = r0 + r;
-      const int h0 = p.side[0].heads, h1 = h0 + p.side[1].heads;
-      const RopeSide& s = vec < h0 ? p.side[0] : vec < h1 ? p.side[1] : p.side[2];
-      const int h = vec < h0 ? vec : vec < h1 ? vec - h0 : vec - h1;
-      long long to = row;
+#pragma unroll
+    for (int x = 0; x < U; ++x) {
+      const int u = base + x * groups;
+      if (u >= units) continue;
+      int r, h;
+      const RopeSide& s = side_of(u, r, h);
       if (s.cached) {
-        if (p.slots) to = __ldg(p.slots + row);
-        if (to >= p.cache_rows) {
+        if (to[x] >= p.cache_rows) {
           if (lane == 0) set_status(p.status, CPATTN_ERR_RANGE);
-          to = -1;
+          to[x] = -1;
         }
-        if (to < 0) continue;  // (the same in the vector's lanes)
+        if (to[x] < 0) continue;  // (the same in the vector's lanes)
       }
-      const int skip = s.rotated ? 2 * s.rotated : 0, head = p.first / 8;  // chunks rotated, and before them
       float f[NI][kItem];
-      int c0[NI], c1[NI];
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
+        raw[x][i][0].values(f[i]);
+        raw[x][i][1].values(f[i] + 8);
         const int j = lane + i * L;
-        c0[i] = c1[i] = -1;
-        if (j * kItem >= s.dim) continue;
-        if (j < s.rotated) {
-          c0[i] = p.first + j * (INTER ? 16 : 8);
-          c1[i] = c0[i] + c_rot;
-        } else {
-          const int n = 2 * (j - s.rotated);
-          c0[i] = 8 * (n < head ? n : n + skip);
-          c1[i] = 8 * (n + 1 < head ? n + 1 : n + 1 + skip);
-        }
-        const long long at = row * s.x_row + h * s.x_head;
-        load8<F32>(s.x, at + c0[i], f[i]);
-        load8<F32>(s.x, at + c1[i], f[i] + 8);
-      }
+        if (j >= s.rotated) continue;
 #pragma unroll
-      for (int i = 0; i < NI; ++i) {
-        const int j = lane + i * L;
-        if (j >= s.rotated || c0[i] < 0) continue;
-        const float4* t = reinterpret_cast<const float4*>(&cs[buf][r * p.pairs + 8 * j]);
+        for (int k = 0; k < 4; ++k) {
+          const float4 v = cs[(r * 4 + k) * eighths + j];
 #pragma unroll
-        for (int e = 0; e < 8; e += 2) {
-          const float4 v = t[e / 2];
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const float c = x ? v.z : v.x, sn = x ? v.w : v.y;
-            float& a = f[i][INTER ? 2 * (e + x) : e + x];
-            float& b = f[i][INTER ? 2 * (e + x) + 1 : e + x + 8];
+          for (int e = 2 * k; e < 2 * k + 2; ++e) {
+            const float c = e & 1 ? v.z : v.x, sn = e & 1 ? v.w : v.y;
+            float& a = f[i][INTER ? 2 * e : e];
+            float& b = f[i][INTER ? 2 * e + 1 : e + 8];
             const float a0 = a, b0 = b;
             a = a0 * c - b0 * sn;
             b = b0 * c + a0 * sn;
           }
         }
       }
-      uint8_t* const y = s.y + to * s.y_row + h * s.y_head;
-      if (!s.cached) {
-#pragma unroll
-        for (int i = 0; i < NI; ++i) {
-          if (c0[i] < 0) continue;
-          if constexpr (F32) {
-            store8_f32(y + 4 * c0[i], f[i]);
-            store8_f32(y + 4 * c1[i], f[i] + 8);
-          } else {
-            store8_bf16(y + 2 * c0[i], f[i]);
-            store8_bf16(y + 2 * c1[i], f[i] + 8);
-          }
-        }
-      } else if (!s.scales) {
-#pragma unroll
-        for (int i = 0; i < NI; ++i) {
-          if (c0[i] < 0) continue;
-          store8_bf16(y + 2 * c0[i], f[i]);
-          store8_bf16(y + 2 * c1[i], f[i] + 8);
-        }
-      } else {
+      float inv = 1.f;
+      if (s.scales) {
         // the largest finite element; the rotated value is rounded once, to its code
         float a = 0.f;
 #pragma unroll
         for (int i = 0; i < NI; ++i)
-          if (c0[i] >= 0)
+          if ((lane + i * L) * kItem < s.dim)
 #pragma unroll
             for (int e = 0; e < kItem; ++e) {
               const float m = fabsf(f[i][e]);
@@ -213,17 +228,28 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p) {
             }
         for (int o = L >> 1; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(mask, a, o));
         const int e = scale_exponent(a);
-        const float inv = exp2_int(-e);
+        inv = exp2_int(-e);
+        if (lane == 0) s.scales[h * s.s_head + to[x]] = exp2_int(e);
+      }
+      uint8_t* const y = s.y + (s.cached ? (long long)to[x] : r0 + r) * s.y_row + h * s.y_head;
 #pragma unroll
-        for (int i = 0; i < NI; ++i) {
-          if (c0[i] < 0) continue;
-          store8_codes(y + c0[i], f[i], inv);
-          store8_codes(y + c1[i], f[i] + 8, inv);
+      for (int i = 0; i < NI; ++i) {
+        const int j = lane + i * L;
+        if (j * kItem >= s.dim) continue;
+        int c0, c1;
+        columns(s, j, c0, c1);
+        if (s.scales) {
+          store8_codes(y + c0, f[i], inv);
+          store8_codes(y + c1, f[i] + 8, inv);
+        } else if (F32 && !s.cached) {
+          store8_f32(y + 4 * c0, f[i]);
+          store8_f32(y + 4 * c1, f[i] + 8);
+        } else {
+          store8_bf16(y + 2 * c0, f[i]);
+          store8_bf16(y + 2 * c1, f[i] + 8);
         }
-        if (lane == 0) s.scales[h * s.s_head + to] = exp2_int(e);
       }
     }
-    buf ^= 1;  // (the next rows' values go to the other half: one barrier a round is enough)
   }
 }
 
@@ -291,14 +317,14 @@ int launch_rope(RopeParams& p, const cp_rope_t* rope, bool f32, cudaStream_t str
   else if (items > 32) p.log_l = 4, ni = 3;
   else
     for (p.log_l = 0; (1 << p.log_l) < items; ++p.log_l) {}
-  // Rows of a block: enough that its threads have a few vectors each, unless the blocks
-  // would be too few for the SMs.
+  // Rows of a block: what its groups have at a time, unless the blocks would be too few for
+  // the SMs.
   const int groups = kThreads >> p.log_l;
-  int rows = std::max(1, 4 * groups / p.vectors);
-  rows = std::min(rows, std::max(1, p.num_rows / (152 * 4)));
+  int rows = std::max(1, units_at_once(f32, ni) * groups / p.vectors);
+  rows = std::min(rows, std::max(1, p.num_rows / (152 * 2)));
   if (p.pairs > 0) rows = std::max(1, std::min(rows, kMaxCs / p.pairs));
   p.rows = rows;
-  const unsigned grid = (unsigned)std::min<long long>(((long long)p.num_rows + rows - 1) / rows, 152 * 8);
+  const unsigned grid = (unsigned)(((long long)p.num_rows + rows - 1) / rows);
   decltype(&rope_kernel<true, true, 1>) const kerns[2][2][3] = {
       {{rope_kernel<false, false, 1>, rope_kernel<false, false, 2>, rope_kernel<false, false, 3>},
        {rope_kernel<false, true, 1>, rope_kernel<false, true, 2>, rope_kernel<false, true, 3>}},
