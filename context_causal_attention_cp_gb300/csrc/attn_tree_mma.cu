@@ -600,17 +600,25 @@ attn_tree_mma_kernel(const __grid_constant__ TreeMaps maps, const TreeParams p) 
             const int packed = pc.r0 + s * BM + r, node = group_div(p, packed);
             const __nv_bfloat16* src = p.q + (long long)(pc.row0 + node) * p.q_row +
                                        (long long)(pc.kv_head * p.g + packed - node * p.g) * p.q_head + c * 8;
-            const uint32_t at = tile + r * 128 + (((c & 7) ^ (r & 7)) << 4);
-            if constexpr (!QUANT) {
-              asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at), "l"(src) : "memory");
-            } else {
-              // bf16 to f16 times 2^f with 2^f max|q| in [2^14, 2^15)
-              const uint4 v = __ldg(reinterpret_cast<const uint4*>(src));
-              uint32_t x[4] = {v.x, v.y, v.z, v.w};
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(tile + r * 128 + (((c & 7) ^ (r & 7)) << 4)),
+                         "l"(src)
+                         : "memory");
+          }
+          asm volatile("cp.async.wait_all;" ::: "memory");
+          if constexpr (QUANT) {
+            // each lane's own chunks, in place: bf16 to f16 times 2^f with 2^f max|q| in [2^14, 2^15)
+            const uint32_t group = (kLanes == 32 ? 0u : ((1u << kLanes) - 1u)) << (lane & ~(kLanes - 1));
+#pragma unroll 4
+            for (int r = lane / kLanes; r < rows; r += kRows) {
+              const uint32_t at = tile + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+              uint32_t x[4];
+              asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                           : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+                           : "r"(at)
+                           : "memory");
               uint32_t mx = __vmaxu2(__vmaxu2(x[0] & 0x7FFF7FFFu, x[1] & 0x7FFF7FFFu),
                                      __vmaxu2(x[2] & 0x7FFF7FFFu, x[3] & 0x7FFF7FFFu));
               mx = max(mx & 0xFFFFu, mx >> 16);
-              const uint32_t group = (kLanes == 32 ? 0u : ((1u << kLanes) - 1u)) << (lane & ~(kLanes - 1));
 #pragma unroll
               for (int o = kLanes / 2; o > 0; o >>= 1) mx = max(mx, __shfl_xor_sync(group, mx, o));
               const int f = min(max(14 - ((int)(mx >> 7) - 127), -126), 126);
@@ -624,7 +632,6 @@ attn_tree_mma_kernel(const __grid_constant__ TreeMaps maps, const TreeParams p) 
               if (c == 0) q_lift[((i & 1) * 2 + s) * BM + r] = (int8_t)f;
             }
           }
-          if constexpr (!QUANT) asm volatile("cp.async.wait_all;" ::: "memory");
           fence_async_shared();
           __syncwarp();
           if (lane == 0 && !p.withhold_q) mbar_arrive(q_full + buf);
