@@ -10,9 +10,9 @@
 //
 // One kernel for both calls, an HBM stream.  L = 2^k lanes share a vector; a lane's item is
 // two 16-byte chunks (of bf16) that hold 8 pairs, or 16 columns that are not rotated.  A
-// group of lanes has U vectors of the block's rows at a time: it starts all their loads,
-// computes its part of the rows' cos and sin (into shared memory: they serve all heads)
-// while these are on their way, and then rotates, rounds or quantises.
+// group of lanes takes vectors of one row, some at a time: it starts their loads, computes
+// its part of the block's cos and sin (into shared memory: they serve all heads) while these
+// are on their way, and then rotates, rounds or quantises.
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
@@ -20,6 +20,7 @@
 #include <cuda_bf16.h>
 
 #include "../../include/cpattn.h"
+#include "attn_common.cuh"
 #include "kv_codes.cuh"
 #include "ptx.cuh"
 #include "trace.h"
@@ -33,17 +34,17 @@ constexpr int kMaxCs = 2048;  // cos and sin values of a block's rows
 constexpr int kItem = 16;     // columns of an item
 
 // Vectors that a group of lanes has at a time, as many as 32 to 48 registers hold.
-constexpr int units_at_once(bool f32, int items) { return f32 ? (items == 1 ? 2 : 1) : items == 1 ? 4 : 2; }
+constexpr int units_at_once(bool f32, int items) { return f32 ? (items == 1 ? 2 : 1) : items == 3 ? 1 : 2; }
 
-struct RopeSide {  // Q, K or V
-  const void* x;
-  long long x_row, x_head;  // elements
-  uint8_t* y;               // codes, or values
-  long long y_row, y_head;  // bytes
-  float* scales;            // codes' scales, or null
+struct RopeSide {  // Q, K or V; strides in 16 bytes
+  const uint8_t* x;
+  uint32_t x_row, x_head;
+  uint8_t* y;  // codes, or values
+  uint32_t y_row, y_head;
+  float* scales;  // codes' scales, or null
   long long s_head;
   int heads, dim;
-  int rotated;  // items that hold pairs (0: none)
+  int rotated;  // whether the table's pairs are
   int cached;   // rows go to their slots, as bf16 or codes; else to their own place, in x's type
 };
 
@@ -54,7 +55,8 @@ struct RopeParams {
   long long axis_stride;
   int pairs, first, axes, inverse;
   const int32_t* slots;
-  int num_rows, cache_rows, vectors, rows, log_l;  // rows: of a block
+  // vectors of a row; rows of a block; 2^log_l lanes have a vector, 2^log_split groups a row
+  int num_rows, cache_rows, vectors, rows, log_l, log_split;
   int32_t* status;
 };
 
@@ -75,8 +77,8 @@ __device__ __forceinline__ float2 cos_sin(int p, uint32_t f_lo, uint32_t f_hi) {
 template <bool F32>
 struct Raw8 {
   uint4 v[F32 ? 2 : 1];
-  __device__ __forceinline__ void load(const void* x, long long at) {
-    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(x) + at * (F32 ? 4 : 2));
+  __device__ __forceinline__ void load(const uint8_t* x) {
+    const uint4* p = reinterpret_cast<const uint4*>(x);
 #pragma unroll
     for (int i = 0; i < (F32 ? 2 : 1); ++i) v[i] = __ldcs(p + i);
   }
@@ -104,94 +106,108 @@ __device__ __forceinline__ void store8_f32(uint8_t* at, const float* f) {
   reinterpret_cast<float4*>(at)[0] = make_float4(f[0], f[1], f[2], f[3]);
   reinterpret_cast<float4*>(at)[1] = make_float4(f[4], f[5], f[6], f[7]);
 }
+__device__ __forceinline__ void fmul2(float& d0, float& d1, float a0, float a1, float b0, float b1) {
+  asm("{\n\t.reg .b64 ra, rb, rd;\n\t"
+      "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+      "mul.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d0), "=f"(d1)
+      : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
 __device__ __forceinline__ void store8_codes(uint8_t* at, const float* f, float inv) {
   uint32_t w[2];
 #pragma unroll
-  for (int j = 0; j < 2; ++j)
-    w[j] = (uint32_t)e4m3x2(f[4 * j] * inv, f[4 * j + 1] * inv) |
-           (uint32_t)e4m3x2(f[4 * j + 2] * inv, f[4 * j + 3] * inv) << 16;
+  for (int j = 0; j < 2; ++j) {
+    float x[4];
+    fmul2(x[0], x[1], f[4 * j], f[4 * j + 1], inv, inv);
+    fmul2(x[2], x[3], f[4 * j + 2], f[4 * j + 3], inv, inv);
+    w[j] = (uint32_t)e4m3x2(x[0], x[1]) | (uint32_t)e4m3x2(x[2], x[3]) << 16;
+  }
   *reinterpret_cast<uint2*>(at) = make_uint2(w[0], w[1]);
 }
 
 // NI: items of a lane.  INTER: pairs are neighbours (a rotated item's chunks then lie
 // side by side); else (c, c + pairs).
 template <bool F32, bool INTER, int NI>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p) {
-  constexpr int U = units_at_once(F32, NI);
-  // cos and sin of pairs 8 j + 2 k, 8 j + 2 k + 1 of row r at [r][k][j]: lanes j side by side
+__global__ void __launch_bounds__(kThreads, NI != 1 || F32 ? 2 : 3) rope_kernel(const RopeParams p) {
+  constexpr int U = units_at_once(F32, NI), kSize = F32 ? 4 : 2;
+  // (c, c', s, s') of pairs 8 j + 2 k, 8 j + 2 k + 1 of row r at [r][k][j]: lanes j side by side
   __shared__ float4 cs[kMaxCs / 2];
-  const int L = 1 << p.log_l, groups = kThreads >> p.log_l;
-  const int lane = threadIdx.x & (L - 1), group = threadIdx.x >> p.log_l;
+  const int L = 1 << p.log_l, lane = threadIdx.x & (L - 1), group = threadIdx.x >> p.log_l;
   const uint32_t mask = (L == 32 ? 0xffffffffu : (1u << L) - 1u) << (threadIdx.x & 31 & ~(L - 1));
-  const int c_rot = INTER ? 8 : p.pairs;  // columns from an item's first chunk to its second
   const int h0 = p.side[0].heads, h1 = h0 + p.side[1].heads, eighths = p.pairs / 8;
   const long long r0 = (long long)blockIdx.x * p.rows;
-  const int rows = (int)min((long long)p.rows, p.num_rows - r0), units = rows * p.vectors;
-  // unit u: a row, and a head of one of the sides
-  auto side_of = [&](int u, int& r, int& h) -> const RopeSide& {
-    r = u / p.vectors;
-    const int vec = u - r * p.vectors;
-    h = vec < h0 ? vec : vec < h1 ? vec - h0 : vec - h1;
-    return vec < h0 ? p.side[0] : vec < h1 ? p.side[1] : p.side[2];
-  };
-  // the columns of item j's chunks
-  auto columns = [&](const RopeSide& s, int j, int& c0, int& c1) {
-    if (j < s.rotated) {
-      c0 = p.first + j * (INTER ? 16 : 8);
-      c1 = c0 + c_rot;
+  const int split = 1 << p.log_split, sub = group & (split - 1), r = group >> p.log_split;
+  const int rows = (int)min((long long)p.rows, p.num_rows - r0);
+  const bool live = r < rows;
+  const uint32_t row = (uint32_t)(r0 + (live ? r : 0));
+  // the row's place in the caches
+  int to = (int)row;
+  if (live && p.slots) to = __ldg(p.slots + row);
+  // byte offsets of the chunks of items in vectors that are rotated (others: 16 columns)
+  int c0[NI], c1[NI];
+#pragma unroll
+  for (int i = 0; i < NI; ++i) {
+    const int j = lane + i * L;
+    if (j < eighths) {
+      c0[i] = p.first + j * (INTER ? 16 : 8);
+      c1[i] = c0[i] + (INTER ? 8 : p.pairs);
     } else {
-      const int n = 2 * (j - s.rotated), skip = 2 * s.rotated, head = p.first / 8;  // chunks rotated, and before them
-      c0 = 8 * (s.rotated == 0 || n < head ? n : n + skip);
-      c1 = 8 * (s.rotated == 0 || n + 1 < head ? n + 1 : n + 1 + skip);
+      const int n = 2 * (j - eighths), head = p.first / 8;  // chunks before the rotated ones
+      c0[i] = 8 * (n < head ? n : n + 2 * eighths);
+      c1[i] = 8 * (n + 1 < head ? n + 1 : n + 1 + 2 * eighths);
     }
+  }
+  // vector vec of a row: a head of one of the sides
+  auto side_of = [&](int vec, uint32_t& h) -> const RopeSide& {
+    const int i = (vec >= h0) + (vec >= h1);
+    h = vec - (i == 0 ? 0 : i == 1 ? h0 : h1);
+    return p.side[i];
   };
-  for (int base = group; base - group < units; base += U * groups) {  // (the same rounds in all threads)
+  constexpr int kKeep = NI == 1 ? 1 : 0;  // a lane's one item: its cos and sin in registers
+  float4 keep[4];
+  for (int base = 0; base < p.vectors; base += U << p.log_split) {  // (the same rounds in all threads)
     Raw8<F32> raw[U][NI][2];
-    int to[U];
 #pragma unroll
     for (int x = 0; x < U; ++x) {
-      const int u = base + x * groups;
-      to[x] = -1;
-      if (u >= units) continue;
-      int r, h;
-      const RopeSide& s = side_of(u, r, h);
-      const long long row = r0 + r, at = row * s.x_row + h * s.x_head;
-      to[x] = s.cached && p.slots ? __ldg(p.slots + row) : (int)row;
+      const int vec = base + (x << p.log_split) + sub;
+      if (!live || vec >= p.vectors) continue;
+      uint32_t h;
+      const RopeSide& s = side_of(vec, h);
+      const uint8_t* at = s.x + (((unsigned long long)row * s.x_row + (unsigned long long)h * s.x_head) << 4);
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
         const int j = lane + i * L;
         if (j * kItem >= s.dim) continue;
-        int c0, c1;
-        columns(s, j, c0, c1);
-        raw[x][i][0].load(s.x, at + c0);
-        raw[x][i][1].load(s.x, at + c1);
+        raw[x][i][0].load(at + (s.rotated ? c0[i] : j * kItem) * kSize);
+        raw[x][i][1].load(at + (s.rotated ? c1[i] : j * kItem + 8) * kSize);
       }
     }
-    if (base == group && p.pairs > 0) {
+    if (base == 0 && p.pairs > 0) {
       for (int i = threadIdx.x; i < rows * p.pairs; i += kThreads) {
-        const int r = i / p.pairs, c = i - r * p.pairs;
+        const int at_row = i / p.pairs, c = i - at_row * p.pairs;
         const int4 f = __ldg(p.table + c);
         const bool ok = f.z >= 0 && f.z < p.axes;
         if (!ok) set_status(p.status, CPATTN_ERR_RANGE);
-        const int at = ok ? __ldg(p.positions + f.z * p.axis_stride + r0 + r) : 0;
-        float2 v = cos_sin(at, (uint32_t)f.x, (uint32_t)f.y);
-        if (p.inverse) v.y = -v.y;
-        reinterpret_cast<float2*>(cs)[(((r * 4 + ((c >> 1) & 3)) * eighths + (c >> 3)) << 1) + (c & 1)] = v;
+        const int at = ok ? __ldg(p.positions + f.z * p.axis_stride + r0 + at_row) : 0;
+        const float2 v = cos_sin(at, (uint32_t)f.x, (uint32_t)f.y);
+        float* const dst = reinterpret_cast<float*>(cs + (at_row * 4 + ((c >> 1) & 3)) * eighths + (c >> 3)) + (c & 1);
+        dst[0] = v.x;
+        dst[2] = p.inverse ? -v.y : v.y;
       }
       __syncthreads();
+      if (kKeep && live && lane < eighths)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) keep[k] = cs[(r * 4 + k) * eighths + lane];
     }
 #pragma unroll
     for (int x = 0; x < U; ++x) {
-      const int u = base + x * groups;
-      if (u >= units) continue;
-      int r, h;
-      const RopeSide& s = side_of(u, r, h);
-      if (s.cached) {
-        if (to[x] >= p.cache_rows) {
-          if (lane == 0) set_status(p.status, CPATTN_ERR_RANGE);
-          to[x] = -1;
-        }
-        if (to[x] < 0) continue;  // (the same in the vector's lanes)
+      const int vec = base + (x << p.log_split) + sub;
+      if (!live || vec >= p.vectors) continue;
+      uint32_t h;
+      const RopeSide& s = side_of(vec, h);
+      if (s.cached && (uint32_t)to >= (uint32_t)p.cache_rows) {  // (the same in the vector's lanes)
+        if (to >= 0 && lane == 0) set_status(p.status, CPATTN_ERR_RANGE);
+        continue;
       }
       float f[NI][kItem];
 #pragma unroll
@@ -199,54 +215,61 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p) {
         raw[x][i][0].values(f[i]);
         raw[x][i][1].values(f[i] + 8);
         const int j = lane + i * L;
-        if (j >= s.rotated) continue;
+        if (!s.rotated || j >= eighths) continue;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const float4 v = cs[(r * 4 + k) * eighths + j];
-#pragma unroll
-          for (int e = 2 * k; e < 2 * k + 2; ++e) {
-            const float c = e & 1 ? v.z : v.x, sn = e & 1 ? v.w : v.y;
-            float& a = f[i][INTER ? 2 * e : e];
-            float& b = f[i][INTER ? 2 * e + 1 : e + 8];
-            const float a0 = a, b0 = b;
-            a = a0 * c - b0 * sn;
-            b = b0 * c + a0 * sn;
-          }
+          const float4 v = kKeep ? keep[k] : cs[(r * 4 + k) * eighths + j];
+          float& a0 = f[i][INTER ? 4 * k : 2 * k];
+          float& a1 = f[i][INTER ? 4 * k + 2 : 2 * k + 1];
+          float& b0 = f[i][INTER ? 4 * k + 1 : 2 * k + 8];
+          float& b1 = f[i][INTER ? 4 * k + 3 : 2 * k + 9];
+          float ac0, ac1, bc0, bc1;
+          fmul2(ac0, ac1, a0, a1, v.x, v.y);
+          fmul2(bc0, bc1, b0, b1, v.x, v.y);
+          ffma2(bc0, bc1, a0, a1, v.z, v.w, bc0, bc1);
+          ffma2(a0, a1, b0, b1, -v.z, -v.w, ac0, ac1);
+          b0 = bc0;
+          b1 = bc1;
         }
       }
       float inv = 1.f;
       if (s.scales) {
         // the largest finite element; the rotated value is rounded once, to its code
-        float a = 0.f;
+        auto largest = [&](bool finite) {
+          float a = 0.f;
 #pragma unroll
-        for (int i = 0; i < NI; ++i)
-          if ((lane + i * L) * kItem < s.dim)
+          for (int i = 0; i < NI; ++i)
+            if ((lane + i * L) * kItem < s.dim)
 #pragma unroll
-            for (int e = 0; e < kItem; ++e) {
-              const float m = fabsf(f[i][e]);
-              a = fmaxf(a, m < INFINITY ? m : 0.f);
-            }
-        for (int o = L >> 1; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(mask, a, o));
+              for (int e = 0; e < kItem; ++e) {
+                const float m = fabsf(f[i][e]);
+                a = fmaxf(a, !finite || m < INFINITY ? m : 0.f);
+              }
+          for (int o = L >> 1; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(mask, a, o));
+          return a;
+        };
+        float a = largest(false);
+        if (a == INFINITY) a = largest(true);  // (fmaxf leaves a NaN out by itself)
         const int e = scale_exponent(a);
         inv = exp2_int(-e);
-        if (lane == 0) s.scales[h * s.s_head + to[x]] = exp2_int(e);
+        if (lane == 0) s.scales[h * s.s_head + to] = exp2_int(e);
       }
-      uint8_t* const y = s.y + (s.cached ? (long long)to[x] : r0 + r) * s.y_row + h * s.y_head;
+      const uint32_t at_row = s.cached ? (uint32_t)to : row;
+      uint8_t* const y = s.y + (((unsigned long long)at_row * s.y_row + (unsigned long long)h * s.y_head) << 4);
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
         const int j = lane + i * L;
         if (j * kItem >= s.dim) continue;
-        int c0, c1;
-        columns(s, j, c0, c1);
+        const int y0 = s.rotated ? c0[i] : j * kItem, y1 = s.rotated ? c1[i] : j * kItem + 8;
         if (s.scales) {
-          store8_codes(y + c0, f[i], inv);
-          store8_codes(y + c1, f[i] + 8, inv);
+          store8_codes(y + y0, f[i], inv);
+          store8_codes(y + y1, f[i] + 8, inv);
         } else if (F32 && !s.cached) {
-          store8_f32(y + 4 * c0, f[i]);
-          store8_f32(y + 4 * c1, f[i] + 8);
+          store8_f32(y + 4 * y0, f[i]);
+          store8_f32(y + 4 * y1, f[i] + 8);
         } else {
-          store8_bf16(y + 2 * c0, f[i]);
-          store8_bf16(y + 2 * c1, f[i] + 8);
+          store8_bf16(y + 2 * y0, f[i]);
+          store8_bf16(y + 2 * y1, f[i] + 8);
         }
       }
     }
@@ -264,6 +287,7 @@ int check_rows(const void* x, int64_t row, int64_t head, int size) {
 int check_out_rows(const void* x, int64_t row, int64_t head, int size, int64_t n, int heads, int dim) {
   const int rc = check_rows(x, row, head, size);
   if (rc != CPATTN_OK) return rc;
+  if (n == 0) return CPATTN_OK;
   const bool by_row = (heads == 1 || head >= dim) && (n == 1 || row >= (heads - 1) * head + dim);
   const bool by_head = (n == 1 || row >= dim) && (heads == 1 || head >= (n - 1) * row + dim);
   return by_row || by_head ? CPATTN_OK : CPATTN_ERR_INVALID_ARG;
@@ -317,14 +341,16 @@ int launch_rope(RopeParams& p, const cp_rope_t* rope, bool f32, cudaStream_t str
   else if (items > 32) p.log_l = 4, ni = 3;
   else
     for (p.log_l = 0; (1 << p.log_l) < items; ++p.log_l) {}
-  // Rows of a block: what its groups have at a time, unless the blocks would be too few for
-  // the SMs.
-  const int groups = kThreads >> p.log_l;
-  int rows = std::max(1, units_at_once(f32, ni) * groups / p.vectors);
-  rows = std::min(rows, std::max(1, p.num_rows / (152 * 2)));
-  if (p.pairs > 0) rows = std::max(1, std::min(rows, kMaxCs / p.pairs));
-  p.rows = rows;
-  const unsigned grid = (unsigned)(((long long)p.num_rows + rows - 1) / rows);
+  // Groups of a row: few, since they share its cos and sin, but so many that there are six
+  // blocks for each SM, and that the block's cos and sin fit.
+  const int log_groups = 8 - p.log_l;
+  p.log_split = 0;
+  while (p.log_split < log_groups && (1 << p.log_split) < p.vectors &&
+         ((long long)p.num_rows << p.log_split >> log_groups) < 152 * 6)
+    ++p.log_split;
+  while (p.pairs << (log_groups - p.log_split) > kMaxCs) ++p.log_split;  // (a row has at most 512)
+  p.rows = 1 << (log_groups - p.log_split);
+  const unsigned grid = (unsigned)(((long long)p.num_rows + p.rows - 1) / p.rows);
   decltype(&rope_kernel<true, true, 1>) const kerns[2][2][3] = {
       {{rope_kernel<false, false, 1>, rope_kernel<false, false, 2>, rope_kernel<false, false, 3>},
        {rope_kernel<false, true, 1>, rope_kernel<false, true, 2>, rope_kernel<false, true, 3>}},
@@ -332,6 +358,18 @@ int launch_rope(RopeParams& p, const cp_rope_t* rope, bool f32, cudaStream_t str
        {rope_kernel<true, true, 1>, rope_kernel<true, true, 2>, rope_kernel<true, true, 3>}}};
   kerns[f32 ? 1 : 0][inter ? 1 : 0][ni - 1]<<<grid, kThreads, 0, stream>>>(p);
   return cudaGetLastError() == cudaSuccess ? CPATTN_OK : CPATTN_ERR_CUDA;
+}
+
+// Strides in bytes to those in 16 bytes, of 32 bits (the one row's or head's is not used).
+int strides16(RopeSide* s, int64_t xr, int64_t xh, int64_t yr, int64_t yh, int rows, int heads) {
+  if (rows <= 1) xr = yr = 0;
+  if (heads == 1) xh = yh = 0;
+  if (std::max(std::max(xr, xh), std::max(yr, yh)) / 16 > 0xffffffffLL) return CPATTN_ERR_TOO_LARGE;
+  s->x_row = (uint32_t)(xr / 16);
+  s->x_head = (uint32_t)(xh / 16);
+  s->y_row = (uint32_t)(yr / 16);
+  s->y_head = (uint32_t)(yh / 16);
+  return CPATTN_OK;
 }
 
 // One rotated tensor of cp_rope, or Q of cp_kv_append.
@@ -343,16 +381,12 @@ int rotated_side(RopeSide* s, const void* x, int64_t xr, int64_t xh, int heads, 
   if (rc != CPATTN_OK) return rc;
   if (num_rows > 0 && (!x || !y)) return CPATTN_ERR_INVALID_ARG;
   if (num_rows > 0 && !apart(x, xr, xh, y, yr, yh, size, num_rows, heads, d)) return CPATTN_ERR_INVALID_ARG;
-  s->x = x;
-  s->x_row = xr;
-  s->x_head = xh;
+  s->x = static_cast<const uint8_t*>(x);
   s->y = static_cast<uint8_t*>(y);
-  s->y_row = yr * size;
-  s->y_head = yh * size;
   s->heads = heads;
   s->dim = d;
-  s->rotated = rope ? rope->pairs / 8 : 0;
-  return CPATTN_OK;
+  s->rotated = rope != nullptr;
+  return strides16(s, xr * size, xh * size, yr * size, yh * size, num_rows, heads);
 }
 
 // K or V of cp_kv_append.
@@ -368,19 +402,16 @@ int cached_side(RopeSide* s, const void* x, int64_t xr, int64_t xh, bool f32, in
   if (c->head_stride < (int64_t)dim * size || c->row_stride < (int64_t)(heads - 1) * c->head_stride + dim * size ||
       (c->scales && c->scale_stride < cache_rows))
     return CPATTN_ERR_INVALID_ARG;
-  s->x = x;
-  s->x_row = xr;
-  s->x_head = xh;
+  s->x = static_cast<const uint8_t*>(x);
   s->y = static_cast<uint8_t*>(c->codes);
-  s->y_row = c->row_stride;
-  s->y_head = c->head_stride;
   s->scales = c->scales;
   s->s_head = c->scale_stride;
   s->heads = heads;
   s->dim = dim;
-  s->rotated = rope ? rope->pairs / 8 : 0;
+  s->rotated = rope != nullptr;
   s->cached = 1;
-  return CPATTN_OK;
+  const int in = f32 ? 4 : 2;
+  return strides16(s, xr * in, xh * in, c->row_stride, c->head_stride, std::max(num_rows, cache_rows), heads);
 }
 
 }  // namespace
@@ -397,7 +428,11 @@ extern "C" int cp_rope_table(const double* inv_freq, const int32_t* axis, int pa
     const int a = axis ? axis[c] : 0;
     if (!(std::fabs(f) <= 0x1p20) || a < 0 || a >= CPATTN_MAX_ROPE_AXES) return CPATTN_ERR_INVALID_ARG;
     const double turns = f * hi, rest = std::fma(f, hi, -turns) + f * lo;
-    const uint64_t F = (uint64_t)std::ldexp(turns - std::floor(turns), 64) + (uint64_t)std::llrint(std::ldexp(rest, 64));
+    // in 2^-64 turns, of a turn's fraction: that part is exact for either sign (turns - floor(turns) is
+    // not below zero), and so is its split at the binary point, so that one rounding is left
+    const double part = std::ldexp(turns - std::trunc(turns), 64), whole = std::trunc(part);
+    const uint64_t up = (uint64_t)std::fabs(whole);
+    const uint64_t F = (whole < 0 ? 0 - up : up) + (uint64_t)std::llrint(std::ldexp(rest, 64) + (part - whole));
     table[4 * c] = (int32_t)(uint32_t)F;
     table[4 * c + 1] = (int32_t)(uint32_t)(F >> 32);
     table[4 * c + 2] = a;

@@ -691,6 +691,7 @@ int cp_rope_table(const double* inv_freq, const int32_t* axis, int pairs, int32_
  *     bytes, >= 0.  An output may be its input (same pointer and strides); otherwise the
  *     two must not overlap (rows side by side in one buffer of equal row strides do not).
  *     No element of an output may have two places.
+ *     Strides of 2^36 bytes and more are CPATTN_ERR_TOO_LARGE.
  *   d: a multiple of 16, at most 1024, >= first + 2*pairs. */
 typedef struct {
   const void *q, *k;
