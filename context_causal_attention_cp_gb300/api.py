@@ -1193,17 +1193,22 @@ def cp_rope(rope: Rope, q, k=None, positions=None, *, inverse=False, out_q=None,
 
 
 # ------------------------------------------------------------- paged cache --
-def _row_side(t, name, index, shape):
-    """One side of a bf16 cache [rows, Hkv, dim] as a cp_kv_codes_t (strides in bytes)."""
+def _row_side(t, name, index, rows, Hkv):
+    """One side of a bf16 cache [rows, Hkv, dim]: its bytes as a cp_kv_codes_t (strides in
+    bytes), which cost a fraction of a ctypes structure, and its dim."""
     if not isinstance(t, torch.Tensor) or t.dtype is not torch.bfloat16 or t.get_device() != index:
         _bad(t, name, torch.bfloat16, index)
-    if t.dim() != 3 or t.shape[:2] != shape or (t.stride(2) != 1 and t.numel()):
+    shape = t.shape
+    if len(shape) != 3 or shape[0] != rows or shape[1] != Hkv or (t.stride(2) != 1 and t.numel()):
         raise ValueError(f"{name} must be [rows, Hkv, dim] with a contiguous last dim, of the "
-                         f"cache's {shape[0]} rows and {shape[1]} heads")
-    rows, Hkv, dim = t.shape
-    hs = t.stride(1) if Hkv > 1 else dim
-    rs = t.stride(0) if rows > 1 else (Hkv - 1) * hs + dim
-    return L.KvCodes(t.data_ptr(), None, 2 * rs, 2 * hs, 0)
+                         f"cache's {rows} rows and {Hkv} heads")
+    dim = shape[2]
+    rs, hs, _ = t.stride()
+    if Hkv == 1:
+        hs = dim
+    if rows <= 1:
+        rs = (Hkv - 1) * hs + dim
+    return L.KV_CODES.pack(t.data_ptr(), 0, 2 * rs, 2 * hs, 0), dim
 
 
 def cp_kv_append(cache, k, v=None, slots=None, *, rope: Optional[Rope] = None, positions=None,
@@ -1217,15 +1222,15 @@ def cp_kv_append(cache, k, v=None, slots=None, *, rope: Optional[Rope] = None, p
     """
     if isinstance(cache, KVCache):
         index, kc, vc = cache._sides()
+        kc, vc = ctypes.byref(kc), None if vc is None else ctypes.byref(vc)
         rows, (Hkv, d, dv) = cache.rows, cache._dims
     else:
         ck, cv = cache
         if not isinstance(ck, torch.Tensor) or ck.dim() != 3 or ck.get_device() < 0:
             raise ValueError("the cache must be CUDA tensors [rows, Hkv, dim]")
         index, (rows, Hkv, d) = ck.get_device(), ck.shape
-        kc = _row_side(ck, "the cache's k", index, (rows, Hkv))
-        vc, dv = (None, 0) if cv is None else (_row_side(cv, "the cache's v", index, (rows, Hkv)),
-                                               cv.shape[2])
+        kc, _ = _row_side(ck, "the cache's k", index, rows, Hkv)
+        vc, dv = (None, 0) if cv is None else _row_side(cv, "the cache's v", index, rows, Hkv)
     if (v is None) != (vc is None):
         raise ValueError("v goes with a cache that has V")
     if (rope is None) != (positions is None):

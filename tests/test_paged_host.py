@@ -113,6 +113,7 @@ def rows(**kw):
 
 def call_append(rope=rope_of(), kc=codes(), vc=codes(codes=0x700000, scales=0x780000), **kw):
     assert set(kw) <= set(APPEND)
+    kc, vc = (None if c is None else ctypes.byref(c) for c in (kc, vc))
     return L.load().cp_kv_append(rope, kc, vc, L.KV_APPEND_ARGS.pack(*{**APPEND, **kw}.values()), None)
 
 
@@ -206,6 +207,7 @@ def test_structures_are_those_of_c(tmp_path):
     gcc = shutil.which("gcc")
     if gcc is None:
         pytest.skip("no C compiler")
+    assert L.KV_CODES.size == ctypes.sizeof(L.KvCodes)
     kinds = (("cp_rope_args_t", L.ROPE_ARGS, ("q_row_stride", "num_rows", "inverse")),
              ("cp_kv_append_args_t", L.KV_APPEND_ARGS, ("k_row_stride", "num_rows", "x_is_fp32")),
              ("cp_attn_tree_args_t", L.ATTN_TREE_ARGS, ("q_row_stride", "num_rows", "scale")))
