@@ -250,6 +250,7 @@ extern "C" int cp_attn_tree(const cp_attn_tree_args_t* a, cudaStream_t stream) {
   p.lse = a->lse;
   int64_t o_at, l_at, bytes;
   plan_sizes(a->Hq, Hkv, d, a->max_nodes, a->num_ctas, &p.unit_rows, &o_at, &l_at, &bytes);
+  while ((1 << p.unit_log) < p.unit_rows) ++p.unit_log;
   p.team = team_of(Hkv, a->num_ctas);
   p.teams = a->num_ctas / p.team;
   p.cut = static_cast<int4*>(a->workspace);

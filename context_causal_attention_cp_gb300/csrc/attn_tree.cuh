@@ -27,7 +27,7 @@ struct TreeParams {
   int num_reqs, num_rows, max_pages, log_page, words;
   int Hq, Hkv, g;
   uint32_t g_mul, g_shift;  // see group_div
-  int unit_rows;
+  int unit_rows, unit_log;  // 2^unit_log
   int team, teams;  // blocks of a team, teams
   const __nv_bfloat16* q;
   long long q_row, q_head;
@@ -91,7 +91,7 @@ __device__ __forceinline__ TreeReq load_req(const TreeParams& p, int b, bool& ba
   return bad ? TreeReq{0, 0, 0} : TreeReq{s0, (int)T, L};
 }
 __device__ __forceinline__ int row_tiles(const TreeParams& p, const TreeReq& r) {
-  return (int)(((long long)r.T * p.g + p.unit_rows - 1) / p.unit_rows);
+  return (int)(((long long)r.T * p.g + p.unit_rows - 1) >> p.unit_log);
 }
 __device__ __forceinline__ long long req_cost(const TreeParams& p, const TreeReq& r) {
   return r.T == 0 ? 0 : (long long)row_tiles(p, r) * (p.Hkv / p.team) * num_tiles(r.L + r.T);
@@ -264,6 +264,34 @@ __device__ __forceinline__ void put_cut(const TreeParams& p, const TreePiece& pc
   p.cut[2 * blockIdx.x] = make_int4(pc.row0, pc.r0, pc.rows, pc.kv_head);
   p.cut[2 * blockIdx.x + 1] = make_int4(blocks, 0, 0, 0);
 }
+
+// The warp that walks the share puts its pieces into the ring, and reads them there itself.
+template <int N>
+struct TreeWalker {
+  TreeWalk w;
+  PieceRing<N>& ring;
+  int walked = 0;
+  bool more = true, ok = true, cut = false;
+  __device__ __forceinline__ TreeWalker(const TreeParams& p, const TreeStart& start, PieceRing<N>& r)
+      : w(p, start), ring(r) {}
+  // Pieces up to number n, and the one without tiles behind the last.
+  __device__ __forceinline__ void upto(const TreeParams& p, int n, const volatile int* abort) {
+    for (; more && ok && walked <= n; ++walked) {
+      TreePiece x;
+      more = w.next(p, x);
+      if (!more) x.tiles = x.rows = x.blocks = 0;
+      if (x.blocks) {
+        cut = true;
+        if ((threadIdx.x & 31) == 0) put_cut(p, x, x.blocks);
+      }
+      ok = ring.put(walked, x, abort, p.timeout_ns);
+    }
+  }
+  // By one lane, when there are no more.
+  __device__ __forceinline__ void end(const TreeParams& p) const {
+    if (!cut) p.cut[2 * blockIdx.x + 1] = make_int4(0, 0, 0, 0);
+  }
+};
 
 // A KV tile for its loader.  The lane's box is whole pages, or 16 rows of a unit's end.
 struct LoadTile {

@@ -41,7 +41,7 @@ template <int D, bool QUANT, bool DUAL>
 struct MmaCfg {
   static constexpr int kThreads = QUANT ? 640 : 384;
   static constexpr int kRegsLaunch = QUANT ? 96 : 168;
-  static constexpr int kRegsSoftmax = QUANT ? 128 : 200, kRegsOther = QUANT ? 72 : 104;
+  static constexpr int kRegsSoftmax = QUANT ? 120 : 200, kRegsOther = QUANT ? 80 : 104;
   static_assert(kRegsSoftmax * 256 + kRegsOther * (kThreads - 256) <= kRegsLaunch * kThreads,
                 "register split exceeds the launch allocation");
   static constexpr int kQTile = BM * D * 2;
@@ -545,33 +545,19 @@ attn_tree_mma_kernel(const __grid_constant__ TreeMaps maps, const TreeParams p) 
       // D / 8 lanes to a row.  Dual: tile s of a piece in buffer s, when the piece before has
       // no product left; single: the pieces' tiles take turns, one ahead.
       constexpr int kLanes = D / 8, kRows = 32 / kLanes;
-      // It also walks the share, two pieces ahead of the queries.
-      TreeWalk w(p, start);
-      TreePiece pc, ahead[2];
-      bool ok = true, cut = false;
+      // It also walks the share, two pieces ahead of the queries (of the first piece they are
+      // on their way before the second is walked).
+      TreeWalker<kPieces> walker(p, start, pieces);
+      TreePiece pc;
+      bool ok = true;
       const int c = lane % kLanes;
       int last[2] = {-1, -1};  // use of each buffer, where a box was its last
-      auto walk = [&](int i) {  // piece i
-        TreePiece x;
-        if (!w.next(p, x)) x.tiles = x.rows = x.blocks = 0;
-        if (x.blocks) {
-          cut = true;
-          if (lane == 0) put_cut(p, x, x.blocks);
-        }
-        ok = ok && pieces.put(i, x, abort_flag, p.timeout_ns);
-        return x;
-      };
-      ahead[0] = walk(0);
-      if (ahead[0].tiles) ahead[1] = walk(1);
-      bool more = true;
-      for (int i = 0; ok && more; ++i) {
-        pc = ahead[0];
-        more = pc.tiles > 0;
-        if (more) {
-          fetch_masks(p, pc);
-          ahead[0] = ahead[1];
-          if (ahead[0].tiles) ahead[1] = walk(i + 2);
-        }
+      for (int i = 0;; ++i) {
+        walker.upto(p, i == 0 ? 0 : i + 2, abort_flag);
+        ok = walker.ok && pieces.get(i, pc, abort_flag, p.timeout_ns);
+        if (!ok) break;
+        // (the end's queries are none, and published all the same: the MMA warp waits for them)
+#pragma unroll
         for (int s = 0; s < (DUAL ? 2 : 1) && ok; ++s) {
           const int buf = DUAL ? s : i & 1, use = DUAL ? i : i >> 1;
           ok = wait_warp(q_empty + buf, (use & 1) ^ 1, abort_flag, p.timeout_ns);
@@ -604,41 +590,58 @@ attn_tree_mma_kernel(const __grid_constant__ TreeMaps maps, const TreeParams p) 
                          "l"(src)
                          : "memory");
           }
-          asm volatile("cp.async.wait_all;" ::: "memory");
-          if constexpr (QUANT) {
-            // each lane's own chunks, in place: bf16 to f16 times 2^f with 2^f max|q| in [2^14, 2^15)
-            const uint32_t group = (kLanes == 32 ? 0u : ((1u << kLanes) - 1u)) << (lane & ~(kLanes - 1));
-#pragma unroll 4
-            for (int r = lane / kLanes; r < rows; r += kRows) {
-              const uint32_t at = tile + r * 128 + (((c & 7) ^ (r & 7)) << 4);
-              uint32_t x[4];
-              asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                           : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
-                           : "r"(at)
-                           : "memory");
-              uint32_t mx = __vmaxu2(__vmaxu2(x[0] & 0x7FFF7FFFu, x[1] & 0x7FFF7FFFu),
-                                     __vmaxu2(x[2] & 0x7FFF7FFFu, x[3] & 0x7FFF7FFFu));
-              mx = max(mx & 0xFFFFu, mx >> 16);
-#pragma unroll
-              for (int o = kLanes / 2; o > 0; o >>= 1) mx = max(mx, __shfl_xor_sync(group, mx, o));
-              const int f = min(max(14 - ((int)(mx >> 7) - 127), -126), 126);
-              const float up = exp2_int(f);
-#pragma unroll
-              for (int y = 0; y < 4; ++y)
-                x[y] = pack_f16x2(__uint_as_float(x[y] << 16) * up, __uint_as_float(x[y] & 0xFFFF0000u) * up);
-              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x[0]), "r"(x[1]), "r"(x[2]),
-                           "r"(x[3])
-                           : "memory");
-              if (c == 0) q_lift[((i & 1) * 2 + s) * BM + r] = (int8_t)f;
-            }
-          }
-          fence_async_shared();
-          __syncwarp();
-          if (lane == 0 && !p.withhold_q) mbar_arrive(q_full + buf);
         }
+        if (!ok) break;
+        if (i == 0) walker.upto(p, 2, abort_flag);
+        if (pc.tiles) fetch_masks(p, pc);
+        if (QUANT || !p.q_boxes) {
+          asm volatile("cp.async.wait_all;" ::: "memory");
+#pragma unroll
+          for (int s = 0; s < (DUAL ? 2 : 1); ++s) {
+            const int buf = DUAL ? s : i & 1;
+            if constexpr (QUANT) {
+              // Each lane's own chunks, in place: bf16 to f16 times 2^f with 2^f max|q| in
+              // [2^14, 2^15).  Loads of a batch before its stores: a chunk at a time costs 230
+              // cycles of latency.  (Rows of the batch behind the tile's last hold anything.)
+              constexpr int kBatch = 4;
+              uint8_t* const tile = smem + buf * C::kQTile + (c >> 3) * (BM * 128);
+              for (int r0 = lane / kLanes; r0 - lane / kLanes < pc.rows - s * BM && r0 < BM; r0 += kBatch * kRows) {
+                uint4 x[kBatch];
+                uint32_t mx[kBatch];
+#pragma unroll
+                for (int y = 0; y < kBatch; ++y) {
+                  const int r = r0 + y * kRows;
+                  x[y] = *reinterpret_cast<const uint4*>(tile + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+                  const uint32_t m = __vmaxu2(__vmaxu2(x[y].x & 0x7FFF7FFFu, x[y].y & 0x7FFF7FFFu),
+                                              __vmaxu2(x[y].z & 0x7FFF7FFFu, x[y].w & 0x7FFF7FFFu));
+                  mx[y] = max(m & 0xFFFFu, m >> 16);
+                }
+#pragma unroll
+                for (int o = kLanes / 2; o > 0; o >>= 1)
+#pragma unroll
+                  for (int y = 0; y < kBatch; ++y) mx[y] = max(mx[y], __shfl_xor_sync(0xffffffffu, mx[y], o));
+#pragma unroll
+                for (int y = 0; y < kBatch; ++y) {
+                  const int r = r0 + y * kRows, f = min(max(14 - ((int)(mx[y] >> 7) - 127), -126), 126);
+                  const float up = exp2_int(f);
+                  auto turn = [&](uint32_t v) {
+                    return pack_f16x2(__uint_as_float(v << 16) * up, __uint_as_float(v & 0xFFFF0000u) * up);
+                  };
+                  *reinterpret_cast<uint4*>(tile + r * 128 + (((c & 7) ^ (r & 7)) << 4)) =
+                      make_uint4(turn(x[y].x), turn(x[y].y), turn(x[y].z), turn(x[y].w));
+                  if (c == 0) q_lift[((i & 1) * 2 + s) * BM + r] = (int8_t)f;
+                }
+              }
+            }
+            fence_async_shared();
+            __syncwarp();
+            if (lane == 0 && !p.withhold_q) mbar_arrive(q_full + buf);
+          }
+        }
+        if (!pc.tiles) break;
       }
       if (lane == 0) {
-        if (!cut) p.cut[2 * blockIdx.x + 1] = make_int4(0, 0, 0, 0);
+        walker.end(p);
         if (!ok) {
           set_status(p.status, CPATTN_ERR_TIMEOUT);
           *abort_flag = 1;
@@ -647,6 +650,7 @@ attn_tree_mma_kernel(const __grid_constant__ TreeMaps maps, const TreeParams p) 
         for (int buf = 0; buf < 2; ++buf)
           if (last[buf] >= 0) wait_one(q_full + buf, last[buf] & 1, nullptr, p.timeout_ns);
       }
+      asm volatile("cp.async.wait_all;" ::: "memory");
     }
     if constexpr (QUANT) if (warp >= kConvertWarp) {
       // --------------------------------------------------- codes to f16 tiles --

@@ -604,28 +604,16 @@ attn_tree_small_kernel(const __grid_constant__ TreeMaps maps, const TreeParams p
         }
       }
     } else if (warp == kWarps + 2) {  // walks the share, two pieces ahead of the queries that it loads
-      TreeWalk w(p, start);
-      TreePiece ahead[2];
-      bool ok = true, cut = false;
-      auto walk = [&](int i) {  // piece i
-        TreePiece x;
-        if (!w.next(p, x)) x.tiles = x.rows = x.blocks = 0;
-        if (x.blocks) {
-          cut = true;
-          if (lane == 0) put_cut(p, x, x.blocks);
-        }
-        ok = ok && pieces.put(i, x, abort_flag, p.timeout_ns);
-        return x;
-      };
-      ahead[0] = walk(0);
-      if (ahead[0].tiles) ahead[1] = walk(1);
-      for (int i = 0; ok && ahead[0].tiles; ++i) {
-        const TreePiece pc = ahead[0];
+      // (the first piece's queries are on their way before the second is walked)
+      TreeWalker<kPieces> walker(p, start, pieces);
+      TreePiece pc;
+      bool ok = true;
+      for (int i = 0;; ++i) {
+        walker.upto(p, i == 0 ? 0 : i + 2, abort_flag);
+        ok = walker.ok && pieces.get(i, pc, abort_flag, p.timeout_ns);
+        if (!ok || pc.tiles == 0) break;
         const int qb = i & 1;
-        fetch_masks(p, pc);
-        ahead[0] = ahead[1];
-        if (ahead[0].tiles) ahead[1] = walk(i + 2);
-        ok = ok && wait_warp(q_empty + qb, ((i >> 1) & 1) ^ 1, abort_flag, p.timeout_ns);
+        ok = wait_warp(q_empty + qb, ((i >> 1) & 1) ^ 1, abort_flag, p.timeout_ns);
         if (!ok) break;
         // the query rows, 16-byte chunks swizzled over a row's length
         for (int x = lane; x < pc.rows * (D / 8); x += 32) {
@@ -638,10 +626,12 @@ attn_tree_small_kernel(const __grid_constant__ TreeMaps maps, const TreeParams p
                        : "memory");
         }
         if (!p.withhold_q) arrive_copies(q_full + qb);
+        fetch_masks(p, pc);
+        if (i == 0) walker.upto(p, 2, abort_flag);
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
       if (lane == 0) {
-        if (!cut) p.cut[2 * blockIdx.x + 1] = make_int4(0, 0, 0, 0);
+        walker.end(p);
         if (!ok) {
           set_status(p.status, CPATTN_ERR_TIMEOUT);
           *abort_flag = 1;
