@@ -12,11 +12,12 @@
 //   warps 8, 9   producers of the K and the V tiles: a lane looks up a page, a tile ahead,
 //                and starts its TMA copies; one ring of tiles in the order of use that runs
 //                across piece ends.
-//   warp 10      MMA issuer (one thread): O += P V and the next S = Q K^T of one stream, then
+//   warp 10      MMA issuer: O += P V and the next S = Q K^T of one stream, then
 //                of the other.
-//   warp 11      query rows to shared memory.
+//   warp 11      query rows to shared memory, over codes turned to f16; walks the share.
 //   warps 12-19  (e4m3 cache) codes to f16 tiles, as in attn_shared.cu.
-// Every wait is bounded; all roles walk the block's share on their own (see attn_tree.cuh).
+// Every wait is bounded; warp 11 walks the block's share and the others read its pieces from
+// a ring (see attn_tree.cuh).
 //
 // Value rows behind the last key, and (among new keys) rows with an infinity or a NaN, become
 // zeros in shared memory before their product: 0 * NaN is NaN, so that masking P alone
@@ -41,7 +42,9 @@ template <int D, bool QUANT, bool DUAL>
 struct MmaCfg {
   static constexpr int kThreads = QUANT ? 640 : 384;
   static constexpr int kRegsLaunch = QUANT ? 96 : 168;
-  static constexpr int kRegsSoftmax = QUANT ? 120 : 200, kRegsOther = QUANT ? 80 : 104;
+  // (e4m3 dual: with 128 and 72 the other warps spill, trees of 64 464 against 440 us; single:
+  // with 120 and 80 the softmax does, trees of 32 323 against 308 us)
+  static constexpr int kRegsSoftmax = !QUANT ? 200 : DUAL ? 120 : 128, kRegsOther = !QUANT ? 104 : DUAL ? 80 : 72;
   static_assert(kRegsSoftmax * 256 + kRegsOther * (kThreads - 256) <= kRegsLaunch * kThreads,
                 "register split exceeds the launch allocation");
   static constexpr int kQTile = BM * D * 2;
@@ -146,9 +149,8 @@ __device__ __forceinline__ void bar_named(int id, int threads) {
 
 // S of a tile to P, for the rows of a warp (one a lane): see softmax_tile in attn_shared.cu.
 // vis: the keys that the row sees (masked: not all); o_scale: what O is multiplied by besides.
-// Over codes S goes through the registers twice, by halves, for its maximum and for P: the
-// converters have the registers that a whole row would take.  (P lies over columns of S that
-// are done.)
+// Over codes S goes through the registers by halves, the first one twice (for the maximum and for
+// P): the converters have the registers that a whole row would take.
 template <int D, bool QUANT>
 __device__ __forceinline__ void softmax_row(uint32_t s_addr, uint32_t o_addr, bool masked, const uint32_t (&vis)[4],
                                             bool has_o, float o_scale, float sl2, float& m_run, float& m_use,
@@ -190,12 +192,12 @@ __device__ __forceinline__ void softmax_row(uint32_t s_addr, uint32_t o_addr, bo
   const float m_new_use = (m_new == -INFINITY) ? 0.f : m_new;
   const float alpha = move ? ex2_approx(m_run - m_new_use) : 1.f;
   float sum0 = 0.f, sum1 = 0.f;
+  // the last part first, which is here
 #pragma unroll
-  for (int part = 0; part < kParts; ++part) {
-    if (kParts > 1) load(part);
+  for (int part = kParts - 1; part >= 0; --part) {
+    uint32_t pk[kCols / 32][16];
 #pragma unroll
     for (int q = 0; q < kCols / 32; ++q) {
-      uint32_t pk[16];
 #pragma unroll
       for (int c = 0; c < 32; c += 2) {
         float a, b;
@@ -205,9 +207,14 @@ __device__ __forceinline__ void softmax_row(uint32_t s_addr, uint32_t o_addr, bo
         fadd2(sum0, sum1, sum0, sum1, a, b);
         // P in 16 bits, the second product's operand type: off by at most 2^-8 (bf16) or
         // 2^-11 (f16) of each weight; l sums the unrounded values
-        pk[c >> 1] = QUANT ? pack_f16x2(a, b) : pack_bf16x2(a, b);
+        pk[q][c >> 1] = QUANT ? pack_f16x2(a, b) : pack_bf16x2(a, b);
       }
-      tmem_st16(s_addr + part * (kCols / 2) + q * 16, pk);
+      if (part == 0) tmem_st16(s_addr + q * 16, pk[q]);
+    }
+    if (part > 0) {
+      load(part - 1);  // (P lies over its columns)
+#pragma unroll
+      for (int q = 0; q < kCols / 32; ++q) tmem_st16(s_addr + part * (kCols / 2) + q * 16, pk[q]);
     }
   }
   l_run = l_run * alpha + (sum0 + sum1);

@@ -28,7 +28,7 @@
 namespace cpattn {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256;  // of a block, at most
 constexpr int kMaxDim = 1024;
 constexpr int kMaxCs = 2048;  // cos and sin values of a block's rows
 constexpr int kItem = 16;     // columns of an item
@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(kThreads, NI != 1 || F32 ? 2 : 3) rope_kernel(
       }
     }
     if (base == 0 && p.pairs > 0) {
-      for (int i = threadIdx.x; i < rows * p.pairs; i += kThreads) {
+      for (int i = threadIdx.x; i < rows * p.pairs; i += blockDim.x) {
         const int at_row = i / p.pairs, c = i - at_row * p.pairs;
         const int4 f = __ldg(p.table + c);
         const bool ok = f.z >= 0 && f.z < p.axes;
@@ -341,14 +341,21 @@ int launch_rope(RopeParams& p, const cp_rope_t* rope, bool f32, cudaStream_t str
   else if (items > 32) p.log_l = 4, ni = 3;
   else
     for (p.log_l = 0; (1 << p.log_l) < items; ++p.log_l) {}
-  // Groups of a row: few, since they share its cos and sin, but so many that there are six
-  // blocks for each SM, and that the block's cos and sin fit.
-  const int log_groups = 8 - p.log_l;
+  // Blocks of 128 threads, whose share of the last wave is smaller than that of 256 (8192 rows
+  // of 40 heads 34.7 -> 33.7 us, 16384 rows of 576 columns 13.5 -> 12.3); of 256 where a
+  // block for each row is on the SMs at once: more threads to a row are sooner through (400 rows
+  // of 48: 3.6 against 4.0 us; 500 rows, a second wave, 5.1 against 4.1).
+  const int log_threads = p.num_rows <= 152 * 3 ? 8 : 7, log_groups = log_threads - p.log_l;
+  // Groups of a row: few, since they share its cos and sin, but so many that there are 18
+  // blocks for each SM (8192 rows: 33.7 us with half as many, 32.4 with these), and six even if
+  // a group then has less than two rounds of vectors (4096 rows of 48: 23.8 us, with twice as
+  // many groups 24.6).
   p.log_split = 0;
   while (p.log_split < log_groups && (1 << p.log_split) < p.vectors &&
-         ((long long)p.num_rows << p.log_split >> log_groups) < 152 * 6)
+         ((long long)p.num_rows << p.log_split >> log_groups) <
+             (p.vectors >> (p.log_split + 1) >= 4 ? 152 * 18 : 152 * 6))
     ++p.log_split;
-  while (p.pairs << (log_groups - p.log_split) > kMaxCs) ++p.log_split;  // (a row has at most 512)
+  while (p.pairs << (log_groups - p.log_split) > kMaxCs) ++p.log_split;  // (its cos and sin fit: a row has at most 512)
   p.rows = 1 << (log_groups - p.log_split);
   const unsigned grid = (unsigned)(((long long)p.num_rows + p.rows - 1) / p.rows);
   decltype(&rope_kernel<true, true, 1>) const kerns[2][2][3] = {
@@ -356,7 +363,7 @@ int launch_rope(RopeParams& p, const cp_rope_t* rope, bool f32, cudaStream_t str
        {rope_kernel<false, true, 1>, rope_kernel<false, true, 2>, rope_kernel<false, true, 3>}},
       {{rope_kernel<true, false, 1>, rope_kernel<true, false, 2>, rope_kernel<true, false, 3>},
        {rope_kernel<true, true, 1>, rope_kernel<true, true, 2>, rope_kernel<true, true, 3>}}};
-  kerns[f32 ? 1 : 0][inter ? 1 : 0][ni - 1]<<<grid, kThreads, 0, stream>>>(p);
+  kerns[f32 ? 1 : 0][inter ? 1 : 0][ni - 1]<<<grid, 1 << log_threads, 0, stream>>>(p);
   return cudaGetLastError() == cudaSuccess ? CPATTN_OK : CPATTN_ERR_CUDA;
 }
 
