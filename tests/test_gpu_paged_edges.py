@@ -8,8 +8,11 @@ import torch
 import context_causal_attention_cp_gb300 as cpa
 from context_causal_attention_cp_gb300 import _lib as L
 from context_causal_attention_cp_gb300 import api
+from oracle import paged as op
 
-from test_gpu_shared import check, make
+import test_gpu_rope as rotation
+from test_gpu_guards import Guarded
+from test_gpu_shared import check, f64, make
 from test_gpu_tree import KINDS, Step, i32
 
 pytestmark = pytest.mark.gpu
@@ -181,3 +184,63 @@ def test_rotation_before_or_with_the_append():
     assert torch.equal(qa, qr)
     for a, b in zip(*caches):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("n, Hq, d, pairs, first", [
+    (600, 2, 1024, 512, 0), (300, 1, 768, 384, 0), (700, 1, 768, 384, 0), (500, 3, 576, 32, 512), (457, 1, 16, 8, 0),
+    (456, 40, 16, 8, 0), (1000, 48, 64, 32, 0), (2000, 3, 272, 8, 256), (9000, 1, 512, 256, 0)])
+def test_rows_on_both_sizes_of_blocks(n, Hq, d, pairs, first, dtype):
+    """Wide and narrow vectors, one and many a row, at numbers of rows that take blocks of
+    either size and rows that end inside a block."""
+    rope, pos, rot, ref = rotation.make(n, n, pairs, 2, first, n % 2 == 1)
+    x = rotation.draw(n, (n, Hq, d), dtype)
+    out, status = Guarded((n, Hq, d), dtype), cpa.new_status()
+    cpa.cp_rope(rope, x, positions=pos, out_q=out.t, status=status)
+    cpa.check_status(status)
+    out.check("q")
+    rotation.check(out.t, x, rot, op.rotate(f64(x), **ref))
+    # the same rows into a cache, backwards
+    cache = (torch.zeros((n + 3, Hq, d), dtype=torch.bfloat16, device="cuda"), None)
+    slots = torch.arange(n - 1, -1, -1, dtype=torch.int32, device="cuda")
+    cpa.cp_kv_append(cache, x, None, slots, rope=rope, positions=pos, status=status)
+    cpa.check_status(status)
+    assert torch.equal(cache[0][:n].flip(0), out.t.bfloat16()) and not cache[0][n:].any()
+
+
+@KINDS
+@pytest.mark.parametrize("d", [64, 128])
+def test_any_number_of_nodes_to_tune_for_and_of_blocks(d, quant):
+    """Units of every size on rows that they were not chosen for, on one block and on more than
+    the device has."""
+    Hq, Hkv = 8, 2
+    s = Step(14, [1, 30, 0, 7, 1], [700, 60, 5, 0, 128], 32)
+    q, k, v, scales, k64, v64 = make(14, s.N, s.rows, Hq, Hkv, d, quant)
+    ref = s.ref(q, k64, v64, 0.1)
+    for most in (1, 2, 4, 5, 32, 33, 100000):
+        for ctas in (1, 2, 7, 152, 4096):
+            status = cpa.new_status()
+            o, lse, _ = s.call(q, k, v, 0.1, max_nodes=most, num_ctas=ctas, status=status, **scales)
+            cpa.check_status(status, f"{most} nodes, {ctas} blocks")
+            check(o, lse, ref, d, 701, f"{most} nodes, {ctas} blocks")
+
+
+@KINDS
+@pytest.mark.parametrize("nodes", [[2, 1], [20, 11], [64, 50]], ids=["small", "single", "dual"])
+def test_a_page_of_65536_rows_and_an_output_at_16_bytes(nodes, quant):
+    Hq, Hkv, d = 4, 1, 64
+    s = Step(15, nodes, [300, 777], 65536, spare=0)
+    q, k, v, scales, k64, v64 = make(15, s.N, s.rows, Hq, Hkv, d, quant)
+    room = torch.full((s.N * Hq * d + 16,), 5.0, dtype=torch.bfloat16, device="cuda")
+    out = room[8:-8].view(s.N, Hq, d)
+    assert out.data_ptr() % 32 == 16
+    o, lse, _ = s.call(q, k, v, 0.1, out=out, **scales)
+    check(o, lse, s.ref(q, k64, v64, 0.1), d, 827)
+    assert (room[:8] == 5.0).all() and (room[-8:] == 5.0).all()
+
+
+def test_k_that_is_v_too():
+    s = Step(16, [3, 9], [200, 31], 16)
+    q, k, _, _, k64, _ = make(16, s.N, s.rows, 8, 2, 128, False)
+    o, lse, _ = s.call(q, k, k, 0.1)
+    check(o, lse, s.ref(q, k64, k64, 0.1), 128, 203)
