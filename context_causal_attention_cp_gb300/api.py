@@ -1144,7 +1144,7 @@ def _positions(rope, positions, n, index):
     strides = positions.stride()
     if strides[-1] != 1 and n > 1:
         raise ValueError("positions needs a contiguous last dim")
-    return positions.data_ptr(), max(strides[0], n) if axes > 1 else n
+    return positions.data_ptr(), strides[0] if axes > 1 else n
 
 
 def _rotated(x, out, name, dtype, n, d, index, stream):

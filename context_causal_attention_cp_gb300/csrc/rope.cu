@@ -318,7 +318,7 @@ int check_rope(const cp_rope_t* r, int d, const int32_t* positions, int64_t axis
   if ((long long)r->first + 2LL * r->pairs > d) return CPATTN_ERR_INVALID_ARG;
   if (!aligned(r->table, 16) || !aligned(positions, 4)) return CPATTN_ERR_ALIGNMENT;
   if (num_rows > 0 && (!r->table || !positions)) return CPATTN_ERR_INVALID_ARG;
-  return r->axes > 1 && axis_stride < num_rows ? CPATTN_ERR_INVALID_ARG : CPATTN_OK;
+  return r->axes > 1 && axis_stride < 0 ? CPATTN_ERR_INVALID_ARG : CPATTN_OK;
 }
 
 int launch_rope(RopeParams& p, const cp_rope_t* rope, bool f32, cudaStream_t stream) {

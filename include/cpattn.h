@@ -684,13 +684,13 @@ int cp_rope_table(const double* inv_freq, const int32_t* axis, int pairs, int32_
 
 /* Rotate the rows of q [num_rows, Hq, d], and of k [num_rows, Hk, d] (Hk = 0: q alone).
  *   positions: device int32, axis a's position of row i at positions[a*axis_stride + i]
- *     (axis_stride >= num_rows where axes > 1); any values.
+ *     (axis_stride >= 0; with 0 all axes follow one row of positions); any values.
  *   inverse: turn by -t.  The rotation is orthogonal, so that this is the gradient: dq
  *     from dq_out.
  *   q, k, q_out, k_out: bf16, or fp32 (x_is_fp32); strides in elements, multiples of 16
  *     bytes, >= 0.  An output may be its input (same pointer and strides); otherwise the
  *     two must not overlap (rows side by side in one buffer of equal row strides do not).
- *     No element of an output may have two places.
+ *     No element of an output may have two places, nor lie in the call's other tensors.
  *     Strides of 2^36 bytes and more are CPATTN_ERR_TOO_LARGE.
  *   d: a multiple of 16, at most 1024, >= first + 2*pairs. */
 typedef struct {

@@ -244,3 +244,21 @@ def test_k_that_is_v_too():
     q, k, _, _, k64, _ = make(16, s.N, s.rows, 8, 2, 128, False)
     o, lse, _ = s.call(q, k, k, 0.1)
     check(o, lse, s.ref(q, k64, k64, 0.1), 128, 203)
+
+
+def test_positions_that_axes_share():
+    """Positions expanded over the axes, cut out of a longer row, or one row's of a table."""
+    n, d = 70, 96
+    rope, _, rot, ref = rotation.make(3, n, 24, 3)
+    x, cache = rotation.draw(4, (n, 2, d), torch.bfloat16), torch.zeros((n, 2, d), dtype=torch.bfloat16, device="cuda")
+    long = torch.arange(5000, 5000 + 3 * n, dtype=torch.int32, device="cuda")
+    wide = torch.stack([long, long + 7, long * 3])
+    for pos in (long[5:5 + n].expand(3, n), wide[:, 9:9 + n], long.view(n, 3).t().contiguous(), wide[:, 30:31].expand(3, n)[:, :1]):
+        m = pos.shape[1]
+        want = op.rotate(f64(x[:m]), **{**ref, "positions": pos.cpu().numpy()})
+        got, _ = cpa.cp_rope(rope, x[:m], positions=pos)
+        rotation.check(got, x[:m], rot, want)
+        cpa.cp_kv_append((cache, None), x[:m], None, rope=rope, positions=pos)
+        assert torch.equal(cache[:m], got)
+    with pytest.raises(ValueError):
+        cpa.cp_rope(rope, x, positions=long.view(n, 3).t())

@@ -46,7 +46,7 @@ def test_rope_refusals():
         BAD: (dict(rope=None), dict(rope=rope_of(pairs=0)), dict(rope=rope_of(pairs=-8)), dict(rope=rope_of(first=-8)),
               dict(rope=rope_of(axes=0)), dict(rope=rope_of(axes=9)), dict(rope=rope_of(first=72)),
               dict(rope=rope_of(first=2 ** 31 - 8)), dict(rope=rope_of(pairs=72)), dict(rope=rope_of(table=None)),
-              dict(rope=rope_of(axes=2), axis=7), dict(at=0), dict(q=0), dict(qo=0), dict(k=0), dict(ko=0), dict(n=-1),
+              dict(rope=rope_of(axes=2), axis=-1), dict(at=0), dict(q=0), dict(qo=0), dict(k=0), dict(ko=0), dict(n=-1),
               dict(Hq=0), dict(Hk=-1), dict(Hq=1 << 21), dict(Hk=1 << 21), dict(qr=-8), dict(kh=-8), dict(qor=0), dict(koh=0),
               dict(qoh=120), dict(kor=248),
               # outputs that meet their inputs
@@ -124,7 +124,7 @@ def test_append_refusals():
               dict(rows=65), dict(kc=codes(codes=None)), dict(kc=codes(scales=None)), dict(vc=rows()),
               dict(kc=codes(head_stride=112)), dict(kc=codes(row_stride=240)), dict(kc=codes(scale_stride=63)),
               dict(kc=rows(row_stride=256), vc=rows()), dict(kc=rows(), vc=rows(head_stride=240)),
-              dict(qo=0x200000 + 256), dict(rope=rope_of(pairs=72)), dict(rope=rope_of(axes=3), axis=7),
+              dict(qo=0x200000 + 256), dict(rope=rope_of(pairs=72)), dict(rope=rope_of(axes=3), axis=-8),
               dict(rope=rope_of(table=None))),
         KIND: (dict(d=120), dict(d=8, rope=None), dict(dv=1040), dict(dv=0), dict(rope=rope_of(pairs=4))),
         ALIGN: (dict(k=0x10008), dict(v=0x100002), dict(q=0x200008), dict(qo=0x300008), dict(slots=0x810002),
