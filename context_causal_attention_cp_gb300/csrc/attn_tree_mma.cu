@@ -14,7 +14,8 @@
 //                across piece ends.
 //   warp 10      MMA issuer: O += P V and the next S = Q K^T of one stream, then
 //                of the other.
-//   warp 11      query rows to shared memory, over codes turned to f16; walks the share.
+//   warp 11      query rows to shared memory, over codes turned to f16 (the first piece's by
+//                the softmax warps); walks the share.
 //   warps 12-19  (e4m3 cache) codes to f16 tiles, as in attn_shared.cu.
 // Every wait is bounded; warp 11 walks the block's share and the others read its pieces from
 // a ring (see attn_tree.cuh).
@@ -26,7 +27,7 @@
 //
 // Measured, 32/8 heads, d = 128, 32 requests on up to 16K keys: trees of 32 (single units) 205 us,
 // HBM (floor 193); trees of 64 (dual) 261 us (floor 194): the tensor pipe is active 57 % of the
-// time, a stream's chain S -> softmax -> P -> P V is what bounds them.  Over codes 308 and 440 us
+// time, a stream's chain S -> softmax -> P -> P V is what bounds them.  Over codes 293 and 431 us
 // (floors 100 and 130): the same chain with S in halves, beside the converters.
 #include <algorithm>
 #include <atomic>
@@ -134,6 +135,21 @@ struct MaskWords {
       const int count = limit - m;
       vis[x] = count >= 32 ? bits : count <= 0 ? 0u : bits & ((1u << count) - 1u);
     }
+  }
+};
+
+// A query row of bf16 to f16 times 2^f with 2^f max|q| in [2^14, 2^15).
+struct QueryLift {
+  float up;
+  __device__ __forceinline__ QueryLift(uint32_t largest, int& f) {  // bits of max|q|
+    f = min(max(14 - ((int)(largest >> 7) - 127), -126), 126);
+    up = exp2_int(f);
+  }
+  __device__ __forceinline__ uint32_t two(uint32_t v) const {
+    return pack_f16x2(__uint_as_float(v << 16) * up, __uint_as_float(v & 0xFFFF0000u) * up);
+  }
+  __device__ __forceinline__ uint4 operator()(const uint4& v) const {
+    return make_uint4(two(v.x), two(v.y), two(v.z), two(v.w));
   }
 };
 
@@ -569,8 +585,9 @@ attn_tree_mma_kernel(const __grid_constant__ TreeMaps maps, const TreeParams p) 
         ok = walker.ok && pieces.get(i, pc, abort_flag, p.timeout_ns);
         if (!ok) break;
         // (the end's queries are none, and published all the same: the MMA warp waits for them)
+        const bool mine = !(QUANT && i == 0 && pc.tiles > 0);  // (else the softmax warps have them)
 #pragma unroll
-        for (int s = 0; s < (DUAL ? 2 : 1) && ok; ++s) {
+        for (int s = 0; s < (DUAL ? 2 : 1) && ok && mine; ++s) {
           const int buf = DUAL ? s : i & 1, use = DUAL ? i : i >> 1;
           ok = wait_warp(q_empty + buf, (use & 1) ^ 1, abort_flag, p.timeout_ns);
           if (!ok) break;
@@ -606,15 +623,15 @@ attn_tree_mma_kernel(const __grid_constant__ TreeMaps maps, const TreeParams p) 
         if (!ok) break;
         if (i == 0) walker.upto(p, 2, abort_flag);
         if (pc.tiles) fetch_masks(p, pc);
-        if (QUANT || !p.q_boxes) {
+        if (mine && (QUANT || !p.q_boxes)) {
           asm volatile("cp.async.wait_all;" ::: "memory");
 #pragma unroll
           for (int s = 0; s < (DUAL ? 2 : 1); ++s) {
             const int buf = DUAL ? s : i & 1;
             if constexpr (QUANT) {
-              // Each lane's own chunks, in place: bf16 to f16 times 2^f with 2^f max|q| in
-              // [2^14, 2^15).  Loads of a batch before its stores: a chunk at a time costs 230
-              // cycles of latency.  (Rows of the batch behind the tile's last hold anything.)
+              // Each lane's own chunks, in place.  Loads of a batch before its stores: a chunk at a
+              // time costs 230 cycles of latency.  (Rows of the batch behind the tile's last hold
+              // anything.)
               constexpr int kBatch = 4;
               uint8_t* const tile = smem + buf * C::kQTile + (c >> 3) * (BM * 128);
               for (int r0 = lane / kLanes; r0 - lane / kLanes < pc.rows - s * BM && r0 < BM; r0 += kBatch * kRows) {
@@ -634,13 +651,10 @@ attn_tree_mma_kernel(const __grid_constant__ TreeMaps maps, const TreeParams p) 
                   for (int y = 0; y < kBatch; ++y) mx[y] = max(mx[y], __shfl_xor_sync(0xffffffffu, mx[y], o));
 #pragma unroll
                 for (int y = 0; y < kBatch; ++y) {
-                  const int r = r0 + y * kRows, f = min(max(14 - ((int)(mx[y] >> 7) - 127), -126), 126);
-                  const float up = exp2_int(f);
-                  auto turn = [&](uint32_t v) {
-                    return pack_f16x2(__uint_as_float(v << 16) * up, __uint_as_float(v & 0xFFFF0000u) * up);
-                  };
-                  *reinterpret_cast<uint4*>(tile + r * 128 + (((c & 7) ^ (r & 7)) << 4)) =
-                      make_uint4(turn(x[y].x), turn(x[y].y), turn(x[y].z), turn(x[y].w));
+                  const int r = r0 + y * kRows;
+                  int f;
+                  const QueryLift lift(mx[y], f);
+                  *reinterpret_cast<uint4*>(tile + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = lift(x[y]);
                   if (c == 0) q_lift[((i & 1) * 2 + s) * BM + r] = (int8_t)f;
                 }
               }
@@ -810,6 +824,37 @@ attn_tree_mma_kernel(const __grid_constant__ TreeMaps maps, const TreeParams p) 
     int n0 = 0;                       // KV tiles before the piece
     int tails = 0;                    // of the stream, with new keys
     int had[2] = {0, 0};              // pieces in which a stream had tiles
+    if constexpr (QUANT) {
+      // The first piece's queries, a row a thread: one warp takes microseconds to bring 256 rows
+      // and to turn them, in which these have nothing to do (trees of 26 at d = 64 35.1 -> 31.8
+      // us, of 64 440 -> 431, of 32 306 -> 293).
+      ok = pieces.get(0, pc, abort_flag, p.timeout_ns);
+      if (DUAL || s == 0) {
+        if (ok && r < pc.rows) {
+          const int packed = pc.r0 + r, node = group_div(p, packed);
+          const uint4* src = reinterpret_cast<const uint4*>(
+              p.q + (long long)(pc.row0 + node) * p.q_row + (long long)(pc.kv_head * p.g + packed - node * p.g) * p.q_head);
+          uint4 v[D / 8];
+#pragma unroll
+          for (int c = 0; c < D / 8; ++c) v[c] = __ldg(src + c);
+          uint32_t mx = 0;
+#pragma unroll
+          for (int c = 0; c < D / 8; ++c)
+            mx = __vmaxu2(__vmaxu2(mx, __vmaxu2(v[c].x & 0x7FFF7FFFu, v[c].y & 0x7FFF7FFFu)),
+                          __vmaxu2(v[c].z & 0x7FFF7FFFu, v[c].w & 0x7FFF7FFFu));
+          int f;
+          const QueryLift lift(max(mx & 0xFFFFu, mx >> 16), f);
+          uint8_t* const line = smem + s * C::kQTile + trow * 128;
+#pragma unroll
+          for (int c = 0; c < D / 8; ++c)
+            *reinterpret_cast<uint4*>(line + (c >> 3) * (BM * 128) + (((c & 7) ^ (trow & 7)) << 4)) = lift(v[c]);
+          q_lift[s * BM + trow] = (int8_t)f;
+        }
+        fence_async_shared();
+        bar_named(2 + s, 128);
+        if (trow == 0 && ok && pc.tiles > 0 && !p.withhold_q) mbar_arrive(q_full + s);
+      }
+    }
     for (int i = 0;; ++i) {
       ok = ok && pieces.get(i, pc, abort_flag, p.timeout_ns);
       if (!bar_all(6, ok && pc.tiles > 0)) break;  // (all eight warps go on, or none)
