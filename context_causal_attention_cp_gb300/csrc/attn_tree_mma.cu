@@ -26,8 +26,8 @@
 // NaN by its sum.
 //
 // Measured, 32/8 heads, d = 128, 32 requests on up to 16K keys: trees of 32 (single units) 205 us,
-// HBM (floor 193); trees of 64 (dual) 261 us (floor 194): the tensor pipe is active 57 % of the
-// time, a stream's chain S -> softmax -> P -> P V is what bounds them.  Over codes 293 and 431 us
+// HBM (floor 193); trees of 64 (dual) 251 us (floor 194): the tensor pipe is active 57 % of the
+// time, a stream's chain S -> softmax -> P -> P V is what bounds them.  Over codes 278 and 399 us
 // (floors 100 and 130): the same chain with S in halves, beside the converters.
 #include <algorithm>
 #include <atomic>
@@ -437,12 +437,24 @@ attn_tree_mma_kernel(const __grid_constant__ TreeMaps maps, const TreeParams p) 
       };
       auto commit = [&](uint64_t* bar) { mma_commit_lead(lead, bar); };
       auto wait = [&](uint64_t* bar, int parity) { return wait_warp(bar, parity, abort_flag, p.timeout_ns); };
+      // P of a stream with the tile's V and, where it follows at once, the next K: every look at
+      // a barrier is some 100 cycles in which the tensor core runs dry.
+      auto wait_pv = [&](uint64_t* p_bar, int parity, uint64_t* v_bar, int v_parity, uint64_t* k_bar, int k_parity) {
+        uint64_t t0 = 0;
+        for (uint32_t i = 1;; ++i) {
+          const bool x = mbar_try_wait(p_bar, parity), y = mbar_try_wait(v_bar, v_parity);
+          const bool z = mbar_try_wait(k_bar, k_parity);
+          if (__all_sync(0xffffffffu, x && y && z)) return true;
+          if (i % kPollsPerCheck == 0 && __shfl_sync(0xffffffffu, (int)give_up(t0, abort_flag, p.timeout_ns), 0))
+            return false;
+        }
+      };
       // Tiles of the pieces for the products Q K^T, which run ahead, and P V.
       int left_q = 0, left_v = 0;  // tiles of the piece behind the one at hand
       int piece_q = -1, piece_v = -1;
       uint32_t k_at = 0, v_at = DUAL ? 1 : 2;  // ring slots, and their phases
       uint32_t k_phase = 0, v_phase = 0;
-      bool head_q = false, ok = true;
+      bool ok = true;
       bool head_v[2] = {false, false};
       auto advance = [&](uint32_t& slot, uint32_t& phase, uint32_t by) {
         slot += by;
@@ -455,8 +467,7 @@ attn_tree_mma_kernel(const __grid_constant__ TreeMaps maps, const TreeParams p) 
       auto tiles_of = [&](int i) { return __shfl_sync(0xffffffffu, pieces.at[i % kPieces].tiles, 0); };
       // The next tile's queries and K; false when there is none, or a wait ran out.
       auto next_q = [&]() {
-        head_q = left_q == 0;
-        if (head_q) {
+        if (left_q == 0) {
           ++piece_q;
           const int buf = DUAL ? 0 : piece_q & 1;
           ok = wait(q_full + buf, (DUAL ? piece_q : piece_q >> 1) & 1);
@@ -469,7 +480,8 @@ attn_tree_mma_kernel(const __grid_constant__ TreeMaps maps, const TreeParams p) 
         ok = ok && wait(full + k_at, k_phase);
         return ok;
       };
-      // (there is one wherever there was a next_q that has not been followed)
+      // The next tile's V, its wait left to wait_pv (there is one wherever there was a next_q that
+      // has not been followed).
       auto next_v = [&]() {
         if (left_v == 0) {
           ++piece_v;
@@ -477,7 +489,6 @@ attn_tree_mma_kernel(const __grid_constant__ TreeMaps maps, const TreeParams p) 
           head_v[0] = head_v[1] = true;
         }
         --left_v;
-        return wait(full + v_at, v_phase);
       };
       if constexpr (DUAL) {
         auto begin = [&](int s) {
@@ -497,18 +508,18 @@ attn_tree_mma_kernel(const __grid_constant__ TreeMaps maps, const TreeParams p) 
           begun();
         }
         for (int n = 0; more && ok; ++n) {
-          ok = next_v();
+          next_v();
           const bool last = left_v == 0;
-          ok = ok && wait(p_full, n & 1);
+          // (a next piece's queries may still be on their way: they do not hold up stream 1)
+          const bool turn = left_q > 0;
+          uint64_t* const v_bar = full + v_at;
+          ok = wait_pv(p_full, n & 1, v_bar, v_phase, turn ? full + k_at : v_bar, turn ? k_phase : v_phase);
           if (!ok) break;
           tc_fence_after();
           issue_pv(0, v_at, head_v[0]);
           if (last) commit(o_full);
-          // (a next piece's queries may still be on their way: they do not hold up stream 1)
-          const bool turn = left_q > 0;
           if (turn) {
-            more = next_q();
-            if (!ok) break;
+            --left_q;
             begin(0);
           }
           ok = wait(p_full + 1, n & 1);
@@ -545,7 +556,11 @@ attn_tree_mma_kernel(const __grid_constant__ TreeMaps maps, const TreeParams p) 
         }
         for (int n = 0; n < ahead && ok; ++n) {
           const int s = n & 1;
-          ok = next_v() && wait(p_full + s, (n >> 1) & 1);
+          next_v();
+          // (bf16 tiles come at the rate of HBM: a K on its way does not hold up the P V before it)
+          const bool early = QUANT && left_q > 0;
+          uint64_t* const v_bar = full + v_at;
+          ok = wait_pv(p_full + s, (n >> 1) & 1, v_bar, v_phase, early ? full + k_at : v_bar, early ? k_phase : v_phase);
           if (!ok) break;
           tc_fence_after();
           issue_pv(s, v_at, head_v[s]);
@@ -553,7 +568,10 @@ attn_tree_mma_kernel(const __grid_constant__ TreeMaps maps, const TreeParams p) 
           if (left_v < 2) commit(o_full + s);
           commit(empty + v_at);
           advance(v_at, v_phase, 2);
-          if (more) {
+          if (early) {
+            --left_q;
+            begin(s);
+          } else if (more) {
             more = next_q();
             if (more) begin(s);
           }
