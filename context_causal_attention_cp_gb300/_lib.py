@@ -62,6 +62,7 @@ class SharedPlanInfo(ctypes.Structure):
 KV_CODES = struct.Struct("@2P3q")               # cp_kv_codes_t
 ROPE_ARGS = struct.Struct("@6P9q6i")            # cp_rope_args_t
 KV_APPEND_ARGS = struct.Struct("@7P9q7i")       # cp_kv_append_args_t
+TREE_LAYOUT_ARGS = struct.Struct("@8Pq5i")      # cp_tree_layout_args_t
 ATTN_TREE_ARGS = struct.Struct("@13P9q13if")    # cp_attn_tree_args_t
 
 # name -> (restype, argtypes); must match include/cpattn.h
@@ -122,7 +123,7 @@ SIGNATURES = {
     "cp_rope_table": (i32, [vp, vp, i32, vp]),
     "cp_rope": (i32, [ctypes.POINTER(RopeInfo), ctypes.c_char_p, vp]),
     "cp_kv_append": (i32, [ctypes.POINTER(RopeInfo), vp, vp, ctypes.c_char_p, vp]),
-    "cp_tree_layout": (i32, [vp, vp, i32, vp, i64, i32, i32, vp, i32, i32, vp, vp, vp, vp, vp]),
+    "cp_tree_layout": (i32, [ctypes.c_char_p, vp]),
     "cp_tree_workspace_size": (i32, [i32, i32, i32, i32, i32, ctypes.POINTER(i64)]),
     "cp_attn_tree": (i32, [ctypes.c_char_p, vp]),
     "cp_attn_debug": (i32, [i32, ctypes.c_longlong]),

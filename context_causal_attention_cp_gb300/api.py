@@ -737,6 +737,9 @@ def cp_select_pass_cost(new_tokens: int, cached_tokens: int, Hq: int, Hkv: int, 
     return ("pass_q" if r == L.PASS_Q else "pass_kv"), ekv.value, eq.value
 
 
+_I32 = torch.int32
+
+
 # --------------------------------------------------------- quantised KV cache --
 # A decode step calls these once a layer, with kernels of a few microseconds: their
 # checks look at each tensor once and leave the messages to the failing path.
@@ -1135,11 +1138,11 @@ def make_rope(inv_freq, *, axes=None, first=0, interleaved=False, device="cuda")
 
 def _positions(rope, positions, n, index):
     """Check the positions of n rows; their address and axis stride."""
-    if not isinstance(positions, torch.Tensor) or positions.dtype is not torch.int32 or \
+    if not isinstance(positions, torch.Tensor) or positions.dtype is not _I32 or \
             positions.get_device() != index:
         _bad(positions, "positions", torch.int32, index)
     shape, axes = positions.shape, rope.axes
-    if shape != (axes, n) and not (axes == 1 and shape == (n,)):
+    if shape != (n,) if axes == 1 and len(shape) == 1 else shape != (axes, n):
         raise ValueError(f"positions must be [{axes}, {n}], got {tuple(shape)}")
     strides = positions.stride()
     if strides[-1] != 1 and n > 1:
@@ -1155,10 +1158,13 @@ def _rotated(x, out, name, dtype, n, d, index, stream):
     H = x.shape[1]
     shape = (n, H, d)
     rs, hs = _new_rows(x, name, dtype, shape, index)
-    if out is None:
-        out = _empty(shape, dtype, x.device, stream)
-    ors, ohs = _new_rows(out, "out_" + name, dtype, shape, index)
-    if (n > 1 and ors == 0 and H) or (H > 1 and ohs == 0 and n):
+    if out is x:  # (in place)
+        ors, ohs = rs, hs
+    else:
+        if out is None:
+            out = _empty(shape, dtype, x.device, stream)
+        ors, ohs = _new_rows(out, "out_" + name, dtype, shape, index)
+    if (ors == 0 and n > 1 and H) or (ohs == 0 and H > 1 and n):
         raise ValueError(f"out_{name} needs a place for each element")
     return out, H, x.data_ptr(), rs, hs, out.data_ptr(), ors, ohs
 
@@ -1261,12 +1267,13 @@ def cp_kv_append(cache, k, v=None, slots=None, *, rope: Optional[Rope] = None, p
 def _batch(q_start, kv_lens, page_table, index):
     """Check a paged batch's arrays; their addresses, and the batch's and table's sizes."""
     for t, name in ((q_start, "q_start"), (kv_lens, "kv_lens"), (page_table, "page_table")):
-        if not isinstance(t, torch.Tensor) or t.dtype is not torch.int32 or t.get_device() != index:
+        if not isinstance(t, torch.Tensor) or t.dtype is not _I32 or t.get_device() != index:
             _bad(t, name, torch.int32, index)
-    B, width = page_table.shape if page_table.dim() == 2 else (-1, 0)
+    shape = page_table.shape
+    B, width = shape if len(shape) == 2 else (-1, 0)
     if kv_lens.shape != (B,) or q_start.shape != (B + 1,):
         raise ValueError("page_table must be [requests, pages], kv_lens [requests] and q_start "
-                         f"[requests + 1], got {tuple(page_table.shape)}, {tuple(kv_lens.shape)} "
+                         f"[requests + 1], got {tuple(shape)}, {tuple(kv_lens.shape)} "
                          f"and {tuple(q_start.shape)}")
     stride, step = page_table.stride()
     if (step != 1 and width > 1 and B) or not kv_lens.is_contiguous() or not q_start.is_contiguous():
@@ -1286,7 +1293,7 @@ def cp_tree_layout(q_start, kv_lens, page_table, page_size, num_rows, *, parents
     made, the mask with bits for ``max_nodes`` rows a request.  Returns (slots [num_rows],
     positions [num_rows], mask [num_rows, words] or None).
     """
-    if not isinstance(q_start, torch.Tensor) or not q_start.is_cuda:
+    if not isinstance(q_start, torch.Tensor) or q_start.get_device() < 0:
         raise ValueError("q_start must be a CUDA int32 tensor")
     index, n = q_start.get_device(), int(num_rows)
     batch = _batch(q_start, kv_lens, page_table, index)
@@ -1305,21 +1312,22 @@ def cp_tree_layout(q_start, kv_lens, page_table, page_size, num_rows, *, parents
     words = 0
     if mask is not None:
         words = _mask_words(mask, n, index)
-    _call(index, stream, L.load().cp_tree_layout, "cp_tree_layout", *batch, int(page_size),
-          _vector(parents, "parents", torch.int32, n, index), n, words,
-          _vector(slots, "slots", torch.int32, n, index),
-          _vector(positions, "positions", torch.int32, n, index),
-          None if mask is None else mask.data_ptr(),
-          _vector(status, "status", torch.int32, 1, index))
+    at_q, at_len, B, at_table, stride, width = batch
+    _call(index, stream, L.load().cp_tree_layout, "cp_tree_layout", L.TREE_LAYOUT_ARGS.pack(
+        at_q, at_len, at_table, _vector(parents, "parents", _I32, n, index) or 0,
+        _vector(slots, "slots", _I32, n, index), _vector(positions, "positions", _I32, n, index),
+        0 if mask is None else mask.data_ptr(), _vector(status, "status", _I32, 1, index) or 0,
+        stride, B, width, int(page_size), n, words))
     return slots, positions, mask
 
 
 def _mask_words(mask, n, index):
-    if not isinstance(mask, torch.Tensor) or mask.dtype is not torch.int32 or mask.get_device() != index:
+    if not isinstance(mask, torch.Tensor) or mask.dtype is not _I32 or mask.get_device() != index:
         _bad(mask, "mask", torch.int32, index)
-    if mask.dim() != 2 or mask.shape[0] != n or mask.shape[1] < 1 or not mask.is_contiguous():
+    shape = mask.shape
+    if len(shape) != 2 or shape[0] != n or shape[1] < 1 or not mask.is_contiguous():
         raise ValueError(f"mask must be contiguous [{n}, words]")
-    return mask.shape[1]
+    return shape[1]
 
 
 _SMS = {}  # of a device, by its index
@@ -1363,7 +1371,7 @@ def cp_attn_tree(q, k, v, page_table, page_size, q_start, kv_lens, scale, *, mas
     heads and max_nodes, allocated when omitted.  Returns (O [N, Hq, d], LSE [N, Hq],
     workspace).
     """
-    if not isinstance(q, torch.Tensor) or not q.is_cuda or q.dim() != 3:
+    if not isinstance(q, torch.Tensor) or q.get_device() < 0 or q.dim() != 3:
         raise ValueError("q must be a CUDA tensor [rows, Hq, d]")
     index = q.get_device()
     quant = k_scale is not None

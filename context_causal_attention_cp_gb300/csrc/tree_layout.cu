@@ -100,38 +100,38 @@ __global__ void __launch_bounds__(kThreads) tree_layout_kernel(const LayoutParam
 
 using namespace cpattn;
 
-extern "C" int cp_tree_layout(const int32_t* q_start, const int32_t* kv_lens, int num_reqs,
-                              const int32_t* page_table, int64_t table_stride, int max_pages, int page_size,
-                              const int32_t* parents, int num_rows, int mask_words, int32_t* slots,
-                              int32_t* positions, int32_t* mask, int32_t* status_dev, cudaStream_t stream) {
+extern "C" int cp_tree_layout(const cp_tree_layout_args_t* a, cudaStream_t stream) {
   CPATTN_TRACE("cp_tree_layout");
-  if (num_reqs < 0 || num_reqs > CPATTN_MAX_REQS || num_rows < 0 || max_pages < 0 || mask_words < 0 ||
-      (parents != nullptr) != (mask != nullptr && mask_words > 0) || (mask && !parents))
+  if (!a) return CPATTN_ERR_INVALID_ARG;
+  if (a->num_reqs < 0 || a->num_reqs > CPATTN_MAX_REQS || a->num_rows < 0 || a->max_pages < 0 || a->mask_words < 0 ||
+      (a->parents != nullptr) != (a->mask != nullptr && a->mask_words > 0) || (a->mask && !a->parents))
     return CPATTN_ERR_INVALID_ARG;
-  if (page_size < 16 || page_size > 65536 || (page_size & (page_size - 1))) return CPATTN_ERR_UNSUPPORTED;
-  if (num_reqs > 1 && table_stride < max_pages) return CPATTN_ERR_INVALID_ARG;
-  for (const void* at : {(const void*)q_start, (const void*)kv_lens, (const void*)page_table, (const void*)parents,
-                         (const void*)slots, (const void*)positions, (const void*)mask, (const void*)status_dev})
+  if (a->page_size < 16 || a->page_size > 65536 || (a->page_size & (a->page_size - 1))) return CPATTN_ERR_UNSUPPORTED;
+  if (a->num_reqs > 1 && a->table_stride < a->max_pages) return CPATTN_ERR_INVALID_ARG;
+  for (const void* at : {(const void*)a->q_start, (const void*)a->kv_lens, (const void*)a->page_table,
+                         (const void*)a->parents, (const void*)a->slots, (const void*)a->positions,
+                         (const void*)a->mask, (const void*)a->status_dev})
     if (reinterpret_cast<uintptr_t>(at) & 3u) return CPATTN_ERR_ALIGNMENT;
-  if (num_rows == 0) return CPATTN_OK;
-  if (!slots || !positions || (num_reqs > 0 && (!q_start || !kv_lens || (max_pages > 0 && !page_table))))
+  if (a->num_rows == 0) return CPATTN_OK;
+  if (!a->slots || !a->positions ||
+      (a->num_reqs > 0 && (!a->q_start || !a->kv_lens || (a->max_pages > 0 && !a->page_table))))
     return CPATTN_ERR_INVALID_ARG;
   LayoutParams p{};
-  p.q_start = q_start;
-  p.kv_lens = kv_lens;
-  p.page_table = page_table;
-  p.table_stride = table_stride;
-  p.parents = parents;
-  p.slots = slots;
-  p.positions = positions;
-  p.mask = mask;
-  p.status = status_dev;
-  p.num_reqs = num_reqs;
-  p.max_pages = max_pages;
-  for (p.log_page = 4; (1 << p.log_page) < page_size; ++p.log_page) {}
-  p.num_rows = num_rows;
-  p.words = mask_words;
-  const unsigned pad = (unsigned)std::min<long long>(((long long)num_rows + kThreads - 1) / kThreads, 32);
-  tree_layout_kernel<<<num_reqs + pad, kThreads, 0, stream>>>(p);
+  p.q_start = a->q_start;
+  p.kv_lens = a->kv_lens;
+  p.page_table = a->page_table;
+  p.table_stride = a->table_stride;
+  p.parents = a->parents;
+  p.slots = a->slots;
+  p.positions = a->positions;
+  p.mask = a->mask;
+  p.status = a->status_dev;
+  p.num_reqs = a->num_reqs;
+  p.max_pages = a->max_pages;
+  for (p.log_page = 4; (1 << p.log_page) < a->page_size; ++p.log_page) {}
+  p.num_rows = a->num_rows;
+  p.words = a->mask_words;
+  const unsigned pad = (unsigned)std::min<long long>(((long long)a->num_rows + kThreads - 1) / kThreads, 32);
+  tree_layout_kernel<<<a->num_reqs + pad, kThreads, 0, stream>>>(p);
   return cudaGetLastError() == cudaSuccess ? CPATTN_OK : CPATTN_ERR_CUDA;
 }

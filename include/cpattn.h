@@ -753,10 +753,13 @@ int cp_kv_append(const cp_rope_t* rope, const cp_kv_codes_t* k_cache, const cp_k
  * (< 0), a parent that is not below its node and a node without a bit (>= 32 *
  * mask_words) set CPATTN_ERR_RANGE; such a request's or node's slot is -1, such a parent
  * counts as none. */
-int cp_tree_layout(const int32_t* q_start, const int32_t* kv_lens, int num_reqs,
-                   const int32_t* page_table, int64_t table_stride, int max_pages, int page_size,
-                   const int32_t* parents, int num_rows, int mask_words, int32_t* slots,
-                   int32_t* positions, int32_t* mask, int32_t* status_dev, cudaStream_t stream);
+typedef struct {
+  const int32_t *q_start, *kv_lens, *page_table, *parents;
+  int32_t *slots, *positions, *mask, *status_dev;
+  int64_t table_stride;
+  int32_t num_reqs, max_pages, page_size, num_rows, mask_words;
+} cp_tree_layout_args_t;
+int cp_tree_layout(const cp_tree_layout_args_t* args, cudaStream_t stream);
 
 /* Attention of the new rows over the paged cache.  Row i of request b sees the cached keys
  * 0 .. kv_lens[b]-1 and the new keys kv_lens[b]+j of the nodes j that its mask names (mask

@@ -137,19 +137,24 @@ def test_append_refusals():
     })
 
 
-LAYOUT = dict(q_start=0x10000, kv_lens=0x20000, reqs=2, table=0x30000, stride=8, pages=8, page=16, parents=0x40000, n=5,
-              words=1, slots=0x50000, positions=0x60000, mask=0x70000, status=None, stream=None)
+LAYOUT = dict(q_start=0x10000, kv_lens=0x20000, table=0x30000, parents=0x40000, slots=0x50000, positions=0x60000,
+              mask=0x70000, status=0, stride=8, reqs=2, pages=8, page=16, n=5, words=1)
 
 
 def test_layout_refusals():
-    refused(lambda **kw: L.load().cp_tree_layout(*{**LAYOUT, **kw}.values()), {
-        BAD: (dict(q_start=None), dict(kv_lens=None), dict(table=None), dict(slots=None), dict(positions=None),
-              dict(mask=None), dict(parents=None), dict(words=0), dict(words=-1), dict(parents=None, mask=None, words=-1),
-              dict(reqs=-1), dict(reqs=1 << 24), dict(n=-1), dict(pages=-1), dict(stride=7)),
+    def call(**kw):
+        assert set(kw) <= set(LAYOUT)
+        return L.load().cp_tree_layout(L.TREE_LAYOUT_ARGS.pack(*{**LAYOUT, **kw}.values()), None)
+
+    assert L.load().cp_tree_layout(None, None) == BAD
+    refused(call, {
+        BAD: (dict(q_start=0), dict(kv_lens=0), dict(table=0), dict(slots=0), dict(positions=0), dict(mask=0),
+              dict(parents=0), dict(words=0), dict(words=-1), dict(parents=0, mask=0, words=-1), dict(reqs=-1),
+              dict(reqs=1 << 24), dict(n=-1), dict(pages=-1), dict(stride=7)),
         KIND: (dict(page=0), dict(page=8), dict(page=24), dict(page=-16), dict(page=1 << 17)),
         ALIGN: (dict(q_start=0x10002), dict(kv_lens=0x20001), dict(table=0x30002), dict(parents=0x40002),
                 dict(slots=0x50001), dict(positions=0x60002), dict(mask=0x70001), dict(status=0x80002)),
-        L.OK: (dict(n=0), dict(n=0, slots=None, positions=None, q_start=None)),
+        L.OK: (dict(n=0), dict(n=0, slots=0, positions=0, q_start=0)),
     })
 
 
@@ -210,6 +215,7 @@ def test_structures_are_those_of_c(tmp_path):
     assert L.KV_CODES.size == ctypes.sizeof(L.KvCodes)
     kinds = (("cp_rope_args_t", L.ROPE_ARGS, ("q_row_stride", "num_rows", "inverse")),
              ("cp_kv_append_args_t", L.KV_APPEND_ARGS, ("k_row_stride", "num_rows", "x_is_fp32")),
+             ("cp_tree_layout_args_t", L.TREE_LAYOUT_ARGS, ("table_stride", "num_reqs", "mask_words")),
              ("cp_attn_tree_args_t", L.ATTN_TREE_ARGS, ("q_row_stride", "num_rows", "scale")))
     body = "".join(f'  printf("%zu", sizeof({c}));\n' + "".join(
         f'  printf(" %zu", offsetof({c}, {f}));\n' for f in fields) + '  printf("\\n");\n' for c, _, fields in kinds)
@@ -223,7 +229,7 @@ def test_structures_are_those_of_c(tmp_path):
         size, first, ints, last = (int(x) for x in line.split())
         head, rest = packed.format.lstrip("@").split("P")
         longs, tail = rest.split("q")
-        assert first == 8 * int(head) and ints == first + 8 * int(longs), name
+        assert first == 8 * int(head) and ints == first + 8 * int(longs or 1), name
         assert last == packed.size - 4 and size == -(-packed.size // 8) * 8, name
 
 
