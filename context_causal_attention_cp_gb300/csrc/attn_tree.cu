@@ -160,14 +160,14 @@ int unit_rows_of(int g, int max_nodes) {
   return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= BM ? BM : 2 * BM;
 }
 
-bool plan_sizes(int Hq, int Hkv, int dv, int max_nodes, int num_ctas, int* unit_rows, int64_t* o_at, int64_t* l_at,
+// Where the parts of a workspace lie, and its size.
+void plan_sizes(int Hq, int Hkv, int dv, int max_nodes, int num_ctas, int* unit_rows, int64_t* o_at, int64_t* l_at,
                 int64_t* bytes) {
   *unit_rows = unit_rows_of(Hq / Hkv, max_nodes);
   const int64_t rows = 2LL * num_ctas * *unit_rows;
   *o_at = 32LL * num_ctas;  // behind the cut units
   *l_at = *o_at + rows * dv * 4;
   *bytes = (*l_at + rows * 4 + 31) & ~31LL;
-  return true;
 }
 
 }  // namespace

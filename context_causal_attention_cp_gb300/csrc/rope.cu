@@ -12,11 +12,12 @@
 // two 16-byte chunks (of bf16) that hold 8 pairs, or 16 columns that are not rotated.  A
 // group of lanes takes vectors of one row, some at a time: it starts their loads, computes
 // its part of the block's cos and sin (into shared memory: they serve all heads) while these
-// are on their way, and then rotates, rounds or quantises.  Measured: 8192 rows of 40 heads of
-// 128 (bf16) 32.2 us, 5.2 TB/s; fp32 56 us, 6.0 TB/s; 4096 rows into an e4m3 cache 23.4 us; 16384
-// rows of 576 columns 12.1 us, 3.1 TB/s (a vector is three items of 16 lanes, one row a group: what
-// is in flight; with the rows' cos and sin computed by 32 of the threads 35.8 us); 64 rows 3.2 us,
-// the launch.  About 190 instructions a warp and item hold the issue slots half of the time.
+// are on their way, and then rotates, rounds or quantises.  Q, K and V have code of their own (one
+// code for all, with the side looked up for each vector: 32.1 against 30.3 us).  Measured: 8192
+// rows of 40 heads of 128 (bf16) 30.3 us, 5.5 TB/s; fp32 54.6 us, 6.2 TB/s; 4096 rows into an e4m3
+// cache 22.5 us; 16384 rows of 576 columns 12.6 us, 3.0 TB/s (a vector is three items of 16 lanes,
+// one row a group: what is in flight; with the rows' cos and sin computed by 32 of the threads
+// 35.8 us); 64 rows 3.2 us, the launch.
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
@@ -48,7 +49,6 @@ struct RopeSide {  // Q, K or V; strides in 16 bytes
   float* scales;  // codes' scales, or null
   long long s_head;
   int heads, dim;
-  int rotated;  // whether the table's pairs are
   int cached;   // rows go to their slots, as bf16 or codes; else to their own place, in x's type
 };
 
@@ -129,100 +129,88 @@ __device__ __forceinline__ void store8_codes(uint8_t* at, const float* f, float 
   *reinterpret_cast<uint2*>(at) = make_uint2(w[0], w[1]);
 }
 
-// NI: items of a lane.  INTER: pairs are neighbours (a rotated item's chunks then lie
-// side by side); else (c, c + pairs).
-template <bool F32, bool INTER, int NI>
-__global__ void __launch_bounds__(kThreads, NI != 1 || F32 ? 2 : 3) rope_kernel(const RopeParams p) {
-  constexpr int U = units_at_once(F32, NI), kSize = F32 ? 4 : 2;
-  // (c, c', s, s') of pairs 8 j + 2 k, 8 j + 2 k + 1 of row r at [r][k][j]: lanes j side by side
-  __shared__ float4 cs[kMaxCs / 2];
-  const int L = 1 << p.log_l, lane = threadIdx.x & (L - 1), group = threadIdx.x >> p.log_l;
-  const uint32_t mask = (L == 32 ? 0xffffffffu : (1u << L) - 1u) << (threadIdx.x & 31 & ~(L - 1));
-  const int h0 = p.side[0].heads, h1 = h0 + p.side[1].heads, eighths = p.pairs / 8;
-  const long long r0 = (long long)blockIdx.x * p.rows;
-  const int split = 1 << p.log_split, sub = group & (split - 1), r = group >> p.log_split;
-  const int rows = (int)min((long long)p.rows, p.num_rows - r0);
-  const bool live = r < rows;
-  const uint32_t row = (uint32_t)(r0 + (live ? r : 0));
-  // the row's place in the caches
-  int to = (int)row;
-  if (live && p.slots) to = __ldg(p.slots + row);
-  // byte offsets of the chunks of items in vectors that are rotated (others: 16 columns)
-  int c0[NI], c1[NI];
-#pragma unroll
-  for (int i = 0; i < NI; ++i) {
-    const int j = lane + i * L;
-    if (j < eighths) {
-      c0[i] = p.first + j * (INTER ? 16 : 8);
-      c1[i] = c0[i] + (INTER ? 8 : p.pairs);
-    } else {
-      const int n = 2 * (j - eighths), head = p.first / 8;  // chunks before the rotated ones
-      c0[i] = 8 * (n < head ? n : n + 2 * eighths);
-      c1[i] = 8 * (n + 1 < head ? n + 1 : n + 1 + 2 * eighths);
+// A group's way through the heads of a side: head h of its row, h + 2^log_split, ...  What a side
+// is not (Q and not cached, V and not rotated) falls away in its copy of the code.
+template <bool F32, bool INTER, int NI, int SIDE>
+struct RopeWalk {
+  static constexpr int U = units_at_once(F32, NI), kSize = F32 ? 4 : 2;
+  const RopeParams& p;
+  const uint8_t* x;
+  uint8_t* y;
+  float* scale;
+  long long x_step, y_step, s_step;
+  int h, lane;
+  bool live;  // the row is one, and has a place here
+
+  __device__ __forceinline__ const RopeSide& side() const { return p.side[SIDE]; }
+  __device__ __forceinline__ bool cached() const { return SIDE == 2 || (SIDE == 1 && side().cached); }
+  __device__ __forceinline__ bool rotated() const { return SIDE < 2 && p.pairs > 0; }
+  __device__ __forceinline__ bool more() const { return live && h < side().heads; }
+
+  // first: heads of the sides before this one (the vectors of a row are dealt in order).
+  __device__ __forceinline__ RopeWalk(const RopeParams& params, int first, int sub, int lane_, uint32_t row, bool live_)
+      : p(params), lane(lane_), live(live_) {
+    const RopeSide& s = side();
+    h = (sub - first) & ((1 << p.log_split) - 1);
+    x = s.x + (((unsigned long long)row * s.x_row + (unsigned long long)h * s.x_head) << 4);
+    x_step = (long long)s.x_head << (4 + p.log_split);
+  }
+  // The outputs; slot: the row's place in the caches (looked at here, when loads are on their way).
+  __device__ __forceinline__ void place(uint32_t row, int slot) {
+    const RopeSide& s = side();
+    const int to = cached() ? slot : (int)row;
+    if (cached() && (uint32_t)to >= (uint32_t)p.cache_rows) {
+      if (live && to >= 0 && lane == 0 && h < s.heads) set_status(p.status, CPATTN_ERR_RANGE);
+      live = false;
+    }
+    y = s.y + (((unsigned long long)(uint32_t)to * s.y_row + (unsigned long long)h * s.y_head) << 4);
+    y_step = (long long)s.y_head << (4 + p.log_split);
+    if (SIDE > 0) {
+      scale = s.scales + (h * s.s_head + to);
+      s_step = s.s_head << p.log_split;
     }
   }
-  // vector vec of a row: a head of one of the sides
-  auto side_of = [&](int vec, uint32_t& h) -> const RopeSide& {
-    const int i = (vec >= h0) + (vec >= h1);
-    h = vec - (i == 0 ? 0 : i == 1 ? h0 : h1);
-    return p.side[i];
-  };
-  constexpr int kKeep = NI == 1 ? 1 : 0;  // a lane's one item: its cos and sin in registers
-  float4 keep[4];
-  for (int base = 0; base < p.vectors; base += U << p.log_split) {  // (the same rounds in all threads)
-    Raw8<F32> raw[U][NI][2];
+  // Columns of item j's chunks.
+  __device__ __forceinline__ int2 columns(int j) const {
+    if (!rotated()) return make_int2(j * kItem, j * kItem + 8);
+    const int eighths = p.pairs / 8;
+    if (j < eighths) {
+      const int c = p.first + j * (INTER ? 16 : 8);
+      return make_int2(c, c + (INTER ? 8 : p.pairs));
+    }
+    const int n = 2 * (j - eighths), head = p.first / 8;  // chunks before the rotated ones
+    return make_int2(8 * (n < head ? n : n + 2 * eighths), 8 * (n + 1 < head ? n + 1 : n + 1 + 2 * eighths));
+  }
+  __device__ __forceinline__ void load(Raw8<F32> (&raw)[U][NI][2]) const {
 #pragma unroll
-    for (int x = 0; x < U; ++x) {
-      const int vec = base + (x << p.log_split) + sub;
-      if (!live || vec >= p.vectors) continue;
-      uint32_t h;
-      const RopeSide& s = side_of(vec, h);
-      const uint8_t* at = s.x + (((unsigned long long)row * s.x_row + (unsigned long long)h * s.x_head) << 4);
+    for (int u = 0; u < U; ++u)
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
-        const int j = lane + i * L;
-        if (j * kItem >= s.dim) continue;
-        raw[x][i][0].load(at + (s.rotated ? c0[i] : j * kItem) * kSize);
-        raw[x][i][1].load(at + (s.rotated ? c1[i] : j * kItem + 8) * kSize);
+        const int j = lane + (i << p.log_l);
+        if (!live || h + (u << p.log_split) >= side().heads || j * kItem >= side().dim) continue;
+        const int2 c = columns(j);
+        raw[u][i][0].load(x + u * x_step + c.x * kSize);
+        raw[u][i][1].load(x + u * x_step + c.y * kSize);
       }
-    }
-    if (base == 0 && p.pairs > 0) {
-      for (int i = threadIdx.x; i < rows * p.pairs; i += blockDim.x) {
-        const int at_row = i / p.pairs, c = i - at_row * p.pairs;
-        const int4 f = __ldg(p.table + c);
-        const bool ok = f.z >= 0 && f.z < p.axes;
-        if (!ok) set_status(p.status, CPATTN_ERR_RANGE);
-        const int at = ok ? __ldg(p.positions + f.z * p.axis_stride + r0 + at_row) : 0;
-        const float2 v = cos_sin(at, (uint32_t)f.x, (uint32_t)f.y);
-        float* const dst = reinterpret_cast<float*>(cs + (at_row * 4 + ((c >> 1) & 3)) * eighths + (c >> 3)) + (c & 1);
-        dst[0] = v.x;
-        dst[2] = p.inverse ? -v.y : v.y;
-      }
-      __syncthreads();
-      if (kKeep && live && lane < eighths)
+  }
+  // cs: cos and sin of the row (see the kernel); keep: those of a lane's one item.
+  __device__ __forceinline__ void store(const Raw8<F32> (&raw)[U][NI][2], const float4* cs, const float4 (&keep)[4],
+                                        uint32_t mask) {
+    const RopeSide& s = side();
+    const int eighths = p.pairs / 8;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) keep[k] = cs[(r * 4 + k) * eighths + lane];
-    }
-#pragma unroll
-    for (int x = 0; x < U; ++x) {
-      const int vec = base + (x << p.log_split) + sub;
-      if (!live || vec >= p.vectors) continue;
-      uint32_t h;
-      const RopeSide& s = side_of(vec, h);
-      if (s.cached && (uint32_t)to >= (uint32_t)p.cache_rows) {  // (the same in the vector's lanes)
-        if (to >= 0 && lane == 0) set_status(p.status, CPATTN_ERR_RANGE);
-        continue;
-      }
+    for (int u = 0; u < U; ++u) {
+      if (!live || h + (u << p.log_split) >= s.heads) continue;  // (the same in the vector's lanes)
       float f[NI][kItem];
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
-        raw[x][i][0].values(f[i]);
-        raw[x][i][1].values(f[i] + 8);
-        const int j = lane + i * L;
-        if (!s.rotated || j >= eighths) continue;
+        raw[u][i][0].values(f[i]);
+        raw[u][i][1].values(f[i] + 8);
+        const int j = lane + (i << p.log_l);
+        if (!rotated() || j >= eighths) continue;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const float4 v = kKeep ? keep[k] : cs[(r * 4 + k) * eighths + j];
+          const float4 v = NI == 1 ? keep[k] : cs[k * eighths + j];
           float& a0 = f[i][INTER ? 4 * k : 2 * k];
           float& a1 = f[i][INTER ? 4 * k + 2 : 2 * k + 1];
           float& b0 = f[i][INTER ? 4 * k + 1 : 2 * k + 8];
@@ -236,46 +224,114 @@ __global__ void __launch_bounds__(kThreads, NI != 1 || F32 ? 2 : 3) rope_kernel(
           b1 = bc1;
         }
       }
+      const bool codes = SIDE > 0 && s.scales;
       float inv = 1.f;
-      if (s.scales) {
+      if (codes) {
         // the largest finite element; the rotated value is rounded once, to its code
         auto largest = [&](bool finite) {
           float a = 0.f;
 #pragma unroll
           for (int i = 0; i < NI; ++i)
-            if ((lane + i * L) * kItem < s.dim)
+            if ((lane + (i << p.log_l)) * kItem < s.dim)
 #pragma unroll
               for (int e = 0; e < kItem; ++e) {
                 const float m = fabsf(f[i][e]);
                 a = fmaxf(a, !finite || m < INFINITY ? m : 0.f);
               }
-          for (int o = L >> 1; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(mask, a, o));
+          for (int o = 1 << p.log_l >> 1; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(mask, a, o));
           return a;
         };
         float a = largest(false);
         if (a == INFINITY) a = largest(true);  // (fmaxf leaves a NaN out by itself)
         const int e = scale_exponent(a);
         inv = exp2_int(-e);
-        if (lane == 0) s.scales[h * s.s_head + to] = exp2_int(e);
+        if (lane == 0) scale[u * s_step] = exp2_int(e);
       }
-      const uint32_t at_row = s.cached ? (uint32_t)to : row;
-      uint8_t* const y = s.y + (((unsigned long long)at_row * s.y_row + (unsigned long long)h * s.y_head) << 4);
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
-        const int j = lane + i * L;
+        const int j = lane + (i << p.log_l);
         if (j * kItem >= s.dim) continue;
-        const int y0 = s.rotated ? c0[i] : j * kItem, y1 = s.rotated ? c1[i] : j * kItem + 8;
-        if (s.scales) {
-          store8_codes(y + y0, f[i], inv);
-          store8_codes(y + y1, f[i] + 8, inv);
-        } else if (F32 && !s.cached) {
-          store8_f32(y + 4 * y0, f[i]);
-          store8_f32(y + 4 * y1, f[i] + 8);
+        const int2 c = columns(j);
+        uint8_t* const at = y + u * y_step;
+        if (codes) {
+          store8_codes(at + c.x, f[i], inv);
+          store8_codes(at + c.y, f[i] + 8, inv);
+        } else if (F32 && !cached()) {
+          store8_f32(at + 4 * c.x, f[i]);
+          store8_f32(at + 4 * c.y, f[i] + 8);
         } else {
-          store8_bf16(y + 2 * y0, f[i]);
-          store8_bf16(y + 2 * y1, f[i] + 8);
+          store8_bf16(at + 2 * c.x, f[i]);
+          store8_bf16(at + 2 * c.y, f[i] + 8);
         }
       }
+    }
+    h += U << p.log_split;
+    x += U * x_step;
+    y += U * y_step;
+    if (SIDE > 0) scale += U * s_step;
+  }
+};
+
+// NI: items of a lane.  INTER: pairs are neighbours (a rotated item's chunks then lie
+// side by side); else (c, c + pairs).
+template <bool F32, bool INTER, int NI>
+__global__ void __launch_bounds__(kThreads, NI != 1 || F32 ? 2 : 3) rope_kernel(const __grid_constant__ RopeParams p) {
+  constexpr int U = units_at_once(F32, NI);
+  // (c, c', s, s') of pairs 8 j + 2 k, 8 j + 2 k + 1 of row r at [r][k][j]: lanes j side by side
+  __shared__ float4 cs[kMaxCs / 2];
+  const int L = 1 << p.log_l, lane = threadIdx.x & (L - 1), group = threadIdx.x >> p.log_l;
+  const uint32_t mask = (L == 32 ? 0xffffffffu : (1u << L) - 1u) << (threadIdx.x & 31 & ~(L - 1));
+  const int h0 = p.side[0].heads, h1 = h0 + p.side[1].heads, eighths = p.pairs / 8;
+  const long long r0 = (long long)blockIdx.x * p.rows;
+  const int sub = group & ((1 << p.log_split) - 1), r = group >> p.log_split;
+  const int rows = (int)min((long long)p.rows, p.num_rows - r0);
+  const bool live = r < rows;
+  const uint32_t row = (uint32_t)(r0 + (live ? r : 0));
+  // the row's place in the caches
+  const int slot = live && p.slots ? __ldg(p.slots + row) : (int)row;
+  RopeWalk<F32, INTER, NI, 0> q(p, 0, sub, lane, row, live);
+  RopeWalk<F32, INTER, NI, 1> k(p, h0, sub, lane, row, live);
+  Raw8<F32> raw[U][NI][2];
+  if (h0 > 0) q.load(raw);
+  else k.load(raw);
+  if (p.pairs > 0) {
+    for (int i = threadIdx.x; i < rows * p.pairs; i += blockDim.x) {
+      const int at_row = i / p.pairs, c = i - at_row * p.pairs;
+      const int4 f = __ldg(p.table + c);
+      const bool ok = f.z >= 0 && f.z < p.axes;
+      if (!ok) set_status(p.status, CPATTN_ERR_RANGE);
+      const int at = ok ? __ldg(p.positions + f.z * p.axis_stride + r0 + at_row) : 0;
+      const float2 v = cos_sin(at, (uint32_t)f.x, (uint32_t)f.y);
+      float* const dst = reinterpret_cast<float*>(cs + (at_row * 4 + ((c >> 1) & 3)) * eighths + (c >> 3)) + (c & 1);
+      dst[0] = v.x;
+      dst[2] = p.inverse ? -v.y : v.y;
+    }
+    __syncthreads();
+  }
+  const float4* const mine = cs + r * 4 * eighths;
+  float4 keep[4];
+  if (NI == 1 && live && lane < eighths)
+#pragma unroll
+    for (int x = 0; x < 4; ++x) keep[x] = mine[x * eighths + lane];
+  k.place(row, slot);
+  if (h0 > 0) {
+    q.place(row, slot);
+    while (q.more()) {
+      q.store(raw, mine, keep, mask);
+      if (q.more()) q.load(raw);
+    }
+    if (k.more()) k.load(raw);
+  }
+  while (k.more()) {
+    k.store(raw, mine, keep, mask);
+    if (k.more()) k.load(raw);
+  }
+  if (p.side[2].heads > 0) {
+    RopeWalk<F32, INTER, NI, 2> v(p, h1, sub, lane, row, live);
+    v.place(row, slot);
+    while (v.more()) {
+      v.load(raw);
+      v.store(raw, mine, keep, mask);
     }
   }
 }
@@ -396,7 +452,6 @@ int rotated_side(RopeSide* s, const void* x, int64_t xr, int64_t xh, int heads, 
   s->y = static_cast<uint8_t*>(y);
   s->heads = heads;
   s->dim = d;
-  s->rotated = rope != nullptr;
   return strides16(s, xr * size, xh * size, yr * size, yh * size, num_rows, heads);
 }
 
@@ -419,7 +474,6 @@ int cached_side(RopeSide* s, const void* x, int64_t xr, int64_t xh, bool f32, in
   s->s_head = c->scale_stride;
   s->heads = heads;
   s->dim = dim;
-  s->rotated = rope != nullptr;
   s->cached = 1;
   const int in = f32 ? 4 : 2;
   return strides16(s, xr * in, xh * in, c->row_stride, c->head_stride, std::max(num_rows, cache_rows), heads);
