@@ -26,7 +26,7 @@
 // NaN by its sum.
 //
 // Measured, 32/8 heads, d = 128, 32 requests on up to 16K keys: trees of 32 (single units) 205 us,
-// HBM (floor 193); trees of 64 (dual) 251 us (floor 194): the tensor pipe is active 57 % of the
+// HBM (floor 193); trees of 64 (dual) 251 us (floor 194): the tensor pipe is active 61 % of the
 // time, a stream's chain S -> softmax -> P -> P V is what bounds them.  Over codes 278 and 399 us
 // (floors 100 and 130): the same chain with S in halves, beside the converters.
 #include <algorithm>
