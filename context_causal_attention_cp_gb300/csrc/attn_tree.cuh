@@ -100,9 +100,10 @@ struct TreeStart {
   int b;
 };
 
-// All threads of the block; sums: a word for each warp.
-__device__ __forceinline__ TreeStart tree_start(const TreeParams& p, long long* sums, long long* found) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+// All threads of the block, of WARPS warps; sums: a word for each, in shared memory as found's two.
+template <int WARPS>
+__device__ __forceinline__ TreeStart tree_start(const TreeParams& p, long long (&sums)[WARPS], long long* found) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int per = (p.num_reqs + blockDim.x - 1) / blockDim.x;
   const long long lo = (long long)threadIdx.x * per, hi = min((long long)p.num_reqs, lo + per);
   long long sum = 0;
@@ -122,7 +123,7 @@ __device__ __forceinline__ TreeStart tree_start(const TreeParams& p, long long* 
   if (lane == 31) sums[warp] = upto;
   __syncthreads();
   long long total = 0, before = 0;
-  for (int w = 0; w < warps; ++w) {
+  for (int w = 0; w < WARPS; ++w) {
     if (w == warp) before = total;
     total += sums[w];
   }

@@ -33,58 +33,10 @@
 #include <atomic>
 #include <type_traits>
 
-#include "attn_tree.cuh"
+#include "attn_tree_smem.cuh"
 
 namespace cpattn {
 namespace {
-
-constexpr int kKWarp = 8, kVWarp = 9, kMmaWarp = 10, kQWarp = 11, kConvertWarp = 12;
-constexpr int kConvertWarps = 8, kConvertThreads = 32 * kConvertWarps;
-
-constexpr int kPieces = 4;  // in the ring
-using Pieces = PieceRing<kPieces>;
-
-template <int D, bool QUANT, bool DUAL>
-struct MmaCfg {
-  static constexpr int kThreads = QUANT ? 640 : 384;
-  static constexpr int kRegsLaunch = QUANT ? 96 : 168;
-  // (e4m3 dual: with 128 and 72 the other warps spill, trees of 64 464 against 440 us; single:
-  // with 120 and 80 the softmax does, trees of 32 323 against 308 us)
-  static constexpr int kRegsSoftmax = !QUANT ? 200 : DUAL ? 120 : 128, kRegsOther = !QUANT ? 104 : DUAL ? 80 : 72;
-  static_assert(kRegsSoftmax * 256 + kRegsOther * (kThreads - 256) <= kRegsLaunch * kThreads,
-                "register split exceeds the launch allocation");
-  static constexpr int kQTile = BM * D * 2;
-  static constexpr int kTile = BN * D * 2;  // a K or V tile of 16-bit elements
-  static constexpr int kRawTile = BN * D;   // an e4m3 K or V tile
-  static constexpr int kStages = QUANT ? (D == 128 ? 3 : 6) : D == 128 ? 5 : 10;
-  static constexpr int kRawStages = !QUANT ? 0 : D == 64 ? 8 : 3;
-  static constexpr int kRingOff = 2 * kQTile;
-  static constexpr int kRawOff = kRingOff + kStages * kTile;
-  static constexpr int kScaleOff = kRawOff + kRawStages * kRawTile;  // of each raw row, and (K) of V's
-  static constexpr int kNoteOff = kScaleOff + kRawStages * BN * 8;   // RawNote of each raw tile
-  static constexpr int kExpOff = kNoteOff + kRawStages * 16;         // (ek, ev) of tiles n mod 8
-  static constexpr int kLiftOff = kExpOff + 64;                      // exponents of query rows, [2][2][BM]
-  static constexpr int kMlOff = kLiftOff + (QUANT ? 4 * BM : 0);     // single: (m, l) of each stream's rows
-  static constexpr int kEvOff = kMlOff + (DUAL ? 0 : 2 * BM * 8);    // and O's exponent
-  static constexpr int kBadOff = kEvOff + (QUANT && !DUAL ? 2 * BM : 0);  // value rows that are not finite
-  static constexpr int kPiecesOff = kBadOff + 2 * 2 * 16 + (QUANT ? kStages * 16 : 0);
-  static constexpr int kBarOff = kPiecesOff + (int)sizeof(Pieces);
-  static constexpr int kNumBars = 2 * kStages + 2 * kRawStages + 2 * 5 + 1;
-  static constexpr int kWordOff = kBarOff + kNumBars * 8;
-  static constexpr int kSumOff = (kWordOff + 64 + 7) & ~7;
-  static constexpr int kSmemBytes = kSumOff + 16 * 8;
-  static_assert(kBarOff % 8 == 0 && kSmemBytes <= 232448, "shared memory budget");
-  static constexpr int kTmemCols = 4 * 128;  // S of each stream, then O of each
-};
-
-// What a producer tells the converters about a raw tile.
-struct RawNote {
-  int live;   // rows up to the unit's end
-  int fresh;  // first row that is a new key
-  int first;  // of its piece and stream
-  int unused;
-};
-static_assert(sizeof(RawNote) == 16, "");
 
 // The MMAs and commits of ptx.cuh, by the lane with `lead` of a whole warp.
 __device__ __forceinline__ void mma_ss_lead(uint32_t lead, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
@@ -316,7 +268,8 @@ attn_tree_mma_kernel(const __grid_constant__ TreeMaps maps, const TreeParams p) 
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* issued = reinterpret_cast<volatile int*>(tmem_slot + 2);  // K and V tiles, for the abort drain
   long long* found = reinterpret_cast<long long*>(tmem_slot + 4);
-  long long* sums = reinterpret_cast<long long*>(smem + C::kSumOff);
+  auto& sums = *reinterpret_cast<long long (*)[C::kThreads / 32]>(smem + C::kSumOff);
+  static_assert(C::kSumOff + sizeof(sums) <= C::kSmemBytes, "shared memory of the launch");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if ((smem_u32(smem) & 1023u) != 0) {  // the swizzled tiles need it (no static shared memory: it holds)

@@ -28,46 +28,15 @@
 #include <algorithm>
 #include <atomic>
 
-#include "attn_tree.cuh"
+#include "attn_tree_smem.cuh"
 
 namespace cpattn {
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kThreads = 384;  // a third warpgroup: the loading warp and three that idle
+constexpr int kWarps = kSmallWarps;
+constexpr int kThreads = kSmallThreads;  // a third warpgroup: the loading warp and three that idle
 constexpr int kRegsLaunch = 168, kRegsWork = 208, kRegsOther = 88;
 static_assert(kRegsWork * 256 + kRegsOther * 128 <= kRegsLaunch * kThreads, "register split exceeds the launch's");
-constexpr int kMaxStages = 12;
-constexpr int kPieces = 4;  // in the ring
-using Pieces = PieceRing<kPieces>;
-
-template <int D, bool QUANT, int NQ>
-struct TreeCfg {
-  static constexpr int kRows = 8 * NQ;  // of a unit
-  static constexpr int kTeams = QUANT ? 2 : 1;
-  static constexpr int kKeys = BN * kTeams / kWarps;  // of a warp in its team's tiles
-  static constexpr int kTile = BN * D * (QUANT ? 1 : 2);
-  static constexpr int kScales = QUANT ? BN * 4 : 0;  // the rows' scales, fp32
-  static constexpr int kQ = kRows * D * 2;            // two of them
-  static constexpr int kJoin = kWarps * 8 * NQ * D * 4;
-  static constexpr int kMl = kWarps * 8 * NQ * 8;
-  static constexpr int kFixed = 2 * kQ + kJoin + kMl + (int)sizeof(Pieces) + (2 * kMaxStages + 4) * 8 + 64 + 256 + 1024;
-  static constexpr int kFit = (232448 - kFixed) / (kTile + kScales);
-  // With two teams a multiple of 4: K and V of the tiles n, n + kStages / 2, ... share slots, and
-  // then one team has them all, so that its warps see every phase of their barriers.
-  static constexpr int kMost = kFit < kMaxStages ? kFit : kMaxStages;
-  static constexpr int kStages = kTeams == 2 ? kMost / 4 * 4 : kMost;
-  static constexpr int kScaleOff = kStages * kTile;
-  static constexpr int kQOff = kScaleOff + kStages * kScales;
-  static constexpr int kJoinOff = kQOff + 2 * kQ;
-  static constexpr int kMlOff = kJoinOff + kJoin;  // (m, l) of each warp's rows
-  static constexpr int kPiecesOff = kMlOff + kMl;
-  static constexpr int kBarOff = kPiecesOff + (int)sizeof(Pieces);
-  static constexpr int kWordOff = kBarOff + (2 * kStages + 4) * 8;
-  static constexpr int kSumOff = kWordOff + 64;  // of tree_start
-  static constexpr int kSmemBytes = kSumOff + 256 + 1024;  // + align slack
-  static_assert(kStages >= 4 && kSmemBytes <= 232448, "shared memory budget");
-};
 
 // The 256 threads of the eight warps; true when any of them says so.
 __device__ __forceinline__ bool bar_warps(bool any) {
@@ -548,7 +517,8 @@ attn_tree_small_kernel(const __grid_constant__ TreeMaps maps, const TreeParams p
   volatile int* issued = abort_flag + 1;  // K and V tiles, for the abort drain
   Pieces& pieces = *reinterpret_cast<Pieces*>(smem + C::kPiecesOff);
   long long* found = reinterpret_cast<long long*>(smem + C::kWordOff + 16);
-  long long* sums = reinterpret_cast<long long*>(smem + C::kSumOff);
+  auto& sums = *reinterpret_cast<long long (*)[kThreads / 32]>(smem + C::kSumOff);
+  static_assert(C::kSumOff + sizeof(sums) + 1024 <= C::kSmemBytes, "shared memory of the launch");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   grid_dep_trigger();  // the merge may be scheduled as blocks of this grid end
   if (threadIdx.x == 0) {
