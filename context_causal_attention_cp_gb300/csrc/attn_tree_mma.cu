@@ -626,7 +626,7 @@ attn_tree_mma_kernel(const __grid_constant__ TreeMaps maps, const TreeParams p) 
                   int f;
                   const QueryLift lift(mx[y], f);
                   *reinterpret_cast<uint4*>(tile + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = lift(x[y]);
-                  if (c == 0) q_lift[((i & 1) * 2 + s) * BM + r] = (int8_t)f;
+                  if (c == 0) q_lift[i % C::kLifts * C::kLiftRows + s * BM + r] = (int8_t)f;
                 }
               }
             }
@@ -844,7 +844,7 @@ attn_tree_mma_kernel(const __grid_constant__ TreeMaps maps, const TreeParams p) 
         tc_fence_after();
         float sl2 = factor, o_scale = 1.f;
         if constexpr (QUANT) {
-          if (first && r < pc.rows) factor = p.scale_log2 * exp2_int(-q_lift[((i & 1) * 2 + (DUAL ? s : 0)) * BM + trow]);
+          if (first && r < pc.rows) factor = p.scale_log2 * exp2_int(-q_lift[i % C::kLifts * C::kLiftRows + r]);
           // written before the K tile went to the tensor core, and not again before this
           // step's P has been used
           const volatile int2* e = tile_exp + (n & 7);

@@ -32,8 +32,11 @@ struct MmaCfg {
   static constexpr int kScaleOff = kRawOff + kRawStages * kRawTile;  // of each raw row, and (K) of V's
   static constexpr int kNoteOff = kScaleOff + kRawStages * BN * 8;   // RawNote of each raw tile
   static constexpr int kExpOff = kNoteOff + kRawStages * 16;         // (ek, ev) of tiles n mod 8
-  static constexpr int kLiftOff = kExpOff + 64;                      // exponents of query rows, [2][2][BM]
-  static constexpr int kMlOff = kLiftOff + (QUANT ? 4 * BM : 0);     // single: (m, l) of each stream's rows
+  static constexpr int kLiftOff = kExpOff + 64;                      // exponents of query rows, [kLifts][units][BM]
+  // A place for each of the piece ring's: the softmax may look at a piece's exponents until it is
+  // done with the piece, which its place in the ring waits for and the queries' buffer does not.
+  static constexpr int kLifts = kPieces, kLiftRows = DUAL ? 2 * BM : BM;
+  static constexpr int kMlOff = kLiftOff + (QUANT ? kLifts * kLiftRows : 0);  // single: (m, l) of each stream's rows
   static constexpr int kEvOff = kMlOff + (DUAL ? 0 : 2 * BM * 8);    // and O's exponent
   static constexpr int kBadOff = kEvOff + (QUANT && !DUAL ? 2 * BM : 0);  // value rows that are not finite
   static constexpr int kPiecesOff = kBadOff + 2 * 2 * 16 + (QUANT ? kStages * 16 : 0);

@@ -262,3 +262,20 @@ def test_positions_that_axes_share():
         assert torch.equal(cache[:m], got)
     with pytest.raises(ValueError):
         cpa.cp_rope(rope, x, positions=long.view(n, 3).t())
+
+
+@pytest.mark.parametrize("nodes", [20, 64], ids=["single", "dual"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_queries_of_many_sizes_in_short_pieces(d, nodes):
+    """Requests of a tile or two whose queries differ by 2^50, many to a block: each piece's
+    scores go by the exponents of its own queries."""
+    Hq, Hkv, B = 8, 2, 48
+    kv = [(37 * b) % 200 for b in range(B)]
+    s = Step(21, [nodes] * B, kv, 16)
+    q, k, v, scales, k64, v64 = make(21, s.N, s.rows, Hq, Hkv, d, True)
+    up = torch.tensor([25 - 50 * (b % 2) for b in range(B)], device="cuda").repeat_interleave(nodes)
+    q = (q.float() * torch.exp2(up.float())[:, None, None]).bfloat16()
+    ref = s.ref(q, k64, v64, 2.0 ** -25)
+    for ctas in (1, 2, 8, 152):
+        o, lse, _ = s.call(q, k, v, 2.0 ** -25, num_ctas=ctas, **scales)
+        check(o, lse, ref, d, 264, f"{ctas} blocks")

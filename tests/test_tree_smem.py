@@ -29,7 +29,9 @@ static void mma(const char* name) {
   area("scales", C::kScaleOff, C::kRawStages * BN * 2LL * sizeof(float));
   area("notes", C::kNoteOff, C::kRawStages * (long long)sizeof(RawNote));
   area("tile_exponents", C::kExpOff, 8 * sizeof(int2));
-  area("query_exponents", C::kLiftOff, QUANT ? 2 * 2 * BM : 0);
+  // (the exponents of every piece that may lie in the ring)
+  static_assert(C::kLifts == sizeof(Pieces::at) / sizeof(TreePiece), "places of the piece ring");
+  area("query_exponents", C::kLiftOff, QUANT ? (long long)C::kLifts * (DUAL ? 2 : 1) * BM : 0);
   area("sums_of_streams", C::kMlOff, DUAL ? 0 : 2 * BM * (long long)sizeof(float2));
   area("output_exponents", C::kEvOff, QUANT && !DUAL ? 2 * BM : 0);
   area("bad_rows", C::kBadOff, 16 * 4 + (QUANT ? C::kStages * 4 * 4 : 0));
