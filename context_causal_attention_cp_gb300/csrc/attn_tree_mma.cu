@@ -25,6 +25,12 @@
 // would not keep them from the rows that do not see them.  A row that does see one becomes
 // NaN by its sum.
 //
+// Codes of cached keys, which all rows of a request see, are turned to f16 with one exponent a tile.
+// In a tile with new keys that would let the scale of a key that a row does not see take the bits
+// of those that it sees: there codes stay as they are, and K's scales go to the scores, V's to the
+// weights (softmax_row_scaled; it costs 2 to 3 us at a piece's end, e4m3 trees of 26 at d = 64 31.6 -> 34 us,
+// while the other tiles' code is rid of its masks).
+//
 // Measured, 32/8 heads, d = 128, 32 requests on up to 16K keys: trees of 32 (single units) 205 us,
 // HBM (floor 193); trees of 64 (dual) 251 us (floor 194): the tensor pipe is active 61 % of the
 // time, a stream's chain S -> softmax -> P -> P V is what bounds them.  Over codes 278 and 399 us
@@ -120,6 +126,22 @@ __device__ __forceinline__ void bar_named(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
+// O of a warp's rows (one a lane) times f, where a row needs it.
+template <int D>
+__device__ __forceinline__ void rescale_row(uint32_t o_addr, bool need, float f) {
+  if (!__any_sync(0xffffffffu, need)) return;
+  const float a = need ? f : 1.f;
+  uint32_t v[32];
+#pragma unroll
+  for (int q = 0; q < D / 32; ++q) {
+    tmem_ld32(o_addr + q * 32, v);
+    tmem_wait_ld();
+#pragma unroll
+    for (int c = 0; c < 32; ++c) v[c] = __float_as_uint(__uint_as_float(v[c]) * a);
+    tmem_st32(o_addr + q * 32, v);
+  }
+}
+
 // S of a tile to P, for the rows of a warp (one a lane): see softmax_tile in attn_shared.cu.
 // vis: the keys that the row sees (masked: not all); o_scale: what O is multiplied by besides.
 // Over codes S goes through the registers by halves, the first one twice (for the maximum and for
@@ -191,19 +213,96 @@ __device__ __forceinline__ void softmax_row(uint32_t s_addr, uint32_t o_addr, bo
     }
   }
   l_run = l_run * alpha + (sum0 + sum1);
-  const bool need = has_o && (move || o_scale != 1.f);
-  if (__any_sync(0xffffffffu, need)) {
-    const float a = need ? alpha * o_scale : 1.f;
-    uint32_t v[32];
+  rescale_row<D>(o_addr, has_o && (move || o_scale != 1.f), alpha * o_scale);
+  tmem_wait_st();
+  m_run = m_new;
+  m_use = m_new_use;
+}
+
+// The same for a tile of codes with new keys, which enter the products as they are.  A key's scale
+// must reach no row that does not see it, as one factor for a tile would: K's multiplies the score and
+// V's the weight, relative to 2^ev of the row's, a power of two above all V scales that the row has
+// seen (or, before, the exponent of the cached tiles).  ks, vs: the tile's scales in shared memory; good: the
+// keys that the row sees and whose values are finite.
+template <int D>
+__device__ __forceinline__ void softmax_row_scaled(uint32_t s_addr, uint32_t o_addr, const uint32_t (&vis)[4],
+                                                   const uint32_t (&good)[4], const float4* ks, const float4* vs,
+                                                   bool has_o, float factor, int& ev, float& m_run, float& m_use,
+                                                   float& l_run) {
+  // (Loops over 32 keys at a time, since this code is met once or twice a piece: unrolled it takes
+  // longer to fetch than to run, e4m3 trees of 26 at d = 64 48 us.)
+  constexpr int kParts = BN / 32;
+  uint32_t see[kParts], use[kParts];
 #pragma unroll
-    for (int q = 0; q < D / 32; ++q) {
-      tmem_ld32(o_addr + q * 32, v);
-      tmem_wait_ld();
-#pragma unroll
-      for (int c = 0; c < 32; ++c) v[c] = __float_as_uint(__uint_as_float(v[c]) * a);
-      tmem_st32(o_addr + q * 32, v);
-    }
+  for (int i = 0; i < kParts; ++i) {
+    see[i] = vis[i];
+    use[i] = good[i];
   }
+  auto turn = [](uint32_t (&w)[kParts]) {
+    const uint32_t first = w[0];
+#pragma unroll
+    for (int i = 0; i + 1 < kParts; ++i) w[i] = w[i + 1];
+    w[kParts - 1] = first;
+  };
+  float top = -INFINITY, most = 0.f;
+#pragma unroll 1
+  for (int part = 0; part < kParts; ++part) {
+    uint32_t v[32];
+    tmem_ld32(s_addr + part * 32, v);
+    tmem_wait_ld();
+#pragma unroll
+    for (int c = 0; c < 32; c += 4) {
+      const float4 k4 = ks[part * 8 + c / 4], v4 = vs[part * 8 + c / 4];
+      const float k[4] = {k4.x, k4.y, k4.z, k4.w}, f[4] = {v4.x, v4.y, v4.z, v4.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float x = (see[0] >> (c + i)) & 1u ? __uint_as_float(v[c + i]) * score_factor(factor, k[i]) : -INFINITY;
+        top = fmaxf(top, x);
+        if ((use[0] >> (c + i)) & 1u) most = fmaxf(most, f[i]);
+        v[c + i] = __float_as_uint(x);
+      }
+    }
+    tmem_st32(s_addr + part * 32, v);
+    turn(see);
+    turn(use);
+  }
+  // (a factor is below 1, so that a weight of up to 2^15 stays one of f16)
+  const int e = max(exponent_of(most) + 1, has_o ? ev : -126);
+  const float o_scale = has_o ? exp2_int(max(ev - e, -126)) : 1.f, down = exp2_int(1 - e);
+  ev = e;
+  const float mx = top - kF16Lift;
+  const bool move = mx > m_run + kMaxSlack;
+  const float m_new = move ? mx : m_run;
+  const float m_new_use = (m_new == -INFINITY) ? 0.f : m_new;
+  const float alpha = move ? ex2_approx(m_run - m_new_use) : 1.f;
+  float sum = 0.f;
+  tmem_wait_st();
+  // (P of a part lies over columns of S that have been loaded)
+#pragma unroll 1
+  for (int part = 0; part < kParts; ++part) {
+    uint32_t v[32], pk[16];
+    tmem_ld32(s_addr + part * 32, v);
+    tmem_wait_ld();
+#pragma unroll
+    for (int c = 0; c < 32; c += 4) {
+      const float4 v4 = vs[part * 8 + c / 4];
+      const float f[4] = {v4.x, v4.y, v4.z, v4.w};
+      float w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        w[i] = ex2_approx(__uint_as_float(v[c + i]) - m_new_use);
+        sum += w[i];
+        w[i] = (use[0] >> (c + i)) & 1u ? w[i] * (f[i] * down * 0.5f) : 0.f;
+      }
+      // P in f16, off by at most 2^-11 of each weight; l sums the unrounded values
+      pk[c / 2] = pack_f16x2(w[0], w[1]);
+      pk[c / 2 + 1] = pack_f16x2(w[2], w[3]);
+    }
+    tmem_st16(s_addr + part * 16, pk);
+    turn(use);
+  }
+  l_run = l_run * alpha + sum;
+  rescale_row<D>(o_addr, has_o && (move || o_scale != 1.f), alpha * o_scale);
   tmem_wait_st();
   m_run = m_new;
   m_use = m_new_use;
@@ -259,6 +358,7 @@ attn_tree_mma_kernel(const __grid_constant__ TreeMaps maps, const TreeParams p) 
   RawNote* raw_note = reinterpret_cast<RawNote*>(smem + C::kNoteOff);
   int2* tile_exp = reinterpret_cast<int2*>(smem + C::kExpOff);
   int8_t* q_lift = reinterpret_cast<int8_t*>(smem + C::kLiftOff);
+  float* tail_scales = reinterpret_cast<float*>(smem + C::kTailOff);
   float2* ml = reinterpret_cast<float2*>(smem + C::kMlOff);
   int8_t* o_exp = reinterpret_cast<int8_t*>(smem + C::kEvOff);
   uint32_t* bad_scan = reinterpret_cast<uint32_t*>(smem + C::kBadOff);  // [2 streams][2][4]
@@ -697,14 +797,18 @@ attn_tree_mma_kernel(const __grid_constant__ TreeMaps maps, const TreeParams p) 
         const float* scales = reinterpret_cast<const float*>(smem + C::kScaleOff + raw * BN * 8);
         // Exponents: K's factors are relative to the tile's largest scale, V's to the largest
         // that the stream has met in the piece (scales are not negative: their bits order as
-        // integers)
+        // integers).  Codes of a tile with new keys stay as they are (see softmax_row_scaled).
+        const bool raw_codes = note.fresh < BN;
         float mx = 0.f, mv = 0.f;
+        if (!raw_codes) {
 #pragma unroll
-        for (int x = 0; x < 4; ++x)
-          if (x * 32 + lane < note.live) {
+          for (int x = 0; x < 4; ++x) {
             mx = fmaxf(mx, scales[x * 32 + lane]);
             if (!is_v) mv = fmaxf(mv, scales[BN + x * 32 + lane]);
           }
+        } else if (!is_v) {
+          tail_scales[n % C::kTails * 2 * BN + w * 32 + lane] = scales[w * 32 + lane];
+        }
         const int most = exponent_of(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mx))));
         const int strm = DUAL ? 0 : n & 1;
         int e = most;
@@ -719,9 +823,9 @@ attn_tree_mma_kernel(const __grid_constant__ TreeMaps maps, const TreeParams p) 
           int& ev = strm ? ev_v[1] : ev_v[0];
           ev = note.first ? most : max(ev, most);
           e = ev;
-          if (note.fresh < BN) {  // new keys: a NaN's row
-            bool bad = false;
+          if (raw_codes) {  // new keys: a NaN's row
             const int row = w * kMine + lane / 2;  // two lanes to a row
+            bool bad = !(scales[row] < INFINITY);
 #pragma unroll
             for (int ch = 0; ch < D / 32; ++ch) {
               const uint4 v = *reinterpret_cast<const uint4*>(src + code_at<D>(row, (lane & 1) * (D / 32) + ch));
@@ -745,7 +849,7 @@ attn_tree_mma_kernel(const __grid_constant__ TreeMaps maps, const TreeParams p) 
           uint32_t m[kBatch];
 #pragma unroll
           for (int x = 0; x < kBatch; ++x) {
-            m[x] = pack_f16x2(mul[r0 + 4 * x] * inv, 0.f);
+            m[x] = pack_f16x2(raw_codes ? 1.f : mul[r0 + 4 * x] * inv, 0.f);
 #pragma unroll
             for (int h = 0; h < kHalves; ++h)
               v[x][h] = *reinterpret_cast<const uint2*>(src + from[x & 1][h] + (r0 + 4 * (x & ~1)) * D);
@@ -847,13 +951,15 @@ attn_tree_mma_kernel(const __grid_constant__ TreeMaps maps, const TreeParams p) 
           if (first && r < pc.rows) factor = p.scale_log2 * exp2_int(-q_lift[i % C::kLifts * C::kLiftRows + r]);
           // written before the K tile went to the tensor core, and not again before this
           // step's P has been used
-          const volatile int2* e = tile_exp + (n & 7);
-          const int ek = e->x, ev_now = e->y;
-          sl2 = score_factor(factor, exp2_int(ek));
-          if (!first && ev_now != ev) o_scale = exp2_int(max(ev - ev_now, -126));
-          ev = ev_now;
+          if (!tail) {
+            const volatile int2* e = tile_exp + (n & 7);
+            const int ek = e->x, ev_now = e->y;
+            sl2 = score_factor(factor, exp2_int(ek));
+            if (!first && ev_now != ev) o_scale = exp2_int(max(ev - ev_now, -126));
+            ev = ev_now;
+          }
         }
-        uint32_t vis[4] = {~0u, ~0u, ~0u, ~0u};
+        uint32_t vis[4] = {~0u, ~0u, ~0u, ~0u}, good[4] = {0, 0, 0, 0};
         float poison = 0.f;
         if (tail) {
           const int slot = v_place<!DUAL>(n) % NS;
@@ -892,11 +998,20 @@ attn_tree_mma_kernel(const __grid_constant__ TreeMaps maps, const TreeParams p) 
           }
           uint32_t hit = 0;
 #pragma unroll
-          for (int x = 0; x < 4; ++x) hit |= vis[x] & bad_words[x];
+          for (int x = 0; x < 4; ++x) {
+            hit |= vis[x] & bad_words[x];
+            if (QUANT) good[x] = vis[x] & ~bad_words[x];
+          }
           if (r < pc.rows && hit) poison = __uint_as_float(0x7FC00000u);
         }
-        if (warp_live && ok)
-          softmax_row<D, QUANT>(s_addr, o_addr, tail, vis, !first, o_scale, sl2, m_run, m_use, l_run);
+        if (warp_live && ok) {
+          if (QUANT && tail) {
+            const float4* const ks = reinterpret_cast<const float4*>(tail_scales + n % max(C::kTails, 1) * 2 * BN);
+            softmax_row_scaled<D>(s_addr, o_addr, vis, good, ks, ks + BN / 4, !first, factor, ev, m_run, m_use, l_run);
+          } else {
+            softmax_row<D, QUANT>(s_addr, o_addr, tail, vis, !first, o_scale, sl2, m_run, m_use, l_run);
+          }
+        }
         l_run += poison;
         first = false;
         if (!DUAL && pending) {

@@ -20,7 +20,8 @@
 // g-th eighth of the columns of its keys 2c, 2c+1, 2c+8, 2c+9 and joins two rows' bytes into
 // a pair for each column, so rows g and g + 8 of product x are columns g D/8 + 2x and + 1.
 // Codes enter as f16, exact; K's scale multiplies the score, V's is taken relative to the
-// largest that the warp has met (O is rescaled when that grows).
+// largest that the warp has met (O is rescaled when that grows); among new keys, of which a row
+// may not see all, V's scale multiplies the weight, relative to the largest that the row has seen.
 //
 // Measured, 32/8 heads, d = 128: 64 tokens on up to 8K keys each, bf16 173 us (6.8 TB/s, the copy
 // bandwidth), e4m3 110 us (5.5 TB/s: codes to f16 and the copies of the scales); one token on 1K
@@ -139,13 +140,13 @@ struct Warp {
                   (QUANT ? score_factor(factor[n][y & 1], k.scale[y >> 1]) : factor[n][y & 1]);
   }
 
-  // Which of the warp's value rows of a tile hold an infinity or NaN.
+  // Which of the warp's value rows of a tile hold an infinity or NaN, in their scale or a code.
   __device__ __forceinline__ uint32_t bad_rows(int slot) const {
     constexpr int kParts = 32 / kKeys;                          // lanes of a row
     constexpr int kN = D * (QUANT ? 1 : 2) / 16 / kParts;       // chunks of a lane
     const uint32_t tile = base + slot * C::kTile;
     const int row = key0 + lane / kParts;
-    bool bad = false;
+    bool bad = QUANT && !(lds_f32(scale_at(slot, row)) < INFINITY);
 #pragma unroll
     for (int x = 0; x < kN; ++x) {
       const int ch = lane % kParts * kN + x;
@@ -232,7 +233,12 @@ __device__ __forceinline__ bool Warp<D, QUANT, NQ>::piece(const TreeParams& p, c
       m_use[n][e] = l_run[n][e] = 0.f;
     }
   }
-  int ev = -126;  // (e4m3) exponent of O
+  // (e4m3) exponent of O: max(ev, er), ev of the rows' tiles while they see the same keys, er of a
+  // row's from there on, a byte each
+  int ev = -126;
+  uint32_t er = 0x82828282u;
+  static_assert(NQ <= 2, "bytes of er");
+  auto unit_of = [&](int x, int e) { return max(ev, (int)(int8_t)(er >> (16 * x + 8 * e))); };
   auto wait_k = [&](int n) {
     const int place = k_place<false>(n);
     return wait_warp(full + place % NS, (place / NS) & 1, abort, p.timeout_ns);
@@ -249,6 +255,46 @@ __device__ __forceinline__ bool Warp<D, QUANT, NQ>::piece(const TreeParams& p, c
       Keys k;
       load_k(k, slot, key0 + 16 * b);
       product(k, q, factor, s[b]);
+    }
+  };
+  // Where rows see different keys V's codes enter the product as they are, and a value's scale its
+  // weight: it must reach no row that does not see the key, as a factor for all rows would.  It is
+  // taken relative to 2^er, a power of two above all scales that the row has seen, so that a weight of
+  // up to 2^15 stays one of f16.  (A key that a row does not see has a weight of 0.)
+  auto weigh = [&](int x, int slot, uint32_t spoilt, float (&alpha)[2], bool& any) {
+    float f[kBlocks][2];
+#pragma unroll
+    for (int b = 0; b < kBlocks; ++b)
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const int kk = 16 * b + g + 8 * y;
+        f[b][y] = (spoilt >> kk) & 1u ? 0.f : lds_f32(scale_at(slot, key0 + kk));
+      }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float most = 0.f;
+#pragma unroll
+      for (int b = 0; b < kBlocks; ++b)
+#pragma unroll
+        for (int y = 0; y < 2; ++y)
+          if (s[b][x][e + 2 * y] != 0.f) most = fmaxf(most, f[b][y]);
+      most = fmaxf(most, __shfl_xor_sync(all, most, 4));
+      most = fmaxf(most, __shfl_xor_sync(all, most, 8));
+      most = fmaxf(most, __shfl_xor_sync(all, most, 16));
+      const int was = unit_of(x, e), now = max(was, exponent_of(most) + 1), at = 16 * x + 8 * e;
+      er = (er & ~(0xFFu << at)) | ((uint32_t)now & 0xFFu) << at;
+      if (now != was) {
+        alpha[e] *= exp2_int(max(was - now, -126));
+        any = true;
+      }
+      const float down = exp2_int(1 - now);
+#pragma unroll
+      for (int b = 0; b < kBlocks; ++b)
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          float& w = s[b][x][e + 2 * y];
+          w = w == 0.f ? 0.f : w * (f[b][y] * down * 0.5f);
+        }
     }
   };
   int t = kTeams == 1 ? 0 : (n0 ^ team) & 1;  // the team's first tile
@@ -269,13 +315,17 @@ __device__ __forceinline__ bool Warp<D, QUANT, NQ>::piece(const TreeParams& p, c
     const uint32_t tile = base + v_slot * C::kTile;
     uint32_t alive = ~0u;  // value rows that count: up to the last key, and (new keys) finite
     uint32_t pb[kBlocks][NQ][2];
+    bool apart = false;  // (e4m3) rows may see different keys of the warp's
     if (work) {
       const bool masked = at + kKeys > pc.L;  // new keys among them, or keys behind the last
+      apart = QUANT && masked && (p.mask || pc.T > 1);
+      uint32_t spoilt = 0;  // new keys whose value rows are not finite
       if (masked) {
         if (pc.keys - at < kKeys) alive = (1u << (pc.keys - at)) - 1u;
         const uint32_t fresh = at >= pc.L ? ~0u : ~0u << min(31, pc.L - at);
         const uint32_t bad = bad_rows(v_slot) & alive & fresh;
         alive &= ~bad;
+        spoilt = bad;
 #pragma unroll
         for (int b = 0; b < kBlocks; ++b)
 #pragma unroll
@@ -322,6 +372,7 @@ __device__ __forceinline__ bool Warp<D, QUANT, NQ>::piece(const TreeParams& p, c
           }
           l_run[x][e] = l_run[x][e] * alpha[x][e] + sum;
         }
+        if (apart) weigh(x, v_slot, spoilt, alpha[x], any);
         // P in 16 bits, the second product's operand type: off by at most 2^-8 (bf16) or
         // 2^-11 (f16) of each weight; l sums the unrounded values.  Queries by rows, keys
         // by columns now
@@ -399,21 +450,25 @@ __device__ __forceinline__ bool Warp<D, QUANT, NQ>::piece(const TreeParams& p, c
                 for (int y = 0; y < D / 32; ++y) u[x][y] = 0u;
               }
           }
-          // factors of the lane's keys, relative to 2^ev
-          const int e = exponent_of(__uint_as_float(
-              __reduce_max_sync(all, __float_as_uint(fmaxf(fmaxf(f[0], f[1]), fmaxf(f[2], f[3]))))));
-          if (e > ev) {  // (the same for the warp)
-            const float down = exp2_int(max(ev - e, -126));
+          // factors of the lane's keys, relative to 2^ev; where rows see different keys the weights have them
+          uint32_t f0 = 0x3C003C00u, f1 = 0x3C003C00u;
+          if (!apart) {
+            const int e = exponent_of(__uint_as_float(
+                __reduce_max_sync(all, __float_as_uint(fmaxf(fmaxf(f[0], f[1]), fmaxf(f[2], f[3]))))));
+            if (e > ev) {  // (the same for the warp)
+              const float down = exp2_int(max(ev - e, -126));
 #pragma unroll
-            for (int y = 0; y < NQ; ++y)
+              for (int y = 0; y < NQ; ++y)
 #pragma unroll
-              for (int x = 0; x < kOut; ++x)
+                for (int x = 0; x < kOut; ++x)
 #pragma unroll
-                for (int z = 0; z < 4; ++z) o[y][x][z] *= down;
-            ev = e;
+                  for (int z = 0; z < 4; ++z) o[y][x][z] *= down;
+              ev = e;
+            }
+            const float inv = exp2_int(-ev);
+            f0 = pack_f16x2(f[0] * inv, f[1] * inv);
+            f1 = pack_f16x2(f[2] * inv, f[3] * inv);
           }
-          const float inv = exp2_int(-ev);
-          const uint32_t f0 = pack_f16x2(f[0] * inv, f[1] * inv), f1 = pack_f16x2(f[2] * inv, f[3] * inv);
 #pragma unroll
           for (int x = 0; x < kOut; ++x) {  // columns 2x, 2x + 1 of the lane's
             const uint32_t a = __byte_perm(u[0][x >> 1], u[1][x >> 1], x & 1 ? 0x7362 : 0x5140);
@@ -429,7 +484,6 @@ __device__ __forceinline__ bool Warp<D, QUANT, NQ>::piece(const TreeParams& p, c
     release(empty + v_slot);
   }
   // ---- join the warps of a row: O = sum_w f_w O_w / L, f_w = 2^(m_w - M), L = sum f_w l_w ----
-  const float down = exp2_int(ev);
   float* const join = reinterpret_cast<float*>(mem + C::kJoinOff);
   float2* const ml = reinterpret_cast<float2*>(mem + C::kMlOff);
 #pragma unroll
@@ -443,6 +497,7 @@ __device__ __forceinline__ bool Warp<D, QUANT, NQ>::piece(const TreeParams& p, c
       const int r = 8 * n + 2 * c + e;  // of the warp's
       if (g == 0) ml[warp * (8 * NQ) + r] = make_float2(m_use[n][e], l);
       float* const dst = join + (warp * (8 * NQ) + r) * D;
+      const float down = QUANT ? exp2_int(unit_of(n, e)) : 1.f;
       if constexpr (!QUANT) {
 #pragma unroll
         for (int x = 0; x < kOut; ++x) {

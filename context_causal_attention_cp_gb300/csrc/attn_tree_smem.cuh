@@ -36,7 +36,13 @@ struct MmaCfg {
   // A place for each of the piece ring's: the softmax may look at a piece's exponents until it is
   // done with the piece, which its place in the ring waits for and the queries' buffer does not.
   static constexpr int kLifts = kPieces, kLiftRows = DUAL ? 2 * BM : BM;
-  static constexpr int kMlOff = kLiftOff + (QUANT ? kLifts * kLiftRows : 0);  // single: (m, l) of each stream's rows
+  // Scales of tiles n mod kTails that hold new keys, [kTails][K, V][BN]: the softmax has them from the
+  // conversion of a K tile to its P V, while the ring takes kStages more places, of which K has every
+  // other one (and one ahead).
+  static constexpr int kTails = !QUANT ? 0 : kStages + 3 < 2 * 4 ? 4 : 8;
+  static_assert(!QUANT || 2 * kTails > kStages + 3, "scales of tiles in flight");
+  static constexpr int kTailOff = kLiftOff + (QUANT ? kLifts * kLiftRows : 0);
+  static constexpr int kMlOff = kTailOff + kTails * 2 * BN * 4;  // single: (m, l) of each stream's rows
   static constexpr int kEvOff = kMlOff + (DUAL ? 0 : 2 * BM * 8);    // and O's exponent
   static constexpr int kBadOff = kEvOff + (QUANT && !DUAL ? 2 * BM : 0);  // value rows that are not finite
   static constexpr int kPiecesOff = kBadOff + 2 * 2 * 16 + (QUANT ? kStages * 16 : 0);

@@ -779,9 +779,10 @@ int cp_tree_layout(const cp_tree_layout_args_t* args, cudaStream_t stream);
  *     dv, max_nodes and num_ctas (lengths play no part); overwritten, nothing in it needs
  *     clearing; not to be shared by calls that may run at the same time.
  * Keys outside what a request's rows see may hold anything, infinities and NaN among
- * them; so may, for the other rows of its request, a new key that only some see.  A row that
- * sees a new key whose value row holds an infinity or a NaN is NaN in all columns.  Weights
- * are rounded as in cp_attn_shared; codes enter the products as described there.
+ * them, in their scales, too; so may, for the other rows of its request, a new key that only
+ * some see.  A row that sees a new key whose value row holds an infinity or a NaN (in its
+ * scale or an element) is NaN in all columns.  Weights are rounded as in cp_attn_shared; codes
+ * enter the products as described there, with the largest scale that of the keys that the row sees.
  * Two launches (the attention, and the merge of what was cut), no order of atomics: the same
  * call gives the same bits.  A request whose rows, length or pages lie outside their
  * arrays sets CPATTN_ERR_RANGE and is skipped; so does a page outside the cache, whose keys

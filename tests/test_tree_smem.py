@@ -32,6 +32,7 @@ static void mma(const char* name) {
   // (the exponents of every piece that may lie in the ring)
   static_assert(C::kLifts == sizeof(Pieces::at) / sizeof(TreePiece), "places of the piece ring");
   area("query_exponents", C::kLiftOff, QUANT ? (long long)C::kLifts * (DUAL ? 2 : 1) * BM : 0);
+  area("scales_of_new_keys", C::kTailOff, C::kTails * 2LL * BN * sizeof(float));
   area("sums_of_streams", C::kMlOff, DUAL ? 0 : 2 * BM * (long long)sizeof(float2));
   area("output_exponents", C::kEvOff, QUANT && !DUAL ? 2 * BM : 0);
   area("bad_rows", C::kBadOff, 16 * 4 + (QUANT ? C::kStages * 4 * 4 : 0));
