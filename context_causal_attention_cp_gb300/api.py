@@ -1121,7 +1121,8 @@ def make_rope(inv_freq, *, axes=None, first=0, interleaved=False, device="cuda")
     first), e.g. time, height or width.  Pairs are columns (first + c, first + pairs + c),
     or (first + 2c, first + 2c + 1) with ``interleaved``.
     """
-    f = torch.as_tensor(inv_freq).detach().to("cpu", torch.float64).contiguous()
+    # (a list of Python's floats would become a tensor of 32 bits)
+    f = torch.as_tensor(inv_freq, dtype=torch.float64).detach().cpu().contiguous()
     if f.dim() != 1 or f.numel() == 0:
         raise ValueError("inv_freq must be 1-D, with an entry for each pair")
     ax = None
