@@ -4,9 +4,9 @@
 // t = p f_c, p the row's position on the pair's axis; the inverse takes -t.  A position
 // times a frequency is up to 2^31 turns, of which fp32 would keep none of the fraction.
 // So a frequency is held in turns as a 64-bit fraction F (f / 2 pi mod 1, times 2^64), and
-// p F mod 2^64 is the phase, exact but for F's rounding: off by |p| 2^-65 turns, two integer
-// multiplications for its upper 32 bits.  The quarter turn next to it is split off before
-// the rest goes to fp32, so that cos and sin are good to fp32 at any position.
+// p F mod 2^64 is the phase, exact but for F's rounding: off by |p| 2^-64 turns at most.  The quarter
+// turn next to it is split off before the rest goes to fp32, with all 64 bits, so that cos and sin keep
+// fp32's relative bits at any position, those of small angles (slow pairs, first positions) among them.
 //
 // One kernel for both calls, an HBM stream.  L = 2^k lanes share a vector; a lane's item is
 // two 16-byte chunks (of bf16) that hold 8 pairs, or 16 columns that are not rotated.  A
@@ -64,12 +64,11 @@ struct RopeParams {
   int32_t* status;
 };
 
-// cos and sin of position p (sign-extended to 64 bits) times frequency F.
+// cos and sin of position p times frequency F.
 __device__ __forceinline__ float2 cos_sin(int p, uint32_t f_lo, uint32_t f_hi) {
-  const uint32_t u = (uint32_t)p;
-  const uint32_t phase = __umulhi(u, f_lo) + u * f_hi - (p < 0 ? f_lo : 0u);  // 2^-32 turns
-  const uint32_t quarter = (phase + 0x20000000u) >> 30;  // nearest, mod 4
-  const float rest = (float)(int)(phase - (quarter << 30)) * 0x1p-31f;  // half turns, |rest| <= 1/4
+  const uint64_t phase = (uint64_t)(long long)p * ((uint64_t)f_hi << 32 | f_lo);  // 2^-64 turns
+  const uint32_t quarter = ((uint32_t)(phase >> 32) + 0x20000000u) >> 30;         // nearest, mod 4
+  const float rest = (float)(long long)(phase - ((uint64_t)quarter << 62)) * 0x1p-63f;  // half turns, |rest| <= 1/4
   float s, c;
   sincospif(rest, &s, &c);
   const float a = quarter & 1 ? s : c, b = quarter & 1 ? c : s;

@@ -668,7 +668,8 @@ int cp_attn_shared(const cp_shared_plan_t* plan, const int32_t* table_dev, const
  * several those of an image or video (time, height, width), each pair following the
  * axis that the table gives it.  The phase is computed in 64-bit fractions of a turn: the
  * angle is off by at most |position| * 2^-64 turns at any position, and cos and sin by fp32's
- * rounding.  The rotation is computed in fp32 and rounded once.
+ * rounding of their own size (those of small angles, too).  The rotation is computed in fp32 and
+ * rounded once.
  *
  * cp_rope_table (host): inv_freq [pairs] (radians a position, |inv_freq| <= 2^20) and
  * axis [pairs] (0 .. CPATTN_MAX_ROPE_AXES - 1; NULL: all 0) to table [pairs][4] (host),
