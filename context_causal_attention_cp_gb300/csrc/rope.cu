@@ -21,6 +21,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <cstdlib>
 
 #include <cuda_bf16.h>
 
@@ -352,7 +353,8 @@ int check_out_rows(const void* x, int64_t row, int64_t head, int size, int64_t n
   return by_row || by_head ? CPATTN_OK : CPATTN_ERR_INVALID_ARG;
 }
 // Whether an output lies apart from its input, or on it with equal strides (each lane
-// reads what it writes).  Side by side in the rows of one buffer counts as apart.
+// reads what it writes).  In rows of equal strides the two may lie side by side, with equal strides of
+// heads also between each other.
 bool apart(const void* x, int64_t xr, int64_t xh, const void* y, int64_t yr, int64_t yh, int size, int64_t n,
            int heads, int dim) {
   if (n == 1) xr = yr = 0;
@@ -361,10 +363,20 @@ bool apart(const void* x, int64_t xr, int64_t xh, const void* y, int64_t yr, int
   const intptr_t a = reinterpret_cast<intptr_t>(x), b = reinterpret_cast<intptr_t>(y);
   const int64_t wx = ((heads - 1) * xh + dim) * size, wy = ((heads - 1) * yh + dim) * size;  // of a row
   if (a + (n - 1) * xr * size + wx <= b || b + (n - 1) * yr * size + wy <= a) return true;
-  const int64_t row = xr * size;
-  if (xr != yr || row <= 0) return false;
-  const int64_t at = ((b - a) % row + row) % row;
-  return at >= wx && at + wy <= row;
+  const int64_t row = xr * size, width = (int64_t)dim * size;
+  if (xr != yr) return false;
+  if (row > 0) {  // side by side in the rows of one buffer
+    const int64_t at = ((b - a) % row + row) % row;
+    if (at >= wx && at + wy <= row) return true;
+  }
+  if (xh != yh) return false;
+  // a vector of y, i rows and j heads further on than one of x, that would lie on it
+  for (int64_t j = 1 - heads; j < heads; ++j) {
+    const int64_t at = b - a + j * xh * size, i0 = row > 0 ? -at / row : 0;
+    for (int64_t i = std::max(i0 - 1, 1 - n); i <= std::min(i0 + 1, n - 1); ++i)
+      if (std::llabs(at + i * row) < width) return false;
+  }
+  return true;
 }
 
 int check_rope(const cp_rope_t* r, int d, const int32_t* positions, int64_t axis_stride, int num_rows) {

@@ -689,8 +689,9 @@ int cp_rope_table(const double* inv_freq, const int32_t* axis, int pairs, int32_
  *   inverse: turn by -t.  The rotation is orthogonal, so that this is the gradient: dq
  *     from dq_out.
  *   q, k, q_out, k_out: bf16, or fp32 (x_is_fp32); strides in elements, multiples of 16
- *     bytes, >= 0.  An output may be its input (same pointer and strides); otherwise the
- *     two must not overlap (rows side by side in one buffer of equal row strides do not).
+ *     bytes, >= 0.  An output may be its input (same pointer and strides); otherwise the two
+ *     must not overlap: one ends before the other, or their rows lie side by side in one buffer
+ *     of equal row strides, or with equal strides no element of one lies on the other.
  *     No element of an output may have two places, nor lie in the call's other tensors.
  *     Strides of 2^36 bytes and more are CPATTN_ERR_TOO_LARGE.
  *   d: a multiple of 16, at most 1024, >= first + 2*pairs. */
