@@ -279,3 +279,17 @@ def test_queries_of_many_sizes_in_short_pieces(d, nodes):
     for ctas in (1, 2, 8, 152):
         o, lse, _ = s.call(q, k, v, 2.0 ** -25, num_ctas=ctas, **scales)
         check(o, lse, ref, d, 264, f"{ctas} blocks")
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_rotated_into_the_slot_beside(dtype):
+    """Q and K of a buffer [rows, heads, 3, d] into its other slots, which no other element meets."""
+    n, H, d = 300, 5, 64
+    rope, pos, rot, ref = rotation.make(22, n, 32)
+    both = rotation.draw(23, (n, H, 3, d), dtype)
+    before = both.clone()
+    cpa.cp_rope(rope, both[:, :, 0], positions=pos, out_q=both[:, :, 2])
+    rotation.check(both[:, :, 2], before[:, :, 0], rot, op.rotate(f64(before[:, :, 0]), **ref))
+    assert torch.equal(both[:, :, :2], before[:, :, :2])
+    with pytest.raises(L.CpAttnError):
+        cpa.cp_rope(rope, both[1:, :, 0], positions=pos[:, 1:], out_q=both[:-1, :, 0])

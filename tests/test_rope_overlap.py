@@ -1,6 +1,6 @@
 """Outputs of a rotation beside their input in one buffer: taken when no element of one lies on the
-other, refused else.  Calls without a table end in the refusal of that, behind the checks of places, so
-that nothing is launched: a call that comes so far has had its places taken.  No GPU."""
+other, refused else.  Each call has a K at an odd address, which is refused behind Q's places, so
+that nothing is launched.  No GPU."""
 
 import itertools
 
@@ -12,14 +12,12 @@ BASE = 1 << 20
 
 
 def call(q, qo, n, Hq, d, qr, qh, qor, qoh):
-    a = dict(q=q, k=0, qo=qo, ko=0, at=0x800000, status=0, qr=qr, qh=qh, kr=256, kh=128, qor=qor, qoh=qoh, kor=256,
-             koh=128, axis=0, n=n, Hq=Hq, Hk=0, d=d, f32=0, inverse=0)
-    # Hk = 1 without a k: refused by itself, after Q's side
-    a.update(Hk=1, k=4, ko=4)
+    a = dict(q=q, k=4, qo=qo, ko=4, at=0x800000, status=0, qr=qr, qh=qh, kr=256, kh=128, qor=qor, qoh=qoh, kor=256,
+             koh=128, axis=0, n=n, Hq=Hq, Hk=1, d=d, f32=0, inverse=0)
     rope = L.RopeInfo(table=0x900000, pairs=8, first=0, interleaved=0, axes=1)
     rc = L.load().cp_rope(rope, L.ROPE_ARGS.pack(*a.values()), None)
     assert rc in (L.ERR_ALIGNMENT, L.ERR_INVALID_ARG)
-    return rc == L.ERR_ALIGNMENT  # (k's address: Q's places were taken)
+    return rc == L.ERR_ALIGNMENT  # (K's, so Q's places were taken)
 
 
 def cells(at, n, H, d, row, head):
