@@ -32,20 +32,26 @@ struct LayoutParams {
 __global__ void __launch_bounds__(kThreads) tree_layout_kernel(const LayoutParams p) {
   __shared__ int32_t held[kHeld];
   const int b = blockIdx.x;
+  auto none = [&](long long row) {  // a row of no request
+    p.slots[row] = -1;
+    p.positions[row] = 0;
+    if (p.mask)
+      for (int w = 0; w < p.words; ++w) p.mask[row * p.words + w] = 0;
+  };
   if (b >= p.num_reqs) {  // padding rows
     const int first = max(0, p.num_reqs > 0 ? __ldg(p.q_start + p.num_reqs) : 0);
     for (long long row = first + (long long)(b - p.num_reqs) * kThreads + threadIdx.x; row < p.num_rows;
-         row += (long long)(gridDim.x - p.num_reqs) * kThreads) {
-      p.slots[row] = -1;
-      p.positions[row] = 0;
-      if (p.mask)
-        for (int w = 0; w < p.words; ++w) p.mask[row * p.words + w] = 0;
-    }
+         row += (long long)(gridDim.x - p.num_reqs) * kThreads)
+      none(row);
     return;
   }
   const int s0 = __ldg(p.q_start + b), s1 = __ldg(p.q_start + b + 1), len = __ldg(p.kv_lens + b);
   if (s0 < 0 || s1 < s0 || s1 > p.num_rows || (b == 0 && s0 != 0)) {
     if (threadIdx.x == 0) set_status(p.status, CPATTN_ERR_RANGE);
+    // the rows between its ends, which may be no other's: an append that follows must not find
+    // there what the memory held (from row 0 on to the end of q_start each row is between some two)
+    const int hi = min(p.num_rows, max(s0, s1));
+    for (long long row = (b == 0 ? 0 : max(0, min(s0, s1))) + (long long)threadIdx.x; row < hi; row += kThreads) none(row);
     return;
   }
   const int T = s1 - s0;

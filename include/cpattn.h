@@ -754,8 +754,8 @@ int cp_kv_append(const cp_rope_t* rope, const cp_kv_codes_t* k_cache, const cp_k
  * A request whose rows, length or pages lie outside their arrays, a page that is not one
  * (< 0), a parent that is not below its node and a node without a bit (>= 32 *
  * mask_words) set CPATTN_ERR_RANGE; such a request's or node's slot is -1, such a parent
- * counts as none. (Rows of a q_start that does not rise within num_rows may be left as they
- * are.) */
+ * counts as none.  Every row is written: where q_start does not rise within num_rows, the rows
+ * between two entries that are no request's have slot -1, those that are another's also may. */
 typedef struct {
   const int32_t *q_start, *kv_lens, *page_table, *parents;
   int32_t *slots, *positions, *mask, *status_dev;
