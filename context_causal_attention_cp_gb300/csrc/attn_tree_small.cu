@@ -233,12 +233,11 @@ __device__ __forceinline__ bool Warp<D, QUANT, NQ>::piece(const TreeParams& p, c
       m_use[n][e] = l_run[n][e] = 0.f;
     }
   }
-  // (e4m3) exponent of O: max(ev, er), ev of the rows' tiles while they see the same keys, er of a
-  // row's from there on, a byte each
+  // (e4m3) exponent of O: ev while the rows see the same keys, and from there on (`parted`) a row's own,
+  // which lies where the join will have the row's (m, l): the loop has no register for it
   int ev = -126;
-  uint32_t er = 0x82828282u;
-  static_assert(NQ <= 2, "bytes of er");
-  auto unit_of = [&](int x, int e) { return max(ev, (int)(int8_t)(er >> (16 * x + 8 * e))); };
+  bool parted = false;
+  int2* const own = reinterpret_cast<int2*>(mem + C::kMlOff) + warp * (8 * NQ);
   auto wait_k = [&](int n) {
     const int place = k_place<false>(n);
     return wait_warp(full + place % NS, (place / NS) & 1, abort, p.timeout_ns);
@@ -259,43 +258,47 @@ __device__ __forceinline__ bool Warp<D, QUANT, NQ>::piece(const TreeParams& p, c
   };
   // Where rows see different keys V's codes enter the product as they are, and a value's scale its
   // weight: it must reach no row that does not see the key, as a factor for all rows would.  It is
-  // taken relative to 2^er, a power of two above all scales that the row has seen, so that a weight of
-  // up to 2^15 stays one of f16.  (A key that a row does not see has a weight of 0.)
-  auto weigh = [&](int x, int slot, uint32_t spoilt, float (&alpha)[2], bool& any) {
-    float f[kBlocks][2];
-#pragma unroll
-    for (int b = 0; b < kBlocks; ++b)
-#pragma unroll
-      for (int y = 0; y < 2; ++y) {
-        const int kk = 16 * b + g + 8 * y;
-        f[b][y] = (spoilt >> kk) & 1u ? 0.f : lds_f32(scale_at(slot, key0 + kk));
-      }
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      float most = 0.f;
+  // taken relative to a power of two above all scales that the row has seen, so that a weight of up to
+  // 2^15 stays one of f16.  (A key that a row does not see has a weight of 0.)  A row at a time, a key a
+  // lane, through the warp's part of the join: on the registers that hold the weights it is so much
+  // code that tiles that do not come here take longer, too (decode of 64 113.2 against 111.2 us).
+  auto weigh = [&](int slot, uint32_t spoilt, float (&alpha)[NQ][2], bool& any) {
+    constexpr int kPitch = 33;  // floats
+    static_assert(!QUANT || (kKeys == 32 && kPitch <= D), "a key a lane, and rows of the join");
+    float* const w = reinterpret_cast<float*>(mem + C::kJoinOff) + warp * (8 * NQ) * D;
+    auto each = [&](auto&& f) {
 #pragma unroll
       for (int b = 0; b < kBlocks; ++b)
 #pragma unroll
-        for (int y = 0; y < 2; ++y)
-          if (s[b][x][e + 2 * y] != 0.f) most = fmaxf(most, f[b][y]);
-      most = fmaxf(most, __shfl_xor_sync(all, most, 4));
-      most = fmaxf(most, __shfl_xor_sync(all, most, 8));
-      most = fmaxf(most, __shfl_xor_sync(all, most, 16));
-      const int was = unit_of(x, e), now = max(was, exponent_of(most) + 1), at = 16 * x + 8 * e;
-      er = (er & ~(0xFFu << at)) | ((uint32_t)now & 0xFFu) << at;
-      if (now != was) {
-        alpha[e] *= exp2_int(max(was - now, -126));
-        any = true;
-      }
-      const float down = exp2_int(1 - now);
+        for (int x = 0; x < NQ; ++x)
 #pragma unroll
-      for (int b = 0; b < kBlocks; ++b)
-#pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          float& w = s[b][x][e + 2 * y];
-          w = w == 0.f ? 0.f : w * (f[b][y] * down * 0.5f);
-        }
+          for (int y = 0; y < 4; ++y) f(s[b][x][y], w[(8 * x + 2 * c + (y & 1)) * kPitch + 16 * b + g + 8 * (y >> 1)]);
+    };
+    each([](float& weight, float& at) { at = weight; });
+    const float f = (spoilt >> lane) & 1u ? 0.f : lds_f32(scale_at(slot, key0 + lane));
+    __syncwarp();
+    const int before = parted && lane < 8 * NQ ? own[lane].x : ev;  // of row `lane`
+    int after = ev;
+#pragma unroll 4
+    for (int r = 0; r < 8 * NQ; ++r) {
+      const float weight = w[r * kPitch + lane];
+      const int now = max(__shfl_sync(all, before, r), exponent_of(__uint_as_float(__reduce_max_sync(
+                                                           all, weight != 0.f ? __float_as_uint(f) : 0u))) + 1);
+      w[r * kPitch + lane] = weight != 0.f ? weight * (f * exp2_int(1 - now) * 0.5f) : 0.f;
+      if (lane == r) after = now;
     }
+    if (lane < 8 * NQ) own[lane] = make_int2(after, before - after);
+    parted = true;
+    __syncwarp();
+    each([](float& weight, float& at) { weight = at; });
+#pragma unroll
+    for (int x = 0; x < NQ; ++x)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int down = own[8 * x + 2 * c + e].y;
+        alpha[x][e] *= exp2_int(max(down, -126));
+        any = any || down != 0;
+      }
   };
   int t = kTeams == 1 ? 0 : (n0 ^ team) & 1;  // the team's first tile
   if (t < pc.tiles) {
@@ -372,7 +375,10 @@ __device__ __forceinline__ bool Warp<D, QUANT, NQ>::piece(const TreeParams& p, c
           }
           l_run[x][e] = l_run[x][e] * alpha[x][e] + sum;
         }
-        if (apart) weigh(x, v_slot, spoilt, alpha[x], any);
+      }
+      if (apart) weigh(v_slot, spoilt, alpha, any);
+#pragma unroll
+      for (int x = 0; x < NQ; ++x) {
         // P in 16 bits, the second product's operand type: off by at most 2^-8 (bf16) or
         // 2^-11 (f16) of each weight; l sums the unrounded values.  Queries by rows, keys
         // by columns now
@@ -441,34 +447,32 @@ __device__ __forceinline__ bool Warp<D, QUANT, NQ>::piece(const TreeParams& p, c
               u[x][0] = v.x; u[x][1] = v.y;
             }
           }
-          if (alive != ~0u) {
+          if (apart || alive != ~0u) {
 #pragma unroll
-            for (int x = 0; x < 4; ++x)
+            for (int x = 0; x < 4; ++x) {
+              if (apart) f[x] = exp2_int(ev);  // (the weights have them: a factor of 1)
               if (!((live >> (2 * c + (x >> 1) * 8 + (x & 1))) & 1u)) {
                 f[x] = 0.f;
 #pragma unroll
                 for (int y = 0; y < D / 32; ++y) u[x][y] = 0u;
               }
-          }
-          // factors of the lane's keys, relative to 2^ev; where rows see different keys the weights have them
-          uint32_t f0 = 0x3C003C00u, f1 = 0x3C003C00u;
-          if (!apart) {
-            const int e = exponent_of(__uint_as_float(
-                __reduce_max_sync(all, __float_as_uint(fmaxf(fmaxf(f[0], f[1]), fmaxf(f[2], f[3]))))));
-            if (e > ev) {  // (the same for the warp)
-              const float down = exp2_int(max(ev - e, -126));
-#pragma unroll
-              for (int y = 0; y < NQ; ++y)
-#pragma unroll
-                for (int x = 0; x < kOut; ++x)
-#pragma unroll
-                  for (int z = 0; z < 4; ++z) o[y][x][z] *= down;
-              ev = e;
             }
-            const float inv = exp2_int(-ev);
-            f0 = pack_f16x2(f[0] * inv, f[1] * inv);
-            f1 = pack_f16x2(f[2] * inv, f[3] * inv);
           }
+          // factors of the lane's keys, relative to 2^ev
+          const int e = exponent_of(__uint_as_float(
+              __reduce_max_sync(all, __float_as_uint(fmaxf(fmaxf(f[0], f[1]), fmaxf(f[2], f[3]))))));
+          if (e > ev) {  // (the same for the warp)
+            const float down = exp2_int(max(ev - e, -126));
+#pragma unroll
+            for (int y = 0; y < NQ; ++y)
+#pragma unroll
+              for (int x = 0; x < kOut; ++x)
+#pragma unroll
+                for (int z = 0; z < 4; ++z) o[y][x][z] *= down;
+            ev = e;
+          }
+          const float inv = exp2_int(-ev);
+          const uint32_t f0 = pack_f16x2(f[0] * inv, f[1] * inv), f1 = pack_f16x2(f[2] * inv, f[3] * inv);
 #pragma unroll
           for (int x = 0; x < kOut; ++x) {  // columns 2x, 2x + 1 of the lane's
             const uint32_t a = __byte_perm(u[0][x >> 1], u[1][x >> 1], x & 1 ? 0x7362 : 0x5140);
@@ -495,9 +499,10 @@ __device__ __forceinline__ bool Warp<D, QUANT, NQ>::piece(const TreeParams& p, c
       l += __shfl_xor_sync(all, l, 8);
       l += __shfl_xor_sync(all, l, 16);
       const int r = 8 * n + 2 * c + e;  // of the warp's
+      const float down = QUANT ? exp2_int(parted ? own[r].x : ev) : 1.f;
+      if (QUANT) __syncwarp();
       if (g == 0) ml[warp * (8 * NQ) + r] = make_float2(m_use[n][e], l);
       float* const dst = join + (warp * (8 * NQ) + r) * D;
-      const float down = QUANT ? exp2_int(unit_of(n, e)) : 1.f;
       if constexpr (!QUANT) {
 #pragma unroll
         for (int x = 0; x < kOut; ++x) {
