@@ -1,9 +1,9 @@
 """cos and sin of small angles, and next to a quarter turn, keep fp32's relative bits.
 
-A pair (1, 0) becomes (cos t, sin t).  The angle is off by at most |p| 2^-64 turns, its rest of a
-quarter turn is rounded to fp32 (2^-24 of the rest, which is what a small sine moves by, and at most
-pi / 2 times that of the sine at its end), the functions by 2 units in the last place (2^-22 of the
-value at most) and the product by 2^-24: together below 2^-21 of the value and 2 pi |p| 2^-64."""
+A pair (1, 0) becomes (cos t, sin t).  The angle is off by at most |p| 2^-64 turns; its rest of a
+quarter turn is rounded to fp32 twice, 2^-23 of the rest, by which a sine moves at most in proportion
+and a cosine by pi / 4 of that; the functions are off by 2 units in the last place (2^-22 of the value at
+most) and the product by 2^-24: together 7 2^-24 of the value, below 2^-21, and 2 pi |p| 2^-64."""
 
 import numpy as np
 import pytest
