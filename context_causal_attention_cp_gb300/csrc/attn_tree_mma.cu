@@ -441,7 +441,7 @@ attn_tree_mma_kernel(const __grid_constant__ TreeMaps maps, const TreeParams p) 
         const int place = is_v ? v_place<!DUAL>(n) : k_place<!DUAL>(n), slot = place % kSt, row = cur.row(p);
         ok = wait_warp(emptyb + slot, ((place / kSt) & 1) ^ 1, abort_flag, p.timeout_ns);
         if (!ok) break;
-        if (QUANT && lane == 0) raw_note[slot] = RawNote{cur.live, cur.fresh, cur.t <= (DUAL ? 0 : 1), 0};
+        if (QUANT && lane == 0) raw_note[slot] = RawNote{cur.live, cur.fresh, cur.t <= (DUAL ? 0 : 1)};
         copy_tile<kChunks, kLine>(p, is_v ? &maps.v : &maps.k, is_v ? &maps.v_tail : &maps.k_tail,
                                   ring + slot * kBytes, fullb + slot, cur, row, whole_log);
         if constexpr (QUANT) {

@@ -35,7 +35,7 @@ namespace cpattn {
 namespace {
 
 constexpr int kWarps = kSmallWarps;
-constexpr int kThreads = kSmallThreads;  // a third warpgroup: the loading warp and three that idle
+constexpr int kThreads = kSmallThreads;  // a third warpgroup: K's loader, V's, the walker, and one that idles
 constexpr int kRegsLaunch = 168, kRegsWork = 208, kRegsOther = 88;
 static_assert(kRegsWork * 256 + kRegsOther * 128 <= kRegsLaunch * kThreads, "register split exceeds the launch's");
 

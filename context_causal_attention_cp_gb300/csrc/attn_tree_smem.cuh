@@ -56,13 +56,12 @@ struct MmaCfg {
 };
 
 // What a producer tells the converters about a raw tile.
-struct RawNote {
+struct alignas(16) RawNote {
   int live;   // rows up to the unit's end
   int fresh;  // first row that is a new key
   int first;  // of its piece and stream
-  int unused;
 };
-static_assert(sizeof(RawNote) == 16, "");
+static_assert(sizeof(RawNote) == 16, "kNoteOff's places");
 
 // ---- 8 and 16 rows (attn_tree_small.cu) ----
 constexpr int kSmallWarps = 8, kSmallThreads = 384;

@@ -459,7 +459,7 @@ int strides16(RopeSide* s, int64_t xr, int64_t xh, int64_t yr, int64_t yh, int r
 
 // One rotated tensor of cp_rope, or Q of cp_kv_append.
 int rotated_side(RopeSide* s, const void* x, int64_t xr, int64_t xh, int heads, void* y, int64_t yr, int64_t yh,
-                 bool f32, int num_rows, int d, const cp_rope_t* rope) {
+                 bool f32, int num_rows, int d) {
   const int size = f32 ? 4 : 2;
   int rc = check_rows(x, xr, xh, size);
   if (rc == CPATTN_OK) rc = check_out_rows(y, yr, yh, size, num_rows, heads, d);
@@ -475,7 +475,7 @@ int rotated_side(RopeSide* s, const void* x, int64_t xr, int64_t xh, int heads, 
 
 // K or V of cp_kv_append.
 int cached_side(RopeSide* s, const void* x, int64_t xr, int64_t xh, bool f32, int heads, int dim,
-                const cp_kv_codes_t* c, int num_rows, int cache_rows, const cp_rope_t* rope) {
+                const cp_kv_codes_t* c, int num_rows, int cache_rows) {
   const int rc = check_rows(x, xr, xh, f32 ? 4 : 2);
   if (rc != CPATTN_OK) return rc;
   if (dim < 16 || dim > kMaxDim || dim % 16) return CPATTN_ERR_UNSUPPORTED;
@@ -535,10 +535,10 @@ extern "C" int cp_rope(const cp_rope_t* rope, const cp_rope_args_t* a, cudaStrea
   RopeParams p{};
   const bool f32 = a->x_is_fp32 != 0;
   rc = rotated_side(&p.side[0], a->q, a->q_row_stride, a->q_head_stride, a->Hq, a->q_out, a->qo_row_stride,
-                    a->qo_head_stride, f32, a->num_rows, a->d, rope);
+                    a->qo_head_stride, f32, a->num_rows, a->d);
   if (rc == CPATTN_OK && a->Hk > 0)
     rc = rotated_side(&p.side[1], a->k, a->k_row_stride, a->k_head_stride, a->Hk, a->k_out, a->ko_row_stride,
-                      a->ko_head_stride, f32, a->num_rows, a->d, rope);
+                      a->ko_head_stride, f32, a->num_rows, a->d);
   if (rc != CPATTN_OK || a->num_rows == 0) return rc;
   p.positions = a->positions;
   p.axis_stride = a->axis_stride;
@@ -561,13 +561,13 @@ extern "C" int cp_kv_append(const cp_rope_t* rope, const cp_kv_codes_t* k_cache,
   RopeParams p{};
   const bool f32 = a->x_is_fp32 != 0;
   rc = cached_side(&p.side[1], a->k, a->k_row_stride, a->k_head_stride, f32, a->Hkv, a->d, k_cache, a->num_rows,
-                   a->cache_rows, rope);
+                   a->cache_rows);
   if (rc == CPATTN_OK && v_cache)
     rc = cached_side(&p.side[2], a->v, a->v_row_stride, a->v_head_stride, f32, a->Hkv, a->dv, v_cache, a->num_rows,
-                     a->cache_rows, nullptr);
+                     a->cache_rows);
   if (rc == CPATTN_OK && a->Hq > 0)
     rc = rotated_side(&p.side[0], a->q, a->q_row_stride, a->q_head_stride, a->Hq, a->q_out, a->qo_row_stride,
-                      a->qo_head_stride, f32, a->num_rows, a->d, rope);
+                      a->qo_head_stride, f32, a->num_rows, a->d);
   if (rc != CPATTN_OK || a->num_rows == 0) return rc;
   p.positions = a->positions;
   p.axis_stride = a->axis_stride;
