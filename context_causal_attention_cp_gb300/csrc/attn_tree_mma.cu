@@ -28,13 +28,14 @@
 // Codes of cached keys, which all rows of a request see, are turned to f16 with one exponent a tile.
 // In a tile with new keys that would let the scale of a key that a row does not see take the bits
 // of those that it sees: there codes stay as they are, and K's scales go to the scores, V's to the
-// weights (softmax_row_scaled; it costs 2 to 3 us at a piece's end, e4m3 trees of 26 at d = 64 31.6 -> 34 us,
-// while the other tiles' code is rid of its masks).
+// weights (softmax_row_scaled; it costs 2 us at a piece's end, e4m3 trees of 26 at d = 64 31.3 -> 33.4 us,
+// while the other tiles' code is rid of its masks, e4m3 trees of 64 407 -> 364).
 //
-// Measured, 32/8 heads, d = 128, 32 requests on up to 16K keys: trees of 32 (single units) 205 us,
-// HBM (floor 193); trees of 64 (dual) 251 us (floor 194): the tensor pipe is active 61 % of the
-// time, a stream's chain S -> softmax -> P -> P V is what bounds them.  Over codes 278 and 399 us
-// (floors 100 and 130): the same chain with S in halves, beside the converters.
+// Measured on the device, 32/8 heads, d = 128, 32 requests on up to 16K keys: trees of 32 (single units)
+// 209 us, HBM (floor 193); trees of 64 (dual) 257 us at 2.07 GHz, 273 at the 1.8 GHz of a steady run
+// (floor 194): the tensor pipe is active 60 % of the cycles, a stream's chain S -> softmax -> P ->
+// P V is what bounds them.  Over codes 262 and 364 us (floors 100 and 130): the same chain with S in
+// halves, beside the converters.
 #include <algorithm>
 #include <atomic>
 #include <type_traits>

@@ -23,8 +23,8 @@
 // largest that the warp has met (O is rescaled when that grows); among new keys, of which a row
 // may not see all, V's scale multiplies the weight, relative to the largest that the row has seen.
 //
-// Measured, 32/8 heads, d = 128: 64 tokens on up to 8K keys each, bf16 173 us (6.8 TB/s, the copy
-// bandwidth), e4m3 110 us (5.5 TB/s: codes to f16 and the copies of the scales); one token on 1K
+// Measured, 32/8 heads, d = 128: 64 tokens on up to 8K keys each, bf16 175 us (6.7 TB/s, the copy
+// bandwidth), e4m3 111 us (5.5 TB/s: codes to f16 and the copies of the scales); one token on 1K
 // 11 us, of which tree_start takes 2, the first piece's walk 1.5, its tiles 3 and the merge 4.
 #include <algorithm>
 #include <atomic>

@@ -14,10 +14,10 @@
 // its part of the block's cos and sin (into shared memory: they serve all heads) while these
 // are on their way, and then rotates, rounds or quantises.  Q, K and V have code of their own (one
 // code for all, with the side looked up for each vector: 32.1 against 30.3 us).  Measured: 8192
-// rows of 40 heads of 128 (bf16) 30.3 us, 5.5 TB/s; fp32 54.6 us, 6.2 TB/s; 4096 rows into an e4m3
-// cache 22.5 us; 16384 rows of 576 columns 12.6 us, 3.0 TB/s (a vector is three items of 16 lanes,
+// rows of 40 heads of 128 (bf16) 30.2 us, 5.6 TB/s; fp32 54.8 us, 6.1 TB/s; 4096 rows into an e4m3
+// cache 22.7 us; 16384 rows of 576 columns 12.6 us, 3.0 TB/s (a vector is three items of 16 lanes,
 // one row a group: what is in flight; with the rows' cos and sin computed by 32 of the threads
-// 35.8 us); 64 rows 3.2 us, the launch.
+// 35.8 us); 64 rows 2.9 us, the launch.
 #include <algorithm>
 #include <cmath>
 #include <cstdint>

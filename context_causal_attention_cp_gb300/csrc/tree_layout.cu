@@ -4,8 +4,8 @@
 // A node's ancestors have lower numbers, so that a walk from the node to its root meets
 // falling bits: a thread a node keeps the current word in a register and writes each word
 // once.  A block a request, the parents in shared memory.  Latency: the walk is as long as
-// the node is deep, each step a shared-memory load (4.8 us for 256 requests of up to 64
-// nodes, 2.3 for one of 8, the launch among them).
+// the node is deep, each step a shared-memory load (4.5 us for 256 requests of up to 64
+// nodes, 2.1 for one of 8, the launch among them).
 #include <algorithm>
 #include <cstdint>
 
